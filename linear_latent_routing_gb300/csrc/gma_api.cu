@@ -5,6 +5,22 @@
 
 #include "gma_internal.cuh"
 
+namespace gma {
+
+gma_status_t usable_device()
+{
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) return GMA_ERR_NO_DEVICE;
+    int major = 0, minor = 0;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
+        return GMA_ERR_NO_DEVICE;
+    if (major != 10 || minor != 3) return GMA_ERR_NO_DEVICE;
+    return GMA_OK;
+}
+
+}  // namespace gma
+
 using namespace gma;
 
 namespace {
@@ -40,18 +56,6 @@ bool single_pass_unsupported(const gma_shape_t &s, int variant)
     return variant == GMA_VARIANT_CAUSAL && (s.flags & GMA_FLAG_SINGLE_PASS) && family_of(s, variant) != 1;
 }
 
-gma_status_t check_device()
-{
-    int dev = -1;
-    if (cudaGetDevice(&dev) != cudaSuccess) return GMA_ERR_NO_DEVICE;
-    int major = 0, minor = 0;
-    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
-        return GMA_ERR_NO_DEVICE;
-    if (major != 10 || minor != 3) return GMA_ERR_NO_DEVICE;
-    return GMA_OK;
-}
-
 // The word a test-of-timeouts call puts in the header (static storage: the copy reads it after
 // the call has returned).
 const unsigned kShortWaits = 1u;
@@ -60,7 +64,7 @@ gma_status_t begin_call_sized(size_t need, void *ws, size_t ws_bytes, cudaStream
 {
     if (!ws || ((uintptr_t)ws & 255u)) return GMA_ERR_WORKSPACE;
     if (need == 0 || ws_bytes < need) return GMA_ERR_WORKSPACE;
-    gma_status_t d = check_device();
+    gma_status_t d = usable_device();
     if (d != GMA_OK) return d;
     if (cudaMemsetAsync(ws, 0, sizeof(WsHeader), st) != cudaSuccess) return GMA_ERR_CUDA;
     if ((flags & GMA_FLAG_TEST_WITHHOLD) &&

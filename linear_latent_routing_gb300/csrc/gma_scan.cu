@@ -1,0 +1,287 @@
+// gma_scan.cu -- the selective state space scan (gma_scan_forward) and its step for one token
+// (gma_scan_step).
+//
+//   h_t[n] = exp(delta_t A[n]) h_{t-1}[n] + delta_t b_t[n] u_t,   y_t = (sum_n c_t[n] h_t[n] + D u_t) silu(z_t)
+//
+// The decay differs from channel to channel and state to state, so there is no matrix product in it:
+// each (token, channel, state) takes one exponential and about five multiply-adds in fp32.
+#include "scan_tile.cuh"
+
+namespace gma {
+namespace blk {
+
+gma_status_t scan_check(const gma_scan_t *s, bool out)
+{
+    if (!s) return GMA_ERR_INVALID_ARG;
+    if (s->B < 1 || s->N < 1 || s->D < 1 || s->S < 1 || s->G < 1 || s->D % s->G) return GMA_ERR_INVALID_ARG;
+    if (s->dtype != GMA_F32 && s->dtype != GMA_BF16) return GMA_ERR_INVALID_ARG;
+    if (!(s->S == 8 || s->S == 16 || s->S == 32 || s->S == 64)) return GMA_ERR_UNSUPPORTED_SHAPE;
+    if (s->B > 65535 || s->D > (1 << 24) || s->N > (1 << 30)) return GMA_ERR_UNSUPPORTED_SHAPE;
+    const int dt = s->dtype;
+    const long long B = s->B, N = s->N, D = s->D, GS = (long long)s->G * s->S;
+    if (!rows_ok(s->u, dt, B, N, D, false) || !rows_ok(s->dt, dt, B, N, D, false) ||
+        !rows_ok(s->b, dt, B, N, GS, false) || !rows_ok(s->c, dt, B, N, GS, false))
+        return GMA_ERR_INVALID_ARG;
+    if (s->z.ptr && !rows_ok(s->z, dt, B, N, D, false)) return GMA_ERR_INVALID_ARG;
+    if (out && !rows_ok(s->y, dt, B, N, D, true)) return GMA_ERR_INVALID_ARG;
+    // states are read and written in pairs and quadruples
+    if (!ptr_ok(s->a_log, 16) || !opt_ok(s->d_skip, 4) || !opt_ok(s->dt_bias, 4) || !opt_ok(s->state_in, 16) ||
+        !opt_ok(s->state_out, 16) || !opt_ok(s->checkpoints, 16) || !opt_ok(s->lengths, 4))
+        return GMA_ERR_INVALID_ARG;
+    return GMA_OK;
+}
+
+bool scan_vec(const gma_scan_t &s)
+{
+    return (s.D / s.G) % 8 == 0 && rows_vec(s.u, s.dtype) && rows_vec(s.dt, s.dtype) &&
+           (!s.z.ptr || rows_vec(s.z, s.dtype)) && rows_vec(s.b, s.dtype) && rows_vec(s.c, s.dtype);
+}
+
+namespace {
+
+template <class K> struct ForwardSmem {
+    static constexpr int U = 0;                                         // u, then p
+    static constexpr int DT = U + K::CHANNEL_FLOATS * 4;
+    static constexpr int PAIRS = (DT + K::CHANNEL_FLOATS * 4 + 15) / 16 * 16;
+    static size_t bytes(int S) { return PAIRS + (size_t)S * K::TT * 8 + (size_t)2 * K::CH * S * 4; }
+};
+
+template <typename T, class K, bool VEC>
+__global__ void __launch_bounds__(K::THREADS) scan_forward_kernel(const ScanArgs<T> a)
+{
+    extern __shared__ __align__(16) unsigned char smem[];
+    float *us = reinterpret_cast<float *>(smem + ForwardSmem<K>::U);
+    float *dts = reinterpret_cast<float *>(smem + ForwardSmem<K>::DT);
+    f2 *bs = reinterpret_cast<f2 *>(smem + ForwardSmem<K>::PAIRS);
+    f2 *cs = bs + a.S / 2 * K::TT;
+    float *rate = reinterpret_cast<float *>(cs + a.S / 2 * K::TT);   // A log2(e), [CH][S]
+    float *hs = rate + K::CH * a.S;                                   // the state before the tile, [CH][S]
+
+    const int b = blockIdx.y, group = blockIdx.x / a.tiles, Dg = a.D / a.G;
+    const int in_group = (blockIdx.x - group * a.tiles) * K::CH;
+    const int c0 = group * Dg + in_group, nch = min(K::CH, Dg - in_group);
+    const int len = row_length(a.lengths, b, a.N);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int tl = lane % K::LT, ch = warp * K::CPW + lane / K::LT;
+    const int nck = (a.N + CKPT - 1) / CKPT;
+
+    for (int i = threadIdx.x; i < K::CH * a.S; i += K::THREADS) {
+        const int k = i / a.S;
+        const long long at = (long long)(c0 + k) * a.S + i % a.S;
+        rate[i] = k < nch ? -expf(a.a_log[at]) * LOG2E : 0.f;
+        hs[i] = k < nch && a.state_in ? a.state_in[(long long)b * a.D * a.S + at] : 0.f;
+    }
+    const float skip = a.d_skip && ch < nch ? a.d_skip[c0 + ch] : 0.f;
+
+    for (int t0 = 0; t0 < len; t0 += K::TT) {
+        __syncthreads();
+        // u and delta of the tile, transposed; zeros behind the last token leave the state alone
+        for (int i = threadIdx.x; i < K::TT * (K::CH / 8); i += K::THREADS) {
+            const int piece = i % (K::CH / 8), t = i / (K::CH / 8), n = min(8, nch - piece * 8);
+            float u[8], d[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) u[k] = d[k] = 0.f;
+            if (t0 + t < len && n > 0) {
+                const int c = c0 + piece * 8;
+                load8<VEC>(a.u.at(b, t0 + t) + c, n, u);
+                load8<VEC>(a.dt.at(b, t0 + t) + c, n, d);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    d[k] = k < n ? softplus(d[k] + (a.dt_bias ? a.dt_bias[c + k] : 0.f)) : 0.f;
+            }
+            const int at = K::pos(t);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                us[K::channel(piece * 8 + k) + at] = u[k];
+                dts[K::channel(piece * 8 + k) + at] = d[k];
+            }
+        }
+        stage_pairs<K, T, VEC>(a.b, b, group * a.S, t0, len, a.S, bs);
+        stage_pairs<K, T, VEC>(a.c, b, group * a.S, t0, len, a.S, cs);
+        __syncthreads();
+
+        {
+            float dt[K::TL], u[K::TL];
+            lane_load<K>(dts + K::channel(ch), tl, dt);
+            lane_load<K>(us + K::channel(ch), tl, u);
+            f2 dt2[K::TL], xu2[K::TL], y2[K::TL];
+            float total = 0.f;
+#pragma unroll
+            for (int i = 0; i < K::TL; ++i) {
+                total += dt[i];
+                dt2[i] = pack2(dt[i], dt[i]);
+                xu2[i] = pack2(dt[i] * u[i], dt[i] * u[i]);
+                y2[i] = pack2(skip * u[i], 0.f);
+            }
+            const f2 total2 = pack2(total, total);
+            const int start = t0 + tl * K::TL;
+            const bool keep = a.ckpt && start % CKPT == 0 && start < len && ch < nch;
+            float *ck = keep ? a.ckpt + (((long long)b * nck + start / CKPT) * a.D + c0 + ch) * a.S : nullptr;
+            for (int p = 0; p < a.S / 2; ++p) {
+                const f2 r2 = *reinterpret_cast<const f2 *>(rate + ch * a.S + 2 * p);
+                f2 *h0 = reinterpret_cast<f2 *>(hs + ch * a.S + 2 * p);
+                f2 a2[K::TL], x2[K::TL], h = 0ull;
+#pragma unroll
+                for (int q = 0; q < K::TL / 2; ++q) pair_load<K>(bs, p, tl, q, x2[2 * q], x2[2 * q + 1]);
+#pragma unroll
+                for (int i = 0; i < K::TL; ++i) {
+                    a2[i] = ex2_2(mul2(dt2[i], r2));
+                    x2[i] = mul2(x2[i], xu2[i]);
+                    h = fma2(a2[i], h, x2[i]);
+                }
+                f2 decay = ex2_2(mul2(total2, r2));
+                scan_up<K::LT>(decay, h, tl);
+                const f2 before = *h0;
+                const f2 d1 = __shfl_up_sync(0xffffffffu, decay, 1, K::LT);
+                const f2 s1 = __shfl_up_sync(0xffffffffu, h, 1, K::LT);
+                const f2 end = fma2(decay, before, h);
+                h = tl ? fma2(d1, before, s1) : before;
+                if (tl == K::LT - 1) *h0 = end;
+                if (keep) *reinterpret_cast<f2 *>(ck + 2 * p) = h;
+#pragma unroll
+                for (int q = 0; q < K::TL / 2; ++q) {
+                    f2 c2[2];
+                    pair_load<K>(cs, p, tl, q, c2[0], c2[1]);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        h = fma2(a2[2 * q + e], h, x2[2 * q + e]);
+                        y2[2 * q + e] = fma2(c2[e], h, y2[2 * q + e]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < K::TL; ++i) {
+                const float2 y = unpack2(y2[i]);
+                u[i] = y.x + y.y;
+            }
+            lane_store<K>(us + K::channel(ch), tl, u);
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < K::TT * (K::CH / 8); i += K::THREADS) {
+            const int piece = i % (K::CH / 8), t = i / (K::CH / 8), n = min(8, nch - piece * 8);
+            if (t0 + t >= len || n <= 0) continue;
+            const int c = c0 + piece * 8, at = K::pos(t);
+            float y[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) y[k] = us[K::channel(piece * 8 + k) + at];
+            if (a.z.p) {
+                float z[8];
+                load8<VEC>(a.z.at(b, t0 + t) + c, n, z);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) y[k] *= silu(z[k]);
+            }
+            store8<VEC>(a.y.at(b, t0 + t) + c, n, y);
+        }
+    }
+    __syncthreads();
+    if (a.state_out)
+        for (int i = threadIdx.x; i < nch * a.S; i += K::THREADS)
+            a.state_out[((long long)b * a.D + c0) * a.S + i] = hs[i];
+}
+
+// One token: a lane holds four states of a channel, S / 4 lanes a channel.  The state is read and
+// written once, which bounds it.
+template <typename T, int S>
+__global__ void __launch_bounds__(256) scan_step_kernel(const ScanArgs<T> a)
+{
+    constexpr int LPC = S / 4, CPB = 256 / LPC;
+    const int b = blockIdx.y, d = blockIdx.x * CPB + threadIdx.x / LPC, q = threadIdx.x % LPC;
+    const bool live = d < a.D;
+    float y = 0.f, u = 0.f;
+    if (live) {
+        const long long at = ((long long)b * a.D + d) * S + 4 * q;
+        const float4 h4 = *reinterpret_cast<const float4 *>(a.state_in + at);
+        const float4 r4 = *reinterpret_cast<const float4 *>(a.a_log + (long long)d * S + 4 * q);
+        const int g = d / (a.D / a.G);
+        const T *bp = a.b.at(b, 0) + g * S + 4 * q, *cp = a.c.at(b, 0) + g * S + 4 * q;
+        u = to_f32<T>(a.u.at(b, 0)[d]);
+        const float delta = softplus(to_f32<T>(a.dt.at(b, 0)[d]) + (a.dt_bias ? a.dt_bias[d] : 0.f));
+        float h[4] = {h4.x, h4.y, h4.z, h4.w};
+        const float r[4] = {r4.x, r4.y, r4.z, r4.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            h[k] = fmaf(ex2(-expf(r[k]) * LOG2E * delta), h[k], delta * u * to_f32<T>(bp[k]));
+            y = fmaf(to_f32<T>(cp[k]), h[k], y);
+        }
+        *reinterpret_cast<float4 *>(a.state_out + at) = make_float4(h[0], h[1], h[2], h[3]);
+    }
+#pragma unroll
+    for (int off = LPC / 2; off; off >>= 1) y += __shfl_xor_sync(0xffffffffu, y, off);
+    if (live && q == 0) {
+        if (a.d_skip) y = fmaf(a.d_skip[d], u, y);
+        if (a.z.p) y *= silu(to_f32<T>(a.z.at(b, 0)[d]));
+        a.y.at(b, 0)[d] = from_f32<T>(y);
+    }
+}
+
+template <typename T, class K, bool VEC> gma_status_t launch_forward(const gma_scan_t &s, cudaStream_t st)
+{
+    ScanArgs<T> a = scan_args<T>(s);
+    a.tiles = (s.D / s.G + K::CH - 1) / K::CH;
+    const size_t smem = ForwardSmem<K>::bytes(s.S);
+    auto kern = scan_forward_kernel<T, K, VEC>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        return GMA_ERR_CUDA;
+    GMA_LAUNCH(KID_SCAN, st, kern<<<dim3(a.tiles * s.G, s.B), K::THREADS, smem, st>>>(a));
+    return GMA_OK;
+}
+
+template <typename T, bool VEC> gma_status_t forward_of(const gma_scan_t &s, cudaStream_t st)
+{
+    return launch_forward<T, Tile<16, 8, 8>, VEC>(s, st);
+}
+
+}  // namespace
+}  // namespace blk
+}  // namespace gma
+
+using namespace gma;
+using namespace gma::blk;
+
+extern "C" {
+
+size_t gma_scan_checkpoint_size(const gma_scan_t *s)
+{
+    if (!s || s->B < 1 || s->N < 1 || s->D < 1 || s->S < 1) return 0;
+    return (size_t)s->B * ((s->N + CKPT - 1) / CKPT) * s->D * s->S * sizeof(float);
+}
+
+size_t gma_scan_workspace_size(const gma_scan_t *) { return 0; }
+
+gma_status_t gma_scan_forward(const gma_scan_t *s, void *ws, size_t ws_bytes, gma_stream_t stream)
+{
+    gma_status_t r = scan_check(s, true);
+    if (r != GMA_OK) return r;
+    if (!ws_ok(ws, ws_bytes, gma_scan_workspace_size(s))) return GMA_ERR_WORKSPACE;
+    if ((r = usable_device()) != GMA_OK) return r;
+    cudaStream_t st = (cudaStream_t)stream;
+    const bool vec = scan_vec(*s) && rows_vec(s->y, s->dtype);
+    if (s->dtype == GMA_BF16)
+        return vec ? forward_of<__nv_bfloat16, true>(*s, st) : forward_of<__nv_bfloat16, false>(*s, st);
+    return vec ? forward_of<float, true>(*s, st) : forward_of<float, false>(*s, st);
+}
+
+gma_status_t gma_scan_step(const gma_scan_t *s, gma_stream_t stream)
+{
+    gma_status_t r = scan_check(s, true);
+    if (r != GMA_OK) return r;
+    if (s->N != 1 || !s->state_in || !s->state_out || s->lengths || s->checkpoints) return GMA_ERR_INVALID_ARG;
+    if ((r = usable_device()) != GMA_OK) return r;
+    cudaStream_t st = (cudaStream_t)stream;
+    auto run = [&](auto t) -> gma_status_t {
+        using T = decltype(t);
+        const ScanArgs<T> a = scan_args<T>(*s);
+        const int cpb = 256 / (s->S / 4);
+        const dim3 grid((s->D + cpb - 1) / cpb, s->B);
+        GMA_LAUNCH(KID_SCAN_STEP, st, switch (s->S) {
+            case 8: scan_step_kernel<T, 8><<<grid, 256, 0, st>>>(a); break;
+            case 16: scan_step_kernel<T, 16><<<grid, 256, 0, st>>>(a); break;
+            case 32: scan_step_kernel<T, 32><<<grid, 256, 0, st>>>(a); break;
+            default: scan_step_kernel<T, 64><<<grid, 256, 0, st>>>(a); break;
+        });
+        return GMA_OK;
+    };
+    return s->dtype == GMA_BF16 ? run(__nv_bfloat16{}) : run(float{});
+}
+
+}  // extern "C"

@@ -58,6 +58,16 @@ const char *kernel_name(int id)
     case KID_BWD_DX: return "bwd_dx";
     case KID_BWD_PARAMS: return "bwd_param_partials";
     case KID_BWD_PFINAL: return "bwd_param_final";
+    case KID_SCAN: return "scan_forward";
+    case KID_SCAN_STEP: return "scan_step";
+    case KID_SCAN_BWD: return "scan_backward";
+    case KID_SCAN_BC: return "scan_backward_bc_sum";
+    case KID_CONV: return "conv_forward";
+    case KID_CONV_STEP: return "conv_step";
+    case KID_CONV_BWD: return "conv_backward";
+    case KID_NORM: return "norm_forward";
+    case KID_NORM_BWD: return "norm_backward";
+    case KID_SUM_ROWS: return "sum_rows";
     }
     return "unknown";
 }

@@ -1,0 +1,140 @@
+// scan_tile.cuh -- the tile shared by the selective scan's forward and backward kernels.
+//
+// A block takes CH channels of one group in one batch row and walks over the sequence in tiles of
+// TT = LT * TL tokens.  A warp's 32 lanes are CPW = 32 / LT channels times LT time lanes, each of which
+// owns TL neighbouring tokens: the recurrence is sequential over a lane's own tokens, with a scan of
+// (decay, state) pairs over the LT time lanes in between, so that a tile's exponentials are computed
+// once and every warp has LT * CPW lanes of independent work whatever the number of channels.  States
+// n and n + 1 share packed fp32 pairs.
+//
+// Tiles lie in shared memory in the order the lanes read them, 16 bytes a lane without bank conflicts:
+// token t = tl * TL + 4 q + e of a channel at (q * LT + tl) * 4 + e, and of a pair of states (2 q + e)
+// at (q * LT + tl) * 2 + e.
+#pragma once
+
+#include "block_common.cuh"
+
+namespace gma {
+namespace blk {
+
+constexpr int CKPT = 128;    // tokens between two checkpoints
+
+template <int LT_, int TL_, int WARPS_> struct Tile {
+    static constexpr int LT = LT_, TL = TL_, WARPS = WARPS_;
+    static constexpr int CPW = 32 / LT, CH = CPW * WARPS, TT = LT * TL, THREADS = 32 * WARPS;
+    static constexpr int PITCH = TT + 4;                       // floats between two channels
+    static constexpr int CHANNEL_FLOATS = CH * PITCH + CH / 8 * 16;
+    static_assert(TL % 4 == 0 && CH % 8 == 0, "16-byte pieces");
+    __host__ __device__ static constexpr int channel(int ch) { return ch * PITCH + ch / 8 * 16; }
+    __device__ static __forceinline__ int pos(int t)
+    {
+        const int tl = t / TL, i = t % TL;
+        return ((i / 4) * LT + tl) * 4 + i % 4;
+    }
+    __device__ static __forceinline__ int pos2(int t)
+    {
+        const int tl = t / TL, i = t % TL;
+        return ((i / 2) * LT + tl) * 2 + i % 2;
+    }
+};
+
+// One lane's TL values of a channel.
+template <class K> __device__ __forceinline__ void lane_load(const float *chan, int tl, float (&v)[K::TL])
+{
+#pragma unroll
+    for (int q = 0; q < K::TL / 4; ++q) {
+        const float4 x = *reinterpret_cast<const float4 *>(chan + (q * K::LT + tl) * 4);
+        v[4 * q] = x.x; v[4 * q + 1] = x.y; v[4 * q + 2] = x.z; v[4 * q + 3] = x.w;
+    }
+}
+template <class K> __device__ __forceinline__ void lane_store(float *chan, int tl, const float (&v)[K::TL])
+{
+#pragma unroll
+    for (int q = 0; q < K::TL / 4; ++q)
+        *reinterpret_cast<float4 *>(chan + (q * K::LT + tl) * 4) =
+            make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+}
+
+// One lane's TL values of a pair of states: two tokens of pair p.
+template <class K> __device__ __forceinline__ void pair_load(const f2 *tile, int p, int tl, int q, f2 &v0, f2 &v1)
+{
+    const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(tile + p * K::TT + (q * K::LT + tl) * 2);
+    v0 = x.x; v1 = x.y;
+}
+
+// Stages tokens t0 .. t0 + TT - 1 of b or c (S values a token) as pairs; zeros behind the last token.
+template <class K, typename T, bool VEC>
+__device__ __forceinline__ void stage_pairs(const Rows<const T> &r, int b, int first, int t0, int len, int S, f2 *tile)
+{
+    const int pieces = S / 8;
+    for (int i = threadIdx.x; i < K::TT * pieces; i += K::THREADS) {
+        const int t = i % K::TT, piece = i / K::TT;
+        float v[8];
+        if (t0 + t < len) {
+            load8<VEC>(r.at(b, t0 + t) + first + piece * 8, 8, v);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = 0.f;
+        }
+        const int at = K::pos2(t);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tile[(piece * 4 + k) * K::TT + at] = pack2(v[2 * k], v[2 * k + 1]);
+    }
+}
+
+// Inclusive scan over the time lanes of (decay, state): state_l += decay_l state_{l - off}.
+template <int LT> __device__ __forceinline__ void scan_up(f2 &decay, f2 &state, int tl)
+{
+#pragma unroll
+    for (int off = 1; off < LT; off *= 2) {
+        const f2 d = __shfl_up_sync(0xffffffffu, decay, off, LT);
+        const f2 s = __shfl_up_sync(0xffffffffu, state, off, LT);
+        if (tl >= off) {
+            state = fma2(decay, s, state);
+            decay = mul2(decay, d);
+        }
+    }
+}
+template <int LT> __device__ __forceinline__ void scan_down(f2 &decay, f2 &state, int tl)
+{
+#pragma unroll
+    for (int off = 1; off < LT; off *= 2) {
+        const f2 d = __shfl_down_sync(0xffffffffu, decay, off, LT);
+        const f2 s = __shfl_down_sync(0xffffffffu, state, off, LT);
+        if (tl + off < LT) {
+            state = fma2(decay, s, state);
+            decay = mul2(decay, d);
+        }
+    }
+}
+
+template <typename T> struct ScanArgs {
+    int B, N, D, S, G, tiles;      // tiles: blocks of CH channels per group
+    Rows<const T> u, dt, z, b, c;
+    const float *a_log, *d_skip, *dt_bias, *state_in;
+    float *state_out;
+    const int *lengths;
+    Rows<T> y;
+    float *ckpt;
+};
+
+template <typename T> inline ScanArgs<T> scan_args(const gma_scan_t &s)
+{
+    ScanArgs<T> a;
+    a.B = s.B; a.N = s.N; a.D = s.D; a.S = s.S; a.G = s.G; a.tiles = 0;
+    a.u = rows_of<const T>(s.u); a.dt = rows_of<const T>(s.dt); a.z = rows_of<const T>(s.z);
+    a.b = rows_of<const T>(s.b); a.c = rows_of<const T>(s.c);
+    a.a_log = s.a_log; a.d_skip = s.d_skip; a.dt_bias = s.dt_bias;
+    a.state_in = s.state_in; a.state_out = s.state_out; a.lengths = s.lengths;
+    a.y = rows_of<T>(s.y);
+    a.ckpt = s.checkpoints;
+    return a;
+}
+
+// What every scan call needs; `out`: y is written.
+gma_status_t scan_check(const gma_scan_t *s, bool out);
+// 16-byte accesses to the rows of u, dt, z, b and c.
+bool scan_vec(const gma_scan_t &s);
+
+}  // namespace blk
+}  // namespace gma
