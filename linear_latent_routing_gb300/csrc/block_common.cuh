@@ -53,6 +53,38 @@ template <bool VEC> __device__ __forceinline__ void load8(const float *p, int n,
     }
 }
 
+// The same eight values as they lie in memory, loaded ahead of their use (VEC rows only).
+template <typename T> struct Raw8 {
+    uint4 q[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T *p)
+    {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) q[i] = reinterpret_cast<const uint4 *>(p)[i];
+    }
+    __device__ __forceinline__ void zero()
+    {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) q[i] = make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const
+    {
+        if (sizeof(T) == 2) {
+            const uint32_t w[4] = {q[0].x, q[0].y, q[0].z, q[0].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[2 * i] = __uint_as_float(w[i] << 16);
+                v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+                v[4 * i] = __uint_as_float(q[i].x); v[4 * i + 1] = __uint_as_float(q[i].y);
+                v[4 * i + 2] = __uint_as_float(q[i].z); v[4 * i + 3] = __uint_as_float(q[i].w);
+            }
+        }
+    }
+};
+
 template <bool VEC> __device__ __forceinline__ void store8(__nv_bfloat16 *p, int n, const float (&v)[8])
 {
     if (VEC) {
@@ -128,11 +160,33 @@ __device__ __forceinline__ f2 ex2_2(f2 v)
     const float2 x = unpack2(v);
     return pack2(ex2(x.x), ex2(x.y));
 }
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
-__device__ __forceinline__ float silu(float x) { return __fdividef(x, 1.f + __expf(-x)); }
+__device__ __forceinline__ float rcp(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// 1 / (1 + exp(-x)): 1 ulp from each of the three steps; exp(-x) may overflow, whose reciprocal is 0.
+__device__ __forceinline__ float sigmoid(float x) { return rcp(1.f + ex2(-LOG2E * x)); }
+__device__ __forceinline__ float silu(float x) { return x * sigmoid(x); }
 // silu'(x) = s (1 + x (1 - s)), s = sigmoid(x)
 __device__ __forceinline__ float dsilu(float x, float s) { return s * (1.f + x * (1.f - s)); }
-__device__ __forceinline__ float softplus(float x) { return x > 20.f ? x : log1pf(__expf(x)); }
+// log(1 + exp(x)) = max(x, 0) + log1p(e), e = exp(-|x|) in [0, 1], without a branch, two at a time.
+// log1p(e) / e is a polynomial of degree 8 fitted on [0, 1] at Chebyshev points (3e-8 relative, 2.8 U with its
+// fp32 rounding); a small e keeps its relative accuracy.
+__device__ __forceinline__ f2 softplus2(f2 x)
+{
+    const float2 v = unpack2(x);
+    const float2 m = make_float2(fabsf(v.x) * -LOG2E, fabsf(v.y) * -LOG2E);
+    const f2 e = pack2(ex2(m.x), ex2(m.y));
+    const float c[9] = {1.0f, -0.49999502301216125f, 0.33319270610809326f, -0.24844369292259216f, 0.19111430644989014f,
+                        -0.13674770295619965f, 0.07836166769266129f, -0.02958850748836994f, 0.005253457929939032f};
+    f2 p = pack2(c[8], c[8]);
+#pragma unroll
+    for (int k = 7; k >= 0; --k) p = fma2(p, e, pack2(c[k], c[k]));
+    return fma2(p, e, pack2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f)));
+}
+__device__ __forceinline__ float softplus(float x) { return unpack2(softplus2(pack2(x, 0.f))).x; }
 
 __device__ __forceinline__ int row_length(const int *lengths, int b, int N)
 {

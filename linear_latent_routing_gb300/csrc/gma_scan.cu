@@ -73,32 +73,64 @@ __global__ void __launch_bounds__(K::THREADS) scan_forward_kernel(const ScanArgs
     }
     const float skip = a.d_skip && ch < nch ? a.d_skip[c0 + ch] : 0.f;
 
+    // A thread stages the same eight channels of UNITS tokens of every tile, and loads the next tile's
+    // while it works on this one.
+    constexpr int UNITS = K::TL / 8, STEP = K::TT / UNITS;
+    const int piece = threadIdx.x % (K::CH / 8), token = threadIdx.x / (K::CH / 8);
+    const int n8 = min(8, nch - piece * 8), cp = c0 + piece * 8;
+    float bias[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) bias[k] = a.dt_bias && k < n8 ? a.dt_bias[cp + k] : 0.f;
+    Raw8<T> ur[UNITS], dr[UNITS], zr[UNITS];
+    auto fetch = [&](int t0) {
+#pragma unroll
+        for (int j = 0; j < UNITS; ++j) {
+            ur[j].zero();
+            dr[j].zero();
+            const int t = t0 + token + j * STEP;
+            if (VEC && t < len && n8 > 0) {
+                ur[j].load(a.u.at(b, t) + cp);
+                dr[j].load(a.dt.at(b, t) + cp);
+            }
+        }
+    };
+    fetch(0);
+
     for (int t0 = 0; t0 < len; t0 += K::TT) {
         __syncthreads();
         // u and delta of the tile, transposed; zeros behind the last token leave the state alone
-        for (int i = threadIdx.x; i < K::TT * (K::CH / 8); i += K::THREADS) {
-            const int piece = i % (K::CH / 8), t = i / (K::CH / 8), n = min(8, nch - piece * 8);
+#pragma unroll
+        for (int j = 0; j < UNITS; ++j) {
+            const int t = token + j * STEP;
+            const bool on = t0 + t < len && n8 > 0;
             float u[8], d[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) u[k] = d[k] = 0.f;
-            if (t0 + t < len && n > 0) {
-                const int c = c0 + piece * 8;
-                load8<VEC>(a.u.at(b, t0 + t) + c, n, u);
-                load8<VEC>(a.dt.at(b, t0 + t) + c, n, d);
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    d[k] = k < n ? softplus(d[k] + (a.dt_bias ? a.dt_bias[c + k] : 0.f)) : 0.f;
+            if (VEC) {
+                ur[j].get(u);
+                dr[j].get(d);
+            } else {
+                load8<false>(a.u.at(b, t0 + t) + cp, on ? n8 : 0, u);
+                load8<false>(a.dt.at(b, t0 + t) + cp, on ? n8 : 0, d);
             }
             const int at = K::pos(t);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            for (int k = 0; k < 8; k += 2) {
+                const float2 s = unpack2(softplus2(add2(pack2(d[k], d[k + 1]), pack2(bias[k], bias[k + 1]))));
                 us[K::channel(piece * 8 + k) + at] = u[k];
-                dts[K::channel(piece * 8 + k) + at] = d[k];
+                us[K::channel(piece * 8 + k + 1) + at] = u[k + 1];
+                dts[K::channel(piece * 8 + k) + at] = on && k < n8 ? s.x : 0.f;
+                dts[K::channel(piece * 8 + k + 1) + at] = on && k + 1 < n8 ? s.y : 0.f;
             }
         }
         stage_pairs<K, T, VEC>(a.b, b, group * a.S, t0, len, a.S, bs);
         stage_pairs<K, T, VEC>(a.c, b, group * a.S, t0, len, a.S, cs);
         __syncthreads();
+        fetch(t0 + K::TT);
+#pragma unroll
+        for (int j = 0; j < UNITS; ++j) {
+            zr[j].zero();
+            const int t = t0 + token + j * STEP;
+            if (VEC && a.z.p && t < len && n8 > 0) zr[j].load(a.z.at(b, t) + cp);
+        }
 
         {
             float dt[K::TL], u[K::TL];
@@ -157,20 +189,21 @@ __global__ void __launch_bounds__(K::THREADS) scan_forward_kernel(const ScanArgs
             lane_store<K>(us + K::channel(ch), tl, u);
         }
         __syncthreads();
-        for (int i = threadIdx.x; i < K::TT * (K::CH / 8); i += K::THREADS) {
-            const int piece = i % (K::CH / 8), t = i / (K::CH / 8), n = min(8, nch - piece * 8);
-            if (t0 + t >= len || n <= 0) continue;
-            const int c = c0 + piece * 8, at = K::pos(t);
+#pragma unroll
+        for (int j = 0; j < UNITS; ++j) {
+            const int t = token + j * STEP, at = K::pos(t);
+            if (t0 + t >= len || n8 <= 0) continue;
             float y[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) y[k] = us[K::channel(piece * 8 + k) + at];
             if (a.z.p) {
                 float z[8];
-                load8<VEC>(a.z.at(b, t0 + t) + c, n, z);
+                if (VEC) zr[j].get(z);
+                else load8<false>(a.z.at(b, t0 + t) + cp, n8, z);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) y[k] *= silu(z[k]);
             }
-            store8<VEC>(a.y.at(b, t0 + t) + c, n, y);
+            store8<VEC>(a.y.at(b, t0 + t) + cp, n8, y);
         }
     }
     __syncthreads();
@@ -228,7 +261,12 @@ template <typename T, class K, bool VEC> gma_status_t launch_forward(const gma_s
 
 template <typename T, bool VEC> gma_status_t forward_of(const gma_scan_t &s, cudaStream_t st)
 {
-    return launch_forward<T, Tile<16, 8, 8>, VEC>(s, st);
+#ifndef VLT
+#define VLT 16
+#define VTL 8
+#define VW 8
+#endif
+    return launch_forward<T, Tile<VLT, VTL, VW>, VEC>(s, st);
 }
 
 }  // namespace

@@ -82,6 +82,15 @@ __device__ __forceinline__ void stage_pairs(const Rows<const T> &r, int b, int f
     }
 }
 
+// state += decay s, decay *= d where `on`: predicated, so that no selects are needed.
+__device__ __forceinline__ void join(f2 &decay, f2 &state, f2 d, f2 s, bool on)
+{
+    asm("{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %4, 0;\n\t"
+        "@p fma.rn.f32x2 %0, %1, %3, %0;\n\t@p mul.rn.f32x2 %1, %1, %2;\n\t}"
+        : "+l"(state), "+l"(decay)
+        : "l"(d), "l"(s), "r"((int)on));
+}
+
 // Inclusive scan over the time lanes of (decay, state): state_l += decay_l state_{l - off}.
 template <int LT> __device__ __forceinline__ void scan_up(f2 &decay, f2 &state, int tl)
 {
@@ -89,10 +98,7 @@ template <int LT> __device__ __forceinline__ void scan_up(f2 &decay, f2 &state, 
     for (int off = 1; off < LT; off *= 2) {
         const f2 d = __shfl_up_sync(0xffffffffu, decay, off, LT);
         const f2 s = __shfl_up_sync(0xffffffffu, state, off, LT);
-        if (tl >= off) {
-            state = fma2(decay, s, state);
-            decay = mul2(decay, d);
-        }
+        join(decay, state, d, s, tl >= off);
     }
 }
 template <int LT> __device__ __forceinline__ void scan_down(f2 &decay, f2 &state, int tl)
@@ -101,10 +107,7 @@ template <int LT> __device__ __forceinline__ void scan_down(f2 &decay, f2 &state
     for (int off = 1; off < LT; off *= 2) {
         const f2 d = __shfl_down_sync(0xffffffffu, decay, off, LT);
         const f2 s = __shfl_down_sync(0xffffffffu, state, off, LT);
-        if (tl + off < LT) {
-            state = fma2(decay, s, state);
-            decay = mul2(decay, d);
-        }
+        join(decay, state, d, s, tl + off < LT);
     }
 }
 

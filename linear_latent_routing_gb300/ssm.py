@@ -5,13 +5,15 @@ Activations are token-major, [B, N, channels], bf16 or fp32, with contiguous cha
 between tokens and batch rows, so that they can be parts of a wider projection's rows.  Parameters
 and scan states are contiguous fp32.  ``lengths`` (int32 [B] on the device) gives each batch row's number
 of tokens; the rows behind them are neither read nor written (in outputs allocated here they are zero).
+
+``stream`` is the stream to run on (default: the current one).  Nothing here waits for the GPU.
 """
 import ctypes
 
 import torch
 
 from . import _marshal as m
-from ._marshal import F32
+from ._marshal import F32, NO_ROWS, dense, rows, rows4, token, token3
 
 _vp, _sz = ctypes.c_void_p, ctypes.c_size_t
 _scan_forward = m.declare("gma_scan_forward", _vp, _vp, _sz, _vp)
@@ -33,11 +35,7 @@ _conv_grad_t = m.layout(_CONV + "RR2Q")
 
 CHECKPOINT_TOKENS = 128
 GMA_CONV_LINEAR = 0x1
-
-
-def _workspace(size, packed, device):
-    n = size(packed)
-    return (torch.empty(n, dtype=torch.uint8, device=device), n) if n else (None, 0)
+_empty, _zeros, _int32 = torch.empty, torch.zeros, torch.int32
 
 
 def _ptr(t):
@@ -47,32 +45,31 @@ def _ptr(t):
 # ------------------------------------------------------------------ selective scan
 
 def _scan_args(u, dt, a_log, b, c, d_skip, dt_bias, z):
-    """(sizes, packed rows of u, dt, z, b, c, packed parameters) of a call on [B, N, D]."""
-    code = m.code(u, "u")
-    T = u.dtype
-    if u.dim() != 3:
+    """The sizes, rows and parameters of a call on [B, N, D], in the header's order."""
+    T, code, dev = m.first(u, "u")
+    full = u.shape
+    if len(full) != 3:
         raise ValueError("u must be [B, N, D]")
-    B, N, D = u.shape
-    if not isinstance(a_log, torch.Tensor) or a_log.dim() != 2:
-        raise ValueError("a_log must be [D, S]")
-    S = a_log.shape[1]
-    bc = (B, N, S)
-    G = 1
-    if isinstance(b, torch.Tensor) and b.dim() == 4:
+    B, N, D = full
+    S = m.last_dim(a_log, "a_log", 2, "[D, S]")
+    if b is not None and getattr(b, "dim", tuple)() == 4:
         G = b.shape[2]
         bc = (B, N, G, S)
-    rows = m.rows(u, "u", (B, N, D), T, u) + m.rows(m.need(dt, "dt"), "dt", (B, N, D), T, u) + \
-        m.rows(z, "z", (B, N, D), T, u) + m.rows(m.need(b, "b"), "b", bc, T, u) + \
-        m.rows(m.need(c, "c"), "c", bc, T, u)
-    params = (m.dense(a_log, "a_log", (D, S), F32, u), m.dense(d_skip, "d_skip", (D,), F32, u),
-              m.dense(dt_bias, "dt_bias", (D,), F32, u))
-    return (B, N, D, S, G, code), rows, params, bc
+        br, cr = rows4(b, "b", bc, T, dev), rows4(c, "c", bc, T, dev)
+    else:
+        G, bc = 1, (B, N, S)
+        br, cr = rows(b, "b", bc, T, dev), rows(c, "c", bc, T, dev)
+    head = (B, N, D, S, G, code, *rows(u, "u", full, T, dev), *rows(dt, "dt", full, T, dev),
+            *(rows(z, "z", full, T, dev) if z is not None else NO_ROWS), *br, *cr,
+            dense(m.need(a_log, "a_log"), "a_log", (D, S), F32, dev), dense(d_skip, "d_skip", (D,), F32, dev),
+            dense(dt_bias, "dt_bias", (D,), F32, dev))
+    return head, T, dev, full, bc
 
 
 def scan_checkpoints(u, S):
     """An uninitialised buffer for the states that ``scan`` keeps for ``scan_backward``."""
     B, N, D = u.shape
-    return torch.empty(B, -(-N // CHECKPOINT_TOKENS), D, S, dtype=F32, device=u.device)
+    return _empty(B, -(-N // CHECKPOINT_TOKENS), D, S, dtype=F32, device=u.device)
 
 
 def scan(u, dt, a_log, b, c, d_skip=None, dt_bias=None, z=None, state=None, state_out=None, lengths=None,
@@ -84,19 +81,22 @@ def scan(u, dt, a_log, b, c, d_skip=None, dt_bias=None, z=None, state=None, stat
     ``state_out`` takes the one after each row's last token and may be ``state``; ``checkpoints`` (from
     ``scan_checkpoints``) takes what ``scan_backward`` needs.  S is 8, 16, 32 or 64.
     """
-    sizes, rows, params, _ = _scan_args(u, dt, a_log, b, c, d_skip, dt_bias, z)
-    B, N, D, S = sizes[:4]
-    with m.on_stream(stream) as st:
-        if out is None:
-            make = torch.empty if lengths is None else torch.zeros
-            out = make(B, N, D, dtype=u.dtype, device=u.device)
-        packed = _scan_t.pack(
-            *sizes, *rows, *params, m.dense(state, "state", (B, D, S), F32, u),
-            m.dense(state_out, "state_out", (B, D, S), F32, u), m.dense(lengths, "lengths", (B,), torch.int32, u),
-            *m.rows(out, "out", (B, N, D), u.dtype, u),
-            m.dense(checkpoints, "checkpoints", (B, -(-N // CHECKPOINT_TOKENS), D, S), F32, u))
-        ws, n = _workspace(_scan_workspace, packed, u.device)
-        m.call(_scan_forward, packed, _ptr(ws), n, st)
+    if stream is not None:
+        with m.on_stream(stream):
+            return scan(u, dt, a_log, b, c, d_skip, dt_bias, z, state, state_out, lengths, checkpoints, out)
+    head, T, dev, full, _ = _scan_args(u, dt, a_log, b, c, d_skip, dt_bias, z)
+    B, N, D, S = head[:4]
+    if out is None:
+        out = (_empty if lengths is None else _zeros)(full, dtype=T, device=u.device)
+    packed = _scan_t.pack(
+        *head, dense(state, "state", (B, D, S), F32, dev), dense(state_out, "state_out", (B, D, S), F32, dev),
+        dense(lengths, "lengths", (B,), _int32, dev), *rows(out, "out", full, T, dev),
+        dense(checkpoints, "checkpoints", (B, -(-N // CHECKPOINT_TOKENS), D, S), F32, dev))
+    n = _scan_workspace(packed)
+    ws = _empty(n, dtype=torch.uint8, device=u.device) if n else None
+    r = _scan_forward(packed, _ptr(ws), n, m.handle(dev))
+    if r:
+        m.failed(r, "gma_scan_forward")
     return out
 
 
@@ -105,27 +105,32 @@ def scan_step(u, dt, a_log, b, c, state, d_skip=None, dt_bias=None, z=None, out=
 
     u, dt and z [B, D], b and c [B, S] or [B, G, S]; parameters as in ``scan``.
     """
-    code = m.code(u, "u")
-    T = u.dtype
-    if u.dim() != 2:
+    if stream is not None:
+        with m.on_stream(stream):
+            return scan_step(u, dt, a_log, b, c, state, d_skip, dt_bias, z, out)
+    T, code, dev = m.first(u, "u")
+    full = u.shape
+    if len(full) != 2:
         raise ValueError("u must be [B, D]")
-    B, D = u.shape
-    if not isinstance(a_log, torch.Tensor) or a_log.dim() != 2:
-        raise ValueError("a_log must be [D, S]")
-    S = a_log.shape[1]
-    G = b.shape[1] if isinstance(b, torch.Tensor) and b.dim() == 3 else 1
-    bc = (B, 1, G, S) if isinstance(b, torch.Tensor) and b.dim() == 3 else (B, 1, S)
-    with m.on_stream(stream) as st:
-        if out is None:
-            out = torch.empty(B, D, dtype=T, device=u.device)
-        h = m.dense(m.need(state, "state"), "state", (B, D, S), F32, u)
-        packed = _scan_t.pack(
-            B, 1, D, S, G, code, *m.token(u, "u", (B, 1, D), T, u), *m.token(m.need(dt, "dt"), "dt", (B, 1, D), T, u),
-            *m.token(z, "z", (B, 1, D), T, u), *m.token(m.need(b, "b"), "b", bc, T, u),
-            *m.token(m.need(c, "c"), "c", bc, T, u), m.dense(a_log, "a_log", (D, S), F32, u),
-            m.dense(d_skip, "d_skip", (D,), F32, u), m.dense(dt_bias, "dt_bias", (D,), F32, u), h, h, 0,
-            *m.token(out, "out", (B, 1, D), T, u), 0)
-        m.call(_scan_step, packed, st)
+    B, D = full
+    S = m.last_dim(a_log, "a_log", 2, "[D, S]")
+    if b is not None and getattr(b, "dim", tuple)() == 3:
+        G = b.shape[1]
+        br, cr = token3(b, "b", (B, G, S), T, dev), token3(c, "c", (B, G, S), T, dev)
+    else:
+        G = 1
+        br, cr = token(b, "b", (B, S), T, dev), token(c, "c", (B, S), T, dev)
+    if out is None:
+        out = _empty(full, dtype=T, device=u.device)
+    h = dense(m.need(state, "state"), "state", (B, D, S), F32, dev)
+    packed = _scan_t.pack(
+        B, 1, D, S, G, code, *token(u, "u", full, T, dev), *token(dt, "dt", full, T, dev),
+        *(token(z, "z", full, T, dev) if z is not None else NO_ROWS), *br, *cr,
+        dense(a_log, "a_log", (D, S), F32, dev), dense(d_skip, "d_skip", (D,), F32, dev),
+        dense(dt_bias, "dt_bias", (D,), F32, dev), h, h, 0, *token(out, "out", full, T, dev), 0)
+    r = _scan_step(packed, m.handle(dev))
+    if r:
+        m.failed(r, "gma_scan_step")
     return out
 
 
@@ -138,82 +143,92 @@ def scan_backward(dy, u, dt, a_log, b, c, checkpoints, d_skip=None, dt_bias=None
     is) and "state" (of the state before the first token) in fp32.  ``out`` may hold tensors, under
     the names "u", "dt", "z", "b" and "c", that take those gradients (rows with strides).
     """
-    sizes, rows, params, bc = _scan_args(u, dt, a_log, b, c, d_skip, dt_bias, z)
-    B, N, D, S = sizes[:4]
-    T, dev = u.dtype, u.device
-    full = (B, N, D)
-    kept = m.dense(m.need(checkpoints, "checkpoints"), "checkpoints", (B, -(-N // CHECKPOINT_TOKENS), D, S), F32, u)
-    with m.on_stream(stream) as st:
-        make = torch.empty if lengths is None else torch.zeros
+    if stream is not None:
+        with m.on_stream(stream):
+            return scan_backward(dy, u, dt, a_log, b, c, checkpoints, d_skip, dt_bias, z, dstate_out, lengths, out)
+    head, T, dev, full, bc = _scan_args(u, dt, a_log, b, c, d_skip, dt_bias, z)
+    B, N, D, S = head[:4]
+    device = u.device
+    kept = dense(m.need(checkpoints, "checkpoints"), "checkpoints", (B, -(-N // CHECKPOINT_TOKENS), D, S), F32, dev)
+    make = _empty if lengths is None else _zeros
 
-        def new(shape):
-            return make(shape, dtype=T, device=dev)
+    def new(shape):
+        return make(shape, dtype=T, device=device)
 
-        g = {"u": m.given(out, "u", lambda: new(full)), "dt": m.given(out, "dt", lambda: new(full)),
-             "z": m.given(out, "z", lambda: new(full)) if z is not None else None,
-             "b": m.given(out, "b", lambda: new(bc)), "c": m.given(out, "c", lambda: new(bc)),
-             "a_log": torch.empty_like(a_log), "d_skip": torch.empty_like(d_skip) if d_skip is not None else None,
-             "dt_bias": torch.empty_like(dt_bias) if dt_bias is not None else None,
-             "state": torch.empty(B, D, S, dtype=F32, device=dev)}
-        packed = _scan_grad_t.pack(
-            *sizes, *rows, *params, 0, 0, m.dense(lengths, "lengths", (B,), torch.int32, u), *m.NO_ROWS, kept,
-            *m.rows(m.need(dy, "dy"), "dy", full, T, u), m.dense(dstate_out, "dstate_out", (B, D, S), F32, u),
-            *m.rows(g["u"], "out['u']", full, T, u), *m.rows(g["dt"], "out['dt']", full, T, u),
-            *m.rows(g["z"], "out['z']", full, T, u), *m.rows(g["b"], "out['b']", bc, T, u),
-            *m.rows(g["c"], "out['c']", bc, T, u), g["a_log"].data_ptr(), _ptr(g["d_skip"]), _ptr(g["dt_bias"]),
-            g["state"].data_ptr())
-        ws, n = _workspace(_scan_backward_workspace, packed, dev)
-        m.call(_scan_backward, packed, _ptr(ws), n, st)
+    g = {"u": m.given(out, "u", lambda: new(full)), "dt": m.given(out, "dt", lambda: new(full)),
+         "z": m.given(out, "z", lambda: new(full)) if z is not None else None,
+         "b": m.given(out, "b", lambda: new(bc)), "c": m.given(out, "c", lambda: new(bc)),
+         "a_log": torch.empty_like(a_log), "d_skip": torch.empty_like(d_skip) if d_skip is not None else None,
+         "dt_bias": torch.empty_like(dt_bias) if dt_bias is not None else None,
+         "state": _empty(B, D, S, dtype=F32, device=device)}
+    of_bc = rows4 if len(bc) == 4 else rows
+    packed = _scan_grad_t.pack(
+        *head, 0, 0, dense(lengths, "lengths", (B,), _int32, dev), *NO_ROWS, kept, *rows(dy, "dy", full, T, dev),
+        dense(dstate_out, "dstate_out", (B, D, S), F32, dev), *rows(g["u"], "out['u']", full, T, dev),
+        *rows(g["dt"], "out['dt']", full, T, dev), *(rows(g["z"], "out['z']", full, T, dev) if z is not None else NO_ROWS),
+        *of_bc(g["b"], "out['b']", bc, T, dev), *of_bc(g["c"], "out['c']", bc, T, dev), g["a_log"].data_ptr(),
+        _ptr(g["d_skip"]), _ptr(g["dt_bias"]), g["state"].data_ptr())
+    n = _scan_backward_workspace(packed)
+    ws = _empty(n, dtype=torch.uint8, device=device) if n else None
+    r = _scan_backward(packed, _ptr(ws), n, m.handle(dev))
+    if r:
+        m.failed(r, "gma_scan_backward")
     return g
 
 
 # ------------------------------------------------------------------ short causal convolution
-
-def _conv_shape(x, weight, dims):
-    code = m.code(x, "x")
-    if x.dim() != dims:
-        raise ValueError("x must be [B, N, D]" if dims == 3 else "x must be [B, D]")
-    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
-        raise ValueError("weight must be [D, W]")
-    return code, weight.shape[1]
-
 
 def conv(x, weight, bias=None, state=None, state_out=None, lengths=None, silu=True, out=None, stream=None):
     """Short causal convolution per channel, with silu unless ``silu`` is False; returns y [B, N, D].
 
     x [B, N, D]; weight [D, W] (W = 2, 3, 4, the last tap on the current token) and bias [D] fp32; ``state``
     [B, W - 1, D] holds the inputs before the first token, oldest first (zeros if None), and
-    ``state_out`` takes the last W - 1 inputs of each row.
+    ``state_out`` takes the last W - 1 inputs of each row (not in place).
     """
-    code, W = _conv_shape(x, weight, 3)
-    B, N, D = x.shape
-    T, past = x.dtype, (B, W - 1, D)
-    with m.on_stream(stream) as st:
-        if out is None:
-            out = (torch.empty if lengths is None else torch.zeros)(B, N, D, dtype=T, device=x.device)
-        packed = _conv_t.pack(
-            B, N, D, W, code, 0 if silu else GMA_CONV_LINEAR, *m.rows(x, "x", (B, N, D), T, x),
-            m.dense(weight, "weight", (D, W), F32, x), m.dense(bias, "bias", (D,), F32, x),
-            m.dense(state, "state", past, T, x), m.dense(state_out, "state_out", past, T, x),
-            m.dense(lengths, "lengths", (B,), torch.int32, x), *m.rows(out, "out", (B, N, D), T, x))
-        m.call(_conv_forward, packed, st)
+    if stream is not None:
+        with m.on_stream(stream):
+            return conv(x, weight, bias, state, state_out, lengths, silu, out)
+    T, code, dev = m.first(x, "x")
+    full = x.shape
+    if len(full) != 3:
+        raise ValueError("x must be [B, N, D]")
+    B, N, D = full
+    W = m.last_dim(weight, "weight", 2, "[D, W]")
+    past = (B, W - 1, D)
+    if out is None:
+        out = (_empty if lengths is None else _zeros)(full, dtype=T, device=x.device)
+    packed = _conv_t.pack(
+        B, N, D, W, code, 0 if silu else GMA_CONV_LINEAR, *rows(x, "x", full, T, dev),
+        dense(weight, "weight", (D, W), F32, dev), dense(bias, "bias", (D,), F32, dev),
+        dense(state, "state", past, T, dev), dense(state_out, "state_out", past, T, dev),
+        dense(lengths, "lengths", (B,), _int32, dev), *rows(out, "out", full, T, dev))
+    r = _conv_forward(packed, m.handle(dev))
+    if r:
+        m.failed(r, "gma_conv_forward")
     return out
 
 
 def conv_step(x, weight, bias, state, silu=True, out=None, stream=None):
     """One token for every sequence; returns y [B, D] and moves ``state`` [B, W - 1, D] on in place."""
-    code, W = _conv_shape(x, weight, 2)
-    B, D = x.shape
-    T = x.dtype
-    with m.on_stream(stream) as st:
-        if out is None:
-            out = torch.empty(B, D, dtype=T, device=x.device)
-        h = m.dense(m.need(state, "state"), "state", (B, W - 1, D), T, x)
-        packed = _conv_t.pack(
-            B, 1, D, W, code, 0 if silu else GMA_CONV_LINEAR, *m.token(x, "x", (B, 1, D), T, x),
-            m.dense(weight, "weight", (D, W), F32, x), m.dense(bias, "bias", (D,), F32, x), h, h, 0,
-            *m.token(out, "out", (B, 1, D), T, x))
-        m.call(_conv_step, packed, st)
+    if stream is not None:
+        with m.on_stream(stream):
+            return conv_step(x, weight, bias, state, silu, out)
+    T, code, dev = m.first(x, "x")
+    full = x.shape
+    if len(full) != 2:
+        raise ValueError("x must be [B, D]")
+    B, D = full
+    W = m.last_dim(weight, "weight", 2, "[D, W]")
+    if out is None:
+        out = _empty(full, dtype=T, device=x.device)
+    h = dense(m.need(state, "state"), "state", (B, W - 1, D), T, dev)
+    packed = _conv_t.pack(
+        B, 1, D, W, code, 0 if silu else GMA_CONV_LINEAR, *token(x, "x", full, T, dev),
+        dense(weight, "weight", (D, W), F32, dev), dense(bias, "bias", (D,), F32, dev), h, h, 0,
+        *token(out, "out", full, T, dev))
+    r = _conv_step(packed, m.handle(dev))
+    if r:
+        m.failed(r, "gma_conv_step")
     return out
 
 
@@ -222,19 +237,26 @@ def conv_backward(dy, x, weight, bias=None, state=None, lengths=None, silu=True,
 
     Returns a dict: "x" in x's dtype (into ``out`` if given), "weight" and "bias" (None without one) in fp32.
     """
-    code, W = _conv_shape(x, weight, 3)
-    B, N, D = x.shape
-    T = x.dtype
-    with m.on_stream(stream) as st:
-        if out is None:
-            out = (torch.empty if lengths is None else torch.zeros)(B, N, D, dtype=T, device=x.device)
-        g = {"x": out, "weight": torch.empty_like(weight), "bias": torch.empty_like(bias) if bias is not None else None}
-        packed = _conv_grad_t.pack(
-            B, N, D, W, code, 0 if silu else GMA_CONV_LINEAR, *m.rows(x, "x", (B, N, D), T, x),
-            m.dense(weight, "weight", (D, W), F32, x), m.dense(bias, "bias", (D,), F32, x),
-            m.dense(state, "state", (B, W - 1, D), T, x), 0, m.dense(lengths, "lengths", (B,), torch.int32, x),
-            *m.NO_ROWS, *m.rows(m.need(dy, "dy"), "dy", (B, N, D), T, x), *m.rows(out, "out", (B, N, D), T, x),
-            g["weight"].data_ptr(), _ptr(g["bias"]))
-        ws, n = _workspace(_conv_backward_workspace, packed, x.device)
-        m.call(_conv_backward, packed, _ptr(ws), n, st)
+    if stream is not None:
+        with m.on_stream(stream):
+            return conv_backward(dy, x, weight, bias, state, lengths, silu, out)
+    T, code, dev = m.first(x, "x")
+    full = x.shape
+    if len(full) != 3:
+        raise ValueError("x must be [B, N, D]")
+    B, N, D = full
+    W = m.last_dim(weight, "weight", 2, "[D, W]")
+    if out is None:
+        out = (_empty if lengths is None else _zeros)(full, dtype=T, device=x.device)
+    g = {"x": out, "weight": torch.empty_like(weight), "bias": torch.empty_like(bias) if bias is not None else None}
+    packed = _conv_grad_t.pack(
+        B, N, D, W, code, 0 if silu else GMA_CONV_LINEAR, *rows(x, "x", full, T, dev),
+        dense(weight, "weight", (D, W), F32, dev), dense(bias, "bias", (D,), F32, dev),
+        dense(state, "state", (B, W - 1, D), T, dev), 0, dense(lengths, "lengths", (B,), _int32, dev), *NO_ROWS,
+        *rows(dy, "dy", full, T, dev), *rows(out, "out", full, T, dev), g["weight"].data_ptr(), _ptr(g["bias"]))
+    n = _conv_backward_workspace(packed)
+    ws = _empty(n, dtype=torch.uint8, device=x.device) if n else None
+    r = _conv_backward(packed, _ptr(ws), n, m.handle(dev))
+    if r:
+        m.failed(r, "gma_conv_backward")
     return g
