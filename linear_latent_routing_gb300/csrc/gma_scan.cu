@@ -284,7 +284,10 @@ size_t gma_scan_checkpoint_size(const gma_scan_t *s)
     return (size_t)s->B * ((s->N + CKPT - 1) / CKPT) * s->D * s->S * sizeof(float);
 }
 
-size_t gma_scan_workspace_size(const gma_scan_t *) { return 0; }
+size_t gma_scan_workspace_size(const gma_scan_t *s)
+{
+    return scan_check(s, false) == GMA_OK && scan_chunked(*s) ? scan_chunk_workspace(*s) : 0;
+}
 
 gma_status_t gma_scan_forward(const gma_scan_t *s, void *ws, size_t ws_bytes, gma_stream_t stream)
 {
@@ -293,6 +296,7 @@ gma_status_t gma_scan_forward(const gma_scan_t *s, void *ws, size_t ws_bytes, gm
     if (!ws_ok(ws, ws_bytes, gma_scan_workspace_size(s))) return GMA_ERR_WORKSPACE;
     if ((r = usable_device()) != GMA_OK) return r;
     cudaStream_t st = (cudaStream_t)stream;
+    if (scan_chunked(*s)) return scan_chunk_forward(*s, ws, st);
     const bool vec = scan_vec(*s) && rows_vec(s->y, s->dtype);
     if (s->dtype == GMA_BF16)
         return vec ? forward_of<__nv_bfloat16, true>(*s, st) : forward_of<__nv_bfloat16, false>(*s, st);

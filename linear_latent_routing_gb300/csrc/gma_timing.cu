@@ -68,6 +68,8 @@ const char *kernel_name(int id)
     case KID_NORM: return "norm_forward";
     case KID_NORM_BWD: return "norm_backward";
     case KID_SUM_ROWS: return "sum_rows";
+    case KID_SCAN_STATE: return "scan_chunk_state";
+    case KID_SCAN_JOIN: return "scan_chunk_join";
     }
     return "unknown";
 }

@@ -139,5 +139,10 @@ gma_status_t scan_check(const gma_scan_t *s, bool out);
 // 16-byte accesses to the rows of u, dt, z, b and c.
 bool scan_vec(const gma_scan_t &s);
 
+// The forward pass in chunks of tokens: whether it takes this call, its workspace, the call.
+bool scan_chunked(const gma_scan_t &s);
+size_t scan_chunk_workspace(const gma_scan_t &s);
+gma_status_t scan_chunk_forward(const gma_scan_t &s, void *ws, cudaStream_t st);
+
 }  // namespace blk
 }  // namespace gma
