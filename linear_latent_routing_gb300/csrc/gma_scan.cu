@@ -262,7 +262,7 @@ template <typename T, class K, bool VEC> gma_status_t launch_forward(const gma_s
 template <typename T, bool VEC> gma_status_t forward_of(const gma_scan_t &s, cudaStream_t st)
 {
 #ifndef VLT
-#define VLT 16
+#define VLT 32
 #define VTL 8
 #define VW 8
 #endif

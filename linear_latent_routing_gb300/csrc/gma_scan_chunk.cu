@@ -1,26 +1,31 @@
 // gma_scan_chunk.cu -- the selective scan's forward pass in chunks of tokens, for states of up to 16.
 //
-// Lanes are channels (two a lane, whose u, dt, z and y are one 4-byte access), every warp walks over the
-// tokens of one chunk with the 2 * S states in registers, and nothing is exchanged between lanes.
+// Lanes are channels, every warp walks over the tokens of one chunk with its states in registers, and
+// nothing but y is exchanged between lanes: a lane holds 32 states, of two channels (S <= 16, whose u, dt, z
+// and y are one access) or of one; with S = 64 two lanes share a channel.
 // The sequence is cut into chunks so that short batches fill the GPU too:
 //   1. scan_chunk_state: each chunk's state from a zero start, and its sum of delta;
 //   2. scan_chunk_join: over the chunks in order, state = exp(A sum delta) state + chunk's state;
 //      what is in front of each chunk is its start (and a checkpoint for the backward pass);
 //   3. scan_chunk_output: each chunk again from its start, with the output.
 // One chunk needs step 3 alone.  Per (token, channel, state) steps 1 and 3 take two exponentials
-// and about six instruction slots, of which the exponentials bind (one warp instruction in four cycles
-// a scheduler).
+// (of 32 a clock and SM) and three and a half packed fp32 instructions; instruction issue binds.
 #include "scan_tile.cuh"
 
 namespace gma {
 namespace blk {
 namespace {
 
-constexpr int CH_WARP = 64;          // channels of a warp
+template <int S> struct Lanes {
+    static constexpr int CPL = S <= 16 ? 2 : 1;              // channels of a lane
+    static constexpr int SL = S <= 32 ? S : 32;              // its states of each
+    static constexpr int SPLIT = S / SL;                     // lanes of a channel
+    static constexpr int CH_WARP = 32 * CPL / SPLIT;         // channels of a warp
+};
 constexpr int STAGES = 3;            // of a warp's ring of staged tokens
 
 // Tokens of a stage: 1 KB of each of u, dt and z.
-template <typename T> constexpr int stage_tokens() { return 1024 / (CH_WARP * (int)sizeof(T)); }
+template <typename T, int S> constexpr int stage_tokens() { return 1024 / (Lanes<S>::CH_WARP * (int)sizeof(T)); }
 constexpr int STAGE_BYTES = 3 * 1024;
 constexpr int RING_BYTES = STAGES * STAGE_BYTES;
 
@@ -38,46 +43,36 @@ template <typename T> struct ChunkArgs {
     float *total;                    // [B][chunks][D]: sums of delta
 };
 
-// Two neighbouring channels of a token, as they lie in memory until they are used.
-template <typename T> struct Raw2;
-template <> struct Raw2<__nv_bfloat16> {
-    uint32_t w;
-    template <bool VEC> __device__ __forceinline__ void load(const __nv_bfloat16 *p, int n)
-    {
-        if (VEC) {
-            w = *reinterpret_cast<const uint32_t *>(p);
-        } else {
-            const unsigned short *q = reinterpret_cast<const unsigned short *>(p);
-            w = (n > 0 ? q[0] : 0u) | (n > 1 ? (uint32_t)q[1] << 16 : 0u);
-        }
-    }
-    __device__ __forceinline__ float2 get() const { return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }
-};
-template <> struct Raw2<float> {
-    float2 w;
-    template <bool VEC> __device__ __forceinline__ void load(const float *p, int n)
-    {
-        if (VEC) w = *reinterpret_cast<const float2 *>(p);
-        else w = make_float2(n > 0 ? p[0] : 0.f, n > 1 ? p[1] : 0.f);
-    }
-    __device__ __forceinline__ float2 get() const { return w; }
-};
-template <bool VEC> __device__ __forceinline__ void store2(__nv_bfloat16 *p, int n, float2 v)
+// One or two (CPL) neighbouring channels of a token, of which n exist.
+template <int CPL, bool VEC> __device__ __forceinline__ float2 load_ch(const __nv_bfloat16 *p, int n)
 {
-    if (VEC) {
+    if (CPL == 2 && VEC) {
+        const uint32_t w = *reinterpret_cast<const uint32_t *>(p);
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    }
+    return make_float2(VEC || n > 0 ? __bfloat162float(p[0]) : 0.f, CPL == 2 && n > 1 ? __bfloat162float(p[1]) : 0.f);
+}
+template <int CPL, bool VEC> __device__ __forceinline__ float2 load_ch(const float *p, int n)
+{
+    if (CPL == 2 && VEC) return *reinterpret_cast<const float2 *>(p);
+    return make_float2(VEC || n > 0 ? p[0] : 0.f, CPL == 2 && n > 1 ? p[1] : 0.f);
+}
+template <int CPL, bool VEC> __device__ __forceinline__ void store_ch(__nv_bfloat16 *p, int n, float2 v)
+{
+    if (CPL == 2 && VEC) {
         *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(v.x, v.y);
     } else {
-        if (n > 0) p[0] = __float2bfloat16_rn(v.x);
-        if (n > 1) p[1] = __float2bfloat16_rn(v.y);
+        p[0] = __float2bfloat16_rn(v.x);
+        if (CPL == 2 && n > 1) p[1] = __float2bfloat16_rn(v.y);
     }
 }
-template <bool VEC> __device__ __forceinline__ void store2(float *p, int n, float2 v)
+template <int CPL, bool VEC> __device__ __forceinline__ void store_ch(float *p, int n, float2 v)
 {
-    if (VEC) {
+    if (CPL == 2 && VEC) {
         *reinterpret_cast<float2 *>(p) = v;
     } else {
-        if (n > 0) p[0] = v.x;
-        if (n > 1) p[1] = v.y;
+        p[0] = v.x;
+        if (CPL == 2 && n > 1) p[1] = v.y;
     }
 }
 
@@ -94,7 +89,7 @@ __device__ __forceinline__ void stage_rows(const Rows<const T> &r, bool vec, int
     }
 }
 
-// The states' rates A log2(e), S / 2 pairs.
+// A lane's states' rates A log2(e), in pairs.
 template <int S> __device__ __forceinline__ void load_rates(const float *a_log, long long at, bool on, f2 (&r)[S / 2])
 {
 #pragma unroll
@@ -125,65 +120,73 @@ template <int S> __device__ __forceinline__ void store_state(float *p, bool on, 
 template <typename T, int S, bool VEC, bool OUT>
 __global__ void __launch_bounds__(256, 2) scan_chunk_kernel(const ChunkArgs<T> g, bool vec_bc)
 {
+    constexpr int CPL = Lanes<S>::CPL, SL = Lanes<S>::SL, SPLIT = Lanes<S>::SPLIT, CH_WARP = Lanes<S>::CH_WARP;
     extern __shared__ __align__(16) float rows_s[];
     const ScanArgs<T> &a = g.s;
     const int b = blockIdx.z, k = blockIdx.y, t0 = k * g.chunk;
     const int len = row_length(a.lengths, b, a.N);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = SPLIT == 2 ? lane >> 4 : 0;
     const int group = blockIdx.x / a.tiles, Dg = a.D / a.G;
-    const int in_group = (blockIdx.x - group * a.tiles) * (blockDim.x * 2) + threadIdx.x * 2;
-    const int n = min(2, Dg - in_group), c = group * Dg + in_group;
+    const int warp_ch = ((blockIdx.x - group * a.tiles) * (blockDim.x / 32) + warp) * CH_WARP;   // in the group
+    const int in_group = warp_ch + (SPLIT == 2 ? lane & 15 : lane * CPL);
+    const int n = max(0, min(CPL, Dg - in_group)), c = group * Dg + in_group;
     const int count = min(g.chunk, len - t0);
     const bool only = g.chunks == 1;
+    const long long in_b = ((long long)b * a.D + c) * S + part * SL;      // states of this lane in [B][D][S]
     if (count <= 0) {
         // an empty sequence's state passes through
-        if (OUT && only && a.state_out && a.state_out != a.state_in)
+        if (OUT && k == 0 && a.state_out && a.state_out != a.state_in && only)
             for (int e = 0; e < n; ++e)
-                for (int i = 0; i < S; ++i) {
-                    const long long at = ((long long)b * a.D + c + e) * S + i;
-                    a.state_out[at] = a.state_in ? a.state_in[at] : 0.f;
-                }
+                for (int i = 0; i < SL; ++i)
+                    a.state_out[in_b + e * S + i] = a.state_in ? a.state_in[in_b + e * S + i] : 0.f;
         return;
     }
     float *bs = rows_s, *cs = rows_s + g.chunk * S;
     stage_rows<T, S>(a.b, vec_bc, b, group * S, t0, count, bs);
     if (OUT) stage_rows<T, S>(a.c, vec_bc, b, group * S, t0, count, cs);
+    bs += part * SL;
+    cs += part * SL;
 
-    f2 r[2][S / 2], h[2][S / 2];
+    f2 r[CPL][SL / 2], h[CPL][SL / 2];
     float2 bias = make_float2(0.f, 0.f), skip = make_float2(0.f, 0.f), total = make_float2(0.f, 0.f);
     const long long row = ((long long)b * g.chunks + k) * a.D + c;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
+    for (int e = 0; e < CPL; ++e) {
         const bool on = e < n;
-        load_rates<S>(a.a_log, (long long)(c + e) * S, on, r[e]);
-        if (OUT && !only) load_state<S>(g.state + (row + e) * S, on, h[e]);
-        else if (OUT && a.state_in) load_state<S>(a.state_in + ((long long)b * a.D + c + e) * S, on, h[e]);
-        else load_state<S>(nullptr, false, h[e]);
-        if (OUT && only && a.ckpt) store_state<S>(a.ckpt + ((long long)b * a.D + c + e) * S, on, h[e]);
+        load_rates<SL>(a.a_log, (long long)(c + e) * S + part * SL, on, r[e]);
+        if (OUT && !only) load_state<SL>(g.state + (row + e) * S + part * SL, on, h[e]);
+        else if (OUT && a.state_in) load_state<SL>(a.state_in + in_b + e * S, on, h[e]);
+        else load_state<SL>(nullptr, false, h[e]);
+        if (OUT && only && a.ckpt) store_state<SL>(a.ckpt + in_b + e * S, on, h[e]);
     }
     if (n > 0 && a.dt_bias) bias.x = a.dt_bias[c];
     if (n > 1 && a.dt_bias) bias.y = a.dt_bias[c + 1];
     if (OUT && n > 0 && a.d_skip) skip.x = a.d_skip[c];
     if (OUT && n > 1 && a.d_skip) skip.y = a.d_skip[c + 1];
     __syncthreads();
-    if (!VEC && n <= 0) return;
 
     T *yp = OUT ? a.y.at(b, t0) + c : nullptr;
     auto token = [&](int t, float2 uu, float2 dd, float2 zz) {
         const float2 dt = unpack2(softplus2(add2(pack2(dd.x, dd.y), pack2(bias.x, bias.y))));
-        const float2 xu = make_float2(dt.x * uu.x, dt.y * uu.y);
-        f2 y[2] = {0ull, 0ull};
-        const f2 dt2[2] = {pack2(dt.x, dt.x), pack2(dt.y, dt.y)}, xu2[2] = {pack2(xu.x, xu.x), pack2(xu.y, xu.y)};
+        const float de[2] = {dt.x, dt.y}, xe[2] = {dt.x * uu.x, dt.y * uu.y};
+        f2 y[CPL], dt2[CPL], xu2[CPL];
+#pragma unroll
+        for (int e = 0; e < CPL; ++e) {
+            y[e] = 0ull;
+            dt2[e] = pack2(de[e], de[e]);
+            xu2[e] = pack2(xe[e], xe[e]);
+        }
         if (!OUT) {
             total.x += dt.x;
             total.y += dt.y;
         }
 #pragma unroll
-        for (int q = 0; q < S / 4; ++q) {
+        for (int q = 0; q < SL / 4; ++q) {
             const ulonglong2 b2 = reinterpret_cast<const ulonglong2 *>(bs + t * S)[q];
             ulonglong2 c2;
             if (OUT) c2 = reinterpret_cast<const ulonglong2 *>(cs + t * S)[q];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+            for (int e = 0; e < CPL; ++e) {
                 h[e][2 * q] = fma2(ex2_2(mul2(dt2[e], r[e][2 * q])), h[e][2 * q], mul2(xu2[e], b2.x));
                 h[e][2 * q + 1] = fma2(ex2_2(mul2(dt2[e], r[e][2 * q + 1])), h[e][2 * q + 1], mul2(xu2[e], b2.y));
                 if (OUT) {
@@ -193,23 +196,26 @@ __global__ void __launch_bounds__(256, 2) scan_chunk_kernel(const ChunkArgs<T> g
             }
         }
         if (OUT) {
-            const float2 y0 = unpack2(y[0]), y1 = unpack2(y[1]);
-            float2 v = make_float2(fmaf(skip.x, uu.x, y0.x + y0.y), fmaf(skip.y, uu.y, y1.x + y1.y));
+            const float2 y0 = unpack2(y[0]), y1 = CPL == 2 ? unpack2(y[CPL - 1]) : make_float2(0.f, 0.f);
+            float2 v = make_float2(y0.x + y0.y, y1.x + y1.y);
+            if (SPLIT == 2) v.x += __shfl_xor_sync(0xffffffffu, v.x, 16);
+            v.x = fmaf(skip.x, uu.x, v.x);
+            v.y = fmaf(skip.y, uu.y, v.y);
             if (a.z.p) {
                 v.x *= silu(zz.x);
-                v.y *= silu(zz.y);
+                if (CPL == 2) v.y *= silu(zz.y);
             }
-            if (!VEC || n > 0) store2<VEC>(yp, n, v);
+            if (n > 0 && part == 0) store_ch<CPL, VEC>(yp, n, v);
             yp += a.y.st;
         }
     };
     if (VEC) {
-        // A warp fetches its 64 channels of a stage's tokens, 16 bytes a lane, two stages ahead.
-        constexpr int TOK = stage_tokens<T>(), ROW = CH_WARP * sizeof(T), SEGS = ROW / 16, PER = 32 / SEGS;
-        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, seg = lane % SEGS, sub = lane / SEGS;
+        // A warp fetches its channels of a stage's tokens, 16 bytes a lane, two stages ahead.
+        constexpr int TOK = stage_tokens<T, S>(), ROW = CH_WARP * (int)sizeof(T), SEGS = ROW / 16, PER = 32 / SEGS;
+        const int seg = lane % SEGS, sub = lane / SEGS;
         unsigned char *ring = reinterpret_cast<unsigned char *>(rows_s) + ((OUT ? 2 : 1) * g.chunk * S * 4) + warp * RING_BYTES;
         const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
-        const int first = in_group - 2 * lane + seg * (16 / (int)sizeof(T));          // channel in the group
+        const int first = warp_ch + seg * (16 / (int)sizeof(T));
         const bool mine = first < Dg;
         const T *up = a.u.at(b, t0) + group * Dg + first, *dp = a.dt.at(b, t0) + group * Dg + first;
         const T *zp = OUT && a.z.p ? a.z.at(b, t0) + group * Dg + first : nullptr;
@@ -233,87 +239,84 @@ __global__ void __launch_bounds__(256, 2) scan_chunk_kernel(const ChunkArgs<T> g
             cp_wait<STAGES - 2>();
             __syncwarp();
             fetch(at + 2 * TOK, stage == 0 ? 2 : stage - 1);
-            const unsigned char *s = ring + stage * STAGE_BYTES + lane * 2 * sizeof(T);
+            const T *s = reinterpret_cast<const T *>(ring + stage * STAGE_BYTES) + (in_group - warp_ch);
+            const int m = min(TOK, count - at);
 #pragma unroll 2
-            for (int i = 0; i < TOK; ++i) {
-                if (at + i >= count) break;
-                Raw2<T> u, d, z;
-                u.template load<true>(reinterpret_cast<const T *>(s + i * ROW), 2);
-                d.template load<true>(reinterpret_cast<const T *>(s + i * ROW + 1024), 2);
-                if (OUT) z.template load<true>(reinterpret_cast<const T *>(s + i * ROW + 2048), 2);
-                token(at + i, u.get(), d.get(), OUT ? z.get() : make_float2(0.f, 0.f));
+            for (int i = 0; i < m; ++i) {
+                const T *p = s + i * CH_WARP;
+                const float2 z = OUT ? load_ch<CPL, true>(p + 2048 / (int)sizeof(T), CPL) : make_float2(0.f, 0.f);
+                token(at + i, load_ch<CPL, true>(p, CPL), load_ch<CPL, true>(p + 1024 / (int)sizeof(T), CPL), z);
             }
             stage = stage == 2 ? 0 : stage + 1;
         }
     } else {
-        for (int t = 0; t < count; ++t) {
-            Raw2<T> u, d, z;
-            u.template load<false>(a.u.at(b, t0 + t) + c, n);
-            d.template load<false>(a.dt.at(b, t0 + t) + c, n);
-            if (OUT && a.z.p) z.template load<false>(a.z.at(b, t0 + t) + c, n);
-            token(t, u.get(), d.get(), OUT && a.z.p ? z.get() : make_float2(0.f, 0.f));
-        }
+        const T *up = a.u.at(b, t0) + c, *dp = a.dt.at(b, t0) + c, *zp = OUT && a.z.p ? a.z.at(b, t0) + c : nullptr;
+        for (int t = 0; t < count; ++t)
+            token(t, load_ch<CPL, false>(up + t * a.u.st, n), load_ch<CPL, false>(dp + t * a.dt.st, n),
+                  zp ? load_ch<CPL, false>(zp + t * a.z.st, n) : make_float2(0.f, 0.f));
     }
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
+    for (int e = 0; e < CPL; ++e) {
         if (!OUT) {
-            store_state<S>(g.state + (row + e) * S, e < n, h[e]);
-            if (e < n) g.total[row + e] = e ? total.y : total.x;
+            store_state<SL>(g.state + (row + e) * S + part * SL, e < n, h[e]);
+            if (e < n && part == 0) g.total[row + e] = e ? total.y : total.x;
         } else if (only && a.state_out) {
-            store_state<S>(a.state_out + ((long long)b * a.D + c + e) * S, e < n, h[e]);
+            store_state<SL>(a.state_out + in_b + e * S, e < n, h[e]);
         }
     }
 }
 
-// Step 2: four states a thread, the next chunks' loads in flight.
+// Step 2: one state a thread, the next chunks' loads in flight.
 template <typename T, int S> __global__ void __launch_bounds__(128) scan_chunk_join_kernel(const ChunkArgs<T> g)
 {
-    constexpr int AHEAD = 8;
+    constexpr int AHEAD = 16;
     const ScanArgs<T> &a = g.s;
-    const int i = blockIdx.x * 128 + threadIdx.x, d = i / (S / 4), q = i % (S / 4), b = blockIdx.y;
+    const int i = blockIdx.x * 128 + threadIdx.x, d = i / S, b = blockIdx.y;
     if (d >= a.D) return;
     const int len = row_length(a.lengths, b, a.N), count = (len + g.chunk - 1) / g.chunk;
-    const long long at = ((long long)b * a.D + d) * S + 4 * q;
-    const float4 al = *reinterpret_cast<const float4 *>(a.a_log + (long long)d * S + 4 * q);
-    const float r[4] = {-expf(al.x) * LOG2E, -expf(al.y) * LOG2E, -expf(al.z) * LOG2E, -expf(al.w) * LOG2E};
-    float4 h = a.state_in ? *reinterpret_cast<const float4 *>(a.state_in + at) : make_float4(0.f, 0.f, 0.f, 0.f);
-    float *state = g.state + ((long long)b * g.chunks * a.D + d) * S + 4 * q;
+    const long long step = (long long)a.D * S, at = b * step + i;
+    const float r = -expf(a.a_log[i]) * LOG2E;
+    float h = a.state_in ? a.state_in[at] : 0.f;
+    float *state = g.state + b * g.chunks * step + i;
     const float *total = g.total + (long long)b * g.chunks * a.D + d;
-    const long long step = (long long)a.D * S;
-    const int nck = (a.N + CKPT - 1) / CKPT, per = CKPT / g.chunk;
-    float *ck = a.ckpt ? a.ckpt + ((long long)b * nck * a.D + d) * S + 4 * q : nullptr;
+    const int nck = (a.N + CKPT - 1) / CKPT;
+    float *ck = a.ckpt ? a.ckpt + b * nck * step + i : nullptr;
     for (int k0 = 0; k0 < count; k0 += AHEAD) {
-        float4 s[AHEAD];
-        float tt[AHEAD];
+        float s[AHEAD], tt[AHEAD];
 #pragma unroll
         for (int j = 0; j < AHEAD; ++j)
             if (k0 + j < count) {
-                s[j] = *reinterpret_cast<const float4 *>(state + (k0 + j) * step);
+                s[j] = state[(k0 + j) * step];
                 tt[j] = total[(long long)(k0 + j) * a.D];
             }
 #pragma unroll
         for (int j = 0; j < AHEAD; ++j)
             if (k0 + j < count) {
-                *reinterpret_cast<float4 *>(state + (k0 + j) * step) = h;
-                if (ck && (k0 + j) % per == 0) *reinterpret_cast<float4 *>(ck + (k0 + j) / per * step) = h;
-                h.x = fmaf(ex2(tt[j] * r[0]), h.x, s[j].x);
-                h.y = fmaf(ex2(tt[j] * r[1]), h.y, s[j].y);
-                h.z = fmaf(ex2(tt[j] * r[2]), h.z, s[j].z);
-                h.w = fmaf(ex2(tt[j] * r[3]), h.w, s[j].w);
+                state[(k0 + j) * step] = h;
+                const int t = (k0 + j) * g.chunk;
+                if (ck && t % CKPT == 0) ck[t / CKPT * step] = h;
+                h = fmaf(ex2(tt[j] * r), h, s[j]);
             }
     }
-    if (a.state_out) *reinterpret_cast<float4 *>(a.state_out + at) = h;
+    if (a.state_out) a.state_out[at] = h;
 }
 
-#ifndef CW
-#define CW 12
-#endif
-// Tokens of a chunk: the longest of 128, 64 and 32 that still gives every SM 16 warps of work.
+template <int S> int warps_of(const gma_scan_t &s) { return (s.D / s.G + Lanes<S>::CH_WARP - 1) / Lanes<S>::CH_WARP; }
+int group_warps(const gma_scan_t &s)
+{
+    return s.S <= 16 ? warps_of<16>(s) : s.S == 32 ? warps_of<32>(s) : warps_of<64>(s);
+}
+
+// Tokens of a chunk: the longest of 256, 128, 64 and 32 that still gives every SM 12 warps of work (of the 16
+// that its registers hold), keeps the chunk's b and c within 32 KB (two blocks an SM) and does not
+// step over a checkpoint.
 int chunk_of(const gma_scan_t &s)
 {
-    const long long warps = (long long)s.B * s.G * ((s.D / s.G + CH_WARP - 1) / CH_WARP);
-    for (int c = CKPT; c > 32; c /= 2)
-        if (warps * ((s.N + c - 1) / c) >= 152 * CW) return c;
+    const long long warps = (long long)s.B * s.G * group_warps(s);
+    int c = 4096 / s.S < 256 ? 4096 / s.S : 256;
+    if (s.checkpoints && c > CKPT) c = CKPT;
+    for (; c > 32; c /= 2)
+        if (warps * ((s.N + c - 1) / c) >= 152 * 12) return c;
     return 32;
 }
 
@@ -325,7 +328,7 @@ template <typename T, int S, bool VEC> gma_status_t run(const gma_scan_t &s, cha
     g.chunks = (s.N + g.chunk - 1) / g.chunk;
     g.state = (float *)ws;
     g.total = (float *)(ws + align_up((size_t)s.B * g.chunks * s.D * S * sizeof(float), 256));
-    const int warps = (s.D / s.G + CH_WARP - 1) / CH_WARP, per = warps < 8 ? warps : 8;
+    const int warps = group_warps(s), per = warps < 8 ? warps : 8;
     g.s.tiles = (warps + per - 1) / per;
     const dim3 grid(g.s.tiles * s.G, g.chunks, s.B);
     const bool vec_bc = rows_vec(s.b, s.dtype) && rows_vec(s.c, s.dtype);
@@ -336,8 +339,7 @@ template <typename T, int S, bool VEC> gma_status_t run(const gma_scan_t &s, cha
             return GMA_ERR_CUDA;
     if (g.chunks > 1) {
         GMA_LAUNCH(KID_SCAN_STATE, st, scan_chunk_kernel<T, S, VEC, false><<<grid, per * 32, rows + ring, st>>>(g, vec_bc));
-        GMA_LAUNCH(KID_SCAN_JOIN, st,
-                   scan_chunk_join_kernel<T, S><<<dim3((s.D * (S / 4) + 127) / 128, s.B), 128, 0, st>>>(g));
+        GMA_LAUNCH(KID_SCAN_JOIN, st, scan_chunk_join_kernel<T, S><<<dim3((s.D * S + 127) / 128, s.B), 128, 0, st>>>(g));
     }
     GMA_LAUNCH(KID_SCAN, st, scan_chunk_kernel<T, S, VEC, true><<<grid, per * 32, 2 * rows + ring, st>>>(g, vec_bc));
     return GMA_OK;
@@ -345,9 +347,13 @@ template <typename T, int S, bool VEC> gma_status_t run(const gma_scan_t &s, cha
 
 }  // namespace
 
+// Worth it from eight warps an SM on: with fewer, a warp's walk over its chunk takes as long as
+// the whole call of the kernel that spreads a tile's tokens over lanes (512 tokens of 1024 channels: 45 us in
+// three launches against 16 us).
 bool scan_chunked(const gma_scan_t &s)
 {
-    return s.S <= 16 && (s.N + 31) / 32 <= 65535;
+    const long long warps = (long long)s.B * s.G * group_warps(s) * ((s.N + 31) / 32);
+    return warps >= 152 * 8 && (s.N + 31) / 32 <= 65535 && (long long)s.D * s.S < (1ll << 31);
 }
 
 size_t scan_chunk_workspace(const gma_scan_t &s)
@@ -369,7 +375,9 @@ gma_status_t scan_chunk_forward(const gma_scan_t &s, void *ws, cudaStream_t st)
     auto with = [&](auto t) -> gma_status_t {
         using T = decltype(t);
         if (s.S == 8) return vec ? run<T, 8, true>(s, (char *)ws, st) : run<T, 8, false>(s, (char *)ws, st);
-        return vec ? run<T, 16, true>(s, (char *)ws, st) : run<T, 16, false>(s, (char *)ws, st);
+        if (s.S == 16) return vec ? run<T, 16, true>(s, (char *)ws, st) : run<T, 16, false>(s, (char *)ws, st);
+        if (s.S == 32) return vec ? run<T, 32, true>(s, (char *)ws, st) : run<T, 32, false>(s, (char *)ws, st);
+        return vec ? run<T, 64, true>(s, (char *)ws, st) : run<T, 64, false>(s, (char *)ws, st);
     };
     return s.dtype == GMA_BF16 ? with(__nv_bfloat16{}) : with(float{});
 }

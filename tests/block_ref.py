@@ -14,6 +14,7 @@ A rounding to bf16 adds half a step, 2^-8 relative, to fp32 2^-24.
 """
 import torch
 
+DEVICE = "cpu"       # where the references compute; long cases use the GPU's fp64 units
 U = 2.0 ** -24
 SLACK = 2.0
 HALF_STEP = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
@@ -58,7 +59,7 @@ class X:
 
 
 def lift(t):
-    return None if t is None else X(t.detach().cpu().double())
+    return None if t is None else X(t.detach().to(DEVICE).double())
 
 
 def stack(xs, dim):
@@ -70,7 +71,12 @@ def where(c, x, y):
 
 
 def zeros(*shape):
-    return X(torch.zeros(*shape, dtype=torch.float64))
+    return X(torch.zeros(*shape, dtype=torch.float64, device=DEVICE))
+
+
+def live_of(count, N):
+    """[B, N]: which tokens are a sequence's."""
+    return torch.arange(N, device=DEVICE) < torch.tensor(count, device=DEVICE)[:, None]
 
 
 def sigmoid(x):
@@ -127,9 +133,9 @@ def scan(u, dt, a_log, b, c, d_skip=None, dt_bias=None, z=None, state=None, leng
     if b.v.dim() == 3:
         b, c = b.map(lambda t: t.unsqueeze(2)), c.map(lambda t: t.unsqueeze(2))
     G = b.v.shape[2]
-    of = torch.arange(D) // (D // G)
+    of = torch.arange(D, device=DEVICE) // (D // G)
     count = lengths_list(lengths, B, N)
-    live = torch.tensor([[t < n for t in range(N)] for n in count])
+    live = live_of(count, N)
     A = rate_of(a_log)
     raw = dt + dt_bias if dt_bias is not None else dt
     delta = softplus(raw)
@@ -190,10 +196,10 @@ def conv(x, weight, bias=None, state=None, lengths=None, silu_=True, dy=None):
     x, weight, bias, state, dy = map(lift, (x, weight, bias, state, dy))
     B, N, D = x.v.shape
     W = weight.v.shape[1]
-    past = state.v if state is not None else torch.zeros(B, W - 1, D, dtype=torch.float64)
+    past = state.v if state is not None else torch.zeros(B, W - 1, D, dtype=torch.float64, device=DEVICE)
     rows = torch.cat([past, x.v], 1)
     count = lengths_list(lengths, B, N)
-    live = torch.tensor([[t < n for t in range(N)] for n in count])[..., None]
+    live = live_of(count, N)[..., None]
     near = X(rows.unfold(1, W, 1))
     pre = (near * weight).sum(3)
     if bias is not None:
@@ -204,7 +210,7 @@ def conv(x, weight, bias=None, state=None, lengths=None, silu_=True, dy=None):
     if dy is None:
         return y, after, None
     dp = where(live, dy * dsilu(pre) if silu_ else dy, nothing)
-    pad = dp.map(lambda v: torch.cat([v, torch.zeros(B, W - 1, D, dtype=torch.float64)], 1).unfold(1, W, 1))
+    pad = dp.map(lambda v: torch.cat([v, torch.zeros(B, W - 1, D, dtype=torch.float64, device=DEVICE)], 1).unfold(1, W, 1))
     dx = where(live, (pad * weight.map(lambda v: v.flip(1))).sum(3), nothing)
     return y, after, {"x": dx, "weight": (dp.map(lambda v: v.unsqueeze(-1)) * near).sum((0, 1)),
                       "bias": dp.sum((0, 1)) if bias is not None else None}
@@ -282,7 +288,7 @@ def norm(o, w_post=None, gate=None, residual=None, scale=None, w_pre=None, eps=1
 def worst(got, ref):
     """The largest error of a result as a share of what its type and the fp32 bound allow (<= 1 is
     right).  Values are finite."""
-    g = got.detach().cpu()
+    g = got.detach().to(ref.v.device)
     assert tuple(g.shape) == tuple(ref.v.shape), (g.shape, ref.v.shape)
     half = HALF_STEP[g.dtype]
     g = g.double()

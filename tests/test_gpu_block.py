@@ -116,6 +116,38 @@ def test_scan_backward(case):
             R.check(g[k], ref[k], k)
 
 
+BIG_SCANS = [  # calls with enough work for the forward pass in chunks: of 32 to 256 tokens, several and one
+    (2, 700, 4096, 16, 1, "bf16", True, True, [700, 301], 0, False),      # 64
+    (5, 33, 8192, 8, 2, "f32", False, True, [33, 0, 32, 1, 30], 0, True),   # 32, rows that end in each of the two
+    (6, 27, 16384, 16, 1, "bf16", True, False, None, 0, False),           # one chunk
+    (2, 900, 1100, 16, 1, "f32", True, False, [900, 513], 1, False),        # rows off 16-byte boundaries
+    (1, 500, 4160, 32, 2, "bf16", True, True, None, 0, True),             # one channel a lane
+    (2, 260, 2056, 64, 1, "f32", False, True, [260, 65], 0, False),         # two lanes a channel
+    (1, 300, 4099, 64, 1, "bf16", True, True, None, 5, True),             # the same, odd
+    (16, 1030, 1040, 16, 1, "bf16", False, False, None, 0, True),         # 128
+    (16, 1500, 1536, 16, 1, "bf16", True, True, None, 0, False),          # 256
+]
+
+
+@pytest.mark.parametrize("case", BIG_SCANS, ids=_id)
+def test_scan_forward_in_chunks(case, monkeypatch):
+    monkeypatch.setattr(R, "DEVICE", "cuda")
+    B, N, D, S, G, dtype, z, state, lengths, pitch, ckpt = case
+    t, _, _ = _scan_inputs(B, N, D, S, G, dtype, z, state, seed=3, pitch=pitch)
+    _, y, h, ck, _ = _run_scan(t, lengths, ckpt=ckpt, out=torch.zeros(B, N, D, dtype=TYPES[dtype], device="cuda"))
+    ry, rh = R.scan(**t, lengths=lengths)
+    R.check(y, ry, "y")
+    R.check(h, rh, "state")
+    if ckpt:      # the state before token 128 is the one after 128 tokens
+        short = {k: v[:, :128] if k in ("u", "dt", "b", "c", "z") and v is not None else v for k, v in t.items()}
+        want = R.scan(**short, lengths=lengths)[1]
+        if N > 128 and lengths is None:
+            R.check(ck[:, 1], want, "checkpoint")
+        first = t["state"] if state else torch.zeros(B, D, S)
+        live = [i for i in range(B) if lengths is None or lengths[i] > 0]
+        assert torch.equal(ck[live, 0].cpu(), first[live])
+
+
 def test_scan_without_optional_parameters():
     ssm, _ = _ops()
     t, dy, _ = _scan_inputs(2, 37, 24, 16, 1, "f32", False, False)
