@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(K::THREADS) scan_forward_kernel(const ScanArgs
                     h = fma2(a2[i], h, x2[i]);
                 }
                 f2 decay = ex2_2(mul2(total2, r2));
-                scan_up<K::LT>(decay, h, tl);
+                scan_lanes<K::LT, true>(decay, h);
                 const f2 before = *h0;
                 const f2 d1 = __shfl_up_sync(0xffffffffu, decay, 1, K::LT);
                 const f2 s1 = __shfl_up_sync(0xffffffffu, h, 1, K::LT);

@@ -307,17 +307,20 @@ int group_warps(const gma_scan_t &s)
     return s.S <= 16 ? warps_of<16>(s) : s.S == 32 ? warps_of<32>(s) : warps_of<64>(s);
 }
 
-// Tokens of a chunk: the longest of 256, 128, 64 and 32 that still gives every SM 12 warps of work (of the 16
-// that its registers hold), keeps the chunk's b and c within 32 KB (two blocks an SM) and does not
-// step over a checkpoint.
+// Tokens of a chunk, of 32, 64, 128 and 256: what takes least by (waves + 1/2) (chunk + 16), where a wave is
+// the 304 blocks that run at once and 16 tokens' time goes into a chunk's start and the join.  A chunk's b and c
+// stay within 32 KB (two blocks an SM), and a chunk does not step over a checkpoint.
 int chunk_of(const gma_scan_t &s)
 {
-    const long long warps = (long long)s.B * s.G * group_warps(s);
-    int c = 4096 / s.S < 256 ? 4096 / s.S : 256;
-    if (s.checkpoints && c > CKPT) c = CKPT;
-    for (; c > 32; c /= 2)
-        if (warps * ((s.N + c - 1) / c) >= 152 * 12) return c;
-    return 32;
+    const int warps = group_warps(s), per = warps < 8 ? warps : 8;
+    const double rows = (double)s.B * s.G * ((warps + per - 1) / per) * per / 8;
+    int best = 32;
+    double least = 0;
+    for (int c = 32; c <= 256 && c * s.S <= 4096 && !(s.checkpoints && c > CKPT); c *= 2) {
+        const double waves = rows * ((s.N + c - 1) / c) / 304 + 0.5, cost = (waves > 1 ? waves : 1) * (c + 16);
+        if (c == 32 || cost < least) best = c, least = cost;
+    }
+    return best;
 }
 
 template <typename T, int S, bool VEC> gma_status_t run(const gma_scan_t &s, char *ws, cudaStream_t st)

@@ -17,7 +17,7 @@
 namespace gma {
 namespace blk {
 
-constexpr int CKPT = 128;    // tokens between two checkpoints
+constexpr int CKPT = 64;     // tokens between two checkpoints
 
 template <int LT_, int TL_, int WARPS_> struct Tile {
     static constexpr int LT = LT_, TL = TL_, WARPS = WARPS_;
@@ -82,33 +82,35 @@ __device__ __forceinline__ void stage_pairs(const Rows<const T> &r, int b, int f
     }
 }
 
-// state += decay s, decay *= d where `on`: predicated, so that no selects are needed.
-__device__ __forceinline__ void join(f2 &decay, f2 &state, f2 d, f2 s, bool on)
+// One step of a scan over lanes in groups of LT: takes (decay, state) of the lane `OFF` before (or
+// behind), and where there is one, state += decay s and decay *= d.  The shuffle's own predicate tells.
+template <int LT, int OFF, bool UP> __device__ __forceinline__ void scan_step(f2 &decay, f2 &state)
 {
-    asm("{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %4, 0;\n\t"
-        "@p fma.rn.f32x2 %0, %1, %3, %0;\n\t@p mul.rn.f32x2 %1, %1, %2;\n\t}"
-        : "+l"(state), "+l"(decay)
-        : "l"(d), "l"(s), "r"((int)on));
+    constexpr int CLAMP = ((32 - LT) << 8) | (UP ? 0 : 31);
+#define GMA_SCAN_STEP(MODE)                                                                        \
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b32 a, b, c, e;\n\t.reg .b64 d, s;\n\t"                 \
+                 "mov.b64 {a, b}, %1;\n\tmov.b64 {c, e}, %0;\n\t"                                 \
+                 "shfl.sync." MODE ".b32 a|p, a, %2, %3, 0xffffffff;\n\t"                          \
+                 "shfl.sync." MODE ".b32 b, b, %2, %3, 0xffffffff;\n\t"                            \
+                 "shfl.sync." MODE ".b32 c, c, %2, %3, 0xffffffff;\n\t"                            \
+                 "shfl.sync." MODE ".b32 e, e, %2, %3, 0xffffffff;\n\t"                            \
+                 "mov.b64 d, {a, b};\n\tmov.b64 s, {c, e};\n\t"                                   \
+                 "@p fma.rn.f32x2 %0, %1, s, %0;\n\t@p mul.rn.f32x2 %1, %1, d;\n\t}"              \
+                 : "+l"(state), "+l"(decay)                                                        \
+                 : "n"(OFF), "n"(CLAMP))
+    if (UP) GMA_SCAN_STEP("up");
+    else GMA_SCAN_STEP("down");
+#undef GMA_SCAN_STEP
 }
 
-// Inclusive scan over the time lanes of (decay, state): state_l += decay_l state_{l - off}.
-template <int LT> __device__ __forceinline__ void scan_up(f2 &decay, f2 &state, int tl)
+// Inclusive scan over the time lanes, from the first one up or from the last one down.
+template <int LT, bool UP> __device__ __forceinline__ void scan_lanes(f2 &decay, f2 &state)
 {
-#pragma unroll
-    for (int off = 1; off < LT; off *= 2) {
-        const f2 d = __shfl_up_sync(0xffffffffu, decay, off, LT);
-        const f2 s = __shfl_up_sync(0xffffffffu, state, off, LT);
-        join(decay, state, d, s, tl >= off);
-    }
-}
-template <int LT> __device__ __forceinline__ void scan_down(f2 &decay, f2 &state, int tl)
-{
-#pragma unroll
-    for (int off = 1; off < LT; off *= 2) {
-        const f2 d = __shfl_down_sync(0xffffffffu, decay, off, LT);
-        const f2 s = __shfl_down_sync(0xffffffffu, state, off, LT);
-        join(decay, state, d, s, tl + off < LT);
-    }
+    if (LT > 1) scan_step<LT, 1, UP>(decay, state);
+    if (LT > 2) scan_step<LT, 2, UP>(decay, state);
+    if (LT > 4) scan_step<LT, 4, UP>(decay, state);
+    if (LT > 8) scan_step<LT, 8, UP>(decay, state);
+    if (LT > 16) scan_step<LT, 16, UP>(decay, state);
 }
 
 template <typename T> struct ScanArgs {

@@ -33,7 +33,7 @@ _CONV = "5iIR5QR"
 _conv_t = m.layout(_CONV)
 _conv_grad_t = m.layout(_CONV + "RR2Q")
 
-CHECKPOINT_TOKENS = 128
+CHECKPOINT_TOKENS = 64
 GMA_CONV_LINEAR = 0x1
 _empty, _zeros, _int32 = torch.empty, torch.zeros, torch.int32
 

@@ -138,10 +138,10 @@ def test_scan_forward_in_chunks(case, monkeypatch):
     ry, rh = R.scan(**t, lengths=lengths)
     R.check(y, ry, "y")
     R.check(h, rh, "state")
-    if ckpt:      # the state before token 128 is the one after 128 tokens
-        short = {k: v[:, :128] if k in ("u", "dt", "b", "c", "z") and v is not None else v for k, v in t.items()}
+    if ckpt:      # the state before token 64 is the one after 64 tokens
+        short = {k: v[:, :64] if k in ("u", "dt", "b", "c", "z") and v is not None else v for k, v in t.items()}
         want = R.scan(**short, lengths=lengths)[1]
-        if N > 128 and lengths is None:
+        if N > 64 and lengths is None:
             R.check(ck[:, 1], want, "checkpoint")
         first = t["state"] if state else torch.zeros(B, D, S)
         live = [i for i in range(B) if lengths is None or lengths[i] > 0]
