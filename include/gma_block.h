@@ -140,8 +140,9 @@ gma_status_t gma_conv_backward(const gma_conv_grad_t *grad, void *workspace, siz
  *                                                                 (v = a without w_post)
  *     r' = residual + scale v, stored in residual_dtype           (r' = v in dtype without residual)
  *     h = w_pre r' / sqrt(mean(r'^2) + eps), of r' as stored      (no h without w_pre)
- * o is the mixers' output layout [B][H][N][d], by strides.  1 <= D <= 16384; group divides D;
- * B <= 65535.  A residual is required for scale; w_post or w_pre is required. */
+ * o is the mixers' output layout [B][H][N][d], by strides.  1 <= D <= 16384; group is D, or 8, 16, 32,
+ * 64, 128 or 256 and divides D; B * N <= 2^30.  A residual is required for scale; w_post or w_pre is
+ * required. */
 typedef struct {
     int32_t B, N, H, d;
     int32_t group;                /* channels per group of the first norm (D: one group)     */

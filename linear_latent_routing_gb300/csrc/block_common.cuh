@@ -138,11 +138,7 @@ __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c)
 __device__ __forceinline__ f2 mul2(f2 a, f2 b)
 {
     f2 d;
-#ifdef MULF
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(0x8000000080000000ull));
-#else
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-#endif
     return d;
 }
 __device__ __forceinline__ f2 add2(f2 a, f2 b)

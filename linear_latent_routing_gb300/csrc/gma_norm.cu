@@ -8,17 +8,40 @@
 // whole block, by the row's width), NV pieces of eight channels a thread; a block holds several
 // narrow rows.  The mixers' layout [B][H][N][d] is read (and its gradient written) in place, head
 // by head, so no transposition runs between a mixer and its norm.
+#include <algorithm>
+#include <type_traits>
+
 #include "block_common.cuh"
 
 namespace gma {
 namespace blk {
 namespace {
 
-constexpr int MAX_WARPS = 32;
+constexpr int MAX_WARPS = 16;
+constexpr int FORWARD_BLOCKS = 4, BACKWARD_BLOCKS = 2;   // blocks of 256 threads an SM, by their registers
+constexpr int TWO_ROWS = 152 * 8;                        // blocks from which a thread takes two rows
+
+// n / d for n < 2^31 by a multiplication (the divisor's rounded-up reciprocal): a row's batch row and token
+// and a channel's head would otherwise take as many instructions as the row's arithmetic.
+struct FastDiv {
+    uint32_t d, m, s1, s2;
+    __device__ __forceinline__ uint32_t div(uint32_t n) const
+    {
+        const uint32_t t = __umulhi(n, m);
+        return (t + ((n - t) >> s1)) >> s2;
+    }
+};
+FastDiv fast_div(uint32_t d)
+{
+    uint32_t l = 0;
+    while ((1ull << l) < d) ++l;
+    return FastDiv{d, (uint32_t)(((1ull << 32) * ((1ull << l) - d)) / d + 1), l ? 1u : 0u, l ? l - 1 : 0u};
+}
 
 template <typename T, typename R> struct NormArgs {
-    int N, d, D, group, tpr;      // tpr: threads per row
-    long long rows;               // B * N
+    int N, D, group, tpr, tpr_log;   // tpr: threads per row, a power of two
+    FastDiv by_n, by_d;
+    int rows;                     // B * N
     float eps, inv_d, inv_group;
     Rows<const T> o;
     long long o_head;
@@ -29,37 +52,40 @@ template <typename T, typename R> struct NormArgs {
     Rows<T> h;
 };
 
+// Offset of channel c in a token of the head layout.
+__device__ __forceinline__ long long head_offset(const FastDiv &by_d, long long head, int c)
+{
+    const int hd = by_d.div(c);
+    return hd * head + (c - hd * (int)by_d.d);
+}
+
 // Channels c0 .. c0 + 7 of token (b, t) in the head layout.  VEC: d is a multiple of eight.
 template <bool VEC, typename T>
-__device__ __forceinline__ void load_heads(const Rows<const T> &o, long long head, int d, int b, int t, int c0, int n,
+__device__ __forceinline__ void load_heads(const Rows<const T> &o, long long head, const FastDiv &by_d, int b, int t, int c0, int n,
                                            float (&v)[8])
 {
     const T *p = o.at(b, t);
     if (VEC) {
-        const int hd = c0 / d;
-        load8<true>(p + hd * head + (c0 - hd * d), n, v);
+        load8<true>(p + head_offset(by_d, head, c0), n, v);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int c = c0 + i, hd = c / d;
-            v[i] = i < n ? to_f32<T>(p[hd * head + (c - hd * d)]) : 0.f;
+            v[i] = i < n ? to_f32<T>(p[head_offset(by_d, head, c0 + i)]) : 0.f;
         }
     }
 }
 
 template <bool VEC, typename T>
-__device__ __forceinline__ void store_heads(const Rows<T> &o, long long head, int d, int b, int t, int c0, int n,
+__device__ __forceinline__ void store_heads(const Rows<T> &o, long long head, const FastDiv &by_d, int b, int t, int c0, int n,
                                             const float (&v)[8])
 {
     T *p = o.at(b, t);
     if (VEC) {
-        const int hd = c0 / d;
-        store8<true>(p + hd * head + (c0 - hd * d), n, v);
+        store8<true>(p + head_offset(by_d, head, c0), n, v);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int c = c0 + i, hd = c / d;
-            if (i < n) p[hd * head + (c - hd * d)] = from_f32<T>(v[i]);
+            if (i < n) p[head_offset(by_d, head, c0 + i)] = from_f32<T>(v[i]);
         }
     }
 }
@@ -104,84 +130,128 @@ __device__ __forceinline__ float group_sum(float v, int lanes)
     return v;
 }
 
-template <typename T, typename R, bool VEC, int NV>
-__global__ void __launch_bounds__(1024) norm_forward_kernel(const NormArgs<T, R> a)
+// A thread takes its pieces of ROWS rows at a time, so that the loads of all of them are in flight
+// together: one row for few rows (latency), two where the GPU is full.
+template <typename T, typename R, bool VEC, int NV, int THREADS, int ROWS>
+__global__ void __launch_bounds__(THREADS, THREADS == 256 ? FORWARD_BLOCKS : 1) norm_forward_kernel(const NormArgs<T, R> a)
 {
-    __shared__ float buf[2][MAX_WARPS][1];
-    const int tid = threadIdx.x % a.tpr;
-    const long long row = (long long)blockIdx.x * (blockDim.x / a.tpr) + threadIdx.x / a.tpr;
-    const bool live = row < a.rows;
-    const int b = live ? (int)(row / a.N) : 0, t = live ? (int)(row - (long long)b * a.N) : 0;
-    float x[NV][8], rstd[NV];
-    float ss[1] = {0.f};
+    __shared__ float buf[2][MAX_WARPS][ROWS];
+    const int tid = threadIdx.x & (a.tpr - 1), lane_row = threadIdx.x >> a.tpr_log, per = THREADS >> a.tpr_log;
+    int b[ROWS], t[ROWS];
+    bool live[ROWS];
+    float x[ROWS][NV][8], res[ROWS][NV][8], rstd[ROWS][NV], ss[ROWS];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int c0 = (j * a.tpr + tid) * 8, n = live ? min(8, a.D - c0) : 0;
+    for (int r = 0; r < ROWS; ++r) {
+        const int row = (blockIdx.x * ROWS + r) * per + lane_row;
+        live[r] = row < a.rows;
+        b[r] = live[r] ? a.by_n.div(row) : 0;
+        t[r] = live[r] ? row - b[r] * a.N : 0;
+    }
+    Raw8<T> on[ROWS][NV], gn[ROWS][NV];
+    Raw8<R> rn[ROWS][NV];
+    if (VEC) {
+        long long head_at[NV];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[j][i] = 0.f;
-        if (n > 0) {
-            load_heads<VEC>(a.o, a.o_head, a.d, b, t, c0, n, x[j]);
-            if (a.gate.p) {
-                float g[8];
-                load8<VEC>(a.gate.at(b, t) + c0, n, g);
+        for (int j = 0; j < NV; ++j) head_at[j] = head_offset(a.by_d, a.o_head, (j * a.tpr + tid) * 8);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[j][i] *= silu(g[i]);
+        for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int c0 = (j * a.tpr + tid) * 8;
+                if (!live[r] || c0 >= a.D) continue;
+                on[r][j].load(a.o.at(b[r], t[r]) + head_at[j]);
+                if (a.gate.p) gn[r][j].load(a.gate.at(b[r], t[r]) + c0);
+                if (a.residual.p) rn[r][j].load(a.residual.at(b[r], t[r]) + c0);
             }
-        }
-        float s = 0.f;
+    }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s = fmaf(x[j][i], x[j][i], s);
-        rstd[j] = s;
-        ss[0] += s;
+    for (int r = 0; r < ROWS; ++r) {
+        ss[r] = 0.f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c0 = (j * a.tpr + tid) * 8, n = live[r] ? min(8, a.D - c0) : 0;
+            float(&v)[8] = x[r][j];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = res[r][j][i] = 0.f;
+            if (n > 0) {
+                float g[8];
+                if (VEC) {
+                    on[r][j].get(v);
+                    if (a.gate.p) gn[r][j].get(g);
+                    if (a.residual.p) rn[r][j].get(res[r][j]);
+                } else {
+                    load_heads<false>(a.o, a.o_head, a.by_d, b[r], t[r], c0, n, v);
+                    if (a.gate.p) load8<false>(a.gate.at(b[r], t[r]) + c0, n, g);
+                    if (a.residual.p) load8<false>(a.residual.at(b[r], t[r]) + c0, n, res[r][j]);
+                }
+                if (a.gate.p) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] *= silu(g[i]);
+                }
+            }
+            float s = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s = fmaf(v[i], v[i], s);
+            rstd[r][j] = s;
+            ss[r] += s;
+        }
     }
     if (a.w_post) {
-        if (a.group == a.D) {
-            row_sum<1>(ss, a.tpr, buf[0]);
+        if (a.group == a.D) row_sum<ROWS>(ss, a.tpr, buf[0]);
 #pragma unroll
-            for (int j = 0; j < NV; ++j) rstd[j] = rsqrtf(ss[0] * a.inv_group + a.eps);
-        } else {
+        for (int r = 0; r < ROWS; ++r)
 #pragma unroll
-            for (int j = 0; j < NV; ++j) rstd[j] = rsqrtf(group_sum(rstd[j], a.group / 8) * a.inv_group + a.eps);
-        }
+            for (int j = 0; j < NV; ++j)
+                rstd[r][j] = rsqrtf((a.group == a.D ? ss[r] : group_sum(rstd[r][j], a.group / 8)) * a.inv_group + a.eps);
     }
-    float s2[1] = {0.f};
+    float s2[ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) s2[r] = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        const int c0 = (j * a.tpr + tid) * 8, n = live ? min(8, a.D - c0) : 0;
-        if (n > 0) {
-            if (a.w_post) {
-                float w[8];
-                load8<VEC>(a.w_post + c0, n, w);
+        const int c0 = (j * a.tpr + tid) * 8, n = min(8, a.D - c0);
+        if (n <= 0) continue;
+        float w[8], sc[8];
+        load_param<VEC>(a.w_post, c0, n, 1.f, w);
+        load_param<VEC>(a.scale, c0, n, 1.f, sc);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[j][i] *= rstd[j] * w[i];
+        for (int r = 0; r < ROWS; ++r) {
+            if (!live[r]) continue;
+            float(&v)[8] = x[r][j];
+            if (a.w_post) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] *= rstd[r][j] * w[i];
             }
             if (a.residual.p) {
-                float sc[8], r[8];
-                load_param<VEC>(a.scale, c0, n, 1.f, sc);
-                load8<VEC>(a.residual.at(b, t) + c0, n, r);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[j][i] = fmaf(sc[i], x[j][i], r[i]);
+                for (int i = 0; i < 8; ++i) v[i] = fmaf(sc[i], v[i], res[r][j][i]);
             }
-            store8<VEC>(a.r.at(b, t) + c0, n, x[j]);
+            store8<VEC>(a.r.at(b[r], t[r]) + c0, n, v);
+            if (a.w_pre) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                x[j][i] = i < n ? to_f32<R>(from_f32<R>(x[j][i])) : 0.f;   // as stored
-                s2[0] = fmaf(x[j][i], x[j][i], s2[0]);
+                for (int i = 0; i < 8; ++i) {
+                    v[i] = i < n ? to_f32<R>(from_f32<R>(v[i])) : 0.f;   // as stored
+                    s2[r] = fmaf(v[i], v[i], s2[r]);
+                }
             }
         }
     }
     if (!a.w_pre) return;
-    row_sum<1>(s2, a.tpr, buf[1]);
-    const float rs = rsqrtf(s2[0] * a.inv_d + a.eps);
+    row_sum<ROWS>(s2, a.tpr, buf[1]);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        const int c0 = (j * a.tpr + tid) * 8, n = live ? min(8, a.D - c0) : 0;
-        if (n > 0) {
-            float w[8];
-            load8<VEC>(a.w_pre + c0, n, w);
+        const int c0 = (j * a.tpr + tid) * 8, n = min(8, a.D - c0);
+        if (n <= 0) continue;
+        float w[8];
+        load_param<VEC>(a.w_pre, c0, n, 1.f, w);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] *= x[j][i] * rs;
-            store8<VEC>(a.h.at(b, t) + c0, n, w);
+        for (int r = 0; r < ROWS; ++r) {
+            if (!live[r]) continue;
+            const float rs = rsqrtf(s2[r] * a.inv_d + a.eps);
+            float h[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) h[i] = w[i] * x[r][j][i] * rs;
+            store8<VEC>(a.h.at(b[r], t[r]) + c0, n, h);
         }
     }
 }
@@ -204,39 +274,78 @@ template <typename T, typename R> struct NormGradArgs {
 //   da = rstd (q - a rstd^2 mean(q a)),  q = w_post dv;   do = da silu(gate), dgate = da o silu'(gate).
 // Blocks walk over the rows with the parameter gradients of their channels in registers, add up
 // their row lanes in order and leave one partial row each; sum_rows adds those in order.
-template <typename T, typename R, bool VEC, int NV>
-__global__ void __launch_bounds__(NV == 1 ? 256 : 1024) norm_backward_kernel(const NormGradArgs<T, R> g)
+template <typename T, typename R, bool VEC, int NV, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS == 256 ? BACKWARD_BLOCKS : 1) norm_backward_kernel(const NormGradArgs<T, R> g)
 {
-    extern __shared__ float part_s[];                      // [blockDim.x][8]
+    extern __shared__ float part_s[];                      // [8][THREADS]
     __shared__ float buf[2][MAX_WARPS][3], buf2[2][MAX_WARPS][1];
+    constexpr bool AHEAD = VEC && NV == 1;
     const NormArgs<T, R> &a = g.f;
-    const int tid = threadIdx.x % a.tpr, lane_row = threadIdx.x / a.tpr, per = blockDim.x / a.tpr;
+    const int tid = threadIdx.x & (a.tpr - 1), lane_row = threadIdx.x >> a.tpr_log, per = THREADS >> a.tpr_log;
     float dwpost[NV][8], dscale[NV][8], dwpre[NV][8];
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
         for (int i = 0; i < 8; ++i) dwpost[j][i] = dscale[j][i] = dwpre[j][i] = 0.f;
+    Raw8<T> on[NV], gn[NV], hn[NV];
+    Raw8<R> dn[NV], rn[NV];
+    const Rows<const R> kept{a.r.p, a.r.sb, a.r.st};
+    long long head_at[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) head_at[j] = head_offset(a.by_d, a.o_head, (j * a.tpr + tid) * 8);
+    auto fetch = [&](int row) {
+        if (!AHEAD || row >= a.rows) return;
+        const int b = a.by_n.div(row), t = row - b * a.N;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c0 = (j * a.tpr + tid) * 8;
+            if (c0 >= a.D) continue;
+            on[j].load(a.o.at(b, t) + head_at[j]);
+            if (a.gate.p) gn[j].load(a.gate.at(b, t) + c0);
+            if (g.dr.p) dn[j].load(g.dr.at(b, t) + c0);
+            if (g.dh.p) {
+                rn[j].load(kept.at(b, t) + c0);
+                hn[j].load(g.dh.at(b, t) + c0);
+            }
+        }
+    };
+    const int step = gridDim.x * per;
+    int row = blockIdx.x * per + lane_row;
+    fetch(row);
     int turn = 0;
-    for (long long row0 = (long long)blockIdx.x * per; row0 < a.rows; row0 += (long long)gridDim.x * per, turn ^= 1) {
-        const long long row = row0 + lane_row;
+    for (int row0 = blockIdx.x * per; row0 < a.rows; row0 += step, row += step, turn ^= 1) {
         const bool live = row < a.rows;
-        const int b = live ? (int)(row / a.N) : 0, t = live ? (int)(row - (long long)b * a.N) : 0;
-        float o[NV][8], gt[NV][8], rf[NV][8], dh[NV][8], dr[NV][8], gs[NV];
-        float sums[3] = {0.f, 0.f, 0.f};                   // r'^2, m r', a^2
+        const int b = live ? a.by_n.div(row) : 0, t = live ? row - b * a.N : 0;
+        // act[] = o silu(gate); by_o[], by_gate[]: its derivatives
+        float act[NV][8], by_o[NV][8], by_gate[NV][8], rf[NV][8], dh[NV][8], dr[NV][8], gs[NV];
+        float sums[3] = {0.f, 0.f, 0.f};                   // r'^2, m r', act^2
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int c0 = (j * a.tpr + tid) * 8, n = live ? min(8, a.D - c0) : 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) o[j][i] = gt[j][i] = rf[j][i] = dh[j][i] = dr[j][i] = 0.f;
+            for (int i = 0; i < 8; ++i) act[j][i] = by_o[j][i] = by_gate[j][i] = rf[j][i] = dh[j][i] = dr[j][i] = 0.f;
             gs[j] = 0.f;
             if (n > 0) {
-                load_heads<VEC>(a.o, a.o_head, a.d, b, t, c0, n, o[j]);
-                if (a.gate.p) load8<VEC>(a.gate.at(b, t) + c0, n, gt[j]);
-                if (g.dr.p) load8<VEC>(g.dr.at(b, t) + c0, n, dr[j]);
+                float o[8], gt[8];
+                if (AHEAD) {
+                    on[j].get(o);
+                    if (a.gate.p) gn[j].get(gt);
+                    if (g.dr.p) dn[j].get(dr[j]);
+                    if (g.dh.p) {
+                        rn[j].get(rf[j]);
+                        hn[j].get(dh[j]);
+                    }
+                } else {
+                    load_heads<VEC>(a.o, a.o_head, a.by_d, b, t, c0, n, o);
+                    if (a.gate.p) load8<VEC>(a.gate.at(b, t) + c0, n, gt);
+                    if (g.dr.p) load8<VEC>(g.dr.at(b, t) + c0, n, dr[j]);
+                    if (g.dh.p) {
+                        load8<VEC>(kept.at(b, t) + c0, n, rf[j]);
+                        load8<VEC>(g.dh.at(b, t) + c0, n, dh[j]);
+                    }
+                }
                 if (g.dh.p) {
                     float w[8];
-                    load8<VEC>(Rows<const R>{a.r.p, a.r.sb, a.r.st}.at(b, t) + c0, n, rf[j]);
-                    load8<VEC>(g.dh.at(b, t) + c0, n, dh[j]);
                     load8<VEC>(a.w_pre + c0, n, w);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
@@ -246,12 +355,20 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 1024) norm_backward_kernel(con
                 }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float v = a.gate.p ? o[j][i] * silu(gt[j][i]) : o[j][i];
-                    gs[j] = fmaf(v, v, gs[j]);
+                    if (a.gate.p) {
+                        const float s = sigmoid(gt[i]);
+                        by_o[j][i] = gt[i] * s;
+                        by_gate[j][i] = o[i] * dsilu(gt[i], s);
+                    } else {
+                        by_o[j][i] = 1.f;
+                    }
+                    act[j][i] = o[i] * by_o[j][i];
+                    gs[j] = fmaf(act[j][i], act[j][i], gs[j]);
                 }
                 sums[2] += gs[j];
             }
         }
+        fetch(row + step);
         if (g.dh.p || (a.w_post && a.group == a.D)) row_sum<3>(sums, a.tpr, buf[turn]);
         const float rs2 = rsqrtf(sums[0] * a.inv_d + a.eps);
         const float k2 = rs2 * rs2 * sums[1] * a.inv_d;
@@ -279,12 +396,11 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 1024) norm_backward_kernel(con
                 load_param<VEC>(a.scale, c0, n, 1.f, sc);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float v = a.gate.p ? o[j][i] * silu(gt[j][i]) : o[j][i];
-                    const float nrm = v * rstd[j], dv = dr[j][i] * sc[i];
+                    const float nrm = act[j][i] * rstd[j], dv = dr[j][i] * sc[i];
                     dscale[j][i] = fmaf(dr[j][i], nrm * w[i], dscale[j][i]);
                     dwpost[j][i] = fmaf(dv, nrm, dwpost[j][i]);
                     dr[j][i] = dv * w[i];                  // q
-                    dots[j] = fmaf(dr[j][i], v, dots[j]);
+                    dots[j] = fmaf(dr[j][i], act[j][i], dots[j]);
                 }
                 dot[0] += dots[j];
             }
@@ -300,13 +416,11 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 1024) norm_backward_kernel(con
                 float dov[8], dg[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float s = a.gate.p ? sigmoid(gt[j][i]) : 1.f, act = a.gate.p ? gt[j][i] * s : 1.f;
-                    const float v = o[j][i] * act;
-                    const float da = rstd[j] * fmaf(-v, k1, dr[j][i]);
-                    dov[i] = da * act;
-                    dg[i] = da * o[j][i] * dsilu(gt[j][i], s);
+                    const float da = rstd[j] * fmaf(-act[j][i], k1, dr[j][i]);
+                    dov[i] = da * by_o[j][i];
+                    dg[i] = da * by_gate[j][i];
                 }
-                store_heads<VEC>(g.d_o, g.d_o_head, a.d, b, t, c0, n, dov);
+                store_heads<VEC>(g.d_o, g.d_o_head, a.by_d, b, t, c0, n, dov);
                 if (a.gate.p) store8<VEC>(g.dgate.at(b, t) + c0, n, dg);
             }
         }
@@ -319,12 +433,12 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 1024) norm_backward_kernel(con
             __syncthreads();
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                part_s[i * blockDim.x + threadIdx.x] = k == 0 ? dwpost[j][i] : k == 1 ? dscale[j][i] : dwpre[j][i];
+                part_s[i * THREADS + threadIdx.x] = k == 0 ? dwpost[j][i] : k == 1 ? dscale[j][i] : dwpre[j][i];
             __syncthreads();
             const int c0 = (j * a.tpr + tid) * 8;
             for (int i = lane_row; i < 8; i += per) {
                 float v = 0.f;
-                for (int l = 0; l < per; ++l) v += part_s[i * blockDim.x + l * a.tpr + tid];
+                for (int l = 0; l < per; ++l) v += part_s[i * THREADS + l * a.tpr + tid];
                 if (c0 + i < a.D) g.part[((long long)blockIdx.x * 3 + k) * g.pitch + c0 + i] = v;
             }
         }
@@ -337,13 +451,14 @@ struct Plan {
 };
 
 // Threads per row: enough for the row's pieces of eight channels, nv pieces a thread, a power of two
-// from 8 on.  Blocks have 256 threads, or one row if that takes more.
-Plan plan(int D, int nv)
+// from 8 on.  Blocks have 256 threads, 512 where a row has more than 256 pieces of channels; a thread then
+// has as many pieces as that takes (up to four, at 16384 channels).
+Plan plan(int D)
 {
     const int pieces = (D + 7) / 8;
-    int tpr = 8;
-    while (tpr * nv < pieces) tpr *= 2;
-    return Plan{tpr, nv, tpr > 256 ? tpr : 256};
+    Plan p = {8, pieces > 1024 ? 4 : pieces > 512 ? 2 : 1, pieces > 256 ? 512 : 256};
+    while (p.tpr * p.nv < pieces) p.tpr *= 2;
+    return p;
 }
 
 gma_status_t check(const gma_norm_t *n, bool forward)
@@ -353,7 +468,7 @@ gma_status_t check(const gma_norm_t *n, bool forward)
     if (n->dtype != GMA_F32 && n->dtype != GMA_BF16) return GMA_ERR_INVALID_ARG;
     if (n->residual.ptr && n->residual_dtype != GMA_F32 && n->residual_dtype != n->dtype) return GMA_ERR_INVALID_ARG;
     const long long D = (long long)n->H * n->d;
-    if (D > 16384 || n->B > 65535 || n->N > (1 << 30)) return GMA_ERR_UNSUPPORTED_SHAPE;
+    if (D > 16384 || (long long)n->B * n->N > (1ll << 30)) return GMA_ERR_UNSUPPORTED_SHAPE;
     const int g = n->group;
     if (g != D && !((g == 8 || g == 16 || g == 32 || g == 64 || g == 128 || g == 256) && D % g == 0))
         return GMA_ERR_UNSUPPORTED_SHAPE;
@@ -374,8 +489,11 @@ gma_status_t check(const gma_norm_t *n, bool forward)
 template <typename T, typename R> NormArgs<T, R> args_of(const gma_norm_t &n, int tpr)
 {
     NormArgs<T, R> a;
-    a.N = n.N; a.d = n.d; a.D = n.H * n.d; a.group = n.group; a.tpr = tpr;
-    a.rows = (long long)n.B * n.N;
+    a.N = n.N; a.D = n.H * n.d; a.group = n.group; a.tpr = tpr; a.tpr_log = 0;
+    while ((1 << a.tpr_log) < tpr) ++a.tpr_log;
+    a.rows = n.B * n.N;
+    a.by_n = fast_div(n.N);
+    a.by_d = fast_div(n.d);
     a.eps = n.eps; a.inv_d = 1.f / a.D; a.inv_group = 1.f / n.group;
     a.o = rows_of<const T>(n.o); a.o_head = n.o_head;
     a.gate = rows_of<const T>(n.gate);
@@ -394,30 +512,29 @@ bool vec_common(const gma_norm_t &n)
            vec_given(n.gate, n.dtype) && opt_ok(n.w_post, 16) && opt_ok(n.scale, 16) && opt_ok(n.w_pre, 16);
 }
 
-// Calls f(T{}, R{}, VEC, NV).
-template <typename F> gma_status_t dispatch(const gma_norm_t &n, bool vec, int nv, F f)
+// Calls f(T{}, R{}, VEC, NV, THREADS).
+template <typename F> gma_status_t dispatch(const gma_norm_t &n, bool vec, const Plan &p, F f)
 {
     auto with_types = [&](auto t, auto r) -> gma_status_t {
-        auto with_nv = [&](auto v) -> gma_status_t {
-            if (nv == 1) return f(t, r, v, std::integral_constant<int, 1>{});
-            return f(t, r, v, std::integral_constant<int, 2>{});
+        auto with_plan = [&](auto v) -> gma_status_t {
+            typedef std::integral_constant<int, 512> Wide;
+            if (p.threads == 256) return f(t, r, v, std::integral_constant<int, 1>{}, std::integral_constant<int, 256>{});
+            if (p.nv == 1) return f(t, r, v, std::integral_constant<int, 1>{}, Wide{});
+            if (p.nv == 2) return f(t, r, v, std::integral_constant<int, 2>{}, Wide{});
+            return f(t, r, v, std::integral_constant<int, 4>{}, Wide{});
         };
-        return vec ? with_nv(std::true_type{}) : with_nv(std::false_type{});
+        return vec ? with_plan(std::true_type{}) : with_plan(std::false_type{});
     };
     if (n.dtype == GMA_F32) return with_types(float{}, float{});
     if (n.residual.ptr && n.residual_dtype == GMA_F32) return with_types(__nv_bfloat16{}, float{});
     return with_types(__nv_bfloat16{}, __nv_bfloat16{});
 }
 
-// Two pieces a thread only where one would take more threads than a block has.
-Plan plan_rows(int D) { return D > 8 * 1024 ? plan(D, 2) : plan(D, 1); }
-Plan plan_grad(int D) { return D > 8 * 256 ? plan(D, 2) : plan(D, 1); }
-
-int grad_blocks(const gma_norm_t &n, const Plan &p)
+// Blocks that walk over the rows: as many as run at once.
+int blocks_of(const gma_norm_t &n, const Plan &p, int per_sm)
 {
     const long long rows = (long long)n.B * n.N, per = p.threads / p.tpr;
-    const long long want = 152ll * (1024 / p.threads);
-    return (int)std::min((rows + per - 1) / per, want);
+    return (int)std::min((rows + per - 1) / per, 152ll * (p.threads == 256 ? per_sm : 1));
 }
 
 }  // namespace
@@ -436,18 +553,24 @@ gma_status_t gma_norm_forward(const gma_norm_t *n, gma_stream_t stream)
     if ((r = usable_device()) != GMA_OK) return r;
     cudaStream_t st = (cudaStream_t)stream;
     const int D = n->H * n->d, rd = n->residual.ptr ? n->residual_dtype : n->dtype;
-    const Plan p = plan_rows(D);
+    const Plan p = plan(D);
     const bool vec = vec_common(*n) && vec_given(n->residual, rd) && rows_vec(n->r, rd) &&
                      (!n->w_pre || rows_vec(n->h, n->dtype));
-    return dispatch(*n, vec, p.nv, [&](auto t, auto rt, auto v, auto nv) -> gma_status_t {
+    return dispatch(*n, vec, p, [&](auto t, auto rt, auto v, auto nv, auto threads) -> gma_status_t {
         using T = decltype(t);
         using R = decltype(rt);
+        constexpr int TH = decltype(threads)::value;
+        constexpr bool V = decltype(v)::value;
+        constexpr int NV = decltype(nv)::value;
         const NormArgs<T, R> a = args_of<T, R>(*n, p.tpr);
-        const long long per = p.threads / p.tpr, blocks = (a.rows + per - 1) / per;
-        if (blocks > 0x7fffffffll) return GMA_ERR_UNSUPPORTED_SHAPE;
-        GMA_LAUNCH(KID_NORM, st,
-                   norm_forward_kernel<T, R, decltype(v)::value, decltype(nv)::value>
-                   <<<(unsigned)blocks, p.threads, 0, st>>>(a));
+        const int per = TH / p.tpr, blocks = (a.rows + per - 1) / per;
+        // two rows a thread from two waves of blocks on
+        if (V && NV == 1 && TH == 256 && blocks > TWO_ROWS)
+            GMA_LAUNCH(KID_NORM, st,
+                       norm_forward_kernel<T, R, V, NV, TH, V && NV == 1 && TH == 256 ? 2 : 1>
+                       <<<(unsigned)((blocks + 1) / 2), TH, 0, st>>>(a));
+        else
+            GMA_LAUNCH(KID_NORM, st, norm_forward_kernel<T, R, V, NV, TH, 1><<<(unsigned)blocks, TH, 0, st>>>(a));
         return GMA_OK;
     });
 }
@@ -456,7 +579,7 @@ size_t gma_norm_backward_workspace_size(const gma_norm_grad_t *g)
 {
     if (!g || check(&g->fwd, false) != GMA_OK) return 0;
     const int D = g->fwd.H * g->fwd.d;
-    return align_up((size_t)grad_blocks(g->fwd, plan_grad(D)) * 3 * ((D + 7) / 8 * 8) * sizeof(float), 256);
+    return align_up((size_t)blocks_of(g->fwd, plan(D), BACKWARD_BLOCKS) * 3 * ((D + 7) / 8 * 8) * sizeof(float), 256);
 }
 
 gma_status_t gma_norm_backward(const gma_norm_grad_t *g, void *ws, size_t ws_bytes, gma_stream_t stream)
@@ -479,12 +602,12 @@ gma_status_t gma_norm_backward(const gma_norm_grad_t *g, void *ws, size_t ws_byt
     if (!ws_ok(ws, ws_bytes, gma_norm_backward_workspace_size(g))) return GMA_ERR_WORKSPACE;
     if ((r = usable_device()) != GMA_OK) return r;
     cudaStream_t st = (cudaStream_t)stream;
-    const Plan p = plan_grad(D);
+    const Plan p = plan(D);
     const bool vec = vec_common(n) && vec_given(g->dr, rd) && vec_given(g->dh, n.dtype) &&
                      (!g->dh.ptr || rows_vec(n.r, rd)) && rows_vec(g->d_o, n.dtype) &&
                      (g->d_o_head * elem_size(n.dtype)) % 16 == 0 && (!n.gate.ptr || rows_vec(g->dgate, n.dtype)) &&
                      vec_given(g->dresidual, rd);
-    return dispatch(n, vec, p.nv, [&](auto t, auto rt, auto v, auto nv) -> gma_status_t {
+    return dispatch(n, vec, p, [&](auto t, auto rt, auto v, auto nv, auto threads) -> gma_status_t {
         using T = decltype(t);
         using R = decltype(rt);
         NormGradArgs<T, R> a;
@@ -497,10 +620,11 @@ gma_status_t gma_norm_backward(const gma_norm_grad_t *g, void *ws, size_t ws_byt
         a.dresidual = rows_of<R>(g->dresidual);
         a.part = (float *)ws;
         a.pitch = (D + 7) / 8 * 8;
-        const int blocks = grad_blocks(n, p);
+        constexpr int TH = decltype(threads)::value;
+        const int blocks = blocks_of(n, p, BACKWARD_BLOCKS);
         GMA_LAUNCH(KID_NORM_BWD, st,
-                   norm_backward_kernel<T, R, decltype(v)::value, decltype(nv)::value>
-                   <<<blocks, p.threads, p.threads * 8 * sizeof(float), st>>>(a));
+                   norm_backward_kernel<T, R, decltype(v)::value, decltype(nv)::value, TH>
+                   <<<blocks, TH, TH * 8 * sizeof(float), st>>>(a));
         SumOut out[3] = {{g->dw_post, 1}, {g->dscale, 1}, {g->dw_pre, 1}};
         for (int k = 0; k < 3; ++k) {      // neighbouring vectors that are wanted, in one launch
             if (!(k == 0 ? (const void *)n.w_post : k == 1 ? (const void *)n.scale : (const void *)n.w_pre)) continue;

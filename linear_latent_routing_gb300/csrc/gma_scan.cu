@@ -261,12 +261,7 @@ template <typename T, class K, bool VEC> gma_status_t launch_forward(const gma_s
 
 template <typename T, bool VEC> gma_status_t forward_of(const gma_scan_t &s, cudaStream_t st)
 {
-#ifndef VLT
-#define VLT 32
-#define VTL 8
-#define VW 8
-#endif
-    return launch_forward<T, Tile<VLT, VTL, VW>, VEC>(s, st);
+    return launch_forward<T, Tile<32, 8, 8>, VEC>(s, st);
 }
 
 }  // namespace
