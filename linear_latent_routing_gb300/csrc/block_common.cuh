@@ -218,15 +218,16 @@ inline bool rows_vec(const gma_rows_t &r, int dtype)
 inline bool ptr_ok(const void *p, size_t align) { return p && ((uintptr_t)p & (align - 1)) == 0; }
 inline bool opt_ok(const void *p, size_t align) { return ((uintptr_t)p & (align - 1)) == 0; }
 
-// Adds up the first K of `per_row` vectors of n fp32 values (vector stride pitch, row stride
-// per_row * pitch) over `rows` rows in a fixed order: vector k's element i goes to out[k].p[i * out[k].stride].
-struct SumOut {
-    float *p;
-    long long stride;
+// Adds up rows of partial sums in a fixed order, up to MAX_SUMS vectors in one launch: element i of a
+// vector is the sum over r < rows of part[r * row_stride + i], and goes to out[i * out_stride].
+struct SumVec {
+    const float *part;
+    long long row_stride, n;
+    float *out;
+    long long out_stride;
 };
 constexpr int MAX_SUMS = 5;
-gma_status_t sum_rows(const float *part, long long rows, int K, int per_row, int n, int pitch, const SumOut *out,
-                      cudaStream_t st);
+gma_status_t sum_rows(const SumVec *vecs, int count, long long rows, cudaStream_t st);
 
 inline bool ws_ok(const void *ws, size_t have, size_t need)
 {

@@ -6,46 +6,57 @@ namespace gma {
 namespace blk {
 namespace {
 
-struct SumOuts {
-    SumOut o[MAX_SUMS];
+struct SumList {
+    SumVec v[MAX_SUMS];
+    unsigned first[MAX_SUMS + 1];        // first block of each vector
+    int count;
 };
 
 // 32 columns a block (one 128-byte line a row), eight warps of four independent sums each over every
 // 32nd row, then the warps in order.  The partial rows were just written and come from L2.
-__global__ void __launch_bounds__(256) sum_rows_kernel(const float *part, long long rows, long long row_stride, int n,
-                                                       int pitch, const SumOuts outs)
+__global__ void __launch_bounds__(256) sum_rows_kernel(const SumList l, long long rows)
 {
     __shared__ float s[8][33];
+    int k = 0;
+#pragma unroll
+    for (int j = 1; j < MAX_SUMS; ++j)
+        if (j < l.count && blockIdx.x >= l.first[j]) k = j;
+    const SumVec v = l.v[k];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int i = blockIdx.x * 32 + lane, k = blockIdx.y;
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
-    if (i < n) {
-        const float *p = part + (long long)k * pitch + i;
+    const long long i = (long long)(blockIdx.x - l.first[k]) * 32 + lane;
+    float a[4] = {0.f, 0.f, 0.f, 0.f};
+    if (i < v.n) {
+        const float *p = v.part + i;
         long long r = warp;
         for (; r + 24 < rows; r += 32)
 #pragma unroll
-            for (int u = 0; u < 4; ++u) v[u] += p[(r + 8 * u) * row_stride];
-        for (; r < rows; r += 8) v[0] += p[r * row_stride];
+            for (int u = 0; u < 4; ++u) a[u] += p[(r + 8 * u) * v.row_stride];
+        for (; r < rows; r += 8) a[0] += p[r * v.row_stride];
     }
-    s[warp][lane] = (v[0] + v[1]) + (v[2] + v[3]);
+    s[warp][lane] = (a[0] + a[1]) + (a[2] + a[3]);
     __syncthreads();
-    if (warp == 0 && i < n) {
+    if (warp == 0 && i < v.n) {
         float t = 0.f;
 #pragma unroll
         for (int w = 0; w < 8; ++w) t += s[w][lane];
-        outs.o[k].p[i * outs.o[k].stride] = t;
+        v.out[i * v.out_stride] = t;
     }
 }
 
 }  // namespace
 
-gma_status_t sum_rows(const float *part, long long rows, int K, int per_row, int n, int pitch, const SumOut *out,
-                      cudaStream_t st)
+gma_status_t sum_rows(const SumVec *vecs, int count, long long rows, cudaStream_t st)
 {
-    SumOuts o = {};
-    for (int k = 0; k < K; ++k) o.o[k] = out[k];
-    GMA_LAUNCH(KID_SUM_ROWS, st,
-               sum_rows_kernel<<<dim3((n + 31) / 32, K), 256, 0, st>>>(part, rows, (long long)per_row * pitch, n, pitch, o));
+    SumList l = {};
+    unsigned blocks = 0;
+    for (int k = 0; k < count; ++k) {
+        l.v[k] = vecs[k];
+        l.first[k] = blocks;
+        blocks += (unsigned)((vecs[k].n + 31) / 32);
+    }
+    l.count = count;
+    if (blocks == 0) return GMA_OK;
+    GMA_LAUNCH(KID_SUM_ROWS, st, sum_rows_kernel<<<blocks, 256, 0, st>>>(l, rows));
     return GMA_OK;
 }
 

@@ -488,10 +488,11 @@ gma_status_t gma_conv_backward(const gma_conv_grad_t *g, void *ws, size_t ws_byt
         GMA_LAUNCH(KID_CONV_BWD, st,
                    conv_backward_kernel<T, W, decltype(v)::value, decltype(s)::value>
                    <<<dim3((unsigned)(a.gtiles * a.rtiles), c.B), 32 * GWARPS, 0, st>>>(a));
-        SumOut out[W + 1];
-        for (int k = 0; k < W; ++k) out[k] = SumOut{g->dweight + k, W};
-        out[W] = SumOut{g->dbias, 1};
-        return sum_rows(a.part, (long long)a.rtiles * c.B, g->dbias ? W + 1 : W, W + 1, c.D, a.f.groups * C, out, st);
+        const long long width = a.f.groups * C;
+        SumVec vecs[W + 1];
+        for (int k = 0; k < W; ++k) vecs[k] = SumVec{a.part + k * width, (W + 1) * width, c.D, g->dweight + k, W};
+        vecs[W] = SumVec{a.part + W * width, (W + 1) * width, c.D, g->dbias, 1};
+        return sum_rows(vecs, g->dbias ? W + 1 : W, (long long)a.rtiles * c.B, st);
     });
 }
 

@@ -72,7 +72,7 @@ enum KernelId {
     KID_TC_CAUSAL_SCAN, KID_TC_CAUSAL_OUT, KID_TC_LSE, KID_TC_DIVIDE, KID_TC_CAUSAL_FUSED, KID_DECODE = 32, KID_DECODE_PARAMS, KID_USAGE_ROWS, KID_USAGE_MASS, KID_USAGE_STATS, KID_BWD_NUMDEN,
     KID_BWD_DQ, KID_BWD_SCAN, KID_BWD_DK, KID_BWD_DX, KID_BWD_PARAMS, KID_BWD_PFINAL,
     KID_SCAN = 64, KID_SCAN_STEP, KID_SCAN_BWD, KID_SCAN_BC, KID_CONV, KID_CONV_STEP, KID_CONV_BWD, KID_NORM,
-    KID_NORM_BWD, KID_SUM_ROWS, KID_SCAN_STATE, KID_SCAN_JOIN, KID_COUNT
+    KID_NORM_BWD, KID_SUM_ROWS, KID_SCAN_STATE, KID_SCAN_JOIN, KID_SCAN_ADJ, KID_COUNT
 };
 const char *kernel_name(int id);
 void timing_begin(cudaStream_t st, int kernel_id);

@@ -625,16 +625,13 @@ gma_status_t gma_norm_backward(const gma_norm_grad_t *g, void *ws, size_t ws_byt
         GMA_LAUNCH(KID_NORM_BWD, st,
                    norm_backward_kernel<T, R, decltype(v)::value, decltype(nv)::value, TH>
                    <<<blocks, TH, TH * 8 * sizeof(float), st>>>(a));
-        SumOut out[3] = {{g->dw_post, 1}, {g->dscale, 1}, {g->dw_pre, 1}};
-        for (int k = 0; k < 3; ++k) {      // neighbouring vectors that are wanted, in one launch
-            if (!(k == 0 ? (const void *)n.w_post : k == 1 ? (const void *)n.scale : (const void *)n.w_pre)) continue;
-            int e = k + 1;
-            while (e < 3 && (e == 1 ? (const void *)n.scale : (const void *)n.w_pre)) ++e;
-            const gma_status_t q = sum_rows(a.part + (size_t)k * a.pitch, blocks, e - k, 3, D, a.pitch, out + k, st);
-            if (q != GMA_OK) return q;
-            k = e - 1;
-        }
-        return GMA_OK;
+        const float *used[3] = {n.w_post, n.scale, n.w_pre};
+        float *out[3] = {g->dw_post, g->dscale, g->dw_pre};
+        SumVec vecs[3];
+        int count = 0;
+        for (int k = 0; k < 3; ++k)
+            if (used[k]) vecs[count++] = SumVec{a.part + (size_t)k * a.pitch, 3ll * a.pitch, D, out[k], 1};
+        return sum_rows(vecs, count, blocks, st);
     });
 }
 

@@ -4,401 +4,433 @@
 //   g_t = c_t dp_t + r_t,   r_{t-1} = exp(delta_t A) g_t   (r behind the last token: dstate_out),
 //   dc_t = sum_d dp_t h_t,   db_t = sum_d g_t delta_t u_t,   x_t = sum_n b_t g_t,   q_t[n] = r_{t-1} h_{t-1},
 //   du = delta x + D dp,   ddelta = u x + sum_n A q,   dA = sum_t delta q,   ddt = ddelta sigmoid(dt + dt_bias).
-// A block walks over its channels' tiles from the last to the first: each tile's states are computed
-// again from the checkpoint in front of it, then the adjoint recurrence runs from the tile's end.  A lane
-// owns TL neighbouring tokens of two channels (the two halves of its packed registers) and takes one state
-// at a time: its tokens' states stay in registers between the two recurrences, and both are
-// sequential over its own tokens with a scan of (decay, state) over the LT time lanes in between.
-// db and dc are sums over channels: a block adds up its own in shared memory, state by state, and leaves
-// partial sums that a last kernel adds in a fixed order.
+// In four launches:
+//   1, 2. the adjoint r behind every chunk of 64 tokens (each chunk's from zero, then joined);
+//   3. every chunk: a warp walks over its channels' tokens forward from the checkpoint, keeping the state in
+//      front of every eighth token in shared memory; then, eight tokens at a time from the last, it
+//      computes their states again into registers and runs the adjoint back over them;
+//   4. sums of the blocks' partial db and dc, and of the chunks' partial parameter gradients.
+// A lane holds eight states of a channel (S / 8 lanes a channel) and their eight tokens' history in 64
+// registers, so that 16 warps fit an SM; x, q and p are added over a channel's lanes by shuffles.  db and dc are
+// sums over channels: a warp passes its lanes' products through shared memory (lanes write rows, read
+// columns), a block adds its warps, and step 4 the blocks, always in the same order.
 #include "scan_tile.cuh"
 
 namespace gma {
 namespace blk {
 namespace {
 
-constexpr int LT = 16, TL = 8, TT = LT * TL;
-static_assert(TT % CKPT == 0, "a tile starts at a checkpoint");
-constexpr int WARPS = 4, THREADS = 32 * WARPS;
-constexpr int SLOTS = WARPS * (32 / LT);        // lane groups of a block, two channels each
-constexpr int CH = 2 * SLOTS;
-constexpr int NB = 16;                          // states whose b and c are staged at a time
+constexpr int WARPS = 4, THREADS = 32 * WARPS, SUB = 8, SUBS = CKPT / SUB;
+constexpr int NF = 4;                        // pairs of states of a lane
+constexpr float LN2 = 0.69314718055994531f;
 
-// A channel pair's tokens: token t = tl * TL + i at ((i / 2) * LT + tl) * 2 + i % 2, as pairs.
-__device__ __forceinline__ int pos(int t) { return ((t % TL / 2) * LT + t / TL) * 2 + t % 2; }
-constexpr int PITCH = TT + 2;                   // f2 between two channel pairs
-constexpr int PAIRS = SLOTS * PITCH;
+template <int S> struct Lane {
+    static constexpr int SPLIT = S / 8, CHW = 32 / SPLIT, CH = WARPS * CHW;   // lanes of a channel; channels
+};
 
 template <typename T> struct GradArgs {
     ScanArgs<T> f;
+    int chunks;
     Rows<const T> dy;
-    const float *dstate_out;
     Rows<T> du, ddt, dz, db, dc;
-    float *da_log, *dd_skip, *ddt_bias, *dstate_in;
-    float2 *bc_part;     // [G * tiles][B][time tiles][S][TT]: db, dc in the order of pos()
-    float *a_part;       // [B][D][S]
-    float *d_part;       // [2][B][D]: d_skip, dt_bias
+    float *state;        // [B][chunks][D][S]: the adjoint behind each chunk, then the chunk's sums for da_log
+    float *skip, *bias;  // [B][chunks][D]: the chunk's sums for d_skip and dt_bias
+    float *bc_part;      // [G * tiles][B][N][2 S]: per eight states, db then dc
 };
 
-// Sums of delta over 1, 2, 4, ... lanes ending (up) or starting (down) at a lane: exp2(rate * sum) is the
-// decay over them, so the scans over lanes exchange states alone.  FAR marks a window that leaves the
-// tile: its decay is 0 (rates are kept at -1e-30 or below, a decay of exactly 1 for any real delta).
-constexpr float FAR = 3e38f;
-constexpr int STEPS = 4;
-static_assert(LT == 1 << STEPS, "");
-template <bool UP> __device__ __forceinline__ void windows(f2 total, int tl, f2 (&w)[STEPS], f2 &outside)
+// Four neighbouring channels.
+template <bool VEC> __device__ __forceinline__ void load4(const __nv_bfloat16 *p, int n, float (&v)[4])
 {
-    f2 sum = total;
+    if (VEC) {
+        const uint2 q = *reinterpret_cast<const uint2 *>(p);
+        v[0] = __uint_as_float(q.x << 16); v[1] = __uint_as_float(q.x & 0xffff0000u);
+        v[2] = __uint_as_float(q.y << 16); v[3] = __uint_as_float(q.y & 0xffff0000u);
+    } else {
 #pragma unroll
-    for (int k = 0; k < STEPS; ++k) {
-        const bool in = UP ? tl >= 1 << k : tl + (1 << k) < LT;
-        w[k] = in ? sum : pack2(FAR, FAR);
-        const f2 far = UP ? __shfl_up_sync(0xffffffffu, sum, 1 << k, LT) : __shfl_down_sync(0xffffffffu, sum, 1 << k, LT);
-        if (in) sum = add2(sum, far);
+        for (int i = 0; i < 4; ++i) v[i] = i < n ? __bfloat162float(p[i]) : 0.f;
     }
-    // everything before (or behind) the lane
-    outside = UP ? __shfl_up_sync(0xffffffffu, sum, 1, LT) : __shfl_down_sync(0xffffffffu, sum, 1, LT);
-    if (UP ? tl == 0 : tl == LT - 1) outside = 0ull;
 }
-// Inclusive scan of a lane's state, then the state that enters it, `edge` being what enters the tile.
-template <bool UP> __device__ __forceinline__ f2 enter(f2 s, const f2 (&w)[STEPS], f2 outside, f2 inner, f2 r2, f2 edge)
+template <bool VEC> __device__ __forceinline__ void load4(const float *p, int n, float (&v)[4])
 {
+    if (VEC) {
+        const float4 q = *reinterpret_cast<const float4 *>(p);
+        v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+    } else {
 #pragma unroll
-    for (int k = 0; k < STEPS; ++k) {
-        const f2 far = UP ? __shfl_up_sync(0xffffffffu, s, 1 << k, LT) : __shfl_down_sync(0xffffffffu, s, 1 << k, LT);
-        s = fma2(ex2_2(mul2(w[k], r2)), far, s);
+        for (int i = 0; i < 4; ++i) v[i] = i < n ? p[i] : 0.f;
     }
-    s = UP ? __shfl_up_sync(0xffffffffu, s, 1, LT) : __shfl_down_sync(0xffffffffu, s, 1, LT);
-    return fma2(ex2_2(mul2(outside, r2)), edge, mul2(s, inner));
+}
+template <bool VEC> __device__ __forceinline__ void store4(__nv_bfloat16 *p, int n, const float (&v)[4])
+{
+    if (VEC) {
+        uint2 q;
+        __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(&q);
+        h[0] = __floats2bfloat162_rn(v[0], v[1]);
+        h[1] = __floats2bfloat162_rn(v[2], v[3]);
+        *reinterpret_cast<uint2 *>(p) = q;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < n) p[i] = __float2bfloat16_rn(v[i]);
+    }
+}
+template <bool VEC> __device__ __forceinline__ void store4(float *p, int n, const float (&v)[4])
+{
+    if (VEC) {
+        *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < n) p[i] = v[i];
+    }
 }
 
-struct Smem {
-    f2 us[PAIRS], dts[PAIRS], dps[PAIRS];
-    f2 red[2][SLOTS][TT];                       // (db, dc) of a state, by lane group
-    f2 bs[NB][TT], cs[NB][TT];                  // (b, b), (c, c)
-    // then: sums of delta q by lane [S][THREADS], rate, state in front, adjoint behind [S][SLOTS], as pairs
+// One warp's share of shared memory.
+template <int S> struct WarpSmem {
+    static constexpr int CHW = Lane<S>::CHW;
+    f2 start[SUBS][NF][32];                                  // the states in front of every eighth token
+    float red[32][20];                                       // a token's products by lane, 16 and padding
+    float dt[SUB][CHW], u[SUB][CHW], dp[SUB][CHW];           // eight tokens: delta, u, dp
+    float x[SUB][CHW], q[SUB][CHW], p[SUB][CHW];             // and what comes of them
 };
-size_t smem_bytes(int S) { return sizeof(Smem) + (size_t)S * THREADS * sizeof(f2) + (size_t)3 * S * SLOTS * sizeof(f2); }
+template <int S> struct Smem {
+    WarpSmem<S> w[WARPS];
+    f2 sums[2][WARPS][SUB][S];                               // db and dc of eight tokens by warp, in turn
+    float b[CKPT][S], c[CKPT][S];
+};
 
-template <typename T, bool VEC, bool Z>
-__global__ void __launch_bounds__(THREADS) scan_backward_kernel(const GradArgs<T> g)
+template <typename T, int S, bool VEC, bool Z>
+__global__ void __launch_bounds__(THREADS, 3) scan_backward_kernel(const GradArgs<T> g)
 {
+    constexpr int SPLIT = Lane<S>::SPLIT, CHW = Lane<S>::CHW, CH = Lane<S>::CH;
     extern __shared__ __align__(16) unsigned char raw[];
-    Smem &sm = *reinterpret_cast<Smem *>(raw);
+    Smem<S> &sm = *reinterpret_cast<Smem<S> *>(raw);
     const ScanArgs<T> &a = g.f;
-    const int S = a.S, nb = S < NB ? S : NB;
-    f2 *das = reinterpret_cast<f2 *>(raw + sizeof(Smem));
-    f2 *rate = das + S * THREADS, *hs = rate + S * SLOTS, *rs = hs + S * SLOTS;
-
-    const int b = blockIdx.y, group = blockIdx.x / a.tiles, Dg = a.D / a.G;
-    const int in_group = (blockIdx.x - group * a.tiles) * CH;
-    const int c0 = group * Dg + in_group, nch = min(CH, Dg - in_group);
-    const int len = row_length(a.lengths, b, a.N);
-    const int lane = threadIdx.x & 31, tl = lane % LT, slot = (threadIdx.x >> 5) * (32 / LT) + lane / LT;
-    const int nck = (a.N + CKPT - 1) / CKPT, ntt = (a.N + TT - 1) / TT;
-
-    for (int i = threadIdx.x; i < S * SLOTS; i += THREADS) {
-        const int n = i / SLOTS, s = i % SLOTS;
-        float v[2] = {0.f, 0.f}, w[2] = {0.f, 0.f};
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-            if (2 * s + e < nch) {
-                const long long at = (long long)(c0 + 2 * s + e) * S + n;
-                v[e] = fminf(-expf(a.a_log[at]) * LOG2E, -1e-30f);   // see FAR
-                if (g.dstate_out) w[e] = g.dstate_out[(long long)b * a.D * S + at];
-            }
-        rate[i] = pack2(v[0], v[1]);
-        rs[i] = pack2(w[0], w[1]);
+    const int b = blockIdx.z, k = blockIdx.y, t0 = k * CKPT;
+    const int len = row_length(a.lengths, b, a.N), count = min(CKPT, len - t0);
+    const int group = blockIdx.x / a.tiles, Dg = a.D / a.G;
+    if (count <= 0) {                                        // no tokens here; the join has cleared `state`
+        const int i = (blockIdx.x - group * a.tiles) * CH + threadIdx.x;
+        const long long to = ((long long)b * g.chunks + k) * a.D + group * Dg + i;
+        static_assert(CH <= THREADS, "a thread a channel");
+        if (threadIdx.x < CH && i < Dg) g.skip[to] = g.bias[to] = 0.f;
+        return;
     }
-    for (int n = 0; n < S; ++n) das[n * THREADS + threadIdx.x] = 0ull;
-    const int mine = nch - 2 * slot;                 // channels of this lane
-    const f2 skip = pack2(a.d_skip && mine > 0 ? a.d_skip[c0 + 2 * slot] : 0.f,
-                          a.d_skip && mine > 1 ? a.d_skip[c0 + 2 * slot + 1] : 0.f);
-    f2 dskip = 0ull, dbias = 0ull;
-    // 0 for the lane at the tile's edge, which has no neighbour there
-    const f2 inner_up = tl ? pack2(1.f, 1.f) : 0ull, inner_down = tl < LT - 1 ? pack2(1.f, 1.f) : 0ull;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = lane / CHW;
+    const int warp_ch = (blockIdx.x - group * a.tiles) * CH + warp * CHW;        // in the group
+    const bool on = warp_ch + lane % CHW < Dg;
+    const int c = group * Dg + warp_ch + lane % CHW;
+    WarpSmem<S> &ws = sm.w[warp];
 
-    // A thread stages and stores the same eight channels of UNITS tokens of every tile.
-    constexpr int UNITS = TT * (CH / 8) / THREADS, STEP = TT / UNITS;
-    const int piece = threadIdx.x % (CH / 8), token = threadIdx.x / (CH / 8);
-    const int n8 = min(8, nch - piece * 8), cp = c0 + piece * 8;
-    float bias[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) bias[k] = a.dt_bias && k < n8 ? a.dt_bias[cp + k] : 0.f;
+    // b and c of the chunk
+    for (int i = threadIdx.x; i < count * (S / 8); i += THREADS) {
+        const int t = i / (S / 8), piece = i % (S / 8) * 8;
+        float v[8];
+        load8<VEC>(a.b.at(b, t0 + t) + group * S + piece, 8, v);
+        store8<true>(&sm.b[t][piece], 8, v);
+        load8<VEC>(a.c.at(b, t0 + t) + group * S + piece, 8, v);
+        store8<true>(&sm.c[t][piece], 8, v);
+    }
+    for (int i = count * S + threadIdx.x; i < (count + SUB - 1) / SUB * SUB * S; i += THREADS)
+        (&sm.b[0][0])[i] = (&sm.c[0][0])[i] = 0.f;
 
-    for (int t0 = (len - 1) / TT * TT; t0 >= 0 && len > 0; t0 -= TT) {
-        __syncthreads();
+    f2 rate[NF], h[NF], r[NF], da[NF];
+    const long long at = (long long)c * S + part * 8, nck = g.chunks;
+    float *state = g.state + ((long long)b * nck + k) * a.D * S + at;
+    {
+        const float *ck = a.ckpt + ((long long)b * nck + k) * a.D * S + at;
 #pragma unroll
-        for (int j = 0; j < UNITS; ++j) {
-            const int t = token + j * STEP, at = pos(t);
-            const bool on = t0 + t < len && n8 > 0;
-            float u[8], d[8], y[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) u[k] = d[k] = y[k] = 0.f;
+        for (int j = 0; j < NF / 2; ++j) {
+            const float4 v = on ? reinterpret_cast<const float4 *>(a.a_log + at)[j] : make_float4(0.f, 0.f, 0.f, 0.f);
+            rate[2 * j] = on ? pack2(-expf(v.x) * LOG2E, -expf(v.y) * LOG2E) : 0ull;
+            rate[2 * j + 1] = on ? pack2(-expf(v.z) * LOG2E, -expf(v.w) * LOG2E) : 0ull;
+            ulonglong2 w = make_ulonglong2(0ull, 0ull), z = w;
             if (on) {
-                load8<VEC>(a.u.at(b, t0 + t) + cp, n8, u);
-                load8<VEC>(a.dt.at(b, t0 + t) + cp, n8, d);
-                load8<VEC>(g.dy.at(b, t0 + t) + cp, n8, y);
-                if (Z) {
-                    float z[8];
-                    load8<VEC>(a.z.at(b, t0 + t) + cp, n8, z);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) y[k] *= silu(z[k]);
-                }
+                w = reinterpret_cast<const ulonglong2 *>(ck)[j];
+                z = reinterpret_cast<const ulonglong2 *>(state)[j];
             }
-#pragma unroll
-            for (int k = 0; k < 8; k += 2) {
-                const float2 s = unpack2(softplus2(add2(pack2(d[k], d[k + 1]), pack2(bias[k], bias[k + 1]))));
-                const int to = (piece * 4 + k / 2) * PITCH + at;
-                sm.us[to] = pack2(u[k], u[k + 1]);
-                sm.dts[to] = pack2(on && k < n8 ? s.x : 0.f, on && k + 1 < n8 ? s.y : 0.f);
-                sm.dps[to] = pack2(y[k], y[k + 1]);
-            }
+            h[2 * j] = w.x; h[2 * j + 1] = w.y;
+            r[2 * j] = z.x; r[2 * j + 1] = z.y;
+            da[2 * j] = da[2 * j + 1] = 0ull;
         }
-        for (int i = threadIdx.x; i < S * SLOTS; i += THREADS) {
-            const int n = i / SLOTS, s = i % SLOTS;
-            const float *ck = a.ckpt + (((long long)b * nck + t0 / CKPT) * a.D + c0 + 2 * s) * S + n;
-            hs[i] = pack2(2 * s < nch ? ck[0] : 0.f, 2 * s + 1 < nch ? ck[S] : 0.f);
-        }
-        __syncthreads();
+    }
 
-        f2 dt[TL], xu[TL], dp[TL], x2[TL], q2[TL], y2[TL], total = 0ull;
+    // Staging: a lane takes four channels of a token, UNITS times, the same channels every time.
+    constexpr int QUADS = CHW / 4, UNITS = QUADS >= 4 ? QUADS / 4 : 1;
+    const int quad = lane % QUADS, first = lane / QUADS;                         // channels, token
+    constexpr int TSTEP = 32 / QUADS;
+    const int n4 = max(0, min(4, Dg - warp_ch - 4 * quad)), c4 = group * Dg + warp_ch + 4 * quad;
+    float bias[4], skip[4], dskip[4], dbias[4];
 #pragma unroll
-        for (int q = 0; q < TL / 2; ++q) {
-            const int at = slot * PITCH + (q * LT + tl) * 2;
-            const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(sm.dts + at);
-            const ulonglong2 u = *reinterpret_cast<const ulonglong2 *>(sm.us + at);
-            const ulonglong2 p = *reinterpret_cast<const ulonglong2 *>(sm.dps + at);
-            dt[2 * q] = v.x; dt[2 * q + 1] = v.y;
-            xu[2 * q] = mul2(v.x, u.x); xu[2 * q + 1] = mul2(v.y, u.y);
-            dp[2 * q] = p.x; dp[2 * q + 1] = p.y;
-            dskip = fma2(p.x, u.x, dskip);
-            dskip = fma2(p.y, u.y, dskip);
-            total = add2(total, add2(v.x, v.y));
-        }
-#pragma unroll
-        for (int i = 0; i < TL; ++i) x2[i] = q2[i] = y2[i] = 0ull;
-        f2 up[STEPS], down[STEPS], before_sum, behind_sum;
-        windows<true>(total, tl, up, before_sum);
-        windows<false>(total, tl, down, behind_sum);
-        float2 *part = g.bc_part + (((long long)blockIdx.x * a.B + b) * ntt + t0 / TT) * S * TT + threadIdx.x;
-
-        for (int n0 = 0; n0 < S; n0 += nb) {
-            if (n0) __syncthreads();
-            for (int i = threadIdx.x; i < TT * (nb / 8); i += THREADS) {
-                const int t = i % TT, k8 = i / TT * 8, at = pos(t);
-                float v[8], w[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) v[k] = w[k] = 0.f;
-                if (t0 + t < len) {
-                    load8<VEC>(a.b.at(b, t0 + t) + group * S + n0 + k8, 8, v);
-                    load8<VEC>(a.c.at(b, t0 + t) + group * S + n0 + k8, 8, w);
-                }
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    sm.bs[k8 + k][at] = pack2(v[k], v[k]);
-                    sm.cs[k8 + k][at] = pack2(w[k], w[k]);
-                }
-            }
-            __syncthreads();
-            for (int m = 0; m < nb; ++m) {
-                const int n = n0 + m;
-                const f2 r2 = rate[n * SLOTS + slot], before = hs[n * SLOTS + slot];
-                const f2 *bl = sm.bs[m] + tl * 2, *cl = sm.cs[m] + tl * 2;
-                f2 a2[TL], h2[TL], h = 0ull, r = 0ull;
-#pragma unroll
-                for (int q = 0; q < TL / 2; ++q) {
-                    const ulonglong2 bv = *reinterpret_cast<const ulonglong2 *>(bl + q * LT * 2);
-                    a2[2 * q] = ex2_2(mul2(dt[2 * q], r2));
-                    a2[2 * q + 1] = ex2_2(mul2(dt[2 * q + 1], r2));
-                    h2[2 * q] = mul2(bv.x, xu[2 * q]);
-                    h2[2 * q + 1] = mul2(bv.y, xu[2 * q + 1]);
-                    h = fma2(a2[2 * q], h, h2[2 * q]);
-                    h = fma2(a2[2 * q + 1], h, h2[2 * q + 1]);
-                }
-                const f2 hin = enter<true>(h, up, before_sum, inner_up, r2, before);
-                h = hin;
-#pragma unroll
-                for (int i = 0; i < TL; ++i) {
-                    h = fma2(a2[i], h, h2[i]);
-                    h2[i] = h;
-                }
-#pragma unroll
-                for (int q = TL / 2 - 1; q >= 0; --q) {
-                    const ulonglong2 cv = *reinterpret_cast<const ulonglong2 *>(cl + q * LT * 2);
-                    if (Z) {
-                        y2[2 * q + 1] = fma2(cv.y, h2[2 * q + 1], y2[2 * q + 1]);
-                        y2[2 * q] = fma2(cv.x, h2[2 * q], y2[2 * q]);
-                    }
-                    r = mul2(a2[2 * q + 1], fma2(cv.y, dp[2 * q + 1], r));
-                    r = mul2(a2[2 * q], fma2(cv.x, dp[2 * q], r));
-                }
-                r = enter<false>(r, down, behind_sum, inner_down, r2, rs[n * SLOTS + slot]);
-                f2 da = das[n * THREADS + threadIdx.x];
-                f2 *red = sm.red[n & 1][slot] + tl * 2;
-#pragma unroll
-                for (int q = TL / 2 - 1; q >= 0; --q) {
-                    const ulonglong2 bv = *reinterpret_cast<const ulonglong2 *>(bl + q * LT * 2);
-                    const ulonglong2 cv = *reinterpret_cast<const ulonglong2 *>(cl + q * LT * 2);
-                    f2 sum[2];
-#pragma unroll
-                    for (int e = 1; e >= 0; --e) {
-                        const int i = 2 * q + e;
-                        const f2 gr = fma2(e ? cv.y : cv.x, dp[i], r);
-                        const float2 db = unpack2(mul2(gr, xu[i])), dc = unpack2(mul2(h2[i], dp[i]));
-                        sum[e] = pack2(db.x + db.y, dc.x + dc.y);
-                        x2[i] = fma2(gr, e ? bv.y : bv.x, x2[i]);
-                        r = mul2(a2[i], gr);
-                        const f2 w = mul2(r, i ? h2[i ? i - 1 : 0] : hin);
-                        q2[i] = fma2(w, r2, q2[i]);
-                        da = fma2(w, dt[i], da);
-                    }
-                    *reinterpret_cast<ulonglong2 *>(red + q * LT * 2) = make_ulonglong2(sum[0], sum[1]);
-                }
-                das[n * THREADS + threadIdx.x] = da;
-                if (tl == 0) rs[n * SLOTS + slot] = r;
-                // The block's channels, a token a thread, in order.  The other half of `red` takes the next
-                // state meanwhile, so one barrier a state is enough.
-                __syncthreads();
-                f2 v = 0ull;
-#pragma unroll
-                for (int k = 0; k < SLOTS; ++k) v = add2(v, sm.red[n & 1][k][threadIdx.x]);
-                part[n * TT] = unpack2(v);
-            }
-        }
-#pragma unroll
-        for (int q = 0; q < TL / 2; ++q) {
-            const int at = slot * PITCH + (q * LT + tl) * 2;
-            const ulonglong2 uv = *reinterpret_cast<const ulonglong2 *>(sm.us + at);
-            f2 du[2], dd[2], pre[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int i = 2 * q + e;
-                const f2 u = e ? uv.y : uv.x;
-                const float2 d = unpack2(dt[i]);
-                // sigmoid(raw) = 1 - exp(-softplus(raw))
-                const f2 slope = pack2(-expm1f(-d.x), -expm1f(-d.y));
-                dd[e] = mul2(slope, fma2(x2[i], u, mul2(q2[i], pack2(0.69314718055994531f, 0.69314718055994531f))));
-                dbias = add2(dbias, dd[e]);
-                du[e] = fma2(x2[i], dt[i], mul2(skip, dp[i]));
-                pre[e] = fma2(skip, u, y2[i]);
-            }
-            *reinterpret_cast<ulonglong2 *>(sm.us + at) = make_ulonglong2(du[0], du[1]);
-            *reinterpret_cast<ulonglong2 *>(sm.dts + at) = make_ulonglong2(dd[0], dd[1]);
-            if (Z) *reinterpret_cast<ulonglong2 *>(sm.dps + at) = make_ulonglong2(pre[0], pre[1]);
-        }
-        __syncthreads();
+    for (int i = 0; i < 4; ++i) {
+        bias[i] = a.dt_bias && i < n4 ? a.dt_bias[c4 + i] : 0.f;
+        skip[i] = a.d_skip && i < n4 ? a.d_skip[c4 + i] : 0.f;
+        dskip[i] = dbias[i] = 0.f;
+    }
+    auto put4 = [](float *to, const float (&v)[4]) { *reinterpret_cast<float4 *>(to) = make_float4(v[0], v[1], v[2], v[3]); };
+    auto get4 = [](const float *from, float (&v)[4]) {
+        const float4 q = *reinterpret_cast<const float4 *>(from);
+        v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+    };
+    // delta and u (and dp) of eight tokens; zeros behind the last one and for channels that are not there
+    auto stage = [&](int s, bool grad) {
 #pragma unroll
         for (int j = 0; j < UNITS; ++j) {
-            const int t = token + j * STEP, at = pos(t);
-            if (t0 + t >= len || n8 <= 0) continue;
-            float v[8];
-            auto gather = [&](const f2 *tile) {
+            const int i = first + j * TSTEP, t = s * SUB + i;
+            if (i >= SUB) continue;
+            float u[4] = {0.f, 0.f, 0.f, 0.f}, d[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
+            if (t < count && n4 > 0) {
+                load4<VEC>(a.u.at(b, t0 + t) + c4, n4, u);
+                load4<VEC>(a.dt.at(b, t0 + t) + c4, n4, d);
+                if (grad) {
+                    load4<VEC>(g.dy.at(b, t0 + t) + c4, n4, y);
+                    if (Z) {
+                        float z[4];
+                        load4<VEC>(a.z.at(b, t0 + t) + c4, n4, z);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float2 w = unpack2(tile[(piece * 4 + k) * PITCH + at]);
-                    v[2 * k] = w.x;
-                    v[2 * k + 1] = w.y;
+                        for (int e = 0; e < 4; ++e) y[e] *= silu(z[e]);
+                    }
                 }
-            };
-            gather(sm.us);
-            store8<VEC>(g.du.at(b, t0 + t) + cp, n8, v);
-            gather(sm.dts);
-            store8<VEC>(g.ddt.at(b, t0 + t) + cp, n8, v);
-            if (Z) {
-                float z[8], y[8];
-                load8<VEC>(a.z.at(b, t0 + t) + cp, n8, z);
-                load8<VEC>(g.dy.at(b, t0 + t) + cp, n8, y);
-                gather(sm.dps);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) v[k] *= y[k] * dsilu(z[k], sigmoid(z[k]));
-                store8<VEC>(g.dz.at(b, t0 + t) + cp, n8, v);
+                for (int e = 0; e < 4; e += 2) {
+                    const float2 v = unpack2(softplus2(pack2(d[e] + bias[e], d[e + 1] + bias[e + 1])));
+                    d[e] = e < n4 ? v.x : 0.f;
+                    d[e + 1] = e + 1 < n4 ? v.y : 0.f;
+                }
+            }
+            put4(&ws.u[i][4 * quad], u);
+            put4(&ws.dt[i][4 * quad], d);
+            if (grad) {
+                put4(&ws.dp[i][4 * quad], y);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) dskip[e] = fmaf(y[e], u[e], dskip[e]);
             }
         }
-    }
+    };
+    const int subs = (count + SUB - 1) / SUB, lc = lane % CHW;
     __syncthreads();
-    for (int i = threadIdx.x; i < S * SLOTS; i += THREADS) {
-        const int n = i % S, s = i / S;
-        // the pair's time lanes, in order
-        const f2 *lanes = das + n * THREADS + s * LT;
-        f2 v = 0ull;
+
+    // forward: the state in front of every eighth token
+    for (int s = 0;; ++s) {
 #pragma unroll
-        for (int l = 0; l < LT; ++l) v = add2(v, lanes[l]);
-        const float2 da = unpack2(mul2(mul2(v, rate[n * SLOTS + s]), pack2(0.69314718055994531f, 0.69314718055994531f)));
-        const float2 r = unpack2(rs[n * SLOTS + s]);
+        for (int j = 0; j < NF; ++j) ws.start[s][j][lane] = h[j];
+        if (s == subs - 1) break;
+        __syncwarp();
+        stage(s, false);
+        __syncwarp();
+#pragma unroll 4
+        for (int i = 0; i < SUB; ++i) {
+            const float d = ws.dt[i][lc], x = d * ws.u[i][lc];
+            const f2 d2 = pack2(d, d), x2 = pack2(x, x);
+            const ulonglong2 *bp = reinterpret_cast<const ulonglong2 *>(&sm.b[s * SUB + i][part * 8]);
+            const ulonglong2 b0 = bp[0], b1 = bp[1];
+            h[0] = fma2(ex2_2(mul2(d2, rate[0])), h[0], mul2(x2, b0.x));
+            h[1] = fma2(ex2_2(mul2(d2, rate[1])), h[1], mul2(x2, b0.y));
+            h[2] = fma2(ex2_2(mul2(d2, rate[2])), h[2], mul2(x2, b1.x));
+            h[3] = fma2(ex2_2(mul2(d2, rate[3])), h[3], mul2(x2, b1.y));
+        }
+    }
+
+    // back, eight tokens at a time
+    for (int s = subs - 1; s >= 0; --s) {
+        __syncwarp();
+        stage(s, true);
+        __syncwarp();
+        f2 hist[SUB + 1][NF];
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-            if (2 * s + e < nch) {
-                const long long at = ((long long)b * a.D + c0 + 2 * s + e) * S + n;
-                g.a_part[at] = e ? da.y : da.x;
-                if (g.dstate_in) g.dstate_in[at] = e ? r.y : r.x;
+        for (int j = 0; j < NF; ++j) hist[0][j] = ws.start[s][j][lane];
+#pragma unroll
+        for (int i = 0; i < SUB; ++i) {
+            const float d = ws.dt[i][lc], x = d * ws.u[i][lc];
+            const f2 d2 = pack2(d, d), x2 = pack2(x, x);
+            const ulonglong2 *bp = reinterpret_cast<const ulonglong2 *>(&sm.b[s * SUB + i][part * 8]);
+            const ulonglong2 b0 = bp[0], b1 = bp[1];
+            hist[i + 1][0] = fma2(ex2_2(mul2(d2, rate[0])), hist[i][0], mul2(x2, b0.x));
+            hist[i + 1][1] = fma2(ex2_2(mul2(d2, rate[1])), hist[i][1], mul2(x2, b0.y));
+            hist[i + 1][2] = fma2(ex2_2(mul2(d2, rate[2])), hist[i][2], mul2(x2, b1.x));
+            hist[i + 1][3] = fma2(ex2_2(mul2(d2, rate[3])), hist[i][3], mul2(x2, b1.y));
+        }
+#pragma unroll
+        for (int i = SUB - 1; i >= 0; --i) {
+            const float d = ws.dt[i][lc], xu = d * ws.u[i][lc], dpv = ws.dp[i][lc];
+            const f2 d2 = pack2(d, d), xu2 = pack2(xu, xu), dp2 = pack2(dpv, dpv);
+            const ulonglong2 *bp = reinterpret_cast<const ulonglong2 *>(&sm.b[s * SUB + i][part * 8]);
+            const ulonglong2 *cp = reinterpret_cast<const ulonglong2 *>(&sm.c[s * SUB + i][part * 8]);
+            const ulonglong2 b0 = bp[0], b1 = bp[1], v0 = cp[0], v1 = cp[1];
+            const f2 bv[NF] = {b0.x, b0.y, b1.x, b1.y}, cv[NF] = {v0.x, v0.y, v1.x, v1.y};
+            f2 x2 = 0ull, q2 = 0ull, p2 = 0ull, db[NF], dc[NF];
+#pragma unroll
+            for (int j = 0; j < NF; ++j) {
+                const f2 gr = fma2(cv[j], dp2, r[j]);
+                db[j] = mul2(gr, xu2);
+                dc[j] = mul2(hist[i + 1][j], dp2);
+                x2 = fma2(gr, bv[j], x2);
+                if (Z) p2 = fma2(cv[j], hist[i + 1][j], p2);
+                r[j] = mul2(ex2_2(mul2(d2, rate[j])), gr);
+                const f2 w = mul2(r[j], hist[i][j]);
+                q2 = fma2(w, rate[j], q2);
+                da[j] = fma2(w, d2, da[j]);
             }
+            ulonglong2 *row = reinterpret_cast<ulonglong2 *>(ws.red[lane]);
+            row[0] = make_ulonglong2(db[0], db[1]);
+            row[1] = make_ulonglong2(db[2], db[3]);
+            row[2] = make_ulonglong2(dc[0], dc[1]);
+            row[3] = make_ulonglong2(dc[2], dc[3]);
+            const float2 xs = unpack2(x2), qs = unpack2(q2), ps = unpack2(p2);
+            float xv = xs.x + xs.y, qv = qs.x + qs.y, pv = ps.x + ps.y;
+#pragma unroll
+            for (int off = CHW; off < 32; off *= 2) {
+                xv += __shfl_xor_sync(0xffffffffu, xv, off);
+                qv += __shfl_xor_sync(0xffffffffu, qv, off);
+                if (Z) pv += __shfl_xor_sync(0xffffffffu, pv, off);
+            }
+            if (part == 0) {
+                ws.x[i][lc] = xv;
+                ws.q[i][lc] = qv;
+                if (Z) ws.p[i][lc] = pv;
+            }
+            __syncwarp();
+            // columns: pair j of part `of` over that part's CHW lanes, eight of them a lane
+            constexpr int COLS = 8 * SPLIT;
+            if (COLS <= 32) {
+                const int col = lane % COLS, from = lane / COLS * 8, of = col / 8, j = col % 8;
+                const f2 *src = reinterpret_cast<const f2 *>(&ws.red[of * CHW + from][2 * j]);
+                f2 v = src[0];
+#pragma unroll
+                for (int l = 1; l < 8; ++l) v = add2(v, src[10 * l]);
+#pragma unroll
+                for (int off = COLS; off < 32; off *= 2) v = add2(v, __shfl_xor_sync(0xffffffffu, v, off));
+                if (lane < COLS) sm.sums[s & 1][warp][i][col] = v;
+            } else {
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    const int col = lane + 32 * m, of = col / 8, j = col % 8;
+                    const f2 *src = reinterpret_cast<const f2 *>(&ws.red[of * CHW][2 * j]);
+                    f2 v = src[0];
+#pragma unroll
+                    for (int l = 1; l < (CHW < 8 ? CHW : 8); ++l) v = add2(v, src[10 * l]);
+                    sm.sums[s & 1][warp][i][col] = v;
+                }
+            }
+            __syncwarp();
+        }
+#pragma unroll
+        for (int j = 0; j < UNITS; ++j) {
+            const int i = first + j * TSTEP, t = s * SUB + i;
+            if (i >= SUB || t >= count || n4 <= 0) continue;
+            float u[4], d[4], dp[4], x[4], q[4], v[4];
+            get4(&ws.u[i][4 * quad], u);
+            get4(&ws.dt[i][4 * quad], d);
+            get4(&ws.dp[i][4 * quad], dp);
+            get4(&ws.x[i][4 * quad], x);
+            get4(&ws.q[i][4 * quad], q);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = fmaf(x[e], d[e], skip[e] * dp[e]);
+            store4<VEC>(g.du.at(b, t0 + t) + c4, n4, v);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                // sigmoid(raw) = 1 - exp(-softplus(raw))
+                v[e] = -expm1f(-d[e]) * fmaf(x[e], u[e], q[e] * LN2);
+                dbias[e] += v[e];
+            }
+            store4<VEC>(g.ddt.at(b, t0 + t) + c4, n4, v);
+            if (Z) {
+                float z[4], y[4], p[4];
+                load4<VEC>(a.z.at(b, t0 + t) + c4, n4, z);
+                load4<VEC>(g.dy.at(b, t0 + t) + c4, n4, y);
+                get4(&ws.p[i][4 * quad], p);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = y[e] * fmaf(skip[e], u[e], p[e]) * dsilu(z[e], sigmoid(z[e]));
+                store4<VEC>(g.dz.at(b, t0 + t) + c4, n4, v);
+            }
+        }
+        // the block's warps; the other half of `sums` takes the next eight tokens meanwhile
+        __syncthreads();
+        const long long row0 = ((long long)blockIdx.x * a.B + b) * a.N + t0 + s * SUB;
+        for (int i = threadIdx.x; i < SUB * S; i += THREADS) {
+            if (s * SUB + i / S >= count) continue;
+            f2 v = sm.sums[s & 1][0][i / S][i % S];
+#pragma unroll
+            for (int w = 1; w < WARPS; ++w) v = add2(v, sm.sums[s & 1][w][i / S][i % S]);
+            *reinterpret_cast<f2 *>(g.bc_part + (row0 + i / S) * 2 * S + 2 * (i % S)) = v;
+        }
+    }
+
+    // the chunk's sums for the parameters
+    if (on) {
+#pragma unroll
+        for (int j = 0; j < NF / 2; ++j)
+            reinterpret_cast<ulonglong2 *>(state)[j] =
+                make_ulonglong2(mul2(mul2(da[2 * j], rate[2 * j]), pack2(LN2, LN2)),
+                                mul2(mul2(da[2 * j + 1], rate[2 * j + 1]), pack2(LN2, LN2)));
     }
 #pragma unroll
-    for (int off = LT / 2; off; off >>= 1) {
-        dskip = add2(dskip, __shfl_xor_sync(0xffffffffu, dskip, off));
-        dbias = add2(dbias, __shfl_xor_sync(0xffffffffu, dbias, off));
-    }
-    if (tl == 0) {
-        const float2 s = unpack2(dskip), t = unpack2(dbias);
-        float *p = g.d_part + (long long)b * a.D + c0 + 2 * slot;
-        if (mine > 0) p[0] = s.x, p[(long long)a.B * a.D] = t.x;
-        if (mine > 1) p[1] = s.y, p[(long long)a.B * a.D + 1] = t.y;
+    for (int off = QUADS; off < 32; off *= 2)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            dskip[e] += __shfl_xor_sync(0xffffffffu, dskip[e], off);
+            dbias[e] += __shfl_xor_sync(0xffffffffu, dbias[e], off);
+        }
+    if (first == 0) {
+        const long long to = ((long long)b * g.chunks + k) * a.D + c4;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (e < n4) {
+                g.skip[to + e] = dskip[e];
+                g.bias[to + e] = dbias[e];
+            }
     }
 }
 
-// db and dc: the groups' blocks of channels in order.  A block takes eight states of a time tile, a
-// thread a token and four of them.
-template <typename T> __global__ void __launch_bounds__(2 * TT) scan_bc_kernel(const GradArgs<T> g)
+// db and dc: the groups' blocks of channels in order, four states a thread.
+template <typename T> __global__ void __launch_bounds__(256) scan_bc_kernel(const GradArgs<T> g)
 {
     const ScanArgs<T> &a = g.f;
-    const int b = blockIdx.y, tile = blockIdx.x, group = blockIdx.z / (a.S / 8);
-    const int n0 = blockIdx.z % (a.S / 8) * 8 + threadIdx.x / TT * 4, i = threadIdx.x % TT;
-    const int len = row_length(a.lengths, b, a.N), ntt = (a.N + TT - 1) / TT;
-    const int t = tile * TT + i;
-    if (t >= len) return;
-    const float2 *p = g.bc_part + ((((long long)group * a.tiles * a.B + b) * ntt + tile) * a.S + n0) * TT + pos(i);
-    const long long step = (long long)a.B * ntt * a.S * TT;
-    float2 s[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) s[k] = make_float2(0.f, 0.f);
-#pragma unroll 4
-    for (int c = 0; c < a.tiles; ++c)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float2 v = p[c * step + k * TT];
-            s[k].x += v.x;
-            s[k].y += v.y;
-        }
-    T *db = g.db.at(b, t) + group * a.S + n0, *dc = g.dc.at(b, t) + group * a.S + n0;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        db[k] = from_f32<T>(s[k].x);
-        dc[k] = from_f32<T>(s[k].y);
+    const int per = a.S / 2;                                  // float4 of a token and group
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+    const int q = (int)(i % per), b = blockIdx.y, group = blockIdx.z;
+    const long long t = i / per;
+    if (t >= row_length(a.lengths, b, a.N)) return;
+    const float4 *p = reinterpret_cast<const float4 *>(g.bc_part) + (((long long)group * a.tiles * a.B + b) * a.N + t) * per + q;
+    const long long step = (long long)a.B * a.N * per;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int k = 0; k < a.tiles; ++k) {
+        const float4 v = p[k * step];
+        s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
     }
+    // per eight states: db, then dc
+    T *out = (q % 4 < 2 ? g.db : g.dc).at(b, (int)t) + group * a.S + q / 4 * 8 + q % 2 * 4;
+    out[0] = from_f32<T>(s.x); out[1] = from_f32<T>(s.y); out[2] = from_f32<T>(s.z); out[3] = from_f32<T>(s.w);
 }
+
+int channels_of(int S) { return S == 8 ? Lane<8>::CH : S == 16 ? Lane<16>::CH : S == 32 ? Lane<32>::CH : Lane<64>::CH; }
 
 struct Layout {
-    size_t bc, a, d, total;
+    size_t bc, state, total, skip, bias, size;
 };
 Layout layout(const gma_scan_t &s)
 {
-    const size_t tiles = (s.D / s.G + CH - 1) / CH, ntt = (s.N + TT - 1) / TT;
+    const size_t tiles = (s.D / s.G + channels_of(s.S) - 1) / channels_of(s.S), chunks = (s.N + CKPT - 1) / CKPT;
+    const size_t row = align_up((size_t)s.B * chunks * s.D * sizeof(float), 256);
     Layout l;
     l.bc = 0;
-    l.a = align_up(s.G * tiles * s.B * ntt * TT * 2 * s.S * sizeof(float), 256);
-    l.d = l.a + align_up((size_t)s.B * s.D * s.S * sizeof(float), 256);
-    l.total = l.d + align_up((size_t)2 * s.B * s.D * sizeof(float), 256);
+    l.state = align_up(s.G * tiles * s.B * s.N * 2 * s.S * sizeof(float), 256);
+    l.skip = l.state + align_up((size_t)s.B * chunks * s.D * s.S * sizeof(float), 256);
+    l.bias = l.skip + row;
+    l.total = l.bias;                        // read before the gradients of dt_bias are written
+    l.size = l.bias + row;
     return l;
 }
 
-template <typename T, bool VEC, bool Z> gma_status_t launch_backward(const GradArgs<T> &g, cudaStream_t st)
+template <typename T, int S> gma_status_t launch(const GradArgs<T> &g, bool vec, cudaStream_t st)
 {
-    auto kern = scan_backward_kernel<T, VEC, Z>;
-    const size_t smem = smem_bytes(g.f.S);
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    const bool z = g.f.z.p != nullptr;
+    auto kern = vec ? (z ? scan_backward_kernel<T, S, true, true> : scan_backward_kernel<T, S, true, false>)
+                    : (z ? scan_backward_kernel<T, S, false, true> : scan_backward_kernel<T, S, false, false>);
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<S>)) != cudaSuccess)
         return GMA_ERR_CUDA;
-    GMA_LAUNCH(KID_SCAN_BWD, st, kern<<<dim3(g.f.tiles * g.f.G, g.f.B), THREADS, smem, st>>>(g));
+    GMA_LAUNCH(KID_SCAN_BWD, st, kern<<<dim3(g.f.tiles * g.f.G, g.chunks, g.f.B), THREADS, sizeof(Smem<S>), st>>>(g));
     return GMA_OK;
 }
 
@@ -406,35 +438,31 @@ template <typename T> gma_status_t backward_of(const gma_scan_grad_t &s, char *w
 {
     const gma_scan_t &f = s.fwd;
     const Layout l = layout(f);
+    const int ch = channels_of(f.S);
     GradArgs<T> g;
     g.f = scan_args<T>(f);
-    g.f.tiles = (f.D / f.G + CH - 1) / CH;
+    g.f.tiles = (f.D / f.G + ch - 1) / ch;
+    g.chunks = (f.N + CKPT - 1) / CKPT;
     g.dy = rows_of<const T>(s.dy);
-    g.dstate_out = s.dstate_out;
     g.du = rows_of<T>(s.du); g.ddt = rows_of<T>(s.ddt); g.dz = rows_of<T>(s.dz);
     g.db = rows_of<T>(s.db); g.dc = rows_of<T>(s.dc);
-    g.da_log = s.da_log; g.dd_skip = s.dd_skip; g.ddt_bias = s.ddt_bias; g.dstate_in = s.dstate_in;
-    g.bc_part = (float2 *)(ws + l.bc); g.a_part = (float *)(ws + l.a); g.d_part = (float *)(ws + l.d);
+    g.bc_part = (float *)(ws + l.bc); g.state = (float *)(ws + l.state);
+    g.skip = (float *)(ws + l.skip); g.bias = (float *)(ws + l.bias);
+    gma_status_t r = scan_chunk_adjoint(s, g.state, (float *)(ws + l.total), st);
+    if (r != GMA_OK) return r;
     const int dt = f.dtype;
     const bool vec = scan_vec(f) && rows_vec(s.dy, dt) && rows_vec(s.du, dt) && rows_vec(s.ddt, dt) &&
                      (!f.z.ptr || rows_vec(s.dz, dt));
-    gma_status_t r;
-    if (f.z.ptr) r = vec ? launch_backward<T, true, true>(g, st) : launch_backward<T, false, true>(g, st);
-    else r = vec ? launch_backward<T, true, false>(g, st) : launch_backward<T, false, false>(g, st);
+    r = f.S == 8 ? launch<T, 8>(g, vec, st) : f.S == 16 ? launch<T, 16>(g, vec, st)
+      : f.S == 32 ? launch<T, 32>(g, vec, st) : launch<T, 64>(g, vec, st);
     if (r != GMA_OK) return r;
-    GMA_LAUNCH(KID_SCAN_BC, st,
-               scan_bc_kernel<T><<<dim3((f.N + TT - 1) / TT, f.B, f.G * (f.S / 8)), 2 * TT, 0, st>>>(g));
-    const SumOut da = {s.da_log, 1};
-    if ((r = sum_rows(g.a_part, f.B, 1, 1, f.D * f.S, f.D * f.S, &da, st)) != GMA_OK) return r;
-    if (f.d_skip) {
-        const SumOut o = {s.dd_skip, 1};
-        if ((r = sum_rows(g.d_part, f.B, 1, 1, f.D, f.D, &o, st)) != GMA_OK) return r;
-    }
-    if (f.dt_bias) {
-        const SumOut o = {s.ddt_bias, 1};
-        if ((r = sum_rows(g.d_part + (size_t)f.B * f.D, f.B, 1, 1, f.D, f.D, &o, st)) != GMA_OK) return r;
-    }
-    return GMA_OK;
+    const long long threads = (long long)f.N * (f.S / 2);
+    GMA_LAUNCH(KID_SCAN_BC, st, scan_bc_kernel<T><<<dim3((unsigned)((threads + 255) / 256), f.B, f.G), 256, 0, st>>>(g));
+    SumVec v[3] = {{g.state, (long long)f.D * f.S, (long long)f.D * f.S, s.da_log, 1}};
+    int count = 1;
+    if (f.d_skip) v[count++] = SumVec{g.skip, f.D, f.D, s.dd_skip, 1};
+    if (f.dt_bias) v[count++] = SumVec{g.bias, f.D, f.D, s.ddt_bias, 1};
+    return sum_rows(v, count, (long long)f.B * g.chunks, st);
 }
 
 }  // namespace
@@ -449,7 +477,7 @@ extern "C" {
 size_t gma_scan_backward_workspace_size(const gma_scan_grad_t *g)
 {
     if (!g || scan_check(&g->fwd, false) != GMA_OK) return 0;
-    return layout(g->fwd).total;
+    return layout(g->fwd).size;
 }
 
 gma_status_t gma_scan_backward(const gma_scan_grad_t *g, void *ws, size_t ws_bytes, gma_stream_t stream)
@@ -467,8 +495,8 @@ gma_status_t gma_scan_backward(const gma_scan_grad_t *g, void *ws, size_t ws_byt
     if (!ptr_ok(g->da_log, 4) || (f.d_skip && !ptr_ok(g->dd_skip, 4)) || (f.dt_bias && !ptr_ok(g->ddt_bias, 4)) ||
         !opt_ok(g->dstate_out, 4) || !opt_ok(g->dstate_in, 4))
         return GMA_ERR_INVALID_ARG;
-    if (D * f.S > 0x7fffffffll || GS / 8 > 65535) return GMA_ERR_UNSUPPORTED_SHAPE;
-    if (!ws_ok(ws, ws_bytes, layout(f).total)) return GMA_ERR_WORKSPACE;
+    if (D * f.S > 0x3fffffffll || f.G > 65535 || (N + CKPT - 1) / CKPT > 65535) return GMA_ERR_UNSUPPORTED_SHAPE;
+    if (!ws_ok(ws, ws_bytes, layout(f).size)) return GMA_ERR_WORKSPACE;
     if ((r = usable_device()) != GMA_OK) return r;
     cudaStream_t st = (cudaStream_t)stream;
     return f.dtype == GMA_BF16 ? backward_of<__nv_bfloat16>(*g, (char *)ws, st) : backward_of<float>(*g, (char *)ws, st);

@@ -116,10 +116,14 @@ template <int S> __device__ __forceinline__ void store_state(float *p, bool on, 
         if (on) reinterpret_cast<ulonglong2 *>(p)[q] = make_ulonglong2(h[2 * q], h[2 * q + 1]);
 }
 
-// OUT: step 3 (states from `state`, or state_in for a single chunk), else step 1.
-template <typename T, int S, bool VEC, bool OUT>
+// STATE: step 1.  OUTPUT: step 3 (states from `state`, or state_in for a single chunk).  ADJOINT: step 1 of
+// the backward pass, over the tokens from the last one back: r = exp(delta A) (c dp + r), where the rows
+// of dy come in u's place.
+enum Mode { STATE, OUTPUT, ADJOINT };
+template <typename T, int S, bool VEC, Mode MODE>
 __global__ void __launch_bounds__(256, 2) scan_chunk_kernel(const ChunkArgs<T> g, bool vec_bc)
 {
+    constexpr bool OUT = MODE == OUTPUT, ADJ = MODE == ADJOINT;
     constexpr int CPL = Lanes<S>::CPL, SL = Lanes<S>::SL, SPLIT = Lanes<S>::SPLIT, CH_WARP = Lanes<S>::CH_WARP;
     extern __shared__ __align__(16) float rows_s[];
     const ScanArgs<T> &a = g.s;
@@ -142,7 +146,7 @@ __global__ void __launch_bounds__(256, 2) scan_chunk_kernel(const ChunkArgs<T> g
         return;
     }
     float *bs = rows_s, *cs = rows_s + g.chunk * S;
-    stage_rows<T, S>(a.b, vec_bc, b, group * S, t0, count, bs);
+    stage_rows<T, S>(ADJ ? a.c : a.b, vec_bc, b, group * S, t0, count, bs);
     if (OUT) stage_rows<T, S>(a.c, vec_bc, b, group * S, t0, count, cs);
     bs += part * SL;
     cs += part * SL;
@@ -168,7 +172,8 @@ __global__ void __launch_bounds__(256, 2) scan_chunk_kernel(const ChunkArgs<T> g
     T *yp = OUT ? a.y.at(b, t0) + c : nullptr;
     auto token = [&](int t, float2 uu, float2 dd, float2 zz) {
         const float2 dt = unpack2(softplus2(add2(pack2(dd.x, dd.y), pack2(bias.x, bias.y))));
-        const float de[2] = {dt.x, dt.y}, xe[2] = {dt.x * uu.x, dt.y * uu.y};
+        if (ADJ && a.z.p) uu = make_float2(uu.x * silu(zz.x), CPL == 2 ? uu.y * silu(zz.y) : 0.f);
+        const float de[2] = {dt.x, dt.y}, xe[2] = {ADJ ? uu.x : dt.x * uu.x, ADJ ? uu.y : dt.y * uu.y};
         f2 y[CPL], dt2[CPL], xu2[CPL];
 #pragma unroll
         for (int e = 0; e < CPL; ++e) {
@@ -187,8 +192,14 @@ __global__ void __launch_bounds__(256, 2) scan_chunk_kernel(const ChunkArgs<T> g
             if (OUT) c2 = reinterpret_cast<const ulonglong2 *>(cs + t * S)[q];
 #pragma unroll
             for (int e = 0; e < CPL; ++e) {
-                h[e][2 * q] = fma2(ex2_2(mul2(dt2[e], r[e][2 * q])), h[e][2 * q], mul2(xu2[e], b2.x));
-                h[e][2 * q + 1] = fma2(ex2_2(mul2(dt2[e], r[e][2 * q + 1])), h[e][2 * q + 1], mul2(xu2[e], b2.y));
+                const f2 a0 = ex2_2(mul2(dt2[e], r[e][2 * q])), a1 = ex2_2(mul2(dt2[e], r[e][2 * q + 1]));
+                if (ADJ) {
+                    h[e][2 * q] = mul2(a0, fma2(xu2[e], b2.x, h[e][2 * q]));
+                    h[e][2 * q + 1] = mul2(a1, fma2(xu2[e], b2.y, h[e][2 * q + 1]));
+                } else {
+                    h[e][2 * q] = fma2(a0, h[e][2 * q], mul2(xu2[e], b2.x));
+                    h[e][2 * q + 1] = fma2(a1, h[e][2 * q + 1], mul2(xu2[e], b2.y));
+                }
                 if (OUT) {
                     y[e] = fma2(c2.x, h[e][2 * q], y[e]);
                     y[e] = fma2(c2.y, h[e][2 * q + 1], y[e]);
@@ -218,12 +229,12 @@ __global__ void __launch_bounds__(256, 2) scan_chunk_kernel(const ChunkArgs<T> g
         const int first = warp_ch + seg * (16 / (int)sizeof(T));
         const bool mine = first < Dg;
         const T *up = a.u.at(b, t0) + group * Dg + first, *dp = a.dt.at(b, t0) + group * Dg + first;
-        const T *zp = OUT && a.z.p ? a.z.at(b, t0) + group * Dg + first : nullptr;
+        const T *zp = (OUT || ADJ) && a.z.p ? a.z.at(b, t0) + group * Dg + first : nullptr;
         auto fetch = [&](int at, int stage) {
 #pragma unroll
             for (int i = 0; i < TOK; i += PER) {
-                const int t = at + i + sub;
-                if (mine && t < count) {
+                const int step = at + i + sub, t = ADJ ? count - 1 - step : step;
+                if (mine && step < count) {
                     const uint32_t to = ring_at + stage * STAGE_BYTES + (i + sub) * ROW + seg * 16;
                     cp_async16(to, up + t * a.u.st);
                     cp_async16(to + 1024, dp + t * a.dt.st);
@@ -244,16 +255,18 @@ __global__ void __launch_bounds__(256, 2) scan_chunk_kernel(const ChunkArgs<T> g
 #pragma unroll 2
             for (int i = 0; i < m; ++i) {
                 const T *p = s + i * CH_WARP;
-                const float2 z = OUT ? load_ch<CPL, true>(p + 2048 / (int)sizeof(T), CPL) : make_float2(0.f, 0.f);
-                token(at + i, load_ch<CPL, true>(p, CPL), load_ch<CPL, true>(p + 1024 / (int)sizeof(T), CPL), z);
+                const float2 z = OUT || ADJ ? load_ch<CPL, true>(p + 2048 / (int)sizeof(T), CPL) : make_float2(0.f, 0.f);
+                token(ADJ ? count - 1 - at - i : at + i, load_ch<CPL, true>(p, CPL), load_ch<CPL, true>(p + 1024 / (int)sizeof(T), CPL), z);
             }
             stage = stage == 2 ? 0 : stage + 1;
         }
     } else {
-        const T *up = a.u.at(b, t0) + c, *dp = a.dt.at(b, t0) + c, *zp = OUT && a.z.p ? a.z.at(b, t0) + c : nullptr;
-        for (int t = 0; t < count; ++t)
+        const T *up = a.u.at(b, t0) + c, *dp = a.dt.at(b, t0) + c, *zp = (OUT || ADJ) && a.z.p ? a.z.at(b, t0) + c : nullptr;
+        for (int i = 0; i < count; ++i) {
+            const int t = ADJ ? count - 1 - i : i;
             token(t, load_ch<CPL, false>(up + t * a.u.st, n), load_ch<CPL, false>(dp + t * a.dt.st, n),
                   zp ? load_ch<CPL, false>(zp + t * a.z.st, n) : make_float2(0.f, 0.f));
+        }
     }
 #pragma unroll
     for (int e = 0; e < CPL; ++e) {
@@ -266,8 +279,10 @@ __global__ void __launch_bounds__(256, 2) scan_chunk_kernel(const ChunkArgs<T> g
     }
 }
 
-// Step 2: one state a thread, the next chunks' loads in flight.
-template <typename T, int S> __global__ void __launch_bounds__(128) scan_chunk_join_kernel(const ChunkArgs<T> g)
+// Step 2: one state a thread, the next chunks' loads in flight.  BACK: from the last chunk to the first, for
+// the backward pass, whose `state_in` is dstate_out and `state_out` dstate_in; the rows of the chunks behind a
+// sequence's end are cleared (they are added up later, with those of the others).
+template <typename T, int S, bool BACK> __global__ void __launch_bounds__(128) scan_chunk_join_kernel(const ChunkArgs<T> g)
 {
     constexpr int AHEAD = 16;
     const ScanArgs<T> &a = g.s;
@@ -286,18 +301,21 @@ template <typename T, int S> __global__ void __launch_bounds__(128) scan_chunk_j
 #pragma unroll
         for (int j = 0; j < AHEAD; ++j)
             if (k0 + j < count) {
-                s[j] = state[(k0 + j) * step];
-                tt[j] = total[(long long)(k0 + j) * a.D];
+                const int k = BACK ? count - 1 - k0 - j : k0 + j;
+                s[j] = state[k * step];
+                tt[j] = total[(long long)k * a.D];
             }
 #pragma unroll
         for (int j = 0; j < AHEAD; ++j)
             if (k0 + j < count) {
-                state[(k0 + j) * step] = h;
-                const int t = (k0 + j) * g.chunk;
-                if (ck && t % CKPT == 0) ck[t / CKPT * step] = h;
+                const int k = BACK ? count - 1 - k0 - j : k0 + j;
+                state[k * step] = h;
+                if (ck && k * g.chunk % CKPT == 0) ck[k * g.chunk / CKPT * step] = h;
                 h = fmaf(ex2(tt[j] * r), h, s[j]);
             }
     }
+    if (BACK)
+        for (int k = count; k < g.chunks; ++k) state[k * step] = 0.f;
     if (a.state_out) a.state_out[at] = h;
 }
 
@@ -323,6 +341,34 @@ int chunk_of(const gma_scan_t &s)
     return best;
 }
 
+// The backward pass's adjoint in front of (behind, in time) every chunk of CKPT tokens.
+template <typename T, int S, bool VEC>
+gma_status_t run_adjoint(const gma_scan_grad_t &grad, float *state, float *total, cudaStream_t st)
+{
+    const gma_scan_t &s = grad.fwd;
+    ChunkArgs<T> g;
+    g.s = scan_args<T>(s);
+    g.s.u = rows_of<const T>(grad.dy);
+    g.s.state_in = grad.dstate_out;
+    g.s.state_out = grad.dstate_in;
+    g.s.ckpt = nullptr;
+    g.chunk = CKPT;
+    g.chunks = (s.N + CKPT - 1) / CKPT;
+    g.state = state;
+    g.total = total;
+    const int warps = group_warps(s), per = warps < 8 ? warps : 8;
+    g.s.tiles = (warps + per - 1) / per;
+    const size_t smem = (size_t)CKPT * S * sizeof(float) + (VEC ? (size_t)per * RING_BYTES : 0);
+    auto kern = scan_chunk_kernel<T, S, VEC, ADJOINT>;
+    if (smem > 48 * 1024 &&
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        return GMA_ERR_CUDA;
+    GMA_LAUNCH(KID_SCAN_ADJ, st, kern<<<dim3(g.s.tiles * s.G, g.chunks, s.B), per * 32, smem, st>>>(g, rows_vec(s.c, s.dtype)));
+    GMA_LAUNCH(KID_SCAN_JOIN, st,
+               scan_chunk_join_kernel<T, S, true><<<dim3((s.D * S + 127) / 128, s.B), 128, 0, st>>>(g));
+    return GMA_OK;
+}
+
 template <typename T, int S, bool VEC> gma_status_t run(const gma_scan_t &s, char *ws, cudaStream_t st)
 {
     ChunkArgs<T> g;
@@ -336,15 +382,15 @@ template <typename T, int S, bool VEC> gma_status_t run(const gma_scan_t &s, cha
     const dim3 grid(g.s.tiles * s.G, g.chunks, s.B);
     const bool vec_bc = rows_vec(s.b, s.dtype) && rows_vec(s.c, s.dtype);
     const size_t rows = (size_t)g.chunk * S * sizeof(float), ring = VEC ? (size_t)per * RING_BYTES : 0;
-    for (auto kern : {scan_chunk_kernel<T, S, VEC, false>, scan_chunk_kernel<T, S, VEC, true>})
+    for (auto kern : {scan_chunk_kernel<T, S, VEC, STATE>, scan_chunk_kernel<T, S, VEC, OUTPUT>})
         if (2 * rows + ring > 48 * 1024 &&
             cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(2 * rows + ring)) != cudaSuccess)
             return GMA_ERR_CUDA;
     if (g.chunks > 1) {
-        GMA_LAUNCH(KID_SCAN_STATE, st, scan_chunk_kernel<T, S, VEC, false><<<grid, per * 32, rows + ring, st>>>(g, vec_bc));
-        GMA_LAUNCH(KID_SCAN_JOIN, st, scan_chunk_join_kernel<T, S><<<dim3((s.D * S + 127) / 128, s.B), 128, 0, st>>>(g));
+        GMA_LAUNCH(KID_SCAN_STATE, st, scan_chunk_kernel<T, S, VEC, STATE><<<grid, per * 32, rows + ring, st>>>(g, vec_bc));
+        GMA_LAUNCH(KID_SCAN_JOIN, st, scan_chunk_join_kernel<T, S, false><<<dim3((s.D * S + 127) / 128, s.B), 128, 0, st>>>(g));
     }
-    GMA_LAUNCH(KID_SCAN, st, scan_chunk_kernel<T, S, VEC, true><<<grid, per * 32, 2 * rows + ring, st>>>(g, vec_bc));
+    GMA_LAUNCH(KID_SCAN, st, scan_chunk_kernel<T, S, VEC, OUTPUT><<<grid, per * 32, 2 * rows + ring, st>>>(g, vec_bc));
     return GMA_OK;
 }
 
@@ -381,6 +427,20 @@ gma_status_t scan_chunk_forward(const gma_scan_t &s, void *ws, cudaStream_t st)
         if (s.S == 16) return vec ? run<T, 16, true>(s, (char *)ws, st) : run<T, 16, false>(s, (char *)ws, st);
         if (s.S == 32) return vec ? run<T, 32, true>(s, (char *)ws, st) : run<T, 32, false>(s, (char *)ws, st);
         return vec ? run<T, 64, true>(s, (char *)ws, st) : run<T, 64, false>(s, (char *)ws, st);
+    };
+    return s.dtype == GMA_BF16 ? with(__nv_bfloat16{}) : with(float{});
+}
+
+gma_status_t scan_chunk_adjoint(const gma_scan_grad_t &grad, float *state, float *total, cudaStream_t st)
+{
+    const gma_scan_t &s = grad.fwd;
+    const bool vec = (s.D / s.G) % 8 == 0 && rows_vec(grad.dy, s.dtype) && rows_vec(s.dt, s.dtype) &&
+                     (!s.z.ptr || rows_vec(s.z, s.dtype));
+    auto with = [&](auto t) -> gma_status_t {
+        using T = decltype(t);
+#define GMA_ADJOINT(n) (vec ? run_adjoint<T, n, true>(grad, state, total, st) : run_adjoint<T, n, false>(grad, state, total, st))
+        return s.S == 8 ? GMA_ADJOINT(8) : s.S == 16 ? GMA_ADJOINT(16) : s.S == 32 ? GMA_ADJOINT(32) : GMA_ADJOINT(64);
+#undef GMA_ADJOINT
     };
     return s.dtype == GMA_BF16 ? with(__nv_bfloat16{}) : with(float{});
 }

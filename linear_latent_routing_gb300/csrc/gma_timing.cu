@@ -70,6 +70,7 @@ const char *kernel_name(int id)
     case KID_SUM_ROWS: return "sum_rows";
     case KID_SCAN_STATE: return "scan_chunk_state";
     case KID_SCAN_JOIN: return "scan_chunk_join";
+    case KID_SCAN_ADJ: return "scan_chunk_adjoint";
     }
     return "unknown";
 }

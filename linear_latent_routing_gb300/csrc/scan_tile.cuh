@@ -145,6 +145,9 @@ bool scan_vec(const gma_scan_t &s);
 bool scan_chunked(const gma_scan_t &s);
 size_t scan_chunk_workspace(const gma_scan_t &s);
 gma_status_t scan_chunk_forward(const gma_scan_t &s, void *ws, cudaStream_t st);
+// The adjoint behind every chunk of CKPT tokens, state [B][chunks][D][S] (zeros behind a sequence's end), and
+// dstate_in; total [B][chunks][D] is scratch.
+gma_status_t scan_chunk_adjoint(const gma_scan_grad_t &grad, float *state, float *total, cudaStream_t st);
 
 }  // namespace blk
 }  // namespace gma
