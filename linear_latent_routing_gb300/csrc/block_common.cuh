@@ -193,6 +193,12 @@ __device__ __forceinline__ int row_length(const int *lengths, int b, int N)
     return lengths ? min(max(lengths[b], 0), N) : N;
 }
 
+// Launches of one call follow one another by programmatic dependent launch: a kernel lets the next one be
+// scheduled when it starts, and waits for the one before it to finish where it first reads what that
+// wrote.  A call's first launch is an ordinary one, which waits for all work before the call.
+__device__ __forceinline__ void let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ------------------------------------------------------------------ host-side checks
 inline size_t elem_size(int dtype) { return dtype == GMA_BF16 ? 2 : 4; }
 

@@ -17,6 +17,7 @@ struct SumList {
 __global__ void __launch_bounds__(256) sum_rows_kernel(const SumList l, long long rows)
 {
     __shared__ float s[8][33];
+    wait_previous();
     int k = 0;
 #pragma unroll
     for (int j = 1; j < MAX_SUMS; ++j)
@@ -56,7 +57,7 @@ gma_status_t sum_rows(const SumVec *vecs, int count, long long rows, cudaStream_
     }
     l.count = count;
     if (blocks == 0) return GMA_OK;
-    GMA_LAUNCH(KID_SUM_ROWS, st, sum_rows_kernel<<<blocks, 256, 0, st>>>(l, rows));
+    GMA_LAUNCH(KID_SUM_ROWS, st, launch_pdl(sum_rows_kernel, dim3(blocks), dim3(256), 0, st, l, rows));
     return GMA_OK;
 }
 

@@ -224,6 +224,7 @@ __global__ void __launch_bounds__(32 * GWARPS, 2) conv_backward_kernel(const Con
     constexpr int F = flight<W>();
     const ConvArgs<T> &a = g.f;
     __shared__ __align__(16) float sums[W + 1][GWARPS][32 * C];
+    let_next();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.y;
     const int grp = blockIdx.x % g.gtiles * 32 + lane, rtile = blockIdx.x / g.gtiles, run = rtile * GWARPS + warp;
     const int len = grp < a.groups && run < g.runs ? row_length(a.lengths, b, a.N) : 0;

@@ -279,7 +279,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? BACKWARD_BLOCKS : 1)
 {
     extern __shared__ float part_s[];                      // [8][THREADS]
     __shared__ float buf[2][MAX_WARPS][3], buf2[2][MAX_WARPS][1];
-    constexpr bool AHEAD = VEC && NV == 1;
+    constexpr bool AHEAD = VEC && NV == 1;        // wider rows have no registers left for it
+    let_next();
     const NormArgs<T, R> &a = g.f;
     const int tid = threadIdx.x & (a.tpr - 1), lane_row = threadIdx.x >> a.tpr_log, per = THREADS >> a.tpr_log;
     float dwpost[NV][8], dscale[NV][8], dwpre[NV][8];

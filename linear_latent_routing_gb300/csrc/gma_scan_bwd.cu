@@ -38,28 +38,35 @@ template <typename T> struct GradArgs {
     float *bc_part;      // [G * tiles][B][N][2 S]: per eight states, db then dc
 };
 
-// Four neighbouring channels.
-template <bool VEC> __device__ __forceinline__ void load4(const __nv_bfloat16 *p, int n, float (&v)[4])
-{
-    if (VEC) {
-        const uint2 q = *reinterpret_cast<const uint2 *>(p);
+// Four neighbouring channels, as they lie in memory until they are used (VEC), or the first n of them.
+template <typename T, bool VEC> struct Raw4;
+template <> struct Raw4<__nv_bfloat16, true> {
+    uint2 q;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p, int) { q = *reinterpret_cast<const uint2 *>(p); }
+    __device__ __forceinline__ void get(float (&v)[4]) const
+    {
         v[0] = __uint_as_float(q.x << 16); v[1] = __uint_as_float(q.x & 0xffff0000u);
         v[2] = __uint_as_float(q.y << 16); v[3] = __uint_as_float(q.y & 0xffff0000u);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = i < n ? __bfloat162float(p[i]) : 0.f;
     }
-}
-template <bool VEC> __device__ __forceinline__ void load4(const float *p, int n, float (&v)[4])
-{
-    if (VEC) {
-        const float4 q = *reinterpret_cast<const float4 *>(p);
-        v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
-    } else {
+};
+template <> struct Raw4<float, true> {
+    float4 q;
+    __device__ __forceinline__ void load(const float *p, int) { q = *reinterpret_cast<const float4 *>(p); }
+    __device__ __forceinline__ void get(float (&v)[4]) const { v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w; }
+};
+template <typename T> struct Raw4<T, false> {
+    float q[4];
+    __device__ __forceinline__ void load(const T *p, int n)
+    {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = i < n ? p[i] : 0.f;
+        for (int i = 0; i < 4; ++i) q[i] = i < n ? to_f32<T>(p[i]) : 0.f;
     }
-}
+    __device__ __forceinline__ void get(float (&v)[4]) const
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = q[i];
+    }
+};
 template <bool VEC> __device__ __forceinline__ void store4(__nv_bfloat16 *p, int n, const float (&v)[4])
 {
     if (VEC) {
@@ -85,17 +92,22 @@ template <bool VEC> __device__ __forceinline__ void store4(float *p, int n, cons
     }
 }
 
+// Rows of products: 20 floats apart, so that lanes write them 16 bytes at a time without bank conflicts, and
+// every block of rows that a half warp reads together with the one before half a line further.
+constexpr int RED_ROW = 20;
+template <int S> __device__ __forceinline__ int red_row(int r) { return r * RED_ROW + r / (S == 16 ? 16 : 8) * 16; }
+
 // One warp's share of shared memory.
 template <int S> struct WarpSmem {
     static constexpr int CHW = Lane<S>::CHW;
     f2 start[SUBS][NF][32];                                  // the states in front of every eighth token
-    float red[32][20];                                       // a token's products by lane, 16 and padding
-    float dt[SUB][CHW], u[SUB][CHW], dp[SUB][CHW];           // eight tokens: delta, u, dp
-    float x[SUB][CHW], q[SUB][CHW], p[SUB][CHW];             // and what comes of them
+    float red[2][32 * RED_ROW + 48];                         // two tokens' products by lane, 16 values a row
+    // eight tokens: delta; u, then du; dp, then ddelta; p
+    float dt[SUB][CHW], u[SUB][CHW], dp[SUB][CHW], p[SUB][CHW];
 };
 template <int S> struct Smem {
     WarpSmem<S> w[WARPS];
-    f2 sums[2][WARPS][SUB][S];                               // db and dc of eight tokens by warp, in turn
+    f2 sums[WARPS][SUB][S];                                  // db and dc of eight tokens by warp
     float b[CKPT][S], c[CKPT][S];
 };
 
@@ -105,11 +117,13 @@ __global__ void __launch_bounds__(THREADS, 3) scan_backward_kernel(const GradArg
     constexpr int SPLIT = Lane<S>::SPLIT, CHW = Lane<S>::CHW, CH = Lane<S>::CH;
     extern __shared__ __align__(16) unsigned char raw[];
     Smem<S> &sm = *reinterpret_cast<Smem<S> *>(raw);
+    let_next();
     const ScanArgs<T> &a = g.f;
     const int b = blockIdx.z, k = blockIdx.y, t0 = k * CKPT;
     const int len = row_length(a.lengths, b, a.N), count = min(CKPT, len - t0);
     const int group = blockIdx.x / a.tiles, Dg = a.D / a.G;
     if (count <= 0) {                                        // no tokens here; the join has cleared `state`
+        wait_previous();
         const int i = (blockIdx.x - group * a.tiles) * CH + threadIdx.x;
         const long long to = ((long long)b * g.chunks + k) * a.D + group * Dg + i;
         static_assert(CH <= THREADS, "a thread a channel");
@@ -138,6 +152,7 @@ __global__ void __launch_bounds__(THREADS, 3) scan_backward_kernel(const GradArg
     const long long at = (long long)c * S + part * 8, nck = g.chunks;
     float *state = g.state + ((long long)b * nck + k) * a.D * S + at;
     {
+        wait_previous();
         const float *ck = a.ckpt + ((long long)b * nck + k) * a.D * S + at;
 #pragma unroll
         for (int j = 0; j < NF / 2; ++j) {
@@ -160,11 +175,10 @@ __global__ void __launch_bounds__(THREADS, 3) scan_backward_kernel(const GradArg
     const int quad = lane % QUADS, first = lane / QUADS;                         // channels, token
     constexpr int TSTEP = 32 / QUADS;
     const int n4 = max(0, min(4, Dg - warp_ch - 4 * quad)), c4 = group * Dg + warp_ch + 4 * quad;
-    float bias[4], skip[4], dskip[4], dbias[4];
+    float bias[4], dskip[4], dbias[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         bias[i] = a.dt_bias && i < n4 ? a.dt_bias[c4 + i] : 0.f;
-        skip[i] = a.d_skip && i < n4 ? a.d_skip[c4 + i] : 0.f;
         dskip[i] = dbias[i] = 0.f;
     }
     auto put4 = [](float *to, const float (&v)[4]) { *reinterpret_cast<float4 *>(to) = make_float4(v[0], v[1], v[2], v[3]); };
@@ -172,7 +186,22 @@ __global__ void __launch_bounds__(THREADS, 3) scan_backward_kernel(const GradArg
         const float4 q = *reinterpret_cast<const float4 *>(from);
         v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
     };
-    // delta and u (and dp) of eight tokens; zeros behind the last one and for channels that are not there
+    // The rows of eight tokens, loaded ahead of their use; then delta and u (and dp), zeros behind the
+    // last token and for channels that are not there.
+    Raw4<T, VEC> ur[UNITS], dr[UNITS], yr[UNITS], zr[UNITS];
+    auto fetch = [&](int s, bool grad) {
+#pragma unroll
+        for (int j = 0; j < UNITS; ++j) {
+            const int i = first + j * TSTEP, t = s * SUB + i;
+            if (i >= SUB || s < 0 || t >= count || n4 <= 0) continue;
+            ur[j].load(a.u.at(b, t0 + t) + c4, n4);
+            dr[j].load(a.dt.at(b, t0 + t) + c4, n4);
+            if (grad) {
+                yr[j].load(g.dy.at(b, t0 + t) + c4, n4);
+                if (Z) zr[j].load(a.z.at(b, t0 + t) + c4, n4);
+            }
+        }
+    };
     auto stage = [&](int s, bool grad) {
 #pragma unroll
         for (int j = 0; j < UNITS; ++j) {
@@ -180,13 +209,13 @@ __global__ void __launch_bounds__(THREADS, 3) scan_backward_kernel(const GradArg
             if (i >= SUB) continue;
             float u[4] = {0.f, 0.f, 0.f, 0.f}, d[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
             if (t < count && n4 > 0) {
-                load4<VEC>(a.u.at(b, t0 + t) + c4, n4, u);
-                load4<VEC>(a.dt.at(b, t0 + t) + c4, n4, d);
+                ur[j].get(u);
+                dr[j].get(d);
                 if (grad) {
-                    load4<VEC>(g.dy.at(b, t0 + t) + c4, n4, y);
+                    yr[j].get(y);
                     if (Z) {
                         float z[4];
-                        load4<VEC>(a.z.at(b, t0 + t) + c4, n4, z);
+                        zr[j].get(z);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) y[e] *= silu(z[e]);
                     }
@@ -208,6 +237,8 @@ __global__ void __launch_bounds__(THREADS, 3) scan_backward_kernel(const GradArg
         }
     };
     const int subs = (count + SUB - 1) / SUB, lc = lane % CHW;
+    const float skip_c = a.d_skip && on ? a.d_skip[c] : 0.f;
+    fetch(0, subs == 1);
     __syncthreads();
 
     // forward: the state in front of every eighth token
@@ -217,6 +248,7 @@ __global__ void __launch_bounds__(THREADS, 3) scan_backward_kernel(const GradArg
         if (s == subs - 1) break;
         __syncwarp();
         stage(s, false);
+        fetch(s + 1, s + 2 == subs);
         __syncwarp();
 #pragma unroll 4
         for (int i = 0; i < SUB; ++i) {
@@ -233,8 +265,12 @@ __global__ void __launch_bounds__(THREADS, 3) scan_backward_kernel(const GradArg
 
     // back, eight tokens at a time
     for (int s = subs - 1; s >= 0; --s) {
-        __syncwarp();
+        __syncthreads();                          // `sums` has been read
         stage(s, true);
+        Raw4<T, VEC> yk[UNITS], zk[UNITS];
+#pragma unroll
+        for (int j = 0; j < UNITS; ++j) yk[j] = yr[j], zk[j] = zr[j];
+        fetch(s - 1, true);
         __syncwarp();
         f2 hist[SUB + 1][NF];
 #pragma unroll
@@ -251,107 +287,99 @@ __global__ void __launch_bounds__(THREADS, 3) scan_backward_kernel(const GradArg
             hist[i + 1][3] = fma2(ex2_2(mul2(d2, rate[3])), hist[i][3], mul2(x2, b1.y));
         }
 #pragma unroll
-        for (int i = SUB - 1; i >= 0; --i) {
-            const float d = ws.dt[i][lc], xu = d * ws.u[i][lc], dpv = ws.dp[i][lc];
-            const f2 d2 = pack2(d, d), xu2 = pack2(xu, xu), dp2 = pack2(dpv, dpv);
-            const ulonglong2 *bp = reinterpret_cast<const ulonglong2 *>(&sm.b[s * SUB + i][part * 8]);
-            const ulonglong2 *cp = reinterpret_cast<const ulonglong2 *>(&sm.c[s * SUB + i][part * 8]);
-            const ulonglong2 b0 = bp[0], b1 = bp[1], v0 = cp[0], v1 = cp[1];
-            const f2 bv[NF] = {b0.x, b0.y, b1.x, b1.y}, cv[NF] = {v0.x, v0.y, v1.x, v1.y};
-            f2 x2 = 0ull, q2 = 0ull, p2 = 0ull, db[NF], dc[NF];
+        for (int i2 = SUB - 2; i2 >= 0; i2 -= 2) {
 #pragma unroll
-            for (int j = 0; j < NF; ++j) {
-                const f2 gr = fma2(cv[j], dp2, r[j]);
-                db[j] = mul2(gr, xu2);
-                dc[j] = mul2(hist[i + 1][j], dp2);
-                x2 = fma2(gr, bv[j], x2);
-                if (Z) p2 = fma2(cv[j], hist[i + 1][j], p2);
-                r[j] = mul2(ex2_2(mul2(d2, rate[j])), gr);
-                const f2 w = mul2(r[j], hist[i][j]);
-                q2 = fma2(w, rate[j], q2);
-                da[j] = fma2(w, d2, da[j]);
-            }
-            ulonglong2 *row = reinterpret_cast<ulonglong2 *>(ws.red[lane]);
-            row[0] = make_ulonglong2(db[0], db[1]);
-            row[1] = make_ulonglong2(db[2], db[3]);
-            row[2] = make_ulonglong2(dc[0], dc[1]);
-            row[3] = make_ulonglong2(dc[2], dc[3]);
-            const float2 xs = unpack2(x2), qs = unpack2(q2), ps = unpack2(p2);
-            float xv = xs.x + xs.y, qv = qs.x + qs.y, pv = ps.x + ps.y;
+            for (int e = 1; e >= 0; --e) {
+                const int i = i2 + e;
+                const float d = ws.dt[i][lc], uv = ws.u[i][lc], xu = d * uv, dpv = ws.dp[i][lc];
+                const f2 d2 = pack2(d, d), xu2 = pack2(xu, xu), dp2 = pack2(dpv, dpv);
+                const ulonglong2 *bp = reinterpret_cast<const ulonglong2 *>(&sm.b[s * SUB + i][part * 8]);
+                const ulonglong2 *cp = reinterpret_cast<const ulonglong2 *>(&sm.c[s * SUB + i][part * 8]);
+                const ulonglong2 b0 = bp[0], b1 = bp[1], v0 = cp[0], v1 = cp[1];
+                const f2 bv[NF] = {b0.x, b0.y, b1.x, b1.y}, cv[NF] = {v0.x, v0.y, v1.x, v1.y};
+                f2 x2 = 0ull, q2 = 0ull, p2 = 0ull, db[NF], dc[NF];
 #pragma unroll
-            for (int off = CHW; off < 32; off *= 2) {
-                xv += __shfl_xor_sync(0xffffffffu, xv, off);
-                qv += __shfl_xor_sync(0xffffffffu, qv, off);
-                if (Z) pv += __shfl_xor_sync(0xffffffffu, pv, off);
-            }
-            if (part == 0) {
-                ws.x[i][lc] = xv;
-                ws.q[i][lc] = qv;
-                if (Z) ws.p[i][lc] = pv;
+                for (int j = 0; j < NF; ++j) {
+                    const f2 gr = fma2(cv[j], dp2, r[j]);
+                    db[j] = mul2(gr, xu2);
+                    dc[j] = mul2(hist[i + 1][j], dp2);
+                    x2 = fma2(gr, bv[j], x2);
+                    if (Z) p2 = fma2(cv[j], hist[i + 1][j], p2);
+                    r[j] = mul2(ex2_2(mul2(d2, rate[j])), gr);
+                    const f2 w = mul2(r[j], hist[i][j]);
+                    q2 = fma2(w, rate[j], q2);
+                    da[j] = fma2(w, d2, da[j]);
+                }
+                ulonglong2 *row = reinterpret_cast<ulonglong2 *>(ws.red[e] + red_row<S>(lane));
+                row[0] = make_ulonglong2(db[0], db[1]);
+                row[1] = make_ulonglong2(db[2], db[3]);
+                row[2] = make_ulonglong2(dc[0], dc[1]);
+                row[3] = make_ulonglong2(dc[2], dc[3]);
+                const float2 xs = unpack2(x2), qs = unpack2(q2), ps = unpack2(p2);
+                float xv = xs.x + xs.y, qv = qs.x + qs.y, pv = ps.x + ps.y;
+#pragma unroll
+                for (int off = CHW; off < 32; off *= 2) {
+                    xv += __shfl_xor_sync(0xffffffffu, xv, off);
+                    qv += __shfl_xor_sync(0xffffffffu, qv, off);
+                    if (Z) pv += __shfl_xor_sync(0xffffffffu, pv, off);
+                }
+                if (part == 0) {          // the other lanes of the channel have read u and dp: the shuffles came after
+                    ws.u[i][lc] = fmaf(xv, d, skip_c * dpv);
+                    ws.dp[i][lc] = fmaf(xv, uv, qv * LN2);
+                    if (Z) ws.p[i][lc] = fmaf(skip_c, uv, pv);
+                }
             }
             __syncwarp();
             // columns: pair j of part `of` over that part's CHW lanes, eight of them a lane
-            constexpr int COLS = 8 * SPLIT;
-            if (COLS <= 32) {
-                const int col = lane % COLS, from = lane / COLS * 8, of = col / 8, j = col % 8;
-                const f2 *src = reinterpret_cast<const f2 *>(&ws.red[of * CHW + from][2 * j]);
-                f2 v = src[0];
+            constexpr int COLS = 8 * SPLIT, PER = COLS <= 32 ? 1 : 2;
 #pragma unroll
-                for (int l = 1; l < 8; ++l) v = add2(v, src[10 * l]);
+            for (int e = 0; e < 2; ++e)
 #pragma unroll
-                for (int off = COLS; off < 32; off *= 2) v = add2(v, __shfl_xor_sync(0xffffffffu, v, off));
-                if (lane < COLS) sm.sums[s & 1][warp][i][col] = v;
-            } else {
-#pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    const int col = lane + 32 * m, of = col / 8, j = col % 8;
-                    const f2 *src = reinterpret_cast<const f2 *>(&ws.red[of * CHW][2 * j]);
+                for (int m = 0; m < PER; ++m) {
+                    const int col = COLS <= 32 ? lane % COLS : lane + 32 * m, from = COLS <= 32 ? lane / COLS * 8 : 0;
+                    const f2 *src = reinterpret_cast<const f2 *>(ws.red[e] + red_row<S>(col / 8 * CHW + from) + col % 8 * 2);
                     f2 v = src[0];
 #pragma unroll
-                    for (int l = 1; l < (CHW < 8 ? CHW : 8); ++l) v = add2(v, src[10 * l]);
-                    sm.sums[s & 1][warp][i][col] = v;
+                    for (int l = 1; l < (CHW < 8 ? CHW : 8); ++l) v = add2(v, src[RED_ROW / 2 * l]);
+#pragma unroll
+                    for (int off = COLS; off < 32; off *= 2) v = add2(v, __shfl_xor_sync(0xffffffffu, v, off));
+                    if (COLS >= 32 || lane < COLS) sm.sums[warp][i2 + e][col] = v;
                 }
-            }
             __syncwarp();
         }
 #pragma unroll
         for (int j = 0; j < UNITS; ++j) {
             const int i = first + j * TSTEP, t = s * SUB + i;
             if (i >= SUB || t >= count || n4 <= 0) continue;
-            float u[4], d[4], dp[4], x[4], q[4], v[4];
-            get4(&ws.u[i][4 * quad], u);
-            get4(&ws.dt[i][4 * quad], d);
-            get4(&ws.dp[i][4 * quad], dp);
-            get4(&ws.x[i][4 * quad], x);
-            get4(&ws.q[i][4 * quad], q);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = fmaf(x[e], d[e], skip[e] * dp[e]);
+            float d[4], v[4];
+            get4(&ws.u[i][4 * quad], v);
             store4<VEC>(g.du.at(b, t0 + t) + c4, n4, v);
+            get4(&ws.dt[i][4 * quad], d);
+            get4(&ws.dp[i][4 * quad], v);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                // sigmoid(raw) = 1 - exp(-softplus(raw))
-                v[e] = -expm1f(-d[e]) * fmaf(x[e], u[e], q[e] * LN2);
+                v[e] *= -expm1f(-d[e]);          // sigmoid(raw) = 1 - exp(-softplus(raw))
                 dbias[e] += v[e];
             }
             store4<VEC>(g.ddt.at(b, t0 + t) + c4, n4, v);
             if (Z) {
-                float z[4], y[4], p[4];
-                load4<VEC>(a.z.at(b, t0 + t) + c4, n4, z);
-                load4<VEC>(g.dy.at(b, t0 + t) + c4, n4, y);
-                get4(&ws.p[i][4 * quad], p);
+                float z[4], y[4];
+                zk[j].get(z);
+                yk[j].get(y);
+                get4(&ws.p[i][4 * quad], v);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = y[e] * fmaf(skip[e], u[e], p[e]) * dsilu(z[e], sigmoid(z[e]));
+                for (int e = 0; e < 4; ++e) v[e] *= y[e] * dsilu(z[e], sigmoid(z[e]));
                 store4<VEC>(g.dz.at(b, t0 + t) + c4, n4, v);
             }
         }
-        // the block's warps; the other half of `sums` takes the next eight tokens meanwhile
+        // the block's warps
         __syncthreads();
         const long long row0 = ((long long)blockIdx.x * a.B + b) * a.N + t0 + s * SUB;
         for (int i = threadIdx.x; i < SUB * S; i += THREADS) {
             if (s * SUB + i / S >= count) continue;
-            f2 v = sm.sums[s & 1][0][i / S][i % S];
+            f2 v = sm.sums[0][i / S][i % S];
 #pragma unroll
-            for (int w = 1; w < WARPS; ++w) v = add2(v, sm.sums[s & 1][w][i / S][i % S]);
+            for (int w = 1; w < WARPS; ++w) v = add2(v, sm.sums[w][i / S][i % S]);
             *reinterpret_cast<f2 *>(g.bc_part + (row0 + i / S) * 2 * S + 2 * (i % S)) = v;
         }
     }
@@ -385,6 +413,8 @@ __global__ void __launch_bounds__(THREADS, 3) scan_backward_kernel(const GradArg
 // db and dc: the groups' blocks of channels in order, four states a thread.
 template <typename T> __global__ void __launch_bounds__(256) scan_bc_kernel(const GradArgs<T> g)
 {
+    let_next();
+    wait_previous();
     const ScanArgs<T> &a = g.f;
     const int per = a.S / 2;                                  // float4 of a token and group
     const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
@@ -430,7 +460,8 @@ template <typename T, int S> gma_status_t launch(const GradArgs<T> &g, bool vec,
                     : (z ? scan_backward_kernel<T, S, false, true> : scan_backward_kernel<T, S, false, false>);
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<S>)) != cudaSuccess)
         return GMA_ERR_CUDA;
-    GMA_LAUNCH(KID_SCAN_BWD, st, kern<<<dim3(g.f.tiles * g.f.G, g.chunks, g.f.B), THREADS, sizeof(Smem<S>), st>>>(g));
+    GMA_LAUNCH(KID_SCAN_BWD, st,
+               launch_pdl(kern, dim3(g.f.tiles * g.f.G, g.chunks, g.f.B), dim3(THREADS), sizeof(Smem<S>), st, g));
     return GMA_OK;
 }
 
@@ -457,7 +488,8 @@ template <typename T> gma_status_t backward_of(const gma_scan_grad_t &s, char *w
       : f.S == 32 ? launch<T, 32>(g, vec, st) : launch<T, 64>(g, vec, st);
     if (r != GMA_OK) return r;
     const long long threads = (long long)f.N * (f.S / 2);
-    GMA_LAUNCH(KID_SCAN_BC, st, scan_bc_kernel<T><<<dim3((unsigned)((threads + 255) / 256), f.B, f.G), 256, 0, st>>>(g));
+    GMA_LAUNCH(KID_SCAN_BC, st,
+               launch_pdl(scan_bc_kernel<T>, dim3((unsigned)((threads + 255) / 256), f.B, f.G), dim3(256), 0, st, g));
     SumVec v[3] = {{g.state, (long long)f.D * f.S, (long long)f.D * f.S, s.da_log, 1}};
     int count = 1;
     if (f.d_skip) v[count++] = SumVec{g.skip, f.D, f.D, s.dd_skip, 1};

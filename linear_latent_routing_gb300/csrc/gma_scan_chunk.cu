@@ -126,6 +126,7 @@ __global__ void __launch_bounds__(256, 2) scan_chunk_kernel(const ChunkArgs<T> g
     constexpr bool OUT = MODE == OUTPUT, ADJ = MODE == ADJOINT;
     constexpr int CPL = Lanes<S>::CPL, SL = Lanes<S>::SL, SPLIT = Lanes<S>::SPLIT, CH_WARP = Lanes<S>::CH_WARP;
     extern __shared__ __align__(16) float rows_s[];
+    let_next();
     const ScanArgs<T> &a = g.s;
     const int b = blockIdx.z, k = blockIdx.y, t0 = k * g.chunk;
     const int len = row_length(a.lengths, b, a.N);
@@ -158,6 +159,7 @@ __global__ void __launch_bounds__(256, 2) scan_chunk_kernel(const ChunkArgs<T> g
     for (int e = 0; e < CPL; ++e) {
         const bool on = e < n;
         load_rates<SL>(a.a_log, (long long)(c + e) * S + part * SL, on, r[e]);
+        if (OUT && e == 0) wait_previous();
         if (OUT && !only) load_state<SL>(g.state + (row + e) * S + part * SL, on, h[e]);
         else if (OUT && a.state_in) load_state<SL>(a.state_in + in_b + e * S, on, h[e]);
         else load_state<SL>(nullptr, false, h[e]);
@@ -285,12 +287,14 @@ __global__ void __launch_bounds__(256, 2) scan_chunk_kernel(const ChunkArgs<T> g
 template <typename T, int S, bool BACK> __global__ void __launch_bounds__(128) scan_chunk_join_kernel(const ChunkArgs<T> g)
 {
     constexpr int AHEAD = 16;
+    let_next();
     const ScanArgs<T> &a = g.s;
     const int i = blockIdx.x * 128 + threadIdx.x, d = i / S, b = blockIdx.y;
     if (d >= a.D) return;
     const int len = row_length(a.lengths, b, a.N), count = (len + g.chunk - 1) / g.chunk;
     const long long step = (long long)a.D * S, at = b * step + i;
     const float r = -expf(a.a_log[i]) * LOG2E;
+    wait_previous();
     float h = a.state_in ? a.state_in[at] : 0.f;
     float *state = g.state + b * g.chunks * step + i;
     const float *total = g.total + (long long)b * g.chunks * a.D + d;
@@ -325,8 +329,8 @@ int group_warps(const gma_scan_t &s)
     return s.S <= 16 ? warps_of<16>(s) : s.S == 32 ? warps_of<32>(s) : warps_of<64>(s);
 }
 
-// Tokens of a chunk, of 32, 64, 128 and 256: what takes least by (waves + 1/2) (chunk + 16), where a wave is
-// the 304 blocks that run at once and 16 tokens' time goes into a chunk's start and the join.  A chunk's b and c
+// Tokens of a chunk, of 32, 64, 128 and 256: what takes least by (waves + 1/2) (chunk + 24), where a wave is
+// the 304 blocks that run at once and 24 tokens' time goes into a chunk's start and the join.  A chunk's b and c
 // stay within 32 KB (two blocks an SM), and a chunk does not step over a checkpoint.
 int chunk_of(const gma_scan_t &s)
 {
@@ -335,7 +339,7 @@ int chunk_of(const gma_scan_t &s)
     int best = 32;
     double least = 0;
     for (int c = 32; c <= 256 && c * s.S <= 4096 && !(s.checkpoints && c > CKPT); c *= 2) {
-        const double waves = rows * ((s.N + c - 1) / c) / 304 + 0.5, cost = (waves > 1 ? waves : 1) * (c + 16);
+        const double waves = rows * ((s.N + c - 1) / c) / 304 + 0.5, cost = (waves > 1 ? waves : 1) * (c + 24);
         if (c == 32 || cost < least) best = c, least = cost;
     }
     return best;
@@ -365,7 +369,7 @@ gma_status_t run_adjoint(const gma_scan_grad_t &grad, float *state, float *total
         return GMA_ERR_CUDA;
     GMA_LAUNCH(KID_SCAN_ADJ, st, kern<<<dim3(g.s.tiles * s.G, g.chunks, s.B), per * 32, smem, st>>>(g, rows_vec(s.c, s.dtype)));
     GMA_LAUNCH(KID_SCAN_JOIN, st,
-               scan_chunk_join_kernel<T, S, true><<<dim3((s.D * S + 127) / 128, s.B), 128, 0, st>>>(g));
+               launch_pdl(scan_chunk_join_kernel<T, S, true>, dim3((s.D * S + 127) / 128, s.B), dim3(128), 0, st, g));
     return GMA_OK;
 }
 
@@ -388,9 +392,14 @@ template <typename T, int S, bool VEC> gma_status_t run(const gma_scan_t &s, cha
             return GMA_ERR_CUDA;
     if (g.chunks > 1) {
         GMA_LAUNCH(KID_SCAN_STATE, st, scan_chunk_kernel<T, S, VEC, STATE><<<grid, per * 32, rows + ring, st>>>(g, vec_bc));
-        GMA_LAUNCH(KID_SCAN_JOIN, st, scan_chunk_join_kernel<T, S, false><<<dim3((s.D * S + 127) / 128, s.B), 128, 0, st>>>(g));
+        GMA_LAUNCH(KID_SCAN_JOIN, st,
+                   launch_pdl(scan_chunk_join_kernel<T, S, false>, dim3((s.D * S + 127) / 128, s.B), dim3(128), 0, st, g));
     }
-    GMA_LAUNCH(KID_SCAN, st, scan_chunk_kernel<T, S, VEC, OUTPUT><<<grid, per * 32, 2 * rows + ring, st>>>(g, vec_bc));
+    if (g.chunks > 1)
+        GMA_LAUNCH(KID_SCAN, st,
+                   launch_pdl(scan_chunk_kernel<T, S, VEC, OUTPUT>, grid, dim3(per * 32), 2 * rows + ring, st, g, vec_bc));
+    else
+        GMA_LAUNCH(KID_SCAN, st, scan_chunk_kernel<T, S, VEC, OUTPUT><<<grid, per * 32, 2 * rows + ring, st>>>(g, vec_bc));
     return GMA_OK;
 }
 
