@@ -1,6 +1,8 @@
 """Host-side checks of include/gma_block.h (no GPU needed): the packed structs have the header's layout,
 workspace sizes, and refusals before anything is enqueued."""
+import ctypes
 import os
+import struct
 import subprocess
 
 import pytest
@@ -10,15 +12,48 @@ FAKE = 1 << 20          # never dereferenced: validation fails first, or there i
 NONE = (0, 0, 0)
 
 
+def _layout(fmt):
+    """A struct of the header: fields in order, no padding (the header's structs have none); R: gma_rows_t."""
+    return struct.Struct("=" + fmt.replace("R", "Qqq"))
+
+
+SCAN, CONV, NORM = "6iRRRRR6QRQ", "5iIR5QR", "7ifRqRR3QRR"
+
+
 @pytest.fixture(scope="module")
 def lib():
     from linear_latent_routing_gb300 import build
     build.build()
-    from linear_latent_routing_gb300 import norm, ssm
+    from linear_latent_routing_gb300 import gma, norm, ssm
+
+    def fn(name, *argtypes, restype=ctypes.c_int):
+        f = getattr(gma.lib, name)
+        f.argtypes, f.restype = list(argtypes), restype
+        return f
+    vp, sz = ctypes.c_void_p, ctypes.c_size_t
+
+    class ssm_:
+        scan, conv = ssm.scan, ssm.conv
+        _scan_t, _scan_grad_t = _layout(SCAN), _layout(SCAN + "RQRRRRR4Q")
+        _conv_t, _conv_grad_t = _layout(CONV), _layout(CONV + "RR2Q")
+        _scan_forward = fn("gma_scan_forward", vp, vp, sz, vp)
+        _scan_step = fn("gma_scan_step", vp, vp)
+        _scan_backward = fn("gma_scan_backward", vp, vp, sz, vp)
+        _scan_backward_workspace = fn("gma_scan_backward_workspace_size", vp, restype=sz)
+        _conv_forward = fn("gma_conv_forward", vp, vp)
+        _conv_step = fn("gma_conv_step", vp, vp)
+        _conv_backward = fn("gma_conv_backward", vp, vp, sz, vp)
+        _conv_backward_workspace = fn("gma_conv_backward_workspace_size", vp, restype=sz)
+
+    class norm_:
+        block_norm = norm.block_norm
+        _norm_t, _norm_grad_t = _layout(NORM), _layout(NORM + "RRRqRR3Q")
+        _norm_forward = fn("gma_norm_forward", vp, vp)
+        _norm_backward = fn("gma_norm_backward", vp, vp, sz, vp)
+        _norm_backward_workspace = fn("gma_norm_backward_workspace_size", vp, restype=sz)
 
     class L:
-        pass
-    L.ssm, L.norm = ssm, norm
+        ssm, norm = ssm_, norm_
     return L
 
 
