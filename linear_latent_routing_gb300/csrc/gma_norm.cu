@@ -109,16 +109,16 @@ template <int K> __device__ __forceinline__ void row_sum(float (&v)[K], int tpr,
 #pragma unroll
         for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], off);
     if (tpr > 32) {
-        const int warp = threadIdx.x >> 5, per = tpr >> 5, first = warp / per * per;
-        if ((threadIdx.x & 31) == 0)
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, per = tpr >> 5, first = warp & ~(per - 1);
+        if (lane == 0)
 #pragma unroll
             for (int k = 0; k < K; ++k) buf[warp][k] = v[k];
         __syncthreads();
 #pragma unroll
-        for (int k = 0; k < K; ++k) v[k] = 0.f;
-        for (int w = 0; w < per; ++w)
+        for (int k = 0; k < K; ++k) v[k] = buf[first + (lane & (per - 1))][k];
+        for (int off = per / 2; off; off >>= 1)
 #pragma unroll
-            for (int k = 0; k < K; ++k) v[k] += buf[first + w][k];
+            for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], off);
     }
 }
 
@@ -274,7 +274,8 @@ template <typename T, typename R> struct NormGradArgs {
 //   da = rstd (q - a rstd^2 mean(q a)),  q = w_post dv;   do = da silu(gate), dgate = da o silu'(gate).
 // Blocks walk over the rows with the parameter gradients of their channels in registers, add up
 // their row lanes in order and leave one partial row each; sum_rows adds those in order.
-template <typename T, typename R, bool VEC, int NV, int THREADS>
+// FULL: every input and parameter is there (a block in training), so nothing branches on them.
+template <typename T, typename R, bool VEC, int NV, int THREADS, bool FULL>
 __global__ void __launch_bounds__(THREADS, THREADS == 256 ? BACKWARD_BLOCKS : 1) norm_backward_kernel(const NormGradArgs<T, R> g)
 {
     extern __shared__ float part_s[];                      // [8][THREADS]
@@ -282,6 +283,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? BACKWARD_BLOCKS : 1)
     constexpr bool AHEAD = VEC && NV == 1;        // wider rows have no registers left for it
     let_next();
     const NormArgs<T, R> &a = g.f;
+    const bool gate = FULL || a.gate.p, has_dr = FULL || g.dr.p, has_dh = FULL || g.dh.p, post = FULL || a.w_post;
     const int tid = threadIdx.x & (a.tpr - 1), lane_row = threadIdx.x >> a.tpr_log, per = THREADS >> a.tpr_log;
     float dwpost[NV][8], dscale[NV][8], dwpre[NV][8];
 #pragma unroll
@@ -302,9 +304,9 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? BACKWARD_BLOCKS : 1)
             const int c0 = (j * a.tpr + tid) * 8;
             if (c0 >= a.D) continue;
             on[j].load(a.o.at(b, t) + head_at[j]);
-            if (a.gate.p) gn[j].load(a.gate.at(b, t) + c0);
-            if (g.dr.p) dn[j].load(g.dr.at(b, t) + c0);
-            if (g.dh.p) {
+            if (gate) gn[j].load(a.gate.at(b, t) + c0);
+            if (has_dr) dn[j].load(g.dr.at(b, t) + c0);
+            if (has_dh) {
                 rn[j].load(kept.at(b, t) + c0);
                 hn[j].load(g.dh.at(b, t) + c0);
             }
@@ -330,22 +332,22 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? BACKWARD_BLOCKS : 1)
                 float o[8], gt[8];
                 if (AHEAD) {
                     on[j].get(o);
-                    if (a.gate.p) gn[j].get(gt);
-                    if (g.dr.p) dn[j].get(dr[j]);
-                    if (g.dh.p) {
+                    if (gate) gn[j].get(gt);
+                    if (has_dr) dn[j].get(dr[j]);
+                    if (has_dh) {
                         rn[j].get(rf[j]);
                         hn[j].get(dh[j]);
                     }
                 } else {
                     load_heads<VEC>(a.o, a.o_head, a.by_d, b, t, c0, n, o);
-                    if (a.gate.p) load8<VEC>(a.gate.at(b, t) + c0, n, gt);
-                    if (g.dr.p) load8<VEC>(g.dr.at(b, t) + c0, n, dr[j]);
-                    if (g.dh.p) {
+                    if (gate) load8<VEC>(a.gate.at(b, t) + c0, n, gt);
+                    if (has_dr) load8<VEC>(g.dr.at(b, t) + c0, n, dr[j]);
+                    if (has_dh) {
                         load8<VEC>(kept.at(b, t) + c0, n, rf[j]);
                         load8<VEC>(g.dh.at(b, t) + c0, n, dh[j]);
                     }
                 }
-                if (g.dh.p) {
+                if (has_dh) {
                     float w[8];
                     load8<VEC>(a.w_pre + c0, n, w);
 #pragma unroll
@@ -356,7 +358,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? BACKWARD_BLOCKS : 1)
                 }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    if (a.gate.p) {
+                    if (gate) {
                         const float s = sigmoid(gt[i]);
                         by_o[j][i] = gt[i] * s;
                         by_gate[j][i] = o[i] * dsilu(gt[i], s);
@@ -370,7 +372,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? BACKWARD_BLOCKS : 1)
             }
         }
         fetch(row + step);
-        if (g.dh.p || (a.w_post && a.group == a.D)) row_sum<3>(sums, a.tpr, buf[turn]);
+        if (has_dh || (post && a.group == a.D)) row_sum<3>(sums, a.tpr, buf[turn]);
         const float rs2 = rsqrtf(sums[0] * a.inv_d + a.eps);
         const float k2 = rs2 * rs2 * sums[1] * a.inv_d;
         float rstd[NV], dots[NV], dot[1] = {0.f};
@@ -378,11 +380,11 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? BACKWARD_BLOCKS : 1)
         for (int j = 0; j < NV; ++j) {
             const int c0 = (j * a.tpr + tid) * 8, n = live ? min(8, a.D - c0) : 0;
             rstd[j] = 1.f;
-            if (a.w_post)
+            if (post)
                 rstd[j] = rsqrtf((a.group == a.D ? sums[2] : group_sum(gs[j], a.group / 8)) * a.inv_group + a.eps);
             dots[j] = 0.f;
             if (n > 0) {
-                if (g.dh.p) {
+                if (has_dh) {
                     float w[8];
                     load8<VEC>(a.w_pre + c0, n, w);
 #pragma unroll
@@ -391,10 +393,15 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? BACKWARD_BLOCKS : 1)
                         dr[j][i] = fmaf(rs2, fmaf(-rf[j][i], k2, dh[j][i] * w[i]), dr[j][i]);
                     }
                 }
-                if (g.dresidual.p) store8<VEC>(g.dresidual.at(b, t) + c0, n, dr[j]);
+                if (FULL || g.dresidual.p) store8<VEC>(g.dresidual.at(b, t) + c0, n, dr[j]);
                 float w[8], sc[8];
-                load_param<VEC>(a.w_post, c0, n, 1.f, w);
-                load_param<VEC>(a.scale, c0, n, 1.f, sc);
+                if (FULL) {
+                    load8<VEC>(a.w_post + c0, n, w);
+                    load8<VEC>(a.scale + c0, n, sc);
+                } else {
+                    load_param<VEC>(a.w_post, c0, n, 1.f, w);
+                    load_param<VEC>(a.scale, c0, n, 1.f, sc);
+                }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const float nrm = act[j][i] * rstd[j], dv = dr[j][i] * sc[i];
@@ -406,12 +413,12 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? BACKWARD_BLOCKS : 1)
                 dot[0] += dots[j];
             }
         }
-        if (a.w_post && a.group == a.D) row_sum<1>(dot, a.tpr, buf2[turn]);
+        if (post && a.group == a.D) row_sum<1>(dot, a.tpr, buf2[turn]);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int c0 = (j * a.tpr + tid) * 8, n = live ? min(8, a.D - c0) : 0;
             float k1 = 0.f;
-            if (a.w_post)
+            if (post)
                 k1 = rstd[j] * rstd[j] * a.inv_group * (a.group == a.D ? dot[0] : group_sum(dots[j], a.group / 8));
             if (n > 0) {
                 float dov[8], dg[8];
@@ -422,7 +429,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? BACKWARD_BLOCKS : 1)
                     dg[i] = da * by_gate[j][i];
                 }
                 store_heads<VEC>(g.d_o, g.d_o_head, a.by_d, b, t, c0, n, dov);
-                if (a.gate.p) store8<VEC>(g.dgate.at(b, t) + c0, n, dg);
+                if (gate) store8<VEC>(g.dgate.at(b, t) + c0, n, dg);
             }
         }
     }
@@ -623,9 +630,16 @@ gma_status_t gma_norm_backward(const gma_norm_grad_t *g, void *ws, size_t ws_byt
         a.pitch = (D + 7) / 8 * 8;
         constexpr int TH = decltype(threads)::value;
         const int blocks = blocks_of(n, p, BACKWARD_BLOCKS);
-        GMA_LAUNCH(KID_NORM_BWD, st,
-                   norm_backward_kernel<T, R, decltype(v)::value, decltype(nv)::value, TH>
-                   <<<blocks, TH, TH * 8 * sizeof(float), st>>>(a));
+        constexpr bool V = decltype(v)::value;
+        constexpr int NV = decltype(nv)::value;
+        const bool full = V && NV == 1 && n.gate.ptr && g->dr.ptr && g->dh.ptr && n.w_post && n.scale && n.w_pre &&
+                          g->dresidual.ptr;
+        if (full)
+            GMA_LAUNCH(KID_NORM_BWD, st,
+                       norm_backward_kernel<T, R, V, NV, TH, V && NV == 1><<<blocks, TH, TH * 8 * sizeof(float), st>>>(a));
+        else
+            GMA_LAUNCH(KID_NORM_BWD, st,
+                       norm_backward_kernel<T, R, V, NV, TH, false><<<blocks, TH, TH * 8 * sizeof(float), st>>>(a));
         const float *used[3] = {n.w_post, n.scale, n.w_pre};
         float *out[3] = {g->dw_post, g->dscale, g->dw_pre};
         SumVec vecs[3];

@@ -405,13 +405,13 @@ template <typename T, int S, bool VEC> gma_status_t run(const gma_scan_t &s, cha
 
 }  // namespace
 
-// Worth it from eight warps an SM on: with fewer, a warp's walk over its chunk takes as long as
-// the whole call of the kernel that spreads a tile's tokens over lanes (512 tokens of 1024 channels: 45 us in
-// three launches against 16 us).
+// Worth it from six warps an SM on: with fewer, a warp's walk over its chunk takes as long as
+// the whole call of the kernel that spreads a tile's tokens over lanes (512 tokens of 1024 channels: 33 us in
+// three launches against 15 us).
 bool scan_chunked(const gma_scan_t &s)
 {
     const long long warps = (long long)s.B * s.G * group_warps(s) * ((s.N + 31) / 32);
-    return warps >= 152 * 8 && (s.N + 31) / 32 <= 65535 && (long long)s.D * s.S < (1ll << 31);
+    return warps >= 152 * 6 && (s.N + 31) / 32 <= 65535 && (long long)s.D * s.S < (1ll << 31);
 }
 
 size_t scan_chunk_workspace(const gma_scan_t &s)
