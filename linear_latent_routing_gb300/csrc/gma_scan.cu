@@ -5,6 +5,8 @@
 //
 // The decay differs from channel to channel and state to state, so there is no matrix product in it:
 // each (token, channel, state) takes one exponential and about five multiply-adds in fp32.
+#include <type_traits>
+
 #include "scan_tile.cuh"
 
 namespace gma {
@@ -213,37 +215,83 @@ __global__ void __launch_bounds__(K::THREADS) scan_forward_kernel(const ScanArgs
 }
 
 // One token: a lane holds four states of a channel, S / 4 lanes a channel.  The state is read and
-// written once, which bounds it.
-template <typename T, int S>
-__global__ void __launch_bounds__(256) scan_step_kernel(const ScanArgs<T> a)
+// written once, which bounds it.  With many batch rows a lane takes ROWS of them, whose loads are in flight
+// together and whose rates are computed once.
+__device__ __forceinline__ void quad(const __nv_bfloat16 *p, bool vec, float (&v)[4])
+{
+    if (vec) {
+        const uint2 q = *reinterpret_cast<const uint2 *>(p);
+        v[0] = __uint_as_float(q.x << 16); v[1] = __uint_as_float(q.x & 0xffff0000u);
+        v[2] = __uint_as_float(q.y << 16); v[3] = __uint_as_float(q.y & 0xffff0000u);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = __bfloat162float(p[k]);
+    }
+}
+__device__ __forceinline__ void quad(const float *p, bool vec, float (&v)[4])
+{
+    if (vec) {
+        const float4 q = *reinterpret_cast<const float4 *>(p);
+        v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = p[k];
+    }
+}
+
+template <typename T, int S, int ROWS>
+__global__ void __launch_bounds__(256) scan_step_kernel(const ScanArgs<T> a, bool vec)
 {
     constexpr int LPC = S / 4, CPB = 256 / LPC;
-    const int b = blockIdx.y, d = blockIdx.x * CPB + threadIdx.x / LPC, q = threadIdx.x % LPC;
-    const bool live = d < a.D;
-    float y = 0.f, u = 0.f;
-    if (live) {
-        const long long at = ((long long)b * a.D + d) * S + 4 * q;
-        const float4 h4 = *reinterpret_cast<const float4 *>(a.state_in + at);
-        const float4 r4 = *reinterpret_cast<const float4 *>(a.a_log + (long long)d * S + 4 * q);
-        const int g = d / (a.D / a.G);
-        const T *bp = a.b.at(b, 0) + g * S + 4 * q, *cp = a.c.at(b, 0) + g * S + 4 * q;
-        u = to_f32<T>(a.u.at(b, 0)[d]);
-        const float delta = softplus(to_f32<T>(a.dt.at(b, 0)[d]) + (a.dt_bias ? a.dt_bias[d] : 0.f));
-        float h[4] = {h4.x, h4.y, h4.z, h4.w};
-        const float r[4] = {r4.x, r4.y, r4.z, r4.w};
+    const int d = blockIdx.x * CPB + threadIdx.x / LPC, q = threadIdx.x % LPC, b0 = blockIdx.y * ROWS;
+    const bool on = d < a.D;
+    float4 h4[ROWS];
+    float u[ROWS], dt[ROWS], z[ROWS], bv[ROWS][4], cv[ROWS][4], y[ROWS];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            h[k] = fmaf(ex2(-expf(r[k]) * LOG2E * delta), h[k], delta * u * to_f32<T>(bp[k]));
-            y = fmaf(to_f32<T>(cp[k]), h[k], y);
-        }
-        *reinterpret_cast<float4 *>(a.state_out + at) = make_float4(h[0], h[1], h[2], h[3]);
+    for (int r = 0; r < ROWS; ++r) {
+        y[r] = 0.f;
+        const int b = b0 + r;
+        if (!on || b >= a.B) continue;
+        const int first = d / (a.D / a.G) * S + 4 * q;
+        h4[r] = *reinterpret_cast<const float4 *>(a.state_in + ((long long)b * a.D + d) * S + 4 * q);
+        u[r] = to_f32<T>(a.u.at(b, 0)[d]);
+        dt[r] = to_f32<T>(a.dt.at(b, 0)[d]);
+        z[r] = a.z.p && q == 0 ? to_f32<T>(a.z.at(b, 0)[d]) : 0.f;
+        quad(a.b.at(b, 0) + first, vec, bv[r]);
+        quad(a.c.at(b, 0) + first, vec, cv[r]);
+    }
+    float rate[4] = {0.f, 0.f, 0.f, 0.f}, bias = 0.f, skip = 0.f;
+    if (on) {
+        const float4 v = *reinterpret_cast<const float4 *>(a.a_log + (long long)d * S + 4 * q);
+        rate[0] = -expf(v.x) * LOG2E; rate[1] = -expf(v.y) * LOG2E;
+        rate[2] = -expf(v.z) * LOG2E; rate[3] = -expf(v.w) * LOG2E;
+        if (a.dt_bias) bias = a.dt_bias[d];
+        if (a.d_skip) skip = a.d_skip[d];
     }
 #pragma unroll
-    for (int off = LPC / 2; off; off >>= 1) y += __shfl_xor_sync(0xffffffffu, y, off);
-    if (live && q == 0) {
-        if (a.d_skip) y = fmaf(a.d_skip[d], u, y);
-        if (a.z.p) y *= silu(to_f32<T>(a.z.at(b, 0)[d]));
-        a.y.at(b, 0)[d] = from_f32<T>(y);
+    for (int r = 0; r < ROWS; ++r) {
+        const int b = b0 + r;
+        if (!on || b >= a.B) continue;
+        const float delta = softplus(dt[r] + bias), xu = delta * u[r];
+        float h[4] = {h4[r].x, h4[r].y, h4[r].z, h4[r].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            h[k] = fmaf(ex2(rate[k] * delta), h[k], xu * bv[r][k]);
+            y[r] = fmaf(cv[r][k], h[k], y[r]);
+        }
+        *reinterpret_cast<float4 *>(a.state_out + ((long long)b * a.D + d) * S + 4 * q) = make_float4(h[0], h[1], h[2], h[3]);
+    }
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+        for (int off = LPC / 2; off; off >>= 1) y[r] += __shfl_xor_sync(0xffffffffu, y[r], off);
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+        const int b = b0 + r;
+        if (!on || b >= a.B || q != 0) continue;
+        float v = fmaf(skip, u[r], y[r]);
+        if (a.z.p) v *= silu(z[r]);
+        a.y.at(b, 0)[d] = from_f32<T>(v);
     }
 }
 
@@ -308,15 +356,19 @@ gma_status_t gma_scan_step(const gma_scan_t *s, gma_stream_t stream)
     auto run = [&](auto t) -> gma_status_t {
         using T = decltype(t);
         const ScanArgs<T> a = scan_args<T>(*s);
-        const int cpb = 256 / (s->S / 4);
-        const dim3 grid((s->D + cpb - 1) / cpb, s->B);
-        GMA_LAUNCH(KID_SCAN_STEP, st, switch (s->S) {
-            case 8: scan_step_kernel<T, 8><<<grid, 256, 0, st>>>(a); break;
-            case 16: scan_step_kernel<T, 16><<<grid, 256, 0, st>>>(a); break;
-            case 32: scan_step_kernel<T, 32><<<grid, 256, 0, st>>>(a); break;
-            default: scan_step_kernel<T, 64><<<grid, 256, 0, st>>>(a); break;
-        });
-        return GMA_OK;
+        const int cpb = 256 / (s->S / 4), tiles = (s->D + cpb - 1) / cpb;
+        const bool vec = rows_vec(s->b, s->dtype) && rows_vec(s->c, s->dtype);
+        // two batch rows a lane once that still leaves four blocks an SM
+        const bool two = (long long)tiles * s->B >= 2 * 4 * 152;
+        const dim3 grid(tiles, two ? (s->B + 1) / 2 : s->B);
+        auto launch = [&](auto n) -> gma_status_t {
+            constexpr int S = decltype(n)::value;
+            GMA_LAUNCH(KID_SCAN_STEP, st, if (two) scan_step_kernel<T, S, 2><<<grid, 256, 0, st>>>(a, vec);
+                       else scan_step_kernel<T, S, 1><<<grid, 256, 0, st>>>(a, vec));
+            return GMA_OK;
+        };
+        return s->S == 8 ? launch(std::integral_constant<int, 8>{}) : s->S == 16 ? launch(std::integral_constant<int, 16>{})
+             : s->S == 32 ? launch(std::integral_constant<int, 32>{}) : launch(std::integral_constant<int, 64>{});
     };
     return s->dtype == GMA_BF16 ? run(__nv_bfloat16{}) : run(float{});
 }
