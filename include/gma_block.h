@@ -19,7 +19,8 @@
  *   - Parameters and states are fp32 and contiguous; sums, states and statistics are held in fp32.
  *   - `lengths` (NULL, or B int32 in device memory) gives every batch row's number of tokens, taken
  *     as min(max(length, 0), N): the rows behind a sequence's last token are neither read nor
- *     written, and the states that come out are those after the last token.
+ *     written (with GMA_ROWS_ZERO_TAIL: are written as zeros), and the states that come out are those
+ *     after the last token.
  *   - The workspace is 256-byte aligned, needs no initialisation, holds nothing between calls and
  *     has no error word (no kernel behind these entry points waits for another one's signal).
  *     Calls that share one are ordered on the GPU.  Where gma_*_workspace_size gives 0 for valid
@@ -34,6 +35,10 @@
 #ifdef __cplusplus
 extern "C" {
 #endif
+
+/* Flags of the scan and the convolution: zeros in the output rows (of gradients too) behind a
+ * sequence's last token, for buffers that hold anything. */
+#define GMA_ROWS_ZERO_TAIL 0x2u
 
 typedef struct {
     void *ptr;             /* first element; NULL: not given */
@@ -51,6 +56,8 @@ typedef struct {
 typedef struct {
     int32_t B, N, D, S, G;
     int32_t dtype;                /* of u, dt, z, b, c, y and their gradients               */
+    uint32_t flags;               /* GMA_ROWS_ZERO_TAIL or 0                                 */
+    uint32_t reserved;            /* 0                                                       */
     gma_rows_t u, dt, z;          /* [B][N][D]; z may be NULL                                */
     gma_rows_t b, c;              /* [B][N][G][S], a token's G * S values contiguous         */
     const float *a_log;           /* [D][S]                                                  */
@@ -103,7 +110,7 @@ gma_status_t gma_scan_backward(const gma_scan_grad_t *grad, void *workspace, siz
 typedef struct {
     int32_t B, N, D, W;
     int32_t dtype;                /* of x, y, the states and the gradients of x              */
-    uint32_t flags;               /* GMA_CONV_* bits                                         */
+    uint32_t flags;               /* GMA_CONV_LINEAR, GMA_ROWS_ZERO_TAIL                     */
     gma_rows_t x;                 /* [B][N][D]                                               */
     const float *weight;          /* [D][W]                                                  */
     const float *bias;            /* [D] or NULL (0)                                         */

@@ -52,7 +52,6 @@ struct Call {
     gma_stream_t stream() const { return (gma_stream_t)c10::cuda::getCurrentCUDAStream(dev).stream(); }
     at::Tensor empty(at::IntArrayRef shape) const { return at::empty(shape, options); }
     at::Tensor empty32(at::IntArrayRef shape) const { return at::empty(shape, f32); }
-    // rows that a call with lengths does not write are zero
     at::Tensor rows(at::IntArrayRef shape, bool zero) const { return zero ? at::zeros(shape, options) : at::empty(shape, options); }
 };
 
@@ -228,7 +227,8 @@ PyObject *scan(PyObject *, PyObject *const *a, Py_ssize_t n)
         s.state_out = dense(a[9], "state_out", {B, D, S}, at::kFloat, c);
         s.lengths = dense<int32_t>(a[10], "lengths", {B}, at::kInt, c);
         s.checkpoints = dense(a[11], "checkpoints", {B, (N + CKPT - 1) / CKPT, D, S}, at::kFloat, c);
-        const at::Tensor y = out_or(a[12], "out", [&] { return c.rows(full, s.lengths != nullptr); });
+        if (s.lengths && !given(a[12])) s.flags |= GMA_ROWS_ZERO_TAIL;      // in a buffer allocated here
+        const at::Tensor y = out_or(a[12], "out", [&] { return c.empty(full); });
         s.y = rows(y, "out", full, 1, c.T, c);
         const Workspace ws(gma_scan_workspace_size(&s), c);
         const gma_status_t r = gma_scan_forward(&s, ws.ptr(), ws.bytes, c.stream());
@@ -266,7 +266,10 @@ PyObject *scan_backward(PyObject *, PyObject *const *a, Py_ssize_t n)
         s.checkpoints = need(a[9], "checkpoints", {B, (N + CKPT - 1) / CKPT, D, S}, at::kFloat, c);
         g.dstate_out = dense(a[10], "dstate_out", {B, D, S}, at::kFloat, c);
         s.lengths = dense<int32_t>(a[11], "lengths", {B}, at::kInt, c);
-        const bool zero = s.lengths != nullptr, z = s.z.ptr != nullptr;
+        // the rows behind a sequence's end: zero in buffers allocated here, left alone in the caller's
+        const bool z = s.z.ptr != nullptr, some = given(a[12]) || given(a[13]) || given(a[14]) || given(a[15]) || given(a[16]);
+        const bool zero = s.lengths && some;
+        if (s.lengths && !some) s.flags |= GMA_ROWS_ZERO_TAIL;
         const at::Tensor du = out_or(a[12], "out['u']", [&] { return c.rows(full, zero); });
         const at::Tensor ddt = out_or(a[13], "out['dt']", [&] { return c.rows(full, zero); });
         const at::Tensor dz = z ? out_or(a[14], "out['z']", [&] { return c.rows(full, zero); }) : at::Tensor();
@@ -327,7 +330,8 @@ PyObject *conv(PyObject *, PyObject *const *a, Py_ssize_t n)
         gma_conv_t s = conv_of(a, false, &c, &full);
         s.state_out = dense<void>(a[5], "state_out", {s.B, s.W - 1, s.D}, c.T, c);
         s.lengths = dense<int32_t>(a[6], "lengths", {s.B}, at::kInt, c);
-        const at::Tensor y = out_or(a[7], "out", [&] { return c.rows(full, s.lengths != nullptr); });
+        if (s.lengths && !given(a[7])) s.flags |= GMA_ROWS_ZERO_TAIL;
+        const at::Tensor y = out_or(a[7], "out", [&] { return c.empty(full); });
         s.y = rows(y, "out", full, 1, c.T, c);
         const gma_status_t r = gma_conv_forward(&s, c.stream());
         return r == GMA_OK ? wrap(y) : raise_status(r, "gma_conv_forward");
@@ -361,7 +365,8 @@ PyObject *conv_backward(PyObject *, PyObject *const *a, Py_ssize_t n)
         gma_conv_t &s = g.fwd;
         g.dy = rows(a[5], "dy", full, 1, c.T, c);
         s.lengths = dense<int32_t>(a[6], "lengths", {s.B}, at::kInt, c);
-        const at::Tensor dx = out_or(a[7], "out", [&] { return c.rows(full, s.lengths != nullptr); });
+        if (s.lengths && !given(a[7])) s.flags |= GMA_ROWS_ZERO_TAIL;
+        const at::Tensor dx = out_or(a[7], "out", [&] { return c.empty(full); });
         g.dx = rows(dx, "out", full, 1, c.T, c);
         const at::Tensor dw = c.empty32({s.D, s.W}), db = s.bias ? c.empty32({s.D}) : at::Tensor();
         g.dweight = (float *)dw.data_ptr();

@@ -18,6 +18,7 @@ constexpr int THREADS = 128, C = 4;
 template <typename T> struct ConvArgs {
     int B, N, D, groups;        // groups = ceil(D / C)
     int run;                    // tokens of one thread's run
+    bool zero;                  // zeros behind a sequence's last token
     Rows<const T> x;
     const float *w, *bias;
     const T *state_in;
@@ -121,6 +122,13 @@ __device__ __forceinline__ f2 dsilu2(f2 v)
     return pack2(dsilu(x.x, sigmoid(x.x)), dsilu(x.y, sigmoid(x.y)));
 }
 
+template <bool VEC, typename T>
+__device__ __forceinline__ void zero_rows(const Rows<T> &r, int b, int from, int to, int c0, int n)
+{
+    const f2 none[2] = {0ull, 0ull};
+    for (int t = from; t < to; ++t) store4<VEC>(r.at(b, t) + c0, n, none);
+}
+
 // Tokens whose loads are in flight together: whole turns of the ring.
 template <int W> constexpr int flight() { return W == 3 ? 3 : 4; }
 
@@ -142,6 +150,7 @@ __global__ void __launch_bounds__(THREADS) conv_forward_kernel(const ConvArgs<T>
             store4<VEC>(a.state_out + ((long long)b * (W - 1) + k) * a.D + c0, n, v);
         }
     }
+    if (a.zero) zero_rows<VEC>(a.y, b, max(t0, len), min(t0 + a.run, a.N), c0, n);
     if (t0 >= len) return;
     f2 wt[W][2], bs[2], x[W][2];
     load_weights<W>(a.w, a.bias, c0, n, wt, bs);
@@ -230,6 +239,7 @@ __global__ void __launch_bounds__(32 * GWARPS, 2) conv_backward_kernel(const Con
     const int len = grp < a.groups && run < g.runs ? row_length(a.lengths, b, a.N) : 0;
     const int c0 = grp * C, n = min(C, a.D - c0);
     const int t0 = run * a.run, end = min(len, t0 + a.run);
+    if (a.zero && grp < a.groups && run < g.runs) zero_rows<VEC>(g.dx, b, max(t0, len), min(t0 + a.run, a.N), c0, n);
     f2 dw[W][2], db[2] = {0ull, 0ull};
 #pragma unroll
     for (int k = 0; k < W; ++k) dw[k][0] = dw[k][1] = 0ull;
@@ -336,6 +346,7 @@ template <typename T> ConvArgs<T> args_of(const gma_conv_t &c, int run)
 {
     ConvArgs<T> a;
     a.run = run;
+    a.zero = c.flags & GMA_ROWS_ZERO_TAIL;
     a.B = c.B; a.N = c.N; a.D = c.D; a.groups = (c.D + C - 1) / C;
     a.x = rows_of<const T>(c.x);
     a.w = c.weight; a.bias = c.bias;
@@ -363,7 +374,7 @@ gma_status_t check(const gma_conv_t *c, bool need_out)
     if (!c) return GMA_ERR_INVALID_ARG;
     if (c->B < 1 || c->N < 1 || c->D < 1) return GMA_ERR_INVALID_ARG;
     if (c->dtype != GMA_F32 && c->dtype != GMA_BF16) return GMA_ERR_INVALID_ARG;
-    if (c->flags & ~GMA_CONV_LINEAR) return GMA_ERR_INVALID_ARG;
+    if (c->flags & ~(GMA_CONV_LINEAR | GMA_ROWS_ZERO_TAIL)) return GMA_ERR_INVALID_ARG;
     if (c->W < 2 || c->W > 4 || c->B > 65535 || c->D > (1 << 24) || c->N > (1 << 30)) return GMA_ERR_UNSUPPORTED_SHAPE;
     const size_t e = elem_size(c->dtype);
     if (!rows_ok(c->x, c->dtype, c->B, c->N, c->D, false)) return GMA_ERR_INVALID_ARG;

@@ -17,6 +17,7 @@ gma_status_t scan_check(const gma_scan_t *s, bool out)
     if (!s) return GMA_ERR_INVALID_ARG;
     if (s->B < 1 || s->N < 1 || s->D < 1 || s->S < 1 || s->G < 1 || s->D % s->G) return GMA_ERR_INVALID_ARG;
     if (s->dtype != GMA_F32 && s->dtype != GMA_BF16) return GMA_ERR_INVALID_ARG;
+    if (s->flags & ~GMA_ROWS_ZERO_TAIL || s->reserved) return GMA_ERR_INVALID_ARG;
     if (!(s->S == 8 || s->S == 16 || s->S == 32 || s->S == 64)) return GMA_ERR_UNSUPPORTED_SHAPE;
     if (s->B > 65535 || s->D > (1 << 24) || s->N > (1 << 30)) return GMA_ERR_UNSUPPORTED_SHAPE;
     const int dt = s->dtype;
@@ -209,6 +210,11 @@ __global__ void __launch_bounds__(K::THREADS) scan_forward_kernel(const ScanArgs
         }
     }
     __syncthreads();
+    if (a.zero && n8 > 0)
+        for (int t = len + token; t < a.N; t += STEP) {
+            const float none[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            store8<VEC>(a.y.at(b, t) + cp, n8, none);
+        }
     if (a.state_out)
         for (int i = threadIdx.x; i < nch * a.S; i += K::THREADS)
             a.state_out[((long long)b * a.D + c0) * a.S + i] = hs[i];

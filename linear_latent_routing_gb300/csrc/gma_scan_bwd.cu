@@ -122,6 +122,17 @@ __global__ void __launch_bounds__(THREADS, 3) scan_backward_kernel(const GradArg
     const int b = blockIdx.z, k = blockIdx.y, t0 = k * CKPT;
     const int len = row_length(a.lengths, b, a.N), count = min(CKPT, len - t0);
     const int group = blockIdx.x / a.tiles, Dg = a.D / a.G;
+    if (a.zero) {
+        const int i0 = (blockIdx.x - group * a.tiles) * CH, rows = min(CKPT, a.N - t0);
+        const float none[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int i = threadIdx.x; i < rows * (CH / 4); i += THREADS) {
+            const int t = i / (CH / 4), ch = i0 + i % (CH / 4) * 4, n = min(4, Dg - ch);
+            if (t < count || n <= 0) continue;
+            store4<VEC>(g.du.at(b, t0 + t) + group * Dg + ch, n, none);
+            store4<VEC>(g.ddt.at(b, t0 + t) + group * Dg + ch, n, none);
+            if (Z) store4<VEC>(g.dz.at(b, t0 + t) + group * Dg + ch, n, none);
+        }
+    }
     if (count <= 0) {                                        // no tokens here; the join has cleared `state`
         wait_previous();
         const int i = (blockIdx.x - group * a.tiles) * CH + threadIdx.x;
@@ -420,7 +431,11 @@ template <typename T> __global__ void __launch_bounds__(256) scan_bc_kernel(cons
     const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
     const int q = (int)(i % per), b = blockIdx.y, group = blockIdx.z;
     const long long t = i / per;
-    if (t >= row_length(a.lengths, b, a.N)) return;
+    T *out = (q % 4 < 2 ? g.db : g.dc).at(b, (int)t) + group * a.S + q / 4 * 8 + q % 2 * 4;   // per eight states: db, then dc
+    if (t >= row_length(a.lengths, b, a.N)) {
+        if (a.zero && t < a.N) out[0] = out[1] = out[2] = out[3] = from_f32<T>(0.f);
+        return;
+    }
     const float4 *p = reinterpret_cast<const float4 *>(g.bc_part) + (((long long)group * a.tiles * a.B + b) * a.N + t) * per + q;
     const long long step = (long long)a.B * a.N * per;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -429,8 +444,6 @@ template <typename T> __global__ void __launch_bounds__(256) scan_bc_kernel(cons
         const float4 v = p[k * step];
         s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
     }
-    // per eight states: db, then dc
-    T *out = (q % 4 < 2 ? g.db : g.dc).at(b, (int)t) + group * a.S + q / 4 * 8 + q % 2 * 4;
     out[0] = from_f32<T>(s.x); out[1] = from_f32<T>(s.y); out[2] = from_f32<T>(s.z); out[3] = from_f32<T>(s.w);
 }
 

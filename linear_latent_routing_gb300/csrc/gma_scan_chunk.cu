@@ -138,6 +138,9 @@ __global__ void __launch_bounds__(256, 2) scan_chunk_kernel(const ChunkArgs<T> g
     const int count = min(g.chunk, len - t0);
     const bool only = g.chunks == 1;
     const long long in_b = ((long long)b * a.D + c) * S + part * SL;      // states of this lane in [B][D][S]
+    if (OUT && a.zero && n > 0 && part == 0)
+        for (int t = max(count, 0); t < min(g.chunk, a.N - t0); ++t)
+            store_ch<CPL, VEC>(a.y.at(b, t0 + t) + c, n, make_float2(0.f, 0.f));
     if (count <= 0) {
         // an empty sequence's state passes through
         if (OUT && k == 0 && a.state_out && a.state_out != a.state_in && only)

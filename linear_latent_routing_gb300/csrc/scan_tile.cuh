@@ -121,6 +121,7 @@ template <typename T> struct ScanArgs {
     const int *lengths;
     Rows<T> y;
     float *ckpt;
+    bool zero;                     // zeros behind a sequence's last token
 };
 
 template <typename T> inline ScanArgs<T> scan_args(const gma_scan_t &s)
@@ -133,6 +134,7 @@ template <typename T> inline ScanArgs<T> scan_args(const gma_scan_t &s)
     a.state_in = s.state_in; a.state_out = s.state_out; a.lengths = s.lengths;
     a.y = rows_of<T>(s.y);
     a.ckpt = s.checkpoints;
+    a.zero = s.flags & GMA_ROWS_ZERO_TAIL;
     return a;
 }
 

@@ -17,7 +17,7 @@ def _layout(fmt):
     return struct.Struct("=" + fmt.replace("R", "Qqq"))
 
 
-SCAN, CONV, NORM = "6iRRRRR6QRQ", "5iIR5QR", "7ifRqRR3QRR"
+SCAN, CONV, NORM = "6i2IRRRRR6QRQ", "5iIR5QR", "7ifRqRR3QRR"
 
 
 @pytest.fixture(scope="module")
@@ -62,7 +62,7 @@ def _rows(width, N=10, ptr=FAKE):
 
 
 def _scan(lib, grad=False, **kw):
-    d = dict(B=2, N=10, D=24, S=16, G=1, dtype=1, a_log=FAKE, d_skip=FAKE, dt_bias=FAKE, state_in=0, state_out=0,
+    d = dict(B=2, N=10, D=24, S=16, G=1, dtype=1, flags=0, reserved=0, a_log=FAKE, d_skip=FAKE, dt_bias=FAKE, state_in=0, state_out=0,
              lengths=0, ckpt=FAKE if grad else 0)
     width = kw.get("D", 24)
     gs = kw.get("G", 1) * kw.get("S", 16)
@@ -70,7 +70,7 @@ def _scan(lib, grad=False, **kw):
     d.update(dy=_rows(width), dstate_out=0, du=_rows(width), ddt=_rows(width), dz=NONE, db=_rows(gs), dc=_rows(gs),
              da=FAKE, dd=FAKE, dbias=FAKE, dstate_in=0)
     d.update(kw)
-    head = (d["B"], d["N"], d["D"], d["S"], d["G"], d["dtype"], *d["u"], *d["dt"], *d["z"], *d["b"], *d["c"], d["a_log"],
+    head = (d["B"], d["N"], d["D"], d["S"], d["G"], d["dtype"], d["flags"], d["reserved"], *d["u"], *d["dt"], *d["z"], *d["b"], *d["c"], d["a_log"],
             d["d_skip"], d["dt_bias"], d["state_in"], d["state_out"], d["lengths"], *d["y"], d["ckpt"])
     if not grad:
         return lib.ssm._scan_t.pack(*head)
@@ -118,14 +118,14 @@ def test_packed_structs_have_the_header_layout(lib, tmp_path):
     sizes = [x.size for x in (s._scan_t, s._scan_grad_t, s._conv_t, s._conv_grad_t, n._norm_t, n._norm_grad_t)]
     assert got[:6] == sizes
     # field offsets, by the packed position of a marked value
-    assert got[6:] == [24, 144, 192, 216, 224, 352, 400, 24, 48, 88, 112, 168, 28, 56, 128, 160, 256, 288, 328]
+    assert got[6:] == [32, 152, 200, 224, 232, 360, 408, 24, 48, 88, 112, 168, 28, 56, 128, 160, 256, 288, 328]
 
 
 @pytest.mark.parametrize("bad,status", [
     (dict(B=0), 1), (dict(N=0), 1), (dict(D=-1), 1), (dict(G=5), 1), (dict(dtype=2), 1), (dict(S=12), 2), (dict(S=128), 2),
     (dict(B=65536), 2), (dict(u=NONE), 1), (dict(dt=(FAKE + 1, 240, 24)), 1), (dict(b=(FAKE, -1, 16)), 1),
     (dict(a_log=0), 1), (dict(a_log=FAKE + 4), 1), (dict(state_in=FAKE + 8), 1), (dict(y=NONE), 1),
-    (dict(y=(FAKE, 240, 23)), 1), (dict(y=(FAKE, 100, 24)), 1), (dict(lengths=FAKE + 2), 1)])
+    (dict(y=(FAKE, 240, 23)), 1), (dict(y=(FAKE, 100, 24)), 1), (dict(lengths=FAKE + 2), 1), (dict(flags=1), 1), (dict(reserved=1), 1)])
 def test_scan_refusals(lib, bad, status):
     assert lib.ssm._scan_forward(_scan(lib, **bad), None, 0, None) == status
 
@@ -154,7 +154,7 @@ def test_scan_workspace(lib):
 
 
 @pytest.mark.parametrize("bad,status", [
-    (dict(W=5), 2), (dict(W=1), 2), (dict(flags=2), 1), (dict(x=NONE), 1), (dict(weight=0), 1), (dict(y=(FAKE, 240, 8)), 1),
+    (dict(W=5), 2), (dict(W=1), 2), (dict(flags=4), 1), (dict(x=NONE), 1), (dict(weight=0), 1), (dict(y=(FAKE, 240, 8)), 1),
     (dict(state_in=FAKE + 1), 1), (dict(state_in=FAKE, state_out=FAKE), 1), (dict(D=0), 1), (dict(B=70000), 2)])
 def test_conv_refusals(lib, bad, status):
     assert lib.ssm._conv_forward(_conv(lib, **bad), None) == status

@@ -185,6 +185,35 @@ def test_scan_rows_behind_the_last_token_are_left_alone():
     assert torch.equal(h[0], d["state"][0])
 
 
+@pytest.mark.parametrize("B,N,D,S", [(3, 140, 24, 16), (4, 300, 8200, 8)])
+def test_rows_behind_the_last_token_are_zero_in_new_buffers(B, N, D, S):
+    """Without a caller's buffer the rows behind a sequence's end come out as zeros (memory that held NaN
+    before), whatever kernel takes the call."""
+    ssm, _ = _ops()
+    lengths = [0, 7, N, 64][:B]
+    t, dy, _ = _scan_inputs(B, N, D, S, 1, "bf16")
+    d, _, _, ck, ln = _run_scan(t, lengths, ckpt=True)
+    x, w, b = d["dt"], _draw(1)(D, 4).cuda(), _draw(2)(D).cuda()
+
+    def dirty():
+        for n in (1, 2, 3, 4, 5):
+            torch.full((n, B, N, D), float("nan"), dtype=BF, device="cuda")
+    dirty()
+    y = ssm.scan(d["u"], d["dt"], d["a_log"], d["b"], d["c"], d["d_skip"], d["dt_bias"], d["z"], lengths=ln)
+    dirty()
+    g = ssm.scan_backward(dy.cuda(), d["u"], d["dt"], d["a_log"], d["b"], d["c"], ck, d["d_skip"], d["dt_bias"], d["z"],
+                          lengths=ln)
+    dirty()
+    f = ssm.conv(x, w, b, lengths=ln)
+    dirty()
+    gc = ssm.conv_backward(dy.cuda(), x, w, b, lengths=ln)
+    for v in (y, g["u"], g["dt"], g["z"], g["b"], g["c"], f, gc["x"]):
+        assert torch.isfinite(v.float()).all()
+        for i, n in enumerate(lengths):
+            assert (v[i, n:] == 0).all()
+            assert n == 0 or (v[i, :n] != 0).any()
+
+
 def test_scan_state_in_place_and_pieces_of_a_sequence():
     """A sequence in pieces, the state updated in place, ends where the whole sequence does; the last
     piece is single tokens."""
