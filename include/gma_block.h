@@ -52,7 +52,8 @@ typedef struct {
  *     h_t[d][n] = exp(delta_t A[d][n]) h_{t-1}[d][n] + delta_t b_t[g][n] u_t[d],
  *     p_t[d] = sum_n c_t[g][n] h_t[d][n] + d_skip[d] u_t[d],
  *     y_t[d] = p_t[d] silu(z_t[d])          (y = p without z).
- * S in {8, 16, 32, 64}; 1 <= G, G divides D; B <= 65535. */
+ * S in {8, 16, 32, 64}; 1 <= G, G divides D; B <= 65535, N <= 2^30 (the backward pass: N <= 64 * 65535,
+ * D * S < 2^30). */
 typedef struct {
     int32_t B, N, D, S, G;
     int32_t dtype;                /* of u, dt, z, b, c, y and their gradients               */

@@ -188,6 +188,10 @@ __device__ __forceinline__ f2 softplus2(f2 x)
 }
 __device__ __forceinline__ float softplus(float x) { return unpack2(softplus2(pack2(x, 0.f))).x; }
 
+// A log2(e) of A = -exp(a_log), kept finite: the decay of a delta of zero (the tokens behind a sequence's
+// end) is one whatever the rate.
+__device__ __forceinline__ float decay_rate(float a_log) { return fmaxf(-expf(a_log) * LOG2E, -3e38f); }
+
 __device__ __forceinline__ int row_length(const int *lengths, int b, int N)
 {
     return lengths ? min(max(lengths[b], 0), N) : N;
@@ -195,7 +199,8 @@ __device__ __forceinline__ int row_length(const int *lengths, int b, int N)
 
 // Launches of one call follow one another by programmatic dependent launch: a kernel lets the next one be
 // scheduled when it starts, and waits for the one before it to finish where it first reads what that
-// wrote.  A call's first launch is an ordinary one, which waits for all work before the call.
+// wrote, or before it returns.  A call's first launch is an ordinary one, which waits for all work
+// before the call, and its last one lets nothing start early.
 __device__ __forceinline__ void let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(K::THREADS) scan_forward_kernel(const ScanArgs
     for (int i = threadIdx.x; i < K::CH * a.S; i += K::THREADS) {
         const int k = i / a.S;
         const long long at = (long long)(c0 + k) * a.S + i % a.S;
-        rate[i] = k < nch ? -expf(a.a_log[at]) * LOG2E : 0.f;
+        rate[i] = k < nch ? decay_rate(a.a_log[at]) : 0.f;
         hs[i] = k < nch && a.state_in ? a.state_in[(long long)b * a.D * a.S + at] : 0.f;
     }
     const float skip = a.d_skip && ch < nch ? a.d_skip[c0 + ch] : 0.f;
@@ -269,8 +269,8 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const ScanArgs<T> a, boo
     float rate[4] = {0.f, 0.f, 0.f, 0.f}, bias = 0.f, skip = 0.f;
     if (on) {
         const float4 v = *reinterpret_cast<const float4 *>(a.a_log + (long long)d * S + 4 * q);
-        rate[0] = -expf(v.x) * LOG2E; rate[1] = -expf(v.y) * LOG2E;
-        rate[2] = -expf(v.z) * LOG2E; rate[3] = -expf(v.w) * LOG2E;
+        rate[0] = decay_rate(v.x); rate[1] = decay_rate(v.y);
+        rate[2] = decay_rate(v.z); rate[3] = decay_rate(v.w);
         if (a.dt_bias) bias = a.dt_bias[d];
         if (a.d_skip) skip = a.d_skip[d];
     }

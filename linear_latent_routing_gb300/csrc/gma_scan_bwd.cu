@@ -168,8 +168,8 @@ __global__ void __launch_bounds__(THREADS, 3) scan_backward_kernel(const GradArg
 #pragma unroll
         for (int j = 0; j < NF / 2; ++j) {
             const float4 v = on ? reinterpret_cast<const float4 *>(a.a_log + at)[j] : make_float4(0.f, 0.f, 0.f, 0.f);
-            rate[2 * j] = on ? pack2(-expf(v.x) * LOG2E, -expf(v.y) * LOG2E) : 0ull;
-            rate[2 * j + 1] = on ? pack2(-expf(v.z) * LOG2E, -expf(v.w) * LOG2E) : 0ull;
+            rate[2 * j] = on ? pack2(decay_rate(v.x), decay_rate(v.y)) : 0ull;
+            rate[2 * j + 1] = on ? pack2(decay_rate(v.z), decay_rate(v.w)) : 0ull;
             ulonglong2 w = make_ulonglong2(0ull, 0ull), z = w;
             if (on) {
                 w = reinterpret_cast<const ulonglong2 *>(ck)[j];

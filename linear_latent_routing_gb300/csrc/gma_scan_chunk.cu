@@ -95,8 +95,8 @@ template <int S> __device__ __forceinline__ void load_rates(const float *a_log, 
 #pragma unroll
     for (int q = 0; q < S / 4; ++q) {
         const float4 v = on ? reinterpret_cast<const float4 *>(a_log + at)[q] : make_float4(0.f, 0.f, 0.f, 0.f);
-        r[2 * q] = on ? pack2(-expf(v.x) * LOG2E, -expf(v.y) * LOG2E) : 0ull;
-        r[2 * q + 1] = on ? pack2(-expf(v.z) * LOG2E, -expf(v.w) * LOG2E) : 0ull;
+        r[2 * q] = on ? pack2(decay_rate(v.x), decay_rate(v.y)) : 0ull;
+        r[2 * q + 1] = on ? pack2(decay_rate(v.z), decay_rate(v.w)) : 0ull;
     }
 }
 template <int S> __device__ __forceinline__ void load_state(const float *p, bool on, f2 (&h)[S / 2])
@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(256, 2) scan_chunk_kernel(const ChunkArgs<T> g
     constexpr bool OUT = MODE == OUTPUT, ADJ = MODE == ADJOINT;
     constexpr int CPL = Lanes<S>::CPL, SL = Lanes<S>::SL, SPLIT = Lanes<S>::SPLIT, CH_WARP = Lanes<S>::CH_WARP;
     extern __shared__ __align__(16) float rows_s[];
-    let_next();
+    if (!OUT) let_next();                 // step 3 is a call's last launch
     const ScanArgs<T> &a = g.s;
     const int b = blockIdx.z, k = blockIdx.y, t0 = k * g.chunk;
     const int len = row_length(a.lengths, b, a.N);
@@ -142,6 +142,7 @@ __global__ void __launch_bounds__(256, 2) scan_chunk_kernel(const ChunkArgs<T> g
         for (int t = max(count, 0); t < min(g.chunk, a.N - t0); ++t)
             store_ch<CPL, VEC>(a.y.at(b, t0 + t) + c, n, make_float2(0.f, 0.f));
     if (count <= 0) {
+        if (OUT) wait_previous();
         // an empty sequence's state passes through
         if (OUT && k == 0 && a.state_out && a.state_out != a.state_in && only)
             for (int e = 0; e < n; ++e)
@@ -296,7 +297,7 @@ template <typename T, int S, bool BACK> __global__ void __launch_bounds__(128) s
     if (d >= a.D) return;
     const int len = row_length(a.lengths, b, a.N), count = (len + g.chunk - 1) / g.chunk;
     const long long step = (long long)a.D * S, at = b * step + i;
-    const float r = -expf(a.a_log[i]) * LOG2E;
+    const float r = decay_rate(a.a_log[i]);
     wait_previous();
     float h = a.state_in ? a.state_in[at] : 0.f;
     float *state = g.state + b * g.chunks * step + i;

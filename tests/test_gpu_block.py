@@ -234,7 +234,8 @@ def test_scan_state_in_place_and_pieces_of_a_sequence():
 
 
 @pytest.mark.parametrize("B,D,S,G,dtype,z", [(1, 1, 8, 1, "f32", False), (3, 70, 16, 2, "bf16", True),
-                                            (130, 33, 32, 1, "bf16", False), (2, 512, 64, 1, "f32", True)])
+                                            (130, 33, 32, 1, "bf16", False), (2, 512, 64, 1, "f32", True),
+                                            (201, 600, 16, 1, "bf16", True), (201, 601, 16, 1, "f32", False)])
 def test_scan_step(B, D, S, G, dtype, z):
     ssm, _ = _ops()
     t, _, _ = _scan_inputs(B, 1, D, S, G, dtype, z, True, seed=6)
@@ -256,6 +257,44 @@ def test_scan_long_sequence_forgets_and_stays_bounded():
     ry, rh = R.scan(**t)
     R.check(y, ry, "y")
     R.check(h, rh, "state")
+
+
+@pytest.mark.parametrize("D", [16, 8208])
+def test_scan_of_rates_that_overflow_or_vanish(D):
+    """a_log of 100 and of -100: decays of exactly zero and of one, in padded batches too."""
+    ssm, _ = _ops()
+    t, dy, _ = _scan_inputs(2, 300, D, 8, 1, "f32", True, True, seed=13)
+    t["a_log"][:, ::3] = 100.0
+    t["a_log"][:, 1::3] = -100.0
+    lengths = [300, 37]
+    d, y, h, ck, ln = _run_scan(t, lengths, ckpt=True)
+    g = ssm.scan_backward(dy.cuda(), d["u"], d["dt"], d["a_log"], d["b"], d["c"], ck, d["d_skip"], d["dt_bias"], d["z"], lengths=ln)
+    for v in [y, h] + list(g.values()):
+        assert torch.isfinite(v).all()
+    # h with a decay of zero is the last token's input, with a decay of one the sum of all
+    delta = torch.nn.functional.softplus(t["dt"].double() + t["dt_bias"].double())
+    x = (delta * t["u"].double())[..., None] * t["b"].double()
+    for i, n in enumerate(lengths):
+        assert torch.allclose(h[i, :, ::3].cpu().double(), x[i, n - 1, :, ::3], rtol=1e-5, atol=1e-30)
+        want = t["state"][i, :, 1::3].double() + x[i, :n, :, 1::3].sum(0)
+        scale = (t["state"][i, :, 1::3].double().abs() + x[i, :n, :, 1::3].abs().sum(0))
+        assert ((h[i, :, 1::3].cpu().double() - want).abs() <= 400 * 2.0 ** -24 * scale).all()
+
+
+def test_calls_of_empty_sequences_alone():
+    """Every sequence empty, on every path: states pass through, gradients are zero, and what follows on
+    the stream sees it."""
+    ssm, _ = _ops()
+    for D in (16, 8208):
+        t, dy, ds = _scan_inputs(2, 130, D, 16, 1, "bf16", True, True, seed=14)
+        for _ in range(3):
+            d, y, h, ck, ln = _run_scan(t, [0, 0], ckpt=True)
+            assert torch.equal(h, d["state"])
+            g = ssm.scan_backward(dy.cuda(), d["u"], d["dt"], d["a_log"], d["b"], d["c"], ck, d["d_skip"], d["dt_bias"], d["z"],
+                                  dstate_out=ds.cuda(), lengths=ln)
+            assert torch.equal(g["state"], ds.cuda())
+            for k in ("a_log", "d_skip", "dt_bias", "u", "dt", "z", "b", "c"):
+                assert (g[k] == 0).all(), k
 
 
 def test_scan_strides_beyond_32_bits():
@@ -355,6 +394,11 @@ NORMS = [  # B, H, N, d, dtype, group, gate, post, res, scale, pre
     (1, 1, 2, 16384, "f32", 0, True, True, "f32", True, True),
     (1, 2, 700, 32, "f32", 32, True, True, None, False, False),
     (2, 1, 6, 333, "bf16", 0, False, False, None, False, True),
+    (1, 16, 1301, 128, "bf16", 128, True, True, None, False, False),      # two rows a thread
+    (1, 1, 1301, 2048, "f32", 0, True, True, "f32", True, True),
+    (1, 32, 5, 128, "bf16", 0, True, True, "f32", True, True),            # 512 threads a row
+    (2, 1, 3, 6000, "f32", 0, True, True, "f32", True, True),             # two pieces a thread
+    (1, 1, 2, 3003, "bf16", 0, True, True, "bf16", True, True),
 ]
 
 
