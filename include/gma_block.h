@@ -71,7 +71,9 @@ typedef struct {
     float *checkpoints;           /* out: the states gma_scan_backward starts from, or NULL  */
 } gma_scan_t;
 
-/* Bytes of `checkpoints`: the state before every 64th token, B * ceil(N / 64) * D * S floats. */
+/* `checkpoints` is [B][ceil(N / t)][D][S], the state before every t-th token, with
+ * t = gma_scan_checkpoint_tokens (64 or 16, by B, N, D and S); its bytes. */
+int gma_scan_checkpoint_tokens(const gma_scan_t *scan);
 size_t gma_scan_checkpoint_size(const gma_scan_t *scan);
 size_t gma_scan_workspace_size(const gma_scan_t *scan);
 gma_status_t gma_scan_forward(const gma_scan_t *scan, void *workspace, size_t workspace_bytes,

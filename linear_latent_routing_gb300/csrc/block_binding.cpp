@@ -17,8 +17,6 @@
 
 namespace {
 
-constexpr int64_t CKPT = 64;      // tokens between two checkpoints (gma_scan_checkpoint_size)
-
 struct Fail {
     PyObject *type;
     std::string words;
@@ -215,6 +213,31 @@ gma_scan_t scan_of(PyObject *const *a, bool step, Call *call, std::vector<int64_
     return s;
 }
 
+int64_t checkpoints_of(const gma_scan_t &s)
+{
+    const int n = gma_scan_checkpoint_tokens(&s);
+    return n ? (s.N + n - 1) / n : 0;
+}
+
+// u, S: a buffer for the checkpoints
+PyObject *scan_checkpoints(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded(n, 2, [&]() -> PyObject * {
+        const at::Tensor &u = tensor(a[0], "u");
+        const Call c = begin(u, "u");
+        const long S = PyLong_AsLong(a[1]);
+        if (PyErr_Occurred()) {
+            PyErr_Clear();
+            type_error("S must be a whole number");
+        }
+        if (u.dim() != 3) value_error("u must be [B, N, D]");
+        if (u.size(0) > INT32_MAX || u.size(1) > INT32_MAX || u.size(2) > INT32_MAX || S > 64 || S < 1) value_error("sizes do not fit");
+        gma_scan_t s = {};
+        s.B = (int32_t)u.size(0); s.N = (int32_t)u.size(1); s.D = (int32_t)u.size(2); s.S = (int32_t)S;
+        return wrap(c.empty32({s.B, checkpoints_of(s), s.D, s.S}));
+    });
+}
+
 // ..., state, state_out, lengths, checkpoints, out
 PyObject *scan(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
@@ -226,7 +249,7 @@ PyObject *scan(PyObject *, PyObject *const *a, Py_ssize_t n)
         s.state_in = dense(a[8], "state", {B, D, S}, at::kFloat, c);
         s.state_out = dense(a[9], "state_out", {B, D, S}, at::kFloat, c);
         s.lengths = dense<int32_t>(a[10], "lengths", {B}, at::kInt, c);
-        s.checkpoints = dense(a[11], "checkpoints", {B, (N + CKPT - 1) / CKPT, D, S}, at::kFloat, c);
+        s.checkpoints = dense(a[11], "checkpoints", {B, checkpoints_of(s), D, S}, at::kFloat, c);
         if (s.lengths && !given(a[12])) s.flags |= GMA_ROWS_ZERO_TAIL;      // in a buffer allocated here
         const at::Tensor y = out_or(a[12], "out", [&] { return c.empty(full); });
         s.y = rows(y, "out", full, 1, c.T, c);
@@ -263,7 +286,7 @@ PyObject *scan_backward(PyObject *, PyObject *const *a, Py_ssize_t n)
         gma_scan_t &s = g.fwd;
         const int64_t B = s.B, N = s.N, D = s.D, S = s.S;
         g.dy = rows(a[8], "dy", full, 1, c.T, c);
-        s.checkpoints = need(a[9], "checkpoints", {B, (N + CKPT - 1) / CKPT, D, S}, at::kFloat, c);
+        s.checkpoints = need(a[9], "checkpoints", {B, checkpoints_of(s), D, S}, at::kFloat, c);
         g.dstate_out = dense(a[10], "dstate_out", {B, D, S}, at::kFloat, c);
         s.lengths = dense<int32_t>(a[11], "lengths", {B}, at::kInt, c);
         // the rows behind a sequence's end: zero in buffers allocated here, left alone in the caller's
@@ -501,7 +524,7 @@ PyObject *block_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n)
 }
 
 #define METHOD(f) {#f, (PyCFunction)(void *)f, METH_FASTCALL, ""}
-PyMethodDef methods[] = {METHOD(scan), METHOD(scan_step), METHOD(scan_backward), METHOD(conv), METHOD(conv_step),
+PyMethodDef methods[] = {METHOD(scan_checkpoints), METHOD(scan), METHOD(scan_step), METHOD(scan_backward), METHOD(conv), METHOD(conv_step),
                          METHOD(conv_backward), METHOD(block_norm), METHOD(block_norm_backward), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_block", "Binding of gma_block.h; see ssm and norm.", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

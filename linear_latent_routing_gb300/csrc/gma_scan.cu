@@ -34,6 +34,12 @@ gma_status_t scan_check(const gma_scan_t *s, bool out)
     return GMA_OK;
 }
 
+int scan_spacing(const gma_scan_t &s)
+{
+    const int lanes = s.S < 8 ? 1 : s.S / 8, channels = lanes < 32 ? 32 / lanes : 1;    // of a channel, of a warp
+    return (double)s.B * ((s.N + 63) / 64) * ((s.D + channels - 1) / channels) < 152 * 6 ? 16 : 64;
+}
+
 bool scan_vec(const gma_scan_t &s)
 {
     return (s.D / s.G) % 8 == 0 && rows_vec(s.u, s.dtype) && rows_vec(s.dt, s.dtype) &&
@@ -66,7 +72,7 @@ __global__ void __launch_bounds__(K::THREADS) scan_forward_kernel(const ScanArgs
     const int len = row_length(a.lengths, b, a.N);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tl = lane % K::LT, ch = warp * K::CPW + lane / K::LT;
-    const int nck = (a.N + CKPT - 1) / CKPT;
+    const int nck = (a.N + a.spacing - 1) / a.spacing;
 
     for (int i = threadIdx.x; i < K::CH * a.S; i += K::THREADS) {
         const int k = i / a.S;
@@ -150,8 +156,8 @@ __global__ void __launch_bounds__(K::THREADS) scan_forward_kernel(const ScanArgs
             }
             const f2 total2 = pack2(total, total);
             const int start = t0 + tl * K::TL;
-            const bool keep = a.ckpt && start % CKPT == 0 && start < len && ch < nch;
-            float *ck = keep ? a.ckpt + (((long long)b * nck + start / CKPT) * a.D + c0 + ch) * a.S : nullptr;
+            const bool keep = a.ckpt && start % a.spacing == 0 && start < len && ch < nch;
+            float *ck = keep ? a.ckpt + (((long long)b * nck + start / a.spacing) * a.D + c0 + ch) * a.S : nullptr;
             for (int p = 0; p < a.S / 2; ++p) {
                 const f2 r2 = *reinterpret_cast<const f2 *>(rate + ch * a.S + 2 * p);
                 f2 *h0 = reinterpret_cast<f2 *>(hs + ch * a.S + 2 * p);
@@ -330,7 +336,13 @@ extern "C" {
 size_t gma_scan_checkpoint_size(const gma_scan_t *s)
 {
     if (!s || s->B < 1 || s->N < 1 || s->D < 1 || s->S < 1) return 0;
-    return (size_t)s->B * ((s->N + CKPT - 1) / CKPT) * s->D * s->S * sizeof(float);
+    const int spacing = scan_spacing(*s);
+    return (size_t)s->B * ((s->N + spacing - 1) / spacing) * s->D * s->S * sizeof(float);
+}
+
+int gma_scan_checkpoint_tokens(const gma_scan_t *s)
+{
+    return !s || s->B < 1 || s->N < 1 || s->D < 1 || s->S < 1 ? 0 : scan_spacing(*s);
 }
 
 size_t gma_scan_workspace_size(const gma_scan_t *s)

@@ -5,7 +5,7 @@
 //   dc_t = sum_d dp_t h_t,   db_t = sum_d g_t delta_t u_t,   x_t = sum_n b_t g_t,   q_t[n] = r_{t-1} h_{t-1},
 //   du = delta x + D dp,   ddelta = u x + sum_n A q,   dA = sum_t delta q,   ddt = ddelta sigmoid(dt + dt_bias).
 // In four launches:
-//   1, 2. the adjoint r behind every chunk of 64 tokens (each chunk's from zero, then joined);
+//   1, 2. the adjoint r behind every chunk of 64 (or 16) tokens (each chunk's from zero, then joined);
 //   3. every chunk: a warp walks over its channels' tokens forward from the checkpoint, keeping the state in
 //      front of every eighth token in shared memory; then, eight tokens at a time from the last, it
 //      computes their states again into registers and runs the adjoint back over them;
@@ -20,7 +20,7 @@ namespace gma {
 namespace blk {
 namespace {
 
-constexpr int WARPS = 4, THREADS = 32 * WARPS, SUB = 8, SUBS = CKPT / SUB;
+constexpr int WARPS = 4, THREADS = 32 * WARPS, SUB = 8;
 constexpr int NF = 4;                        // pairs of states of a lane
 constexpr float LN2 = 0.69314718055994531f;
 
@@ -97,33 +97,34 @@ template <bool VEC> __device__ __forceinline__ void store4(float *p, int n, cons
 constexpr int RED_ROW = 20;
 template <int S> __device__ __forceinline__ int red_row(int r) { return r * RED_ROW + r / (S == 16 ? 16 : 8) * 16; }
 
-// One warp's share of shared memory.
-template <int S> struct WarpSmem {
+// One warp's share of shared memory; CK: the chunk's tokens.
+template <int S, int CK> struct WarpSmem {
     static constexpr int CHW = Lane<S>::CHW;
-    f2 start[SUBS][NF][32];                                  // the states in front of every eighth token
+    f2 start[CK / SUB][NF][32];                                // the states in front of every eighth token
     float red[2][32 * RED_ROW + 48];                         // two tokens' products by lane, 16 values a row
     // eight tokens: delta; u, then du; dp, then ddelta; p
     float dt[SUB][CHW], u[SUB][CHW], dp[SUB][CHW], p[SUB][CHW];
 };
-template <int S> struct Smem {
-    WarpSmem<S> w[WARPS];
+template <int S, int CK> struct Smem {
+    WarpSmem<S, CK> w[WARPS];
     f2 sums[WARPS][SUB][S];                                  // db and dc of eight tokens by warp
-    float b[CKPT][S], c[CKPT][S];
+    float b[CK][S], c[CK][S];
 };
 
-template <typename T, int S, bool VEC, bool Z>
+template <typename T, int S, int CK, bool VEC, bool Z>
 __global__ void __launch_bounds__(THREADS, 3) scan_backward_kernel(const GradArgs<T> g)
 {
     constexpr int SPLIT = Lane<S>::SPLIT, CHW = Lane<S>::CHW, CH = Lane<S>::CH;
     extern __shared__ __align__(16) unsigned char raw[];
-    Smem<S> &sm = *reinterpret_cast<Smem<S> *>(raw);
+    typedef Smem<S, CK> Sm;
+    Sm &sm = *reinterpret_cast<Sm *>(raw);
     let_next();
     const ScanArgs<T> &a = g.f;
-    const int b = blockIdx.z, k = blockIdx.y, t0 = k * CKPT;
-    const int len = row_length(a.lengths, b, a.N), count = min(CKPT, len - t0);
+    const int b = blockIdx.z, k = blockIdx.y, t0 = k * CK;
+    const int len = row_length(a.lengths, b, a.N), count = min(CK, len - t0);
     const int group = blockIdx.x / a.tiles, Dg = a.D / a.G;
     if (a.zero) {
-        const int i0 = (blockIdx.x - group * a.tiles) * CH, rows = min(CKPT, a.N - t0);
+        const int i0 = (blockIdx.x - group * a.tiles) * CH, rows = min(CK, a.N - t0);
         const float none[4] = {0.f, 0.f, 0.f, 0.f};
         for (int i = threadIdx.x; i < rows * (CH / 4); i += THREADS) {
             const int t = i / (CH / 4), ch = i0 + i % (CH / 4) * 4, n = min(4, Dg - ch);
@@ -145,7 +146,7 @@ __global__ void __launch_bounds__(THREADS, 3) scan_backward_kernel(const GradArg
     const int warp_ch = (blockIdx.x - group * a.tiles) * CH + warp * CHW;        // in the group
     const bool on = warp_ch + lane % CHW < Dg;
     const int c = group * Dg + warp_ch + lane % CHW;
-    WarpSmem<S> &ws = sm.w[warp];
+    WarpSmem<S, CK> &ws = sm.w[warp];
 
     // b and c of the chunk
     for (int i = threadIdx.x; i < count * (S / 8); i += THREADS) {
@@ -454,7 +455,7 @@ struct Layout {
 };
 Layout layout(const gma_scan_t &s)
 {
-    const size_t tiles = (s.D / s.G + channels_of(s.S) - 1) / channels_of(s.S), chunks = (s.N + CKPT - 1) / CKPT;
+    const size_t tiles = (s.D / s.G + channels_of(s.S) - 1) / channels_of(s.S), chunks = (s.N + scan_spacing(s) - 1) / scan_spacing(s);
     const size_t row = align_up((size_t)s.B * chunks * s.D * sizeof(float), 256);
     Layout l;
     l.bc = 0;
@@ -466,16 +467,21 @@ Layout layout(const gma_scan_t &s)
     return l;
 }
 
-template <typename T, int S> gma_status_t launch(const GradArgs<T> &g, bool vec, cudaStream_t st)
+template <typename T, int S, int CK> gma_status_t launch_ck(const GradArgs<T> &g, bool vec, cudaStream_t st)
 {
     const bool z = g.f.z.p != nullptr;
-    auto kern = vec ? (z ? scan_backward_kernel<T, S, true, true> : scan_backward_kernel<T, S, true, false>)
-                    : (z ? scan_backward_kernel<T, S, false, true> : scan_backward_kernel<T, S, false, false>);
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<S>)) != cudaSuccess)
+    auto kern = vec ? (z ? scan_backward_kernel<T, S, CK, true, true> : scan_backward_kernel<T, S, CK, true, false>)
+                    : (z ? scan_backward_kernel<T, S, CK, false, true> : scan_backward_kernel<T, S, CK, false, false>);
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<S, CK>)) != cudaSuccess)
         return GMA_ERR_CUDA;
     GMA_LAUNCH(KID_SCAN_BWD, st,
-               launch_pdl(kern, dim3(g.f.tiles * g.f.G, g.chunks, g.f.B), dim3(THREADS), sizeof(Smem<S>), st, g));
+               launch_pdl(kern, dim3(g.f.tiles * g.f.G, g.chunks, g.f.B), dim3(THREADS), sizeof(Smem<S, CK>), st, g));
     return GMA_OK;
+}
+
+template <typename T, int S> gma_status_t launch(const GradArgs<T> &g, bool vec, cudaStream_t st)
+{
+    return g.f.spacing == 16 ? launch_ck<T, S, 16>(g, vec, st) : launch_ck<T, S, 64>(g, vec, st);
 }
 
 template <typename T> gma_status_t backward_of(const gma_scan_grad_t &s, char *ws, cudaStream_t st)
@@ -486,7 +492,7 @@ template <typename T> gma_status_t backward_of(const gma_scan_grad_t &s, char *w
     GradArgs<T> g;
     g.f = scan_args<T>(f);
     g.f.tiles = (f.D / f.G + ch - 1) / ch;
-    g.chunks = (f.N + CKPT - 1) / CKPT;
+    g.chunks = (f.N + g.f.spacing - 1) / g.f.spacing;
     g.dy = rows_of<const T>(s.dy);
     g.du = rows_of<T>(s.du); g.ddt = rows_of<T>(s.ddt); g.dz = rows_of<T>(s.dz);
     g.db = rows_of<T>(s.db); g.dc = rows_of<T>(s.dc);
@@ -540,7 +546,7 @@ gma_status_t gma_scan_backward(const gma_scan_grad_t *g, void *ws, size_t ws_byt
     if (!ptr_ok(g->da_log, 4) || (f.d_skip && !ptr_ok(g->dd_skip, 4)) || (f.dt_bias && !ptr_ok(g->ddt_bias, 4)) ||
         !opt_ok(g->dstate_out, 4) || !opt_ok(g->dstate_in, 4))
         return GMA_ERR_INVALID_ARG;
-    if (D * f.S > 0x3fffffffll || f.G > 65535 || (N + CKPT - 1) / CKPT > 65535) return GMA_ERR_UNSUPPORTED_SHAPE;
+    if (D * f.S > 0x3fffffffll || f.G > 65535 || (N + scan_spacing(f) - 1) / scan_spacing(f) > 65535) return GMA_ERR_UNSUPPORTED_SHAPE;
     if (!ws_ok(ws, ws_bytes, layout(f).size)) return GMA_ERR_WORKSPACE;
     if ((r = usable_device()) != GMA_OK) return r;
     cudaStream_t st = (cudaStream_t)stream;

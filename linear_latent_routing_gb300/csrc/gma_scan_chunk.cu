@@ -302,7 +302,8 @@ template <typename T, int S, bool BACK> __global__ void __launch_bounds__(128) s
     float h = a.state_in ? a.state_in[at] : 0.f;
     float *state = g.state + b * g.chunks * step + i;
     const float *total = g.total + (long long)b * g.chunks * a.D + d;
-    const int nck = (a.N + CKPT - 1) / CKPT;
+    // chunks between two checkpoints, a power of two
+    const int nck = (a.N + a.spacing - 1) / a.spacing, per = max(1, a.spacing / g.chunk), per_log = 31 - __clz(per);
     float *ck = a.ckpt ? a.ckpt + b * nck * step + i : nullptr;
     for (int k0 = 0; k0 < count; k0 += AHEAD) {
         float s[AHEAD], tt[AHEAD];
@@ -318,7 +319,7 @@ template <typename T, int S, bool BACK> __global__ void __launch_bounds__(128) s
             if (k0 + j < count) {
                 const int k = BACK ? count - 1 - k0 - j : k0 + j;
                 state[k * step] = h;
-                if (ck && k * g.chunk % CKPT == 0) ck[k * g.chunk / CKPT * step] = h;
+                if (ck && (k & (per - 1)) == 0) ck[(k >> per_log) * step] = h;
                 h = fmaf(ex2(tt[j] * r), h, s[j]);
             }
     }
@@ -342,14 +343,14 @@ int chunk_of(const gma_scan_t &s)
     const double rows = (double)s.B * s.G * ((warps + per - 1) / per) * per / 8;
     int best = 32;
     double least = 0;
-    for (int c = 32; c <= 256 && c * s.S <= 4096 && !(s.checkpoints && c > CKPT); c *= 2) {
+    for (int c = 32; c <= 256 && c * s.S <= 4096 && !(s.checkpoints && c > scan_spacing(s)); c *= 2) {
         const double waves = rows * ((s.N + c - 1) / c) / 304 + 0.5, cost = (waves > 1 ? waves : 1) * (c + 24);
         if (c == 32 || cost < least) best = c, least = cost;
     }
     return best;
 }
 
-// The backward pass's adjoint in front of (behind, in time) every chunk of CKPT tokens.
+// The backward pass's adjoint behind every chunk.
 template <typename T, int S, bool VEC>
 gma_status_t run_adjoint(const gma_scan_grad_t &grad, float *state, float *total, cudaStream_t st)
 {
@@ -360,13 +361,13 @@ gma_status_t run_adjoint(const gma_scan_grad_t &grad, float *state, float *total
     g.s.state_in = grad.dstate_out;
     g.s.state_out = grad.dstate_in;
     g.s.ckpt = nullptr;
-    g.chunk = CKPT;
-    g.chunks = (s.N + CKPT - 1) / CKPT;
+    g.chunk = g.s.spacing;
+    g.chunks = (s.N + g.chunk - 1) / g.chunk;
     g.state = state;
     g.total = total;
     const int warps = group_warps(s), per = warps < 8 ? warps : 8;
     g.s.tiles = (warps + per - 1) / per;
-    const size_t smem = (size_t)CKPT * S * sizeof(float) + (VEC ? (size_t)per * RING_BYTES : 0);
+    const size_t smem = (size_t)g.chunk * S * sizeof(float) + (VEC ? (size_t)per * RING_BYTES : 0);
     auto kern = scan_chunk_kernel<T, S, VEC, ADJOINT>;
     if (smem > 48 * 1024 &&
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
@@ -415,7 +416,7 @@ template <typename T, int S, bool VEC> gma_status_t run(const gma_scan_t &s, cha
 bool scan_chunked(const gma_scan_t &s)
 {
     const long long warps = (long long)s.B * s.G * group_warps(s) * ((s.N + 31) / 32);
-    return warps >= 152 * 6 && (s.N + 31) / 32 <= 65535 && (long long)s.D * s.S < (1ll << 31);
+    return warps >= 152 * 6 && !(s.checkpoints && scan_spacing(s) < 32) && (s.N + 31) / 32 <= 65535 && (long long)s.D * s.S < (1ll << 31);
 }
 
 size_t scan_chunk_workspace(const gma_scan_t &s)

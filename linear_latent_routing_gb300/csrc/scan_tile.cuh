@@ -17,7 +17,9 @@
 namespace gma {
 namespace blk {
 
-constexpr int CKPT = 64;     // tokens between two checkpoints
+// Tokens between two checkpoints, and of a chunk of the backward pass: 64, or 16 where that leaves fewer than six
+// warps an SM to walk over the chunks (2 x 301 x 384 channels: a walk over 64 tokens takes 33 us).
+int scan_spacing(const gma_scan_t &s);
 
 template <int LT_, int TL_, int WARPS_> struct Tile {
     static constexpr int LT = LT_, TL = TL_, WARPS = WARPS_;
@@ -121,6 +123,7 @@ template <typename T> struct ScanArgs {
     const int *lengths;
     Rows<T> y;
     float *ckpt;
+    int spacing;                   // tokens between two checkpoints
     bool zero;                     // zeros behind a sequence's last token
 };
 
@@ -134,6 +137,7 @@ template <typename T> inline ScanArgs<T> scan_args(const gma_scan_t &s)
     a.state_in = s.state_in; a.state_out = s.state_out; a.lengths = s.lengths;
     a.y = rows_of<T>(s.y);
     a.ckpt = s.checkpoints;
+    a.spacing = scan_spacing(s);
     a.zero = s.flags & GMA_ROWS_ZERO_TAIL;
     return a;
 }
@@ -147,7 +151,7 @@ bool scan_vec(const gma_scan_t &s);
 bool scan_chunked(const gma_scan_t &s);
 size_t scan_chunk_workspace(const gma_scan_t &s);
 gma_status_t scan_chunk_forward(const gma_scan_t &s, void *ws, cudaStream_t st);
-// The adjoint behind every chunk of CKPT tokens, state [B][chunks][D][S] (zeros behind a sequence's end), and
+// The adjoint behind every chunk of scan_spacing() tokens, state [B][chunks][D][S] (zeros behind a sequence's end), and
 // dstate_in; total [B][chunks][D] is scratch.
 gma_status_t scan_chunk_adjoint(const gma_scan_grad_t &grad, float *state, float *total, cudaStream_t st);
 

@@ -14,15 +14,12 @@ import torch
 from . import gma  # noqa: F401  (loads libgma.so, which _block is linked against)
 from . import _block
 
-CHECKPOINT_TOKENS = 64
-
 
 # ------------------------------------------------------------------ selective scan
 
 def scan_checkpoints(u, S):
     """An uninitialised buffer for the states that ``scan`` keeps for ``scan_backward``."""
-    B, N, D = u.shape
-    return torch.empty(B, -(-N // CHECKPOINT_TOKENS), D, S, dtype=torch.float32, device=u.device)
+    return _block.scan_checkpoints(u, S)
 
 
 def scan(u, dt, a_log, b, c, d_skip=None, dt_bias=None, z=None, state=None, state_out=None, lengths=None,

@@ -138,14 +138,41 @@ def test_scan_forward_in_chunks(case, monkeypatch):
     ry, rh = R.scan(**t, lengths=lengths)
     R.check(y, ry, "y")
     R.check(h, rh, "state")
-    if ckpt:      # the state before token 64 is the one after 64 tokens
-        short = {k: v[:, :64] if k in ("u", "dt", "b", "c", "z") and v is not None else v for k, v in t.items()}
+    if ckpt:      # the state before the second checkpoint's token
+        n = 64 if ck.shape[1] == -(-N // 64) else 16
+        assert ck.shape[1] == -(-N // n)
+        short = {k: v[:, :n] if k in ("u", "dt", "b", "c", "z") and v is not None else v for k, v in t.items()}
         want = R.scan(**short, lengths=lengths)[1]
-        if N > 64 and lengths is None:
+        if N > n and lengths is None:
             R.check(ck[:, 1], want, "checkpoint")
         first = t["state"] if state else torch.zeros(B, D, S)
         live = [i for i in range(B) if lengths is None or lengths[i] > 0]
         assert torch.equal(ck[live, 0].cpu(), first[live])
+
+
+BIG_GRADS = [  # enough work for chunks of 64 tokens
+    (2, 700, 1040, 16, 1, "bf16", True, True, [700, 301], 0),
+    (3, 129, 8200, 8, 2, "f32", False, True, [128, 0, 129], 0),
+    (2, 500, 1001, 32, 1, "f32", True, False, None, 3),
+    (1, 450, 520, 64, 2, "bf16", True, True, None, 0),
+]
+
+
+@pytest.mark.parametrize("case", BIG_GRADS, ids=_id)
+def test_scan_backward_in_long_chunks(case, monkeypatch):
+    monkeypatch.setattr(R, "DEVICE", "cuda")
+    B, N, D, S, G, dtype, z, state, lengths, pitch = case
+    ssm, _ = _ops()
+    t, dy, ds = _scan_inputs(B, N, D, S, G, dtype, z, state, seed=15, pitch=pitch)
+    d, y, h, ck, ln = _run_scan(t, lengths, ckpt=True)
+    assert ck.shape[1] == -(-N // 64)
+    g = ssm.scan_backward(dy.cuda(), d["u"], d["dt"], d["a_log"], d["b"], d["c"], ck, d["d_skip"], d["dt_bias"], d["z"],
+                          dstate_out=ds.cuda(), lengths=ln)
+    _, _, ref = R.scan(**t, lengths=lengths, dy=dy, dstate_out=ds)
+    for k in ("u", "dt", "z", "b", "c", "a_log", "d_skip", "dt_bias", "state"):
+        assert (g[k] is None) == (ref[k] is None), k
+        if g[k] is not None:
+            R.check(g[k], ref[k], k)
 
 
 def test_scan_without_optional_parameters():
@@ -276,6 +303,7 @@ def test_scan_of_rates_that_overflow_or_vanish(D):
     x = (delta * t["u"].double())[..., None] * t["b"].double()
     for i, n in enumerate(lengths):
         assert torch.allclose(h[i, :, ::3].cpu().double(), x[i, n - 1, :, ::3], rtol=1e-5, atol=1e-30)
+        # 300 additions and a few roundings of each term
         want = t["state"][i, :, 1::3].double() + x[i, :n, :, 1::3].sum(0)
         scale = (t["state"][i, :, 1::3].double().abs() + x[i, :n, :, 1::3].abs().sum(0))
         assert ((h[i, :, 1::3].cpu().double() - want).abs() <= 400 * 2.0 ** -24 * scale).all()
