@@ -7,6 +7,8 @@
 // front of a run; a warp's accesses are 256 neighbouring bytes of a row (bf16).  Four channels and not eight:
 // the windows then take few enough registers for twice the warps, which hide the loads.  The window is a
 // ring whose slots are fixed by unrolling a whole turn, so no value is moved.
+// Measured (W = 4, bf16): forward 2 x 16384 x 2080 in 57 us (4.8 TB/s; eight channels a thread 71 us, with moved
+// windows 150 us); backward 32 x 1024 x 512, half of it padding, 28 us (42 instructions an element at 128 registers).
 #include "block_common.cuh"
 
 namespace gma {
