@@ -99,12 +99,6 @@ def softplus(x):
     return X(v, torch.special.expit(x.v) * x.e + (x.v.abs() + 10) * U * v)
 
 
-def slope_of_softplus(delta):
-    """sigmoid(x) of delta = softplus(x): 1 - exp(-delta)."""
-    v = -torch.expm1(-delta.v)
-    return X(v, torch.exp(-delta.v) * delta.e + 4 * U * v)
-
-
 def rate_of(a_log):
     """A = -exp(a_log), with the two constants that turn it to base 2 and back."""
     v = -a_log.v.exp()
@@ -177,7 +171,7 @@ def scan(u, dt, a_log, b, c, d_skip=None, dt_bias=None, z=None, state=None, leng
         q = back * (hs[t - 1] if t else first)
         du = x * delta[:, t]
         dus[t] = du + d_skip * dp[:, t] if d_skip is not None else du
-        ddts[t] = (x * u[:, t] + (q * A).sum(2)) * slope_of_softplus(delta[:, t])
+        ddts[t] = (x * u[:, t] + (q * A).sum(2)) * sigmoid(raw[:, t])
         da = da + (q * delta[:, t].map(wide)).sum(0)
         r = where(on, back, r)
     ddt = where(live[..., None], stack(ddts, 1), nothing)
