@@ -302,11 +302,11 @@ template <typename T, int S, bool BACK> __global__ void __launch_bounds__(128) s
     const float r = decay_rate(a.a_log[i]);
     wait_previous();
     float h = a.state_in ? a.state_in[at] : 0.f;
-    float *state = g.state + b * g.chunks * step + i;
+    float *state = g.state + (long long)b * g.chunks * step + i;
     const float *total = g.total + (long long)b * g.chunks * a.D + d;
     // chunks between two checkpoints, a power of two
     const int nck = (a.N + a.spacing - 1) / a.spacing, per = max(1, a.spacing / g.chunk), per_log = 31 - __clz(per);
-    float *ck = a.ckpt ? a.ckpt + b * nck * step + i : nullptr;
+    float *ck = a.ckpt ? a.ckpt + (long long)b * nck * step + i : nullptr;
     for (int k0 = 0; k0 < count; k0 += AHEAD) {
         float s[AHEAD], tt[AHEAD];
 #pragma unroll
