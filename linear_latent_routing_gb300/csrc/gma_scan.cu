@@ -181,6 +181,7 @@ __global__ void __launch_bounds__(K::THREADS) scan_forward_kernel(const ScanArgs
                 const f2 s1 = __shfl_up_sync(0xffffffffu, h, 1, K::LT);
                 const f2 end = fma2(decay, before, h);
                 h = tl ? fma2(d1, before, s1) : before;
+                __syncwarp();                  // every lane has read h0
                 if (tl == K::LT - 1) *h0 = end;
                 if (keep) *reinterpret_cast<f2 *>(ck + 2 * p) = h;
 #pragma unroll

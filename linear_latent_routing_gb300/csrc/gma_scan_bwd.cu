@@ -318,6 +318,7 @@ __global__ void __launch_bounds__(THREADS, 3) scan_backward_kernel(const GradArg
         }
 #pragma unroll
         for (int i2 = SUB - 2; i2 >= 0; i2 -= 2) {
+            float du[2], ddelta[2], pre[2];
 #pragma unroll
             for (int e = 1; e >= 0; --e) {
                 const int i = i2 + e;
@@ -353,13 +354,18 @@ __global__ void __launch_bounds__(THREADS, 3) scan_backward_kernel(const GradArg
                     qv += __shfl_xor_sync(0xffffffffu, qv, off);
                     if (Z) pv += __shfl_xor_sync(0xffffffffu, pv, off);
                 }
-                if (part == 0) {          // the other lanes of the channel have read u and dp: the shuffles came after
-                    ws.u[i][lc] = fmaf(xv, d, skip_c * dpv);
-                    ws.dp[i][lc] = fmaf(xv, uv, qv * LN2);
-                    if (Z) ws.p[i][lc] = fmaf(skip_c, uv, pv);
-                }
+                du[e] = fmaf(xv, d, skip_c * dpv);
+                ddelta[e] = fmaf(xv, uv, qv * LN2);
+                if (Z) pre[e] = fmaf(skip_c, uv, pv);
             }
             __syncwarp();
+            if (part == 0)                // behind the barrier: every lane of the channel has read u and dp
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    ws.u[i2 + e][lc] = du[e];
+                    ws.dp[i2 + e][lc] = ddelta[e];
+                    if (Z) ws.p[i2 + e][lc] = pre[e];
+                }
             // columns: pair j of part `of` over that part's CHW lanes, eight of them a lane
             constexpr int COLS = 8 * SPLIT, PER = COLS <= 32 ? 1 : 2;
 #pragma unroll
