@@ -16,7 +16,8 @@
  *     projection's rows, and any element alignment is taken.  Rows whose addresses and strides are
  *     multiples of 16 bytes take wider accesses.  Output rows must not overlap one another or any
  *     input, unless an entry point says so.  Strides are >= 0.
- *   - Parameters and states are fp32 and contiguous; sums, states and statistics are held in fp32.
+ *   - Parameters and states are fp32 and contiguous; the scan's a_log, states and checkpoints start on
+ *     16-byte boundaries.  Sums, states and statistics are held in fp32.
  *   - `lengths` (NULL, or B int32 in device memory) gives every batch row's number of tokens, taken
  *     as min(max(length, 0), N): the rows behind a sequence's last token are neither read nor
  *     written (with GMA_ROWS_ZERO_TAIL: are written as zeros), and the states that come out are those

@@ -103,6 +103,14 @@ gma_rows_t heads(const at::Tensor &t, const char *name, at::IntArrayRef shape, c
     return gma_rows_t{t.data_ptr(), s[0], shape.size() == 4 ? s[2] : s[1]};
 }
 
+// An output must not start where another tensor of the call does (the header forbids any overlap; rows of one
+// buffer may lie beside one another, so that is as much as the addresses tell).
+void apart(const gma_rows_t &out, const char *name, std::initializer_list<const gma_rows_t *> others)
+{
+    for (const gma_rows_t *o : others)
+        if (out.ptr && out.ptr == o->ptr) value_error(std::string(name) + " must not be another tensor of the call");
+}
+
 template <typename P = float> P *dense(PyObject *o, const char *name, at::IntArrayRef shape, at::ScalarType T, const Call &c)
 {
     if (!given(o)) return nullptr;
@@ -253,6 +261,7 @@ PyObject *scan(PyObject *, PyObject *const *a, Py_ssize_t n)
         if (s.lengths && !given(a[12])) s.flags |= GMA_ROWS_ZERO_TAIL;      // in a buffer allocated here
         const at::Tensor y = out_or(a[12], "out", [&] { return c.empty(full); });
         s.y = rows(y, "out", full, 1, c.T, c);
+        if (given(a[12])) apart(s.y, "out", {&s.u, &s.dt, &s.z, &s.b, &s.c});
         const Workspace ws(gma_scan_workspace_size(&s), c);
         const gma_status_t r = gma_scan_forward(&s, ws.ptr(), ws.bytes, c.stream());
         return r == GMA_OK ? wrap(y) : raise_status(r, "gma_scan_forward");
@@ -270,6 +279,7 @@ PyObject *scan_step(PyObject *, PyObject *const *a, Py_ssize_t n)
         s.state_in = s.state_out;
         const at::Tensor y = out_or(a[9], "out", [&] { return c.empty(full); });
         s.y = rows(y, "out", full, 0, c.T, c);
+        if (given(a[9])) apart(s.y, "out", {&s.u, &s.dt, &s.z, &s.b, &s.c});
         const gma_status_t r = gma_scan_step(&s, c.stream());
         return r == GMA_OK ? wrap(y) : raise_status(r, "gma_scan_step");
     });
@@ -303,6 +313,13 @@ PyObject *scan_backward(PyObject *, PyObject *const *a, Py_ssize_t n)
         if (z) g.dz = rows(dz, "out['z']", full, 1, c.T, c);
         g.db = rows(db, "out['b']", bc, 1, c.T, c);
         g.dc = rows(dc, "out['c']", bc, 1, c.T, c);
+        if (some) {
+            const gma_rows_t *outs[5] = {&g.du, &g.ddt, &g.dz, &g.db, &g.dc};
+            for (int i = 0; i < 5; ++i) {
+                apart(*outs[i], "an output", {&s.u, &s.dt, &s.z, &s.b, &s.c, &g.dy});
+                for (int j = 0; j < i; ++j) apart(*outs[i], "an output", {outs[j]});
+            }
+        }
         const at::Tensor da = c.empty32({D, S}), dstate = c.empty32({B, D, S});
         const at::Tensor dskip = s.d_skip ? c.empty32({D}) : at::Tensor(), dbias = s.dt_bias ? c.empty32({D}) : at::Tensor();
         g.da_log = (float *)da.data_ptr();
@@ -356,6 +373,7 @@ PyObject *conv(PyObject *, PyObject *const *a, Py_ssize_t n)
         if (s.lengths && !given(a[7])) s.flags |= GMA_ROWS_ZERO_TAIL;
         const at::Tensor y = out_or(a[7], "out", [&] { return c.empty(full); });
         s.y = rows(y, "out", full, 1, c.T, c);
+        if (given(a[7])) apart(s.y, "out", {&s.x});
         const gma_status_t r = gma_conv_forward(&s, c.stream());
         return r == GMA_OK ? wrap(y) : raise_status(r, "gma_conv_forward");
     });
@@ -372,6 +390,7 @@ PyObject *conv_step(PyObject *, PyObject *const *a, Py_ssize_t n)
         s.state_out = const_cast<void *>(s.state_in);
         const at::Tensor y = out_or(a[5], "out", [&] { return c.empty(full); });
         s.y = rows(y, "out", full, 0, c.T, c);
+        if (given(a[5])) apart(s.y, "out", {&s.x});
         const gma_status_t r = gma_conv_step(&s, c.stream());
         return r == GMA_OK ? wrap(y) : raise_status(r, "gma_conv_step");
     });
@@ -391,6 +410,7 @@ PyObject *conv_backward(PyObject *, PyObject *const *a, Py_ssize_t n)
         if (s.lengths && !given(a[7])) s.flags |= GMA_ROWS_ZERO_TAIL;
         const at::Tensor dx = out_or(a[7], "out", [&] { return c.empty(full); });
         g.dx = rows(dx, "out", full, 1, c.T, c);
+        if (given(a[7])) apart(g.dx, "out", {&s.x, &g.dy});
         const at::Tensor dw = c.empty32({s.D, s.W}), db = s.bias ? c.empty32({s.D}) : at::Tensor();
         g.dweight = (float *)dw.data_ptr();
         if (s.bias) g.dbias = (float *)db.data_ptr();
@@ -458,10 +478,12 @@ PyObject *block_norm(PyObject *, PyObject *const *a, Py_ssize_t n)
         }
         const at::Tensor r = out_or(a[8], "out", [&] { return at::empty(full, c.options.dtype(R)); });
         s.r = rows(r, "out", full, 1, R, c);
+        if (given(a[8])) apart(s.r, "out", {&s.o, &s.gate});
         at::Tensor h;
         if (s.w_pre) {
             h = out_or(a[9], "out_h", [&] { return c.empty(full); });
             s.h = rows(h, "out_h", full, 1, c.T, c);
+            if (given(a[9])) apart(s.h, "out_h", {&s.o, &s.gate, &s.residual, &s.r});
         }
         const gma_status_t q = gma_norm_forward(&s, c.stream());
         if (q != GMA_OK) return raise_status(q, "gma_norm_forward");
@@ -496,6 +518,7 @@ PyObject *block_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n)
         const at::IntArrayRef shape = tensor(a[0], "o").sizes();
         const at::Tensor d_o = out_or(a[11], "out", [&] { return c.empty(shape); });
         g.d_o = heads(d_o, "out", shape, c, &g.d_o_head);
+        if (given(a[11])) apart(g.d_o, "out", {&s.o, &s.gate, &s.r, &g.dr, &g.dh});
         at::Tensor dgate, dres, dw[3];
         if (s.gate.ptr) {
             dgate = c.empty(full);

@@ -20,7 +20,8 @@ def block_norm(o, w_post=None, gate=None, residual=None, scale=None, w_pre=None,
     Returns (r, h): r [B, N, D] is the new residual stream, in the residual's dtype (the o dtype and v
     itself without a residual), and h [B, N, D] its norm, or None without ``w_pre``.  ``group`` is the
     number of channels that the first norm's mean runs over: 0 for all, or a power of two from 8 to 256
-    that divides D (a head's d, for a norm per head).  ``out`` may be ``residual``.
+    that divides D (a head's d, for a norm per head).  ``out`` may be ``residual``; otherwise outputs do not
+    overlap the inputs or one another.
     """
     if stream is not None:
         with torch.cuda.stream(stream):

@@ -3,7 +3,8 @@ tensors: a binding over ``gma_scan_*`` and ``gma_conv_*`` (``include/gma_block.h
 
 Activations are token-major, [B, N, channels], bf16 or fp32, with contiguous channels and any strides
 between tokens and batch rows, so that they can be parts of a wider projection's rows.  Parameters
-and scan states are contiguous fp32.  ``lengths`` (int32 [B] on the device) gives each batch row's number
+and scan states are contiguous fp32, ``a_log``, states and checkpoints on 16-byte boundaries.  Outputs given
+by the caller must not overlap the inputs or one another.  ``lengths`` (int32 [B] on the device) gives each batch row's number
 of tokens; the rows behind them are neither read nor written (in outputs allocated here they are zero).
 
 ``stream`` is the stream to run on (default: the current one).  Nothing here waits for the GPU.  Tensors
@@ -60,6 +61,8 @@ def scan_backward(dy, u, dt, a_log, b, c, checkpoints, d_skip=None, dt_bias=None
     if stream is not None:
         with torch.cuda.stream(stream):
             return scan_backward(dy, u, dt, a_log, b, c, checkpoints, d_skip, dt_bias, z, dstate_out, lengths, out)
+    if out and not out.keys() <= {"u", "dt", "z", "b", "c"}:
+        raise ValueError(f"out takes 'u', 'dt', 'z', 'b' and 'c', not {sorted(out.keys() - {'u', 'dt', 'z', 'b', 'c'})}")
     given = (out.get(k) for k in ("u", "dt", "z", "b", "c")) if out else (None,) * 5
     return _block.scan_backward(u, dt, a_log, b, c, d_skip, dt_bias, z, dy, checkpoints, dstate_out, lengths, *given)
 

@@ -640,3 +640,32 @@ def test_bindings_refuse_what_does_not_fit():
         norm.block_norm(d["u"], torch.ones(16, device="cuda"), group=12)
     with pytest.raises(ValueError):
         norm.block_norm(d["u"], torch.ones(15, device="cuda"))
+
+
+def test_outputs_that_are_inputs_are_refused():
+    ssm, norm = _ops()
+
+    def bf(*shape):
+        return torch.zeros(*shape, device="cuda", dtype=BF)
+    u, dt, b, c, dy = bf(2, 20, 32), bf(2, 20, 32), bf(2, 20, 16), bf(2, 20, 16), bf(2, 20, 32)
+    a_log = torch.zeros(32, 16, device="cuda")
+    ck = ssm.scan_checkpoints(u, 16)
+    ssm.scan(u, dt, a_log, b, c, checkpoints=ck)
+    w, wn = torch.zeros(32, 4, device="cuda"), torch.ones(32, device="cuda")
+    state = torch.zeros(2, 32, 16, device="cuda")
+    same = bf(2, 20, 32)
+    for call in (lambda: ssm.scan(u, dt, a_log, b, c, out=u), lambda: ssm.scan(u, dt, a_log, b, c, z=same, out=same),
+                 lambda: ssm.scan_step(u[:, 0], dt[:, 0], a_log, b[:, 0], c[:, 0], state, out=dt[:, 0]),
+                 lambda: ssm.scan_backward(dy, u, dt, a_log, b, c, ck, out={"u": dy}),
+                 lambda: ssm.scan_backward(dy, u, dt, a_log, b, c, ck, out={"u": same, "dt": same}),
+                 lambda: ssm.scan_backward(dy, u, dt, a_log, b, c, ck, out={"du": same}),
+                 lambda: ssm.conv(u, w, out=u), lambda: ssm.conv_step(u[:, 0], w, None, bf(2, 3, 32), out=u[:, 0]),
+                 lambda: ssm.conv_backward(dy, u, w, out=dy), lambda: ssm.conv_backward(dy, u, w, out=u),
+                 lambda: norm.block_norm(u, wn, out=u), lambda: norm.block_norm(u, wn, w_pre=wn, out=same, out_h=same),
+                 lambda: norm.block_norm_backward(dy, u, same, wn, out=dy)):
+        with pytest.raises(ValueError):
+            call()
+    # parts of one wider buffer's rows are not the same tensor
+    wide, want = bf(2, 20, 64), ssm.scan(u, dt, a_log, b, c)
+    wide[..., :32] = u
+    assert torch.equal(ssm.scan(wide[..., :32], dt, a_log, b, c, out=wide[..., 32:]), want)
