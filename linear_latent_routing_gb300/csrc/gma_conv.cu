@@ -7,7 +7,7 @@
 // front of a run; a warp's accesses are 256 neighbouring bytes of a row (bf16).  Four channels and not eight:
 // the windows then take few enough registers for twice the warps, which hide the loads.  The window is a
 // ring whose slots are fixed by unrolling a whole turn, so no value is moved.
-// Measured (W = 4, bf16): forward 2 x 16384 x 2080 in 57 us (4.8 TB/s; eight channels a thread 71 us, with moved
+// Measured (W = 4, bf16): forward 2 x 16384 x 2080 in 56 us (4.9 TB/s; eight channels a thread 71 us, with moved
 // windows 150 us); backward 32 x 1024 x 512, half of it padding, 28 us (42 instructions an element at 128 registers).
 #include "block_common.cuh"
 
@@ -334,13 +334,15 @@ __global__ void __launch_bounds__(32 * GWARPS, 2) conv_backward_kernel(const Con
     }
 }
 
-// Tokens of a thread's run: the rows in front of it are read a second time ((W - 1) / run extra), so long
-// runs where there are threads enough (1024 an SM) without cutting further.
-int run_of(const gma_conv_t &c, int longest)
+// Tokens of a thread's run: the rows in front of it are read a second time ((W - 1) / run extra), and its start and
+// end cost as much as a few tokens, so runs as long as they can be with 768 threads an SM, up to 256.  2 x 16384 x 2080: 128 tokens
+// 56 us, 64 tokens 58 us, 256 tokens (384 threads an SM) 68 us; backward 4 x 16384 x 4096: 256 tokens 324 us, 32 tokens
+// 400 us, 512 tokens 354 us.
+int run_of(const gma_conv_t &c)
 {
     const long long groups = (long long)c.B * ((c.D + C - 1) / C);
-    int run = longest;
-    while (run > 8 && groups * ((c.N + run - 1) / run) < 152 * 1024) run /= 2;
+    int run = 256;
+    while (run > 8 && groups * ((c.N + run - 1) / run) < 152 * 768) run /= 2;
     return run;
 }
 
@@ -408,11 +410,9 @@ template <typename F> gma_status_t dispatch(const gma_conv_t &c, bool vec, F f)
     return c.dtype == GMA_BF16 ? with_w(__nv_bfloat16{}) : with_w(float{});
 }
 
-constexpr int RUN = 64, GRUN = 32;      // the longest runs
-
 int grad_runs(const gma_conv_t &c)
 {
-    const int run = run_of(c, GRUN);
+    const int run = run_of(c);
     return (c.N + run - 1) / run;
 }
 
@@ -435,7 +435,7 @@ gma_status_t gma_conv_forward(const gma_conv_t *c, gma_stream_t stream)
     const bool vec = vec_states(*c) && vec4(c->x, c->dtype) && vec4(c->y, c->dtype);
     return dispatch(*c, vec, [&](auto t, auto w, auto v, auto s) -> gma_status_t {
         using T = decltype(t);
-        const ConvArgs<T> a = args_of<T>(*c, run_of(*c, RUN));
+        const ConvArgs<T> a = args_of<T>(*c, run_of(*c));
         // one run more when the sequence ends at the end of the last one (it writes the state)
         const long long runs = c->N / a.run + 1, items = runs * a.groups;
         const long long blocks = (items + THREADS - 1) / THREADS;
@@ -492,7 +492,7 @@ gma_status_t gma_conv_backward(const gma_conv_grad_t *g, void *ws, size_t ws_byt
         using T = decltype(t);
         constexpr int W = decltype(w)::value;
         ConvGradArgs<T> a;
-        a.f = args_of<T>(c, run_of(c, GRUN));
+        a.f = args_of<T>(c, run_of(c));
         a.dy = rows_of<const T>(g->dy);
         a.dx = rows_of<T>(g->dx);
         a.part = (float *)ws;

@@ -349,6 +349,8 @@ CONVS = [  # B, N, D, W, dtype, silu, bias, state, lengths, pitch
     (2, 33, 17, 3, "bf16", False, True, True, [33, 32], 1),
     (2, 64, 520, 4, "bf16", True, True, False, None, 24),
     (4, 47, 8, 2, "f32", True, True, True, [1, 47, 16, 48], 8),
+    (2, 2000, 8208, 4, "bf16", True, True, True, [1937, 64], 0),         # runs of 64 tokens
+    (1, 4100, 8200, 3, "f32", True, False, False, None, 0),
 ]
 
 
