@@ -176,6 +176,7 @@ __global__ void __launch_bounds__(256, 2) scan_chunk_kernel(const ChunkArgs<T> g
     if (OUT && n > 0 && a.d_skip) skip.x = a.d_skip[c];
     if (OUT && n > 1 && a.d_skip) skip.y = a.d_skip[c + 1];
     __syncthreads();
+    if (warp_ch >= Dg) return;
 
     T *yp = OUT ? a.y.at(b, t0) + c : nullptr;
     auto token = [&](int t, float2 uu, float2 dd, float2 zz) {
@@ -336,13 +337,23 @@ int group_warps(const gma_scan_t &s)
     return s.S <= 16 ? warps_of<16>(s) : s.S == 32 ? warps_of<32>(s) : warps_of<64>(s);
 }
 
+// Blocks of up to eight warps over a group's channels, as even as they can be (260 channels of 32 a warp: 5 + 5, not 8 + 8).
+struct Blocks {
+    int tiles, warps;
+};
+Blocks blocks_of(const gma_scan_t &s)
+{
+    const int warps = group_warps(s), tiles = (warps + 7) / 8;
+    return Blocks{tiles, (warps + tiles - 1) / tiles};
+}
+
 // Tokens of a chunk, of 32, 64, 128 and 256: what takes least by (waves + 1/2) (chunk + 24), where a wave is
 // the 304 blocks that run at once and 24 tokens' time goes into a chunk's start and the join.  A chunk's b and c
 // stay within 32 KB (two blocks an SM), and a chunk does not step over a checkpoint.
 int chunk_of(const gma_scan_t &s)
 {
-    const int warps = group_warps(s), per = warps < 8 ? warps : 8;
-    const double rows = (double)s.B * s.G * ((warps + per - 1) / per) * per / 8;
+    const Blocks blocks = blocks_of(s);
+    const double rows = (double)s.B * s.G * blocks.tiles * blocks.warps / 8;
     int best = 32;
     double least = 0;
     for (int c = 32; c <= 256 && c * s.S <= 4096 && !(s.checkpoints && c > scan_spacing(s)); c *= 2) {
@@ -367,8 +378,9 @@ gma_status_t run_adjoint(const gma_scan_grad_t &grad, float *state, float *total
     g.chunks = (s.N + g.chunk - 1) / g.chunk;
     g.state = state;
     g.total = total;
-    const int warps = group_warps(s), per = warps < 8 ? warps : 8;
-    g.s.tiles = (warps + per - 1) / per;
+    const Blocks blocks = blocks_of(s);
+    const int per = blocks.warps;
+    g.s.tiles = blocks.tiles;
     const size_t smem = (size_t)g.chunk * S * sizeof(float) + (VEC ? (size_t)per * RING_BYTES : 0);
     auto kern = scan_chunk_kernel<T, S, VEC, ADJOINT>;
     if (smem > 48 * 1024 &&
@@ -388,8 +400,9 @@ template <typename T, int S, bool VEC> gma_status_t run(const gma_scan_t &s, cha
     g.chunks = (s.N + g.chunk - 1) / g.chunk;
     g.state = (float *)ws;
     g.total = (float *)(ws + align_up((size_t)s.B * g.chunks * s.D * S * sizeof(float), 256));
-    const int warps = group_warps(s), per = warps < 8 ? warps : 8;
-    g.s.tiles = (warps + per - 1) / per;
+    const Blocks blocks = blocks_of(s);
+    const int per = blocks.warps;
+    g.s.tiles = blocks.tiles;
     const dim3 grid(g.s.tiles * s.G, g.chunks, s.B);
     const bool vec_bc = rows_vec(s.b, s.dtype) && rows_vec(s.c, s.dtype);
     const size_t rows = (size_t)g.chunk * S * sizeof(float), ring = VEC ? (size_t)per * RING_BYTES : 0;
