@@ -238,6 +238,45 @@ struct SumVec {
     long long out_stride;
 };
 constexpr int MAX_SUMS = 5;
+struct SumList {
+    SumVec v[MAX_SUMS];
+    unsigned first[MAX_SUMS + 1];        // first block of each vector; [count]: how many there are
+    int count;
+    long long rows;
+};
+SumList sum_list(const SumVec *vecs, int count, long long rows);
+
+// A block of 256 threads' share: 32 columns (one 128-byte line a row), eight warps of four independent sums each over
+// every 32nd row, then the warps in order.  The partial rows were just written and come from L2.
+__device__ __forceinline__ void sum_rows_block(const SumList &l, unsigned block)
+{
+    __shared__ float s[8][33];
+    int k = 0;
+#pragma unroll
+    for (int j = 1; j < MAX_SUMS; ++j)
+        if (j < l.count && block >= l.first[j]) k = j;
+    const SumVec v = l.v[k];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long i = (long long)(block - l.first[k]) * 32 + lane;
+    float a[4] = {0.f, 0.f, 0.f, 0.f};
+    if (i < v.n) {
+        const float *p = v.part + i;
+        long long r = warp;
+        for (; r + 24 < l.rows; r += 32)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) a[u] += p[(r + 8 * u) * v.row_stride];
+        for (; r < l.rows; r += 8) a[0] += p[r * v.row_stride];
+    }
+    s[warp][lane] = (a[0] + a[1]) + (a[2] + a[3]);
+    __syncthreads();
+    if (warp == 0 && i < v.n) {
+        float t = 0.f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) t += s[w][lane];
+        v.out[i * v.out_stride] = t;
+    }
+}
+
 gma_status_t sum_rows(const SumVec *vecs, int count, long long rows, cudaStream_t st);
 
 inline bool ws_ok(const void *ws, size_t have, size_t need)

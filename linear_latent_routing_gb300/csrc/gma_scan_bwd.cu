@@ -9,7 +9,7 @@
 //   3. every chunk: a warp walks over its channels' tokens forward from the checkpoint, keeping the state in
 //      front of every eighth token in shared memory; then, eight tokens at a time from the last, it
 //      computes their states again into registers and runs the adjoint back over them;
-//   4. sums of the blocks' partial db and dc, and of the chunks' partial parameter gradients.
+//   4. sums of the blocks' partial db and dc, and of the chunks' partial parameter gradients, in one launch.
 // A lane holds eight states of a channel (S / 8 lanes a channel) and their eight tokens' history in 64
 // registers, so that 16 warps fit an SM; x, q and p are added over a channel's lanes by shuffles.  db and dc are
 // sums over channels: a warp passes its lanes' products through shared memory (lanes write rows, read
@@ -449,15 +449,20 @@ __global__ void __launch_bounds__(THREADS, 3) scan_backward_kernel(const GradArg
     }
 }
 
-// db and dc: the groups' blocks of channels in order, four states a thread.
-template <typename T> __global__ void __launch_bounds__(256) scan_bc_kernel(const GradArgs<T> g)
+// The parameters' sums (the first blocks), and db and dc: the groups' blocks of channels in order, four states a thread,
+// `blocks` blocks a batch row and group.
+template <typename T> __global__ void __launch_bounds__(256) scan_sums_kernel(const GradArgs<T> g, const SumList l, unsigned blocks)
 {
-    let_next();
     wait_previous();
+    if (blockIdx.x < l.first[l.count]) {
+        sum_rows_block(l, blockIdx.x);
+        return;
+    }
     const ScanArgs<T> &a = g.f;
     const int per = a.S / 2;                                  // float4 of a token and group
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-    const int q = (int)(i % per), b = blockIdx.y, group = blockIdx.z;
+    const unsigned block = blockIdx.x - l.first[l.count], row = block / blocks;
+    const long long i = (long long)(block - row * blocks) * 256 + threadIdx.x;
+    const int q = (int)(i % per), b = row % a.B, group = row / a.B;
     const long long t = i / per;
     T *out = (q % 4 < 2 ? g.db : g.dc).at(b, (int)t) + group * a.S + q / 4 * 8 + q % 2 * 4;   // per eight states: db, then dc
     if (t >= row_length(a.lengths, b, a.N)) {
@@ -476,6 +481,9 @@ template <typename T> __global__ void __launch_bounds__(256) scan_bc_kernel(cons
 }
 
 int channels_of(int S) { return S == 8 ? Lane<8>::CH : S == 16 ? Lane<16>::CH : S == 32 ? Lane<32>::CH : Lane<64>::CH; }
+
+// Blocks of step 4 for db and dc of a batch row and group.
+long long bc_blocks(const gma_scan_t &s) { return ((long long)s.N * (s.S / 2) + 255) / 256; }
 
 struct Layout {
     size_t bc, state, total, skip, bias, size;
@@ -533,14 +541,15 @@ template <typename T> gma_status_t backward_of(const gma_scan_grad_t &s, char *w
     r = f.S == 8 ? launch<T, 8>(g, vec, st) : f.S == 16 ? launch<T, 16>(g, vec, st)
       : f.S == 32 ? launch<T, 32>(g, vec, st) : launch<T, 64>(g, vec, st);
     if (r != GMA_OK) return r;
-    const long long threads = (long long)f.N * (f.S / 2);
-    GMA_LAUNCH(KID_SCAN_BC, st,
-               launch_pdl(scan_bc_kernel<T>, dim3((unsigned)((threads + 255) / 256), f.B, f.G), dim3(256), 0, st, g));
     SumVec v[3] = {{g.state, (long long)f.D * f.S, (long long)f.D * f.S, s.da_log, 1}};
     int count = 1;
     if (f.d_skip) v[count++] = SumVec{g.skip, f.D, f.D, s.dd_skip, 1};
     if (f.dt_bias) v[count++] = SumVec{g.bias, f.D, f.D, s.ddt_bias, 1};
-    return sum_rows(v, count, (long long)f.B * g.chunks, st);
+    const SumList sums = sum_list(v, count, (long long)f.B * g.chunks);
+    const unsigned blocks = (unsigned)bc_blocks(f);
+    GMA_LAUNCH(KID_SCAN_BC, st,
+               launch_pdl(scan_sums_kernel<T>, dim3(sums.first[count] + blocks * f.B * f.G), dim3(256), 0, st, g, sums, blocks));
+    return GMA_OK;
 }
 
 }  // namespace
@@ -573,7 +582,7 @@ gma_status_t gma_scan_backward(const gma_scan_grad_t *g, void *ws, size_t ws_byt
     if (!ptr_ok(g->da_log, 4) || (f.d_skip && !ptr_ok(g->dd_skip, 4)) || (f.dt_bias && !ptr_ok(g->ddt_bias, 4)) ||
         !opt_ok(g->dstate_out, 4) || !opt_ok(g->dstate_in, 4))
         return GMA_ERR_INVALID_ARG;
-    if (D * f.S > 0x3fffffffll || f.G > 65535 || (N + scan_spacing(f) - 1) / scan_spacing(f) > 65535) return GMA_ERR_UNSUPPORTED_SHAPE;
+    if (D * f.S > 0x3fffffffll || f.G > 65535 || bc_blocks(f) * B * f.G > 0x3fffffffll || (N + scan_spacing(f) - 1) / scan_spacing(f) > 65535) return GMA_ERR_UNSUPPORTED_SHAPE;
     if (!ws_ok(ws, ws_bytes, layout(f).size)) return GMA_ERR_WORKSPACE;
     if ((r = usable_device()) != GMA_OK) return r;
     cudaStream_t st = (cudaStream_t)stream;

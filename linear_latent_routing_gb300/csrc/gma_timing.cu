@@ -61,7 +61,7 @@ const char *kernel_name(int id)
     case KID_SCAN: return "scan_forward";
     case KID_SCAN_STEP: return "scan_step";
     case KID_SCAN_BWD: return "scan_backward";
-    case KID_SCAN_BC: return "scan_backward_bc_sum";
+    case KID_SCAN_BC: return "scan_backward_sums";
     case KID_CONV: return "conv_forward";
     case KID_CONV_STEP: return "conv_step";
     case KID_CONV_BWD: return "conv_backward";
