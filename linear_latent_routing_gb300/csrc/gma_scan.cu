@@ -7,7 +7,7 @@
 // each (token, channel, state) takes one exponential and about five multiply-adds in fp32.  The kernel here
 // spreads a tile's tokens over the lanes of a warp and needs one launch; it takes the calls with too few channels
 // and tokens to fill the GPU in chunks (gma_scan_chunk.cu).  Latency bounds it there: 512 tokens of 1024
-// channels x 16 states take 15 us, 32 tokens 12 us.  The step moves its state once: 128 x 2048 x 16 in 10 us
+// channels x 16 states take 15 us, 32 tokens 12 us.  The step moves its state once: 128 x 2048 x 16 in 11 us
 // (33.5 MB), one row of 1024 channels in the time of a launch.
 #include <type_traits>
 
@@ -231,9 +231,9 @@ __global__ void __launch_bounds__(K::THREADS) scan_forward_kernel(const ScanArgs
             a.state_out[((long long)b * a.D + c0) * a.S + i] = hs[i];
 }
 
-// One token: a lane holds four states of a channel, S / 4 lanes a channel.  The state is read and
-// written once, which bounds it.  With many batch rows a lane takes ROWS of them, whose loads are in flight
-// together and whose rates are computed once.
+// One token: a lane holds four states of a channel, S / 4 lanes a channel.  The state is read and written once, which
+// bounds it.  A block walks over batch rows, the next row's loads in flight, with its channels' rates computed once:
+// 512 x 2048 x 16 in 29 us (a block for every two rows 38 us, every row 43 us), 128 in 11 us (13, 15).
 __device__ __forceinline__ void quad(const __nv_bfloat16 *p, bool vec, float (&v)[4])
 {
     if (vec) {
@@ -256,27 +256,31 @@ __device__ __forceinline__ void quad(const float *p, bool vec, float (&v)[4])
     }
 }
 
-template <typename T, int S, int ROWS>
-__global__ void __launch_bounds__(256) scan_step_kernel(const ScanArgs<T> a, bool vec)
+constexpr int STEP_BLOCKS = 4;       // an SM
+template <typename T, int S>
+__global__ void __launch_bounds__(256, STEP_BLOCKS) scan_step_kernel(const ScanArgs<T> a, bool vec, int rows)
 {
     constexpr int LPC = S / 4, CPB = 256 / LPC;
-    const int d = blockIdx.x * CPB + threadIdx.x / LPC, q = threadIdx.x % LPC, b0 = blockIdx.y * ROWS;
+    const int d = blockIdx.x * CPB + threadIdx.x / LPC, q = threadIdx.x % LPC;
+    const int b0 = blockIdx.y * rows, end = min(a.B, b0 + rows);
     const bool on = d < a.D;
-    float4 h4[ROWS];
-    float u[ROWS], dt[ROWS], z[ROWS], bv[ROWS][4], cv[ROWS][4], y[ROWS];
-#pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-        y[r] = 0.f;
-        const int b = b0 + r;
-        if (!on || b >= a.B) continue;
-        const int first = d / (a.D / a.G) * S + 4 * q;
-        h4[r] = *reinterpret_cast<const float4 *>(a.state_in + ((long long)b * a.D + d) * S + 4 * q);
-        u[r] = to_f32<T>(a.u.at(b, 0)[d]);
-        dt[r] = to_f32<T>(a.dt.at(b, 0)[d]);
-        z[r] = a.z.p && q == 0 ? to_f32<T>(a.z.at(b, 0)[d]) : 0.f;
-        quad(a.b.at(b, 0) + first, vec, bv[r]);
-        quad(a.c.at(b, 0) + first, vec, cv[r]);
-    }
+    struct Row {
+        float4 h;
+        T u, dt, z;
+        float b[4], c[4];
+    };
+    const int first = d / (a.D / a.G) * S + 4 * q;
+    auto load = [&](int b, Row &r) {
+        if (!on || b >= end) return;
+        r.h = *reinterpret_cast<const float4 *>(a.state_in + ((long long)b * a.D + d) * S + 4 * q);
+        r.u = a.u.at(b, 0)[d];
+        r.dt = a.dt.at(b, 0)[d];
+        if (a.z.p && q == 0) r.z = a.z.at(b, 0)[d];
+        quad(a.b.at(b, 0) + first, vec, r.b);
+        quad(a.c.at(b, 0) + first, vec, r.c);
+    };
+    Row cur, next;
+    load(b0, cur);
     float rate[4] = {0.f, 0.f, 0.f, 0.f}, bias = 0.f, skip = 0.f;
     if (on) {
         const float4 v = *reinterpret_cast<const float4 *>(a.a_log + (long long)d * S + 4 * q);
@@ -285,30 +289,27 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const ScanArgs<T> a, boo
         if (a.dt_bias) bias = a.dt_bias[d];
         if (a.d_skip) skip = a.d_skip[d];
     }
+    for (int b = b0; b < end; ++b) {
+        load(b + 1, next);
+        float y = 0.f;
+        if (on) {
+            const float delta = softplus(to_f32<T>(cur.dt) + bias), xu = delta * to_f32<T>(cur.u);
+            float h[4] = {cur.h.x, cur.h.y, cur.h.z, cur.h.w};
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-        const int b = b0 + r;
-        if (!on || b >= a.B) continue;
-        const float delta = softplus(dt[r] + bias), xu = delta * u[r];
-        float h[4] = {h4[r].x, h4[r].y, h4[r].z, h4[r].w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            h[k] = fmaf(ex2(rate[k] * delta), h[k], xu * bv[r][k]);
-            y[r] = fmaf(cv[r][k], h[k], y[r]);
+            for (int k = 0; k < 4; ++k) {
+                h[k] = fmaf(ex2(rate[k] * delta), h[k], xu * cur.b[k]);
+                y = fmaf(cur.c[k], h[k], y);
+            }
+            *reinterpret_cast<float4 *>(a.state_out + ((long long)b * a.D + d) * S + 4 * q) = make_float4(h[0], h[1], h[2], h[3]);
         }
-        *reinterpret_cast<float4 *>(a.state_out + ((long long)b * a.D + d) * S + 4 * q) = make_float4(h[0], h[1], h[2], h[3]);
-    }
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r)
-#pragma unroll
-        for (int off = LPC / 2; off; off >>= 1) y[r] += __shfl_xor_sync(0xffffffffu, y[r], off);
-#pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-        const int b = b0 + r;
-        if (!on || b >= a.B || q != 0) continue;
-        float v = fmaf(skip, u[r], y[r]);
-        if (a.z.p) v *= silu(z[r]);
-        a.y.at(b, 0)[d] = from_f32<T>(v);
+        for (int off = LPC / 2; off; off >>= 1) y += __shfl_xor_sync(0xffffffffu, y, off);
+        if (on && q == 0) {
+            float v = fmaf(skip, to_f32<T>(cur.u), y);
+            if (a.z.p) v *= silu(to_f32<T>(cur.z));
+            a.y.at(b, 0)[d] = from_f32<T>(v);
+        }
+        cur = next;
     }
 }
 
@@ -381,13 +382,12 @@ gma_status_t gma_scan_step(const gma_scan_t *s, gma_stream_t stream)
         const ScanArgs<T> a = scan_args<T>(*s);
         const int cpb = 256 / (s->S / 4), tiles = (s->D + cpb - 1) / cpb;
         const bool vec = rows_vec(s->b, s->dtype) && rows_vec(s->c, s->dtype);
-        // two batch rows a lane once that still leaves four blocks an SM
-        const bool two = (long long)tiles * s->B >= 2 * 4 * 152;
-        const dim3 grid(tiles, two ? (s->B + 1) / 2 : s->B);
+        // as many batch rows a block as leave STEP_BLOCKS blocks an SM
+        const long long at_once = 152 * STEP_BLOCKS;
+        const int rows = (int)(((long long)tiles * s->B + at_once - 1) / at_once);
+        const dim3 grid(tiles, (s->B + rows - 1) / rows);
         auto launch = [&](auto n) -> gma_status_t {
-            constexpr int S = decltype(n)::value;
-            GMA_LAUNCH(KID_SCAN_STEP, st, if (two) scan_step_kernel<T, S, 2><<<grid, 256, 0, st>>>(a, vec);
-                       else scan_step_kernel<T, S, 1><<<grid, 256, 0, st>>>(a, vec));
+            GMA_LAUNCH(KID_SCAN_STEP, st, scan_step_kernel<T, decltype(n)::value><<<grid, 256, 0, st>>>(a, vec, rows));
             return GMA_OK;
         };
         return s->S == 8 ? launch(std::integral_constant<int, 8>{}) : s->S == 16 ? launch(std::integral_constant<int, 16>{})

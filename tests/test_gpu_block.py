@@ -262,7 +262,8 @@ def test_scan_state_in_place_and_pieces_of_a_sequence():
 
 @pytest.mark.parametrize("B,D,S,G,dtype,z", [(1, 1, 8, 1, "f32", False), (3, 70, 16, 2, "bf16", True),
                                             (130, 33, 32, 1, "bf16", False), (2, 512, 64, 1, "f32", True),
-                                            (201, 600, 16, 1, "bf16", True), (201, 601, 16, 1, "f32", False)])
+                                            (201, 600, 16, 1, "bf16", True), (201, 601, 16, 1, "f32", False),
+                                            (67, 1000, 16, 1, "f32", True), (301, 520, 64, 2, "bf16", True)])
 def test_scan_step(B, D, S, G, dtype, z):
     ssm, _ = _ops()
     t, _, _ = _scan_inputs(B, 1, D, S, G, dtype, z, True, seed=6)
