@@ -11,13 +11,14 @@
 //      computes their states again into registers and runs the adjoint back over them;
 //   4. sums of the blocks' partial db and dc, and of the chunks' partial parameter gradients, in one launch.
 // A lane holds eight states of a channel (S / 8 lanes a channel) and their eight tokens' history in 64
-// registers, so that 16 warps fit an SM; x, q and p are added over a channel's lanes by shuffles.  db and dc are
+// registers, so that 12 warps fit an SM; x, q and p are added over a channel's lanes by shuffles.  db and dc are
 // sums over channels: a warp passes its lanes' products through shared memory (lanes write rows, read
 // columns), a block adds its warps, and step 4 the blocks, always in the same order.
-// Measured: 4 x 2048 x 1024 channels x 16 states, bf16 with a gate: 41 us, 10 us, 186 us and 12 + 8 us.  Step 3
-// takes 422 instructions an element (three exponentials a state, 47 shared-memory loads) at 53 % of the issue
-// slots with 11 warps an SM; waits on shared memory and shuffles are what is left.  Tokens over
-// lanes, as in gma_scan.cu, took 303 us for the same step.
+// Measured: 4 x 2048 x 1024 channels x 16 states, bf16 with a gate: 41 us, 10 us, 184 us and 10 us.  Step 3
+// takes 422 instructions an element (three exponentials a state) at 50 % of the issue slots with 11 warps an SM; the
+// shared-memory pipe binds it (76 % busy: 78 wavefronts a token of a warp, 32 of them the column sums').  Two channels
+// of four states a lane halve those, but stage every value twice and spill: 224 us.  Tokens over lanes, as in
+// gma_scan.cu, took 303 us.
 #include "scan_tile.cuh"
 
 namespace gma {
