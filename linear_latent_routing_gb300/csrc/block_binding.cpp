@@ -23,6 +23,7 @@ struct Fail {
 };
 [[noreturn]] void type_error(const std::string &w) { throw Fail{PyExc_TypeError, w}; }
 [[noreturn]] void value_error(const std::string &w) { throw Fail{PyExc_ValueError, w}; }
+struct Raised {};        // a Python exception is set already
 
 std::string list_of(at::IntArrayRef s)
 {
@@ -154,6 +155,7 @@ template <typename F> PyObject *guarded(Py_ssize_t have, Py_ssize_t want, F f)
         return f();
     } catch (const Fail &e) {
         PyErr_SetString(e.type, e.words.c_str());
+    } catch (const Raised &) {
     } catch (const c10::OutOfMemoryError &e) {
         PyErr_SetString(PyExc_MemoryError, e.what_without_backtrace());
     } catch (const std::exception &e) {
@@ -495,7 +497,7 @@ PyObject *block_norm(PyObject *, PyObject *const *a, Py_ssize_t n)
     });
 }
 
-// ..., dr, r, dh, residual (truth value or None), out
+// ..., dr, r, dh, residual (the forward call's tensor, a truth value or None), out
 PyObject *block_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
     return guarded(n, 12, [&]() -> PyObject * {
@@ -507,7 +509,15 @@ PyObject *block_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n)
         const at::Tensor &kept = tensor(a[8], "r");
         const at::ScalarType R = stream_type(kept, "r", c);
         s.r = rows(kept, "r", full, 1, R, c);
-        const bool residual = given(a[10]) ? PyObject_IsTrue(a[10]) == 1 : s.scale || R != c.T;
+        bool residual = s.scale || R != c.T;
+        if (given(a[10]) && THPVariable_Check(a[10])) {
+            rows(a[10], "residual", full, 1, R, c);       // checked alone: its values are not used
+            residual = true;
+        } else if (given(a[10])) {
+            const int truth = PyObject_IsTrue(a[10]);
+            if (truth < 0) throw Raised{};
+            residual = truth != 0;
+        }
         if (!residual && R != c.T) type_error("without a residual r has o's dtype");
         if (residual) {
             s.residual = s.r;

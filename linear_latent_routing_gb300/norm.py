@@ -34,8 +34,8 @@ def block_norm_backward(dr, o, r, w_post=None, gate=None, scale=None, w_pre=None
     """Gradients of sum(dr * r) + sum(dh * h) of ``block_norm`` with the same arguments.
 
     ``r`` is what the forward call returned (its dtype tells the residual stream's); ``residual`` says
-    whether there was a residual; by default there was one if there is a ``scale`` or r's dtype is
-    another than o's.  Either of dr and dh may be None.  Returns a dict: "o" (o's layout, contiguous, or
+    whether there was a residual: the forward call's tensor, whose values are not used, or a truth value.
+    By default there was one if there is a ``scale`` or r's dtype is another than o's.  Either of dr and dh may be None.  Returns a dict: "o" (o's layout, contiguous, or
     ``out``), "gate", "residual" (None without one), "w_post", "scale", "w_pre" (None where the
     argument is).
     """

@@ -672,3 +672,31 @@ def test_outputs_that_are_inputs_are_refused():
     wide, want = bf(2, 20, 64), ssm.scan(u, dt, a_log, b, c)
     wide[..., :32] = u
     assert torch.equal(ssm.scan(wide[..., :32], dt, a_log, b, c, out=wide[..., 32:]), want)
+
+
+def test_norm_backward_takes_the_forward_calls_residual():
+    """`residual` may be what the forward call was given (or its in-place result), a truth value or None; what
+    has no truth value raises its own error, and rows that are not r's are refused."""
+    _, norm = _ops()
+    for res, scale in (("bf16", True), ("bf16", False), ("f32", False)):
+        t, dr, dh = _norm_inputs((2, 4, 6, 32, "bf16", 0, True, True, res, scale, True), seed=21)
+        d = {k: v.cuda() if v is not None else None for k, v in t.items()}
+        r, _ = norm.block_norm(**d)
+        back = dict(w_post=d["w_post"], gate=d["gate"], scale=d["scale"], w_pre=d["w_pre"], dh=dh.cuda())
+        ref = R.norm(**t, r_stored=r.cpu(), dr=dr, dh=dh)[2]
+        for residual in (d["residual"], r, True):
+            g = norm.block_norm_backward(dr.cuda(), d["o"], r, **back, residual=residual)
+            for k in ("o", "gate", "residual", "w_post", "scale", "w_pre"):
+                assert (g[k] is None) == (ref[k] is None), k
+                if g[k] is not None:
+                    R.check(g[k], ref[k], k)
+        with pytest.raises(ValueError):
+            norm.block_norm_backward(dr.cuda(), d["o"], r, **back, residual=d["residual"][:, :5])
+        with pytest.raises(TypeError):
+            norm.block_norm_backward(dr.cuda(), d["o"], r, **back, residual=d["residual"].double())
+
+    class Neither:
+        def __bool__(self):
+            raise KeyError("neither")
+    with pytest.raises(KeyError):
+        norm.block_norm_backward(dr.cuda(), d["o"], r, **back, residual=Neither())
