@@ -189,8 +189,12 @@ __device__ __forceinline__ f2 softplus2(f2 x)
 __device__ __forceinline__ float softplus(float x) { return unpack2(softplus2(pack2(x, 0.f))).x; }
 
 // A log2(e) of A = -exp(a_log), kept finite: the decay of a delta of zero (the tokens behind a sequence's
-// end) is one whatever the rate.
-__device__ __forceinline__ float decay_rate(float a_log) { return fmaxf(-expf(a_log) * LOG2E, -3e38f); }
+// end) is one whatever the rate.  Not fmaxf, which would turn a NaN into a rate.
+__device__ __forceinline__ float decay_rate(float a_log)
+{
+    const float r = -expf(a_log) * LOG2E;
+    return r < -3e38f ? -3e38f : r;
+}
 
 __device__ __forceinline__ int row_length(const int *lengths, int b, int N)
 {

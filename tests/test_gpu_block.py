@@ -700,3 +700,37 @@ def test_norm_backward_takes_the_forward_calls_residual():
             raise KeyError("neither")
     with pytest.raises(KeyError):
         norm.block_norm_backward(dr.cuda(), d["o"], r, **back, residual=Neither())
+
+
+@pytest.mark.parametrize("D", [16, 8208])
+def test_scan_of_a_rate_that_is_not_a_number(D):
+    """A NaN in a_log comes out as NaN in what it enters and nowhere else, on every path: over lanes of tokens and
+    in chunks, one token, and the backward pass with either spacing of checkpoints."""
+    ssm, _ = _ops()
+    t, dy, ds = _scan_inputs(2, 130, D, 16, 1, "f32", True, True, seed=22)
+    bad, at, state = torch.tensor([5]), 5, 3
+    others = torch.tensor([i for i in range(D) if i != at], device="cuda")
+
+    def run():
+        d, y, h, ck, _ = _run_scan(t, ckpt=True)
+        _, y2, _, _, _ = _run_scan(t)
+        g = ssm.scan_backward(dy.cuda(), d["u"], d["dt"], d["a_log"], d["b"], d["c"], ck, d["d_skip"], d["dt_bias"], d["z"],
+                              dstate_out=ds.cuda())
+        s = {k: d[k][:, 0] for k in ("u", "dt", "b", "c", "z")}
+        h1 = d["state"].clone()
+        y1 = ssm.scan_step(s["u"], s["dt"], d["a_log"], s["b"], s["c"], h1, d["d_skip"], d["dt_bias"], s["z"])
+        return y, y2, h, g, y1, h1
+    good = run()
+    t["a_log"][bad, state] = float("nan")
+    y, y2, h, g, y1, h1 = run()
+    for v, w in ((y, good[0]), (y2, good[1]), (y1, good[4])):
+        assert v[..., at].isnan().all()
+        assert torch.equal(v[..., others], w[..., others])
+    for v, w in ((h, good[2]), (h1, good[5])):
+        assert v[:, at, state].isnan().all()
+        assert torch.equal(v[:, others], w[:, others])
+    assert g["a_log"][at, state].isnan()
+    assert torch.equal(g["a_log"][others], good[3]["a_log"][others])
+    for k in ("u", "dt"):
+        assert g[k][..., at].isnan().all() and torch.equal(g[k][..., others], good[3][k][..., others]), k
+    assert g["state"][:, at, state].isnan().all() and torch.equal(g["state"][:, others], good[3]["state"][:, others])
