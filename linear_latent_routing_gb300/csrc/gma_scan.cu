@@ -319,8 +319,7 @@ template <typename T, class K, bool VEC> gma_status_t launch_forward(const gma_s
     a.tiles = (s.D / s.G + K::CH - 1) / K::CH;
     const size_t smem = ForwardSmem<K>::bytes(s.S);
     auto kern = scan_forward_kernel<T, K, VEC>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-        return GMA_ERR_CUDA;
+    if (!allow_smem(kern, smem, ForwardSmem<K>::bytes(MAX_S))) return GMA_ERR_CUDA;
     GMA_LAUNCH(KID_SCAN, st, kern<<<dim3(a.tiles * s.G, s.B), K::THREADS, smem, st>>>(a));
     return GMA_OK;
 }

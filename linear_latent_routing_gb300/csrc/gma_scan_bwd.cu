@@ -508,8 +508,7 @@ template <typename T, int S, int CK> gma_status_t launch_ck(const GradArgs<T> &g
     const bool z = g.f.z.p != nullptr;
     auto kern = vec ? (z ? scan_backward_kernel<T, S, CK, true, true> : scan_backward_kernel<T, S, CK, true, false>)
                     : (z ? scan_backward_kernel<T, S, CK, false, true> : scan_backward_kernel<T, S, CK, false, false>);
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<S, CK>)) != cudaSuccess)
-        return GMA_ERR_CUDA;
+    if (!allow_smem(kern, sizeof(Smem<S, CK>), sizeof(Smem<S, CK>))) return GMA_ERR_CUDA;
     GMA_LAUNCH(KID_SCAN_BWD, st,
                launch_pdl(kern, dim3(g.f.tiles * g.f.G, g.chunks, g.f.B), dim3(THREADS), sizeof(Smem<S, CK>), st, g));
     return GMA_OK;

@@ -30,6 +30,8 @@ constexpr int STAGES = 3;            // of a warp's ring of staged tokens
 template <typename T, int S> struct Stage { static constexpr int TOKENS = 1024 / (Lanes<S>::CH_WARP * (int)sizeof(T)); };
 constexpr int STAGE_BYTES = 3 * 1024;
 constexpr int RING_BYTES = STAGES * STAGE_BYTES;
+constexpr int MAX_WARPS = 8, MAX_ROWS = 4096;      // of a block; of a chunk's b or c, in values
+constexpr size_t MAX_SMEM = 2 * MAX_ROWS * sizeof(float) + MAX_WARPS * RING_BYTES;
 
 __device__ __forceinline__ void cp_async16(uint32_t to, const void *from)
 {
@@ -374,7 +376,7 @@ struct Blocks {
 };
 Blocks blocks_of(const gma_scan_t &s)
 {
-    const int warps = group_warps(s), tiles = (warps + 7) / 8;
+    const int warps = group_warps(s), tiles = (warps + MAX_WARPS - 1) / MAX_WARPS;
     return Blocks{tiles, (warps + tiles - 1) / tiles};
 }
 
@@ -387,7 +389,7 @@ int chunk_of(const gma_scan_t &s)
     const double rows = (double)s.B * s.G * blocks.tiles * blocks.warps / 8;
     int best = 32;
     double least = 0;
-    for (int c = 32; c <= 256 && c * s.S <= 4096 && !(s.checkpoints && c > scan_spacing(s)); c *= 2) {
+    for (int c = 32; c <= 256 && c * s.S <= MAX_ROWS && !(s.checkpoints && c > scan_spacing(s)); c *= 2) {
         const double waves = rows * ((s.N + c - 1) / c) / 304 + 0.5, cost = (waves > 1 ? waves : 1) * (c + 24);
         if (c == 32 || cost < least) best = c, least = cost;
     }
@@ -414,9 +416,7 @@ gma_status_t run_adjoint(const gma_scan_grad_t &grad, float *state, float *total
     g.s.tiles = blocks.tiles;
     const size_t smem = (size_t)g.chunk * S * sizeof(float) + (size_t)per * (VEC ? RING_BYTES : STAGE_BYTES);
     auto kern = scan_chunk_kernel<T, S, VEC, ADJOINT>;
-    if (smem > 48 * 1024 &&
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-        return GMA_ERR_CUDA;
+    if (!allow_smem(kern, smem, MAX_SMEM)) return GMA_ERR_CUDA;
     GMA_LAUNCH(KID_SCAN_ADJ, st, kern<<<dim3(g.s.tiles * s.G, g.chunks, s.B), per * 32, smem, st>>>(g, rows_vec(s.c, s.dtype)));
     GMA_LAUNCH(KID_SCAN_JOIN, st,
                launch_pdl(scan_chunk_join_kernel<T, S, true>, dim3((s.D * S + 127) / 128, s.B), dim3(128), 0, st, g));
@@ -438,9 +438,7 @@ template <typename T, int S, bool VEC> gma_status_t run(const gma_scan_t &s, cha
     const bool vec_bc = rows_vec(s.b, s.dtype) && rows_vec(s.c, s.dtype);
     const size_t rows = (size_t)g.chunk * S * sizeof(float), ring = (size_t)per * (VEC ? RING_BYTES : STAGE_BYTES);
     for (auto kern : {scan_chunk_kernel<T, S, VEC, STATE>, scan_chunk_kernel<T, S, VEC, OUTPUT>})
-        if (2 * rows + ring > 48 * 1024 &&
-            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(2 * rows + ring)) != cudaSuccess)
-            return GMA_ERR_CUDA;
+        if (!allow_smem(kern, 2 * rows + ring, MAX_SMEM)) return GMA_ERR_CUDA;
     if (g.chunks > 1) {
         GMA_LAUNCH(KID_SCAN_STATE, st, scan_chunk_kernel<T, S, VEC, STATE><<<grid, per * 32, rows + ring, st>>>(g, vec_bc));
         GMA_LAUNCH(KID_SCAN_JOIN, st,

@@ -142,6 +142,15 @@ template <typename T> inline ScanArgs<T> scan_args(const gma_scan_t &s)
     return a;
 }
 
+// Lets a kernel have the dynamic shared memory of a launch that wants `need` bytes (its static part is none).  The
+// limit belongs to the kernel and is set to `most`, what the largest of its launches takes, by every call that needs
+// more than the default: two host threads that each set their own call's would undo each other's.
+template <typename... P> inline bool allow_smem(void (*kern)(P...), size_t need, size_t most)
+{
+    return need <= 48 * 1024 || cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) == cudaSuccess;
+}
+constexpr int MAX_S = 64;
+
 // What every scan call needs; `out`: y is written.
 gma_status_t scan_check(const gma_scan_t *s, bool out);
 // 16-byte accesses to the rows of u, dt, z, b and c.

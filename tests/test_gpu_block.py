@@ -734,3 +734,41 @@ def test_scan_of_a_rate_that_is_not_a_number(D):
     for k in ("u", "dt"):
         assert g[k][..., at].isnan().all() and torch.equal(g[k][..., others], good[3][k][..., others]), k
     assert g["state"][:, at, state].isnan().all() and torch.equal(g["state"][:, others], good[3]["state"][:, others])
+
+
+def test_scan_calls_from_two_host_threads():
+    """Calls of one kernel with different amounts of shared memory from two host threads at once, on streams of their
+    own: each gets the launch that it asked for."""
+    import ctypes
+    import threading
+
+    from linear_latent_routing_gb300 import gma
+    from test_block_abi import SCAN, _layout
+    forward = gma.lib.gma_scan_forward
+    forward.argtypes, forward.restype = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p], ctypes.c_int
+
+    def job(B, N, D, S):
+        t = {k: torch.zeros(B, N, n, device="cuda") for k, n in (("u", D), ("dt", D), ("b", S), ("c", S), ("y", D))}
+        a_log = torch.zeros(D, S, device="cuda")
+        rows = {k: (v.data_ptr(), v.stride(0), v.stride(1)) for k, v in t.items()}
+        call = _layout(SCAN).pack(B, N, D, S, 1, 0, 0, 0, *rows["u"], *rows["dt"], 0, 0, 0, *rows["b"], *rows["c"], a_log.data_ptr(),
+                                  0, 0, 0, 0, 0, *rows["y"], 0)
+        return call, torch.cuda.Stream(), (t, a_log)
+    for shapes in (((1, 8, 8, 8), (1, 8, 8, 64)),                  # tokens over lanes: 8 and 64 states
+                   ((184, 32, 320, 16), (114, 32, 512, 16))):      # one chunk: blocks of five and of eight warps
+        jobs = [job(*s) for s in shapes]
+        torch.cuda.synchronize()
+        ready, results = threading.Barrier(2), [[], []]
+
+        def work(i):
+            call, stream, _ = jobs[i]
+            ready.wait()
+            for _ in range(2000):
+                results[i].append(forward(call, None, 0, stream.cuda_stream))
+        threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+        for th in threads:
+            th.start()
+        for th in threads:
+            th.join()
+        torch.cuda.synchronize()
+        assert [set(r) for r in results] == [{0}, {0}], shapes
