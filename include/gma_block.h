@@ -166,7 +166,7 @@ typedef struct {
     const float *w_post;          /* [D] or NULL                                             */
     const float *scale;           /* [D] or NULL (1)                                         */
     const float *w_pre;           /* [D] or NULL                                             */
-    gma_rows_t r, h;              /* [B][N][D] out; r may be residual; h required with w_pre */
+    gma_rows_t r, h;              /* [B][N][D] out; r may be residual (the same strides); h required with w_pre */
 } gma_norm_t;
 
 gma_status_t gma_norm_forward(const gma_norm_t *norm, gma_stream_t stream);
@@ -181,7 +181,7 @@ typedef struct {
     gma_rows_t d_o;               /* [B][H][N][d] in dtype, strides of batch rows and tokens */
     int64_t d_o_head;             /* stride between its heads                                */
     gma_rows_t dgate;             /* [B][N][D] in dtype, required with gate                  */
-    gma_rows_t dresidual;         /* [B][N][D] in residual_dtype, or NULL; may be dr         */
+    gma_rows_t dresidual;         /* [B][N][D] in residual_dtype, or NULL; may be dr (the same strides) */
     float *dw_post, *dscale, *dw_pre; /* [D], required with the parameter                    */
 } gma_norm_grad_t;
 

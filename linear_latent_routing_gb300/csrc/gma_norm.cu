@@ -477,6 +477,13 @@ Plan plan(int D)
     return p;
 }
 
+// An output in place of an input: each thread reads its piece of a row before it writes that piece, so their rows have
+// to be the same ones (a broadcast input's first row is also the others' input).
+bool same_rows(const gma_rows_t &out, const gma_rows_t &in, int B, int N)
+{
+    return out.ptr != in.ptr || ((B == 1 || out.batch == in.batch) && (N == 1 || out.token == in.token));
+}
+
 gma_status_t check(const gma_norm_t *n, bool forward)
 {
     if (!n) return GMA_ERR_INVALID_ARG;
@@ -497,6 +504,7 @@ gma_status_t check(const gma_norm_t *n, bool forward)
     if (forward) {
         if (n->residual.ptr && !rows_ok(n->residual, rd, n->B, n->N, D, false)) return GMA_ERR_INVALID_ARG;
         if (!rows_ok(n->r, rd, n->B, n->N, D, true)) return GMA_ERR_INVALID_ARG;
+        if (!same_rows(n->r, n->residual, n->B, n->N)) return GMA_ERR_INVALID_ARG;
         if (n->w_pre && !rows_ok(n->h, n->dtype, n->B, n->N, D, true)) return GMA_ERR_INVALID_ARG;
     }
     return GMA_OK;
@@ -618,6 +626,7 @@ gma_status_t gma_norm_backward(const gma_norm_grad_t *g, void *ws, size_t ws_byt
     if (!rows_ok(g->d_o, n.dtype, n.B, n.N, n.d, true) || (n.H > 1 && g->d_o_head < n.d)) return GMA_ERR_INVALID_ARG;
     if (n.gate.ptr && !rows_ok(g->dgate, n.dtype, n.B, n.N, D, true)) return GMA_ERR_INVALID_ARG;
     if (g->dresidual.ptr && !rows_ok(g->dresidual, rd, n.B, n.N, D, true)) return GMA_ERR_INVALID_ARG;
+    if (g->dresidual.ptr && !same_rows(g->dresidual, g->dr, n.B, n.N)) return GMA_ERR_INVALID_ARG;
     if ((n.w_post && !ptr_ok(g->dw_post, 4)) || (n.scale && !ptr_ok(g->dscale, 4)) ||
         (n.w_pre && !ptr_ok(g->dw_pre, 4)))
         return GMA_ERR_INVALID_ARG;

@@ -221,3 +221,16 @@ def test_bindings_refuse_cpu_tensors(lib):
         lib.ssm.conv(t, torch.zeros(8, 4))
     with pytest.raises(TypeError):
         lib.norm.block_norm(t, torch.ones(8))
+
+
+def test_norm_in_place_takes_the_same_rows_alone(lib):
+    """r in place of a residual with other strides (a broadcast one) would be read and written by different threads."""
+    import torch
+    for bad in (dict(residual=(FAKE, 0, 32)), dict(residual=(FAKE, 320, 0)), dict(r=(FAKE, 640, 32))):
+        assert lib.norm._norm_forward(_norm(lib, **bad), None) == 1
+    for bad in (dict(dres=(FAKE, 640, 64)), dict(dr=(FAKE, 0, 32))):
+        assert lib.norm._norm_backward(_norm(lib, True, **bad), FAKE, 1 << 30, None) == 1
+    if not torch.cuda.is_available():      # strides that no row uses do not count
+        assert lib.norm._norm_forward(_norm(lib, B=1, residual=(FAKE, 0, 32)), None) == 7
+        assert lib.norm._norm_forward(_norm(lib, N=1, r=(FAKE, 320, 7)), None) == 7
+        assert lib.norm._norm_backward(_norm(lib, True, B=1, dr=(FAKE, 0, 32)), FAKE, 1 << 30, None) == 7
