@@ -447,8 +447,11 @@ gma_status_t gma_conv_forward(const gma_conv_t *c, gma_stream_t stream)
     });
 }
 
-gma_status_t gma_conv_step(const gma_conv_t *c, gma_stream_t stream)
+gma_status_t gma_conv_step(const gma_conv_t *conv, gma_stream_t stream)
 {
+    if (!conv) return GMA_ERR_INVALID_ARG;
+    gma_conv_t one = *conv, *c = &one;       // its token strides are ignored
+    one.x.token = one.y.token = 0;
     gma_status_t r = check(c, true);
     if (r != GMA_OK) return r;
     if (c->N != 1 || !c->state_in || !c->state_out || c->lengths) return GMA_ERR_INVALID_ARG;

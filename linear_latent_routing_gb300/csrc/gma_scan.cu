@@ -369,8 +369,11 @@ gma_status_t gma_scan_forward(const gma_scan_t *s, void *ws, size_t ws_bytes, gm
     return vec ? forward_of<float, true>(*s, st) : forward_of<float, false>(*s, st);
 }
 
-gma_status_t gma_scan_step(const gma_scan_t *s, gma_stream_t stream)
+gma_status_t gma_scan_step(const gma_scan_t *scan, gma_stream_t stream)
 {
+    if (!scan) return GMA_ERR_INVALID_ARG;
+    gma_scan_t one = *scan, *s = &one;       // its token strides are ignored
+    one.u.token = one.dt.token = one.z.token = one.b.token = one.c.token = one.y.token = 0;
     gma_status_t r = scan_check(s, true);
     if (r != GMA_OK) return r;
     if (s->N != 1 || !s->state_in || !s->state_out || s->lengths || s->checkpoints) return GMA_ERR_INVALID_ARG;

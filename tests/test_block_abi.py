@@ -234,3 +234,14 @@ def test_norm_in_place_takes_the_same_rows_alone(lib):
         assert lib.norm._norm_forward(_norm(lib, B=1, residual=(FAKE, 0, 32)), None) == 7
         assert lib.norm._norm_forward(_norm(lib, N=1, r=(FAKE, 320, 7)), None) == 7
         assert lib.norm._norm_backward(_norm(lib, True, B=1, dr=(FAKE, 0, 32)), FAKE, 1 << 30, None) == 7
+
+
+def test_steps_ignore_token_strides(lib):
+    """Strides that the header says are ignored refuse nothing: a call that is otherwise valid gets as far as the device."""
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present")
+    odd = {k: (FAKE, 24, -5) for k in ("u", "dt", "z", "y")}
+    odd.update({k: (FAKE, 16, -7) for k in ("b", "c")})
+    assert lib.ssm._scan_step(_scan(lib, N=1, state_in=FAKE, state_out=FAKE, **odd), None) == 7
+    assert lib.ssm._conv_step(_conv(lib, N=1, state_in=FAKE, state_out=FAKE, x=(FAKE, 24, -1), y=(FAKE, 24, -1)), None) == 7
