@@ -73,7 +73,8 @@ typedef struct {
 } gma_scan_t;
 
 /* `checkpoints` is [B][ceil(N / t)][D][S], the state before every t-th token, with
- * t = gma_scan_checkpoint_tokens (64 or 16, by B, N, D and S); its bytes. */
+ * t = gma_scan_checkpoint_tokens (64 or 16, by B, N, D and S, the only fields that these two look at); its
+ * bytes.  Both are 0 for sizes that no call takes. */
 int gma_scan_checkpoint_tokens(const gma_scan_t *scan);
 size_t gma_scan_checkpoint_size(const gma_scan_t *scan);
 size_t gma_scan_workspace_size(const gma_scan_t *scan);

@@ -244,7 +244,9 @@ PyObject *scan_checkpoints(PyObject *, PyObject *const *a, Py_ssize_t n)
         if (u.size(0) > INT32_MAX || u.size(1) > INT32_MAX || u.size(2) > INT32_MAX || S > 64 || S < 1) value_error("sizes do not fit");
         gma_scan_t s = {};
         s.B = (int32_t)u.size(0); s.N = (int32_t)u.size(1); s.D = (int32_t)u.size(2); s.S = (int32_t)S;
-        return wrap(c.empty32({s.B, checkpoints_of(s), s.D, s.S}));
+        const int64_t kept = checkpoints_of(s);
+        if (!kept && s.B && s.N && s.D) value_error("sizes do not fit");
+        return wrap(c.empty32({s.B, kept, s.D, s.S}));
     });
 }
 

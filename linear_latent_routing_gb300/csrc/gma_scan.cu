@@ -16,14 +16,20 @@
 namespace gma {
 namespace blk {
 
+static gma_status_t scan_sizes(const gma_scan_t &s)
+{
+    if (s.B < 1 || s.N < 1 || s.D < 1 || s.S < 1) return GMA_ERR_INVALID_ARG;
+    const bool states = s.S == 8 || s.S == 16 || s.S == 32 || s.S == 64;
+    return !states || s.B > 65535 || s.D > (1 << 24) || s.N > (1 << 30) ? GMA_ERR_UNSUPPORTED_SHAPE : GMA_OK;
+}
+
 gma_status_t scan_check(const gma_scan_t *s, bool out)
 {
-    if (!s) return GMA_ERR_INVALID_ARG;
-    if (s->B < 1 || s->N < 1 || s->D < 1 || s->S < 1 || s->G < 1 || s->D % s->G) return GMA_ERR_INVALID_ARG;
+    if (!s || s->G < 1 || s->D < 1 || s->D % s->G) return GMA_ERR_INVALID_ARG;
     if (s->dtype != GMA_F32 && s->dtype != GMA_BF16) return GMA_ERR_INVALID_ARG;
     if (s->flags & ~GMA_ROWS_ZERO_TAIL || s->reserved) return GMA_ERR_INVALID_ARG;
-    if (!(s->S == 8 || s->S == 16 || s->S == 32 || s->S == 64)) return GMA_ERR_UNSUPPORTED_SHAPE;
-    if (s->B > 65535 || s->D > (1 << 24) || s->N > (1 << 30)) return GMA_ERR_UNSUPPORTED_SHAPE;
+    const gma_status_t sizes = scan_sizes(*s);
+    if (sizes != GMA_OK) return sizes;
     const int dt = s->dtype;
     const long long B = s->B, N = s->N, D = s->D, GS = (long long)s->G * s->S;
     if (!rows_ok(s->u, dt, B, N, D, false) || !rows_ok(s->dt, dt, B, N, D, false) ||
@@ -338,16 +344,12 @@ using namespace gma::blk;
 
 extern "C" {
 
+int gma_scan_checkpoint_tokens(const gma_scan_t *s) { return s && scan_sizes(*s) == GMA_OK ? scan_spacing(*s) : 0; }
+
 size_t gma_scan_checkpoint_size(const gma_scan_t *s)
 {
-    if (!s || s->B < 1 || s->N < 1 || s->D < 1 || s->S < 1) return 0;
-    const int spacing = scan_spacing(*s);
-    return (size_t)s->B * ((s->N + spacing - 1) / spacing) * s->D * s->S * sizeof(float);
-}
-
-int gma_scan_checkpoint_tokens(const gma_scan_t *s)
-{
-    return !s || s->B < 1 || s->N < 1 || s->D < 1 || s->S < 1 ? 0 : scan_spacing(*s);
+    const int spacing = gma_scan_checkpoint_tokens(s);
+    return spacing ? (size_t)s->B * ((s->N + spacing - 1) / spacing) * s->D * s->S * sizeof(float) : 0;
 }
 
 size_t gma_scan_workspace_size(const gma_scan_t *s)

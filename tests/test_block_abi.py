@@ -245,3 +245,19 @@ def test_steps_ignore_token_strides(lib):
     odd.update({k: (FAKE, 16, -7) for k in ("b", "c")})
     assert lib.ssm._scan_step(_scan(lib, N=1, state_in=FAKE, state_out=FAKE, **odd), None) == 7
     assert lib.ssm._conv_step(_conv(lib, N=1, state_in=FAKE, state_out=FAKE, x=(FAKE, 24, -1), y=(FAKE, 24, -1)), None) == 7
+
+
+def test_scan_checkpoint_sizes(lib):
+    """64 or 16 tokens, the buffer's bytes, and 0 where no call takes the sizes (2^31 - 1 tokens included)."""
+    from linear_latent_routing_gb300 import gma
+    tokens, size = gma.lib.gma_scan_checkpoint_tokens, gma.lib.gma_scan_checkpoint_size
+    for f, t in ((tokens, ctypes.c_int), (size, ctypes.c_size_t)):
+        f.argtypes, f.restype = [ctypes.c_void_p], t
+    for B, N, D, S, n in ((2, 301, 384, 8, 16), (4, 2048, 1024, 16, 64), (1, 1, 1, 64, 16), (1, 2 ** 30, 8, 8, 64), (65535, 65, 8, 32, 64)):
+        c = _scan(lib, B=B, N=N, D=D, S=S)
+        assert tokens(c) == n and size(c) == B * -(-N // n) * D * S * 4
+    for bad in (dict(N=2 ** 31 - 1), dict(N=2 ** 30 + 1), dict(S=12), dict(S=128), dict(B=0), dict(N=-1), dict(D=0), dict(B=65536),
+                dict(D=2 ** 24 + 1)):
+        c = _scan(lib, **bad)
+        assert tokens(c) == 0 and size(c) == 0, bad
+    assert tokens(None) == 0 and size(None) == 0

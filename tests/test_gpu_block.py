@@ -772,3 +772,12 @@ def test_scan_calls_from_two_host_threads():
             th.join()
         torch.cuda.synchronize()
         assert [set(r) for r in results] == [{0}, {0}], shapes
+
+
+def test_scan_checkpoints_of_sizes_that_no_call_takes():
+    ssm, _ = _ops()
+    u = torch.zeros(1, 1, 8, dtype=BF, device="cuda")
+    for tokens, S in ((10, 12), (10, 128), (2 ** 31 - 1, 16), (2 ** 30 + 1, 16)):
+        with pytest.raises(ValueError):
+            ssm.scan_checkpoints(u.expand(1, tokens, 8), S)
+    assert ssm.scan_checkpoints(u.expand(1, 33, 8), 64).shape == (1, 3, 8, 64)
