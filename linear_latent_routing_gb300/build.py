@@ -3,13 +3,16 @@ binding of ``include/gma_block.h`` (``csrc/block_binding.cpp``, against the inst
 
 Each translation unit compiles in parallel with nvcc (the binding with the host compiler), then one
 link step produces the shared library next to this file.  No CMake; a rebuild happens only when a
-source or header is newer than what it goes into.
+source or header is newer than what it goes into, or the binding was made for another torch.  Where no torch
+with CUDA is installed, libgma.so is built alone.
 """
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,6 +22,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgma.so")
 BINDING_SRC = os.path.join(CSRC, "block_binding.cpp")
 BINDING = os.path.join(PKG, "_block.so")
+BINDING_STAMP = os.path.join(BUILD, "block_binding.for")
 
 NVCC = os.environ.get("NVCC", "nvcc")
 CXX = os.environ.get("CXX", "g++")
@@ -53,17 +57,32 @@ def _compile(src, verbose_ptxas=False):
     return obj, p.stderr
 
 
-def _binding_stale():
+def _torch_dir():
+    """Where the installed torch lies, without importing it; None if there is none, or one without CUDA."""
+    spec = importlib.util.find_spec("torch")
+    where = os.path.dirname(spec.origin) if spec and spec.origin else ""
+    return where if os.path.exists(os.path.join(where, "lib", "libc10_cuda.so")) else None
+
+
+def _binding_for(torch_dir):
+    """What the binding's object code depends on beside the sources: this interpreter and that torch."""
+    with open(os.path.join(torch_dir, "version.py")) as f:
+        return "\n".join([sysconfig.get_config_var("EXT_SUFFIX"), torch_dir, f.read()])
+
+
+def _binding_stale(torch_dir):
     deps = [BINDING_SRC, os.path.abspath(__file__)] + glob.glob(os.path.join(INCLUDE, "*.h"))
-    return not os.path.exists(BINDING) or any(os.path.getmtime(p) > os.path.getmtime(BINDING) for p in deps)
+    if not os.path.exists(BINDING) or any(os.path.getmtime(p) > os.path.getmtime(BINDING) for p in deps):
+        return True
+    if not os.path.exists(BINDING_STAMP):
+        return True
+    with open(BINDING_STAMP) as f:
+        return f.read() != _binding_for(torch_dir)
 
 
-def _compile_binding():
+def _compile_binding(torch_dir):
     """The binding's object file; it is linked once libgma.so is there."""
-    import sysconfig
-
     import torch
-    torch_dir = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(shutil.which(NVCC) or "/usr/local/cuda/bin/nvcc")))
     includes = [INCLUDE, os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
                 sysconfig.get_paths()["include"], os.path.join(cuda, "include"), "/usr/local/cuda/include"]
@@ -75,31 +94,37 @@ def _compile_binding():
     p = subprocess.run(cmd + ["-c", BINDING_SRC, "-o", obj], capture_output=True, text=True)
     if p.returncode != 0:
         raise RuntimeError(f"{CXX} failed for {BINDING_SRC}:\n{p.stdout}\n{p.stderr}")
-    return obj, os.path.join(torch_dir, "lib")
+    return obj
 
 
-def _link_binding(obj, torch_lib):
+def _link_binding(obj, torch_dir):
     tmp = BINDING + f".tmp{os.getpid()}"
-    cmd = [CXX, "-shared", "-o", tmp, obj, "-L", PKG, "-l:libgma.so", "-Wl,-rpath,$ORIGIN", "-L", torch_lib, "-ltorch_python", "-ltorch",
-           "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    cmd = [CXX, "-shared", "-o", tmp, obj, "-L", PKG, "-l:libgma.so", "-Wl,-rpath,$ORIGIN", "-L", os.path.join(torch_dir, "lib"),
+           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
     p = subprocess.run(cmd, capture_output=True, text=True)
     if p.returncode != 0:
         raise RuntimeError(f"link failed:\n{p.stdout}\n{p.stderr}")
     os.replace(tmp, BINDING)
+    with open(BINDING_STAMP, "w") as f:
+        f.write(_binding_for(torch_dir))
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    """Compile and link libgma.so and its binding if needed; return the library's path."""
-    lib_stale, binding_stale = force or _stale(), force or _binding_stale()
+    """Compile and link libgma.so and, where torch is installed, its binding if needed; return the library's path.
+
+    Without torch the C ABI is all there is to use, and nvcc all that it needs.
+    """
+    torch_dir = _torch_dir()
+    lib_stale, binding_stale = force or _stale(), torch_dir is not None and (force or _binding_stale(torch_dir))
     if not lib_stale and not binding_stale:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=8) as ex:
-        binding = ex.submit(_compile_binding) if binding_stale else None
+        binding = ex.submit(_compile_binding, torch_dir) if binding_stale else None
         if lib_stale:
             _build_library(ex, verbose_ptxas)
         if binding:
-            _link_binding(*binding.result())
+            _link_binding(binding.result(), torch_dir)
     return LIB
 
 
