@@ -7,6 +7,7 @@
 #include <string>
 #include <vector>
 
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <ATen/ops/empty.h>
 #include <ATen/ops/zeros.h>
@@ -156,8 +157,8 @@ template <typename F> PyObject *guarded(Py_ssize_t have, Py_ssize_t want, F f)
     } catch (const Fail &e) {
         PyErr_SetString(e.type, e.words.c_str());
     } catch (const Raised &) {
-    } catch (const c10::OutOfMemoryError &e) {
-        PyErr_SetString(PyExc_MemoryError, e.what_without_backtrace());
+    } catch (const c10::OutOfMemoryError &) {
+        torch::translate_exception_to_python(std::current_exception());      // torch.OutOfMemoryError
     } catch (const std::exception &e) {
         PyErr_SetString(PyExc_RuntimeError, e.what());
     }

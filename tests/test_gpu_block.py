@@ -781,3 +781,11 @@ def test_scan_checkpoints_of_sizes_that_no_call_takes():
         with pytest.raises(ValueError):
             ssm.scan_checkpoints(u.expand(1, tokens, 8), S)
     assert ssm.scan_checkpoints(u.expand(1, 33, 8), 64).shape == (1, 3, 8, 64)
+
+
+def test_memory_that_is_not_there_raises_torchs_error():
+    """As every other call that allocates through torch does."""
+    ssm, _ = _ops()
+    u = torch.zeros(1, 1, 8, dtype=BF, device="cuda").expand(60000, 2 ** 20, 8)      # 2 TB of checkpoints
+    with pytest.raises(torch.OutOfMemoryError):
+        ssm.scan_checkpoints(u, 64)
