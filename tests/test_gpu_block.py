@@ -789,3 +789,153 @@ def test_memory_that_is_not_there_raises_torchs_error():
     u = torch.zeros(1, 1, 8, dtype=BF, device="cuda").expand(60000, 2 ** 20, 8)      # 2 TB of checkpoints
     with pytest.raises(torch.OutOfMemoryError):
         ssm.scan_checkpoints(u, 64)
+
+
+# ------------------------------------------------------------------ long chunks and runs
+#
+# Calls that fill the GPU with chunks of 128 and 256 tokens have 10^8 elements.  Channels do not meet in the scan's output
+# and state, nor in the convolution: a few distinct ones, repeated over the width, are compared with the
+# reference, and every repetition has to give the same bits.
+
+def _fake_rows(width, N):
+    return 1 << 20, N * width, width
+
+
+def _chunk_tokens(B, N, D, S, dtype):
+    """The chunk that the forward pass without checkpoints takes, by what its workspace holds: the states and one sum per
+    channel of each chunk."""
+    import ctypes
+
+    from linear_latent_routing_gb300 import gma
+    from test_block_abi import SCAN, _layout
+    size = gma.lib.gma_scan_workspace_size
+    size.argtypes, size.restype = [ctypes.c_void_p], ctypes.c_size_t
+    rows, pair = _fake_rows(D, N), _fake_rows(S, N)
+    got = size(_layout(SCAN).pack(B, N, D, S, 1, int(dtype == "bf16"), 0, 0, *rows, *rows, 0, 0, 0, *pair, *pair, 1 << 20, 0, 0, 0, 0, 0, *rows, 0))
+
+    def up(n):
+        return -(-n // 256) * 256
+    fits = [c for c in (32, 64, 128, 256) if up(B * -(-N // c) * D * S * 4) + up(B * -(-N // c) * D * 4) == got]
+    return fits[0] if len(fits) == 1 else None
+
+
+LONG_SCANS = [  # distinct channels, repetitions, S, dtype, z, chunk; 3 x 3000 tokens
+    (46, 256, 16, "bf16", True, 256),
+    (51, 231, 8, "f32", False, 256),          # an odd width: rows off every boundary
+    (16, 256, 16, "f32", True, 128),
+    (17, 241, 8, "bf16", False, 128),         # odd
+    (32, 128, 32, "bf16", True, 128),         # one channel a lane
+]
+
+
+@pytest.mark.parametrize("case", LONG_SCANS, ids=lambda c: "-".join(str(x) for x in c))
+def test_scan_forward_in_the_longest_chunks(case, monkeypatch):
+    """Lengths that end inside a chunk, on its edge and at the sequence's end."""
+    monkeypatch.setattr(R, "DEVICE", "cuda")
+    few, times, S, dtype, z, chunk = case
+    ssm, _ = _ops()
+    B, N, lengths, D = 3, 3000, [3000, 2817, 512], few * times
+    assert _chunk_tokens(B, N, D, S, dtype) == chunk
+    t, _, _ = _scan_inputs(B, N, few, S, 1, dtype, z, True, seed=31)
+    t["b"], t["c"] = t["b"].squeeze(2), t["c"].squeeze(2)
+    ry, rh = R.scan(**t, lengths=lengths)
+    d = {k: v.cuda() if v is not None else None for k, v in t.items()}
+    for k in ("u", "dt", "z"):
+        d[k] = d[k].repeat(1, 1, times) if d[k] is not None else None
+    d["a_log"], d["state"] = d["a_log"].repeat(times, 1), d["state"].repeat(1, times, 1)
+    d["d_skip"], d["dt_bias"] = d["d_skip"].repeat(times), d["dt_bias"].repeat(times)
+    h = torch.full((B, D, S), float("nan"), device="cuda")
+    y = ssm.scan(**d, state_out=h, lengths=torch.tensor(lengths, dtype=torch.int32, device="cuda"))
+    y, h = y.unflatten(2, (times, few)), h.unflatten(1, (times, few))
+    R.check(y[:, :, 0], ry, "y")
+    R.check(h[:, 0], rh, "state")
+    assert (y == y[:, :, :1]).all() and (h == h[:, :1]).all()
+
+
+def _run_tokens(B, N, D, W, dtype):
+    """The tokens of a thread's run in the convolution, by the rows of partial sums in its backward workspace: one for
+    every eight runs."""
+    import ctypes
+
+    from linear_latent_routing_gb300 import gma
+    from test_block_abi import CONV, _layout
+    size = gma.lib.gma_conv_backward_workspace_size
+    size.argtypes, size.restype = [ctypes.c_void_p], ctypes.c_size_t
+    rows = _fake_rows(D, N)
+    got = size(_layout(CONV + "RR2Q").pack(B, N, D, W, int(dtype == "bf16"), 0, *rows, 1 << 20, 1 << 20, 0, 0, 0, *rows, *rows, *rows, 1 << 20, 1 << 20))
+    fits = [r for r in (8, 16, 32, 64, 128, 256) if -(-B * -(-(-(-N // r)) // 8) * (W + 1) * (-(-D // 4) * 4) * 4 // 256) * 256 == got]
+    return fits[0] if len(fits) == 1 else None
+
+
+LONG_CONVS = [  # distinct channels, repetitions, W, dtype, tokens, lengths, run
+    (24, 342, 4, "bf16", 7500, [7500, 5000], 256),
+    (139, 59, 3, "f32", 7500, None, 256),              # an odd width
+    (24, 342, 2, "f32", 4000, [4000, 2561], 128),
+    (139, 59, 4, "bf16", 4000, [3968, 129], 128),       # odd
+]
+
+
+@pytest.mark.parametrize("case", LONG_CONVS, ids=lambda c: "-".join(str(x) for x in c[:5]))
+def test_conv_in_the_longest_runs(case, monkeypatch):
+    monkeypatch.setattr(R, "DEVICE", "cuda")
+    few, times, W, dtype, N, lengths, run = case
+    ssm, _ = _ops()
+    B, D, r, T = 2, few * times, _draw(32), TYPES[dtype]
+    assert _run_tokens(B, N, D, W, dtype) == run
+    t = {"x": r(B, N, few, dtype=T), "weight": r(few, W, std=0.6), "bias": r(few), "state": r(B, W - 1, few, dtype=T)}
+    dy = r(B, N, few, dtype=T)
+    ry, after, ref = R.conv(**t, lengths=lengths, dy=dy)
+    d = {k: v.cuda().repeat(1, 1, times) for k, v in (("x", t["x"]), ("state", t["state"]), ("dy", dy))}
+    w, b = t["weight"].cuda().repeat(times, 1), t["bias"].cuda().repeat(times)
+    ln = torch.tensor(lengths, dtype=torch.int32, device="cuda") if lengths is not None else None
+    so = torch.full((B, W - 1, D), float("nan"), dtype=T, device="cuda")
+    y = ssm.conv(d["x"], w, b, state=d["state"], state_out=so, lengths=ln)
+    g = ssm.conv_backward(d["dy"], d["x"], w, b, state=d["state"], lengths=ln)
+    assert torch.equal(so[..., :few].double(), after) and torch.equal(so, so[..., :few].repeat(1, 1, times))
+    for got, want, name in ((y, ry, "y"), (g["x"], ref["x"], "x")):
+        R.check(got[..., :few], want, name)
+        assert torch.equal(got, got[..., :few].repeat(1, 1, times)), name
+    for name in ("weight", "bias"):
+        R.check(g[name][:few], ref[name], name)
+        assert torch.equal(g[name], g[name][:few].repeat(*((times, 1) if name == "weight" else (times,)))), name
+
+
+def test_scan_backward_into_some_of_the_callers_rows():
+    """With lengths and a part of `out`: the caller's rows behind a sequence's end are left alone, the other gradients are
+    zero there, and every one has the bits that it has without `out`."""
+    ssm, _ = _ops()
+    for D, lengths in ((24, [0, 7, 130]), (8200, [129, 0, 64])):
+        t, dy, ds = _scan_inputs(3, 140, D, 16, 1, "bf16", seed=33)
+        d, _, _, ck, ln = _run_scan(t, lengths, ckpt=True)
+        args = (dy.cuda(), d["u"], d["dt"], d["a_log"], d["b"], d["c"], ck, d["d_skip"], d["dt_bias"], d["z"])
+        want = ssm.scan_backward(*args, dstate_out=ds.cuda(), lengths=ln)
+        for names in (("u",), ("dt", "b"), ("z", "c")):
+            wide = {k: torch.full((*t[k].shape[:2], t[k][0, 0].numel() + 8), 5.0, dtype=BF, device="cuda") for k in names}
+            mine = {k: (wide[k][..., 8:].unflatten(2, t[k].shape[2:]) if k in "bc" else wide[k][..., 8:]) for k in names}
+            torch.full((5, 3, 140, D), float("nan"), dtype=BF, device="cuda")          # what a new buffer may hold
+            g = ssm.scan_backward(*args, dstate_out=ds.cuda(), lengths=ln, out=mine)
+            for k in g:
+                if k not in names:
+                    assert torch.equal(g[k], want[k]), k
+                    continue
+                assert g[k] is mine[k] and (wide[k][..., :8] == 5.0).all(), k
+                for i, n in enumerate(lengths):
+                    assert torch.equal(g[k][i, :n], want[k][i, :n]) and (g[k][i, n:] == 5.0).all(), k
+
+
+@pytest.mark.parametrize("d", [32, 10])
+def test_norm_backward_into_strided_rows(d):
+    """`out` as heads of token-major rows with a gap beside them: the bits of a contiguous one, the gap left alone."""
+    _, norm = _ops()
+    B, H, N = 2, 4, 6
+    t, dr, dh = _norm_inputs((B, H, N, d, "bf16", 0, True, True, "f32", True, True), seed=34)
+    c = {k: v.cuda() if v is not None else None for k, v in t.items()}
+    r, _ = norm.block_norm(**c)
+    args = dict(w_post=c["w_post"], gate=c["gate"], scale=c["scale"], w_pre=c["w_pre"], dh=dh.cuda())
+    want = norm.block_norm_backward(dr.cuda(), c["o"], r, **args)
+    wide = torch.full((B, N, H * d + 8), 5.0, dtype=BF, device="cuda")
+    out = wide[..., 8:].unflatten(2, (H, d)).transpose(1, 2)
+    g = norm.block_norm_backward(dr.cuda(), c["o"], r, **args, out=out)
+    assert g["o"] is out and (wide[..., :8] == 5.0).all()
+    for k in want:
+        assert torch.equal(g[k], want[k]), k
