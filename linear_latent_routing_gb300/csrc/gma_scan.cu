@@ -11,7 +11,7 @@
 // (33.5 MB), one row of 1024 channels in the time of a launch.
 #include <type_traits>
 
-#include "scan_tile.cuh"
+#include "scan_args.cuh"
 
 namespace gma {
 namespace blk {
@@ -58,33 +58,128 @@ bool scan_vec(const gma_scan_t &s)
 
 namespace {
 
-template <class K> struct ForwardSmem {
+// ------------------------------------------------------------------ tokens over lanes
+// A block takes CH channels of one group in one batch row, a warp each, and walks over the sequence in tiles of
+// TT tokens.  A warp's lanes are time lanes, each of which owns TL neighbouring tokens: the recurrence is
+// sequential over a lane's own tokens, with a scan of (decay, state) pairs over the lanes in between, so that a
+// tile's exponentials are computed once and every warp has 32 lanes of independent work whatever the number of
+// channels.  States n and n + 1 share packed fp32 pairs.
+//
+// Tiles lie in shared memory in the order the lanes read them, 16 bytes a lane without bank conflicts:
+// token t = tl * TL + 4 q + e of a channel at (q * LT + tl) * 4 + e, and of a pair of states (2 q + e)
+// at (q * LT + tl) * 2 + e.
+constexpr int LT = 32, TL = 8, CH = 8;                      // time lanes, tokens of a lane, channels (one a warp)
+constexpr int TT = LT * TL, THREADS = LT * CH;
+static_assert(THREADS == TT && CH == 8, "a thread stages eight channels of one token");
+constexpr int PITCH = TT + 4;                               // floats between two channels
+__device__ __forceinline__ int pos(int t)
+{
+    const int tl = t / TL, i = t % TL;
+    return ((i / 4) * LT + tl) * 4 + i % 4;
+}
+__device__ __forceinline__ int pos2(int t)
+{
+    const int tl = t / TL, i = t % TL;
+    return ((i / 2) * LT + tl) * 2 + i % 2;
+}
+
+// One lane's TL values of a channel.
+__device__ __forceinline__ void lane_load(const float *chan, int tl, float (&v)[TL])
+{
+#pragma unroll
+    for (int q = 0; q < TL / 4; ++q) {
+        const float4 x = *reinterpret_cast<const float4 *>(chan + (q * LT + tl) * 4);
+        v[4 * q] = x.x; v[4 * q + 1] = x.y; v[4 * q + 2] = x.z; v[4 * q + 3] = x.w;
+    }
+}
+__device__ __forceinline__ void lane_store(float *chan, int tl, const float (&v)[TL])
+{
+#pragma unroll
+    for (int q = 0; q < TL / 4; ++q)
+        *reinterpret_cast<float4 *>(chan + (q * LT + tl) * 4) =
+            make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+}
+
+// One lane's TL values of a pair of states: two tokens of pair p.
+__device__ __forceinline__ void pair_load(const f2 *tile, int p, int tl, int q, f2 &v0, f2 &v1)
+{
+    const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(tile + p * TT + (q * LT + tl) * 2);
+    v0 = x.x; v1 = x.y;
+}
+
+// Stages tokens t0 .. t0 + TT - 1 of b or c (S values a token) as pairs; zeros behind the last token.
+template <typename T, bool VEC>
+__device__ __forceinline__ void stage_pairs(const Rows<const T> &r, int b, int first, int t0, int len, int S, f2 *tile)
+{
+    const int pieces = S / 8;
+    for (int i = threadIdx.x; i < TT * pieces; i += THREADS) {
+        const int t = i % TT, piece = i / TT;
+        float v[8];
+        if (t0 + t < len) {
+            load8<VEC>(r.at(b, t0 + t) + first + piece * 8, 8, v);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = 0.f;
+        }
+        const int at = pos2(t);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tile[(piece * 4 + k) * TT + at] = pack2(v[2 * k], v[2 * k + 1]);
+    }
+}
+
+// One step of a scan over the time lanes: takes (decay, state) of the lane `OFF` before, and where there is one,
+// state += decay s and decay *= d.  The shuffle's own predicate tells.
+template <int OFF> __device__ __forceinline__ void scan_step(f2 &decay, f2 &state)
+{
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b32 a, b, c, e;\n\t.reg .b64 d, s;\n\t"
+                 "mov.b64 {a, b}, %1;\n\tmov.b64 {c, e}, %0;\n\t"
+                 "shfl.sync.up.b32 a|p, a, %2, 0, 0xffffffff;\n\t"
+                 "shfl.sync.up.b32 b, b, %2, 0, 0xffffffff;\n\t"
+                 "shfl.sync.up.b32 c, c, %2, 0, 0xffffffff;\n\t"
+                 "shfl.sync.up.b32 e, e, %2, 0, 0xffffffff;\n\t"
+                 "mov.b64 d, {a, b};\n\tmov.b64 s, {c, e};\n\t"
+                 "@p fma.rn.f32x2 %0, %1, s, %0;\n\t@p mul.rn.f32x2 %1, %1, d;\n\t}"
+                 : "+l"(state), "+l"(decay)
+                 : "n"(OFF));
+}
+
+// Inclusive scan over the time lanes.
+__device__ __forceinline__ void scan_lanes(f2 &decay, f2 &state)
+{
+    scan_step<1>(decay, state);
+    scan_step<2>(decay, state);
+    scan_step<4>(decay, state);
+    scan_step<8>(decay, state);
+    scan_step<16>(decay, state);
+}
+
+struct ForwardSmem {
     static constexpr int U = 0;                                         // u, then p
-    static constexpr int DT = U + K::CHANNEL_FLOATS * 4;
-    static constexpr int PAIRS = (DT + K::CHANNEL_FLOATS * 4 + 15) / 16 * 16;
-    static size_t bytes(int S) { return PAIRS + (size_t)S * K::TT * 8 + (size_t)2 * K::CH * S * 4; }
+    static constexpr int DT = U + CH * PITCH * 4;
+    static constexpr int PAIRS = DT + CH * PITCH * 4;
+    static_assert(PITCH % 4 == 0, "16-byte pieces");
+    static size_t bytes(int S) { return PAIRS + (size_t)S * TT * 8 + (size_t)2 * CH * S * 4; }
 };
 
-template <typename T, class K, bool VEC>
-__global__ void __launch_bounds__(K::THREADS) scan_forward_kernel(const ScanArgs<T> a)
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(THREADS) scan_forward_kernel(const ScanArgs<T> a)
 {
     extern __shared__ __align__(16) unsigned char smem[];
-    float *us = reinterpret_cast<float *>(smem + ForwardSmem<K>::U);
-    float *dts = reinterpret_cast<float *>(smem + ForwardSmem<K>::DT);
-    f2 *bs = reinterpret_cast<f2 *>(smem + ForwardSmem<K>::PAIRS);
-    f2 *cs = bs + a.S / 2 * K::TT;
-    float *rate = reinterpret_cast<float *>(cs + a.S / 2 * K::TT);   // A log2(e), [CH][S]
-    float *hs = rate + K::CH * a.S;                                   // the state before the tile, [CH][S]
+    float *us = reinterpret_cast<float *>(smem + ForwardSmem::U);
+    float *dts = reinterpret_cast<float *>(smem + ForwardSmem::DT);
+    f2 *bs = reinterpret_cast<f2 *>(smem + ForwardSmem::PAIRS);
+    f2 *cs = bs + a.S / 2 * TT;
+    float *rate = reinterpret_cast<float *>(cs + a.S / 2 * TT);   // A log2(e), [CH][S]
+    float *hs = rate + CH * a.S;                                   // the state before the tile, [CH][S]
 
     const int b = blockIdx.y, group = blockIdx.x / a.tiles, Dg = a.D / a.G;
-    const int in_group = (blockIdx.x - group * a.tiles) * K::CH;
-    const int c0 = group * Dg + in_group, nch = min(K::CH, Dg - in_group);
+    const int in_group = (blockIdx.x - group * a.tiles) * CH;
+    const int c0 = group * Dg + in_group, nch = min(CH, Dg - in_group);
     const int len = row_length(a.lengths, b, a.N);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int tl = lane % K::LT, ch = warp * K::CPW + lane / K::LT;
+    const int ch = threadIdx.x / LT, tl = threadIdx.x % LT;
     const int nck = (a.N + a.spacing - 1) / a.spacing;
 
-    for (int i = threadIdx.x; i < K::CH * a.S; i += K::THREADS) {
+    for (int i = threadIdx.x; i < CH * a.S; i += THREADS) {
         const int k = i / a.S;
         const long long at = (long long)(c0 + k) * a.S + i % a.S;
         rate[i] = k < nch ? decay_rate(a.a_log[at]) : 0.f;
@@ -92,108 +187,95 @@ __global__ void __launch_bounds__(K::THREADS) scan_forward_kernel(const ScanArgs
     }
     const float skip = a.d_skip && ch < nch ? a.d_skip[c0 + ch] : 0.f;
 
-    // A thread stages the same eight channels of UNITS tokens of every tile, and loads the next tile's
-    // while it works on this one.
-    constexpr int UNITS = K::TL / 8, STEP = K::TT / UNITS;
-    const int piece = threadIdx.x % (K::CH / 8), token = threadIdx.x / (K::CH / 8);
-    const int n8 = min(8, nch - piece * 8), cp = c0 + piece * 8;
-    float bias[8];
+    // A thread stages the block's channels of one token of every tile, and loads the next tile's while it works on this one.
+    const int token = threadIdx.x;
+    float bias[CH];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) bias[k] = a.dt_bias && k < n8 ? a.dt_bias[cp + k] : 0.f;
-    Raw8<T> ur[UNITS], dr[UNITS], zr[UNITS];
+    for (int k = 0; k < CH; ++k) bias[k] = a.dt_bias && k < nch ? a.dt_bias[c0 + k] : 0.f;
+    Raw8<T> ur, dr, zr;
     auto fetch = [&](int t0) {
-#pragma unroll
-        for (int j = 0; j < UNITS; ++j) {
-            ur[j].zero();
-            dr[j].zero();
-            const int t = t0 + token + j * STEP;
-            if (VEC && t < len && n8 > 0) {
-                ur[j].load(a.u.at(b, t) + cp);
-                dr[j].load(a.dt.at(b, t) + cp);
-            }
+        ur.zero();
+        dr.zero();
+        if (VEC && t0 + token < len) {
+            ur.load(a.u.at(b, t0 + token) + c0);
+            dr.load(a.dt.at(b, t0 + token) + c0);
         }
     };
     fetch(0);
 
-    for (int t0 = 0; t0 < len; t0 += K::TT) {
+    for (int t0 = 0; t0 < len; t0 += TT) {
+        const int t = t0 + token, at = pos(token);
+        const bool on = t < len;
         __syncthreads();
         // u and delta of the tile, transposed; zeros behind the last token leave the state alone
-#pragma unroll
-        for (int j = 0; j < UNITS; ++j) {
-            const int t = token + j * STEP;
-            const bool on = t0 + t < len && n8 > 0;
-            float u[8], d[8];
+        {
+            float u[CH], d[CH];
             if (VEC) {
-                ur[j].get(u);
-                dr[j].get(d);
+                ur.get(u);
+                dr.get(d);
             } else {
-                load8<false>(a.u.at(b, t0 + t) + cp, on ? n8 : 0, u);
-                load8<false>(a.dt.at(b, t0 + t) + cp, on ? n8 : 0, d);
+                load8<false>(a.u.at(b, t) + c0, on ? nch : 0, u);
+                load8<false>(a.dt.at(b, t) + c0, on ? nch : 0, d);
             }
-            const int at = K::pos(t);
 #pragma unroll
-            for (int k = 0; k < 8; k += 2) {
+            for (int k = 0; k < CH; k += 2) {
                 const float2 s = unpack2(softplus2(add2(pack2(d[k], d[k + 1]), pack2(bias[k], bias[k + 1]))));
-                us[K::channel(piece * 8 + k) + at] = u[k];
-                us[K::channel(piece * 8 + k + 1) + at] = u[k + 1];
-                dts[K::channel(piece * 8 + k) + at] = on && k < n8 ? s.x : 0.f;
-                dts[K::channel(piece * 8 + k + 1) + at] = on && k + 1 < n8 ? s.y : 0.f;
+                us[k * PITCH + at] = u[k];
+                us[(k + 1) * PITCH + at] = u[k + 1];
+                dts[k * PITCH + at] = on && k < nch ? s.x : 0.f;
+                dts[(k + 1) * PITCH + at] = on && k + 1 < nch ? s.y : 0.f;
             }
         }
-        stage_pairs<K, T, VEC>(a.b, b, group * a.S, t0, len, a.S, bs);
-        stage_pairs<K, T, VEC>(a.c, b, group * a.S, t0, len, a.S, cs);
+        stage_pairs<T, VEC>(a.b, b, group * a.S, t0, len, a.S, bs);
+        stage_pairs<T, VEC>(a.c, b, group * a.S, t0, len, a.S, cs);
         __syncthreads();
-        fetch(t0 + K::TT);
-#pragma unroll
-        for (int j = 0; j < UNITS; ++j) {
-            zr[j].zero();
-            const int t = t0 + token + j * STEP;
-            if (VEC && a.z.p && t < len && n8 > 0) zr[j].load(a.z.at(b, t) + cp);
-        }
+        fetch(t0 + TT);
+        zr.zero();
+        if (VEC && a.z.p && on) zr.load(a.z.at(b, t) + c0);
 
         {
-            float dt[K::TL], u[K::TL];
-            lane_load<K>(dts + K::channel(ch), tl, dt);
-            lane_load<K>(us + K::channel(ch), tl, u);
-            f2 dt2[K::TL], xu2[K::TL], y2[K::TL];
+            float dt[TL], u[TL];
+            lane_load(dts + ch * PITCH, tl, dt);
+            lane_load(us + ch * PITCH, tl, u);
+            f2 dt2[TL], xu2[TL], y2[TL];
             float total = 0.f;
 #pragma unroll
-            for (int i = 0; i < K::TL; ++i) {
+            for (int i = 0; i < TL; ++i) {
                 total += dt[i];
                 dt2[i] = pack2(dt[i], dt[i]);
                 xu2[i] = pack2(dt[i] * u[i], dt[i] * u[i]);
                 y2[i] = pack2(skip * u[i], 0.f);
             }
             const f2 total2 = pack2(total, total);
-            const int start = t0 + tl * K::TL;
+            const int start = t0 + tl * TL;
             const bool keep = a.ckpt && start % a.spacing == 0 && start < len && ch < nch;
             float *ck = keep ? a.ckpt + (((long long)b * nck + start / a.spacing) * a.D + c0 + ch) * a.S : nullptr;
             for (int p = 0; p < a.S / 2; ++p) {
                 const f2 r2 = *reinterpret_cast<const f2 *>(rate + ch * a.S + 2 * p);
                 f2 *h0 = reinterpret_cast<f2 *>(hs + ch * a.S + 2 * p);
-                f2 a2[K::TL], x2[K::TL], h = 0ull;
+                f2 a2[TL], x2[TL], h = 0ull;
 #pragma unroll
-                for (int q = 0; q < K::TL / 2; ++q) pair_load<K>(bs, p, tl, q, x2[2 * q], x2[2 * q + 1]);
+                for (int q = 0; q < TL / 2; ++q) pair_load(bs, p, tl, q, x2[2 * q], x2[2 * q + 1]);
 #pragma unroll
-                for (int i = 0; i < K::TL; ++i) {
+                for (int i = 0; i < TL; ++i) {
                     a2[i] = ex2_2(mul2(dt2[i], r2));
                     x2[i] = mul2(x2[i], xu2[i]);
                     h = fma2(a2[i], h, x2[i]);
                 }
                 f2 decay = ex2_2(mul2(total2, r2));
-                scan_lanes<K::LT, true>(decay, h);
+                scan_lanes(decay, h);
                 const f2 before = *h0;
-                const f2 d1 = __shfl_up_sync(0xffffffffu, decay, 1, K::LT);
-                const f2 s1 = __shfl_up_sync(0xffffffffu, h, 1, K::LT);
+                const f2 d1 = __shfl_up_sync(0xffffffffu, decay, 1, LT);
+                const f2 s1 = __shfl_up_sync(0xffffffffu, h, 1, LT);
                 const f2 end = fma2(decay, before, h);
                 h = tl ? fma2(d1, before, s1) : before;
                 __syncwarp();                  // every lane has read h0
-                if (tl == K::LT - 1) *h0 = end;
+                if (tl == LT - 1) *h0 = end;
                 if (keep) *reinterpret_cast<f2 *>(ck + 2 * p) = h;
 #pragma unroll
-                for (int q = 0; q < K::TL / 2; ++q) {
+                for (int q = 0; q < TL / 2; ++q) {
                     f2 c2[2];
-                    pair_load<K>(cs, p, tl, q, c2[0], c2[1]);
+                    pair_load(cs, p, tl, q, c2[0], c2[1]);
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         h = fma2(a2[2 * q + e], h, x2[2 * q + e]);
@@ -202,38 +284,35 @@ __global__ void __launch_bounds__(K::THREADS) scan_forward_kernel(const ScanArgs
                 }
             }
 #pragma unroll
-            for (int i = 0; i < K::TL; ++i) {
+            for (int i = 0; i < TL; ++i) {
                 const float2 y = unpack2(y2[i]);
                 u[i] = y.x + y.y;
             }
-            lane_store<K>(us + K::channel(ch), tl, u);
+            lane_store(us + ch * PITCH, tl, u);
         }
         __syncthreads();
+        if (on) {
+            float y[CH];
 #pragma unroll
-        for (int j = 0; j < UNITS; ++j) {
-            const int t = token + j * STEP, at = K::pos(t);
-            if (t0 + t >= len || n8 <= 0) continue;
-            float y[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) y[k] = us[K::channel(piece * 8 + k) + at];
+            for (int k = 0; k < CH; ++k) y[k] = us[k * PITCH + at];
             if (a.z.p) {
-                float z[8];
-                if (VEC) zr[j].get(z);
-                else load8<false>(a.z.at(b, t0 + t) + cp, n8, z);
+                float z[CH];
+                if (VEC) zr.get(z);
+                else load8<false>(a.z.at(b, t) + c0, nch, z);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) y[k] *= silu(z[k]);
+                for (int k = 0; k < CH; ++k) y[k] *= silu(z[k]);
             }
-            store8<VEC>(a.y.at(b, t0 + t) + cp, n8, y);
+            store8<VEC>(a.y.at(b, t) + c0, nch, y);
         }
     }
     __syncthreads();
-    if (a.zero && n8 > 0)
-        for (int t = len + token; t < a.N; t += STEP) {
-            const float none[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            store8<VEC>(a.y.at(b, t) + cp, n8, none);
+    if (a.zero)
+        for (int t = len + token; t < a.N; t += THREADS) {
+            const float none[CH] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            store8<VEC>(a.y.at(b, t) + c0, nch, none);
         }
     if (a.state_out)
-        for (int i = threadIdx.x; i < nch * a.S; i += K::THREADS)
+        for (int i = threadIdx.x; i < nch * a.S; i += THREADS)
             a.state_out[((long long)b * a.D + c0) * a.S + i] = hs[i];
 }
 
@@ -319,20 +398,15 @@ __global__ void __launch_bounds__(256, STEP_BLOCKS) scan_step_kernel(const ScanA
     }
 }
 
-template <typename T, class K, bool VEC> gma_status_t launch_forward(const gma_scan_t &s, cudaStream_t st)
-{
-    ScanArgs<T> a = scan_args<T>(s);
-    a.tiles = (s.D / s.G + K::CH - 1) / K::CH;
-    const size_t smem = ForwardSmem<K>::bytes(s.S);
-    auto kern = scan_forward_kernel<T, K, VEC>;
-    if (!allow_smem(kern, smem, ForwardSmem<K>::bytes(MAX_S))) return GMA_ERR_CUDA;
-    GMA_LAUNCH(KID_SCAN, st, kern<<<dim3(a.tiles * s.G, s.B), K::THREADS, smem, st>>>(a));
-    return GMA_OK;
-}
-
 template <typename T, bool VEC> gma_status_t forward_of(const gma_scan_t &s, cudaStream_t st)
 {
-    return launch_forward<T, Tile<32, 8, 8>, VEC>(s, st);
+    ScanArgs<T> a = scan_args<T>(s);
+    a.tiles = (s.D / s.G + CH - 1) / CH;
+    const size_t smem = ForwardSmem::bytes(s.S);
+    auto kern = scan_forward_kernel<T, VEC>;
+    if (!allow_smem(kern, smem, ForwardSmem::bytes(MAX_S))) return GMA_ERR_CUDA;
+    GMA_LAUNCH(KID_SCAN, st, kern<<<dim3(a.tiles * s.G, s.B), THREADS, smem, st>>>(a));
+    return GMA_OK;
 }
 
 }  // namespace

@@ -19,7 +19,7 @@
 // shared-memory pipe binds it (76 % busy: 78 wavefronts a token of a warp, 32 of them the column sums').  Two channels
 // of four states a lane halve those, but stage every value twice and spill: 224 us.  Tokens over lanes, as in
 // gma_scan.cu, took 303 us.
-#include "scan_tile.cuh"
+#include "scan_args.cuh"
 
 namespace gma {
 namespace blk {

@@ -1,4 +1,4 @@
-// gma_scan_chunk.cu -- the selective scan's forward pass in chunks of tokens, for states of up to 16.
+// gma_scan_chunk.cu -- the selective scan's forward pass in chunks of tokens, and the adjoint behind every chunk of the backward pass.
 //
 // Lanes are channels, every warp walks over the tokens of one chunk with its states in registers, and
 // nothing but y is exchanged between lanes: a lane holds 32 states, of two channels (S <= 16, whose u, dt, z
@@ -12,7 +12,7 @@
 // (of 32 a clock and SM) and three and a half packed fp32 instructions; instruction issue binds.
 // Measured: 65536 tokens of 2048 channels x 16 states, bf16 with a gate: 354 us, 31 us and 504 us (69 and 99
 // instructions an element, 62 % of the issue slots used); 4 x 2048 x 1024: 37, 10 and 47 us.
-#include "scan_tile.cuh"
+#include "scan_args.cuh"
 
 namespace gma {
 namespace blk {
