@@ -939,3 +939,37 @@ def test_norm_backward_into_strided_rows(d):
     assert g["o"] is out and (wide[..., :8] == 5.0).all()
     for k in want:
         assert torch.equal(g[k], want[k]), k
+
+
+def test_strides_beyond_32_bits_on_every_path():
+    """Batch rows more than 2^31 elements apart give the bits of neighbouring ones: the scan in chunks, its backward
+    pass, the convolution and the norms, inputs and outputs."""
+    ssm, norm = _ops()
+    N, D = 300, 4096
+    gap = 2 ** 31 + 64
+    store = [torch.empty(gap + N * D, dtype=BF, device="cuda") for _ in range(2)]
+
+    def far(i, t=None):
+        v = store[i].as_strided((2, N, D), (gap, D, 1))
+        return v if t is None else v.copy_(t)
+    t, dy, _ = _scan_inputs(2, N, D, 16, 1, "bf16", True, False, seed=41)
+    d, y, _, ck, _ = _run_scan(t, ckpt=True)
+    rest = (d["dt"], d["a_log"], d["b"], d["c"])
+    more = (d["d_skip"], d["dt_bias"], d["z"])
+    assert torch.equal(ssm.scan(far(0, d["u"]), *rest, *more, out=far(1)), y)
+    g = ssm.scan_backward(dy.cuda(), d["u"], *rest, ck, *more)
+    f = ssm.scan_backward(dy.cuda(), far(0), *rest, ck, *more, out={"u": far(1)})
+    for k in g:
+        assert (g[k] is None and f[k] is None) or torch.equal(g[k], f[k]), k
+    r = _draw(42)
+    w, b, wn = r(D, 4).cuda(), r(D).cuda(), (1 + r(D, std=0.3)).cuda()
+    assert torch.equal(ssm.conv(far(0), w, b, out=far(1)), ssm.conv(d["u"], w, b))
+    g, f = ssm.conv_backward(dy.cuda(), d["u"], w, b), ssm.conv_backward(dy.cuda(), far(0), w, b, out=far(1))
+    for k in g:
+        assert torch.equal(g[k], f[k]), k
+    v, vf = norm.block_norm(d["u"], wn, gate=d["z"])[0], norm.block_norm(far(0), wn, gate=d["z"], out=far(1))[0]
+    assert torch.equal(v, vf)
+    args = dict(w_post=wn, gate=d["z"])
+    g, f = norm.block_norm_backward(dy.cuda(), d["u"], v, **args), norm.block_norm_backward(dy.cuda(), far(0), v, **args, out=far(1))
+    for k in g:
+        assert (g[k] is None and f[k] is None) or torch.equal(g[k], f[k]), k
