@@ -9,7 +9,8 @@
  * Conventions shared by these entry points
  *   - Everything gma.h says about ownership, streams and errors holds: device memory of the
  *     current CUDA device, caller-owned buffers, no allocation and no synchronisation, all work
- *     on `stream`, argument errors before anything is enqueued, status codes of gma_status_t.
+ *     on `stream`, argument errors before anything is enqueued, status codes of gma_status_t.  Calls from
+ *     several host threads at once are fine.
  *   - Activations are bf16 or fp32 (gma_dtype_t) in token-major rows: gma_rows_t names a tensor
  *     [B][N][width] by its first element and the strides, in elements, between batch rows and
  *     between tokens.  The channels of one token are contiguous; rows may be part of a wider
@@ -53,8 +54,8 @@ typedef struct {
  *     h_t[d][n] = exp(delta_t A[d][n]) h_{t-1}[d][n] + delta_t b_t[g][n] u_t[d],
  *     p_t[d] = sum_n c_t[g][n] h_t[d][n] + d_skip[d] u_t[d],
  *     y_t[d] = p_t[d] silu(z_t[d])          (y = p without z).
- * S in {8, 16, 32, 64}; 1 <= G, G divides D; B <= 65535, N <= 2^30 (the backward pass: N <= 64 * 65535,
- * D * S < 2^30). */
+ * S in {8, 16, 32, 64}; 1 <= G, G divides D; 1 <= B <= 65535, 1 <= N <= 2^30, 1 <= D <= 2^24 (the backward
+ * pass: N <= 64 * 65535, D * S < 2^30, G <= 65535, B * G * ceil(N * S / 512) < 2^30). */
 typedef struct {
     int32_t B, N, D, S, G;
     int32_t dtype;                /* of u, dt, z, b, c, y and their gradients               */
@@ -101,6 +102,8 @@ typedef struct {
     float *dstate_in;             /* [B][D][S] or NULL                                       */
 } gma_scan_grad_t;
 
+/* About B * N * G * 8 S * ceil(D S / (1024 G)) bytes: S^2 / 128 a (token, channel), 2 at 16 states and 32 at 64, and
+ * the states of every chunk beside them. */
 size_t gma_scan_backward_workspace_size(const gma_scan_grad_t *grad);
 gma_status_t gma_scan_backward(const gma_scan_grad_t *grad, void *workspace, size_t workspace_bytes,
                                gma_stream_t stream);
@@ -109,7 +112,8 @@ gma_status_t gma_scan_backward(const gma_scan_grad_t *grad, void *workspace, siz
  *
  * Per batch row and channel, taps k = 0 .. W - 1, with x_{-1}, ..., x_{-(W-1)} the state's rows:
  *     p_t = sum_k weight[d][k] x_{t - W + 1 + k}[d] + bias[d],   y_t = silu(p_t), or p_t.
- * W in {2, 3, 4}; B <= 65535.  The state is the last W - 1 inputs, oldest first, in dtype. */
+ * W in {2, 3, 4}; 1 <= B <= 65535, 1 <= N <= 2^30, 1 <= D <= 2^24, B, N and D such that the runs of tokens (at most 256
+ * each) of four channels stay below 2^31.  The state is the last W - 1 inputs, oldest first, in dtype. */
 #define GMA_CONV_LINEAR 0x1u      /* y_t = p_t */
 
 typedef struct {

@@ -8,7 +8,8 @@
 // the windows then take few enough registers for twice the warps, which hide the loads.  The window is a
 // ring whose slots are fixed by unrolling a whole turn, so no value is moved.
 // Measured (W = 4, bf16): forward 2 x 16384 x 2080 in 56 us (4.9 TB/s; eight channels a thread 71 us, with moved
-// windows 150 us); backward 32 x 1024 x 512, half of it padding, 28 us (42 instructions an element at 128 registers).
+// windows 150 us); backward 32 x 1024 x 512, half of it padding, 28 us (42 instructions an element at 128 registers),
+// 4 x 16384 x 4096 324 us (5.0 TB/s).  In fp32 with W = 4 the backward kernel spills about 200 bytes a thread.
 #include "block_common.cuh"
 
 namespace gma {

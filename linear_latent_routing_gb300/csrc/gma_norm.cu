@@ -9,7 +9,8 @@
 // narrow rows.  The mixers' layout [B][H][N][d] is read (and its gradient written) in place, head
 // by head, so no transposition runs between a mixer and its norm.
 // Measured: per-head norm with a gate of 65536 x 2048 bf16 in 125 us (6.4 TB/s); both norms with gate, scale and an
-// fp32 residual of 8192 x 2048 in 44 us (5.3 TB/s) forward and 81 us (4.6 TB/s) backward.
+// fp32 residual of 8192 x 2048 in 44 us (5.3 TB/s) forward and 81 us (4.6 TB/s) backward.  From 4097 channels on the
+// backward kernels spill (about 430 bytes a thread, 2100 from 8193 on); those widths are not timed.
 #include <algorithm>
 #include <type_traits>
 

@@ -8,7 +8,7 @@
 // spreads a tile's tokens over the lanes of a warp and needs one launch; it takes the calls with too few channels
 // and tokens to fill the GPU in chunks (gma_scan_chunk.cu).  Latency bounds it there: 512 tokens of 1024
 // channels x 16 states take 15 us, 32 tokens 12 us.  The step moves its state once: 128 x 2048 x 16 in 11 us
-// (33.5 MB), one row of 1024 channels in the time of a launch.
+// (33.5 MB), 512 rows in 29 us (4.9 TB/s), one row of 1024 channels in the time of a launch.
 #include <type_traits>
 
 #include "scan_args.cuh"

@@ -13,11 +13,13 @@
 // A lane holds eight states of a channel (S / 8 lanes a channel) and their eight tokens' history in 64
 // registers, so that 12 warps fit an SM; x, q and p are added over a channel's lanes by shuffles.  db and dc are
 // sums over channels: a warp passes its lanes' products through shared memory (lanes write rows, read
-// columns), a block adds its warps, and step 4 the blocks, always in the same order.
+// columns), a block adds its warps, and step 4 the blocks, always in the same order.  The blocks' parts go through
+// memory: S^2 / 128 bytes a (token, channel), 2 at 16 states and 32 at 64.
 // Measured: 4 x 2048 x 1024 channels x 16 states, bf16 with a gate: 41 us, 10 us, 184 us and 10 us.  Step 3
 // takes 422 instructions an element (three exponentials a state) at 50 % of the issue slots with 11 warps an SM; the
 // shared-memory pipe binds it (76 % busy: 78 wavefronts a token of a warp, 32 of them the column sums').  Two channels
-// of four states a lane halve those, but stage every value twice and spill: 224 us.  Tokens over lanes, as in
+// of four states a lane halve those, but stage every value twice and spill more (this form spills 24 bytes a thread, with other
+// types, states and rows 12 to 316): 224 us.  Tokens over lanes, as in
 // gma_scan.cu, took 303 us.
 #include "scan_args.cuh"
 

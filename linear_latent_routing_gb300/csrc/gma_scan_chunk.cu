@@ -1,17 +1,19 @@
-// gma_scan_chunk.cu -- the selective scan's forward pass in chunks of tokens, and the adjoint behind every chunk of the backward pass.
+// gma_scan_chunk.cu -- the selective scan's forward pass in chunks of tokens, and the adjoint behind every chunk of
+// its backward pass.
 //
 // Lanes are channels, every warp walks over the tokens of one chunk with its states in registers, and
-// nothing but y is exchanged between lanes: a lane holds 32 states, of two channels (S <= 16, whose u, dt, z
-// and y are one access) or of one; with S = 64 two lanes share a channel.
+// nothing but y is exchanged between lanes: a lane holds the states of two channels (8 or 16 each, whose u, dt, z
+// and y are one access) or 32 of one; with S = 64 two lanes share a channel.
 // The sequence is cut into chunks so that short batches fill the GPU too:
 //   1. scan_chunk_state: each chunk's state from a zero start, and its sum of delta;
 //   2. scan_chunk_join: over the chunks in order, state = exp(A sum delta) state + chunk's state;
 //      what is in front of each chunk is its start (and a checkpoint for the backward pass);
 //   3. scan_chunk_output: each chunk again from its start, with the output.
 // One chunk needs step 3 alone.  Per (token, channel, state) steps 1 and 3 take two exponentials
-// (of 32 a clock and SM) and three and a half packed fp32 instructions; instruction issue binds.
-// Measured: 65536 tokens of 2048 channels x 16 states, bf16 with a gate: 354 us, 31 us and 504 us (69 and 99
-// instructions an element, 62 % of the issue slots used); 4 x 2048 x 1024: 37, 10 and 47 us.
+// (of 32 a clock and SM) and three and a half packed fp32 instructions; issue (62 % while an SM has work, 51 % of the
+// elapsed time), the exponentials' pipe (53 and 43 %) and the last wave's empty places bind together.
+// Measured: 65536 tokens of 2048 channels x 16 states, bf16 with a gate: 354 us, 32 us and 508 us (69 and 99
+// instructions an element); 4 x 2048 x 1024: 37, 10 and 47 us.
 #include "scan_args.cuh"
 
 namespace gma {
@@ -456,7 +458,8 @@ template <typename T, int S, bool VEC> gma_status_t run(const gma_scan_t &s, cha
 
 // Worth it from six warps an SM on: with fewer, a warp's walk over its chunk takes as long as
 // the whole call of the kernel that spreads a tile's tokens over lanes (512 tokens of 1024 channels: 33 us in
-// three launches against 15 us).
+// three launches against 15 us).  That kernel walks over its tiles of 256 tokens one after another; a few channels over
+// many thousand tokens are not measured on either side of the rule.
 bool scan_chunked(const gma_scan_t &s)
 {
     const long long warps = (long long)s.B * s.G * group_warps(s) * ((s.N + 31) / 32);
