@@ -4,7 +4,9 @@
  *
  *   gma_scan_*  the selective state space scan, the other mixer with a fixed state per sequence;
  *   gma_conv_*  the short causal convolution per channel in front of it;
- *   gma_norm_*  the norms before and after a block, fused with its gate and residual scale.
+ *   gma_norm_*  the norms before and after a block, fused with its gate and residual scale;
+ *   gma_attn_*  softmax attention, the exact layers of a hybrid stack: whole sequences, their backward
+ *               pass, and new tokens over a paged cache.
  *
  * Conventions shared by these entry points
  *   - Everything gma.h says about ownership, streams and errors holds: device memory of the
@@ -24,7 +26,8 @@
  *     written (with GMA_ROWS_ZERO_TAIL: are written as zeros), and the states that come out are those
  *     after the last token.
  *   - The workspace is 256-byte aligned, needs no initialisation, holds nothing between calls and
- *     has no error word (no kernel behind these entry points waits for another one's signal).
+ *     has no error word (no kernel behind these entry points waits for another one's signal), but for
+ *     gma_attn_*, whose bounded waits record a time-out in it for gma_check_workspace.
  *     Calls that share one are ordered on the GPU.  Where gma_*_workspace_size gives 0 for valid
  *     arguments, NULL will do.
  *   - Repeated calls on the same inputs give the same bits.
@@ -193,6 +196,84 @@ typedef struct {
 size_t gma_norm_backward_workspace_size(const gma_norm_grad_t *grad);
 gma_status_t gma_norm_backward(const gma_norm_grad_t *grad, void *workspace, size_t workspace_bytes,
                                gma_stream_t stream);
+
+/* ------------------------------------------------------------------ softmax attention
+ *
+ * Query head h (of H) reads key and value head g = h / (H / G).  Per sequence, over the keys j that row i sees:
+ *     s_ij = scale q_i . k_j,   p_ij = exp(s_ij) / sum_j exp(s_ij),   o_i = sum_j p_ij v_j,
+ *     lse_i = log sum_j exp(s_ij).
+ * gma_attn_forward: row i sees every row of its sequence, or with GMA_ATTN_CAUSAL the rows j <= i.
+ * gma_attn_paged: row i of a sequence's n new tokens sees the cache's first cached - n + i + 1 tokens; a row that sees
+ * none has o = 0 and lse = -inf.
+ *
+ * Heads: gma_heads_t names a tensor [B][N][heads][width] by its first element and the strides, in elements, between
+ * batch rows, tokens and heads; a head's elements are contiguous.  The mixers' layout [B][H][N][d] is one of them.
+ * Padded: `lengths` (NULL: N each) gives every batch row's tokens, taken as min(max(length, 0), N).  Packed: with
+ * `offsets` (B + 1 int32 in device memory, not falling, taken as min(max(offset, 0), N)) the tensors are
+ * [N][heads][width], sequence b is rows offsets[b] .. offsets[b + 1] - 1, batch strides are ignored and lengths is NULL.  Rows that belong to no
+ * sequence are neither read nor written (outputs with GMA_ROWS_ZERO_TAIL: are written as zeros).
+ * 1 <= d, dv <= 128; G divides H, H <= 4096; B <= 65535; B * N <= 2^28 rows (packed: N).  scale > 0.
+ * The elements of a sequence's tokens are finite: where they are not, or a score overflows, that sequence's outputs are
+ * unspecified; other sequences' are not touched.
+ *
+ * bf16 runs on the tensor cores (products of bf16 values in fp32; the probabilities, and in the backward
+ * pass ds, are rounded to bf16 for the second product), fp32 on the CUDA cores.  Sums, statistics and lse are fp32. */
+#define GMA_ATTN_CAUSAL 0x1u
+
+typedef struct {
+    void *ptr;                    /* first element                  */
+    int64_t batch, token, head;   /* strides in elements            */
+} gma_heads_t;
+
+typedef struct {
+    int32_t B, N, H, G;           /* sequences, rows of each (packed: in all), query heads, key and value heads */
+    int32_t d, dv;                /* width of q and k, of v and o                                */
+    int32_t dtype;                /* of q, k, v, o and their gradients                           */
+    uint32_t flags;               /* GMA_ATTN_CAUSAL, GMA_ROWS_ZERO_TAIL                         */
+    float scale;                  /* > 0                                                         */
+    uint32_t reserved;            /* 0                                                           */
+    gma_heads_t q, k, v;          /* [B][N][H][d], [B][N][G][d], [B][N][G][dv]                   */
+    gma_heads_t o;                /* [B][N][H][dv] out                                           */
+    float *lse;                   /* out, [B][H][N] (packed: [H][N]), or NULL                    */
+    const int32_t *lengths;       /* [B] or NULL                                                 */
+    const int32_t *offsets;       /* [B + 1] or NULL                                             */
+} gma_attn_t;
+
+size_t gma_attn_workspace_size(const gma_attn_t *attn);
+gma_status_t gma_attn_forward(const gma_attn_t *attn, void *workspace, size_t workspace_bytes, gma_stream_t stream);
+
+/* The gradients of sum(d_o * o).  `fwd` holds the forward call's arguments with o and lse as that call wrote them (inputs here,
+ * lse required).  Outputs are written, not accumulated; dk and dv are sums over the query heads of a group. */
+typedef struct {
+    gma_attn_t fwd;
+    gma_heads_t d_o, dq, dk, dv;  /* like o, q, k and v */
+} gma_attn_grad_t;
+
+size_t gma_attn_backward_workspace_size(const gma_attn_grad_t *grad);
+gma_status_t gma_attn_backward(const gma_attn_grad_t *grad, void *workspace, size_t workspace_bytes, gma_stream_t stream);
+
+/* A cache of pages, and new tokens.  Token t of sequence b lies in slot t % page of page table[b * table_stride + t / page].
+ * cached[b], taken as min(max(cached, 0), table_pages * page), counts the sequence's tokens with the new ones, which are its last.
+ * Table entries behind a sequence's last token are not read.  An entry outside 0 .. pages - 1 reads as zeros and takes no writes.
+ * `attn` names the new tokens: q, o and lse (gma_attn_paged), k and v (gma_attn_append; not used otherwise); its flags
+ * may be GMA_ROWS_ZERO_TAIL. */
+typedef struct {
+    gma_attn_t attn;
+    gma_heads_t k_pages, v_pages; /* [pages][page][G][d], [pages][page][G][dv]: batch is the stride between pages,
+                                     token between their slots                                   */
+    int32_t pages, page;          /* pages >= 1, 1 <= page <= 65536, pages * page < 2^40         */
+    int32_t table_pages;          /* entries of a sequence's row of the table, table_pages * page <= 2^28 */
+    uint32_t reserved;            /* 0                                                           */
+    int64_t table_stride;         /* between those rows                                          */
+    const int32_t *table;         /* [B][table_pages]                                            */
+    const int32_t *cached;        /* [B]                                                         */
+} gma_attn_paged_t;
+
+/* Writes k and v of the new tokens to their slots (tokens whose place would be before the first one are left out). */
+gma_status_t gma_attn_append(const gma_attn_paged_t *paged, gma_stream_t stream);
+
+size_t gma_attn_paged_workspace_size(const gma_attn_paged_t *paged);
+gma_status_t gma_attn_paged(const gma_attn_paged_t *paged, void *workspace, size_t workspace_bytes, gma_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -1,9 +1,10 @@
 // block_binding.cpp -- the Python binding of include/gma_block.h (module _block): checks torch CUDA tensors,
 // allocates outputs and workspaces through torch, fills the header's structs and calls libgma.so on the
 // current stream.  A call for one token takes a few microseconds on the GPU; with the marshalling in
-// Python the host took 17 us a call, here 5.  ssm.py and norm.py hold the documented functions; each passes its
+// Python the host took 17 us a call, here 5.  ssm.py, norm.py and attention.py hold the documented functions; each passes its
 // arguments on in order.  Tensors are checked for type, device, dtype, shape and contiguous channels; what the C
 // entry points refuse comes back as gma.GmaError.
+#include <cmath>
 #include <string>
 #include <vector>
 
@@ -559,10 +560,258 @@ PyObject *block_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n)
     });
 }
 
+// ------------------------------------------------------------------ softmax attention
+
+// Heads [B, N, heads, width] (or [T, heads, width]: rows of one batch row, or with `one` a token of every batch row).
+gma_heads_t attn_heads(const at::Tensor &t, const char *name, at::IntArrayRef shape, bool one, const Call &c)
+{
+    check(t, name, shape, c.T, c);
+    const at::IntArrayRef s = t.strides();
+    if (s.back() != 1 && shape.back() != 1) value_error(std::string(name) + "'s heads must be contiguous");
+    if (shape.size() == 4) return gma_heads_t{t.data_ptr(), s[0], s[1], s[2]};
+    return one ? gma_heads_t{t.data_ptr(), s[0], 0, s[1]} : gma_heads_t{t.data_ptr(), 0, s[0], s[1]};
+}
+gma_heads_t attn_heads(PyObject *o, const char *name, at::IntArrayRef shape, bool one, const Call &c)
+{
+    return attn_heads(tensor(o, name), name, shape, one, c);
+}
+
+void apart(const gma_heads_t &out, const char *name, std::initializer_list<const gma_heads_t *> others)
+{
+    for (const gma_heads_t *o : others)
+        if (out.ptr && out.ptr == o->ptr) value_error(std::string(name) + " must not be another tensor of the call");
+}
+
+int truth(PyObject *o, const char *name)
+{
+    const int t = PyObject_IsTrue(o);
+    if (t < 0) {
+        PyErr_Clear();
+        type_error(std::string(name) + " must be a truth value");
+    }
+    return t;
+}
+
+// What the calls share: the batch of `t` (the new tokens' or the prompt's rows), lengths, offsets and scale.  `paged`: rows
+// [T, heads, width] without offsets are one token for each of `sequences`.
+struct Shape {
+    std::vector<int64_t> lead;        // [B, N], or [T]
+    bool one;                         // [B, heads, width], one token each
+    std::vector<int64_t> with(int64_t heads, int64_t width) const
+    {
+        std::vector<int64_t> v = lead;
+        v.push_back(heads);
+        v.push_back(width);
+        return v;
+    }
+};
+
+Shape attn_shape(gma_attn_t *a, const at::Tensor &t, const char *name, PyObject *lengths, PyObject *offsets, PyObject *scale, int64_t width,
+                 bool paged, const Call &c)
+{
+    if (t.dim() != 3 && t.dim() != 4) value_error(std::string(name) + " must be [B, N, heads, width] or [T, heads, width]");
+    Shape s;
+    s.lead = t.sizes().slice(0, t.dim() - 2).vec();
+    if (given(offsets)) {
+        if (t.dim() != 3) value_error("with offsets " + std::string(name) + " must be [T, heads, width]");
+        if (given(lengths)) value_error("lengths and offsets exclude one another");
+        const at::Tensor &o = tensor(offsets, "offsets");
+        if (o.dim() != 1 || o.size(0) < 2) value_error("offsets must be [B + 1]");
+        a->offsets = dense<int32_t>(offsets, "offsets", {o.size(0)}, at::kInt, c);
+    }
+    s.one = paged && t.dim() == 3 && !given(offsets);
+    const int64_t B = a->offsets ? tensor(offsets, "offsets").size(0) - 1 : t.dim() == 4 || s.one ? t.size(0) : 1;
+    const int64_t N = s.one ? 1 : t.size(t.dim() - 3);
+    if (B > INT32_MAX || N > INT32_MAX || t.size(-1) > INT32_MAX || t.size(-2) > INT32_MAX) value_error("a size is too large");
+    a->B = (int32_t)B;
+    a->N = (int32_t)N;
+    if (given(lengths)) a->lengths = dense<int32_t>(lengths, paged ? "new_lengths" : "lengths", {B}, at::kInt, c);
+    double x = 1.0 / std::sqrt((double)(width > 0 ? width : 1));
+    if (given(scale)) {
+        x = PyFloat_AsDouble(scale);
+        if (PyErr_Occurred()) {
+            PyErr_Clear();
+            type_error("scale must be a number");
+        }
+    }
+    a->scale = (float)x;
+    a->dtype = c.dtype();
+    return s;
+}
+
+// lse [B, H, N], or [H, T] packed ([B, H] for one token each)
+float *attn_lse(PyObject *o, const gma_attn_t &a, const Shape &s, const Call &c)
+{
+    if (!given(o)) return nullptr;
+    if (s.one) return dense(o, "lse", {a.B, a.H}, at::kFloat, c);
+    if (s.lead.size() == 1) return dense(o, "lse", {a.H, a.N}, at::kFloat, c);
+    return dense(o, "lse", {a.B, a.H, a.N}, at::kFloat, c);
+}
+
+int64_t dim_of(PyObject *o, const char *name, int64_t dims, int64_t d)
+{
+    const at::Tensor &t = tensor(o, name);
+    if (t.dim() != dims) value_error(std::string(name) + (dims == 4 ? " must have four dimensions" : " must have three dimensions"));
+    if (t.size(d) > INT32_MAX) value_error("a size is too large");
+    return t.size(d);
+}
+
+gma_status_t attn_checked(gma_status_t r, bool check, const Workspace &ws, const Call &c)
+{
+    return r == GMA_OK && check && ws.bytes ? gma_check_workspace(ws.ptr(), c.stream()) : r;
+}
+
+// q, k, v, causal, scale, lengths, offsets: arguments 0 .. 6 of the calls on whole sequences
+Shape attn_of(PyObject *const *p, gma_attn_t *a, Call *c)
+{
+    const at::Tensor &q = tensor(p[0], "q");
+    *c = begin(q, "q");
+    const Shape s = attn_shape(a, q, "q", p[5], p[6], p[4], q.dim() ? q.size(-1) : 1, false, *c);
+    a->H = (int32_t)q.size(-2);
+    a->d = (int32_t)q.size(-1);
+    a->G = (int32_t)dim_of(p[1], "k", q.dim(), q.dim() - 2);
+    a->dv = (int32_t)dim_of(p[2], "v", q.dim(), q.dim() - 1);
+    a->flags = truth(p[3], "causal") ? GMA_ATTN_CAUSAL : 0;
+    a->q = attn_heads(q, "q", s.with(a->H, a->d), false, *c);
+    a->k = attn_heads(p[1], "k", s.with(a->G, a->d), false, *c);
+    a->v = attn_heads(p[2], "v", s.with(a->G, a->dv), false, *c);
+    return s;
+}
+
+// ..., lse, out, check
+PyObject *attn_prompt(PyObject *, PyObject *const *p, Py_ssize_t n)
+{
+    return guarded(n, 10, [&]() -> PyObject * {
+        Call c;
+        gma_attn_t a = {};
+        const Shape s = attn_of(p, &a, &c);
+        a.lse = attn_lse(p[7], a, s, c);
+        if (!given(p[8])) a.flags |= GMA_ROWS_ZERO_TAIL;
+        const std::vector<int64_t> shape = s.with(a.H, a.dv);
+        const at::Tensor o = out_or(p[8], "out", [&] { return c.empty(shape); });
+        a.o = attn_heads(o, "out", shape, false, c);
+        if (given(p[8])) apart(a.o, "out", {&a.q, &a.k, &a.v});
+        const bool check = truth(p[9], "check");
+        const Workspace ws(gma_attn_workspace_size(&a), c);
+        const gma_status_t r = attn_checked(gma_attn_forward(&a, ws.ptr(), ws.bytes, c.stream()), check, ws, c);
+        return r == GMA_OK ? wrap(o) : raise_status(r, "gma_attn_forward");
+    });
+}
+
+// ..., do, o, lse, out of q, k and v, check
+PyObject *attn_backward(PyObject *, PyObject *const *p, Py_ssize_t n)
+{
+    return guarded(n, 14, [&]() -> PyObject * {
+        Call c;
+        gma_attn_grad_t g = {};
+        gma_attn_t &a = g.fwd;
+        const Shape s = attn_of(p, &a, &c);
+        const std::vector<int64_t> qs = s.with(a.H, a.d), ks = s.with(a.G, a.d), vs = s.with(a.G, a.dv), os = s.with(a.H, a.dv);
+        g.d_o = attn_heads(p[7], "do", os, false, c);
+        a.o = attn_heads(p[8], "o", os, false, c);
+        if (!given(p[9])) type_error("lse is required");
+        a.lse = attn_lse(p[9], a, s, c);
+        // the rows of no sequence: zero in buffers allocated here, left alone in the caller's
+        const bool some = given(p[10]) || given(p[11]) || given(p[12]), ragged = a.lengths || a.offsets;
+        if (!some) a.flags |= GMA_ROWS_ZERO_TAIL;
+        const at::Tensor dq = out_or(p[10], "out['q']", [&] { return c.rows(qs, some && ragged); });
+        const at::Tensor dk = out_or(p[11], "out['k']", [&] { return c.rows(ks, some && ragged); });
+        const at::Tensor dv = out_or(p[12], "out['v']", [&] { return c.rows(vs, some && ragged); });
+        g.dq = attn_heads(dq, "out['q']", qs, false, c);
+        g.dk = attn_heads(dk, "out['k']", ks, false, c);
+        g.dv = attn_heads(dv, "out['v']", vs, false, c);
+        if (some) {
+            const gma_heads_t *outs[3] = {&g.dq, &g.dk, &g.dv};
+            for (int i = 0; i < 3; ++i) {
+                apart(*outs[i], "an output", {&a.q, &a.k, &a.v, &a.o, &g.d_o});
+                for (int j = 0; j < i; ++j) apart(*outs[i], "an output", {outs[j]});
+            }
+        }
+        const bool check = truth(p[13], "check");
+        const Workspace ws(gma_attn_backward_workspace_size(&g), c);
+        const gma_status_t r = attn_checked(gma_attn_backward(&g, ws.ptr(), ws.bytes, c.stream()), check, ws, c);
+        if (r != GMA_OK) return raise_status(r, "gma_attn_backward");
+        PyObject *d = PyDict_New();
+        if (!d) return nullptr;
+        set(d, "q", dq); set(d, "k", dk); set(d, "v", dv);
+        return d;
+    });
+}
+
+// k_pages, v_pages, table, cached into the struct whose batch is known
+void attn_cache(gma_attn_paged_t *p, PyObject *kp, PyObject *vp, PyObject *table, PyObject *cached, const Call &c)
+{
+    gma_attn_t &a = p->attn;
+    p->pages = (int32_t)dim_of(kp, "k_pages", 4, 0);
+    p->page = (int32_t)dim_of(kp, "k_pages", 4, 1);
+    p->k_pages = attn_heads(kp, "k_pages", {p->pages, p->page, a.G, a.d}, false, c);
+    p->v_pages = attn_heads(vp, "v_pages", {p->pages, p->page, a.G, a.dv}, false, c);
+    const at::Tensor &t = tensor(table, "table");
+    if (t.dim() != 2) value_error("table must be [B, pages]");
+    if (t.size(1) > INT32_MAX) value_error("a size is too large");
+    check(t, "table", {a.B, t.size(1)}, at::kInt, c);
+    if (t.size(1) > 1 && t.stride(1) != 1) value_error("table's rows must be contiguous");
+    p->table_pages = (int32_t)t.size(1);
+    p->table_stride = t.stride(0);
+    p->table = (const int32_t *)t.data_ptr();
+    p->cached = need<int32_t>(cached, "lengths", {a.B}, at::kInt, c);
+}
+
+// k, v, k_pages, v_pages, table, lengths, new_lengths, offsets
+PyObject *attn_append(PyObject *, PyObject *const *p, Py_ssize_t n)
+{
+    return guarded(n, 8, [&]() -> PyObject * {
+        gma_attn_paged_t g = {};
+        gma_attn_t &a = g.attn;
+        const at::Tensor &k = tensor(p[0], "k");
+        const Call c = begin(k, "k");
+        const Shape s = attn_shape(&a, k, "k", p[6], p[7], Py_None, 1, true, c);
+        a.G = a.H = (int32_t)k.size(-2);
+        a.d = (int32_t)k.size(-1);
+        a.dv = (int32_t)dim_of(p[1], "v", k.dim(), k.dim() - 1);
+        a.k = attn_heads(k, "k", s.with(a.G, a.d), s.one, c);
+        a.v = attn_heads(p[1], "v", s.with(a.G, a.dv), s.one, c);
+        attn_cache(&g, p[2], p[3], p[4], p[5], c);
+        apart(g.k_pages, "k_pages", {&a.k, &a.v, &g.v_pages});
+        apart(g.v_pages, "v_pages", {&a.k, &a.v});
+        const gma_status_t r = gma_attn_append(&g, c.stream());
+        return r == GMA_OK ? none() : raise_status(r, "gma_attn_append");
+    });
+}
+
+// q, k_pages, v_pages, table, lengths, new_lengths, offsets, scale, lse, out, check
+PyObject *attn_paged(PyObject *, PyObject *const *p, Py_ssize_t n)
+{
+    return guarded(n, 11, [&]() -> PyObject * {
+        gma_attn_paged_t g = {};
+        gma_attn_t &a = g.attn;
+        const at::Tensor &q = tensor(p[0], "q");
+        const Call c = begin(q, "q");
+        const Shape s = attn_shape(&a, q, "q", p[5], p[6], p[7], q.dim() ? q.size(-1) : 1, true, c);
+        a.H = (int32_t)q.size(-2);
+        a.d = (int32_t)q.size(-1);
+        a.G = (int32_t)dim_of(p[1], "k_pages", 4, 2);
+        a.dv = (int32_t)dim_of(p[2], "v_pages", 4, 3);
+        a.q = attn_heads(q, "q", s.with(a.H, a.d), s.one, c);
+        attn_cache(&g, p[1], p[2], p[3], p[4], c);
+        a.lse = attn_lse(p[8], a, s, c);
+        if (!given(p[9])) a.flags |= GMA_ROWS_ZERO_TAIL;
+        const std::vector<int64_t> shape = s.with(a.H, a.dv);
+        const at::Tensor o = out_or(p[9], "out", [&] { return c.empty(shape); });
+        a.o = attn_heads(o, "out", shape, s.one, c);
+        if (given(p[9])) apart(a.o, "out", {&a.q, &g.k_pages, &g.v_pages});
+        const bool check = truth(p[10], "check");
+        const Workspace ws(gma_attn_paged_workspace_size(&g), c);
+        const gma_status_t r = attn_checked(gma_attn_paged(&g, ws.ptr(), ws.bytes, c.stream()), check, ws, c);
+        return r == GMA_OK ? wrap(o) : raise_status(r, "gma_attn_paged");
+    });
+}
+
 #define METHOD(f) {#f, (PyCFunction)(void *)f, METH_FASTCALL, ""}
 PyMethodDef methods[] = {METHOD(scan_checkpoints), METHOD(scan), METHOD(scan_step), METHOD(scan_backward), METHOD(conv), METHOD(conv_step),
-                         METHOD(conv_backward), METHOD(block_norm), METHOD(block_norm_backward), {nullptr, nullptr, 0, nullptr}};
-PyModuleDef module = {PyModuleDef_HEAD_INIT, "_block", "Binding of gma_block.h; see ssm and norm.", -1, methods,
+                         METHOD(conv_backward), METHOD(block_norm), METHOD(block_norm_backward), METHOD(attn_prompt), METHOD(attn_backward),
+                         METHOD(attn_append), METHOD(attn_paged), {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_block", "Binding of gma_block.h; see ssm, norm and attention.", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

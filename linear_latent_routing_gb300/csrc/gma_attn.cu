@@ -1,0 +1,443 @@
+// gma_attn.cu -- softmax attention: the entry points' checks, the plan of a call, and the small kernels around the
+// products: tokens into the cache's pages, zeros behind sequences, do . o of every row.
+#include <algorithm>
+
+#include "attn_common.cuh"
+
+namespace gma {
+namespace att {
+namespace {
+
+constexpr int PT = 1024;               // threads of the plan's block
+constexpr int BUCKETS = 1024;          // items are ordered by size up to so many key tiles
+
+// Tiles of sequence q and the key tiles (by_keys: query tiles) of the one that starts at token `tok`.
+__device__ __forceinline__ int item_cost(const PlanArgs &a, const Seq &q, int tok, int tokens, int *first)
+{
+    *first = 0;
+    if (a.by_keys) {                   // a tile of keys: the query tiles from the one that first sees it
+        *first = a.g.causal ? tok / a.keys : 0;
+        return (q.n + a.keys - 1) / a.keys - *first;
+    }
+    const int last = min(tok + tokens, q.n) - 1;
+    return max((q.seen(a.g, last) + a.keys - 1) / a.keys, 1);
+}
+
+__global__ void __launch_bounds__(PT) plan_kernel(const PlanArgs a0, const PlanArgs a1)
+{
+    const PlanArgs &a = blockIdx.x ? a1 : a0;
+    __shared__ unsigned long long total;
+    __shared__ int count, slots, joins, share, hist[BUCKETS], warps[32];
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    blk::let_next();
+    if (t == 0) { total = 0; count = 0; slots = 0; joins = 0; }
+    hist[t] = 0;
+    if (a.hdr && t < (int)(sizeof(WsHeader) / 4)) reinterpret_cast<unsigned *>(a.hdr)[t] = 0;
+    __syncthreads();
+    // wide tiles, or narrow ones
+    int mine = 0;
+    for (int s = t; s < a.g.B; s += PT) {
+        const Seq q = sequence(a.g, s);
+        mine += (q.n + a.wide - 1) / a.wide;
+    }
+    if (mine) atomicAdd(&count, mine);
+    __syncthreads();
+    const int tokens = (long long)count * a.heads < SMS ? a.narrow : a.wide;
+    // all items' key tiles, and an SM's share of them
+    unsigned long long work = 0;
+    int first;
+    for (int s = warp; s < a.g.B; s += PT / 32) {
+        const Seq q = sequence(a.g, s);
+        for (int k = lane; k * (long long)tokens < q.n; k += 32) work += item_cost(a, q, k * tokens, tokens, &first);
+    }
+    if (work) atomicAdd(&total, work);
+    __syncthreads();
+    if (t == 0) {
+        const unsigned long long per = (total * a.heads + a.target - 1) / a.target;
+        share = a.max_slots ? (int)min(max(per, (unsigned long long)a.least), 0x7fffffffull) : 0x7fffffff;
+        count = 0;
+    }
+    __syncthreads();
+    // how many of each size, where those of a size start, and the list
+    for (int pass = 0; pass < 2; ++pass) {
+        for (int s = warp; s < a.g.B; s += PT / 32) {
+            const Seq q = sequence(a.g, s);
+            for (int k = lane; k * (long long)tokens < q.n; k += 32) {
+                const int cost = item_cost(a, q, k * tokens, tokens, &first);
+                const int parts = (int)(((long long)cost + share - 1) / share), size = (cost + parts - 1) / parts;
+                const int bucket = BUCKETS - 1 - min(size, BUCKETS - 1);
+                const int at = atomicAdd(&hist[bucket], parts);
+                if (pass == 0) continue;
+                const int slot = parts > 1 ? atomicAdd(&slots, parts) : 0, join = parts > 1 ? atomicAdd(&joins, 1) : 0;
+                if (parts > 1 && slot + parts > a.max_slots) continue;       // offsets that fall: more tiles than rows
+                for (int p = 0; p < parts; ++p)
+                    if (at + p < a.max_items)
+                        a.items[at + p] = Item{s, k * tokens, first + min(p * size, cost), first + min((p + 1) * size, cost), slot,
+                                               parts, p, join};
+            }
+        }
+        __syncthreads();
+        if (pass) break;
+        const int own = hist[t];
+        int sum = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int up = __shfl_up_sync(~0u, sum, o);
+            if (lane >= o) sum += up;
+        }
+        if (lane == 31) warps[warp] = sum;
+        __syncthreads();
+        int before = 0;
+        for (int w = 0; w < warp; ++w) before += warps[w];
+        hist[t] = before + sum - own;
+        if (t == PT - 1) count = before + sum;
+        __syncthreads();
+    }
+    for (int i = t; i < joins * a.heads && i < a.max_slots * a.heads; i += PT) a.join[i] = 0;
+    if (t == 0) {
+        a.head->items = min(count, a.max_items);
+        a.head->tokens = tokens;
+    }
+}
+
+// Rows that belong to no sequence: zeros.  A warp a row of [rows][heads * width].
+template <typename T>
+__global__ void __launch_bounds__(256) attn_tail_kernel(const Geo g, const Heads<T> x, int heads, int width, long long rows)
+{
+    const int lane = threadIdx.x & 31;
+    for (long long r = blockIdx.x * 8ll + (threadIdx.x >> 5); r < rows; r += gridDim.x * 8ll) {
+        long long b = 0, i = r;
+        if (g.offsets) {
+            if (r >= max(g.offsets[0], 0) && r < g.offsets[g.B]) continue;
+        } else {
+            b = r / g.N;
+            i = r - b * g.N;
+            if (i < blk::row_length(g.lengths, (int)b, g.N)) continue;
+        }
+        for (int h = 0; h < heads; ++h)
+            for (int c = lane; c < width; c += 32) x.at(b, i, h)[c] = from_f32<T>(0.f);
+    }
+}
+
+// delta = do . o: a warp a (row, head).
+template <typename T>
+__global__ void __launch_bounds__(256) attn_delta_kernel(const Geo g, const Heads<const T> o, const Heads<const T> d_o, float *delta,
+                                                         long long rows)
+{
+    const int lane = threadIdx.x & 31;
+    blk::let_next();
+    for (long long r = blockIdx.x * 8ll + (threadIdx.x >> 5); r < rows; r += gridDim.x * 8ll) {
+        const long long bh = r / g.N, i = r - bh * g.N;
+        const int b = (int)(bh / g.H), h = (int)(bh - (long long)b * g.H);
+        if (g.offsets) {
+            if (i < max(g.offsets[0], 0) || i >= g.offsets[g.B]) continue;
+        } else if (i >= blk::row_length(g.lengths, b, g.N)) {
+            continue;
+        }
+        const T *x = o.at(b, i, h), *y = d_o.at(b, i, h);
+        float s = 0.f;
+        for (int c = lane; c < g.dv; c += 32) s = fmaf(to_f32<T>(x[c]), to_f32<T>(y[c]), s);
+#pragma unroll
+        for (int m = 16; m; m >>= 1) s += __shfl_xor_sync(~0u, s, m);
+        if (lane == 0) delta[r] = s;
+    }
+    blk::wait_previous();
+}
+
+// The new tokens' keys and values into their slots: a warp a (token, head), both tensors.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256) attn_append_kernel(const Geo g, const Heads<const T> k, const Heads<const T> v, const Heads<T> kp,
+                                                          const Heads<T> vp, long long rows)
+{
+    const int lane = threadIdx.x & 31;
+    for (long long r = blockIdx.x * 8ll + (threadIdx.x >> 5); r < rows; r += gridDim.x * 8ll) {
+        const int h = (int)(r % g.G);
+        const long long tok = r / g.G;
+        int s, i;
+        if (g.offsets) {               // the last sequence that starts at or before the row
+            int lo = 0, hi = g.B;      // empty ones may share a start: the last of them holds the row
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (g.offsets[mid] <= tok) lo = mid; else hi = mid;
+            }
+            s = lo;
+        } else {
+            s = (int)(tok / g.N);
+        }
+        const Seq q = sequence(g, s);
+        i = (int)(g.offsets ? tok - q.row0 : tok - (long long)s * g.N);
+        const int j = q.pos0 + i;
+        if (i < 0 || i >= q.n || j < 0 || j >= q.L) continue;
+        int slot;
+        const int p = page_of(g, s, j, &slot);
+        if (p < 0) continue;
+        const T *ks = k.at(q.b, q.row0 + i, h), *vs = v.at(q.b, q.row0 + i, h);
+        T *kd = kp.at(p, slot, h), *vd = vp.at(p, slot, h);
+        if (VEC) {
+            constexpr int E = 16 / sizeof(T);
+            for (int c = lane * E; c < g.d; c += 32 * E) *reinterpret_cast<uint4 *>(kd + c) = *reinterpret_cast<const uint4 *>(ks + c);
+            for (int c = lane * E; c < g.dv; c += 32 * E) *reinterpret_cast<uint4 *>(vd + c) = *reinterpret_cast<const uint4 *>(vs + c);
+        } else {
+            for (int c = lane; c < g.d; c += 32) kd[c] = ks[c];
+            for (int c = lane; c < g.dv; c += 32) vd[c] = vs[c];
+        }
+    }
+}
+
+unsigned row_blocks(long long rows) { return (unsigned)std::min<long long>((rows + 7) / 8, SMS * 16); }
+
+// ------------------------------------------------------------------ checks
+// One of [B][N][heads][width]: aligned to its elements, strides that are not negative; outputs' rows apart.
+bool heads_ok(const gma_heads_t &r, int dtype, long long B, long long N, long long heads, long long width, bool out)
+{
+    if (!r.ptr || ((uintptr_t)r.ptr & (blk::elem_size(dtype) - 1)) || r.batch < 0 || r.token < 0 || r.head < 0) return false;
+    if (!out) return true;
+    // each stride that is used steps over the extent of the smaller ones
+    struct Dim { long long size, stride; } dims[3] = {{heads, r.head}, {N, r.token}, {B, r.batch}};
+    std::sort(dims, dims + 3, [](const Dim &x, const Dim &y) { return x.stride < y.stride; });
+    long long extent = width;
+    for (const Dim &m : dims) {
+        if (m.size <= 1) continue;
+        if (m.stride < extent) return false;
+        extent += (m.size - 1) * m.stride;
+    }
+    return true;
+}
+
+bool heads_vec(const gma_heads_t &r, int dtype)
+{
+    const size_t e = blk::elem_size(dtype);
+    return (((uintptr_t)r.ptr | (uintptr_t)(r.batch * e) | (uintptr_t)(r.token * e) | (uintptr_t)(r.head * e)) & 15u) == 0;
+}
+
+gma_status_t check_sizes(const gma_attn_t *a, uint32_t flags)
+{
+    if (!a || a->reserved || (a->flags & ~flags)) return GMA_ERR_INVALID_ARG;
+    if (a->B < 1 || a->N < 1 || a->H < 1 || a->G < 1 || a->d < 1 || a->dv < 1 || a->H % a->G) return GMA_ERR_INVALID_ARG;
+    if (a->dtype != GMA_BF16 && a->dtype != GMA_F32) return GMA_ERR_INVALID_ARG;
+    if (!(a->scale > 0.f) || !(a->scale < 1e30f)) return GMA_ERR_INVALID_ARG;
+    if (a->lengths && a->offsets) return GMA_ERR_INVALID_ARG;
+    if (!blk::opt_ok(a->lengths, 4) || !blk::opt_ok(a->offsets, 4) || !blk::opt_ok(a->lse, 4)) return GMA_ERR_INVALID_ARG;
+    if (a->d > 128 || a->dv > 128 || a->H > 4096 || a->B > 65535) return GMA_ERR_UNSUPPORTED_SHAPE;
+    if ((a->offsets ? 1 : (long long)a->B) * a->N > (1 << 28)) return GMA_ERR_UNSUPPORTED_SHAPE;
+    return GMA_OK;
+}
+
+// Batch rows that the tensors have.
+long long batches(const gma_attn_t &a) { return a.offsets ? 1 : a.B; }
+
+gma_status_t check(const gma_attn_t *a, bool out)
+{
+    gma_status_t r = check_sizes(a, GMA_ATTN_CAUSAL | GMA_ROWS_ZERO_TAIL);
+    if (r != GMA_OK) return r;
+    const long long B = batches(*a), N = a->N;
+    if (!heads_ok(a->q, a->dtype, B, N, a->H, a->d, false) || !heads_ok(a->k, a->dtype, B, N, a->G, a->d, false) ||
+        !heads_ok(a->v, a->dtype, B, N, a->G, a->dv, false) || !heads_ok(a->o, a->dtype, B, N, a->H, a->dv, out))
+        return GMA_ERR_INVALID_ARG;
+    return GMA_OK;
+}
+
+gma_status_t check_grad(const gma_attn_grad_t *g)
+{
+    if (!g) return GMA_ERR_INVALID_ARG;
+    const gma_attn_t &a = g->fwd;
+    gma_status_t r = check(&a, false);
+    if (r != GMA_OK) return r;
+    const long long B = batches(a), N = a.N;
+    if (!a.lse || !heads_ok(g->d_o, a.dtype, B, N, a.H, a.dv, false) || !heads_ok(g->dq, a.dtype, B, N, a.H, a.d, true) ||
+        !heads_ok(g->dk, a.dtype, B, N, a.G, a.d, true) || !heads_ok(g->dv, a.dtype, B, N, a.G, a.dv, true))
+        return GMA_ERR_INVALID_ARG;
+    return GMA_OK;
+}
+
+// `attend`: q and o are used, otherwise k and v.
+gma_status_t check_paged(const gma_attn_paged_t *p, bool attend)
+{
+    if (!p || p->reserved) return GMA_ERR_INVALID_ARG;
+    const gma_attn_t &a = p->attn;
+    gma_status_t r = check_sizes(&a, GMA_ROWS_ZERO_TAIL);
+    if (r != GMA_OK) return r;
+    if (p->pages < 1 || p->page < 1 || p->table_pages < 1 || p->table_stride < 0) return GMA_ERR_INVALID_ARG;
+    if (!blk::ptr_ok(p->table, 4) || !blk::ptr_ok(p->cached, 4)) return GMA_ERR_INVALID_ARG;
+    if (p->page > 65536 || (long long)p->pages * p->page >= (1ll << 40) || (long long)p->table_pages * p->page > (1 << 28))
+        return GMA_ERR_UNSUPPORTED_SHAPE;
+    const long long B = batches(a), N = a.N;
+    if (!heads_ok(p->k_pages, a.dtype, p->pages, p->page, a.G, a.d, !attend) ||
+        !heads_ok(p->v_pages, a.dtype, p->pages, p->page, a.G, a.dv, !attend))
+        return GMA_ERR_INVALID_ARG;
+    if (attend && (!heads_ok(a.q, a.dtype, B, N, a.H, a.d, false) || !heads_ok(a.o, a.dtype, B, N, a.H, a.dv, true)))
+        return GMA_ERR_INVALID_ARG;
+    if (!attend && (!heads_ok(a.k, a.dtype, B, N, a.G, a.d, false) || !heads_ok(a.v, a.dtype, B, N, a.G, a.dv, false)))
+        return GMA_ERR_INVALID_ARG;
+    return GMA_OK;
+}
+
+// Zeros in the rows of an output that no sequence has.
+gma_status_t zero_tail(const gma_attn_t &a, const gma_heads_t &x, int heads, int width, cudaStream_t st)
+{
+    if (!(a.flags & GMA_ROWS_ZERO_TAIL) || (!a.lengths && !a.offsets)) return GMA_OK;
+    const Geo g = geo_of(a, nullptr);
+    const long long rows = batches(a) * a.N;
+    if (a.dtype == GMA_BF16)
+        GMA_LAUNCH(KID_ATTN_TAIL, st, attn_tail_kernel<__nv_bfloat16><<<row_blocks(rows), 256, 0, st>>>(g, heads_of<__nv_bfloat16>(x), heads, width, rows));
+    else
+        GMA_LAUNCH(KID_ATTN_TAIL, st, attn_tail_kernel<float><<<row_blocks(rows), 256, 0, st>>>(g, heads_of<float>(x), heads, width, rows));
+    return GMA_OK;
+}
+
+}  // namespace
+
+Geo geo_of(const gma_attn_t &a, const gma_attn_paged_t *p)
+{
+    Geo g = {};
+    g.B = a.B; g.N = a.N; g.H = a.H; g.G = a.G; g.group = a.H / a.G; g.d = a.d; g.dv = a.dv;
+    g.causal = p || (a.flags & GMA_ATTN_CAUSAL);
+    g.scale = a.scale;
+    g.sl2 = a.scale * LOG2E;
+    g.lengths = a.lengths; g.offsets = a.offsets;
+    if (p) {
+        g.cached = p->cached; g.table = p->table; g.table_stride = p->table_stride;
+        g.table_pages = p->table_pages; g.page = p->page; g.pages = p->pages;
+    }
+    return g;
+}
+
+Plan make_plan(const gma_attn_t &a, bool paged, int pack, int wide_rows, int narrow_rows, int keys, int target, int least, bool split,
+               Carve *ws)
+{
+    Plan p = {};
+    p.pack = pack;
+    p.heads = a.H / pack;
+    p.wide = std::max(wide_rows / pack, 1);
+    p.narrow = std::max(narrow_rows / pack, 1);
+    p.keys = keys;
+    p.target = target;
+    p.least = least;
+    // tiles of n rows and of every sequence's last rows; wide tiles are the fewer
+    const long long n = (long long)a.N * batches(a);
+    long long narrow = n / p.narrow + a.B, wide = n / p.wide + a.B;
+    // narrow ones are taken where the wide ones are fewer than SMS / heads, so that they are at most twice as many and one
+    const long long most = std::max(wide, std::min(narrow, (long long)(wide_rows / narrow_rows + 1) * (SMS / p.heads + 1)));
+    const long long extra = split ? 2ll * target / p.heads + 2 : 0;          // parts beyond the first of each
+    p.max_items = (int)(most + extra);
+    p.max_slots = (int)extra;
+    p.rows = (int)std::min<long long>(p.wide, n) * pack;
+    p.head_at = ws->take(sizeof(PlanHead));
+    p.items_at = ws->take((size_t)p.max_items * sizeof(Item));
+    p.join_at = ws->take((size_t)p.max_slots * p.heads * sizeof(int));
+    p.stat_at = ws->take((size_t)p.max_slots * p.heads * p.rows * 2 * sizeof(float));
+    p.part_at = ws->take((size_t)p.max_slots * p.heads * p.rows * a.dv * sizeof(float));
+    return p;
+}
+
+PlanArgs plan_args(const Geo &g, const Plan &p, void *ws)
+{
+    char *w = (char *)ws;
+    return PlanArgs{g, p.wide, p.narrow, p.keys, p.target, p.least, p.heads, p.max_items, p.max_slots, p.by_keys, (WsHeader *)ws,
+                    (PlanHead *)(w + p.head_at), (Item *)(w + p.items_at), (int *)(w + p.join_at)};
+}
+
+gma_status_t launch_plan(const PlanArgs &a, const PlanArgs *second, cudaStream_t st)
+{
+    GMA_LAUNCH(KID_ATTN_PLAN, st, plan_kernel<<<second ? 2 : 1, PT, 0, st>>>(a, second ? *second : a));
+    return GMA_OK;
+}
+
+gma_status_t launch_delta(const gma_attn_grad_t &g, float *delta, cudaStream_t st)
+{
+    const gma_attn_t &a = g.fwd;
+    const Geo geo = geo_of(a, nullptr);
+    const long long rows = batches(a) * a.H * a.N;
+    const unsigned blocks = row_blocks(rows);
+    if (a.dtype == GMA_BF16)
+        GMA_LAUNCH(KID_ATTN_DELTA, st, launch_pdl(attn_delta_kernel<__nv_bfloat16>, blocks, 256, 0, st, geo, heads_of<const __nv_bfloat16>(a.o),
+                                                  heads_of<const __nv_bfloat16>(g.d_o), delta, rows));
+    else
+        GMA_LAUNCH(KID_ATTN_DELTA, st, launch_pdl(attn_delta_kernel<float>, blocks, 256, 0, st, geo, heads_of<const float>(a.o),
+                                                  heads_of<const float>(g.d_o), delta, rows));
+    return GMA_OK;
+}
+
+}  // namespace att
+}  // namespace gma
+
+using namespace gma;
+using namespace gma::att;
+
+extern "C" {
+
+size_t gma_attn_workspace_size(const gma_attn_t *a)
+{
+    return check(a, true) == GMA_OK ? simt_workspace(*a, nullptr) : 0;
+}
+
+gma_status_t gma_attn_forward(const gma_attn_t *a, void *ws, size_t ws_bytes, gma_stream_t stream)
+{
+    gma_status_t r = check(a, true);
+    if (r != GMA_OK) return r;
+    if (!blk::ws_ok(ws, ws_bytes, gma_attn_workspace_size(a))) return GMA_ERR_WORKSPACE;
+    if ((r = usable_device()) != GMA_OK) return r;
+    cudaStream_t st = (cudaStream_t)stream;
+    if ((r = zero_tail(*a, a->o, a->H, a->dv, st)) != GMA_OK) return r;
+    return simt_forward(*a, nullptr, ws, st);
+}
+
+size_t gma_attn_backward_workspace_size(const gma_attn_grad_t *g)
+{
+    return check_grad(g) == GMA_OK ? simt_backward_workspace(*g) : 0;
+}
+
+gma_status_t gma_attn_backward(const gma_attn_grad_t *g, void *ws, size_t ws_bytes, gma_stream_t stream)
+{
+    gma_status_t r = check_grad(g);
+    if (r != GMA_OK) return r;
+    if (!blk::ws_ok(ws, ws_bytes, gma_attn_backward_workspace_size(g))) return GMA_ERR_WORKSPACE;
+    if ((r = usable_device()) != GMA_OK) return r;
+    cudaStream_t st = (cudaStream_t)stream;
+    const gma_attn_t &a = g->fwd;
+    if ((r = zero_tail(a, g->dq, a.H, a.d, st)) != GMA_OK) return r;
+    if ((r = zero_tail(a, g->dk, a.G, a.d, st)) != GMA_OK) return r;
+    if ((r = zero_tail(a, g->dv, a.G, a.dv, st)) != GMA_OK) return r;
+    return simt_backward(*g, ws, st);
+}
+
+gma_status_t gma_attn_append(const gma_attn_paged_t *p, gma_stream_t stream)
+{
+    gma_status_t r = check_paged(p, false);
+    if (r != GMA_OK) return r;
+    if ((r = usable_device()) != GMA_OK) return r;
+    cudaStream_t st = (cudaStream_t)stream;
+    const gma_attn_t &a = p->attn;
+    const Geo g = geo_of(a, p);
+    const long long rows = batches(a) * a.N * a.G;
+    const int e = 16 / (int)blk::elem_size(a.dtype);
+    const bool vec = a.d % e == 0 && a.dv % e == 0 && heads_vec(a.k, a.dtype) && heads_vec(a.v, a.dtype) && heads_vec(p->k_pages, a.dtype) &&
+                     heads_vec(p->v_pages, a.dtype);
+    auto launch = [&](auto type, auto v) -> gma_status_t {
+        using T = decltype(type);
+        GMA_LAUNCH(KID_ATTN_APPEND, st, attn_append_kernel<T, decltype(v)::value><<<row_blocks(rows), 256, 0, st>>>(
+                                            g, heads_of<const T>(a.k), heads_of<const T>(a.v), heads_of<T>(p->k_pages), heads_of<T>(p->v_pages), rows));
+        return GMA_OK;
+    };
+    if (a.dtype == GMA_BF16)
+        return vec ? launch(__nv_bfloat16(), std::true_type()) : launch(__nv_bfloat16(), std::false_type());
+    return vec ? launch(float(), std::true_type()) : launch(float(), std::false_type());
+}
+
+size_t gma_attn_paged_workspace_size(const gma_attn_paged_t *p)
+{
+    return check_paged(p, true) == GMA_OK ? simt_workspace(p->attn, p) : 0;
+}
+
+gma_status_t gma_attn_paged(const gma_attn_paged_t *p, void *ws, size_t ws_bytes, gma_stream_t stream)
+{
+    gma_status_t r = check_paged(p, true);
+    if (r != GMA_OK) return r;
+    if (!blk::ws_ok(ws, ws_bytes, gma_attn_paged_workspace_size(p))) return GMA_ERR_WORKSPACE;
+    if ((r = usable_device()) != GMA_OK) return r;
+    cudaStream_t st = (cudaStream_t)stream;
+    if ((r = zero_tail(p->attn, p->attn.o, p->attn.H, p->attn.dv, st)) != GMA_OK) return r;
+    return simt_forward(p->attn, p, ws, st);
+}
+
+}  // extern "C"

@@ -71,6 +71,17 @@ const char *kernel_name(int id)
     case KID_SCAN_STATE: return "scan_chunk_state";
     case KID_SCAN_JOIN: return "scan_chunk_join";
     case KID_SCAN_ADJ: return "scan_chunk_adjoint";
+    case KID_ATTN_PLAN: return "attn_plan";
+    case KID_ATTN: return "attn_forward";
+    case KID_ATTN_DKV: return "attn_backward_dkv";
+    case KID_ATTN_DQ: return "attn_backward_dq";
+    case KID_ATTN_SIMT: return "attn_simt_forward";
+    case KID_ATTN_SIMT_DKV: return "attn_simt_backward_dkv";
+    case KID_ATTN_SIMT_DQ: return "attn_simt_backward_dq";
+    case KID_ATTN_DELTA: return "attn_delta";
+    case KID_ATTN_APPEND: return "attn_append";
+    case KID_ATTN_TAIL: return "attn_zero_rows";
+    case KID_ATTN_REPACK: return "attn_repack";
     }
     return "unknown";
 }

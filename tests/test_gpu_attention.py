@@ -1,0 +1,573 @@
+"""Softmax attention on the GPU against the 64-bit reference of attn_ref.py, with the error bounds derived there."""
+import pytest
+import torch
+
+import attn_ref as R
+
+pytestmark = pytest.mark.gpu
+TYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    from linear_latent_routing_gb300 import build
+    build.build()
+    R.DEVICE = "cuda"
+
+
+def A():
+    from linear_latent_routing_gb300 import attention
+    return attention
+
+
+def _draw(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+
+    def normal(*shape, dtype="bf16", std=1.0):
+        return (torch.randn(*shape, generator=g, device="cuda") * std).to(TYPES[dtype])
+    return normal
+
+
+def _ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def _offsets(n, start=0):
+    o = [start]
+    for x in n:
+        o.append(o[-1] + x)
+    return o
+
+
+# ------------------------------------------------------------------ whole sequences
+
+PROMPTS = [  # lengths, H, G, d, dv, dtype, causal, layout
+    ([1], 1, 1, 64, 64, "bf16", True, "packed"),
+    ([1, 2, 0, 3], 4, 2, 64, 64, "bf16", True, "packed"),
+    ([127, 128, 129], 2, 1, 64, 64, "bf16", True, "packed"),
+    ([255, 256, 257, 1], 4, 4, 128, 128, "bf16", True, "packed"),
+    ([700, 31, 0, 385], 6, 2, 128, 64, "bf16", True, "padded"),
+    ([513, 100], 3, 3, 64, 128, "bf16", False, "packed"),
+    ([1300], 4, 1, 32, 64, "bf16", False, "plain"),
+    ([640, 640], 8, 2, 128, 128, "bf16", True, "mixer"),
+    ([300, 77, 260], 5, 1, 48, 24, "bf16", True, "packed"),
+    ([200, 190], 2, 2, 16, 16, "bf16", False, "padded"),
+    ([333, 12], 3, 1, 100, 20, "bf16", True, "packed"),          # rows off 16-byte boundaries
+    ([150, 9], 2, 1, 7, 5, "bf16", True, "padded"),
+    ([270], 2, 1, 117, 117, "bf16", False, "plain"),
+    ([1, 0, 65], 4, 2, 64, 64, "f32", True, "packed"),
+    ([200, 64, 63], 6, 3, 40, 40, "f32", True, "padded"),
+    ([129, 300], 2, 2, 128, 100, "f32", False, "packed"),
+    ([67], 3, 1, 1, 3, "f32", True, "plain"),
+    ([100, 30], 4, 2, 128, 128, "f32", True, "mixer"),
+]
+
+
+def _id(c):
+    return "-".join(str(x) for x in c[1:]) + "-" + "_".join(str(x) for x in c[0])
+
+
+def _prompt(case, seed=0, extra=0):
+    """Tensors of a case, parts of one projection's rows where they are not in the mixers' layout; and a function that
+    gives sequence i's rows of one."""
+    n, H, G, d, dv, dtype, causal, layout = case
+    r = _draw(seed)
+    how = dict(causal=causal, scale=d ** -0.5 * 1.3)
+    if layout == "packed":
+        lead = (sum(n) + extra,)
+        off = _offsets(n, extra // 2)
+        how["offsets"] = _ints(off)
+        rows = lambda t, i: t[off[i]:off[i + 1]]      # noqa: E731
+    else:
+        lead = (len(n), max(n) + extra)
+        if layout in ("padded", "mixer"):
+            how["lengths"] = _ints(n)
+        rows = lambda t, i: t[i, :n[i]]               # noqa: E731
+    if layout == "mixer":
+        q, k, v, do = (r(len(n), h, max(n), w, dtype=dtype).transpose(1, 2) for h, w in ((H, d), (G, d), (G, dv), (H, dv)))
+    else:
+        x = r(*lead, H * d + G * (d + dv), dtype=dtype)
+        q = x[..., :H * d].unflatten(-1, (H, d))
+        k = x[..., H * d:(H + G) * d].unflatten(-1, (G, d))
+        v = x[..., (H + G) * d:].unflatten(-1, (G, dv))
+        do = r(*lead, H, dv, dtype=dtype)
+    return q, k, v, do, how, rows
+
+
+def _stat_rows(lse, rows, i, case):
+    """Sequence i's part of lse, [H, n]."""
+    return rows(lse.transpose(-1, -2), i).transpose(-1, -2)
+
+
+@pytest.mark.parametrize("case", PROMPTS, ids=_id)
+def test_prompt(case):
+    q, k, v, _, how, rows = _prompt(case)
+    lse = A().prompt_lse(q).fill_(float("nan"))
+    o = A().prompt(q, k, v, lse=lse, check=True, **how)
+    for i in range(len(case[0])):
+        want, stat = R.attend(rows(q, i), rows(k, i), rows(v, i), how["scale"], 0, how["causal"], T=TYPES[case[5]])
+        R.check(rows(o, i), want, f"o of sequence {i}")
+        R.check(_stat_rows(lse, rows, i, case), stat, f"lse of sequence {i}")
+
+
+@pytest.mark.parametrize("case", PROMPTS, ids=_id)
+def test_prompt_backward(case):
+    q, k, v, do, how, rows = _prompt(case, 1)
+    lse = A().prompt_lse(q).fill_(float("nan"))
+    o = A().prompt(q, k, v, lse=lse, **how)
+    g = A().prompt_backward(do, q, k, v, o, lse, check=True, **how)
+    for i in range(len(case[0])):
+        want = R.attend(rows(q, i), rows(k, i), rows(v, i), how["scale"], 0, how["causal"], do=rows(do, i), T=TYPES[case[5]])
+        for name, w in zip("qkv", want[2:]):
+            R.check(rows(g[name], i), w, f"d{name} of sequence {i}")
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 20), ("f32", 24)])
+def test_gradients_against_differences(dtype, d):
+    """The gradients against central differences of the forward pass in 64 bits along random directions."""
+    n, H, G = [5, 40], 4, 2
+    case = (n, H, G, d, d, dtype, True, "packed")
+    q, k, v, do, how, rows = _prompt(case, 2)
+    lse = A().prompt_lse(q)
+    o = A().prompt(q, k, v, lse=lse, **how)
+    g = A().prompt_backward(do, q, k, v, o, lse, **how)
+    f64 = [t.double() for t in (q, k, v)]
+
+    def value(x):
+        return sum((R.attend(*(rows(t, i) for t in x), how["scale"], 0, True)[0][0] * rows(do, i).double()).sum() for i in range(2))
+    r = _draw(3)
+    for at, name in enumerate("qkv"):
+        way = r(*f64[at].shape, dtype="f32").double()
+        step = 1e-4
+        moved = [[t + (s * step * way if j == at else 0) for j, t in enumerate(f64)] for s in (1, -1)]
+        slope = (value(moved[0]) - value(moved[1])) / (2 * step)
+        # every element is off by at most what the reference allows, and the differences by their own order
+        allowed = sum((R.attend(*(rows(t, i) for t in (q, k, v)), how["scale"], 0, True, do=rows(do, i), T=TYPES[dtype])[2 + at][1]
+                       * rows(way, i).abs()).sum() for i in range(2))
+        got = (g[name].double() * way).sum()
+        assert (got - slope).abs() <= allowed + 1e-6 * way.norm() ** 2, name
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("layout", ["packed", "padded"])
+def test_rows_of_no_sequence(dtype, layout):
+    """Rows before, behind and between sequences: what lies there (NaN, infinities) touches nothing, the caller's outputs keep
+    their rows there, and outputs allocated by the call are zero."""
+    n = [70, 0, 130]
+    case = (n, 4, 2, 64, 64, dtype, True, layout)
+    q, k, v, do, how, rows = _prompt(case, 4, extra=9)
+    used = torch.zeros(q.shape[:-2], dtype=torch.bool, device="cuda")
+    for i in range(3):
+        rows(used, i).fill_(True)
+    bad = torch.where(torch.arange(64, device="cuda") % 2 == 0, float("nan"), float("inf"))
+    clean = [t.clone() for t in (q, k, v, do)]
+    for t in clean:
+        t[~used] = 0
+    dirty = [t.clone() for t in clean]
+    for t in dirty:
+        t[~used] = bad.to(t.dtype)
+    got = []
+    for q, k, v, do in (clean, dirty):
+        lse = A().prompt_lse(q).fill_(7)
+        o = A().prompt(q, k, v, lse=lse, **how)
+        g = A().prompt_backward(do, q, k, v, o, lse, **how)
+        got.append([o, g["q"], g["k"], g["v"], lse])
+        assert (lse.transpose(-1, -2)[~used] == 7).all()
+        mine = {x: torch.full_like(t, 5) for x, t in zip("oqkv", got[-1])}
+        assert A().prompt(q, k, v, out=mine["o"], **how) is not None
+        A().prompt_backward(do, q, k, v, o, lse, out={x: mine[x] for x in "qkv"}, **how)
+        for x, t in zip("oqkv", got[-1]):
+            assert (t[~used] == 0).all() and (mine[x][~used] == 5).all(), x
+            assert torch.equal(mine[x][used], t[used]), x
+        only = A().prompt_backward(do, q, k, v, o, lse, out={"k": torch.full_like(k, 5)}, **how)
+        assert (only["k"][~used] == 5).all() and (only["q"][~used] == 0).all() and torch.equal(only["q"], g["q"])
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_sequence_that_is_not_finite_touches_no_other(dtype):
+    n = [60, 140, 33]
+    case = (n, 2, 1, 64, 64, dtype, True, "packed")
+    q, k, v, do, how, rows = _prompt(case, 5)
+    got = []
+    for x in (0.0, float("nan")):
+        t = [rows(t, 1) for t in (q, k, v, do)]
+        for y in t:
+            y[::7] = x
+        lse = A().prompt_lse(q)
+        o = A().prompt(q, k, v, lse=lse, **how)
+        g = A().prompt_backward(do, q, k, v, o, lse, **how)
+        got.append([o, g["q"], g["k"], g["v"]])
+    for a, b in zip(*got):
+        for i in (0, 2):
+            assert torch.equal(rows(a, i), rows(b, i))
+
+
+@pytest.mark.parametrize("std", [30.0, 1e-3])
+def test_prompt_large_and_small_scores(std):
+    """Scores of some thousands (one probability is all there is) and scores that are all alike."""
+    n, H, d = [300], 2, 64
+    r = _draw(6)
+    q, k, v, do = (r(300, H, d, std=s) for s in (std, std, 1.0, 1.0))
+    lse = A().prompt_lse(q)
+    o = A().prompt(q, k, v, scale=1.0, lse=lse, check=True)
+    want = R.attend(q, k, v, 1.0, do=do)
+    R.check(o, want[0], "o")
+    R.check(lse, want[1], "lse")
+    g = A().prompt_backward(do, q, k, v, o, lse, scale=1.0)
+    for name, w in zip("qkv", want[2:]):
+        R.check(g[name], w, name)
+
+
+def test_prompt_repeats_bits():
+    case = ([900, 1, 411], 8, 2, 128, 128, "bf16", True, "packed")
+    q, k, v, do, how, _ = _prompt(case, 7)
+    got = []
+    for _ in range(3):
+        lse = A().prompt_lse(q).zero_()
+        o = A().prompt(q, k, v, lse=lse, **how)
+        g = A().prompt_backward(do, q, k, v, o, lse, **how)
+        got.append([o, lse, g["q"], g["k"], g["v"]])
+    for x in got[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(got[0], x))
+
+
+# ------------------------------------------------------------------ a cache of pages
+
+PAGED = [  # new tokens, tokens with them, H, G, d, dv, dtype, page, layout
+    ([1], [1], 1, 1, 64, 64, "bf16", 16, "plain"),
+    ([1, 1, 1], [1, 17, 300], 8, 2, 128, 128, "bf16", 16, "single"),
+    ([1, 1], [5000, 129], 16, 2, 128, 128, "bf16", 64, "single"),
+    ([1], [20001], 4, 4, 64, 64, "bf16", 128, "plain"),
+    ([4, 1, 0, 7], [100, 1, 50, 513], 10, 2, 64, 64, "bf16", 32, "packed"),
+    ([130, 40], [400, 40], 6, 2, 128, 64, "bf16", 256, "padded"),
+    ([300, 700], [900, 700], 4, 1, 128, 128, "bf16", 128, "packed"),
+    ([64], [2500], 16, 4, 64, 128, "bf16", 8, "plain"),
+    ([3, 5], [2, 0], 4, 2, 64, 64, "bf16", 16, "packed"),           # rows that see nothing
+    ([9, 200], [70, 333], 3, 1, 96, 32, "bf16", 24, "packed"),      # a page that is no power of two
+    ([2, 17], [450, 80], 4, 2, 21, 50, "bf16", 16, "padded"),       # rows off 16-byte boundaries
+    ([1, 1], [40, 700], 24, 1, 64, 64, "bf16", 1, "single"),
+    ([1, 1, 1], [3000, 1, 65], 8, 4, 64, 64, "f32", 16, "single"),
+    ([5, 70], [300, 70], 6, 3, 40, 72, "f32", 24, "packed"),
+    ([3], [1], 2, 1, 128, 128, "f32", 64, "plain"),
+]
+
+
+def _paged(case, seed=0):
+    new, total, H, G, d, dv, dtype, page, layout = case
+    r = _draw(seed)
+    B, used = len(new), [-(-t // page) for t in total]
+    pages = sum(used) + 2
+    g = torch.Generator()
+    g.manual_seed(seed)
+    order = torch.randperm(pages, generator=g).tolist()
+    table = torch.full((B, max(max(used), 1) + 1), -7, dtype=torch.int32)
+    at = 0
+    for b in range(B):
+        table[b, :used[b]] = torch.tensor(order[at:at + used[b]], dtype=torch.int32)
+        at += used[b]
+    kp, vp = r(pages, page, G, d, dtype=dtype), r(pages, page, G, dv, dtype=dtype)
+    how = {}
+    if layout == "packed":
+        off = _offsets(new)
+        how["offsets"] = _ints(off)
+        lead = (sum(new),)
+        rows = lambda t, i: t[off[i]:off[i + 1]]                 # noqa: E731
+    elif layout == "single":
+        lead = (B,)
+        rows = lambda t, i: t[i:i + 1]                           # noqa: E731
+    else:
+        lead = (B, max(new))
+        if layout == "padded":
+            how["new_lengths"] = _ints(new)
+        rows = lambda t, i: t[i, :new[i]]                        # noqa: E731
+    q, k, v = r(*lead, H, d, dtype=dtype), r(*lead, G, d, dtype=dtype), r(*lead, G, dv, dtype=dtype)
+    return q, k, v, kp, vp, table.cuda(), _ints(total), how, rows
+
+
+def _cached(pages, table, b, L):
+    """The first L tokens of sequence b; pages that the table does not name are zeros."""
+    page = pages.shape[1]
+    t = table[b, :-(-L // page)].long()
+    good = (t >= 0) & (t < pages.shape[0])
+    x = torch.where(good[:, None, None, None], pages[t.clamp(0, pages.shape[0] - 1)], torch.zeros_like(pages[:1]))
+    return x.flatten(0, 1)[:L]
+
+
+@pytest.mark.parametrize("case", PAGED, ids=lambda c: "-".join(str(x) for x in c[2:]) + "-" + "_".join(str(x) for x in c[1]))
+def test_paged(case):
+    new, total, H, G, d, dv, dtype, page, layout = case
+    q, k, v, kp, vp, table, lengths, how, rows = _paged(case)
+    before = kp.clone(), vp.clone()
+    A().append(k, v, kp, vp, table, lengths, **how)
+    want = [t.clone() for t in before]
+    for b, (n, L) in enumerate(zip(new, total)):
+        for i in range(n):
+            j = L - n + i
+            if j >= 0:
+                for t, x in zip(want, (k, v)):
+                    t[table[b, j // page], j % page] = rows(x, b)[i]
+    assert torch.equal(kp, want[0]) and torch.equal(vp, want[1])
+    lse = torch.full((len(new), H) if layout == "single" else (H, q.shape[0]) if q.dim() == 3 else (len(new), H, max(new)), float("nan"),
+                     device="cuda")
+    o = A().paged(q, kp, vp, table, lengths, lse=lse, check=True, **how)
+    for b, (n, L) in enumerate(zip(new, total)):
+        ref, stat = R.attend(rows(q, b), _cached(kp, table, b, L), _cached(vp, table, b, L), d ** -0.5, L - n, True, T=TYPES[dtype])
+        R.check(rows(o, b), ref, f"o of sequence {b}")
+        mine = lse[b][:, None] if layout == "single" else rows(lse.transpose(-1, -2), b).transpose(-1, -2)
+        R.check(mine, stat, f"lse of sequence {b}")
+
+
+@pytest.mark.parametrize("dtype,page", [("bf16", 32), ("bf16", 24), ("f32", 32)])
+def test_paged_behind_the_end(dtype, page):
+    """What lies in pages behind a sequence's last token (NaN, infinities) touches nothing; rows of no sequence stay as they are."""
+    case = ([3, 40], [75, 170], 4, 2, 64, 64, dtype, page, "padded")
+    q, k, v, kp, vp, table, lengths, how, rows = _paged(case, 1)
+    A().append(k, v, kp, vp, table, lengths, **how)
+    live = torch.zeros(kp.shape[:2], dtype=torch.bool, device="cuda")
+    for b, L in enumerate(case[1]):
+        for j in range(L):
+            live[table[b, j // page], j % page] = True
+    o = A().paged(q, kp, vp, table, lengths, **how)
+    for t in (kp, vp):
+        t[~live] = float("nan")
+    q[0, 3:] = float("inf")
+    out = torch.full_like(o, 3)
+    A().paged(q, kp, vp, table, lengths, out=out, **how)
+    assert (out[0, 3:] == 3).all() and (o[0, 3:] == 0).all()
+    assert torch.equal(out[0, :3], o[0, :3]) and torch.equal(out[1], o[1])
+
+
+@pytest.mark.parametrize("dtype,page,N", [("bf16", 16, 1), ("bf16", 16, 200), ("bf16", 24, 1), ("f32", 16, 2)])
+def test_paged_bad_pages_and_lengths(dtype, page, N):
+    """Table entries outside the cache read as zeros and take no writes; lengths beyond the table are cut, negative ones are 0."""
+    r = _draw(2)
+    B, G, H, d, P = 3, 2, 4, 64, 40
+    q, k, v = r(B, N, H, d, dtype=dtype), r(B, N, G, d, dtype=dtype), r(B, N, G, d, dtype=dtype)
+    kp, vp = r(P, page, G, d, dtype=dtype), r(P, page, G, d, dtype=dtype)
+    table = torch.randperm(P)[:36].view(3, 12).int().cuda()
+    table[0, 3], table[0, 4], table[1, 11] = -1, P, 1 << 30
+    lengths = _ints([12 * page - 5, 10 ** 9, -4])
+    L = [12 * page - 5, 12 * page, 0]
+    before = kp.clone()
+    A().append(k, v, kp, vp, table, lengths)
+    for b in range(3):
+        for i in range(N):
+            j = L[b] - N + i
+            if j >= 0 and 0 <= table[b, j // page] < P:
+                before[table[b, j // page], j % page] = k[b, i]
+    assert torch.equal(before, kp)
+    o = A().paged(q, kp, vp, table, lengths, check=True)
+    for b in range(3):
+        ref, _ = R.attend(q[b], _cached(kp, table, b, L[b]), _cached(vp, table, b, L[b]), d ** -0.5, L[b] - N, True, T=TYPES[dtype])
+        R.check(o[b], ref, f"sequence {b}")
+
+
+def test_paged_pools_with_strides_beyond_32_bits():
+    """A cache whose pages lie more than 2^31 elements apart, keys and values interleaved in one buffer."""
+    G, d, page, far = 2, 64, 16, 1 << 30
+    buffer = torch.zeros(4 * far, dtype=torch.bfloat16, device="cuda")
+    pool = buffer.as_strided((4, page, 2, G, d), (far, 2 * G * d, G * d, d, 1))
+    kp, vp = pool[:, :, 0], pool[:, :, 1]
+    r = _draw(3)
+    kp.copy_(r(4, page, G, d))
+    vp.copy_(r(4, page, G, d))
+    q, k, v = r(1, 2, 4, d), r(1, 2, G, d), r(1, 2, G, d)
+    table = _ints([[3, 0, 2, 1]])
+    lengths = _ints([61])
+    A().append(k, v, kp, vp, table, lengths)
+    o = A().paged(q, kp, vp, table, lengths, check=True)
+    ref, _ = R.attend(q[0], _cached(kp, table, 0, 61), _cached(vp, table, 0, 61), d ** -0.5, 59, True)
+    R.check(o[0], ref, "o")
+    assert torch.equal(_cached(kp, table, 0, 61)[59:], k[0])
+
+
+# ------------------------------------------------------------------ together
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_prompt_in_chunks_and_single_tokens(dtype):
+    """Prompts that go through the cache in chunks and then token by token give what the whole sequences give."""
+    total, chunks, page, H, G, d = [390, 151], [128, 200, 20, 1, 1], 32, 8, 2, 64
+    r = _draw(8)
+    T = max(total)
+    q, k, v = r(2, T, H, d, dtype=dtype), r(2, T, G, d, dtype=dtype), r(2, T, G, d, dtype=dtype)
+    whole, stat = [], []
+    for b in range(2):
+        o, s = R.attend(q[b, :total[b]], k[b, :total[b]], v[b, :total[b]], d ** -0.5, T=TYPES[dtype])
+        whole.append(o)
+    P = sum(-(-t // page) for t in total)
+    kp, vp = (torch.full((P, page, G, d), float("nan"), dtype=TYPES[dtype], device="cuda") for _ in range(2))
+    table = torch.full((2, -(-T // page)), -1, dtype=torch.int32)
+    table[0], table[1, :5] = torch.arange(13)[:table.shape[1]], torch.arange(13, 18)
+    table = table.cuda()
+    done = [0, 0]
+    while done != total:
+        size = chunks[0] if len(chunks) == 1 else chunks.pop(0)
+        new = [min(size, t - x) for t, x in zip(total, done)]
+        pick = lambda t: torch.cat([t[b, done[b]:done[b] + new[b]] for b in range(2)])      # noqa: E731
+        how = dict(offsets=_ints(_offsets(new)))
+        done = [x + y for x, y in zip(done, new)]
+        lengths = _ints(done)
+        before = [x - y for x, y in zip(done, new)]
+        rows = [t for t in (torch.cat([x[b, before[b]:done[b]] for b in range(2)]) for x in (q, k, v))]
+        A().append(rows[1], rows[2], kp, vp, table, lengths, **how)
+        o = A().paged(rows[0], kp, vp, table, lengths, **how)
+        for b, part in enumerate(torch.split(o, new)):
+            R.check(part, tuple(x[before[b]:done[b]] for x in whole[b]), f"sequence {b}, tokens {before[b]} to {done[b]}")
+
+
+def test_a_hybrid_block():
+    """One block around an exact layer: the attention's output through the block's norm, gate and residual, and back."""
+    from linear_latent_routing_gb300 import norm
+    r = _draw(9)
+    B, N, H, d = 2, 150, 4, 64
+    D = H * d
+    x = r(B, N, 4 * D)
+    q, k, v = (x[..., i * D:(i + 1) * D].unflatten(-1, (H, d)) for i in range(3))
+    gate, res = x[..., 3 * D:], r(B, N, D, dtype="f32")
+    w = 1 + 0.1 * r(D, dtype="f32")
+    lse = A().prompt_lse(q)
+    o = A().prompt(q, k, v, lse=lse)
+    heads = o.transpose(1, 2)                                  # the mixers' layout, where the norm reads it
+    rr, _ = norm.block_norm(heads, w, gate=gate, residual=res)
+    leaf = [t.double().detach().requires_grad_() for t in (q, k, v)]
+    score = torch.einsum("bihd,bjhd->bhij", leaf[0], leaf[1]) * d ** -0.5
+    score = score.masked_fill(torch.ones(N, N, device="cuda").triu(1).bool(), float("-inf"))
+    of = torch.einsum("bhij,bjhd->bihd", torch.softmax(score, -1), leaf[2])
+    a = of.reshape(B, N, D) * torch.nn.functional.silu(gate.double())
+    y = res.double() + a / (a.pow(2).mean(-1, keepdim=True) + 1e-6).sqrt() * w.double()
+    dr = r(B, N, D, dtype="f32")
+    y.backward(dr.double())
+    g = norm.block_norm_backward(dr, heads, rr, w, gate=gate, residual=True)
+    grads = A().prompt_backward(g["o"].transpose(1, 2), q, k, v, o, lse)
+    # o, its norm's input and each gradient are rounded to bf16 (2^-8 at most, 2^-9 in the mean), three roundings in a row and p's
+    assert (rr.double() - y).norm() / y.norm() < 4 * 2.0 ** -8
+    for name, t in zip("qkv", leaf):
+        assert (grads[name].double() - t.grad).norm() / t.grad.norm() < 6 * 2.0 ** -8, name
+
+
+def test_streams_and_graphs():
+    """Another stream, and two captured graphs whose replays interleave, give the same bits as eager calls."""
+    case = ([300, 45], 4, 2, 64, 64, "bf16", True, "packed")
+    q, k, v, do, how, _ = _prompt(case, 10)
+
+    def train():
+        lse = A().prompt_lse(q).zero_()
+        o = A().prompt(q, k, v, lse=lse, **how)
+        g = A().prompt_backward(do, q, k, v, o, lse, **how)
+        return [o, lse, g["q"], g["k"], g["v"]]
+    pq, pk, pv, kp, vp, table, lengths, phow, _ = _paged(PAGED[2], 3)
+
+    def serve():
+        A().append(pk, pv, kp, vp, table, lengths, **phow)
+        return [A().paged(pq, kp, vp, table, lengths, **phow)]
+    eager = train() + serve()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    other = A().prompt(q, k, v, stream=s, **how)
+    paged = A().paged(pq, kp, vp, table, lengths, stream=s, **phow)
+    s.synchronize()
+    assert torch.equal(other, eager[0]) and torch.equal(paged, eager[-1])
+    graphs, outs = [], []
+    for f in (train, serve, train):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(f())
+        graphs.append(g)
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(outs[0] + outs[1], eager):
+        assert torch.equal(a, b)
+    for a, b in zip(outs[2], eager):
+        assert torch.equal(a, b)
+
+
+def test_more_sequences_than_blocks():
+    """Many short sequences, packed: more tiles than the GPU has SMs, and sequences without tokens between them."""
+    n = [(7 * i) % 19 for i in range(1500)]
+    case = (n, 2, 1, 64, 64, "bf16", True, "packed")
+    q, k, v, do, how, rows = _prompt(case, 11)
+    lse = A().prompt_lse(q)
+    o = A().prompt(q, k, v, lse=lse, **how)
+    g = A().prompt_backward(do, q, k, v, o, lse, **how)
+    for i in list(range(0, 1500, 97)) + [1499]:
+        want = R.attend(rows(q, i), rows(k, i), rows(v, i), how["scale"], 0, True, do=rows(do, i))
+        R.check(rows(o, i), want[0], f"o of sequence {i}")
+        for name, w in zip("qkv", want[2:]):
+            R.check(rows(g[name], i), w, f"d{name} of sequence {i}")
+
+
+def test_offsets_that_fall_or_reach_out():
+    """Offsets outside the tensors are cut, falling ones make empty sequences; nothing outside the tensors is touched."""
+    r = _draw(12)
+    q, k, v = r(100, 2, 64), r(100, 1, 64), r(100, 1, 64)
+    o = A().prompt(q, k, v, offsets=_ints([-5, 40, 30, 900]), check=True)
+    # rows 30 to 39 are two sequences': either may have written them last
+    whole = R.attend(q[:40], k[:40], v[:40], 64 ** -0.5)[0]
+    R.check(o[:30], tuple(x[:30] for x in whole), "first")
+    last = R.attend(q[30:], k[30:], v[30:], 64 ** -0.5)[0]
+    R.check(o[40:], tuple(x[10:] for x in last), "last")
+
+
+def test_refusals():
+    from linear_latent_routing_gb300 import gma
+    a, r = A(), _draw(13)
+    q, k, v = r(2, 10, 4, 64), r(2, 10, 2, 64), r(2, 10, 2, 64)
+    lse = a.prompt_lse(q)
+    o = a.prompt(q, k, v, lse=lse)
+    with pytest.raises(TypeError):
+        a.prompt(q.cpu(), k, v)
+    with pytest.raises(TypeError):
+        a.prompt(q.half(), k.half(), v.half())
+    with pytest.raises(TypeError):
+        a.prompt(q, k.float(), v)
+    with pytest.raises(ValueError):
+        a.prompt(q, k[:, :9], v)
+    with pytest.raises(ValueError):
+        a.prompt(q, k, v, lengths=_ints([1, 2]), offsets=_ints([0, 5]))
+    with pytest.raises(ValueError):
+        a.prompt(q, k, v, offsets=_ints([0, 5, 10]))
+    with pytest.raises(ValueError):
+        a.prompt(q, k, v, lengths=_ints([1, 2, 3]))
+    with pytest.raises(ValueError):
+        a.prompt(q, k, v, out=q)
+    with pytest.raises(ValueError):
+        a.prompt(q.transpose(2, 3), k, v)
+    with pytest.raises(gma.GmaError):
+        a.prompt(q, k, v, scale=0.0)
+    with pytest.raises(gma.GmaError):
+        a.prompt(q, k, v, scale=float("nan"))
+    with pytest.raises(gma.GmaError):
+        a.prompt(r(2, 10, 4, 160), r(2, 10, 2, 160), v)
+    with pytest.raises(gma.GmaError):
+        a.prompt(q, r(2, 10, 3, 64), r(2, 10, 3, 64))
+    with pytest.raises(gma.GmaError):
+        a.prompt(q[:, :0], k[:, :0], v[:, :0])
+    with pytest.raises(gma.GmaError):
+        a.prompt(q, k, v, out=torch.empty(1, 10, 4, 64, dtype=q.dtype, device="cuda").expand(2, 10, 4, 64))
+    with pytest.raises(TypeError):
+        a.prompt_backward(o, q, k, v, o, None)
+    with pytest.raises(ValueError):
+        a.prompt_backward(o, q, k, v, o, lse, out={"x": q})
+    with pytest.raises(ValueError):
+        a.prompt_backward(o, q, k, v, o, lse, out={"q": q})
+    kp, vp, table, n = r(4, 16, 2, 64), r(4, 16, 2, 64), _ints([[0, 1], [2, 3]]), _ints([12, 30])
+    with pytest.raises(ValueError):
+        a.append(k, v, kp, kp, table, n)
+    with pytest.raises(ValueError):
+        a.append(k, v, kp, vp, table[:1], n)
+    with pytest.raises(TypeError):
+        a.append(k, v, kp, vp, table.long(), n)
+    with pytest.raises(TypeError):
+        a.paged(q, kp, vp, table, None)
+    with pytest.raises(ValueError):
+        a.paged(q, kp, vp, table, n, offsets=_ints([0, 2]))
+    with pytest.raises(ValueError):
+        a.paged(q, kp[:3], vp, table, n)
+    with pytest.raises(ValueError):
+        a.paged(q, kp, vp, table, n, out=q)
