@@ -1,0 +1,98 @@
+// attn_tc.cuh -- what the tensor-core attention kernels share: operand tiles of 128 rows in shared memory, their TMA loads and
+// descriptors, and rows of tensor memory.
+//
+// A tile is 128 rows of up to 128 bf16 elements: one or two boxes of 64 columns (128 bytes a row, 128-byte swizzle), 16 KB
+// each, columns behind the width and rows behind the tensor zero.  The same tile serves as a K-major operand (products over the
+// width) and as an MN-major one (products over the rows).
+#pragma once
+
+#include <cuda.h>
+
+#include "attn_common.cuh"
+#include "tc_ptx.cuh"
+
+namespace gma {
+namespace att {
+
+using namespace tc;
+typedef __nv_bfloat16 bf16;
+
+constexpr int TILE = 128;
+constexpr uint32_t BOX = TILE * 128;          // bytes of 64 columns of a tile
+constexpr uint32_t SMEM_MAX = 232448;         // 227 KB
+
+// k-step s (16 columns) of a K-major tile, and k-step s (16 rows) of an MN-major one.
+__device__ __forceinline__ uint64_t k_desc(uint32_t base, int s)
+{
+    return smem_desc(base + (uint32_t)((s >> 2) * BOX + (s & 3) * 32), 16, 1024, SW_128B);
+}
+__device__ __forceinline__ uint64_t mn_desc(uint32_t base, int s)
+{
+    return smem_desc(base + (uint32_t)(s * 16 * 128), BOX, 1024, SW_128B);
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, uint64_t *bar, int x, int y, int z, int w)
+{
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+                 "l"((uint64_t)map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+                 : "memory");
+}
+
+// Zeros in rows `from` to 127 of a tile's boxes, by one warp; the tensor cores see them after the fence.
+__device__ __forceinline__ void zero_rows(uint8_t *tile, int boxes, int from)
+{
+    const int lane = threadIdx.x & 31;
+    for (int b = 0; b < boxes; ++b)
+        for (int i = from * 8 + lane; i < TILE * 8; i += 32)
+            *reinterpret_cast<uint4 *>(tile + b * BOX + i * 16) = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+    __syncwarp();
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+template <int N> __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// Columns [0, width) of this warp's lanes at `tl`, times f, as a row of bf16 (one row a thread; `valid`: it is there).
+__device__ __forceinline__ void store_row(uint32_t tl, int width, float f, bool valid, bf16 *row, bool vec)
+{
+#pragma unroll 1
+    for (int c = 0; c < width; c += 32) {
+        uint32_t r[32];
+        tmem_ld32(tl + c, r);
+        tmem_ld_wait();
+        if (!valid) continue;
+        if (vec) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (c + 8 * q < width) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        w[e] = pack_bf16(__uint_as_float(r[8 * q + 2 * e]) * f, __uint_as_float(r[8 * q + 2 * e + 1]) * f);
+                    *reinterpret_cast<uint4 *>(row + c + 8 * q) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                if (c + e < width) row[c + e] = __float2bfloat16_rn(__uint_as_float(r[e]) * f);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ host side
+// Whether TMA can read these heads: bf16, 16-byte aligned strides that step.
+bool tma_heads(const gma_heads_t &r, long long B, long long N, long long heads);
+// Boxes of 64 columns x bh heads x bt tokens.
+bool heads_map(CUtensorMap *m, const gma_heads_t &r, long long B, long long N, long long heads, int width, int bh, int bt);
+// Whether rows of `width` can be stored 16 bytes at a time.
+bool store_vec(const gma_heads_t &r, int width);
+
+}  // namespace att
+}  // namespace gma

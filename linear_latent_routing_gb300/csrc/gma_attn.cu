@@ -3,6 +3,7 @@
 #include <algorithm>
 
 #include "attn_common.cuh"
+#include "attn_tc_host.cuh"
 
 namespace gma {
 namespace att {
@@ -308,8 +309,8 @@ Plan make_plan(const gma_attn_t &a, bool paged, int pack, int wide_rows, int nar
     Plan p = {};
     p.pack = pack;
     p.heads = a.H / pack;
-    p.wide = std::max(wide_rows / pack, 1);
     p.narrow = std::max(narrow_rows / pack, 1);
+    p.wide = p.narrow * (wide_rows / narrow_rows);
     p.keys = keys;
     p.target = target;
     p.least = least;
@@ -368,7 +369,7 @@ extern "C" {
 
 size_t gma_attn_workspace_size(const gma_attn_t *a)
 {
-    return check(a, true) == GMA_OK ? simt_workspace(*a, nullptr) : 0;
+    return check(a, true) != GMA_OK ? 0 : tc_takes(*a, nullptr) ? tc_workspace(*a, nullptr) : simt_workspace(*a, nullptr);
 }
 
 gma_status_t gma_attn_forward(const gma_attn_t *a, void *ws, size_t ws_bytes, gma_stream_t stream)
@@ -379,7 +380,7 @@ gma_status_t gma_attn_forward(const gma_attn_t *a, void *ws, size_t ws_bytes, gm
     if ((r = usable_device()) != GMA_OK) return r;
     cudaStream_t st = (cudaStream_t)stream;
     if ((r = zero_tail(*a, a->o, a->H, a->dv, st)) != GMA_OK) return r;
-    return simt_forward(*a, nullptr, ws, st);
+    return tc_takes(*a, nullptr) ? tc_forward(*a, nullptr, ws, st) : simt_forward(*a, nullptr, ws, st);
 }
 
 size_t gma_attn_backward_workspace_size(const gma_attn_grad_t *g)
@@ -426,7 +427,7 @@ gma_status_t gma_attn_append(const gma_attn_paged_t *p, gma_stream_t stream)
 
 size_t gma_attn_paged_workspace_size(const gma_attn_paged_t *p)
 {
-    return check_paged(p, true) == GMA_OK ? simt_workspace(p->attn, p) : 0;
+    return check_paged(p, true) != GMA_OK ? 0 : tc_takes(p->attn, p) ? tc_workspace(p->attn, p) : simt_workspace(p->attn, p);
 }
 
 gma_status_t gma_attn_paged(const gma_attn_paged_t *p, void *ws, size_t ws_bytes, gma_stream_t stream)
@@ -437,7 +438,7 @@ gma_status_t gma_attn_paged(const gma_attn_paged_t *p, void *ws, size_t ws_bytes
     if ((r = usable_device()) != GMA_OK) return r;
     cudaStream_t st = (cudaStream_t)stream;
     if ((r = zero_tail(p->attn, p->attn.o, p->attn.H, p->attn.dv, st)) != GMA_OK) return r;
-    return simt_forward(p->attn, p, ws, st);
+    return tc_takes(p->attn, p) ? tc_forward(p->attn, p, ws, st) : simt_forward(p->attn, p, ws, st);
 }
 
 }  // extern "C"

@@ -1,0 +1,507 @@
+// gma_attn_tc.cu -- softmax attention on the tensor cores (tcgen05), bf16: whole sequences, and new tokens over a cache of pages.
+//
+// A block runs two streams of 128 query rows against key tiles of 128, each with its scores and its output in tensor
+// memory (S0 S1 O0 O1, 512 columns): while one stream's warps take exponentials the tensor cores work for the other.
+// An item of more than 128 rows gives each stream its own rows, and both read every key tile; an item of fewer (few new
+// tokens) gives both the same rows and each every other key tile, and their results are joined in shared memory at the end.
+// Keys and values pass through one ring of tiles.  P, rounded to bf16 (half a step, 2^-8 relative, which leaves the result's
+// own rounding as large; its sum is taken before that, in fp32), replaces S in tensor memory as the second product's
+// first operand.  The maximum that the exponentials are relative to is moved only when it would grow by more than 2^8, so that
+// the output is rarely rescaled: fp32 sums do not mind the factor, and bf16 holds p at any scale.
+//
+// Warps: 0-3 and 4-7 the streams (a thread a row), 8 issues the products, 9 loads.
+#include "attn_tc.cuh"
+#include "attn_tc_host.cuh"
+
+namespace gma {
+
+namespace tck {
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                                  const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                                  CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_fn();
+}  // namespace tck
+
+namespace att {
+namespace {
+
+constexpr int THREADS = 384;
+constexpr int MAX_SLOTS = 10;
+constexpr float GROW = 8.f;                  // by so much (in powers of two) the maximum may lag
+
+struct TcArgs {
+    Geo g;
+    Heads<bf16> o;
+    float *lse;
+    int pack, heads;           // query heads in a row tile, heads of the grid
+    int o_vec;
+    const PlanHead *head;
+    const Item *items;
+    Parts parts;
+    WsHeader *hdr;
+    int q_boxes, v_boxes;      // boxes of 64 columns of q and k, of v
+    uint32_t slot_bytes;
+    int slots;
+    int page_rows, tile_pages; // rows of a page's box, such boxes in a tile
+};
+
+// shared memory: query tiles, the ring, the barriers
+struct Bars {
+    uint64_t q, full[MAX_SLOTS], empty[MAX_SLOTS], s[2], p[2], o[2], drain;
+    uint32_t tmem;
+    int abort, flag;
+    float merge[TILE][2];
+};
+
+template <bool PAGED>
+__global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const TcArgs a, const __grid_constant__ CUtensorMap qmap,
+                                                             const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap)
+{
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    const uint32_t q_tile = (uint32_t)a.q_boxes * BOX;
+    uint8_t *ring = smem + 2 * q_tile;
+    Bars *bars = reinterpret_cast<Bars *>(ring + (size_t)a.slots * a.slot_bytes);
+    volatile int *abort = &bars->abort;
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    if (t == 256) {
+        mbar_init(&bars->q, 1);
+        for (int i = 0; i < a.slots; ++i) {
+            mbar_init(&bars->full[i], 1);
+            mbar_init(&bars->empty[i], 1);
+        }
+        for (int w = 0; w < 2; ++w) {
+            mbar_init(&bars->s[w], 1);
+            mbar_init(&bars->p[w], TILE);
+            mbar_init(&bars->o[w], 1);
+        }
+        mbar_init(&bars->drain, 1);
+        bars->abort = 0;
+        fence_mbar_init();
+    }
+    blk::wait_previous();
+    const int rank = blockIdx.x / a.heads, head = blockIdx.x % a.heads;
+    if (rank >= a.head->items) return;
+    if (warp == 8) tmem_alloc(&bars->tmem, 512);
+    const Geo &g = a.g;
+    const Item it = a.items[rank];
+    const Seq sq = sequence(g, it.seq);
+    const int pack = a.pack, per = TILE / pack;                  // tokens of a row tile
+    const int tokens = min(a.head->tokens, sq.n - it.tok0);
+    const bool two = tokens > per;                               // each stream has its own rows
+    const int kvh = pack == 1 ? head / g.group : head;
+    // key tiles: [t0, t1), of which stream 0 with rows of its own sees those before e0
+    const int t0 = it.t0;
+    const int t1 = min(it.t1, (sq.seen(g, it.tok0 + tokens - 1) + TILE - 1) / TILE);
+    const int e0 = two ? min(t1, (sq.seen(g, it.tok0 + per - 1) + TILE - 1) / TILE) : t1;
+    const int step = two ? 1 : 2;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem;
+    const uint32_t sb = smem_u32(smem), rb = smem_u32(ring);
+
+    if (warp >= 8) {
+        if (warp == 8) {
+            // ============================================================ products
+            const uint32_t id_s = idesc_f16(TILE, TILE, 1, 1, 0, 0), id_o = idesc_f16(TILE, (uint32_t)(g.dv + 15) & ~15u, 1, 1, 0, 1);
+            const int ksteps = (g.d + 15) >> 4;
+            bool ok = t1 > t0 && mbar_wait_abortable(&bars->q, 0, a.hdr, 200, abort);
+            int done[2] = {0, 0};
+            auto slot = [&](int c) { return c % a.slots; };
+            auto loaded = [&](int c) { return mbar_wait_abortable(&bars->full[slot(c)], (uint32_t)(c / a.slots) & 1u, a.hdr, 201, abort); };
+            auto release = [&](int c) { if (lane == 0) mma_commit(&bars->empty[slot(c)]); };
+            // S_w = Q_w K_t^T
+            auto scores = [&](int w, int kt) {
+                if (lane == 0) {
+                    const uint32_t q = sb + (two ? w * q_tile : 0u), k = rb + (uint32_t)slot(2 * (kt - t0)) * a.slot_bytes;
+                    for (int s = 0; s < ksteps; ++s) mma_f16(tmem + w * TILE, k_desc(q, s), k_desc(k, s), id_s, s > 0);
+                    mma_commit(&bars->s[w]);
+                }
+            };
+            // O_w += P_w V_t
+            auto output = [&](int w, int kt) {
+                if (lane == 0) {
+                    const uint32_t v = rb + (uint32_t)slot(2 * (kt - t0) + 1) * a.slot_bytes;
+#pragma unroll
+                    for (int s = 0; s < TILE / 16; ++s)
+                        mma_f16_tmem_a(tmem + 256 + w * TILE, tmem + w * TILE + 8 * s, mn_desc(v, s), id_o, done[w] > 0 || s > 0);
+                }
+                ++done[w];
+            };
+            if (ok && (ok = loaded(0))) {
+                if (t0 < e0) scores(0, t0);
+                if (two) scores(1, t0);
+                release(0);
+                if (!two && t0 + 1 < t1 && (ok = loaded(2))) {
+                    scores(1, t0 + 1);
+                    release(2);
+                }
+            }
+            for (int kt = t0; ok && kt < t1; ++kt) {
+                const int cv = 2 * (kt - t0) + 1;
+                if (!(ok = loaded(cv))) break;
+                const int have = sq.L - kt * TILE;
+                // values behind the sequence's end meet probabilities of zero, and may be anything
+                if (have < TILE) zero_rows(ring + (size_t)slot(cv) * a.slot_bytes, a.v_boxes, have);
+                const int next = kt + step;
+                for (int w = two ? 0 : (kt - t0) & 1; ok && w < 2; ++w) {
+                    if (two && w == 0 && kt >= e0) continue;
+                    if (!(ok = mbar_wait_abortable(&bars->p[w], done[w] & 1, a.hdr, 202, abort))) break;
+                    tc_fence_after();
+                    output(w, kt);
+                    const bool last_user = !two || w == 1;
+                    if (last_user) release(cv);
+                    if (next < (two && w == 0 ? e0 : t1)) {
+                        if (!(ok = loaded(cv - 1 + 2 * step))) break;
+                        scores(w, next);
+                        if (last_user) release(cv - 1 + 2 * step);
+                    } else if (lane == 0) {
+                        mma_commit(&bars->o[w]);
+                    }
+                    if (!two) break;
+                }
+            }
+            // after a wait that gave up: products in flight end before their operands and results go
+            if (*abort) {
+                if (lane == 0) mma_commit(&bars->drain);
+                mbar_wait(&bars->drain, 0, a.hdr, 209);
+            }
+        } else if (warp == 9) {
+            // ============================================================ loads
+            bool ok = t1 > t0;
+            int issued = 0;
+            if (ok) {
+                if (lane == 0) {
+                    const uint32_t box = (uint32_t)(per * pack) * 128u;
+                    const int tiles = two ? 2 : 1;
+                    mbar_arrive_expect_tx(&bars->q, box * tiles * a.q_boxes);
+                    for (int w = 0; w < tiles; ++w)
+                        for (int b = 0; b < a.q_boxes; ++b)
+                            tma_load_4d(sb + w * q_tile + b * BOX, &qmap, &bars->q, 64 * b, head * pack, sq.row0 + it.tok0 + w * per, sq.b);
+                }
+                int entry = 0;
+                // the page of this lane's box of a tile
+                auto page_entry = [&](int kt) {
+                    const int j = kt * TILE + lane * a.page_rows;
+                    if (lane >= a.tile_pages || j >= sq.L) return 0;
+                    return g.table[(long long)it.seq * g.table_stride + j / g.page];
+                };
+                if (PAGED) entry = page_entry(t0);
+                for (int kt = t0; ok && kt < t1; ++kt) {
+                    const int have = min(sq.L - kt * TILE, TILE), boxes = PAGED ? (have + a.page_rows - 1) / a.page_rows : 1;
+                    const int in_page = PAGED ? kt * TILE % g.page : 0;
+                    const int ahead = PAGED && kt + 1 < t1 ? page_entry(kt + 1) : 0;
+                    for (int half = 0; half < 2; ++half) {
+                        const int c = 2 * (kt - t0) + half, s = c % a.slots;
+                        if (!(ok = mbar_wait_abortable(&bars->empty[s], ((uint32_t)(c / a.slots) & 1u) ^ 1u, a.hdr, 203, abort))) break;
+                        const uint32_t dst = rb + (uint32_t)s * a.slot_bytes;
+                        const int nb = half ? a.v_boxes : a.q_boxes;
+                        const CUtensorMap *map = half ? &vmap : &kmap;
+                        if (lane == 0)
+                            mbar_arrive_expect_tx(&bars->full[s], PAGED ? (uint32_t)(boxes * a.page_rows * 128 * nb) : BOX * nb);
+                        __syncwarp();
+                        if (PAGED) {
+                            // an entry that names no page: a coordinate behind the pool, which reads as zeros
+                            const int page = entry >= 0 && entry < g.pages ? entry : g.pages;
+                            if (lane < boxes)
+                                for (int b = 0; b < nb; ++b)
+                                    tma_load_4d(dst + b * BOX + lane * a.page_rows * 128, map, &bars->full[s], 64 * b, kvh, in_page, page);
+                        } else if (lane == 0) {
+                            for (int b = 0; b < nb; ++b) tma_load_4d(dst + b * BOX, map, &bars->full[s], 64 * b, kvh, sq.row0 + kt * TILE, sq.b);
+                        }
+                        issued = c + 1;
+                    }
+                    entry = ahead;
+                }
+                // loads that no product waited for (another wait gave up) end before the block does
+                if (*abort) {
+                    mbar_wait(&bars->q, 0, a.hdr, 204);
+                    for (int c = issued > a.slots ? issued - a.slots : 0; c < issued; ++c)
+                        mbar_wait(&bars->full[c % a.slots], (uint32_t)(c / a.slots) & 1u, a.hdr, 205);
+                }
+            }
+        }
+    } else {
+        // ================================================================ a stream's rows
+        const int w = warp >> 2, row = t & (TILE - 1);
+        const int first = it.tok0 + (two ? w * per : 0), tok = first + row / pack;
+        const bool valid = row < per * pack && tok < it.tok0 + tokens;
+        const bool busy = __any_sync(~0u, valid);
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + lanes + w * TILE, to = tmem + lanes + 256 + w * TILE;
+        const int seen = valid ? sq.seen(g, tok) : sq.L;
+        const int begin = two ? t0 : t0 + w, end = two && w == 0 ? e0 : t1;
+        float m = -INFINITY;
+        blk::f2 l2 = blk::pack2(0.f, 0.f), l3 = l2;
+        bool ok = true;
+        int n = 0;
+        for (int kt = begin; kt < end; kt += step, ++n) {
+            if (!(ok = mbar_wait_abortable(&bars->s[w], n & 1, a.hdr, 206, abort))) break;
+            tc_fence_after();
+            if (busy) {
+                uint32_t r[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, r[c]);
+                tmem_ld_wait();
+                const int lim = seen - kt * TILE;
+                if (__any_sync(~0u, lim < TILE)) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (32 * c + e >= lim) r[c][e] = 0xff800000u;
+                }
+                float x[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    x[c] = __uint_as_float(r[c][0]);
+#pragma unroll
+                    for (int e = 1; e < 32; ++e) x[c] = fmaxf(x[c], __uint_as_float(r[c][e]));
+                }
+                const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * g.sl2;
+                if (__any_sync(~0u, top > m + GROW)) {
+                    const float now = fmaxf(m, top), f = now == -INFINITY ? 1.f : ex2(m - now);
+                    m = now;
+                    const blk::f2 ff = blk::pack2(f, f);
+                    l2 = blk::mul2(l2, ff);
+                    l3 = blk::mul2(l3, ff);
+                    if (n) {
+#pragma unroll 1
+                        for (int c = 0; c < g.dv; c += 32) {
+                            uint32_t v[32];
+                            tmem_ld32(to + c, v);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
+                            tmem_st16(to + c, *reinterpret_cast<uint32_t(*)[16]>(v));
+                            tmem_st16(to + c + 16, *reinterpret_cast<uint32_t(*)[16]>(v + 16));
+                        }
+                    }
+                }
+                const float base = m == -INFINITY ? 0.f : -m;
+                const blk::f2 scale = blk::pack2(g.sl2, g.sl2), shift = blk::pack2(base, base);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t p[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const blk::f2 y = blk::ex2_2(
+                            blk::fma2(blk::pack2(__uint_as_float(r[c][2 * e]), __uint_as_float(r[c][2 * e + 1])), scale, shift));
+                        if (e & 1) l3 = blk::add2(l3, y); else l2 = blk::add2(l2, y);
+                        const float2 z = blk::unpack2(y);
+                        p[e] = pack_bf16(z.x, z.y);
+                    }
+                    tmem_st16(ts + 16 * c, p);
+                }
+                tmem_st_wait();
+            }
+            tc_fence_before();
+            mbar_arrive(&bars->p[w]);
+        }
+        const float2 la = blk::unpack2(blk::add2(l2, l3));
+        float l = la.x + la.y;
+        if (n && ok) ok = mbar_wait_abortable(&bars->o[w], 0, a.hdr, 207, abort);
+        // the ring takes stream 1's result: both streams' last products have read it
+        if (!two && w == 1 && n && ok) ok = mbar_wait_abortable(&bars->o[0], 0, a.hdr, 208, abort);
+        tc_fence_after();
+        bool store = two || w == 0;
+        float mine = 1.f;                          // factor of this stream's sums
+        bool other = false;
+        float theirs = 0.f;
+        float *mo = reinterpret_cast<float *>(smem + 2 * q_tile);       // [dv / 4][128 rows][4]: the ring is empty by now
+        if (!two && t1 - t0 > 1) {
+            if (w == 1 && busy) {
+                bars->merge[row][0] = m;
+                bars->merge[row][1] = l;
+#pragma unroll 1
+                for (int c = 0; c < g.dv; c += 32) {
+                    uint32_t v[32];
+                    tmem_ld32(to + c, v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        *reinterpret_cast<uint4 *>(mo + ((c / 4 + q) * TILE + row) * 4) = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                }
+            }
+            named_bar_sync(1, 256);
+            if (w == 0 && busy) {
+                const float m1 = bars->merge[row][0], l1 = bars->merge[row][1], now = fmaxf(m, m1);
+                mine = now == -INFINITY ? 0.f : ex2(m - now);
+                theirs = now == -INFINITY ? 0.f : ex2(m1 - now);
+                l = l * mine + l1 * theirs;
+                m = now;
+                other = true;
+            }
+        }
+        if (store && busy && ok) {
+            const int h = pack == 1 ? head : head * pack + row % pack;
+            const int item_row = (two ? w * per * pack : 0) + row;
+            const bool whole = it.parts == 1;
+            const float inv = l > 0.f ? 1.f / l : 0.f, f = whole ? inv : 1.f;
+            if (l == 0.f) mine = theirs = 0.f;
+            bf16 *out = a.o.at(sq.b, sq.row0 + (valid ? tok : it.tok0), h);
+            float *part = whole ? nullptr : a.parts.o_at(it.slot + it.part, head, valid ? item_row : 0);
+            if (valid) {
+                if (whole) {
+                    if (a.lse) a.lse[stat_at(g, sq, h, tok)] = l > 0.f ? (m + log2f(l)) * LN2 : -INFINITY;
+                } else {
+                    float *st = a.parts.stat_at(it.slot + it.part, head, item_row);
+                    st[0] = l > 0.f ? m : -INFINITY;
+                    st[1] = l;
+                }
+            }
+#pragma unroll 1
+            for (int c = 0; c < g.dv; c += 32) {
+                uint32_t v[32];
+                float y[32];
+                if (n) {
+                    tmem_ld32(to + c, v);
+                    tmem_ld_wait();
+                }
+#pragma unroll
+                for (int e = 0; e < 32; ++e) y[e] = l > 0.f && n ? __uint_as_float(v[e]) * mine : 0.f;
+                if (other && theirs != 0.f) {
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const float4 z = *reinterpret_cast<const float4 *>(mo + ((c / 4 + q) * TILE + row) * 4);
+                        y[4 * q] = fmaf(z.x, theirs, y[4 * q]);
+                        y[4 * q + 1] = fmaf(z.y, theirs, y[4 * q + 1]);
+                        y[4 * q + 2] = fmaf(z.z, theirs, y[4 * q + 2]);
+                        y[4 * q + 3] = fmaf(z.w, theirs, y[4 * q + 3]);
+                    }
+                }
+                if (!valid) continue;
+                if (!whole) {
+                    if (g.dv % 4 == 0) {
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            if (c + 4 * q < g.dv) *reinterpret_cast<float4 *>(part + c + 4 * q) = make_float4(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (c + e < g.dv) part[c + e] = y[e];
+                    }
+                } else if (a.o_vec) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (c + 8 * q < g.dv)
+                            *reinterpret_cast<uint4 *>(out + c + 8 * q) =
+                                make_uint4(pack_bf16(y[8 * q] * f, y[8 * q + 1] * f), pack_bf16(y[8 * q + 2] * f, y[8 * q + 3] * f),
+                                           pack_bf16(y[8 * q + 4] * f, y[8 * q + 5] * f), pack_bf16(y[8 * q + 6] * f, y[8 * q + 7] * f));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (c + e < g.dv) out[c + e] = __float2bfloat16_rn(y[e] * f);
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    if (it.parts > 1 && last_part(a.parts, it, head, &bars->flag)) {
+        const int rows = tokens * pack;
+        for (int r = warp; r < rows; r += THREADS / 32) {
+            const int h = pack == 1 ? head : head * pack + r % pack, tok = it.tok0 + r / pack;
+            join_row<bf16>(a.parts, it, head, r, a.o.at(sq.b, sq.row0 + tok, h), a.lse ? a.lse + stat_at(g, sq, h, tok) : nullptr);
+        }
+    }
+    __syncthreads();
+    if (warp == 8) tmem_dealloc(tmem, 512);
+}
+
+}  // namespace
+
+// ------------------------------------------------------------------ host side
+bool tma_heads(const gma_heads_t &r, long long B, long long N, long long heads)
+{
+    auto fits = [](long long size, long long stride) { return size <= 1 || (stride > 0 && stride % 8 == 0 && stride < (1ll << 38)); };
+    return ((uintptr_t)r.ptr & 15u) == 0 && fits(heads, r.head) && fits(N, r.token) && fits(B, r.batch);
+}
+
+bool heads_map(CUtensorMap *m, const gma_heads_t &r, long long B, long long N, long long heads, int width, int bh, int bt)
+{
+    const tck::EncodeTiledFn fn = tck::encode_fn();
+    if (!fn) return false;
+    auto bytes = [](long long size, long long stride) { return (cuuint64_t)(size > 1 ? stride * 2 : 16); };
+    const cuuint64_t dims[4] = {(cuuint64_t)width, (cuuint64_t)heads, (cuuint64_t)N, (cuuint64_t)B};
+    const cuuint64_t strides[3] = {bytes(heads, r.head), bytes(N, r.token), bytes(B, r.batch)};
+    const cuuint32_t box[4] = {64, (cuuint32_t)bh, (cuuint32_t)bt, 1}, es[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, r.ptr, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool store_vec(const gma_heads_t &r, int width)
+{
+    return width % 8 == 0 && (((uintptr_t)r.ptr | (uintptr_t)(r.batch * 2) | (uintptr_t)(r.token * 2) | (uintptr_t)(r.head * 2)) & 15u) == 0;
+}
+
+namespace {
+
+Plan plan_of(const gma_attn_t &a, const gma_attn_paged_t *paged, Carve *c)
+{
+    const int group = a.H / a.G, pack = paged && group <= TILE ? group : 1;
+    return make_plan(a, paged != nullptr, pack, 2 * TILE, TILE, TILE, paged ? 3 * SMS : SMS, 4, true, c);
+}
+
+}  // namespace
+
+bool tc_takes(const gma_attn_t &a, const gma_attn_paged_t *p)
+{
+    if (a.dtype != GMA_BF16) return false;
+    const long long B = a.offsets ? 1 : a.B;
+    if (!tma_heads(a.q, B, a.N, a.H)) return false;
+    if (!p) return tma_heads(a.k, B, a.N, a.G) && tma_heads(a.v, B, a.N, a.G);
+    return p->page >= 8 && (p->page & (p->page - 1)) == 0 && tma_heads(p->k_pages, p->pages, p->page, a.G) &&
+           tma_heads(p->v_pages, p->pages, p->page, a.G);
+}
+
+size_t tc_workspace(const gma_attn_t &a, const gma_attn_paged_t *paged)
+{
+    Carve c;
+    plan_of(a, paged, &c);
+    return c.total();
+}
+
+gma_status_t tc_forward(const gma_attn_t &a, const gma_attn_paged_t *p, void *ws, cudaStream_t st)
+{
+    Carve c;
+    const Plan pl = plan_of(a, p, &c);
+    char *w = (char *)ws;
+    TcArgs x = {};
+    x.g = geo_of(a, p);
+    x.o = heads_of<bf16>(a.o);
+    x.lse = a.lse;
+    x.pack = pl.pack;
+    x.heads = pl.heads;
+    x.o_vec = store_vec(a.o, a.dv);
+    x.head = (const PlanHead *)(w + pl.head_at);
+    x.items = (const Item *)(w + pl.items_at);
+    x.parts = Parts{(float *)(w + pl.part_at), (float *)(w + pl.stat_at), pl.rows, pl.heads, a.dv, (int *)(w + pl.join_at)};
+    x.hdr = (WsHeader *)ws;
+    x.q_boxes = (a.d + 63) / 64;
+    x.v_boxes = (a.dv + 63) / 64;
+    x.slot_bytes = BOX * (uint32_t)(x.q_boxes > x.v_boxes ? x.q_boxes : x.v_boxes);
+    const uint32_t fixed = 2 * BOX * (uint32_t)x.q_boxes + 1024 + (uint32_t)sizeof(Bars);
+    x.slots = (int)((SMEM_MAX - fixed) / x.slot_bytes);
+    if (x.slots > MAX_SLOTS) x.slots = MAX_SLOTS;
+    const uint32_t smem = fixed + (uint32_t)x.slots * x.slot_bytes;
+    x.page_rows = p ? (p->page < TILE ? p->page : TILE) : TILE;
+    x.tile_pages = TILE / x.page_rows;
+    const long long B = a.offsets ? 1 : a.B;
+    CUtensorMap qm, km, vm;
+    const int per = TILE / pl.pack;
+    if (!heads_map(&qm, a.q, B, a.N, a.H, a.d, pl.pack, per)) return GMA_ERR_CUDA;
+    if (p ? !heads_map(&km, p->k_pages, p->pages, p->page, a.G, a.d, 1, x.page_rows) || !heads_map(&vm, p->v_pages, p->pages, p->page, a.G, a.dv, 1, x.page_rows)
+          : !heads_map(&km, a.k, B, a.N, a.G, a.d, 1, TILE) || !heads_map(&vm, a.v, B, a.N, a.G, a.dv, 1, TILE))
+        return GMA_ERR_CUDA;
+    gma_status_t r = launch_plan(plan_args(x.g, pl, ws), nullptr, st);
+    if (r != GMA_OK) return r;
+    const unsigned grid = (unsigned)pl.max_items * pl.heads;
+    auto kern = p ? attn_tc_kernel<true> : attn_tc_kernel<false>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_MAX) != cudaSuccess) return GMA_ERR_CUDA;
+    GMA_LAUNCH(KID_ATTN, st, launch_pdl(kern, grid, THREADS, smem, st, x, qm, km, vm));
+    return GMA_OK;
+}
+
+}  // namespace att
+}  // namespace gma
