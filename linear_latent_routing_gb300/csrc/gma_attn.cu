@@ -385,7 +385,7 @@ gma_status_t gma_attn_forward(const gma_attn_t *a, void *ws, size_t ws_bytes, gm
 
 size_t gma_attn_backward_workspace_size(const gma_attn_grad_t *g)
 {
-    return check_grad(g) == GMA_OK ? simt_backward_workspace(*g) : 0;
+    return check_grad(g) != GMA_OK ? 0 : tc_takes_backward(*g) ? tc_backward_workspace(*g) : simt_backward_workspace(*g);
 }
 
 gma_status_t gma_attn_backward(const gma_attn_grad_t *g, void *ws, size_t ws_bytes, gma_stream_t stream)
@@ -399,7 +399,7 @@ gma_status_t gma_attn_backward(const gma_attn_grad_t *g, void *ws, size_t ws_byt
     if ((r = zero_tail(a, g->dq, a.H, a.d, st)) != GMA_OK) return r;
     if ((r = zero_tail(a, g->dk, a.G, a.d, st)) != GMA_OK) return r;
     if ((r = zero_tail(a, g->dv, a.G, a.dv, st)) != GMA_OK) return r;
-    return simt_backward(*g, ws, st);
+    return tc_takes_backward(*g) ? tc_backward(*g, ws, st) : simt_backward(*g, ws, st);
 }
 
 gma_status_t gma_attn_append(const gma_attn_paged_t *p, gma_stream_t stream)

@@ -1,0 +1,532 @@
+// gma_attn_tc_bwd.cu -- backward pass of softmax attention over whole sequences on the tensor cores (tcgen05), bf16.
+//
+// Scores are computed again from q, k and the rows' log-sum-exp, once with keys as rows (dk, dv) and once with queries as rows
+// (dq): seven products of a tile instead of five, but every sum is one block's in one order, without atomics and without an
+// fp32 copy of dq, so that repeated calls give the same bits.
+//
+// dk, dv: a block owns 128 keys of one key head and walks over the query tiles that see them, of every query head of the group.
+//   S^T = K Q^T, dP^T = V dO^T, P^T = exp2(S^T - lse), dS^T = P^T (dP^T - delta), dV += P^T dO, dK += dS^T Q.
+// Tensor memory: S^T | dP^T | dV | dK, 128 columns each.  P^T and dS^T, rounded to bf16 (half a step, 2^-8 relative), take the place of
+// S^T and dP^T as first operands.  The products' order hides the warps' work: while they take exponentials the tensor cores run dK
+// of the tile before and dP^T of this one, while they form dS^T they run dV of this tile and S^T of the next.
+//
+// dq: a block owns 128 query rows of one head and walks over their key tiles.  Tensor memory: S | S | dP | dQ; S of the next tile
+// and dQ of the tile before run while the warps form dS of this one, in place of its S.
+//
+// Warps: 0-3 and 4-7 each take half a tile's columns (a thread a row), 8 issues the products, 9 loads.
+#include "attn_tc.cuh"
+#include "attn_tc_host.cuh"
+
+namespace gma {
+namespace att {
+namespace {
+
+constexpr int THREADS = 384;
+constexpr int STAGES = 4, SLOTS = 8;         // at most
+
+struct GradArgs {
+    Geo g;
+    Heads<bf16> dq, dk, dv;
+    const float *lse, *delta;
+    const PlanHead *q_head, *k_head;
+    const Item *q_items, *k_items;
+    int q_vec, k_vec, v_vec;     // 16-byte stores
+    WsHeader *hdr;
+    int q_boxes, v_boxes;
+    int stages, slots;           // of the two kernels' rings
+    uint32_t slot_bytes;
+};
+
+// The first operand of a product in tensor memory, k-step s: each half of the columns lies at its half's first ones.
+__device__ __forceinline__ uint32_t half_col(int s) { return (uint32_t)(8 * s + (s >= 4 ? 32 : 0)); }
+
+// 32 columns' values back as bf16 pairs in 16 columns.
+__device__ __forceinline__ void put_pairs(uint32_t at, const float (&v)[32])
+{
+    uint32_t w[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) w[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
+    tmem_st16(at, w);
+}
+
+// ------------------------------------------------------------------ dk, dv
+struct KeyBars {
+    uint64_t kv, fq[STAGES], fo[STAGES], eq[STAGES], eo[STAGES], s, dp, p, ds, done, drain;
+    uint32_t tmem;
+    int abort;
+    alignas(16) float lse2[STAGES][TILE], delta[STAGES][TILE];
+};
+
+__global__ void __launch_bounds__(THREADS, 1) attn_dkv_kernel(const GradArgs a, const __grid_constant__ CUtensorMap qmap,
+                                                              const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                                                              const __grid_constant__ CUtensorMap omap)
+{
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    const uint32_t q_tile = (uint32_t)a.q_boxes * BOX, v_tile = (uint32_t)a.v_boxes * BOX, stage = q_tile + v_tile;
+    uint8_t *ring = smem + stage;                                // K and V lie before it
+    KeyBars *bars = reinterpret_cast<KeyBars *>(ring + (size_t)a.stages * stage);
+    volatile int *abort = &bars->abort;
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    if (t == 256) {
+        mbar_init(&bars->kv, 1);
+        for (int i = 0; i < a.stages; ++i) {
+            mbar_init(&bars->fq[i], 2);
+            mbar_init(&bars->fo[i], 1);
+            mbar_init(&bars->eq[i], 1);
+            mbar_init(&bars->eo[i], 1);
+        }
+        mbar_init(&bars->s, 1);
+        mbar_init(&bars->dp, 1);
+        mbar_init(&bars->p, 256);
+        mbar_init(&bars->ds, 256);
+        mbar_init(&bars->done, 1);
+        mbar_init(&bars->drain, 1);
+        bars->abort = 0;
+        fence_mbar_init();
+    }
+    blk::let_next();
+    blk::wait_previous();
+    const Geo &g = a.g;
+    const int rank = blockIdx.x / g.G, kvh = blockIdx.x % g.G;
+    if (rank >= a.k_head->items) return;
+    if (warp == 8) tmem_alloc(&bars->tmem, 512);
+    const Item it = a.k_items[rank];
+    const Seq sq = sequence(g, it.seq);
+    const int tiles = it.t1 - it.t0, steps = tiles * g.group;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem, sb = smem_u32(smem), rb = smem_u32(ring);
+
+    if (warp == 8) {
+        const uint32_t id_s = idesc_f16(TILE, TILE, 1, 1, 0, 0);
+        const uint32_t id_v = idesc_f16(TILE, (uint32_t)(g.dv + 15) & ~15u, 1, 1, 0, 1), id_k = idesc_f16(TILE, (uint32_t)(g.d + 15) & ~15u, 1, 1, 0, 1);
+        const int kq = (g.d + 15) >> 4, ko = (g.dv + 15) >> 4;
+        bool ok = mbar_wait_abortable(&bars->kv, 0, a.hdr, 220, abort);
+        auto have = [&](int i) { return sq.n - (it.t0 + i % tiles) * TILE; };
+        auto at = [&](int i) { return i % a.stages; };
+        auto phase = [&](int i) { return (uint32_t)(i / a.stages) & 1u; };
+        // rows behind the sequence's end meet zeros of P and dS, and may be anything
+        auto scores = [&](int i) {
+            if (!mbar_wait_abortable(&bars->fq[at(i)], phase(i), a.hdr, 221, abort)) return false;
+            if (have(i) < TILE) zero_rows(ring + at(i) * stage, a.q_boxes, have(i));
+            tc_fence_after();
+            if (lane == 0) {
+                const uint32_t q = rb + at(i) * stage;
+                for (int s = 0; s < kq; ++s) mma_f16(tmem, k_desc(sb, s), k_desc(q, s), id_s, s > 0);
+                mma_commit(&bars->s);
+            }
+            return true;
+        };
+        auto dprobs = [&](int i) {
+            if (!mbar_wait_abortable(&bars->fo[at(i)], phase(i), a.hdr, 222, abort)) return false;
+            if (have(i) < TILE) zero_rows(ring + at(i) * stage + q_tile, a.v_boxes, have(i));
+            tc_fence_after();
+            if (lane == 0) {
+                const uint32_t o = rb + at(i) * stage + q_tile;
+                for (int s = 0; s < ko; ++s) mma_f16(tmem + 128, k_desc(sb + q_tile, s), k_desc(o, s), id_s, s > 0);
+                mma_commit(&bars->dp);
+            }
+            return true;
+        };
+        ok = ok && scores(0) && dprobs(0);
+        for (int i = 0; ok && i < steps; ++i) {
+            if (!(ok = mbar_wait_abortable(&bars->p, i & 1, a.hdr, 223, abort))) break;
+            tc_fence_after();
+            if (lane == 0) {
+                const uint32_t o = rb + at(i) * stage + q_tile;
+#pragma unroll
+                for (int s = 0; s < 8; ++s) mma_f16_tmem_a(tmem + 256, tmem + half_col(s), mn_desc(o, s), id_v, i > 0 || s > 0);
+                mma_commit(&bars->eo[at(i)]);
+            }
+            if (i + 1 < steps && !(ok = scores(i + 1))) break;
+            if (!(ok = mbar_wait_abortable(&bars->ds, i & 1, a.hdr, 224, abort))) break;
+            tc_fence_after();
+            if (lane == 0) {
+                const uint32_t q = rb + at(i) * stage;
+#pragma unroll
+                for (int s = 0; s < 8; ++s) mma_f16_tmem_a(tmem + 384, tmem + 128 + half_col(s), mn_desc(q, s), id_k, i > 0 || s > 0);
+                mma_commit(&bars->eq[at(i)]);
+            }
+            if (i + 1 < steps && !(ok = dprobs(i + 1))) break;
+        }
+        if (ok && lane == 0) mma_commit(&bars->done);
+        if (*abort) {
+            if (lane == 0) mma_commit(&bars->drain);
+            mbar_wait(&bars->drain, 0, a.hdr, 225);
+        }
+    } else if (warp == 9) {
+        if (lane == 0) {
+            mbar_arrive_expect_tx(&bars->kv, stage);
+            for (int b = 0; b < a.q_boxes; ++b) tma_load_4d(sb + b * BOX, &kmap, &bars->kv, 64 * b, kvh, sq.row0 + it.tok0, sq.b);
+            for (int b = 0; b < a.v_boxes; ++b) tma_load_4d(sb + q_tile + b * BOX, &vmap, &bars->kv, 64 * b, kvh, sq.row0 + it.tok0, sq.b);
+        }
+        bool ok = true;
+        int issued_q = 0, issued_o = 0;
+        for (int i = 0; ok && i < steps; ++i) {
+            const int h = kvh * g.group + i / tiles, q0 = (it.t0 + i % tiles) * TILE, s = i % a.stages;
+            const uint32_t free = ((uint32_t)(i / a.stages) & 1u) ^ 1u;
+            // this tile's statistics, on their way while its place is waited for
+            float l[4], e[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int r = q0 + lane + 32 * k;
+                const long long at = r < sq.n ? stat_at(g, sq, h, r) : 0;
+                l[k] = r < sq.n ? a.lse[at] * LOG2E : INFINITY;         // a row that is not there has probabilities of zero
+                e[k] = r < sq.n ? a.delta[at] : 0.f;
+            }
+            if (!(ok = mbar_wait_abortable(&bars->eq[s], free, a.hdr, 226, abort))) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&bars->fq[s], q_tile);
+                for (int b = 0; b < a.q_boxes; ++b) tma_load_4d(rb + s * stage + b * BOX, &qmap, &bars->fq[s], 64 * b, h, sq.row0 + q0, sq.b);
+            }
+            issued_q = i + 1;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                bars->lse2[s][lane + 32 * k] = l[k];
+                bars->delta[s][lane + 32 * k] = e[k];
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->fq[s]);
+            if (!(ok = mbar_wait_abortable(&bars->eo[s], free, a.hdr, 227, abort))) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&bars->fo[s], v_tile);
+                for (int b = 0; b < a.v_boxes; ++b) tma_load_4d(rb + s * stage + q_tile + b * BOX, &omap, &bars->fo[s], 64 * b, h, sq.row0 + q0, sq.b);
+            }
+            issued_o = i + 1;
+        }
+        if (*abort) {          // loads that no product waited for
+            mbar_wait(&bars->kv, 0, a.hdr, 228);
+            for (int i = issued_q > a.stages ? issued_q - a.stages : 0; i < issued_q; ++i)
+                mbar_wait(&bars->fq[i % a.stages], (uint32_t)(i / a.stages) & 1u, a.hdr, 229);
+            for (int i = issued_o > a.stages ? issued_o - a.stages : 0; i < issued_o; ++i)
+                mbar_wait(&bars->fo[i % a.stages], (uint32_t)(i / a.stages) & 1u, a.hdr, 230);
+        }
+    } else if (warp < 8) {
+        const int w = warp >> 2, row = t & (TILE - 1), key = it.tok0 + row;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + lanes + 64 * w, td = ts + 128;
+        bool ok = true;
+        for (int i = 0; i < steps; ++i) {
+            const int s = i % a.stages, q0 = (it.t0 + i % tiles) * TILE + 64 * w;
+            if (!(ok = mbar_wait_abortable(&bars->fq[s], (uint32_t)(i / a.stages) & 1u, a.hdr, 231, abort))) break;
+            if (!(ok = mbar_wait_abortable(&bars->s, i & 1, a.hdr, 232, abort))) break;
+            tc_fence_after();
+            float p[2][32];
+            const bool edge = g.causal && __any_sync(~0u, q0 < key);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t r[32];
+                tmem_ld32(ts + 32 * c, r);
+                tmem_ld_wait();
+                const float *lse2 = &bars->lse2[s][64 * w + 32 * c];
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    const float4 l = *reinterpret_cast<const float4 *>(lse2 + e);
+                    p[c][e] = ex2(fmaf(__uint_as_float(r[e]), g.sl2, -l.x));
+                    p[c][e + 1] = ex2(fmaf(__uint_as_float(r[e + 1]), g.sl2, -l.y));
+                    p[c][e + 2] = ex2(fmaf(__uint_as_float(r[e + 2]), g.sl2, -l.z));
+                    p[c][e + 3] = ex2(fmaf(__uint_as_float(r[e + 3]), g.sl2, -l.w));
+                }
+                if (edge) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (q0 + 32 * c + e < key) p[c][e] = 0.f;
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) put_pairs(ts + 16 * c, p[c]);
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(&bars->p);
+            if (!(ok = mbar_wait_abortable(&bars->dp, i & 1, a.hdr, 233, abort))) break;
+            tc_fence_after();
+            uint32_t r[2][32];
+            tmem_ld32(td, r[0]);
+            tmem_ld32(td + 32, r[1]);
+            tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const float *delta = &bars->delta[s][64 * w + 32 * c];
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    const float4 l = *reinterpret_cast<const float4 *>(delta + e);
+                    p[c][e] *= __uint_as_float(r[c][e]) - l.x;
+                    p[c][e + 1] *= __uint_as_float(r[c][e + 1]) - l.y;
+                    p[c][e + 2] *= __uint_as_float(r[c][e + 2]) - l.z;
+                    p[c][e + 3] *= __uint_as_float(r[c][e + 3]) - l.w;
+                }
+                put_pairs(td + 16 * c, p[c]);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(&bars->ds);
+        }
+        if (ok && mbar_wait_abortable(&bars->done, 0, a.hdr, 234, abort)) {
+            tc_fence_after();
+            const bool valid = key < sq.n;
+            const int r = sq.row0 + (valid ? key : it.tok0);
+            if (w == 0) store_row(tmem + lanes + 256, g.dv, 1.f, valid, a.dv.at(sq.b, r, kvh), a.v_vec);
+            else store_row(tmem + lanes + 384, g.d, g.scale, valid, a.dk.at(sq.b, r, kvh), a.k_vec);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------------------ dq
+struct QueryBars {
+    uint64_t q, full[SLOTS], empty[SLOTS], s[2], dp, ds, done, drain;
+    uint32_t tmem;
+    int abort;
+};
+
+__global__ void __launch_bounds__(THREADS, 1) attn_dq_kernel(const GradArgs a, const __grid_constant__ CUtensorMap qmap,
+                                                             const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                                                             const __grid_constant__ CUtensorMap omap)
+{
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    const uint32_t q_tile = (uint32_t)a.q_boxes * BOX, v_tile = (uint32_t)a.v_boxes * BOX;
+    uint8_t *ring = smem + q_tile + v_tile;
+    QueryBars *bars = reinterpret_cast<QueryBars *>(ring + (size_t)a.slots * a.slot_bytes);
+    volatile int *abort = &bars->abort;
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    if (t == 256) {
+        mbar_init(&bars->q, 1);
+        for (int i = 0; i < a.slots; ++i) {
+            mbar_init(&bars->full[i], 1);
+            mbar_init(&bars->empty[i], 1);
+        }
+        mbar_init(&bars->s[0], 1);
+        mbar_init(&bars->s[1], 1);
+        mbar_init(&bars->dp, 1);
+        mbar_init(&bars->ds, 256);
+        mbar_init(&bars->done, 1);
+        mbar_init(&bars->drain, 1);
+        bars->abort = 0;
+        fence_mbar_init();
+    }
+    blk::wait_previous();
+    const Geo &g = a.g;
+    const int rank = blockIdx.x / g.H, h = blockIdx.x % g.H, kvh = h / g.group;
+    if (rank >= a.q_head->items) return;
+    if (warp == 8) tmem_alloc(&bars->tmem, 512);
+    const Item it = a.q_items[rank];
+    const Seq sq = sequence(g, it.seq);
+    const int tiles = it.t1 - it.t0;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem, sb = smem_u32(smem), rb = smem_u32(ring);
+
+    if (warp == 8) {
+        const uint32_t id_s = idesc_f16(TILE, TILE, 1, 1, 0, 0), id_q = idesc_f16(TILE, (uint32_t)(g.d + 15) & ~15u, 1, 1, 0, 1);
+        const int kq = (g.d + 15) >> 4, ko = (g.dv + 15) >> 4;
+        bool ok = mbar_wait_abortable(&bars->q, 0, a.hdr, 240, abort);
+        auto tile = [&](int c) { return rb + (uint32_t)(c % a.slots) * a.slot_bytes; };
+        auto loaded = [&](int c) { return mbar_wait_abortable(&bars->full[c % a.slots], (uint32_t)(c / a.slots) & 1u, a.hdr, 241, abort); };
+        auto scores = [&](int j) {
+            if (!loaded(2 * j)) return false;
+            // keys behind the sequence's end meet zeros of dS, and may be anything
+            const int have = sq.L - (it.t0 + j) * TILE;
+            if (have < TILE) zero_rows(ring + (size_t)(2 * j % a.slots) * a.slot_bytes, a.q_boxes, have);
+            tc_fence_after();
+            if (lane == 0) {
+                for (int s = 0; s < kq; ++s) mma_f16(tmem + 128 * (j & 1), k_desc(sb, s), k_desc(tile(2 * j), s), id_s, s > 0);
+                mma_commit(&bars->s[j & 1]);
+            }
+            return true;
+        };
+        auto dprobs = [&](int j) {
+            if (!loaded(2 * j + 1)) return false;
+            tc_fence_after();
+            if (lane == 0) {
+                for (int s = 0; s < ko; ++s) mma_f16(tmem + 256, k_desc(sb + q_tile, s), k_desc(tile(2 * j + 1), s), id_s, s > 0);
+                mma_commit(&bars->dp);
+                mma_commit(&bars->empty[(2 * j + 1) % a.slots]);
+            }
+            return true;
+        };
+        ok = ok && scores(0) && dprobs(0);
+        for (int j = 0; ok && j < tiles; ++j) {
+            if (j + 1 < tiles && !(ok = scores(j + 1))) break;
+            if (!(ok = mbar_wait_abortable(&bars->ds, j & 1, a.hdr, 242, abort))) break;
+            if (j + 1 < tiles && !(ok = dprobs(j + 1))) break;
+            tc_fence_after();
+            if (lane == 0) {
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+                    mma_f16_tmem_a(tmem + 384, tmem + 128 * (j & 1) + half_col(s), mn_desc(tile(2 * j), s), id_q, j > 0 || s > 0);
+                mma_commit(&bars->empty[2 * j % a.slots]);
+            }
+        }
+        if (ok && lane == 0) mma_commit(&bars->done);
+        if (*abort) {
+            if (lane == 0) mma_commit(&bars->drain);
+            mbar_wait(&bars->drain, 0, a.hdr, 243);
+        }
+    } else if (warp == 9) {
+        if (lane == 0) {
+            mbar_arrive_expect_tx(&bars->q, q_tile + v_tile);
+            for (int b = 0; b < a.q_boxes; ++b) tma_load_4d(sb + b * BOX, &qmap, &bars->q, 64 * b, h, sq.row0 + it.tok0, sq.b);
+            for (int b = 0; b < a.v_boxes; ++b) tma_load_4d(sb + q_tile + b * BOX, &omap, &bars->q, 64 * b, h, sq.row0 + it.tok0, sq.b);
+        }
+        bool ok = true;
+        int issued = 0;
+        for (int c = 0; ok && c < 2 * tiles; ++c) {
+            const int s = c % a.slots, row = sq.row0 + (it.t0 + c / 2) * TILE;
+            if (!(ok = mbar_wait_abortable(&bars->empty[s], ((uint32_t)(c / a.slots) & 1u) ^ 1u, a.hdr, 244, abort))) break;
+            if (lane == 0) {
+                const int nb = c & 1 ? a.v_boxes : a.q_boxes;
+                mbar_arrive_expect_tx(&bars->full[s], BOX * nb);
+                for (int b = 0; b < nb; ++b) tma_load_4d(rb + s * a.slot_bytes + b * BOX, c & 1 ? &vmap : &kmap, &bars->full[s], 64 * b, kvh, row, sq.b);
+            }
+            issued = c + 1;
+        }
+        if (*abort) {
+            mbar_wait(&bars->q, 0, a.hdr, 245);
+            for (int c = issued > a.slots ? issued - a.slots : 0; c < issued; ++c)
+                mbar_wait(&bars->full[c % a.slots], (uint32_t)(c / a.slots) & 1u, a.hdr, 246);
+        }
+    } else if (warp < 8) {
+        const int w = warp >> 2, row = t & (TILE - 1), tok = it.tok0 + row;
+        const bool valid = tok < sq.n;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const int seen = valid ? sq.seen(g, tok) : sq.L;
+        const long long at = valid ? stat_at(g, sq, h, tok) : 0;
+        const float lse2 = valid ? a.lse[at] * LOG2E : 0.f, delta = valid ? a.delta[at] : 0.f;
+        bool ok = true;
+        for (int j = 0; j < tiles; ++j) {
+            const uint32_t ts = tmem + lanes + 128 * (j & 1) + 64 * w, td = tmem + lanes + 256 + 64 * w;
+            if (!(ok = mbar_wait_abortable(&bars->s[j & 1], (j >> 1) & 1, a.hdr, 247, abort))) break;
+            tc_fence_after();
+            const int lim = seen - (it.t0 + j) * TILE - 64 * w;
+            float p[2][32];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t r[32];
+                tmem_ld32(ts + 32 * c, r);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) p[c][e] = ex2(fmaf(__uint_as_float(r[e]), g.sl2, -lse2));
+            }
+            if (!(ok = mbar_wait_abortable(&bars->dp, j & 1, a.hdr, 248, abort))) break;
+            tc_fence_after();
+            const bool edge = __any_sync(~0u, lim < 64);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t r[32];
+                tmem_ld32(td + 32 * c, r);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) p[c][e] *= __uint_as_float(r[e]) - delta;
+                if (edge) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (32 * c + e >= lim) p[c][e] = 0.f;
+                }
+                put_pairs(ts + 16 * c, p[c]);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(&bars->ds);
+        }
+        if (ok && mbar_wait_abortable(&bars->done, 0, a.hdr, 249, abort)) {
+            tc_fence_after();
+            // each half of the warps takes half of the columns
+            const int from = 64 * w, width = min(g.d - from, 64);
+            if (width > 0)
+                store_row(tmem + lanes + 384 + from, width, g.scale, valid, a.dq.at(sq.b, sq.row0 + (valid ? tok : it.tok0), h) + from, a.q_vec);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) tmem_dealloc(tmem, 512);
+}
+
+struct GradPlan {
+    Plan q, k;
+    size_t delta_at;
+};
+
+GradPlan grad_plan(const gma_attn_t &a, Carve *c)
+{
+    GradPlan p;
+    p.q = make_plan(a, false, 1, TILE, TILE, TILE, SMS, 1, false, c);
+    gma_attn_t by = a;
+    by.H = a.G;                       // a tile of keys serves the whole group
+    p.k = make_plan(by, false, 1, TILE, TILE, TILE, SMS, 1, false, c);
+    p.k.by_keys = true;
+    p.delta_at = c->take((size_t)(a.offsets ? 1 : a.B) * a.H * a.N * sizeof(float));
+    return p;
+}
+
+}  // namespace
+
+bool tc_takes_backward(const gma_attn_grad_t &g)
+{
+    const gma_attn_t &a = g.fwd;
+    const long long B = a.offsets ? 1 : a.B;
+    return tc_takes(a, nullptr) && tma_heads(g.d_o, B, a.N, a.H);
+}
+
+size_t tc_backward_workspace(const gma_attn_grad_t &g)
+{
+    Carve c;
+    grad_plan(g.fwd, &c);
+    return c.total();
+}
+
+gma_status_t tc_backward(const gma_attn_grad_t &g, void *ws, cudaStream_t st)
+{
+    const gma_attn_t &a = g.fwd;
+    Carve c;
+    const GradPlan p = grad_plan(a, &c);
+    char *w = (char *)ws;
+    GradArgs x = {};
+    x.g = geo_of(a, nullptr);
+    x.dq = heads_of<bf16>(g.dq); x.dk = heads_of<bf16>(g.dk); x.dv = heads_of<bf16>(g.dv);
+    x.lse = a.lse;
+    float *delta = (float *)(w + p.delta_at);
+    x.delta = delta;
+    x.q_head = (const PlanHead *)(w + p.q.head_at);
+    x.k_head = (const PlanHead *)(w + p.k.head_at);
+    x.q_items = (const Item *)(w + p.q.items_at);
+    x.k_items = (const Item *)(w + p.k.items_at);
+    x.q_vec = store_vec(g.dq, a.d);
+    x.k_vec = store_vec(g.dk, a.d);
+    x.v_vec = store_vec(g.dv, a.dv);
+    x.hdr = (WsHeader *)ws;
+    x.q_boxes = (a.d + 63) / 64;
+    x.v_boxes = (a.dv + 63) / 64;
+    const uint32_t pair = BOX * (uint32_t)(x.q_boxes + x.v_boxes), k_fixed = pair + 1024 + (uint32_t)sizeof(KeyBars),
+                   q_fixed = pair + 1024 + (uint32_t)sizeof(QueryBars);
+    x.stages = (int)((SMEM_MAX - k_fixed) / pair);
+    if (x.stages > STAGES) x.stages = STAGES;
+    x.slot_bytes = BOX * (uint32_t)(x.q_boxes > x.v_boxes ? x.q_boxes : x.v_boxes);
+    x.slots = (int)((SMEM_MAX - q_fixed) / x.slot_bytes);
+    if (x.slots > SLOTS) x.slots = SLOTS;
+    const long long B = a.offsets ? 1 : a.B;
+    CUtensorMap qm, km, vm, om;
+    if (!heads_map(&qm, a.q, B, a.N, a.H, a.d, 1, TILE) || !heads_map(&km, a.k, B, a.N, a.G, a.d, 1, TILE) ||
+        !heads_map(&vm, a.v, B, a.N, a.G, a.dv, 1, TILE) || !heads_map(&om, g.d_o, B, a.N, a.H, a.dv, 1, TILE))
+        return GMA_ERR_CUDA;
+    const PlanArgs first = plan_args(x.g, p.q, ws);
+    PlanArgs second = plan_args(x.g, p.k, ws);
+    second.hdr = nullptr;
+    gma_status_t r = launch_plan(first, &second, st);
+    if (r != GMA_OK) return r;
+    if ((r = launch_delta(g, delta, st)) != GMA_OK) return r;
+    if (cudaFuncSetAttribute(attn_dkv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_MAX) != cudaSuccess ||
+        cudaFuncSetAttribute(attn_dq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_MAX) != cudaSuccess)
+        return GMA_ERR_CUDA;
+    GMA_LAUNCH(KID_ATTN_DKV, st, launch_pdl(attn_dkv_kernel, (unsigned)p.k.max_items * a.G, THREADS, k_fixed + x.stages * pair, st, x, qm, km, vm, om));
+    GMA_LAUNCH(KID_ATTN_DQ, st, launch_pdl(attn_dq_kernel, (unsigned)p.q.max_items * a.H, THREADS, q_fixed + x.slots * x.slot_bytes, st, x, qm, km, vm, om));
+    return GMA_OK;
+}
+
+}  // namespace att
+}  // namespace gma
