@@ -21,15 +21,34 @@ constexpr int TILE = 128;
 constexpr uint32_t BOX = TILE * 128;          // bytes of 64 columns of a tile
 constexpr uint32_t SMEM_MAX = 232448;         // 227 KB
 
-// k-step s (16 columns) of a K-major tile, and k-step s (16 rows) of an MN-major one.
-__device__ __forceinline__ uint64_t k_desc(uint32_t base, int s)
+// Descriptors of a tile as a K-major operand and as an MN-major one, and what one k-step (16 columns, 16 rows) adds to them: the
+// address field counts 16 bytes, and tiles lie below 256 KB, so that a plain sum stays in it.
+__device__ __forceinline__ uint64_t k_desc(uint32_t tile) { return smem_desc(tile, 16, 1024, SW_128B); }
+__device__ __forceinline__ uint64_t mn_desc(uint32_t tile) { return smem_desc(tile, BOX, 1024, SW_128B); }
+constexpr __host__ __device__ uint32_t k_step(int s) { return ((uint32_t)(s >> 2) * BOX + (uint32_t)(s & 3) * 32u) >> 4; }
+constexpr __host__ __device__ uint32_t mn_step(int s) { return (uint32_t)(s * 16 * 128) >> 4; }
+
+// D = A B^T over `steps` k-steps of two K-major tiles.
+__device__ __forceinline__ void mma_tiles(uint32_t d, uint64_t a, uint64_t b, uint32_t id, int steps)
 {
-    return smem_desc(base + (uint32_t)((s >> 2) * BOX + (s & 3) * 32), 16, 1024, SW_128B);
+#pragma unroll
+    for (int s = 0; s < TILE / 16; ++s)
+        if (s < steps) mma_f16(d, a + k_step(s), b + k_step(s), id, s > 0);
 }
-__device__ __forceinline__ uint64_t mn_desc(uint32_t base, int s)
-{
-    return smem_desc(base + (uint32_t)(s * 16 * 128), BOX, 1024, SW_128B);
-}
+
+// A place in a ring of tiles, and the parity of its turn.
+struct RingPos {
+    int s;
+    uint32_t turn;
+    __device__ __forceinline__ void step(int n, int slots)      // n <= slots
+    {
+        s += n;
+        if (s >= slots) {
+            s -= slots;
+            turn ^= 1u;
+        }
+    }
+};
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, uint64_t *bar, int x, int y, int z, int w)
 {
@@ -37,6 +56,32 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map
                  " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
                  "l"((uint64_t)map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
                  : "memory");
+}
+
+// One lane of a converged warp, the same one every time.  Where it issues the products the compiler knows that one thread does, and
+// their operands stay in uniform registers.
+__device__ __forceinline__ bool elect()
+{
+    uint32_t is;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(is));
+    return is != 0;
+}
+
+// mbar_wait_abortable without its long suspension: the products and the warps that feed them wait for one another several
+// times a tile, and a thread that sleeps in try_wait comes back late (the 8192-token prompt with 16 heads of 128: %s).
+__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, WsHeader *hdr, unsigned where, volatile int *abort)
+{
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!mbar_try_wait(bar, parity)) {
+        if (*abort) return false;
+        if (wait_expired(clock64() - t0, hdr)) {
+            record_error(hdr, GMA_ERR_TIMEOUT, where);
+            *abort = 1;
+            return false;
+        }
+    }
+    return true;
 }
 
 // Zeros in rows `from` to 127 of a tile's boxes, by one warp; the tensor cores see them after the fence.

@@ -43,6 +43,7 @@ struct TcArgs {
     uint32_t slot_bytes;
     int slots;
     int page_rows, tile_pages; // rows of a page's box, such boxes in a tile
+    int page_shift;            // pages are powers of two
 };
 
 // shared memory: query tiles, the ring, the barriers
@@ -106,65 +107,68 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const TcArgs a, con
             // ============================================================ products
             const uint32_t id_s = idesc_f16(TILE, TILE, 1, 1, 0, 0), id_o = idesc_f16(TILE, (uint32_t)(g.dv + 15) & ~15u, 1, 1, 0, 1);
             const int ksteps = (g.d + 15) >> 4;
-            bool ok = t1 > t0 && mbar_wait_abortable(&bars->q, 0, a.hdr, 200, abort);
-            int done[2] = {0, 0};
-            auto slot = [&](int c) { return c % a.slots; };
-            auto loaded = [&](int c) { return mbar_wait_abortable(&bars->full[slot(c)], (uint32_t)(c / a.slots) & 1u, a.hdr, 201, abort); };
-            auto release = [&](int c) { if (lane == 0) mma_commit(&bars->empty[slot(c)]); };
-            // S_w = Q_w K_t^T
-            auto scores = [&](int w, int kt) {
-                if (lane == 0) {
-                    const uint32_t q = sb + (two ? w * q_tile : 0u), k = rb + (uint32_t)slot(2 * (kt - t0)) * a.slot_bytes;
-                    for (int s = 0; s < ksteps; ++s) mma_f16(tmem + w * TILE, k_desc(q, s), k_desc(k, s), id_s, s > 0);
+            bool ok = t1 > t0 && bar_wait(&bars->q, 0, a.hdr, 200, abort);
+            uint32_t turn[2] = {0, 0};             // parity of a stream's tiles
+            bool begun[2] = {false, false};
+            const uint64_t q_desc = k_desc(sb), q_next = two ? q_tile >> 4 : 0;
+            auto loaded = [&](const RingPos &r) { return bar_wait(&bars->full[r.s], r.turn, a.hdr, 201, abort); };
+            // S_w = Q_w K^T, and with it the tile is given back
+            auto scores = [&](int w, const RingPos &k, bool last) {
+                if (elect()) {
+                    mma_tiles(tmem + w * TILE, q_desc + (w ? q_next : 0), k_desc(rb + (uint32_t)k.s * a.slot_bytes), id_s, ksteps);
                     mma_commit(&bars->s[w]);
+                    if (last) mma_commit(&bars->empty[k.s]);
                 }
             };
-            // O_w += P_w V_t
-            auto output = [&](int w, int kt) {
-                if (lane == 0) {
-                    const uint32_t v = rb + (uint32_t)slot(2 * (kt - t0) + 1) * a.slot_bytes;
+            // O_w += P_w V
+            auto output = [&](int w, const RingPos &v, bool last) {
+                if (elect()) {
+                    const uint64_t desc = mn_desc(rb + (uint32_t)v.s * a.slot_bytes);
+                    const uint32_t p = tmem + w * TILE, o = tmem + 256 + w * TILE;
 #pragma unroll
-                    for (int s = 0; s < TILE / 16; ++s)
-                        mma_f16_tmem_a(tmem + 256 + w * TILE, tmem + w * TILE + 8 * s, mn_desc(v, s), id_o, done[w] > 0 || s > 0);
+                    for (int s = 0; s < TILE / 16; ++s) mma_f16_tmem_a(o, p + 8 * s, desc + mn_step(s), id_o, s > 0 || begun[w]);
+                    if (last) mma_commit(&bars->empty[v.s]);
                 }
-                ++done[w];
+                begun[w] = true;
+                turn[w] ^= 1u;
             };
-            if (ok && (ok = loaded(0))) {
-                if (t0 < e0) scores(0, t0);
-                if (two) scores(1, t0);
-                release(0);
-                if (!two && t0 + 1 < t1 && (ok = loaded(2))) {
-                    scores(1, t0 + 1);
-                    release(2);
+            // the values of the tile at hand and the keys that the next scores take
+            RingPos v{1, 0}, k{0, 0};
+            if (ok && (ok = loaded(k))) {
+                if (t0 < e0) scores(0, k, !two);
+                if (two) scores(1, k, true);
+                k.step(2, a.slots);
+                if (!two) {
+                    if (t0 + 1 < t1 && (ok = loaded(k))) scores(1, k, true);
+                    k.step(2, a.slots);
                 }
             }
             for (int kt = t0; ok && kt < t1; ++kt) {
-                const int cv = 2 * (kt - t0) + 1;
-                if (!(ok = loaded(cv))) break;
+                if (!(ok = loaded(v))) break;
                 const int have = sq.L - kt * TILE;
                 // values behind the sequence's end meet probabilities of zero, and may be anything
-                if (have < TILE) zero_rows(ring + (size_t)slot(cv) * a.slot_bytes, a.v_boxes, have);
+                if (have < TILE) zero_rows(ring + (size_t)v.s * a.slot_bytes, a.v_boxes, have);
                 const int next = kt + step;
-                for (int w = two ? 0 : (kt - t0) & 1; ok && w < 2; ++w) {
-                    if (two && w == 0 && kt >= e0) continue;
-                    if (!(ok = mbar_wait_abortable(&bars->p[w], done[w] & 1, a.hdr, 202, abort))) break;
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    if (two ? w == 0 && kt >= e0 : w != ((kt - t0) & 1)) continue;
+                    if (!(ok = bar_wait(&bars->p[w], turn[w], a.hdr, 202, abort))) break;
                     tc_fence_after();
-                    output(w, kt);
-                    const bool last_user = !two || w == 1;
-                    if (last_user) release(cv);
+                    const bool last = !two || w == 1;
+                    output(w, v, last);
                     if (next < (two && w == 0 ? e0 : t1)) {
-                        if (!(ok = loaded(cv - 1 + 2 * step))) break;
-                        scores(w, next);
-                        if (last_user) release(cv - 1 + 2 * step);
-                    } else if (lane == 0) {
+                        if (!(ok = loaded(k))) break;
+                        scores(w, k, last);
+                    } else if (elect()) {
                         mma_commit(&bars->o[w]);
                     }
-                    if (!two) break;
                 }
+                v.step(2, a.slots);
+                k.step(2, a.slots);
             }
             // after a wait that gave up: products in flight end before their operands and results go
             if (*abort) {
-                if (lane == 0) mma_commit(&bars->drain);
+                if (elect()) mma_commit(&bars->drain);
                 mbar_wait(&bars->drain, 0, a.hdr, 209);
             }
         } else if (warp == 9) {
@@ -180,37 +184,38 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const TcArgs a, con
                         for (int b = 0; b < a.q_boxes; ++b)
                             tma_load_4d(sb + w * q_tile + b * BOX, &qmap, &bars->q, 64 * b, head * pack, sq.row0 + it.tok0 + w * per, sq.b);
                 }
-                int entry = 0;
                 // the page of this lane's box of a tile
                 auto page_entry = [&](int kt) {
                     const int j = kt * TILE + lane * a.page_rows;
                     if (lane >= a.tile_pages || j >= sq.L) return 0;
-                    return g.table[(long long)it.seq * g.table_stride + j / g.page];
+                    return g.table[(long long)it.seq * g.table_stride + (j >> a.page_shift)];
                 };
-                if (PAGED) entry = page_entry(t0);
+                RingPos r{0, 1};
+                int entry = PAGED ? page_entry(t0) : 0;
                 for (int kt = t0; ok && kt < t1; ++kt) {
                     const int have = min(sq.L - kt * TILE, TILE), boxes = PAGED ? (have + a.page_rows - 1) / a.page_rows : 1;
-                    const int in_page = PAGED ? kt * TILE % g.page : 0;
+                    const int in_page = PAGED ? (kt * TILE) & (g.page - 1) : 0;
                     const int ahead = PAGED && kt + 1 < t1 ? page_entry(kt + 1) : 0;
+#pragma unroll
                     for (int half = 0; half < 2; ++half) {
-                        const int c = 2 * (kt - t0) + half, s = c % a.slots;
-                        if (!(ok = mbar_wait_abortable(&bars->empty[s], ((uint32_t)(c / a.slots) & 1u) ^ 1u, a.hdr, 203, abort))) break;
-                        const uint32_t dst = rb + (uint32_t)s * a.slot_bytes;
+                        if (!(ok = bar_wait(&bars->empty[r.s], r.turn, a.hdr, 203, abort))) break;
+                        const uint32_t dst = rb + (uint32_t)r.s * a.slot_bytes;
+                        uint64_t *full = &bars->full[r.s];
                         const int nb = half ? a.v_boxes : a.q_boxes;
                         const CUtensorMap *map = half ? &vmap : &kmap;
-                        if (lane == 0)
-                            mbar_arrive_expect_tx(&bars->full[s], PAGED ? (uint32_t)(boxes * a.page_rows * 128 * nb) : BOX * nb);
+                        if (lane == 0) mbar_arrive_expect_tx(full, PAGED ? (uint32_t)(boxes * a.page_rows * 128 * nb) : BOX * nb);
                         __syncwarp();
                         if (PAGED) {
                             // an entry that names no page: a coordinate behind the pool, which reads as zeros
                             const int page = entry >= 0 && entry < g.pages ? entry : g.pages;
                             if (lane < boxes)
                                 for (int b = 0; b < nb; ++b)
-                                    tma_load_4d(dst + b * BOX + lane * a.page_rows * 128, map, &bars->full[s], 64 * b, kvh, in_page, page);
+                                    tma_load_4d(dst + b * BOX + lane * a.page_rows * 128, map, full, 64 * b, kvh, in_page, page);
                         } else if (lane == 0) {
-                            for (int b = 0; b < nb; ++b) tma_load_4d(dst + b * BOX, map, &bars->full[s], 64 * b, kvh, sq.row0 + kt * TILE, sq.b);
+                            for (int b = 0; b < nb; ++b) tma_load_4d(dst + b * BOX, map, full, 64 * b, kvh, sq.row0 + kt * TILE, sq.b);
                         }
-                        issued = c + 1;
+                        ++issued;
+                        r.step(1, a.slots);
                     }
                     entry = ahead;
                 }
@@ -237,7 +242,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const TcArgs a, con
         bool ok = true;
         int n = 0;
         for (int kt = begin; kt < end; kt += step, ++n) {
-            if (!(ok = mbar_wait_abortable(&bars->s[w], n & 1, a.hdr, 206, abort))) break;
+            if (!(ok = bar_wait(&bars->s[w], n & 1, a.hdr, 206, abort))) break;
             tc_fence_after();
             if (busy) {
                 uint32_t r[4][32];
@@ -301,9 +306,9 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const TcArgs a, con
         }
         const float2 la = blk::unpack2(blk::add2(l2, l3));
         float l = la.x + la.y;
-        if (n && ok) ok = mbar_wait_abortable(&bars->o[w], 0, a.hdr, 207, abort);
+        if (n && ok) ok = bar_wait(&bars->o[w], 0, a.hdr, 207, abort);
         // the ring takes stream 1's result: both streams' last products have read it
-        if (!two && w == 1 && n && ok) ok = mbar_wait_abortable(&bars->o[0], 0, a.hdr, 208, abort);
+        if (!two && w == 1 && n && ok) ok = bar_wait(&bars->o[0], 0, a.hdr, 208, abort);
         tc_fence_after();
         bool store = two || w == 0;
         float mine = 1.f;                          // factor of this stream's sums
@@ -487,6 +492,7 @@ gma_status_t tc_forward(const gma_attn_t &a, const gma_attn_paged_t *p, void *ws
     const uint32_t smem = fixed + (uint32_t)x.slots * x.slot_bytes;
     x.page_rows = p ? (p->page < TILE ? p->page : TILE) : TILE;
     x.tile_pages = TILE / x.page_rows;
+    while (p && (1 << x.page_shift) < p->page) ++x.page_shift;
     const long long B = a.offsets ? 1 : a.B;
     CUtensorMap qm, km, vm;
     const int per = TILE / pl.pack;

@@ -103,57 +103,60 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dkv_kernel(const GradArgs a, 
         const uint32_t id_s = idesc_f16(TILE, TILE, 1, 1, 0, 0);
         const uint32_t id_v = idesc_f16(TILE, (uint32_t)(g.dv + 15) & ~15u, 1, 1, 0, 1), id_k = idesc_f16(TILE, (uint32_t)(g.d + 15) & ~15u, 1, 1, 0, 1);
         const int kq = (g.d + 15) >> 4, ko = (g.dv + 15) >> 4;
-        bool ok = mbar_wait_abortable(&bars->kv, 0, a.hdr, 220, abort);
-        auto have = [&](int i) { return sq.n - (it.t0 + i % tiles) * TILE; };
-        auto at = [&](int i) { return i % a.stages; };
-        auto phase = [&](int i) { return (uint32_t)(i / a.stages) & 1u; };
+        bool ok = bar_wait(&bars->kv, 0, a.hdr, 220, abort);
+        const uint64_t kd = k_desc(sb), vd = k_desc(sb + q_tile);
+        // the steps whose scores and whose dP come next, and the one at hand; rows that a step's tile has
+        RingPos rs{0, 0}, rp{0, 0}, rc{0, 0};
+        int js = 0, jp = 0;
+        auto rows = [&](int j) { return sq.n - (it.t0 + j) * TILE; };
         // rows behind the sequence's end meet zeros of P and dS, and may be anything
-        auto scores = [&](int i) {
-            if (!mbar_wait_abortable(&bars->fq[at(i)], phase(i), a.hdr, 221, abort)) return false;
-            if (have(i) < TILE) zero_rows(ring + at(i) * stage, a.q_boxes, have(i));
-            tc_fence_after();
-            if (lane == 0) {
-                const uint32_t q = rb + at(i) * stage;
-                for (int s = 0; s < kq; ++s) mma_f16(tmem, k_desc(sb, s), k_desc(q, s), id_s, s > 0);
+        auto scores = [&]() {
+            if (!bar_wait(&bars->fq[rs.s], rs.turn, a.hdr, 221, abort)) return false;
+            if (rows(js) < TILE) zero_rows(ring + rs.s * stage, a.q_boxes, rows(js));
+            if (++js == tiles) js = 0;
+            if (elect()) {
+                mma_tiles(tmem, kd, k_desc(rb + rs.s * stage), id_s, kq);
                 mma_commit(&bars->s);
             }
+            rs.step(1, a.stages);
             return true;
         };
-        auto dprobs = [&](int i) {
-            if (!mbar_wait_abortable(&bars->fo[at(i)], phase(i), a.hdr, 222, abort)) return false;
-            if (have(i) < TILE) zero_rows(ring + at(i) * stage + q_tile, a.v_boxes, have(i));
-            tc_fence_after();
-            if (lane == 0) {
-                const uint32_t o = rb + at(i) * stage + q_tile;
-                for (int s = 0; s < ko; ++s) mma_f16(tmem + 128, k_desc(sb + q_tile, s), k_desc(o, s), id_s, s > 0);
+        auto dprobs = [&]() {
+            if (!bar_wait(&bars->fo[rp.s], rp.turn, a.hdr, 222, abort)) return false;
+            if (rows(jp) < TILE) zero_rows(ring + rp.s * stage + q_tile, a.v_boxes, rows(jp));
+            if (++jp == tiles) jp = 0;
+            if (elect()) {
+                mma_tiles(tmem + 128, vd, k_desc(rb + rp.s * stage + q_tile), id_s, ko);
                 mma_commit(&bars->dp);
             }
+            rp.step(1, a.stages);
             return true;
         };
-        ok = ok && scores(0) && dprobs(0);
+        ok = ok && scores() && dprobs();
         for (int i = 0; ok && i < steps; ++i) {
-            if (!(ok = mbar_wait_abortable(&bars->p, i & 1, a.hdr, 223, abort))) break;
+            if (!(ok = bar_wait(&bars->p, i & 1, a.hdr, 223, abort))) break;
             tc_fence_after();
-            if (lane == 0) {
-                const uint32_t o = rb + at(i) * stage + q_tile;
+            if (elect()) {
+                const uint64_t o = mn_desc(rb + rc.s * stage + q_tile);
 #pragma unroll
-                for (int s = 0; s < 8; ++s) mma_f16_tmem_a(tmem + 256, tmem + half_col(s), mn_desc(o, s), id_v, i > 0 || s > 0);
-                mma_commit(&bars->eo[at(i)]);
+                for (int s = 0; s < 8; ++s) mma_f16_tmem_a(tmem + 256, tmem + half_col(s), o + mn_step(s), id_v, i > 0 || s > 0);
+                mma_commit(&bars->eo[rc.s]);
             }
-            if (i + 1 < steps && !(ok = scores(i + 1))) break;
-            if (!(ok = mbar_wait_abortable(&bars->ds, i & 1, a.hdr, 224, abort))) break;
+            if (i + 1 < steps && !(ok = scores())) break;
+            if (!(ok = bar_wait(&bars->ds, i & 1, a.hdr, 224, abort))) break;
             tc_fence_after();
-            if (lane == 0) {
-                const uint32_t q = rb + at(i) * stage;
+            if (elect()) {
+                const uint64_t q = mn_desc(rb + rc.s * stage);
 #pragma unroll
-                for (int s = 0; s < 8; ++s) mma_f16_tmem_a(tmem + 384, tmem + 128 + half_col(s), mn_desc(q, s), id_k, i > 0 || s > 0);
-                mma_commit(&bars->eq[at(i)]);
+                for (int s = 0; s < 8; ++s) mma_f16_tmem_a(tmem + 384, tmem + 128 + half_col(s), q + mn_step(s), id_k, i > 0 || s > 0);
+                mma_commit(&bars->eq[rc.s]);
             }
-            if (i + 1 < steps && !(ok = dprobs(i + 1))) break;
+            if (i + 1 < steps && !(ok = dprobs())) break;
+            rc.step(1, a.stages);
         }
-        if (ok && lane == 0) mma_commit(&bars->done);
+        if (ok && elect()) mma_commit(&bars->done);
         if (*abort) {
-            if (lane == 0) mma_commit(&bars->drain);
+            if (elect()) mma_commit(&bars->drain);
             mbar_wait(&bars->drain, 0, a.hdr, 225);
         }
     } else if (warp == 9) {
@@ -164,19 +167,21 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dkv_kernel(const GradArgs a, 
         }
         bool ok = true;
         int issued_q = 0, issued_o = 0;
+        RingPos r{0, 1};
+        int h = kvh * g.group, j = 0;
         for (int i = 0; ok && i < steps; ++i) {
-            const int h = kvh * g.group + i / tiles, q0 = (it.t0 + i % tiles) * TILE, s = i % a.stages;
-            const uint32_t free = ((uint32_t)(i / a.stages) & 1u) ^ 1u;
+            const int q0 = (it.t0 + j) * TILE, s = r.s;
+            const uint32_t free = r.turn;
             // this tile's statistics, on their way while its place is waited for
             float l[4], e[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const int r = q0 + lane + 32 * k;
-                const long long at = r < sq.n ? stat_at(g, sq, h, r) : 0;
-                l[k] = r < sq.n ? a.lse[at] * LOG2E : INFINITY;         // a row that is not there has probabilities of zero
-                e[k] = r < sq.n ? a.delta[at] : 0.f;
+                const int row = q0 + lane + 32 * k;
+                const long long at = row < sq.n ? stat_at(g, sq, h, row) : 0;
+                l[k] = row < sq.n ? a.lse[at] * LOG2E : INFINITY;       // a row that is not there has probabilities of zero
+                e[k] = row < sq.n ? a.delta[at] : 0.f;
             }
-            if (!(ok = mbar_wait_abortable(&bars->eq[s], free, a.hdr, 226, abort))) break;
+            if (!(ok = bar_wait(&bars->eq[s], free, a.hdr, 226, abort))) break;
             if (lane == 0) {
                 mbar_arrive_expect_tx(&bars->fq[s], q_tile);
                 for (int b = 0; b < a.q_boxes; ++b) tma_load_4d(rb + s * stage + b * BOX, &qmap, &bars->fq[s], 64 * b, h, sq.row0 + q0, sq.b);
@@ -189,12 +194,17 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dkv_kernel(const GradArgs a, 
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->fq[s]);
-            if (!(ok = mbar_wait_abortable(&bars->eo[s], free, a.hdr, 227, abort))) break;
+            if (!(ok = bar_wait(&bars->eo[s], free, a.hdr, 227, abort))) break;
             if (lane == 0) {
                 mbar_arrive_expect_tx(&bars->fo[s], v_tile);
                 for (int b = 0; b < a.v_boxes; ++b) tma_load_4d(rb + s * stage + q_tile + b * BOX, &omap, &bars->fo[s], 64 * b, h, sq.row0 + q0, sq.b);
             }
             issued_o = i + 1;
+            r.step(1, a.stages);
+            if (++j == tiles) {
+                j = 0;
+                ++h;
+            }
         }
         if (*abort) {          // loads that no product waited for
             mbar_wait(&bars->kv, 0, a.hdr, 228);
@@ -208,10 +218,14 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dkv_kernel(const GradArgs a, 
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + 64 * w, td = ts + 128;
         bool ok = true;
+        RingPos ring_at{0, 0};
+        int j = 0;
         for (int i = 0; i < steps; ++i) {
-            const int s = i % a.stages, q0 = (it.t0 + i % tiles) * TILE + 64 * w;
-            if (!(ok = mbar_wait_abortable(&bars->fq[s], (uint32_t)(i / a.stages) & 1u, a.hdr, 231, abort))) break;
-            if (!(ok = mbar_wait_abortable(&bars->s, i & 1, a.hdr, 232, abort))) break;
+            const int s = ring_at.s, q0 = (it.t0 + j) * TILE + 64 * w;
+            if (++j == tiles) j = 0;
+            if (!(ok = bar_wait(&bars->fq[s], ring_at.turn, a.hdr, 231, abort))) break;
+            ring_at.step(1, a.stages);
+            if (!(ok = bar_wait(&bars->s, i & 1, a.hdr, 232, abort))) break;
             tc_fence_after();
             float p[2][32];
             const bool edge = g.causal && __any_sync(~0u, q0 < key);
@@ -240,7 +254,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dkv_kernel(const GradArgs a, 
             tmem_st_wait();
             tc_fence_before();
             mbar_arrive(&bars->p);
-            if (!(ok = mbar_wait_abortable(&bars->dp, i & 1, a.hdr, 233, abort))) break;
+            if (!(ok = bar_wait(&bars->dp, i & 1, a.hdr, 233, abort))) break;
             tc_fence_after();
             uint32_t r[2][32];
             tmem_ld32(td, r[0]);
@@ -263,7 +277,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dkv_kernel(const GradArgs a, 
             tc_fence_before();
             mbar_arrive(&bars->ds);
         }
-        if (ok && mbar_wait_abortable(&bars->done, 0, a.hdr, 234, abort)) {
+        if (ok && bar_wait(&bars->done, 0, a.hdr, 234, abort)) {
             tc_fence_after();
             const bool valid = key < sq.n;
             const int r = sq.row0 + (valid ? key : it.tok0);
@@ -325,47 +339,51 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dq_kernel(const GradArgs a, c
     if (warp == 8) {
         const uint32_t id_s = idesc_f16(TILE, TILE, 1, 1, 0, 0), id_q = idesc_f16(TILE, (uint32_t)(g.d + 15) & ~15u, 1, 1, 0, 1);
         const int kq = (g.d + 15) >> 4, ko = (g.dv + 15) >> 4;
-        bool ok = mbar_wait_abortable(&bars->q, 0, a.hdr, 240, abort);
-        auto tile = [&](int c) { return rb + (uint32_t)(c % a.slots) * a.slot_bytes; };
-        auto loaded = [&](int c) { return mbar_wait_abortable(&bars->full[c % a.slots], (uint32_t)(c / a.slots) & 1u, a.hdr, 241, abort); };
+        bool ok = bar_wait(&bars->q, 0, a.hdr, 240, abort);
+        const uint64_t qd = k_desc(sb), od = k_desc(sb + q_tile);
+        // the ring's places of the keys whose scores come next, of the values whose dP does, and of the keys at hand
+        RingPos rk{0, 0}, rv{1, 0}, rc{0, 0};
+        auto loaded = [&](const RingPos &r) { return bar_wait(&bars->full[r.s], r.turn, a.hdr, 241, abort); };
         auto scores = [&](int j) {
-            if (!loaded(2 * j)) return false;
+            if (!loaded(rk)) return false;
             // keys behind the sequence's end meet zeros of dS, and may be anything
             const int have = sq.L - (it.t0 + j) * TILE;
-            if (have < TILE) zero_rows(ring + (size_t)(2 * j % a.slots) * a.slot_bytes, a.q_boxes, have);
-            tc_fence_after();
-            if (lane == 0) {
-                for (int s = 0; s < kq; ++s) mma_f16(tmem + 128 * (j & 1), k_desc(sb, s), k_desc(tile(2 * j), s), id_s, s > 0);
+            if (have < TILE) zero_rows(ring + (size_t)rk.s * a.slot_bytes, a.q_boxes, have);
+            if (elect()) {
+                mma_tiles(tmem + 128 * (j & 1), qd, k_desc(rb + (uint32_t)rk.s * a.slot_bytes), id_s, kq);
                 mma_commit(&bars->s[j & 1]);
             }
+            rk.step(2, a.slots);
             return true;
         };
-        auto dprobs = [&](int j) {
-            if (!loaded(2 * j + 1)) return false;
-            tc_fence_after();
-            if (lane == 0) {
-                for (int s = 0; s < ko; ++s) mma_f16(tmem + 256, k_desc(sb + q_tile, s), k_desc(tile(2 * j + 1), s), id_s, s > 0);
+        auto dprobs = [&]() {
+            if (!loaded(rv)) return false;
+            if (elect()) {
+                mma_tiles(tmem + 256, od, k_desc(rb + (uint32_t)rv.s * a.slot_bytes), id_s, ko);
                 mma_commit(&bars->dp);
-                mma_commit(&bars->empty[(2 * j + 1) % a.slots]);
+                mma_commit(&bars->empty[rv.s]);
             }
+            rv.step(2, a.slots);
             return true;
         };
-        ok = ok && scores(0) && dprobs(0);
+        ok = ok && scores(0) && dprobs();
         for (int j = 0; ok && j < tiles; ++j) {
             if (j + 1 < tiles && !(ok = scores(j + 1))) break;
-            if (!(ok = mbar_wait_abortable(&bars->ds, j & 1, a.hdr, 242, abort))) break;
-            if (j + 1 < tiles && !(ok = dprobs(j + 1))) break;
+            if (!(ok = bar_wait(&bars->ds, j & 1, a.hdr, 242, abort))) break;
             tc_fence_after();
-            if (lane == 0) {
+            if (j + 1 < tiles && !(ok = dprobs())) break;
+            if (elect()) {
+                const uint64_t k = mn_desc(rb + (uint32_t)rc.s * a.slot_bytes);
+                const uint32_t ds = tmem + 128 * (j & 1);
 #pragma unroll
-                for (int s = 0; s < 8; ++s)
-                    mma_f16_tmem_a(tmem + 384, tmem + 128 * (j & 1) + half_col(s), mn_desc(tile(2 * j), s), id_q, j > 0 || s > 0);
-                mma_commit(&bars->empty[2 * j % a.slots]);
+                for (int s = 0; s < 8; ++s) mma_f16_tmem_a(tmem + 384, ds + half_col(s), k + mn_step(s), id_q, j > 0 || s > 0);
+                mma_commit(&bars->empty[rc.s]);
             }
+            rc.step(2, a.slots);
         }
-        if (ok && lane == 0) mma_commit(&bars->done);
+        if (ok && elect()) mma_commit(&bars->done);
         if (*abort) {
-            if (lane == 0) mma_commit(&bars->drain);
+            if (elect()) mma_commit(&bars->drain);
             mbar_wait(&bars->drain, 0, a.hdr, 243);
         }
     } else if (warp == 9) {
@@ -376,9 +394,11 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dq_kernel(const GradArgs a, c
         }
         bool ok = true;
         int issued = 0;
+        RingPos r{0, 1};
         for (int c = 0; ok && c < 2 * tiles; ++c) {
-            const int s = c % a.slots, row = sq.row0 + (it.t0 + c / 2) * TILE;
-            if (!(ok = mbar_wait_abortable(&bars->empty[s], ((uint32_t)(c / a.slots) & 1u) ^ 1u, a.hdr, 244, abort))) break;
+            const int s = r.s, row = sq.row0 + (it.t0 + (c >> 1)) * TILE;
+            if (!(ok = bar_wait(&bars->empty[s], r.turn, a.hdr, 244, abort))) break;
+            r.step(1, a.slots);
             if (lane == 0) {
                 const int nb = c & 1 ? a.v_boxes : a.q_boxes;
                 mbar_arrive_expect_tx(&bars->full[s], BOX * nb);
@@ -401,7 +421,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dq_kernel(const GradArgs a, c
         bool ok = true;
         for (int j = 0; j < tiles; ++j) {
             const uint32_t ts = tmem + lanes + 128 * (j & 1) + 64 * w, td = tmem + lanes + 256 + 64 * w;
-            if (!(ok = mbar_wait_abortable(&bars->s[j & 1], (j >> 1) & 1, a.hdr, 247, abort))) break;
+            if (!(ok = bar_wait(&bars->s[j & 1], (j >> 1) & 1, a.hdr, 247, abort))) break;
             tc_fence_after();
             const int lim = seen - (it.t0 + j) * TILE - 64 * w;
             float p[2][32];
@@ -413,7 +433,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dq_kernel(const GradArgs a, c
 #pragma unroll
                 for (int e = 0; e < 32; ++e) p[c][e] = ex2(fmaf(__uint_as_float(r[e]), g.sl2, -lse2));
             }
-            if (!(ok = mbar_wait_abortable(&bars->dp, j & 1, a.hdr, 248, abort))) break;
+            if (!(ok = bar_wait(&bars->dp, j & 1, a.hdr, 248, abort))) break;
             tc_fence_after();
             const bool edge = __any_sync(~0u, lim < 64);
 #pragma unroll
@@ -434,7 +454,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dq_kernel(const GradArgs a, c
             tc_fence_before();
             mbar_arrive(&bars->ds);
         }
-        if (ok && mbar_wait_abortable(&bars->done, 0, a.hdr, 249, abort)) {
+        if (ok && bar_wait(&bars->done, 0, a.hdr, 249, abort)) {
             tc_fence_after();
             // each half of the warps takes half of the columns
             const int from = 64 * w, width = min(g.d - from, 64);
