@@ -104,12 +104,14 @@ struct PlanHead {      // behind the workspace header
     int pad[62];
 };
 
+constexpr int NEVER = 1 << 30;
+
 struct Plan {          // host side: sizes and places in the workspace
     int pack, heads;           // query heads in a row tile, tiles' heads (grid: items * heads)
     int wide, narrow;          // tokens of a wide and of a narrow tile
-    int keys;                  // keys of a key tile
-    int target;                // items wanted for the whole GPU
-    int least;                 // key tiles of a part, at least
+    int key_shift;             // log2 of the keys of a key tile
+    int blocks;                // that run at a time
+    int least, fine;           // key tiles of a part, at least; of a block's share from which a part is half of it (0: no parts)
     int max_items, max_slots;  // of the list, and of the parts' results a head
     int rows;                  // rows of a part's results
     bool by_keys;              // items are tiles of keys, their cost the query tiles that see them (backward pass)
@@ -118,28 +120,27 @@ struct Plan {          // host side: sizes and places in the workspace
 
 struct PlanArgs {
     Geo g;
-    int wide, narrow, keys, target, least, heads, max_items, max_slots, by_keys;
+    int wide, narrow, key_shift, blocks, least, fine, heads, max_items, max_slots, by_keys;
     WsHeader *hdr;
     PlanHead *head;
     Item *items;
     int *join;
 };
 
-Plan make_plan(const gma_attn_t &a, bool paged, int pack, int wide_rows, int narrow_rows, int keys, int target, int least, bool split,
-               Carve *ws);
+Plan make_plan(const gma_attn_t &a, int pack, int wide_rows, int narrow_rows, int key_shift, int blocks, int least, int fine, Carve *ws);
 PlanArgs plan_args(const Geo &g, const Plan &p, void *ws);
 gma_status_t launch_plan(const PlanArgs &a, const PlanArgs *second, cudaStream_t st);
 
 // ------------------------------------------------------------------ joining the parts of an item
-// Part results: unnormalised sums over the part's keys relative to its maximum, [slot][head][rows][dv], and per row the
-// maximum (in units of the exponent of two; -inf: no key seen) and the sum, [slot][head][rows][2].
+// Part results: unnormalised sums over the part's keys relative to its maximum, [slot][head][rows][pitch] (dv rounded up to
+// four), and per row the maximum (in units of the exponent of two; -inf: no key seen) and the sum, [slot][head][rows][2].
 struct Parts {
     float *o, *stat;
-    int rows, heads, dv;
+    int rows, heads, dv, pitch;
     int *join;
     __device__ __forceinline__ float *o_at(int slot, int head, int row) const
     {
-        return o + (((long long)slot * heads + head) * rows + row) * dv;
+        return o + (((long long)slot * heads + head) * rows + row) * pitch;
     }
     __device__ __forceinline__ float *stat_at(int slot, int head, int row) const
     {
@@ -160,29 +161,49 @@ __device__ __forceinline__ bool last_part(const Parts &p, const Item &it, int he
     return last;
 }
 
-// One warp's row of a joined item: lane-strided columns.
+// One warp's row of a joined item: lanes are parts for the weights, then four columns each for the sums, with the loads of sixteen parts
+// in flight.
 template <typename T>
 __device__ __forceinline__ void join_row(const Parts &p, const Item &it, int head, int row, T *o, float *lse)
 {
     const int lane = threadIdx.x & 31;
     float m = -INFINITY;
-    for (int k = 0; k < it.parts; ++k) m = fmaxf(m, __ldcg(p.stat_at(it.slot + k, head, row)));
-    float l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-    if (m != -INFINITY)
-        for (int k = 0; k < it.parts; ++k) {
-            const float *s = p.stat_at(it.slot + k, head, row);
-            const float f = ex2(__ldcg(s) - m);
-            if (f == 0.f) continue;            // a part that saw nothing wrote no sums
-            l += f * __ldcg(s + 1);
-            const float *x = p.o_at(it.slot + k, head, row);
+    for (int k = lane; k < it.parts; k += 32) m = fmaxf(m, __ldcg(p.stat_at(it.slot + k, head, row)));
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-                if (lane + 32 * c < p.dv) acc[c] += f * __ldcg(x + lane + 32 * c);
+    for (int s = 16; s; s >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, s));
+    float l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const bool mine = 4 * lane < p.dv;
+    for (int k0 = 0; m != -INFINITY && k0 < it.parts; k0 += 32) {
+        float w = 0.f;
+        if (k0 + lane < it.parts) {
+            const float2 s = __ldcg(reinterpret_cast<const float2 *>(p.stat_at(it.slot + k0 + lane, head, row)));
+            w = ex2(s.x - m);
+            l = fmaf(w, s.y, l);
         }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+        const int n = min(32, it.parts - k0);
+        for (int j0 = 0; j0 < n; j0 += 16) {
+            float4 x[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (mine && j0 + j < n) x[j] = __ldcg(reinterpret_cast<const float4 *>(p.o_at(it.slot + k0 + j0 + j, head, row)) + lane);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const float f = __shfl_sync(~0u, w, j0 + j);
+                if (f == 0.f || j0 + j >= n) continue;      // a part that saw nothing wrote no sums
+                acc.x = fmaf(f, x[j].x, acc.x);
+                acc.y = fmaf(f, x[j].y, acc.y);
+                acc.z = fmaf(f, x[j].z, acc.z);
+                acc.w = fmaf(f, x[j].w, acc.w);
+            }
+        }
+    }
+#pragma unroll
+    for (int s = 16; s; s >>= 1) l += __shfl_xor_sync(~0u, l, s);
+    const float inv = l > 0.f ? 1.f / l : 0.f, y[4] = {acc.x, acc.y, acc.z, acc.w};
 #pragma unroll
     for (int c = 0; c < 4; ++c)
-        if (lane + 32 * c < p.dv) o[lane + 32 * c] = from_f32<T>(acc[c] * inv);
+        if (4 * lane + c < p.dv) o[4 * lane + c] = from_f32<T>(y[c] * inv);
     if (lse && lane == 0) *lse = l > 0.f ? (m + log2f(l)) * LN2 : -INFINITY;
 }
 

@@ -1,6 +1,7 @@
 // gma_attn.cu -- softmax attention: the entry points' checks, the plan of a call, and the small kernels around the
 // products: tokens into the cache's pages, zeros behind sequences, do . o of every row.
 #include <algorithm>
+#include <type_traits>
 
 #include "attn_common.cuh"
 #include "attn_tc_host.cuh"
@@ -9,91 +10,136 @@ namespace gma {
 namespace att {
 namespace {
 
+typedef __nv_bfloat16 bf16;
 constexpr int PT = 1024;               // threads of the plan's block
 constexpr int BUCKETS = 1024;          // items are ordered by size up to so many key tiles
 
-// Tiles of sequence q and the key tiles (by_keys: query tiles) of the one that starts at token `tok`.
-__device__ __forceinline__ int item_cost(const PlanArgs &a, const Seq &q, int tok, int tokens, int *first)
+// Exclusive sum over the block's threads; *all: the sum of all of them.
+__device__ __forceinline__ int block_scan(int own, int *warps, int *all)
 {
-    *first = 0;
-    if (a.by_keys) {                   // a tile of keys: the query tiles from the one that first sees it
-        *first = a.g.causal ? tok / a.keys : 0;
-        return (q.n + a.keys - 1) / a.keys - *first;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int sum = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(~0u, sum, o);
+        if (lane >= o) sum += up;
     }
-    const int last = min(tok + tokens, q.n) - 1;
-    return max((q.seen(a.g, last) + a.keys - 1) / a.keys, 1);
+    __syncthreads();
+    if (lane == 31) warps[warp] = sum;
+    __syncthreads();
+    int w = warps[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(~0u, w, o);
+        if (lane >= o) w += up;
+    }
+    *all = __shfl_sync(~0u, w, 31);
+    return sum - own + (warp ? __shfl_sync(~0u, w, warp - 1) : 0);
 }
 
+// A thread a sequence for their numbers of tiles, then a thread a tile (found by bisection) for everything else.  Up to PT sequences
+// are read once; more are gone through PT at a time in every pass.
 __global__ void __launch_bounds__(PT) plan_kernel(const PlanArgs a0, const PlanArgs a1)
 {
     const PlanArgs &a = blockIdx.x ? a1 : a0;
     __shared__ unsigned long long total;
-    __shared__ int count, slots, joins, share, hist[BUCKETS], warps[32];
-    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    __shared__ int slots, joins, hist[BUCKETS], warps[32], first[PT + 1], rows[PT], keys[PT];
+    const int t = threadIdx.x, B = a.g.B, mask = (1 << a.key_shift) - 1;
     blk::let_next();
-    if (t == 0) { total = 0; count = 0; slots = 0; joins = 0; }
+    if (t == 0) { total = 0; slots = 0; joins = 0; }
     hist[t] = 0;
     if (a.hdr && t < (int)(sizeof(WsHeader) / 4)) reinterpret_cast<unsigned *>(a.hdr)[t] = 0;
-    __syncthreads();
-    // wide tiles, or narrow ones
-    int mine = 0;
-    for (int s = t; s < a.g.B; s += PT) {
-        const Seq q = sequence(a.g, s);
-        mine += (q.n + a.wide - 1) / a.wide;
-    }
-    if (mine) atomicAdd(&count, mine);
-    __syncthreads();
-    const int tokens = (long long)count * a.heads < SMS ? a.narrow : a.wide;
-    // all items' key tiles, and an SM's share of them
-    unsigned long long work = 0;
-    int first;
-    for (int s = warp; s < a.g.B; s += PT / 32) {
-        const Seq q = sequence(a.g, s);
-        for (int k = lane; k * (long long)tokens < q.n; k += 32) work += item_cost(a, q, k * tokens, tokens, &first);
-    }
-    if (work) atomicAdd(&total, work);
-    __syncthreads();
-    if (t == 0) {
-        const unsigned long long per = (total * a.heads + a.target - 1) / a.target;
-        share = a.max_slots ? (int)min(max(per, (unsigned long long)a.least), 0x7fffffffull) : 0x7fffffff;
-        count = 0;
-    }
-    __syncthreads();
-    // how many of each size, where those of a size start, and the list
-    for (int pass = 0; pass < 2; ++pass) {
-        for (int s = warp; s < a.g.B; s += PT / 32) {
-            const Seq q = sequence(a.g, s);
-            for (int k = lane; k * (long long)tokens < q.n; k += 32) {
-                const int cost = item_cost(a, q, k * tokens, tokens, &first);
-                const int parts = (int)(((long long)cost + share - 1) / share), size = (cost + parts - 1) / parts;
-                const int bucket = BUCKETS - 1 - min(size, BUCKETS - 1);
-                const int at = atomicAdd(&hist[bucket], parts);
-                if (pass == 0) continue;
-                const int slot = parts > 1 ? atomicAdd(&slots, parts) : 0, join = parts > 1 ? atomicAdd(&joins, 1) : 0;
-                if (parts > 1 && slot + parts > a.max_slots) continue;       // offsets that fall: more tiles than rows
-                for (int p = 0; p < parts; ++p)
-                    if (at + p < a.max_items)
-                        a.items[at + p] = Item{s, k * tokens, first + min(p * size, cost), first + min((p + 1) * size, cost), slot,
-                                               parts, p, join};
+    int tokens = a.wide, count = 0;
+    // reads the sequences from `base` on; the tiles of those before each
+    auto read = [&](int base) {
+        Seq q = {};
+        if (base + t < B) q = sequence(a.g, base + t);
+        __syncthreads();
+        rows[t] = q.n;
+        keys[t] = q.L;
+    };
+    auto number = [&]() {
+        const int n = rows[t], k = n ? (n - 1) / tokens + 1 : 0;
+        int all;
+        const int before = block_scan(k, warps, &all);
+        first[t] = before;
+        if (t == PT - 1) first[PT] = all;
+        __syncthreads();
+        return all;
+    };
+    // f(sequence, first token, first key tile, key tiles) of every tile; by_keys: query tiles of a tile of keys
+    auto each = [&](auto f) {
+        for (int base = 0; base < B; base += PT) {
+            if (B > PT) {
+                read(base);
+                number();
+            }
+            for (int i = t; i < first[PT]; i += PT) {
+                int lo = 0, hi = PT;
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (first[mid] <= i) lo = mid; else hi = mid;
+                }
+                const int n = rows[lo], L = keys[lo], tok = (i - first[lo]) * tokens;
+                int from = 0, cost;
+                if (a.by_keys) {
+                    from = a.g.causal ? tok >> a.key_shift : 0;
+                    cost = ((n + mask) >> a.key_shift) - from;
+                } else {
+                    const int last = min(tok + tokens, n) - 1, pos0 = a.g.cached ? L - n : 0;
+                    const int seen = a.g.causal ? min(max(pos0 + last + 1, 0), L) : L;
+                    cost = max((seen + mask) >> a.key_shift, 1);
+                }
+                f(base + lo, tok, from, cost);
             }
         }
-        __syncthreads();
-        if (pass) break;
-        const int own = hist[t];
-        int sum = own;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int up = __shfl_up_sync(~0u, sum, o);
-            if (lane >= o) sum += up;
-        }
-        if (lane == 31) warps[warp] = sum;
-        __syncthreads();
-        int before = 0;
-        for (int w = 0; w < warp; ++w) before += warps[w];
-        hist[t] = before + sum - own;
-        if (t == PT - 1) count = before + sum;
-        __syncthreads();
+    };
+    // wide tiles, or narrow ones where the wide ones are fewer than the SMs
+    for (int base = 0; base < B; base += PT) {
+        read(base);
+        count += number();
     }
+    if ((long long)count * a.heads < SMS && a.narrow < a.wide) {
+        tokens = a.narrow;
+        if (B <= PT) number();
+    }
+    // all items' key tiles, and a part's share of them
+    int share = 0x7fffffff;
+    if (a.max_slots) {
+        unsigned long long work = 0;
+        each([&](int, int, int, int cost) { work += cost; });
+#pragma unroll
+        for (int o = 16; o; o >>= 1) work += __shfl_xor_sync(~0u, work, o);
+        if ((t & 31) == 0 && work) atomicAdd(&total, work);
+        __syncthreads();
+        const unsigned long long all = total * a.heads;
+        unsigned long long per = (all + a.blocks - 1) / a.blocks;              // a block's share
+        // long shares are cut further, so that blocks that finish early find more to do
+        if (per > (unsigned long long)a.fine) per = max((unsigned long long)a.fine, (per + 1) / 2);
+        share = (int)min(max(per, (unsigned long long)a.least), 0x7fffffffull);
+    }
+    // how many of each size, where those of a size start, and the list
+    auto parts_of = [&](int cost) { return cost <= share ? 1 : (cost - 1) / share + 1; };
+    auto bucket_of = [&](int cost, int parts) { return BUCKETS - 1 - min(parts == 1 ? cost : (cost - 1) / parts + 1, BUCKETS - 1); };
+    each([&](int, int, int, int cost) {
+        const int parts = parts_of(cost);
+        atomicAdd(&hist[bucket_of(cost, parts)], parts);
+    });
+    __syncthreads();
+    const int own = hist[t];
+    const int start = block_scan(own, warps, &count);
+    hist[t] = start;
+    __syncthreads();
+    each([&](int s, int tok, int from, int cost) {
+        const int parts = parts_of(cost), size = parts == 1 ? cost : (cost - 1) / parts + 1;
+        const int at = atomicAdd(&hist[bucket_of(cost, parts)], parts);
+        const int slot = parts > 1 ? atomicAdd(&slots, parts) : 0, join = parts > 1 ? atomicAdd(&joins, 1) : 0;
+        if (parts > 1 && slot + parts > a.max_slots) return;         // offsets that fall: more tiles than rows
+        for (int p = 0; p < parts; ++p)
+            if (at + p < a.max_items)
+                a.items[at + p] = Item{s, tok, from + min(p * size, cost), from + min((p + 1) * size, cost), slot, parts, p, join};
+    });
+    __syncthreads();
     for (int i = t; i < joins * a.heads && i < a.max_slots * a.heads; i += PT) a.join[i] = 0;
     if (t == 0) {
         a.head->items = min(count, a.max_items);
@@ -120,27 +166,38 @@ __global__ void __launch_bounds__(256) attn_tail_kernel(const Geo g, const Heads
     }
 }
 
-// delta = do . o: a warp a (row, head).
-template <typename T>
+// delta = do . o: LANES lanes a (row, head), eight elements each (VEC) or every LANES-th.
+template <typename T, bool VEC, int LANES>
 __global__ void __launch_bounds__(256) attn_delta_kernel(const Geo g, const Heads<const T> o, const Heads<const T> d_o, float *delta,
                                                          long long rows)
 {
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x % LANES;
     blk::let_next();
-    for (long long r = blockIdx.x * 8ll + (threadIdx.x >> 5); r < rows; r += gridDim.x * 8ll) {
-        const long long bh = r / g.N, i = r - bh * g.N;
-        const int b = (int)(bh / g.H), h = (int)(bh - (long long)b * g.H);
-        if (g.offsets) {
-            if (i < max(g.offsets[0], 0) || i >= g.offsets[g.B]) continue;
-        } else if (i >= blk::row_length(g.lengths, b, g.N)) {
-            continue;
-        }
-        const T *x = o.at(b, i, h), *y = d_o.at(b, i, h);
+    for (long long r0 = blockIdx.x * (256ll / LANES); r0 < rows; r0 += gridDim.x * (256ll / LANES)) {
+        const long long r = r0 + threadIdx.x / LANES;         // heads inner: neighbouring rows of lanes read neighbouring heads
+        bool is = r < rows;
+        const long long bi = r / g.H;
+        const int h = (int)(r - bi * g.H), b = (int)(bi / g.N);
+        const long long i = bi - (long long)b * g.N;
+        if (is) is = g.offsets ? i >= max(g.offsets[0], 0) && i < g.offsets[g.B] : i < blk::row_length(g.lengths, b, g.N);
         float s = 0.f;
-        for (int c = lane; c < g.dv; c += 32) s = fmaf(to_f32<T>(x[c]), to_f32<T>(y[c]), s);
+        if (is) {
+            const T *x = o.at(b, i, h), *y = d_o.at(b, i, h);
+            if (VEC) {
+                if (8 * lane < g.dv) {
+                    float u[8], v[8];
+                    blk::load8<true>(x + 8 * lane, 8, u);
+                    blk::load8<true>(y + 8 * lane, 8, v);
 #pragma unroll
-        for (int m = 16; m; m >>= 1) s += __shfl_xor_sync(~0u, s, m);
-        if (lane == 0) delta[r] = s;
+                    for (int c = 0; c < 8; ++c) s = fmaf(u[c], v[c], s);
+                }
+            } else {
+                for (int c = lane; c < g.dv; c += LANES) s = fmaf(to_f32<T>(x[c]), to_f32<T>(y[c]), s);
+            }
+        }
+#pragma unroll
+        for (int m = LANES / 2; m; m >>= 1) s += __shfl_xor_sync(~0u, s, m);
+        if (is && lane == 0) delta[((long long)b * g.H + h) * g.N + i] = s;
     }
     blk::wait_previous();
 }
@@ -303,23 +360,24 @@ Geo geo_of(const gma_attn_t &a, const gma_attn_paged_t *p)
     return g;
 }
 
-Plan make_plan(const gma_attn_t &a, bool paged, int pack, int wide_rows, int narrow_rows, int keys, int target, int least, bool split,
-               Carve *ws)
+Plan make_plan(const gma_attn_t &a, int pack, int wide_rows, int narrow_rows, int key_shift, int blocks, int least, int fine, Carve *ws)
 {
     Plan p = {};
     p.pack = pack;
     p.heads = a.H / pack;
     p.narrow = std::max(narrow_rows / pack, 1);
     p.wide = p.narrow * (wide_rows / narrow_rows);
-    p.keys = keys;
-    p.target = target;
+    p.key_shift = key_shift;
+    p.blocks = blocks;
     p.least = least;
+    p.fine = fine;
     // tiles of n rows and of every sequence's last rows; wide tiles are the fewer
     const long long n = (long long)a.N * batches(a);
     long long narrow = n / p.narrow + a.B, wide = n / p.wide + a.B;
     // narrow ones are taken where the wide ones are fewer than SMS / heads, so that they are at most twice as many and one
     const long long most = std::max(wide, std::min(narrow, (long long)(wide_rows / narrow_rows + 1) * (SMS / p.heads + 1)));
-    const long long extra = split ? 2ll * target / p.heads + 2 : 0;          // parts beyond the first of each
+    // items longer than a part become at most twice as many parts as the call's work holds, which is `blocks` shares
+    const long long extra = !fine ? 0 : (fine < NEVER ? 4ll : 2ll) * blocks / p.heads + 2;
     p.max_items = (int)(most + extra);
     p.max_slots = (int)extra;
     p.rows = (int)std::min<long long>(p.wide, n) * pack;
@@ -327,14 +385,14 @@ Plan make_plan(const gma_attn_t &a, bool paged, int pack, int wide_rows, int nar
     p.items_at = ws->take((size_t)p.max_items * sizeof(Item));
     p.join_at = ws->take((size_t)p.max_slots * p.heads * sizeof(int));
     p.stat_at = ws->take((size_t)p.max_slots * p.heads * p.rows * 2 * sizeof(float));
-    p.part_at = ws->take((size_t)p.max_slots * p.heads * p.rows * a.dv * sizeof(float));
+    p.part_at = ws->take((size_t)p.max_slots * p.heads * p.rows * ((a.dv + 3) & ~3) * sizeof(float));
     return p;
 }
 
 PlanArgs plan_args(const Geo &g, const Plan &p, void *ws)
 {
     char *w = (char *)ws;
-    return PlanArgs{g, p.wide, p.narrow, p.keys, p.target, p.least, p.heads, p.max_items, p.max_slots, p.by_keys, (WsHeader *)ws,
+    return PlanArgs{g, p.wide, p.narrow, p.key_shift, p.blocks, p.least, p.fine, p.heads, p.max_items, p.max_slots, p.by_keys, (WsHeader *)ws,
                     (PlanHead *)(w + p.head_at), (Item *)(w + p.items_at), (int *)(w + p.join_at)};
 }
 
@@ -349,14 +407,22 @@ gma_status_t launch_delta(const gma_attn_grad_t &g, float *delta, cudaStream_t s
     const gma_attn_t &a = g.fwd;
     const Geo geo = geo_of(a, nullptr);
     const long long rows = batches(a) * a.H * a.N;
-    const unsigned blocks = row_blocks(rows);
-    if (a.dtype == GMA_BF16)
-        GMA_LAUNCH(KID_ATTN_DELTA, st, launch_pdl(attn_delta_kernel<__nv_bfloat16>, blocks, 256, 0, st, geo, heads_of<const __nv_bfloat16>(a.o),
-                                                  heads_of<const __nv_bfloat16>(g.d_o), delta, rows));
-    else
-        GMA_LAUNCH(KID_ATTN_DELTA, st, launch_pdl(attn_delta_kernel<float>, blocks, 256, 0, st, geo, heads_of<const float>(a.o),
-                                                  heads_of<const float>(g.d_o), delta, rows));
-    return GMA_OK;
+    const bool vec = a.dv % 8 == 0 && heads_vec(a.o, a.dtype) && heads_vec(g.d_o, a.dtype);
+    auto launch = [&](auto type, auto v, auto lanes) -> gma_status_t {
+        using T = decltype(type);
+        constexpr int LANES = decltype(lanes)::value;
+        const unsigned blocks = (unsigned)std::min<long long>((rows + 256 / LANES - 1) / (256 / LANES), SMS * 32);
+        GMA_LAUNCH(KID_ATTN_DELTA, st, launch_pdl(attn_delta_kernel<T, decltype(v)::value, LANES>, blocks, 256, 0, st, geo, heads_of<const T>(a.o),
+                                                  heads_of<const T>(g.d_o), delta, rows));
+        return GMA_OK;
+    };
+    using Yes = std::true_type;
+    using No = std::false_type;
+    if (!vec)
+        return a.dtype == GMA_BF16 ? launch(bf16(), No(), std::integral_constant<int, 32>()) : launch(float(), No(), std::integral_constant<int, 32>());
+    if (a.dv <= 64)
+        return a.dtype == GMA_BF16 ? launch(bf16(), Yes(), std::integral_constant<int, 8>()) : launch(float(), Yes(), std::integral_constant<int, 8>());
+    return a.dtype == GMA_BF16 ? launch(bf16(), Yes(), std::integral_constant<int, 16>()) : launch(float(), Yes(), std::integral_constant<int, 16>());
 }
 
 }  // namespace att

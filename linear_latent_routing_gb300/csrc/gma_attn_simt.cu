@@ -348,7 +348,7 @@ template <typename... P> bool allow(void (*kern)(P...))
 Plan plan_of(const gma_attn_t &a, const gma_attn_paged_t *paged, Carve *c)
 {
     const int group = a.H / a.G, pack = paged && group <= R ? group : 1;
-    return make_plan(a, paged != nullptr, pack, R, R, KT, 2 * SMS, 4, true, c);
+    return make_plan(a, pack, R, R, 6, SMS, 2, paged ? 32 : NEVER, c);
 }
 
 template <typename T>
@@ -366,7 +366,7 @@ Args<T> args_of(const gma_attn_t &a, const gma_attn_paged_t *paged, const Plan &
     x.heads = p.heads;
     x.head = (const PlanHead *)(w + p.head_at);
     x.items = (const Item *)(w + p.items_at);
-    x.parts = Parts{(float *)(w + p.part_at), (float *)(w + p.stat_at), p.rows, p.heads, a.dv, (int *)(w + p.join_at)};
+    x.parts = Parts{(float *)(w + p.part_at), (float *)(w + p.stat_at), p.rows, p.heads, a.dv, (a.dv + 3) & ~3, (int *)(w + p.join_at)};
     return x;
 }
 
@@ -397,10 +397,10 @@ struct GradPlan {
 GradPlan grad_plan(const gma_attn_t &a, Carve *c)
 {
     GradPlan p;
-    p.q = make_plan(a, false, 1, R, R, KT, SMS, 1, false, c);
+    p.q = make_plan(a, 1, R, R, 6, SMS, 1, 0, c);
     gma_attn_t by = a;
     by.H = a.G;                       // a tile of keys serves the whole group
-    p.k = make_plan(by, false, 1, R, R, KT, SMS, 1, false, c);
+    p.k = make_plan(by, 1, R, R, 6, SMS, 1, 0, c);
     p.k.by_keys = true;
     p.delta_at = c->take((size_t)(a.offsets ? 1 : a.B) * a.H * a.N * sizeof(float));
     return p;

@@ -445,7 +445,7 @@ namespace {
 Plan plan_of(const gma_attn_t &a, const gma_attn_paged_t *paged, Carve *c)
 {
     const int group = a.H / a.G, pack = paged && group <= TILE ? group : 1;
-    return make_plan(a, paged != nullptr, pack, 2 * TILE, TILE, TILE, paged ? 3 * SMS : SMS, 4, true, c);
+    return make_plan(a, pack, 2 * TILE, TILE, 7, SMS, 4, paged ? 32 : NEVER, c);
 }
 
 }  // namespace
@@ -481,7 +481,7 @@ gma_status_t tc_forward(const gma_attn_t &a, const gma_attn_paged_t *p, void *ws
     x.o_vec = store_vec(a.o, a.dv);
     x.head = (const PlanHead *)(w + pl.head_at);
     x.items = (const Item *)(w + pl.items_at);
-    x.parts = Parts{(float *)(w + pl.part_at), (float *)(w + pl.stat_at), pl.rows, pl.heads, a.dv, (int *)(w + pl.join_at)};
+    x.parts = Parts{(float *)(w + pl.part_at), (float *)(w + pl.stat_at), pl.rows, pl.heads, a.dv, (a.dv + 3) & ~3, (int *)(w + pl.join_at)};
     x.hdr = (WsHeader *)ws;
     x.q_boxes = (a.d + 63) / 64;
     x.v_boxes = (a.dv + 63) / 64;
