@@ -89,30 +89,29 @@ __device__ __forceinline__ int page_of(const Geo &g, int s, int j, int *slot)
 // ------------------------------------------------------------------ the plan
 // A launch of one block cuts a call into items: a tile of query rows of one sequence (all heads alike) and a range of
 // key tiles.  A row of the tile is a (token, head of a group of `pack`) pair, tokens outer.  Items come largest first,
-// so that the last ones to start are short.  Tiles are narrow ones where wide ones would leave SMs without work, and
-// items whose keys are more than an SM's share of the call are cut, their parts joined by the last one to finish.
+// so that the last ones to start are short.  Tiles are narrow ones where wide ones would leave SMs without work; over a cache,
+// where few rows may face many keys, items are cut into parts, which a last launch joins.
 struct Item {
     int seq, tok0;     // sequence, first token of the tile
     int t0, t1;        // key tiles
     int slot, parts;   // first slot of the parts' results, how many parts (1: no slot)
-    int part, join;    // this part, counter of the parts that have finished
+    int part, pad;     // this part
 };
 
 struct PlanHead {      // behind the workspace header
     int items;         // how many
     int tokens;        // tokens of a tile
-    int pad[62];
+    int ticket;        // of the next item, where blocks take them one after another
+    int joins;         // items that were cut
+    int pad[60];
 };
-
-constexpr int NEVER = 1 << 30;
 
 struct Plan {          // host side: sizes and places in the workspace
     int pack, heads;           // query heads in a row tile, tiles' heads (grid: items * heads)
     int wide, narrow;          // tokens of a wide and of a narrow tile
     int key_shift;             // log2 of the keys of a key tile
     int blocks;                // that run at a time
-    int least, fine;           // key tiles of a part, at least; of a block's share from which a part is half of it (0: no parts)
-    int max_items, max_slots;  // of the list, and of the parts' results a head
+    int max_items, max_slots;  // of the list, and of the parts' results a head (0: items are not cut)
     int rows;                  // rows of a part's results
     bool by_keys;              // items are tiles of keys, their cost the query tiles that see them (backward pass)
     size_t head_at, items_at, join_at, part_at, stat_at;
@@ -120,24 +119,24 @@ struct Plan {          // host side: sizes and places in the workspace
 
 struct PlanArgs {
     Geo g;
-    int wide, narrow, key_shift, blocks, least, fine, heads, max_items, max_slots, by_keys;
+    int wide, narrow, key_shift, blocks, heads, max_items, max_slots, by_keys;
+    float part_cost;           // what a part costs beside its keys, in key tiles
     WsHeader *hdr;
     PlanHead *head;
     Item *items;
-    int *join;
+    int *join;                 // first parts of the items that were cut
 };
 
-Plan make_plan(const gma_attn_t &a, int pack, int wide_rows, int narrow_rows, int key_shift, int blocks, int least, int fine, Carve *ws);
+Plan make_plan(const gma_attn_t &a, int pack, int wide_rows, int narrow_rows, int key_shift, int blocks, bool cut, Carve *ws);
 PlanArgs plan_args(const Geo &g, const Plan &p, void *ws);
 gma_status_t launch_plan(const PlanArgs &a, const PlanArgs *second, cudaStream_t st);
 
-// ------------------------------------------------------------------ joining the parts of an item
+// ------------------------------------------------------------------ the parts of an item
 // Part results: unnormalised sums over the part's keys relative to its maximum, [slot][head][rows][pitch] (dv rounded up to
 // four), and per row the maximum (in units of the exponent of two; -inf: no key seen) and the sum, [slot][head][rows][2].
 struct Parts {
     float *o, *stat;
     int rows, heads, dv, pitch;
-    int *join;
     __device__ __forceinline__ float *o_at(int slot, int head, int row) const
     {
         return o + (((long long)slot * heads + head) * rows + row) * pitch;
@@ -148,64 +147,13 @@ struct Parts {
     }
 };
 
-// Called by all threads of a block once its part lies in its slot: whether this block is the last of its item's.  The
-// parts are then added in their order, whoever adds them.
-__device__ __forceinline__ bool last_part(const Parts &p, const Item &it, int head, int *flag)
+inline Parts parts_of(const Plan &p, const gma_attn_t &a, void *ws)
 {
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) *flag = atomicAdd(p.join + (long long)it.join * p.heads + head, 1) == it.parts - 1;
-    __syncthreads();
-    const bool last = *flag != 0;
-    if (last) __threadfence();
-    return last;
+    return Parts{(float *)((char *)ws + p.part_at), (float *)((char *)ws + p.stat_at), p.rows, p.heads, a.dv, (a.dv + 3) & ~3};
 }
 
-// One warp's row of a joined item: lanes are parts for the weights, then four columns each for the sums, with the loads of sixteen parts
-// in flight.
-template <typename T>
-__device__ __forceinline__ void join_row(const Parts &p, const Item &it, int head, int row, T *o, float *lse)
-{
-    const int lane = threadIdx.x & 31;
-    float m = -INFINITY;
-    for (int k = lane; k < it.parts; k += 32) m = fmaxf(m, __ldcg(p.stat_at(it.slot + k, head, row)));
-#pragma unroll
-    for (int s = 16; s; s >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, s));
-    float l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    const bool mine = 4 * lane < p.dv;
-    for (int k0 = 0; m != -INFINITY && k0 < it.parts; k0 += 32) {
-        float w = 0.f;
-        if (k0 + lane < it.parts) {
-            const float2 s = __ldcg(reinterpret_cast<const float2 *>(p.stat_at(it.slot + k0 + lane, head, row)));
-            w = ex2(s.x - m);
-            l = fmaf(w, s.y, l);
-        }
-        const int n = min(32, it.parts - k0);
-        for (int j0 = 0; j0 < n; j0 += 16) {
-            float4 x[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-                if (mine && j0 + j < n) x[j] = __ldcg(reinterpret_cast<const float4 *>(p.o_at(it.slot + k0 + j0 + j, head, row)) + lane);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const float f = __shfl_sync(~0u, w, j0 + j);
-                if (f == 0.f || j0 + j >= n) continue;      // a part that saw nothing wrote no sums
-                acc.x = fmaf(f, x[j].x, acc.x);
-                acc.y = fmaf(f, x[j].y, acc.y);
-                acc.z = fmaf(f, x[j].z, acc.z);
-                acc.w = fmaf(f, x[j].w, acc.w);
-            }
-        }
-    }
-#pragma unroll
-    for (int s = 16; s; s >>= 1) l += __shfl_xor_sync(~0u, l, s);
-    const float inv = l > 0.f ? 1.f / l : 0.f, y[4] = {acc.x, acc.y, acc.z, acc.w};
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-        if (4 * lane + c < p.dv) o[4 * lane + c] = from_f32<T>(y[c] * inv);
-    if (lse && lane == 0) *lse = l > 0.f ? (m + log2f(l)) * LN2 : -INFINITY;
-}
+// Adds up the parts of the items that the plan cut, in their order.
+gma_status_t launch_join(const gma_attn_t &a, const Geo &g, const Plan &p, void *ws, cudaStream_t st);
 
 // ------------------------------------------------------------------ kernels
 Geo geo_of(const gma_attn_t &a, const gma_attn_paged_t *paged);

@@ -58,6 +58,11 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map
                  : "memory");
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)map) : "memory");
+}
+
 // One lane of a converged warp, the same one every time.  Where it issues the products the compiler knows that one thread does, and
 // their operands stay in uniform registers.
 __device__ __forceinline__ bool elect()

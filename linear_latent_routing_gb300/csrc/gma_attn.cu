@@ -13,6 +13,8 @@ namespace {
 typedef __nv_bfloat16 bf16;
 constexpr int PT = 1024;               // threads of the plan's block
 constexpr int BUCKETS = 1024;          // items are ordered by size up to so many key tiles
+constexpr int COSTS = 4096;            // tiles up to which cutting is looked at
+constexpr float ITEM_COST = 2.f;       // what an item costs beside its keys, in key tiles
 
 // Exclusive sum over the block's threads; *all: the sum of all of them.
 __device__ __forceinline__ int block_scan(int own, int *warps, int *all)
@@ -43,10 +45,11 @@ __global__ void __launch_bounds__(PT) plan_kernel(const PlanArgs a0, const PlanA
 {
     const PlanArgs &a = blockIdx.x ? a1 : a0;
     __shared__ unsigned long long total;
-    __shared__ int slots, joins, hist[BUCKETS], warps[32], first[PT + 1], rows[PT], keys[PT];
+    __shared__ int slots, joins, filled, largest, hist[BUCKETS], warps[32], first[PT + 1], rows[PT], keys[PT], costs[COSTS], sizes[32];
+    __shared__ float times[32];
     const int t = threadIdx.x, B = a.g.B, mask = (1 << a.key_shift) - 1;
     blk::let_next();
-    if (t == 0) { total = 0; slots = 0; joins = 0; }
+    if (t == 0) { total = 0; slots = 0; joins = 0; filled = 0; largest = 0; }
     hist[t] = 0;
     if (a.hdr && t < (int)(sizeof(WsHeader) / 4)) reinterpret_cast<unsigned *>(a.hdr)[t] = 0;
     int tokens = a.wide, count = 0;
@@ -103,20 +106,57 @@ __global__ void __launch_bounds__(PT) plan_kernel(const PlanArgs a0, const PlanA
         tokens = a.narrow;
         if (B <= PT) number();
     }
-    // all items' key tiles, and a part's share of them
+    // a part's key tiles: each warp estimates the time with another size, half a block's share of the call to five of them
     int share = 0x7fffffff;
     if (a.max_slots) {
         unsigned long long work = 0;
-        each([&](int, int, int, int cost) { work += cost; });
+        int most = 0;
+        each([&](int, int, int, int cost) {
+            work += cost;
+            most = max(most, cost);
+            const int at = atomicAdd(&filled, 1);
+            if (at < COSTS) costs[at] = cost;
+        });
 #pragma unroll
-        for (int o = 16; o; o >>= 1) work += __shfl_xor_sync(~0u, work, o);
-        if ((t & 31) == 0 && work) atomicAdd(&total, work);
+        for (int o = 16; o; o >>= 1) {
+            work += __shfl_xor_sync(~0u, work, o);
+            most = max(most, __shfl_xor_sync(~0u, most, o));
+        }
+        if ((t & 31) == 0 && work) {
+            atomicAdd(&total, work);
+            atomicMax(&largest, most);
+        }
         __syncthreads();
-        const unsigned long long all = total * a.heads;
-        unsigned long long per = (all + a.blocks - 1) / a.blocks;              // a block's share
-        // long shares are cut further, so that blocks that finish early find more to do
-        if (per > (unsigned long long)a.fine) per = max((unsigned long long)a.fine, (per + 1) / 2);
-        share = (int)min(max(per, (unsigned long long)a.least), 0x7fffffffull);
+        const int n = filled;
+        const float all = (float)total * a.heads, per = all / a.blocks;
+        if (n <= COSTS && n) {                       // more tiles than that fill the GPU as they are
+            const int warp = t >> 5, lane = t & 31;
+            const int size = max((int)ceilf(per * 0.5f * exp2f(warp * (3.3f / 31))), 1);
+            int parts = 0, cut = 0;
+            for (int i = lane; i < n; i += 32) {
+                const int k = costs[i] <= size ? 1 : (costs[i] - 1) / size + 1;
+                parts += k;
+                if (k > 1) cut += k;
+            }
+#pragma unroll
+            for (int o = 16; o; o >>= 1) {
+                parts += __shfl_xor_sync(~0u, parts, o);
+                cut += __shfl_xor_sync(~0u, cut, o);
+            }
+            const float items = (float)parts * a.heads, extra = ITEM_COST * items + a.part_cost * cut * a.heads;
+            const int cuts = largest <= size ? 1 : (largest - 1) / size + 1;
+            const float longest = (float)((largest - 1) / cuts + 1) + ITEM_COST + (cuts > 1 ? a.part_cost : 0.f);
+            const float mean = (all + extra) / items, waves = ceilf(items / a.blocks);
+            // equal items run in whole waves; unequal ones, the longest first, fill the gaps
+            const float time = longest < 1.2f * mean || items <= a.blocks ? waves * longest
+                                                                          : fmaxf((all + extra) / a.blocks + 0.5f * mean, longest);
+            if (lane == 0) times[warp] = time, sizes[warp] = size;
+            __syncthreads();
+            float best = times[0];
+            share = sizes[0];
+            for (int w = 1; w < 32; ++w)
+                if (times[w] <= best) best = times[w], share = sizes[w];
+        }
     }
     // how many of each size, where those of a size start, and the list
     auto parts_of = [&](int cost) { return cost <= share ? 1 : (cost - 1) / share + 1; };
@@ -133,17 +173,78 @@ __global__ void __launch_bounds__(PT) plan_kernel(const PlanArgs a0, const PlanA
     each([&](int s, int tok, int from, int cost) {
         const int parts = parts_of(cost), size = parts == 1 ? cost : (cost - 1) / parts + 1;
         const int at = atomicAdd(&hist[bucket_of(cost, parts)], parts);
-        const int slot = parts > 1 ? atomicAdd(&slots, parts) : 0, join = parts > 1 ? atomicAdd(&joins, 1) : 0;
-        if (parts > 1 && slot + parts > a.max_slots) return;         // offsets that fall: more tiles than rows
+        const int slot = parts > 1 ? atomicAdd(&slots, parts) : 0;
         for (int p = 0; p < parts; ++p)
-            if (at + p < a.max_items)
-                a.items[at + p] = Item{s, tok, from + min(p * size, cost), from + min((p + 1) * size, cost), slot, parts, p, join};
+            if (at + p < a.max_items) {
+                // offsets that fall may make more tiles than there are rows: an item without room for its parts is not worked on
+                const bool room = parts == 1 || (slot + parts <= a.max_slots && at + parts <= a.max_items);
+                a.items[at + p] = Item{s, tok, from + min(p * size, cost), from + min((p + 1) * size, cost), room ? slot : 0, parts, room ? p : -1, 0};
+                if (room && parts > 1 && p == 0) a.join[atomicAdd(&joins, 1)] = at;
+            }
     });
     __syncthreads();
-    for (int i = t; i < joins * a.heads && i < a.max_slots * a.heads; i += PT) a.join[i] = 0;
     if (t == 0) {
         a.head->items = min(count, a.max_items);
         a.head->tokens = tokens;
+        a.head->ticket = 0;
+        a.head->joins = joins;
+    }
+}
+
+// A warp a row of a cut item: lanes are parts for the weights, then four columns each for the sums, with the loads of sixteen parts
+// in flight.
+template <typename T>
+__global__ void __launch_bounds__(256) attn_join_kernel(const Geo g, const PlanHead *head, const Item *items, const int *join, const Parts p,
+                                                        const Heads<T> out, float *lse, int pack)
+{
+    const int lane = threadIdx.x & 31;
+    blk::wait_previous();
+    const long long rows = (long long)head->tokens * pack, n = (long long)head->joins * p.heads * rows;
+    for (long long i = blockIdx.x * 8ll + (threadIdx.x >> 5); i < n; i += gridDim.x * 8ll) {
+        const int row = (int)(i % rows), hj = (int)((i / rows) % p.heads);
+        const Item it = items[join[i / (rows * p.heads)]];
+        const Seq q = sequence(g, it.seq);
+        const int tok = it.tok0 + row / pack, h = pack == 1 ? hj : hj * pack + row % pack;
+        if (tok >= q.n) continue;
+        float m = -INFINITY;
+        for (int k = lane; k < it.parts; k += 32) m = fmaxf(m, p.stat_at(it.slot + k, hj, row)[0]);
+#pragma unroll
+        for (int s = 16; s; s >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, s));
+        float l = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        const bool mine = 4 * lane < p.dv;
+        for (int k0 = 0; m != -INFINITY && k0 < it.parts; k0 += 32) {
+            float w = 0.f;
+            if (k0 + lane < it.parts) {
+                const float2 s = *reinterpret_cast<const float2 *>(p.stat_at(it.slot + k0 + lane, hj, row));
+                w = ex2(s.x - m);
+                l = fmaf(w, s.y, l);
+            }
+            const int n = min(32, it.parts - k0);
+            for (int j0 = 0; j0 < n; j0 += 16) {
+                float4 x[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (mine && j0 + j < n) x[j] = reinterpret_cast<const float4 *>(p.o_at(it.slot + k0 + j0 + j, hj, row))[lane];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const float f = __shfl_sync(~0u, w, j0 + j);
+                    if (f == 0.f || j0 + j >= n) continue;      // a part that saw nothing wrote no sums
+                    acc.x = fmaf(f, x[j].x, acc.x);
+                    acc.y = fmaf(f, x[j].y, acc.y);
+                    acc.z = fmaf(f, x[j].z, acc.z);
+                    acc.w = fmaf(f, x[j].w, acc.w);
+                }
+            }
+        }
+#pragma unroll
+        for (int s = 16; s; s >>= 1) l += __shfl_xor_sync(~0u, l, s);
+        const float inv = l > 0.f ? 1.f / l : 0.f, y[4] = {acc.x, acc.y, acc.z, acc.w};
+        T *o = out.at(q.b, q.row0 + tok, h);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            if (4 * lane + c < p.dv) o[4 * lane + c] = from_f32<T>(y[c] * inv);
+        if (lse && lane == 0) lse[stat_at(g, q, h, tok)] = l > 0.f ? (m + log2f(l)) * LN2 : -INFINITY;
     }
 }
 
@@ -360,7 +461,7 @@ Geo geo_of(const gma_attn_t &a, const gma_attn_paged_t *p)
     return g;
 }
 
-Plan make_plan(const gma_attn_t &a, int pack, int wide_rows, int narrow_rows, int key_shift, int blocks, int least, int fine, Carve *ws)
+Plan make_plan(const gma_attn_t &a, int pack, int wide_rows, int narrow_rows, int key_shift, int blocks, bool cut, Carve *ws)
 {
     Plan p = {};
     p.pack = pack;
@@ -369,21 +470,19 @@ Plan make_plan(const gma_attn_t &a, int pack, int wide_rows, int narrow_rows, in
     p.wide = p.narrow * (wide_rows / narrow_rows);
     p.key_shift = key_shift;
     p.blocks = blocks;
-    p.least = least;
-    p.fine = fine;
     // tiles of n rows and of every sequence's last rows; wide tiles are the fewer
     const long long n = (long long)a.N * batches(a);
     long long narrow = n / p.narrow + a.B, wide = n / p.wide + a.B;
     // narrow ones are taken where the wide ones are fewer than SMS / heads, so that they are at most twice as many and one
     const long long most = std::max(wide, std::min(narrow, (long long)(wide_rows / narrow_rows + 1) * (SMS / p.heads + 1)));
-    // items longer than a part become at most twice as many parts as the call's work holds, which is `blocks` shares
-    const long long extra = !fine ? 0 : (fine < NEVER ? 4ll : 2ll) * blocks / p.heads + 2;
+    // the call's work is `blocks` shares and a part at least half of one; items longer than a part make at most twice as many
+    const long long extra = cut ? 4ll * blocks / p.heads + 2 : 0;
     p.max_items = (int)(most + extra);
     p.max_slots = (int)extra;
     p.rows = (int)std::min<long long>(p.wide, n) * pack;
     p.head_at = ws->take(sizeof(PlanHead));
     p.items_at = ws->take((size_t)p.max_items * sizeof(Item));
-    p.join_at = ws->take((size_t)p.max_slots * p.heads * sizeof(int));
+    p.join_at = ws->take((size_t)p.max_slots * sizeof(int));
     p.stat_at = ws->take((size_t)p.max_slots * p.heads * p.rows * 2 * sizeof(float));
     p.part_at = ws->take((size_t)p.max_slots * p.heads * p.rows * ((a.dv + 3) & ~3) * sizeof(float));
     return p;
@@ -392,13 +491,29 @@ Plan make_plan(const gma_attn_t &a, int pack, int wide_rows, int narrow_rows, in
 PlanArgs plan_args(const Geo &g, const Plan &p, void *ws)
 {
     char *w = (char *)ws;
-    return PlanArgs{g, p.wide, p.narrow, p.key_shift, p.blocks, p.least, p.fine, p.heads, p.max_items, p.max_slots, p.by_keys, (WsHeader *)ws,
+    return PlanArgs{g, p.wide, p.narrow, p.key_shift, p.blocks, p.heads, p.max_items, p.max_slots, p.by_keys, 1.f + p.rows / 64.f, (WsHeader *)ws,
                     (PlanHead *)(w + p.head_at), (Item *)(w + p.items_at), (int *)(w + p.join_at)};
 }
 
 gma_status_t launch_plan(const PlanArgs &a, const PlanArgs *second, cudaStream_t st)
 {
     GMA_LAUNCH(KID_ATTN_PLAN, st, plan_kernel<<<second ? 2 : 1, PT, 0, st>>>(a, second ? *second : a));
+    return GMA_OK;
+}
+
+gma_status_t launch_join(const gma_attn_t &a, const Geo &g, const Plan &p, void *ws, cudaStream_t st)
+{
+    const char *w = (const char *)ws;
+    const PlanHead *head = (const PlanHead *)(w + p.head_at);
+    const Item *items = (const Item *)(w + p.items_at);
+    const int *join = (const int *)(w + p.join_at);
+    const Parts parts = parts_of(p, a, ws);
+    // as many rows as there may be in the parts
+    const unsigned blocks = (unsigned)std::min<long long>(((long long)p.max_slots / 2 * p.heads * p.rows + 7) / 8, 4 * SMS);
+    if (a.dtype == GMA_BF16)
+        GMA_LAUNCH(KID_ATTN_JOIN, st, launch_pdl(attn_join_kernel<bf16>, blocks, 256, 0, st, g, head, items, join, parts, heads_of<bf16>(a.o), a.lse, p.pack));
+    else
+        GMA_LAUNCH(KID_ATTN_JOIN, st, launch_pdl(attn_join_kernel<float>, blocks, 256, 0, st, g, head, items, join, parts, heads_of<float>(a.o), a.lse, p.pack));
     return GMA_OK;
 }
 

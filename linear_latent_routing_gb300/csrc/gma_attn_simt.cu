@@ -96,13 +96,14 @@ template <typename T, bool PAGED>
 __global__ void __launch_bounds__(TH, 2) attn_simt_kernel(const Args<T> a)
 {
     extern __shared__ __align__(16) float smem[];
-    __shared__ int flag;
     __shared__ long long page_at[KT];            // page * 2^20 + slot of every key of the tile, or -1
+    if (PAGED) blk::let_next();
     blk::wait_previous();
     const int rank = blockIdx.x / a.heads, head = blockIdx.x % a.heads;
     if (rank >= a.head->items) return;
     const Geo &g = a.g;
     const Item it = a.items[rank];
+    if (it.part < 0) return;
     const Seq s = sequence(g, it.seq);
     const int pack = a.pack, kvh = pack == 1 ? head / g.group : head;
     const int tokens = min(a.head->tokens, s.n - it.tok0), rows = tokens * pack;
@@ -202,11 +203,6 @@ __global__ void __launch_bounds__(TH, 2) attn_simt_kernel(const Args<T> a)
             st[0] = m[i];
             st[1] = l[i];
         }
-    }
-    if (whole || !last_part(a.parts, it, head, &flag)) return;
-    for (int r = t >> 5; r < rows; r += TH / 32) {
-        const int h = head_of(r), tok = it.tok0 + r / pack;
-        join_row<T>(a.parts, it, head, r, a.o.at(s.b, s.row0 + tok, h), a.lse ? a.lse + stat_at(g, s, h, tok) : nullptr);
     }
 }
 
@@ -348,7 +344,7 @@ template <typename... P> bool allow(void (*kern)(P...))
 Plan plan_of(const gma_attn_t &a, const gma_attn_paged_t *paged, Carve *c)
 {
     const int group = a.H / a.G, pack = paged && group <= R ? group : 1;
-    return make_plan(a, pack, R, R, 6, SMS, 2, paged ? 32 : NEVER, c);
+    return make_plan(a, pack, R, R, 6, SMS, paged != nullptr, c);
 }
 
 template <typename T>
@@ -366,7 +362,7 @@ Args<T> args_of(const gma_attn_t &a, const gma_attn_paged_t *paged, const Plan &
     x.heads = p.heads;
     x.head = (const PlanHead *)(w + p.head_at);
     x.items = (const Item *)(w + p.items_at);
-    x.parts = Parts{(float *)(w + p.part_at), (float *)(w + p.stat_at), p.rows, p.heads, a.dv, (a.dv + 3) & ~3, (int *)(w + p.join_at)};
+    x.parts = parts_of(p, a, ws);
     return x;
 }
 
@@ -382,6 +378,7 @@ template <typename T> gma_status_t forward(const gma_attn_t &a, const gma_attn_p
     if (paged) {
         if (!allow(attn_simt_kernel<T, true>)) return GMA_ERR_CUDA;
         GMA_LAUNCH(KID_ATTN_SIMT, st, launch_pdl(attn_simt_kernel<T, true>, grid, TH, smem, st, x));
+        return launch_join(a, x.g, p, ws, st);
     } else {
         if (!allow(attn_simt_kernel<T, false>)) return GMA_ERR_CUDA;
         GMA_LAUNCH(KID_ATTN_SIMT, st, launch_pdl(attn_simt_kernel<T, false>, grid, TH, smem, st, x));
@@ -397,10 +394,10 @@ struct GradPlan {
 GradPlan grad_plan(const gma_attn_t &a, Carve *c)
 {
     GradPlan p;
-    p.q = make_plan(a, 1, R, R, 6, SMS, 1, 0, c);
+    p.q = make_plan(a, 1, R, R, 6, SMS, false, c);
     gma_attn_t by = a;
     by.H = a.G;                       // a tile of keys serves the whole group
-    p.k = make_plan(by, 1, R, R, 6, SMS, 1, 0, c);
+    p.k = make_plan(by, 1, R, R, 6, SMS, false, c);
     p.k.by_keys = true;
     p.delta_at = c->take((size_t)(a.offsets ? 1 : a.B) * a.H * a.N * sizeof(float));
     return p;

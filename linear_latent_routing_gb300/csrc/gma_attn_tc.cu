@@ -35,7 +35,7 @@ struct TcArgs {
     float *lse;
     int pack, heads;           // query heads in a row tile, heads of the grid
     int o_vec;
-    const PlanHead *head;
+    PlanHead *head;
     const Item *items;
     Parts parts;
     WsHeader *hdr;
@@ -46,11 +46,22 @@ struct TcArgs {
     int page_shift;            // pages are powers of two
 };
 
+// An item of one head as its block's warps see it.
+struct Job {
+    Seq sq;
+    int seq, tok0, tokens;     // sequence, first token, tokens (0: no more jobs)
+    int t0, t1, e0;            // key tiles, and where stream 0's end if it has rows of its own
+    int two;                   // each stream has its own rows
+    int head, kvh;
+    int slot, parts, part;
+};
+
 // shared memory: query tiles, the ring, the barriers
 struct Bars {
-    uint64_t q, full[MAX_SLOTS], empty[MAX_SLOTS], s[2], p[2], o[2], drain;
+    uint64_t q, q_free, full[MAX_SLOTS], empty[MAX_SLOTS], s[2], p[2], o[2], job[2], job_free[2], sync, drain;
     uint32_t tmem;
-    int abort, flag;
+    int abort;
+    Job jobs[2];
     float merge[TILE][2];
 };
 
@@ -67,6 +78,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const TcArgs a, con
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
     if (t == 256) {
         mbar_init(&bars->q, 1);
+        mbar_init(&bars->q_free, 1);
         for (int i = 0; i < a.slots; ++i) {
             mbar_init(&bars->full[i], 1);
             mbar_init(&bars->empty[i], 1);
@@ -75,49 +87,64 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const TcArgs a, con
             mbar_init(&bars->s[w], 1);
             mbar_init(&bars->p[w], TILE);
             mbar_init(&bars->o[w], 1);
+            mbar_init(&bars->job[w], 1);
+            mbar_init(&bars->job_free[w], 9);
         }
+        mbar_init(&bars->sync, 256);
         mbar_init(&bars->drain, 1);
         bars->abort = 0;
         fence_mbar_init();
     }
-    blk::wait_previous();
-    const int rank = blockIdx.x / a.heads, head = blockIdx.x % a.heads;
-    if (rank >= a.head->items) return;
     if (warp == 8) tmem_alloc(&bars->tmem, 512);
-    const Geo &g = a.g;
-    const Item it = a.items[rank];
-    const Seq sq = sequence(g, it.seq);
-    const int pack = a.pack, per = TILE / pack;                  // tokens of a row tile
-    const int tokens = min(a.head->tokens, sq.n - it.tok0);
-    const bool two = tokens > per;                               // each stream has its own rows
-    const int kvh = pack == 1 ? head / g.group : head;
-    // key tiles: [t0, t1), of which stream 0 with rows of its own sees those before e0
-    const int t0 = it.t0;
-    const int t1 = min(it.t1, (sq.seen(g, it.tok0 + tokens - 1) + TILE - 1) / TILE);
-    const int e0 = two ? min(t1, (sq.seen(g, it.tok0 + per - 1) + TILE - 1) / TILE) : t1;
-    const int step = two ? 1 : 2;
+    if (t == 288) {
+        prefetch_map(&qmap);
+        prefetch_map(&kmap);
+        prefetch_map(&vmap);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bars->tmem;
     const uint32_t sb = smem_u32(smem), rb = smem_u32(ring);
+    const Geo &g = a.g;
+    const int pack = a.pack, per = TILE / pack;                  // tokens of a row tile
+    int js = 0;                                                  // the job at hand, and the parity of its turn
+    uint32_t jt = 0;
 
-    if (warp >= 8) {
-        if (warp == 8) {
-            // ============================================================ products
-            const uint32_t id_s = idesc_f16(TILE, TILE, 1, 1, 0, 0), id_o = idesc_f16(TILE, (uint32_t)(g.dv + 15) & ~15u, 1, 1, 0, 1);
-            const int ksteps = (g.d + 15) >> 4;
-            bool ok = t1 > t0 && bar_wait(&bars->q, 0, a.hdr, 200, abort);
-            uint32_t turn[2] = {0, 0};             // parity of a stream's tiles
+    if (warp == 8) {
+        // ================================================================ products
+        reg_dec<88>();
+        const uint32_t id_s = idesc_f16(TILE, TILE, 1, 1, 0, 0), id_o = idesc_f16(TILE, (uint32_t)(g.dv + 15) & ~15u, 1, 1, 0, 1);
+        const int ksteps = (g.d + 15) >> 4;
+        const uint64_t q_desc = k_desc(sb);
+        bool ok = true;
+        uint32_t turn[2] = {0, 0}, qt = 0;         // parities of the streams' tiles and of the query tiles
+        RingPos v{1, 0}, kb{0, 0};
+        while ((ok = bar_wait(&bars->job[js], jt, a.hdr, 210, abort))) {
+            const Job &job = bars->jobs[js];
+            if (!job.tokens) break;
+            const int t0 = job.t0, t1 = job.t1, e0 = job.e0, L = job.sq.L;
+            const bool two = job.two;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->job_free[js]);
+            js ^= 1;
+            if (!js) jt ^= 1u;
+            if (t1 <= t0) continue;
+            if (!(ok = bar_wait(&bars->q, qt, a.hdr, 200, abort))) break;
+            qt ^= 1u;
             bool begun[2] = {false, false};
-            const uint64_t q_desc = k_desc(sb), q_next = two ? q_tile >> 4 : 0;
+            const uint64_t q_next = two ? q_tile >> 4 : 0;
+            const int step = two ? 1 : 2;
             auto loaded = [&](const RingPos &r) { return bar_wait(&bars->full[r.s], r.turn, a.hdr, 201, abort); };
-            // S_w = Q_w K^T, and with it the tile is given back
-            auto scores = [&](int w, const RingPos &k, bool last) {
+            // S_w = Q_w K^T; after a tile's last one it is given back, after the job's last one the queries too
+            auto scores = [&](int w, const RingPos &k, bool last, int kt) {
                 if (elect()) {
                     mma_tiles(tmem + w * TILE, q_desc + (w ? q_next : 0), k_desc(rb + (uint32_t)k.s * a.slot_bytes), id_s, ksteps);
                     mma_commit(&bars->s[w]);
-                    if (last) mma_commit(&bars->empty[k.s]);
+                    if (last) {
+                        mma_commit(&bars->empty[k.s]);
+                        if (kt + 1 == t1) mma_commit(&bars->q_free);
+                    }
                 }
             };
             // O_w += P_w V
@@ -132,20 +159,22 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const TcArgs a, con
                 begun[w] = true;
                 turn[w] ^= 1u;
             };
-            // the values of the tile at hand and the keys that the next scores take
-            RingPos v{1, 0}, k{0, 0};
-            if (ok && (ok = loaded(k))) {
-                if (t0 < e0) scores(0, k, !two);
-                if (two) scores(1, k, true);
-                k.step(2, a.slots);
-                if (!two) {
-                    if (t0 + 1 < t1 && (ok = loaded(k))) scores(1, k, true);
-                    k.step(2, a.slots);
+            // the keys that the next scores take
+            RingPos k = kb;
+            if (!(ok = loaded(k))) break;
+            if (t0 < e0) scores(0, k, !two, t0);
+            if (two) scores(1, k, true, t0);
+            k.step(2, a.slots);
+            if (!two) {
+                if (t0 + 1 < t1) {
+                    if (!(ok = loaded(k))) break;
+                    scores(1, k, true, t0 + 1);
                 }
+                k.step(2, a.slots);
             }
             for (int kt = t0; ok && kt < t1; ++kt) {
                 if (!(ok = loaded(v))) break;
-                const int have = sq.L - kt * TILE;
+                const int have = L - kt * TILE;
                 // values behind the sequence's end meet probabilities of zero, and may be anything
                 if (have < TILE) zero_rows(ring + (size_t)v.s * a.slot_bytes, a.v_boxes, have);
                 const int next = kt + step;
@@ -158,40 +187,86 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const TcArgs a, con
                     output(w, v, last);
                     if (next < (two && w == 0 ? e0 : t1)) {
                         if (!(ok = loaded(k))) break;
-                        scores(w, k, last);
+                        scores(w, k, last, next);
                     } else if (elect()) {
                         mma_commit(&bars->o[w]);
                     }
                 }
                 v.step(2, a.slots);
                 k.step(2, a.slots);
+                kb.step(2, a.slots);
             }
-            // after a wait that gave up: products in flight end before their operands and results go
-            if (*abort) {
-                if (elect()) mma_commit(&bars->drain);
-                mbar_wait(&bars->drain, 0, a.hdr, 209);
+            if (!ok) break;
+        }
+        // after a wait that gave up: products in flight end before their operands and results go
+        if (*abort) {
+            if (elect()) mma_commit(&bars->drain);
+            mbar_wait(&bars->drain, 0, a.hdr, 209);
+        }
+    } else if (warp == 9) {
+        // ================================================================ jobs and loads
+        reg_dec<88>();
+        if (PAGED) blk::let_next();
+        blk::wait_previous();
+        const int all = a.head->items * a.heads, tile_tokens = a.head->tokens;
+        bool ok = true;
+        int issued = 0, queries = 0;
+        RingPos r{0, 1};
+        uint32_t qt = 1;
+        jt = 1;
+        int ticket = 0;
+        if (lane == 0) ticket = atomicAdd(&a.head->ticket, 1);
+        ticket = __shfl_sync(~0u, ticket, 0);
+        while (true) {
+            Job job;
+            job.tokens = 0;
+            if (ticket < all) {
+                const int rank = ticket / a.heads;
+                const Item it = a.items[rank];
+                job.head = ticket - rank * a.heads;
+                job.sq = sequence(g, it.seq);
+                job.seq = it.seq;
+                job.tok0 = it.tok0;
+                job.tokens = min(tile_tokens, job.sq.n - it.tok0);
+                job.two = job.tokens > per;
+                job.kvh = pack == 1 ? job.head / g.group : job.head;
+                job.t0 = it.t0;
+                job.t1 = it.part < 0 ? it.t0 : min(it.t1, (job.sq.seen(g, it.tok0 + job.tokens - 1) + TILE - 1) / TILE);
+                job.e0 = job.two ? min(job.t1, (job.sq.seen(g, it.tok0 + per - 1) + TILE - 1) / TILE) : job.t1;
+                job.slot = it.slot;
+                job.parts = it.parts;
+                job.part = it.part;
             }
-        } else if (warp == 9) {
-            // ============================================================ loads
-            bool ok = t1 > t0;
-            int issued = 0;
-            if (ok) {
+            if (!(ok = bar_wait(&bars->job_free[js], jt, a.hdr, 211, abort))) break;
+            if (lane == 0) bars->jobs[js] = job;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->job[js]);
+            js ^= 1;
+            if (!js) jt ^= 1u;
+            if (!job.tokens) break;
+            // the next one's ticket, on its way while this one's tiles are loaded
+            if (lane == 0) ticket = atomicAdd(&a.head->ticket, 1);
+            const Seq &sq = job.sq;
+            const int t0 = job.t0, t1 = job.t1;
+            // the page of this lane's box of a tile
+            auto page_entry = [&](int kt) {
+                const int j = kt * TILE + lane * a.page_rows;
+                if (lane >= a.tile_pages || j >= sq.L) return 0;
+                return g.table[(long long)job.seq * g.table_stride + (j >> a.page_shift)];
+            };
+            if (t1 > t0) {
+                int entry = PAGED ? page_entry(t0) : 0;
+                if (!(ok = bar_wait(&bars->q_free, qt, a.hdr, 212, abort))) break;
+                qt ^= 1u;
                 if (lane == 0) {
                     const uint32_t box = (uint32_t)(per * pack) * 128u;
-                    const int tiles = two ? 2 : 1;
+                    const int tiles = job.two ? 2 : 1;
                     mbar_arrive_expect_tx(&bars->q, box * tiles * a.q_boxes);
                     for (int w = 0; w < tiles; ++w)
                         for (int b = 0; b < a.q_boxes; ++b)
-                            tma_load_4d(sb + w * q_tile + b * BOX, &qmap, &bars->q, 64 * b, head * pack, sq.row0 + it.tok0 + w * per, sq.b);
+                            tma_load_4d(sb + w * q_tile + b * BOX, &qmap, &bars->q, 64 * b, job.head * pack, sq.row0 + job.tok0 + w * per, sq.b);
                 }
-                // the page of this lane's box of a tile
-                auto page_entry = [&](int kt) {
-                    const int j = kt * TILE + lane * a.page_rows;
-                    if (lane >= a.tile_pages || j >= sq.L) return 0;
-                    return g.table[(long long)it.seq * g.table_stride + (j >> a.page_shift)];
-                };
-                RingPos r{0, 1};
-                int entry = PAGED ? page_entry(t0) : 0;
+                ++queries;
                 for (int kt = t0; ok && kt < t1; ++kt) {
                     const int have = min(sq.L - kt * TILE, TILE), boxes = PAGED ? (have + a.page_rows - 1) / a.page_rows : 1;
                     const int in_page = PAGED ? (kt * TILE) & (g.page - 1) : 0;
@@ -210,206 +285,204 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const TcArgs a, con
                             const int page = entry >= 0 && entry < g.pages ? entry : g.pages;
                             if (lane < boxes)
                                 for (int b = 0; b < nb; ++b)
-                                    tma_load_4d(dst + b * BOX + lane * a.page_rows * 128, map, full, 64 * b, kvh, in_page, page);
+                                    tma_load_4d(dst + b * BOX + lane * a.page_rows * 128, map, full, 64 * b, job.kvh, in_page, page);
                         } else if (lane == 0) {
-                            for (int b = 0; b < nb; ++b) tma_load_4d(dst + b * BOX, map, full, 64 * b, kvh, sq.row0 + kt * TILE, sq.b);
+                            for (int b = 0; b < nb; ++b) tma_load_4d(dst + b * BOX, map, full, 64 * b, job.kvh, sq.row0 + kt * TILE, sq.b);
                         }
                         ++issued;
                         r.step(1, a.slots);
                     }
                     entry = ahead;
                 }
-                // loads that no product waited for (another wait gave up) end before the block does
-                if (*abort) {
-                    mbar_wait(&bars->q, 0, a.hdr, 204);
-                    for (int c = issued > a.slots ? issued - a.slots : 0; c < issued; ++c)
-                        mbar_wait(&bars->full[c % a.slots], (uint32_t)(c / a.slots) & 1u, a.hdr, 205);
-                }
+                if (!ok) break;
             }
+            ticket = __shfl_sync(~0u, ticket, 0);
         }
-    } else {
-        // ================================================================ a stream's rows
+        // loads that no product waited for (a wait gave up) end before the block does
+        if (*abort) {
+            if (queries) mbar_wait(&bars->q, (uint32_t)(queries - 1) & 1u, a.hdr, 204);
+            for (int c = issued > a.slots ? issued - a.slots : 0; c < issued; ++c)
+                mbar_wait(&bars->full[c % a.slots], (uint32_t)(c / a.slots) & 1u, a.hdr, 205);
+        }
+    } else if (warp < 8) {
+        // ================================================================ a stream's rows (registers: 256 x 208 + 128 x 88 = 384 x 168)
+        reg_inc<208>();
         const int w = warp >> 2, row = t & (TILE - 1);
-        const int first = it.tok0 + (two ? w * per : 0), tok = first + row / pack;
-        const bool valid = row < per * pack && tok < it.tok0 + tokens;
-        const bool busy = __any_sync(~0u, valid);
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + w * TILE, to = tmem + lanes + 256 + w * TILE;
-        const int seen = valid ? sq.seen(g, tok) : sq.L;
-        const int begin = two ? t0 : t0 + w, end = two && w == 0 ? e0 : t1;
-        float m = -INFINITY;
-        blk::f2 l2 = blk::pack2(0.f, 0.f), l3 = l2;
-        bool ok = true;
-        int n = 0;
-        for (int kt = begin; kt < end; kt += step, ++n) {
-            if (!(ok = bar_wait(&bars->s[w], n & 1, a.hdr, 206, abort))) break;
-            tc_fence_after();
-            if (busy) {
-                uint32_t r[4][32];
+        uint32_t st = 0, ot[2] = {0, 0}, yt = 0;   // parities of this stream's scores, of both streams' results, of their meetings
+        auto streams_sync = [&]() {
+            mbar_arrive(&bars->sync);
+            const bool met = bar_wait(&bars->sync, yt, a.hdr, 214, abort);
+            yt ^= 1u;
+            return met;
+        };
+        while (bar_wait(&bars->job[js], jt, a.hdr, 213, abort)) {
+            const Job &job = bars->jobs[js];
+            if (!job.tokens) break;
+            const bool two = job.two;
+            const int tok = job.tok0 + (two ? w * per : 0) + row / pack;
+            const bool valid = row < per * pack && tok < job.tok0 + job.tokens;
+            const bool busy = __any_sync(~0u, valid);
+            const int seen = valid ? job.sq.seen(g, tok) : job.sq.L;
+            const int step = two ? 1 : 2, begin = two ? job.t0 : job.t0 + w, end = two && w == 0 ? job.e0 : job.t1;
+            float m = -INFINITY;
+            blk::f2 l2 = blk::pack2(0.f, 0.f), l3 = l2;
+            bool ok = true;
+            int n = 0;
+            for (int kt = begin; kt < end; kt += step, ++n) {
+                if (!(ok = bar_wait(&bars->s[w], st, a.hdr, 206, abort))) break;
+                st ^= 1u;
+                tc_fence_after();
+                if (busy) {
+                    uint32_t r[4][32];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, r[c]);
-                tmem_ld_wait();
-                const int lim = seen - kt * TILE;
-                if (__any_sync(~0u, lim < TILE)) {
+                    for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, r[c]);
+                    tmem_ld_wait();
+                    const int lim = seen - kt * TILE;
+                    if (__any_sync(~0u, lim < TILE)) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
+                        for (int c = 0; c < 4; ++c)
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (32 * c + e >= lim) r[c][e] = 0xff800000u;
-                }
-                float x[4];
+                            for (int e = 0; e < 32; ++e)
+                                if (32 * c + e >= lim) r[c][e] = 0xff800000u;
+                    }
+                    float x[4];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    x[c] = __uint_as_float(r[c][0]);
+                    for (int c = 0; c < 4; ++c) {
+                        x[c] = __uint_as_float(r[c][0]);
 #pragma unroll
-                    for (int e = 1; e < 32; ++e) x[c] = fmaxf(x[c], __uint_as_float(r[c][e]));
-                }
-                const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * g.sl2;
-                if (__any_sync(~0u, top > m + GROW)) {
-                    const float now = fmaxf(m, top), f = now == -INFINITY ? 1.f : ex2(m - now);
-                    m = now;
-                    const blk::f2 ff = blk::pack2(f, f);
-                    l2 = blk::mul2(l2, ff);
-                    l3 = blk::mul2(l3, ff);
-                    if (n) {
+                        for (int e = 1; e < 32; ++e) x[c] = fmaxf(x[c], __uint_as_float(r[c][e]));
+                    }
+                    const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * g.sl2;
+                    if (__any_sync(~0u, top > m + GROW)) {
+                        const float now = fmaxf(m, top), f = now == -INFINITY ? 1.f : ex2(m - now);
+                        m = now;
+                        const blk::f2 ff = blk::pack2(f, f);
+                        l2 = blk::mul2(l2, ff);
+                        l3 = blk::mul2(l3, ff);
+                        if (n) {
 #pragma unroll 1
-                        for (int c = 0; c < g.dv; c += 32) {
-                            uint32_t v[32];
-                            tmem_ld32(to + c, v);
-                            tmem_ld_wait();
+                            for (int c = 0; c < g.dv; c += 32) {
+                                uint32_t v[32];
+                                tmem_ld32(to + c, v);
+                                tmem_ld_wait();
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
-                            tmem_st16(to + c, *reinterpret_cast<uint32_t(*)[16]>(v));
-                            tmem_st16(to + c + 16, *reinterpret_cast<uint32_t(*)[16]>(v + 16));
+                                for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
+                                tmem_st16(to + c, *reinterpret_cast<uint32_t(*)[16]>(v));
+                                tmem_st16(to + c + 16, *reinterpret_cast<uint32_t(*)[16]>(v + 16));
+                            }
                         }
                     }
-                }
-                const float base = m == -INFINITY ? 0.f : -m;
-                const blk::f2 scale = blk::pack2(g.sl2, g.sl2), shift = blk::pack2(base, base);
+                    const float base = m == -INFINITY ? 0.f : -m;
+                    const blk::f2 scale = blk::pack2(g.sl2, g.sl2), shift = blk::pack2(base, base);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t p[16];
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t p[16];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const blk::f2 y = blk::ex2_2(
-                            blk::fma2(blk::pack2(__uint_as_float(r[c][2 * e]), __uint_as_float(r[c][2 * e + 1])), scale, shift));
-                        if (e & 1) l3 = blk::add2(l3, y); else l2 = blk::add2(l2, y);
-                        const float2 z = blk::unpack2(y);
-                        p[e] = pack_bf16(z.x, z.y);
+                        for (int e = 0; e < 16; ++e) {
+                            const blk::f2 y = blk::ex2_2(
+                                blk::fma2(blk::pack2(__uint_as_float(r[c][2 * e]), __uint_as_float(r[c][2 * e + 1])), scale, shift));
+                            if (e & 1) l3 = blk::add2(l3, y); else l2 = blk::add2(l2, y);
+                            const float2 z = blk::unpack2(y);
+                            p[e] = pack_bf16(z.x, z.y);
+                        }
+                        tmem_st16(ts + 16 * c, p);
                     }
-                    tmem_st16(ts + 16 * c, p);
+                    tmem_st_wait();
                 }
-                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(&bars->p[w]);
             }
-            tc_fence_before();
-            mbar_arrive(&bars->p[w]);
-        }
-        const float2 la = blk::unpack2(blk::add2(l2, l3));
-        float l = la.x + la.y;
-        if (n && ok) ok = bar_wait(&bars->o[w], 0, a.hdr, 207, abort);
-        // the ring takes stream 1's result: both streams' last products have read it
-        if (!two && w == 1 && n && ok) ok = bar_wait(&bars->o[0], 0, a.hdr, 208, abort);
-        tc_fence_after();
-        bool store = two || w == 0;
-        float mine = 1.f;                          // factor of this stream's sums
-        bool other = false;
-        float theirs = 0.f;
-        float *mo = reinterpret_cast<float *>(smem + 2 * q_tile);       // [dv / 4][128 rows][4]: the ring is empty by now
-        if (!two && t1 - t0 > 1) {
-            if (w == 1 && busy) {
-                bars->merge[row][0] = m;
-                bars->merge[row][1] = l;
+            if (!ok) break;
+            const float2 la = blk::unpack2(blk::add2(l2, l3));
+            float l = la.x + la.y;
+            const bool shared = !two && job.t1 - job.t0 > 1;        // both streams have parts of the same rows
+            if (n && !bar_wait(&bars->o[w], ot[w], a.hdr, 207, abort)) break;
+            if (shared && w == 0 && !bar_wait(&bars->o[1], ot[1], a.hdr, 208, abort)) break;
+            if (two ? job.e0 > job.t0 : job.t1 > job.t0) ot[0] ^= 1u;
+            if (two ? job.t1 > job.t0 : shared) ot[1] ^= 1u;
+            tc_fence_after();
+            float mine = 1.f, theirs = 0.f;                         // factors of the streams' sums
+            if (shared) {
+                if (w == 1) {
+                    bars->merge[row][0] = m;
+                    bars->merge[row][1] = l;
+                }
+                if (!streams_sync()) break;
+                if (w == 0) {
+                    const float m1 = bars->merge[row][0], l1 = bars->merge[row][1], now = fmaxf(m, m1);
+                    mine = now == -INFINITY ? 0.f : ex2(m - now);
+                    theirs = now == -INFINITY ? 0.f : ex2(m1 - now);
+                    l = l * mine + l1 * theirs;
+                    m = now;
+                }
+            }
+            const bool whole = job.parts == 1;
+            if (busy && (two || w == 0) && job.part >= 0) {
+                const int h = pack == 1 ? job.head : job.head * pack + row % pack;
+                const int item_row = (two ? w * per * pack : 0) + row;
+                const float f = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+                mine *= f;
+                theirs *= f;
+                bf16 *out = a.o.at(job.sq.b, job.sq.row0 + (valid ? tok : job.tok0), h);
+                float *part = whole ? nullptr : a.parts.o_at(job.slot + job.part, job.head, valid ? item_row : 0);
+                if (valid) {
+                    if (whole) {
+                        if (a.lse) a.lse[stat_at(g, job.sq, h, tok)] = l > 0.f ? (m + log2f(l)) * LN2 : -INFINITY;
+                    } else {
+                        float *stat = a.parts.stat_at(job.slot + job.part, job.head, item_row);
+                        stat[0] = l > 0.f ? m : -INFINITY;
+                        stat[1] = l;
+                    }
+                }
 #pragma unroll 1
                 for (int c = 0; c < g.dv; c += 32) {
                     uint32_t v[32];
-                    tmem_ld32(to + c, v);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        *reinterpret_cast<uint4 *>(mo + ((c / 4 + q) * TILE + row) * 4) = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-                }
-            }
-            named_bar_sync(1, 256);
-            if (w == 0 && busy) {
-                const float m1 = bars->merge[row][0], l1 = bars->merge[row][1], now = fmaxf(m, m1);
-                mine = now == -INFINITY ? 0.f : ex2(m - now);
-                theirs = now == -INFINITY ? 0.f : ex2(m1 - now);
-                l = l * mine + l1 * theirs;
-                m = now;
-                other = true;
-            }
-        }
-        if (store && busy && ok) {
-            const int h = pack == 1 ? head : head * pack + row % pack;
-            const int item_row = (two ? w * per * pack : 0) + row;
-            const bool whole = it.parts == 1;
-            const float inv = l > 0.f ? 1.f / l : 0.f, f = whole ? inv : 1.f;
-            if (l == 0.f) mine = theirs = 0.f;
-            bf16 *out = a.o.at(sq.b, sq.row0 + (valid ? tok : it.tok0), h);
-            float *part = whole ? nullptr : a.parts.o_at(it.slot + it.part, head, valid ? item_row : 0);
-            if (valid) {
-                if (whole) {
-                    if (a.lse) a.lse[stat_at(g, sq, h, tok)] = l > 0.f ? (m + log2f(l)) * LN2 : -INFINITY;
-                } else {
-                    float *st = a.parts.stat_at(it.slot + it.part, head, item_row);
-                    st[0] = l > 0.f ? m : -INFINITY;
-                    st[1] = l;
-                }
-            }
-#pragma unroll 1
-            for (int c = 0; c < g.dv; c += 32) {
-                uint32_t v[32];
-                float y[32];
-                if (n) {
-                    tmem_ld32(to + c, v);
-                    tmem_ld_wait();
-                }
-#pragma unroll
-                for (int e = 0; e < 32; ++e) y[e] = l > 0.f && n ? __uint_as_float(v[e]) * mine : 0.f;
-                if (other && theirs != 0.f) {
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        const float4 z = *reinterpret_cast<const float4 *>(mo + ((c / 4 + q) * TILE + row) * 4);
-                        y[4 * q] = fmaf(z.x, theirs, y[4 * q]);
-                        y[4 * q + 1] = fmaf(z.y, theirs, y[4 * q + 1]);
-                        y[4 * q + 2] = fmaf(z.z, theirs, y[4 * q + 2]);
-                        y[4 * q + 3] = fmaf(z.w, theirs, y[4 * q + 3]);
+                    float y[32];
+                    if (n) {
+                        tmem_ld32(to + c, v);
+                        tmem_ld_wait();
                     }
-                }
-                if (!valid) continue;
-                if (!whole) {
-                    if (g.dv % 4 == 0) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) y[e] = n && mine != 0.f ? __uint_as_float(v[e]) * mine : 0.f;
+                    if (shared) {
+                        tmem_ld32(to + TILE + c, v);                // the other stream's rows lie in the same lanes
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) y[e] = theirs != 0.f ? fmaf(__uint_as_float(v[e]), theirs, y[e]) : y[e];
+                    }
+                    if (!valid) continue;
+                    if (!whole) {
 #pragma unroll
                         for (int q = 0; q < 8; ++q)
                             if (c + 4 * q < g.dv) *reinterpret_cast<float4 *>(part + c + 4 * q) = make_float4(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]);
+                    } else if (a.o_vec) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            if (c + 8 * q < g.dv)
+                                *reinterpret_cast<uint4 *>(out + c + 8 * q) =
+                                    make_uint4(pack_bf16(y[8 * q], y[8 * q + 1]), pack_bf16(y[8 * q + 2], y[8 * q + 3]),
+                                               pack_bf16(y[8 * q + 4], y[8 * q + 5]), pack_bf16(y[8 * q + 6], y[8 * q + 7]));
                     } else {
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
-                            if (c + e < g.dv) part[c + e] = y[e];
+                            if (c + e < g.dv) out[c + e] = __float2bfloat16_rn(y[e]);
                     }
-                } else if (a.o_vec) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        if (c + 8 * q < g.dv)
-                            *reinterpret_cast<uint4 *>(out + c + 8 * q) =
-                                make_uint4(pack_bf16(y[8 * q] * f, y[8 * q + 1] * f), pack_bf16(y[8 * q + 2] * f, y[8 * q + 3] * f),
-                                           pack_bf16(y[8 * q + 4] * f, y[8 * q + 5] * f), pack_bf16(y[8 * q + 6] * f, y[8 * q + 7] * f));
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (c + e < g.dv) out[c + e] = __float2bfloat16_rn(y[e] * f);
                 }
             }
+            // the next job's products over these results, and its exchange, wait for all that read this one's
+            tc_fence_before();
+            if (shared && !streams_sync()) break;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->job_free[js]);
+            js ^= 1;
+            if (!js) jt ^= 1u;
         }
+    } else {
+        reg_dec<88>();
     }
     tc_fence_before();
-    if (it.parts > 1 && last_part(a.parts, it, head, &bars->flag)) {
-        const int rows = tokens * pack;
-        for (int r = warp; r < rows; r += THREADS / 32) {
-            const int h = pack == 1 ? head : head * pack + r % pack, tok = it.tok0 + r / pack;
-            join_row<bf16>(a.parts, it, head, r, a.o.at(sq.b, sq.row0 + tok, h), a.lse ? a.lse + stat_at(g, sq, h, tok) : nullptr);
-        }
-    }
     __syncthreads();
     if (warp == 8) tmem_dealloc(tmem, 512);
 }
@@ -445,7 +518,7 @@ namespace {
 Plan plan_of(const gma_attn_t &a, const gma_attn_paged_t *paged, Carve *c)
 {
     const int group = a.H / a.G, pack = paged && group <= TILE ? group : 1;
-    return make_plan(a, pack, 2 * TILE, TILE, 7, SMS, 4, paged ? 32 : NEVER, c);
+    return make_plan(a, pack, 2 * TILE, TILE, 7, SMS, paged != nullptr, c);
 }
 
 }  // namespace
@@ -479,9 +552,9 @@ gma_status_t tc_forward(const gma_attn_t &a, const gma_attn_paged_t *p, void *ws
     x.pack = pl.pack;
     x.heads = pl.heads;
     x.o_vec = store_vec(a.o, a.dv);
-    x.head = (const PlanHead *)(w + pl.head_at);
+    x.head = (PlanHead *)(w + pl.head_at);
     x.items = (const Item *)(w + pl.items_at);
-    x.parts = Parts{(float *)(w + pl.part_at), (float *)(w + pl.stat_at), pl.rows, pl.heads, a.dv, (a.dv + 3) & ~3, (int *)(w + pl.join_at)};
+    x.parts = parts_of(pl, a, ws);
     x.hdr = (WsHeader *)ws;
     x.q_boxes = (a.d + 63) / 64;
     x.v_boxes = (a.dv + 63) / 64;
@@ -502,11 +575,13 @@ gma_status_t tc_forward(const gma_attn_t &a, const gma_attn_paged_t *p, void *ws
         return GMA_ERR_CUDA;
     gma_status_t r = launch_plan(plan_args(x.g, pl, ws), nullptr, st);
     if (r != GMA_OK) return r;
-    const unsigned grid = (unsigned)pl.max_items * pl.heads;
+    // blocks stay and take items until there are no more
+    const long long most = (long long)pl.max_items * pl.heads;
+    const unsigned grid = most < SMS ? (unsigned)most : SMS;
     auto kern = p ? attn_tc_kernel<true> : attn_tc_kernel<false>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_MAX) != cudaSuccess) return GMA_ERR_CUDA;
     GMA_LAUNCH(KID_ATTN, st, launch_pdl(kern, grid, THREADS, smem, st, x, qm, km, vm));
-    return GMA_OK;
+    return p ? launch_join(a, x.g, pl, ws, st) : GMA_OK;
 }
 
 }  // namespace att

@@ -475,10 +475,10 @@ struct GradPlan {
 GradPlan grad_plan(const gma_attn_t &a, Carve *c)
 {
     GradPlan p;
-    p.q = make_plan(a, 1, TILE, TILE, 7, SMS, 1, 0, c);
+    p.q = make_plan(a, 1, TILE, TILE, 7, SMS, false, c);
     gma_attn_t by = a;
     by.H = a.G;                       // a tile of keys serves the whole group
-    p.k = make_plan(by, 1, TILE, TILE, 7, SMS, 1, 0, c);
+    p.k = make_plan(by, 1, TILE, TILE, 7, SMS, false, c);
     p.k.by_keys = true;
     p.delta_at = c->take((size_t)(a.offsets ? 1 : a.B) * a.H * a.N * sizeof(float));
     return p;
