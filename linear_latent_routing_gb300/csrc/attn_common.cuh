@@ -98,6 +98,12 @@ struct Item {
     int part, pad;     // this part
 };
 
+struct Join {          // an item that was cut
+    int slot, parts;   // its parts' results
+    int b, row, tokens; // batch row, first row and tokens of the tile
+    int pad[3];
+};
+
 struct PlanHead {      // behind the workspace header
     int items;         // how many
     int tokens;        // tokens of a tile
@@ -124,7 +130,7 @@ struct PlanArgs {
     WsHeader *hdr;
     PlanHead *head;
     Item *items;
-    int *join;                 // first parts of the items that were cut
+    Join *join;                // the items that were cut
 };
 
 Plan make_plan(const gma_attn_t &a, int pack, int wide_rows, int narrow_rows, int key_shift, int blocks, bool cut, Carve *ws);

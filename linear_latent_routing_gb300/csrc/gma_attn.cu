@@ -11,9 +11,10 @@ namespace att {
 namespace {
 
 typedef __nv_bfloat16 bf16;
-constexpr int PT = 1024;               // threads of the plan's block
+constexpr int PT = 256;                // threads of the plan's block
 constexpr int BUCKETS = 1024;          // items are ordered by size up to so many key tiles
-constexpr int COSTS = 4096;            // tiles up to which cutting is looked at
+constexpr int TILES = 2048;            // tiles up to which cutting is looked at
+constexpr int SIZES = 24;              // of parts that are tried
 constexpr float ITEM_COST = 2.f;       // what an item costs beside its keys, in key tiles
 
 // Exclusive sum over the block's threads; *all: the sum of all of them.
@@ -26,31 +27,35 @@ __device__ __forceinline__ int block_scan(int own, int *warps, int *all)
         const int up = __shfl_up_sync(~0u, sum, o);
         if (lane >= o) sum += up;
     }
-    __syncthreads();
     if (lane == 31) warps[warp] = sum;
     __syncthreads();
-    int w = warps[lane];
+    int before = 0, total = 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int up = __shfl_up_sync(~0u, w, o);
-        if (lane >= o) w += up;
+    for (int w = 0; w < PT / 32; ++w) {
+        const int x = warps[w];
+        before += w < warp ? x : 0;
+        total += x;
     }
-    *all = __shfl_sync(~0u, w, 31);
-    return sum - own + (warp ? __shfl_sync(~0u, w, warp - 1) : 0);
+    __syncthreads();
+    *all = total;
+    return before + sum - own;
 }
 
-// A thread a sequence for their numbers of tiles, then a thread a tile (found by bisection) for everything else.  Up to PT sequences
-// are read once; more are gone through PT at a time in every pass.
+// A thread a sequence for their numbers of tiles, then a thread a tile (its sequence found by bisection) for everything else.  Up to PT
+// sequences are read once, and up to TILES tiles looked up once; more are gone through again in every pass.
+// Latency is all: 256 threads, whose barriers are cheap.
 __global__ void __launch_bounds__(PT) plan_kernel(const PlanArgs a0, const PlanArgs a1)
 {
     const PlanArgs &a = blockIdx.x ? a1 : a0;
     __shared__ unsigned long long total;
-    __shared__ int slots, joins, filled, largest, hist[BUCKETS], warps[32], first[PT + 1], rows[PT], keys[PT], costs[COSTS], sizes[32];
-    __shared__ float times[32];
+    __shared__ int slots, joins, largest, hist[BUCKETS], warps[PT / 32], first[PT + 1], rows[PT], keys[PT], costs[TILES], sizes[SIZES];
+    __shared__ unsigned short seqs[TILES];
+    __shared__ float times[SIZES];
     const int t = threadIdx.x, B = a.g.B, mask = (1 << a.key_shift) - 1;
     blk::let_next();
-    if (t == 0) { total = 0; slots = 0; joins = 0; filled = 0; largest = 0; }
-    hist[t] = 0;
+    if (t == 0) { total = 0; slots = 0; joins = 0; largest = 0; }
+#pragma unroll
+    for (int i = 0; i < BUCKETS / PT; ++i) hist[t + i * PT] = 0;
     if (a.hdr && t < (int)(sizeof(WsHeader) / 4)) reinterpret_cast<unsigned *>(a.hdr)[t] = 0;
     int tokens = a.wide, count = 0;
     // reads the sequences from `base` on; the tiles of those before each
@@ -64,12 +69,12 @@ __global__ void __launch_bounds__(PT) plan_kernel(const PlanArgs a0, const PlanA
     auto number = [&]() {
         const int n = rows[t], k = n ? (n - 1) / tokens + 1 : 0;
         int all;
-        const int before = block_scan(k, warps, &all);
-        first[t] = before;
+        first[t] = block_scan(k, warps, &all);
         if (t == PT - 1) first[PT] = all;
         __syncthreads();
         return all;
     };
+    bool known = false;          // costs and seqs hold all tiles
     // f(sequence, first token, first key tile, key tiles) of every tile; by_keys: query tiles of a tile of keys
     auto each = [&](auto f) {
         for (int base = 0; base < B; base += PT) {
@@ -78,20 +83,29 @@ __global__ void __launch_bounds__(PT) plan_kernel(const PlanArgs a0, const PlanA
                 number();
             }
             for (int i = t; i < first[PT]; i += PT) {
-                int lo = 0, hi = PT;
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) >> 1;
-                    if (first[mid] <= i) lo = mid; else hi = mid;
-                }
-                const int n = rows[lo], L = keys[lo], tok = (i - first[lo]) * tokens;
-                int from = 0, cost;
-                if (a.by_keys) {
-                    from = a.g.causal ? tok >> a.key_shift : 0;
-                    cost = ((n + mask) >> a.key_shift) - from;
+                int lo, cost, from = 0;
+                if (known) {
+                    lo = seqs[i];
                 } else {
-                    const int last = min(tok + tokens, n) - 1, pos0 = a.g.cached ? L - n : 0;
+                    int hi = PT;
+                    lo = 0;
+                    while (hi - lo > 1) {
+                        const int mid = (lo + hi) >> 1;
+                        if (first[mid] <= i) lo = mid; else hi = mid;
+                    }
+                }
+                const int n = rows[lo], tok = (i - first[lo]) * tokens;
+                if (a.by_keys && a.g.causal) from = tok >> a.key_shift;
+                if (known) {
+                    cost = costs[i];
+                } else {
+                    const int L = keys[lo], last = min(tok + tokens, n) - 1, pos0 = a.g.cached ? L - n : 0;
                     const int seen = a.g.causal ? min(max(pos0 + last + 1, 0), L) : L;
-                    cost = max((seen + mask) >> a.key_shift, 1);
+                    cost = a.by_keys ? ((n + mask) >> a.key_shift) - from : max((seen + mask) >> a.key_shift, 1);
+                    if (B <= PT && i < TILES) {
+                        costs[i] = cost;
+                        seqs[i] = (unsigned short)lo;
+                    }
                 }
                 f(base + lo, tok, from, cost);
             }
@@ -104,19 +118,18 @@ __global__ void __launch_bounds__(PT) plan_kernel(const PlanArgs a0, const PlanA
     }
     if ((long long)count * a.heads < SMS && a.narrow < a.wide) {
         tokens = a.narrow;
-        if (B <= PT) number();
+        if (B <= PT) count = number();
     }
-    // a part's key tiles: each warp estimates the time with another size, half a block's share of the call to five of them
+    // a part's key tiles: an estimate of the time with SIZES sizes, from half a block's share of the call to five of them
     int share = 0x7fffffff;
-    if (a.max_slots) {
+    if (a.max_slots && B <= PT && count <= TILES && count) {     // more tiles than that fill the GPU as they are
         unsigned long long work = 0;
         int most = 0;
         each([&](int, int, int, int cost) {
             work += cost;
             most = max(most, cost);
-            const int at = atomicAdd(&filled, 1);
-            if (at < COSTS) costs[at] = cost;
         });
+        known = true;
 #pragma unroll
         for (int o = 16; o; o >>= 1) {
             work += __shfl_xor_sync(~0u, work, o);
@@ -127,35 +140,39 @@ __global__ void __launch_bounds__(PT) plan_kernel(const PlanArgs a0, const PlanA
             atomicMax(&largest, most);
         }
         __syncthreads();
-        const int n = filled;
         const float all = (float)total * a.heads, per = all / a.blocks;
-        if (n <= COSTS && n) {                       // more tiles than that fill the GPU as they are
-            const int warp = t >> 5, lane = t & 31;
-            const int size = max((int)ceilf(per * 0.5f * exp2f(warp * (3.3f / 31))), 1);
+        const int warp = t >> 5, lane = t & 31, top = largest;
+#pragma unroll 1
+        for (int c = warp; c < SIZES; c += PT / 32) {
+            const int size = max((int)ceilf(per * 0.5f * exp2f(c * (3.3f / (SIZES - 1)))), 1);
+            const float inv = 1.f / size;
             int parts = 0, cut = 0;
-            for (int i = lane; i < n; i += 32) {
-                const int k = costs[i] <= size ? 1 : (costs[i] - 1) / size + 1;
+            for (int i = lane; i < count; i += 32) {
+                // (an estimate: the quotient may be off by one)
+                const int k = costs[i] <= size ? 1 : (int)((costs[i] - 1) * inv) + 1;
                 parts += k;
                 if (k > 1) cut += k;
             }
-#pragma unroll
-            for (int o = 16; o; o >>= 1) {
-                parts += __shfl_xor_sync(~0u, parts, o);
-                cut += __shfl_xor_sync(~0u, cut, o);
-            }
+            parts = __reduce_add_sync(~0u, parts);
+            cut = __reduce_add_sync(~0u, cut);
             const float items = (float)parts * a.heads, extra = ITEM_COST * items + a.part_cost * cut * a.heads;
-            const int cuts = largest <= size ? 1 : (largest - 1) / size + 1;
-            const float longest = (float)((largest - 1) / cuts + 1) + ITEM_COST + (cuts > 1 ? a.part_cost : 0.f);
+            const int cuts = top <= size ? 1 : (int)((top - 1) * inv) + 1;
+            const float longest = (float)((top - 1) / cuts + 1) + ITEM_COST + (cuts > 1 ? a.part_cost : 0.f);
             const float mean = (all + extra) / items, waves = ceilf(items / a.blocks);
             // equal items run in whole waves; unequal ones, the longest first, fill the gaps
             const float time = longest < 1.2f * mean || items <= a.blocks ? waves * longest
                                                                           : fmaxf((all + extra) / a.blocks + 0.5f * mean, longest);
-            if (lane == 0) times[warp] = time, sizes[warp] = size;
-            __syncthreads();
-            float best = times[0];
-            share = sizes[0];
-            for (int w = 1; w < 32; ++w)
-                if (times[w] <= best) best = times[w], share = sizes[w];
+            if (lane == 0) times[c] = time, sizes[c] = size;
+        }
+        __syncthreads();
+        float best = times[0];
+        share = sizes[0];
+#pragma unroll
+        for (int w = 1; w < SIZES; ++w) {
+            const float x = times[w];
+            const int size = sizes[w];
+            share = x <= best ? size : share;
+            best = fminf(x, best);
         }
     }
     // how many of each size, where those of a size start, and the list
@@ -165,22 +182,34 @@ __global__ void __launch_bounds__(PT) plan_kernel(const PlanArgs a0, const PlanA
         const int parts = parts_of(cost);
         atomicAdd(&hist[bucket_of(cost, parts)], parts);
     });
+    known = known || (B <= PT && count <= TILES);
     __syncthreads();
-    const int own = hist[t];
-    const int start = block_scan(own, warps, &count);
-    hist[t] = start;
+    int own[BUCKETS / PT], sum = 0;
+#pragma unroll
+    for (int i = 0; i < BUCKETS / PT; ++i) {
+        own[i] = sum;
+        sum += hist[t * (BUCKETS / PT) + i];
+    }
+    const int start = block_scan(sum, warps, &count);
+#pragma unroll
+    for (int i = 0; i < BUCKETS / PT; ++i) hist[t * (BUCKETS / PT) + i] = start + own[i];
     __syncthreads();
     each([&](int s, int tok, int from, int cost) {
         const int parts = parts_of(cost), size = parts == 1 ? cost : (cost - 1) / parts + 1;
         const int at = atomicAdd(&hist[bucket_of(cost, parts)], parts);
-        const int slot = parts > 1 ? atomicAdd(&slots, parts) : 0;
-        for (int p = 0; p < parts; ++p)
-            if (at + p < a.max_items) {
-                // offsets that fall may make more tiles than there are rows: an item without room for its parts is not worked on
-                const bool room = parts == 1 || (slot + parts <= a.max_slots && at + parts <= a.max_items);
-                a.items[at + p] = Item{s, tok, from + min(p * size, cost), from + min((p + 1) * size, cost), room ? slot : 0, parts, room ? p : -1, 0};
-                if (room && parts > 1 && p == 0) a.join[atomicAdd(&joins, 1)] = at;
-            }
+        if (parts == 1) {
+            if (at < a.max_items) a.items[at] = Item{s, tok, from, from + cost, 0, 1, 0, 0};
+            return;
+        }
+        // cuts are within the bounds that the lists were made for (offsets that fall make tiles that are not cut: more than TILES, or too many)
+        const int slot = atomicAdd(&slots, parts);
+        const bool room = slot + parts <= a.max_slots && at + parts <= a.max_items;
+        for (int p = 0; p < parts && at + p < a.max_items; ++p)
+            a.items[at + p] = Item{s, tok, min(p * size, cost), min((p + 1) * size, cost), room ? slot : 0, parts, room ? p : -1, 0};
+        if (room) {
+            const Seq q = sequence(a.g, s);
+            a.join[atomicAdd(&joins, 1)] = Join{slot, parts, q.b, q.row0 + tok, min(tokens, q.n - tok), 0, 0, 0};
+        }
     });
     __syncthreads();
     if (t == 0) {
@@ -194,57 +223,64 @@ __global__ void __launch_bounds__(PT) plan_kernel(const PlanArgs a0, const PlanA
 // A warp a row of a cut item: lanes are parts for the weights, then four columns each for the sums, with the loads of sixteen parts
 // in flight.
 template <typename T>
-__global__ void __launch_bounds__(256) attn_join_kernel(const Geo g, const PlanHead *head, const Item *items, const int *join, const Parts p,
-                                                        const Heads<T> out, float *lse, int pack)
+__global__ void __launch_bounds__(256) attn_join_kernel(const Geo g, const PlanHead *head, const Join *join, const Parts p, const Heads<T> out,
+                                                        float *lse, int pack)
 {
-    const int lane = threadIdx.x & 31;
+    const unsigned lane = threadIdx.x & 31;
     blk::wait_previous();
-    const long long rows = (long long)head->tokens * pack, n = (long long)head->joins * p.heads * rows;
-    for (long long i = blockIdx.x * 8ll + (threadIdx.x >> 5); i < n; i += gridDim.x * 8ll) {
-        const int row = (int)(i % rows), hj = (int)((i / rows) % p.heads);
-        const Item it = items[join[i / (rows * p.heads)]];
-        const Seq q = sequence(g, it.seq);
-        const int tok = it.tok0 + row / pack, h = pack == 1 ? hj : hj * pack + row % pack;
-        if (tok >= q.n) continue;
-        float m = -INFINITY;
-        for (int k = lane; k < it.parts; k += 32) m = fmaxf(m, p.stat_at(it.slot + k, hj, row)[0]);
-#pragma unroll
-        for (int s = 16; s; s >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, s));
-        float l = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const unsigned rows = (unsigned)head->tokens * pack, n = (unsigned)head->joins * p.heads * rows;
+    for (unsigned i = blockIdx.x * 8 + (threadIdx.x >> 5); i < n; i += gridDim.x * 8) {
+        const unsigned hj = i / rows, row = i - hj * rows, j = hj / p.heads, hd = hj - j * p.heads;
+        const Join it = join[j];
+        const int tok = row / pack, h = pack == 1 ? hd : hd * pack + row % pack;
+        if (tok >= it.tokens) continue;
+        const float *stat = p.stat_at(it.slot, hd, row), *part = p.o_at(it.slot, hd, row) + 4 * lane;
+        const long long stat_step = (long long)p.heads * p.rows * 2, part_step = (long long)p.heads * p.rows * p.pitch;
         const bool mine = 4 * lane < p.dv;
-        for (int k0 = 0; m != -INFINITY && k0 < it.parts; k0 += 32) {
-            float w = 0.f;
-            if (k0 + lane < it.parts) {
-                const float2 s = *reinterpret_cast<const float2 *>(p.stat_at(it.slot + k0 + lane, hj, row));
-                w = ex2(s.x - m);
-                l = fmaf(w, s.y, l);
-            }
+        float m = -INFINITY, l = 0.f;            // so far
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k0 = 0; k0 < it.parts; k0 += 32) {
+            // a first batch of sums, on its way beside the weights
             const int n = min(32, it.parts - k0);
-            for (int j0 = 0; j0 < n; j0 += 16) {
-                float4 x[16];
+            float4 x[16];
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    if (mine && j0 + j < n) x[j] = reinterpret_cast<const float4 *>(p.o_at(it.slot + k0 + j0 + j, hj, row))[lane];
+            for (int k = 0; k < 16; ++k)
+                if (mine && k < n) x[k] = *reinterpret_cast<const float4 *>(part + (k0 + k) * part_step);
+            float2 s = make_float2(-INFINITY, 0.f);
+            if ((int)lane < n) s = *reinterpret_cast<const float2 *>(stat + (k0 + lane) * stat_step);
+            float top = s.x;
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const float f = __shfl_sync(~0u, w, j0 + j);
-                    if (f == 0.f || j0 + j >= n) continue;      // a part that saw nothing wrote no sums
-                    acc.x = fmaf(f, x[j].x, acc.x);
-                    acc.y = fmaf(f, x[j].y, acc.y);
-                    acc.z = fmaf(f, x[j].z, acc.z);
-                    acc.w = fmaf(f, x[j].w, acc.w);
+            for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+            const float now = fmaxf(m, top), base = now == -INFINITY ? 0.f : now, f0 = ex2(m - base);
+            const float w = ex2(s.x - base);     // of a part that saw nothing: 0, and it wrote no sums
+            m = now;
+            l = l * f0 + w * s.y;
+            acc.x *= f0; acc.y *= f0; acc.z *= f0; acc.w *= f0;
+            for (int k1 = 0; k1 < n; k1 += 16) {
+                if (k1) {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k)
+                        if (mine && k1 + k < n) x[k] = *reinterpret_cast<const float4 *>(part + (k0 + k1 + k) * part_step);
+                }
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    const float f = __shfl_sync(~0u, w, k1 + k);
+                    if (f == 0.f) continue;
+                    acc.x = fmaf(f, x[k].x, acc.x);
+                    acc.y = fmaf(f, x[k].y, acc.y);
+                    acc.z = fmaf(f, x[k].z, acc.z);
+                    acc.w = fmaf(f, x[k].w, acc.w);
                 }
             }
         }
 #pragma unroll
-        for (int s = 16; s; s >>= 1) l += __shfl_xor_sync(~0u, l, s);
+        for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
         const float inv = l > 0.f ? 1.f / l : 0.f, y[4] = {acc.x, acc.y, acc.z, acc.w};
-        T *o = out.at(q.b, q.row0 + tok, h);
+        T *o = out.at(it.b, it.row + tok, h);
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-            if (4 * lane + c < p.dv) o[4 * lane + c] = from_f32<T>(y[c] * inv);
-        if (lse && lane == 0) lse[stat_at(g, q, h, tok)] = l > 0.f ? (m + log2f(l)) * LN2 : -INFINITY;
+            if ((int)(4 * lane + c) < p.dv) o[4 * lane + c] = from_f32<T>(y[c] * inv);
+        if (lse && lane == 0) lse[((long long)it.b * g.H + h) * g.N + it.row + tok] = l > 0.f ? (m + log2f(l)) * LN2 : -INFINITY;
     }
 }
 
@@ -482,7 +518,7 @@ Plan make_plan(const gma_attn_t &a, int pack, int wide_rows, int narrow_rows, in
     p.rows = (int)std::min<long long>(p.wide, n) * pack;
     p.head_at = ws->take(sizeof(PlanHead));
     p.items_at = ws->take((size_t)p.max_items * sizeof(Item));
-    p.join_at = ws->take((size_t)p.max_slots * sizeof(int));
+    p.join_at = ws->take((size_t)p.max_slots * sizeof(Join));
     p.stat_at = ws->take((size_t)p.max_slots * p.heads * p.rows * 2 * sizeof(float));
     p.part_at = ws->take((size_t)p.max_slots * p.heads * p.rows * ((a.dv + 3) & ~3) * sizeof(float));
     return p;
@@ -492,7 +528,7 @@ PlanArgs plan_args(const Geo &g, const Plan &p, void *ws)
 {
     char *w = (char *)ws;
     return PlanArgs{g, p.wide, p.narrow, p.key_shift, p.blocks, p.heads, p.max_items, p.max_slots, p.by_keys, 1.f + p.rows / 64.f, (WsHeader *)ws,
-                    (PlanHead *)(w + p.head_at), (Item *)(w + p.items_at), (int *)(w + p.join_at)};
+                    (PlanHead *)(w + p.head_at), (Item *)(w + p.items_at), (Join *)(w + p.join_at)};
 }
 
 gma_status_t launch_plan(const PlanArgs &a, const PlanArgs *second, cudaStream_t st)
@@ -505,15 +541,14 @@ gma_status_t launch_join(const gma_attn_t &a, const Geo &g, const Plan &p, void 
 {
     const char *w = (const char *)ws;
     const PlanHead *head = (const PlanHead *)(w + p.head_at);
-    const Item *items = (const Item *)(w + p.items_at);
-    const int *join = (const int *)(w + p.join_at);
+    const Join *join = (const Join *)(w + p.join_at);
     const Parts parts = parts_of(p, a, ws);
     // as many rows as there may be in the parts
     const unsigned blocks = (unsigned)std::min<long long>(((long long)p.max_slots / 2 * p.heads * p.rows + 7) / 8, 4 * SMS);
     if (a.dtype == GMA_BF16)
-        GMA_LAUNCH(KID_ATTN_JOIN, st, launch_pdl(attn_join_kernel<bf16>, blocks, 256, 0, st, g, head, items, join, parts, heads_of<bf16>(a.o), a.lse, p.pack));
+        GMA_LAUNCH(KID_ATTN_JOIN, st, launch_pdl(attn_join_kernel<bf16>, blocks, 256, 0, st, g, head, join, parts, heads_of<bf16>(a.o), a.lse, p.pack));
     else
-        GMA_LAUNCH(KID_ATTN_JOIN, st, launch_pdl(attn_join_kernel<float>, blocks, 256, 0, st, g, head, items, join, parts, heads_of<float>(a.o), a.lse, p.pack));
+        GMA_LAUNCH(KID_ATTN_JOIN, st, launch_pdl(attn_join_kernel<float>, blocks, 256, 0, st, g, head, join, parts, heads_of<float>(a.o), a.lse, p.pack));
     return GMA_OK;
 }
 
