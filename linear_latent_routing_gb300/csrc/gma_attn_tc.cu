@@ -65,6 +65,30 @@ struct Bars {
     float merge[TILE][2];
 };
 
+// exp2(s sl2 - m) of 64 of a row's scores (from group `c0` of 32 on) as bf16 pairs into tensor memory, their sums in fp32, and (MAX)
+// the largest of these scores and of the 64 behind them.
+__device__ __forceinline__ void exponentials(const uint32_t (&r)[4][32], uint32_t ts, float sl2, float m, blk::f2 (&sum)[2], float (&x)[2])
+{
+    const float base = m == -INFINITY ? 0.f : -m;
+    const blk::f2 scale = blk::pack2(sl2, sl2), shift = blk::pack2(base, base);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        uint32_t p[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const float u = __uint_as_float(r[c][2 * e]), v = __uint_as_float(r[c][2 * e + 1]);
+            const blk::f2 y = blk::ex2_2(blk::fma2(blk::pack2(u, v), scale, shift));
+            {
+                x[e & 1] = fmaxf(x[e & 1], fmaxf(u, v));
+            }
+            sum[e & 1] = blk::add2(sum[e & 1], y);
+            const float2 z = blk::unpack2(y);
+            p[e] = pack_bf16(z.x, z.y);
+        }
+        tmem_st16(ts + 16 * c, p);
+    }
+}
+
 template <bool PAGED>
 __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const TcArgs a, const __grid_constant__ CUtensorMap qmap,
                                                              const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap)
@@ -244,8 +268,6 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const TcArgs a, con
             js ^= 1;
             if (!js) jt ^= 1u;
             if (!job.tokens) break;
-            // the next one's ticket, on its way while this one's tiles are loaded
-            if (lane == 0) ticket = atomicAdd(&a.head->ticket, 1);
             const Seq &sq = job.sq;
             const int t0 = job.t0, t1 = job.t1;
             // the page of this lane's box of a tile
@@ -296,6 +318,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const TcArgs a, con
                 }
                 if (!ok) break;
             }
+            // taken when this one's last tiles are on their way, not before: a block with a long item would hold on to a second one
+            if (lane == 0) ticket = atomicAdd(&a.head->ticket, 1);
             ticket = __shfl_sync(~0u, ticket, 0);
         }
         // loads that no product waited for (a wait gave up) end before the block does
@@ -347,48 +371,46 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const TcArgs a, con
                             for (int e = 0; e < 32; ++e)
                                 if (32 * c + e >= lim) r[c][e] = 0xff800000u;
                     }
-                    float x[4];
+                    blk::f2 half_sum[2];
+                    float top = -INFINITY;
+                    bool known = n > 0;
+                    while (true) {
+                        if (!known) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        x[c] = __uint_as_float(r[c][0]);
+                            for (int c = 0; c < 4; ++c) {
+                                float x = __uint_as_float(r[c][0]);
 #pragma unroll
-                        for (int e = 1; e < 32; ++e) x[c] = fmaxf(x[c], __uint_as_float(r[c][e]));
-                    }
-                    const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * g.sl2;
-                    if (__any_sync(~0u, top > m + GROW)) {
-                        const float now = fmaxf(m, top), f = now == -INFINITY ? 1.f : ex2(m - now);
-                        m = now;
-                        const blk::f2 ff = blk::pack2(f, f);
-                        l2 = blk::mul2(l2, ff);
-                        l3 = blk::mul2(l3, ff);
-                        if (n) {
+                                for (int e = 1; e < 32; ++e) x = fmaxf(x, __uint_as_float(r[c][e]));
+                                top = fmaxf(top, x);
+                            }
+                            const float now = fmaxf(m, top * g.sl2), f = now == -INFINITY ? 1.f : ex2(m - now);
+                            m = now;
+                            const blk::f2 ff = blk::pack2(f, f);
+                            l2 = blk::mul2(l2, ff);
+                            l3 = blk::mul2(l3, ff);
+                            if (n) {
 #pragma unroll 1
-                            for (int c = 0; c < g.dv; c += 32) {
-                                uint32_t v[32];
-                                tmem_ld32(to + c, v);
-                                tmem_ld_wait();
+                                for (int c = 0; c < g.dv; c += 16) {
+                                    uint32_t v[16];
+                                    tmem_ld16(to + c, v);
+                                    tmem_ld_wait();
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
-                                tmem_st16(to + c, *reinterpret_cast<uint32_t(*)[16]>(v));
-                                tmem_st16(to + c + 16, *reinterpret_cast<uint32_t(*)[16]>(v + 16));
+                                    for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
+                                    tmem_st16(to + c, v);
+                                }
                             }
                         }
+                        half_sum[0] = l2;
+                        half_sum[1] = l3;
+                        float x[2] = {-INFINITY, -INFINITY};
+                        exponentials(r, ts, g.sl2, m, half_sum, x);
+                        if (!known) break;
+                        top = fmaxf(x[0], x[1]);
+                        if (!__any_sync(~0u, top * g.sl2 > m + GROW)) break;
+                        known = false;
                     }
-                    const float base = m == -INFINITY ? 0.f : -m;
-                    const blk::f2 scale = blk::pack2(g.sl2, g.sl2), shift = blk::pack2(base, base);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t p[16];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const blk::f2 y = blk::ex2_2(
-                                blk::fma2(blk::pack2(__uint_as_float(r[c][2 * e]), __uint_as_float(r[c][2 * e + 1])), scale, shift));
-                            if (e & 1) l3 = blk::add2(l3, y); else l2 = blk::add2(l2, y);
-                            const float2 z = blk::unpack2(y);
-                            p[e] = pack_bf16(z.x, z.y);
-                        }
-                        tmem_st16(ts + 16 * c, p);
-                    }
+                    l2 = half_sum[0];
+                    l3 = half_sum[1];
                     tmem_st_wait();
                 }
                 tc_fence_before();
