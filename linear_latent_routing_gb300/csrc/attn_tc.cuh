@@ -28,6 +28,9 @@ __device__ __forceinline__ uint64_t mn_desc(uint32_t tile) { return smem_desc(ti
 constexpr __host__ __device__ uint32_t k_step(int s) { return ((uint32_t)(s >> 2) * BOX + (uint32_t)(s & 3) * 32u) >> 4; }
 constexpr __host__ __device__ uint32_t mn_step(int s) { return (uint32_t)(s * 16 * 128) >> 4; }
 
+// A first operand in tensor memory, k-step s: each half of its columns lies at the first ones of its half.
+__device__ __forceinline__ uint32_t half_col(int s) { return (uint32_t)(8 * s + (s >= 4 ? 32 : 0)); }
+
 // D = A B^T over `steps` k-steps of two K-major tiles.
 __device__ __forceinline__ void mma_tiles(uint32_t d, uint64_t a, uint64_t b, uint32_t id, int steps)
 {

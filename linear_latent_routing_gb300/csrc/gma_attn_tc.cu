@@ -67,25 +67,33 @@ struct Bars {
 
 // exp2(s sl2 - m) of 64 of a row's scores (from group `c0` of 32 on) as bf16 pairs into tensor memory, their sums in fp32, and (MAX)
 // the largest of these scores and of the 64 behind them.
-__device__ __forceinline__ void exponentials(const uint32_t (&r)[4][32], uint32_t ts, float sl2, float m, blk::f2 (&sum)[2], float (&x)[2])
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+template <bool MAX>
+__device__ __forceinline__ void exponentials(const uint32_t (&r)[4][32], int c0, uint32_t ts, float sl2, float m, blk::f2 (&sum)[2], float (&x)[2])
 {
     const float base = m == -INFINITY ? 0.f : -m;
     const blk::f2 scale = blk::pack2(sl2, sl2), shift = blk::pack2(base, base);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 0; c < 2; ++c) {
         uint32_t p[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-            const float u = __uint_as_float(r[c][2 * e]), v = __uint_as_float(r[c][2 * e + 1]);
+            const float u = __uint_as_float(r[c0 + c][2 * e]), v = __uint_as_float(r[c0 + c][2 * e + 1]);
             const blk::f2 y = blk::ex2_2(blk::fma2(blk::pack2(u, v), scale, shift));
-            {
-                x[e & 1] = fmaxf(x[e & 1], fmaxf(u, v));
+            if (MAX) {
+                x[0] = max3(x[0], u, v);
+                x[1] = max3(x[1], __uint_as_float(r[c0 + c + 2][2 * e]), __uint_as_float(r[c0 + c + 2][2 * e + 1]));
             }
             sum[e & 1] = blk::add2(sum[e & 1], y);
             const float2 z = blk::unpack2(y);
             p[e] = pack_bf16(z.x, z.y);
         }
-        tmem_st16(ts + 16 * c, p);
+        tmem_st16(ts + 16 * (c0 + c), p);
     }
 }
 
@@ -403,12 +411,14 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const TcArgs a, con
                         half_sum[0] = l2;
                         half_sum[1] = l3;
                         float x[2] = {-INFINITY, -INFINITY};
-                        exponentials(r, ts, g.sl2, m, half_sum, x);
+                        exponentials<true>(r, 0, ts, g.sl2, m, half_sum, x);
                         if (!known) break;
                         top = fmaxf(x[0], x[1]);
                         if (!__any_sync(~0u, top * g.sl2 > m + GROW)) break;
                         known = false;
                     }
+                    float none[2];
+                    exponentials<false>(r, 2, ts, g.sl2, m, half_sum, none);
                     l2 = half_sum[0];
                     l3 = half_sum[1];
                     tmem_st_wait();

@@ -37,9 +37,6 @@ struct GradArgs {
     uint32_t slot_bytes;
 };
 
-// The first operand of a product in tensor memory, k-step s: each half of the columns lies at its half's first ones.
-__device__ __forceinline__ uint32_t half_col(int s) { return (uint32_t)(8 * s + (s >= 4 ? 32 : 0)); }
-
 // 32 columns' values back as bf16 pairs in 16 columns.
 __device__ __forceinline__ void put_pairs(uint32_t at, const float (&v)[32])
 {
