@@ -410,7 +410,7 @@ gma_status_t check_sizes(const gma_attn_t *a, uint32_t flags)
     if (!a || a->reserved || (a->flags & ~flags)) return GMA_ERR_INVALID_ARG;
     if (a->B < 1 || a->N < 1 || a->H < 1 || a->G < 1 || a->d < 1 || a->dv < 1 || a->H % a->G) return GMA_ERR_INVALID_ARG;
     if (a->dtype != GMA_BF16 && a->dtype != GMA_F32) return GMA_ERR_INVALID_ARG;
-    if (!(a->scale > 0.f) || !(a->scale < 1e30f)) return GMA_ERR_INVALID_ARG;
+    if (!(a->scale >= 1e-12f) || !(a->scale <= 1e12f)) return GMA_ERR_INVALID_ARG;
     if (a->lengths && a->offsets) return GMA_ERR_INVALID_ARG;
     if (!blk::opt_ok(a->lengths, 4) || !blk::opt_ok(a->offsets, 4) || !blk::opt_ok(a->lse, 4)) return GMA_ERR_INVALID_ARG;
     if (a->d > 128 || a->dv > 128 || a->H > 4096 || a->B > 65535) return GMA_ERR_UNSUPPORTED_SHAPE;

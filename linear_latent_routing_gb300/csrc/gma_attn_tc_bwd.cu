@@ -5,7 +5,9 @@
 // fp32 copy of dq, so that repeated calls give the same bits.
 //
 // dk, dv: a block owns 128 keys of one key head and walks over the query tiles that see them, of every query head of the group.
-//   S^T = K Q^T, dP^T = V dO^T, P^T = exp2(S^T - lse), dS^T = P^T (dP^T - delta), dV += P^T dO, dK += dS^T Q.
+//   S^T = K Q^T - lse / scale, dP^T = V dO^T - delta, P^T = exp(scale S^T), dS^T = P^T dP^T, dV += P^T dO, dK += dS^T Q.
+// lse and delta belong to the columns here.  Read from shared memory they doubled the time of the exponentials (whose loads wait behind the
+// products'); so they are a k-step of the products, in three bf16 terms each.
 // Tensor memory: S^T | dP^T | dV | dK, 128 columns each.  P^T and dS^T, rounded to bf16 (half a step, 2^-8 relative), take the place of
 // S^T and dP^T as first operands.  The products' order hides the warps' work: while they take exponentials the tensor cores run dK
 // of the tile before and dP^T of this one, while they form dS^T they run dV of this tile and S^T of the next.
@@ -37,13 +39,33 @@ struct GradArgs {
     uint32_t slot_bytes;
 };
 
+// A row's statistic enters its products as one more k-step: three bf16 terms that add up to it in fp32's 24 bits, against ones.
+// Tiles of 128 rows of 16 (K-major, 32-byte swizzle), 4 KB.
+constexpr uint32_t EXTRA = TILE * 32;
+__device__ __forceinline__ uint64_t extra_desc(uint32_t tile) { return smem_desc(tile, 16, 256, SW_32B); }
+__device__ __forceinline__ void put_extra(uint8_t *tile, int row, float x)
+{
+    const bf16 hi = __float2bfloat16_rn(x);
+    const float r1 = x - __bfloat162float(hi);
+    const bf16 mid = __float2bfloat16_rn(r1), lo = __float2bfloat16_rn(r1 - __bfloat162float(mid));
+    const uint32_t a = (uint32_t)__bfloat16_as_ushort(hi) | (uint32_t)__bfloat16_as_ushort(mid) << 16, b = __bfloat16_as_ushort(lo);
+    *reinterpret_cast<uint4 *>(tile + row * 32 + (((row >> 2) & 1) << 4)) = make_uint4(a, b, 0, 0);
+}
+
 // 32 columns' values back as bf16 pairs in 16 columns.
-__device__ __forceinline__ void put_pairs(uint32_t at, const float (&v)[32])
+__device__ __forceinline__ void put_pairs(uint32_t at, const blk::f2 (&v)[16])
 {
     uint32_t w[16];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) w[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
+    for (int e = 0; e < 16; ++e) {
+        const float2 x = blk::unpack2(v[e]);
+        w[e] = pack_bf16(x.x, x.y);
+    }
     tmem_st16(at, w);
+}
+__device__ __forceinline__ blk::f2 pair_of(const uint32_t (&r)[32], int e)
+{
+    return blk::pack2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
 }
 
 // ------------------------------------------------------------------ dk, dv
@@ -51,7 +73,6 @@ struct KeyBars {
     uint64_t kv, fq[STAGES], fo[STAGES], eq[STAGES], eo[STAGES], s, dp, p, ds, done, drain;
     uint32_t tmem;
     int abort;
-    alignas(16) float lse2[STAGES][TILE], delta[STAGES][TILE];
 };
 
 __global__ void __launch_bounds__(THREADS, 1) attn_dkv_kernel(const GradArgs a, const __grid_constant__ CUtensorMap qmap,
@@ -62,7 +83,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dkv_kernel(const GradArgs a, 
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     const uint32_t q_tile = (uint32_t)a.q_boxes * BOX, v_tile = (uint32_t)a.v_boxes * BOX, stage = q_tile + v_tile;
     uint8_t *ring = smem + stage;                                // K and V lie before it
-    KeyBars *bars = reinterpret_cast<KeyBars *>(ring + (size_t)a.stages * stage);
+    uint8_t *ones = ring + (size_t)a.stages * stage, *extra = ones + EXTRA;      // extra: of each stage, -lse / scale and -delta
+    KeyBars *bars = reinterpret_cast<KeyBars *>(extra + (size_t)a.stages * 2 * EXTRA);
     volatile int *abort = &bars->abort;
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
     if (t == 256) {
@@ -91,6 +113,13 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dkv_kernel(const GradArgs a, 
     const Item it = a.k_items[rank];
     const Seq sq = sequence(g, it.seq);
     const int tiles = it.t1 - it.t0, steps = tiles * g.group;
+    for (int i = t; i < TILE; i += THREADS) {
+        *reinterpret_cast<uint4 *>(ones + i * 32 + (((i >> 2) & 1) << 4)) = make_uint4(0x3f803f80u, 0x3f80u, 0, 0);
+        *reinterpret_cast<uint4 *>(ones + i * 32 + ((((i >> 2) & 1) ^ 1) << 4)) = make_uint4(0, 0, 0, 0);
+    }
+    for (int i = t; i < a.stages * 2 * TILE; i += THREADS)
+        *reinterpret_cast<uint4 *>(extra + i * 32 + ((((i >> 2) & 1) ^ 1) << 4)) = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -101,7 +130,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dkv_kernel(const GradArgs a, 
         const uint32_t id_v = idesc_f16(TILE, (uint32_t)(g.dv + 15) & ~15u, 1, 1, 0, 1), id_k = idesc_f16(TILE, (uint32_t)(g.d + 15) & ~15u, 1, 1, 0, 1);
         const int kq = (g.d + 15) >> 4, ko = (g.dv + 15) >> 4;
         bool ok = bar_wait(&bars->kv, 0, a.hdr, 220, abort);
-        const uint64_t kd = k_desc(sb), vd = k_desc(sb + q_tile);
+        const uint64_t kd = k_desc(sb), vd = k_desc(sb + q_tile), ones_desc = extra_desc(smem_u32(ones));
+        const uint32_t xb = smem_u32(extra);
         // the steps whose scores and whose dP come next, and the one at hand; rows that a step's tile has
         RingPos rs{0, 0}, rp{0, 0}, rc{0, 0};
         int js = 0, jp = 0;
@@ -113,6 +143,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dkv_kernel(const GradArgs a, 
             if (++js == tiles) js = 0;
             if (elect()) {
                 mma_tiles(tmem, kd, k_desc(rb + rs.s * stage), id_s, kq);
+                mma_f16(tmem, ones_desc, extra_desc(xb + rs.s * 2 * EXTRA), id_s, 1u);
                 mma_commit(&bars->s);
             }
             rs.step(1, a.stages);
@@ -124,6 +155,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dkv_kernel(const GradArgs a, 
             if (++jp == tiles) jp = 0;
             if (elect()) {
                 mma_tiles(tmem + 128, vd, k_desc(rb + rp.s * stage + q_tile), id_s, ko);
+                mma_f16(tmem + 128, ones_desc, extra_desc(xb + rp.s * 2 * EXTRA + EXTRA), id_s, 1u);
                 mma_commit(&bars->dp);
             }
             rp.step(1, a.stages);
@@ -165,6 +197,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dkv_kernel(const GradArgs a, 
         bool ok = true;
         int issued_q = 0, issued_o = 0;
         RingPos r{0, 1};
+        const float inv_scale = 1.f / g.scale;
         int h = kvh * g.group, j = 0;
         for (int i = 0; ok && i < steps; ++i) {
             const int q0 = (it.t0 + j) * TILE, s = r.s;
@@ -175,8 +208,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dkv_kernel(const GradArgs a, 
             for (int k = 0; k < 4; ++k) {
                 const int row = q0 + lane + 32 * k;
                 const long long at = row < sq.n ? stat_at(g, sq, h, row) : 0;
-                l[k] = row < sq.n ? a.lse[at] * LOG2E : INFINITY;       // a row that is not there has probabilities of zero
-                e[k] = row < sq.n ? a.delta[at] : 0.f;
+                l[k] = row < sq.n ? -a.lse[at] * inv_scale : 0.f;
+                e[k] = row < sq.n ? -a.delta[at] : 0.f;
             }
             if (!(ok = bar_wait(&bars->eq[s], free, a.hdr, 226, abort))) break;
             if (lane == 0) {
@@ -186,9 +219,10 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dkv_kernel(const GradArgs a, 
             issued_q = i + 1;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                bars->lse2[s][lane + 32 * k] = l[k];
-                bars->delta[s][lane + 32 * k] = e[k];
+                put_extra(extra + s * 2 * EXTRA, lane + 32 * k, l[k]);
+                put_extra(extra + s * 2 * EXTRA + EXTRA, lane + 32 * k, e[k]);
             }
+            fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->fq[s]);
             if (!(ok = bar_wait(&bars->eo[s], free, a.hdr, 227, abort))) break;
@@ -215,39 +249,37 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dkv_kernel(const GradArgs a, 
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + 64 * w, td = ts + 128;
         bool ok = true;
-        RingPos ring_at{0, 0};
         int j = 0;
+        const blk::f2 scale = blk::pack2(g.sl2, g.sl2);
         for (int i = 0; i < steps; ++i) {
-            const int s = ring_at.s, q0 = (it.t0 + j) * TILE + 64 * w;
+            const int q0 = (it.t0 + j) * TILE + 64 * w;
             if (++j == tiles) j = 0;
-            if (!(ok = bar_wait(&bars->fq[s], ring_at.turn, a.hdr, 231, abort))) break;
-            ring_at.step(1, a.stages);
+            // columns that this row's key is seen by, of those that are there: [from, to)
+            const int from = g.causal ? key - q0 : 0, to = sq.n - q0;
+            const bool edge = __any_sync(~0u, from > 0 || to < 64);
             if (!(ok = bar_wait(&bars->s, i & 1, a.hdr, 232, abort))) break;
             tc_fence_after();
-            float p[2][32];
-            const bool edge = g.causal && __any_sync(~0u, q0 < key);
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t r[32];
-                tmem_ld32(ts + 32 * c, r);
+            blk::f2 p[2][16];
+            {
+                uint32_t r[2][32];
+                tmem_ld32(ts, r[0]);
+                tmem_ld32(ts + 32, r[1]);
                 tmem_ld_wait();
-                const float *lse2 = &bars->lse2[s][64 * w + 32 * c];
 #pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                    const float4 l = *reinterpret_cast<const float4 *>(lse2 + e);
-                    p[c][e] = ex2(fmaf(__uint_as_float(r[e]), g.sl2, -l.x));
-                    p[c][e + 1] = ex2(fmaf(__uint_as_float(r[e + 1]), g.sl2, -l.y));
-                    p[c][e + 2] = ex2(fmaf(__uint_as_float(r[e + 2]), g.sl2, -l.z));
-                    p[c][e + 3] = ex2(fmaf(__uint_as_float(r[e + 3]), g.sl2, -l.w));
-                }
-                if (edge) {
+                for (int c = 0; c < 2; ++c) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (q0 + 32 * c + e < key) p[c][e] = 0.f;
+                    for (int e = 0; e < 16; ++e) p[c][e] = blk::ex2_2(blk::mul2(pair_of(r[c], e), scale));
+                    if (edge) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const int col = 32 * c + 2 * e;
+                            const float2 x = blk::unpack2(p[c][e]);
+                            p[c][e] = blk::pack2(col >= from && col < to ? x.x : 0.f, col + 1 >= from && col + 1 < to ? x.y : 0.f);
+                        }
+                    }
+                    put_pairs(ts + 16 * c, p[c]);
                 }
             }
-#pragma unroll
-            for (int c = 0; c < 2; ++c) put_pairs(ts + 16 * c, p[c]);
             tmem_st_wait();
             tc_fence_before();
             mbar_arrive(&bars->p);
@@ -259,15 +291,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dkv_kernel(const GradArgs a, 
             tmem_ld_wait();
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                const float *delta = &bars->delta[s][64 * w + 32 * c];
 #pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                    const float4 l = *reinterpret_cast<const float4 *>(delta + e);
-                    p[c][e] *= __uint_as_float(r[c][e]) - l.x;
-                    p[c][e + 1] *= __uint_as_float(r[c][e + 1]) - l.y;
-                    p[c][e + 2] *= __uint_as_float(r[c][e + 2]) - l.z;
-                    p[c][e + 3] *= __uint_as_float(r[c][e + 3]) - l.w;
-                }
+                for (int e = 0; e < 16; ++e) p[c][e] = blk::mul2(p[c][e], pair_of(r[c], e));
                 put_pairs(td + 16 * c, p[c]);
             }
             tmem_st_wait();
@@ -415,35 +440,42 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dq_kernel(const GradArgs a, c
         const int seen = valid ? sq.seen(g, tok) : sq.L;
         const long long at = valid ? stat_at(g, sq, h, tok) : 0;
         const float lse2 = valid ? a.lse[at] * LOG2E : 0.f, delta = valid ? a.delta[at] : 0.f;
+        const blk::f2 scale = blk::pack2(g.sl2, g.sl2), less = blk::pack2(-lse2, -lse2), minus = blk::pack2(-delta, -delta);
         bool ok = true;
         for (int j = 0; j < tiles; ++j) {
             const uint32_t ts = tmem + lanes + 128 * (j & 1) + 64 * w, td = tmem + lanes + 256 + 64 * w;
             if (!(ok = bar_wait(&bars->s[j & 1], (j >> 1) & 1, a.hdr, 247, abort))) break;
             tc_fence_after();
             const int lim = seen - (it.t0 + j) * TILE - 64 * w;
-            float p[2][32];
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t r[32];
-                tmem_ld32(ts + 32 * c, r);
+            const bool edge = __any_sync(~0u, lim < 64);
+            blk::f2 p[2][16];
+            {
+                uint32_t r[2][32];
+                tmem_ld32(ts, r[0]);
+                tmem_ld32(ts + 32, r[1]);
                 tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 32; ++e) p[c][e] = ex2(fmaf(__uint_as_float(r[e]), g.sl2, -lse2));
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) p[c][e] = blk::ex2_2(blk::fma2(pair_of(r[c], e), scale, less));
             }
             if (!(ok = bar_wait(&bars->dp, j & 1, a.hdr, 248, abort))) break;
             tc_fence_after();
-            const bool edge = __any_sync(~0u, lim < 64);
+            uint32_t r[2][32];
+            tmem_ld32(td, r[0]);
+            tmem_ld32(td + 32, r[1]);
+            tmem_ld_wait();
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                uint32_t r[32];
-                tmem_ld32(td + 32 * c, r);
-                tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 32; ++e) p[c][e] *= __uint_as_float(r[e]) - delta;
+                for (int e = 0; e < 16; ++e) p[c][e] = blk::mul2(p[c][e], blk::add2(pair_of(r[c], e), minus));
                 if (edge) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (32 * c + e >= lim) p[c][e] = 0.f;
+                    for (int e = 0; e < 16; ++e) {
+                        const int col = 32 * c + 2 * e;
+                        const float2 x = blk::unpack2(p[c][e]);
+                        p[c][e] = blk::pack2(col < lim ? x.x : 0.f, col + 1 < lim ? x.y : 0.f);
+                    }
                 }
                 put_pairs(ts + 16 * c, p[c]);
             }
@@ -519,9 +551,10 @@ gma_status_t tc_backward(const gma_attn_grad_t &g, void *ws, cudaStream_t st)
     x.hdr = (WsHeader *)ws;
     x.q_boxes = (a.d + 63) / 64;
     x.v_boxes = (a.dv + 63) / 64;
-    const uint32_t pair = BOX * (uint32_t)(x.q_boxes + x.v_boxes), k_fixed = pair + 1024 + (uint32_t)sizeof(KeyBars),
+    const uint32_t pair = BOX * (uint32_t)(x.q_boxes + x.v_boxes), k_fixed = pair + EXTRA + 1024 + (uint32_t)sizeof(KeyBars),
                    q_fixed = pair + 1024 + (uint32_t)sizeof(QueryBars);
-    x.stages = (int)((SMEM_MAX - k_fixed) / pair);
+    const uint32_t k_stage = pair + 2 * EXTRA;
+    x.stages = (int)((SMEM_MAX - k_fixed) / k_stage);
     if (x.stages > STAGES) x.stages = STAGES;
     x.slot_bytes = BOX * (uint32_t)(x.q_boxes > x.v_boxes ? x.q_boxes : x.v_boxes);
     x.slots = (int)((SMEM_MAX - q_fixed) / x.slot_bytes);
@@ -540,7 +573,7 @@ gma_status_t tc_backward(const gma_attn_grad_t &g, void *ws, cudaStream_t st)
     if (cudaFuncSetAttribute(attn_dkv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_MAX) != cudaSuccess ||
         cudaFuncSetAttribute(attn_dq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_MAX) != cudaSuccess)
         return GMA_ERR_CUDA;
-    GMA_LAUNCH(KID_ATTN_DKV, st, launch_pdl(attn_dkv_kernel, (unsigned)p.k.max_items * a.G, THREADS, k_fixed + x.stages * pair, st, x, qm, km, vm, om));
+    GMA_LAUNCH(KID_ATTN_DKV, st, launch_pdl(attn_dkv_kernel, (unsigned)p.k.max_items * a.G, THREADS, k_fixed + x.stages * k_stage, st, x, qm, km, vm, om));
     GMA_LAUNCH(KID_ATTN_DQ, st, launch_pdl(attn_dq_kernel, (unsigned)p.q.max_items * a.H, THREADS, q_fixed + x.slots * x.slot_bytes, st, x, qm, km, vm, om));
     return GMA_OK;
 }
