@@ -24,7 +24,7 @@ namespace att {
 namespace {
 
 constexpr int THREADS = 384;
-constexpr int STAGES = 4, SLOTS = 8;         // at most
+constexpr int STAGES = 4, SLOTS = 5;         // at most
 
 struct GradArgs {
     Geo g;
@@ -35,21 +35,20 @@ struct GradArgs {
     int q_vec, k_vec, v_vec;     // 16-byte stores
     WsHeader *hdr;
     int q_boxes, v_boxes;
-    int stages, slots;           // of the two kernels' rings
-    uint32_t slot_bytes;
+    int stages, k_slots, v_slots; // of the two kernels' rings
 };
 
 // A row's statistic enters its products as one more k-step: three bf16 terms that add up to it in fp32's 24 bits, against ones.
-// Tiles of 128 rows of 16 (K-major, 32-byte swizzle), 4 KB.
+// Tiles of 128 rows of 16 (K-major, not swizzled: 8 rows of 16 bytes at a time, the first eight columns of all rows before the others), 4 KB.
 constexpr uint32_t EXTRA = TILE * 32;
-__device__ __forceinline__ uint64_t extra_desc(uint32_t tile) { return smem_desc(tile, 16, 256, SW_32B); }
+__device__ __forceinline__ uint64_t extra_desc(uint32_t tile) { return smem_desc(tile, TILE * 16, 128, SW_NONE); }
 __device__ __forceinline__ void put_extra(uint8_t *tile, int row, float x)
 {
     const bf16 hi = __float2bfloat16_rn(x);
     const float r1 = x - __bfloat162float(hi);
     const bf16 mid = __float2bfloat16_rn(r1), lo = __float2bfloat16_rn(r1 - __bfloat162float(mid));
     const uint32_t a = (uint32_t)__bfloat16_as_ushort(hi) | (uint32_t)__bfloat16_as_ushort(mid) << 16, b = __bfloat16_as_ushort(lo);
-    *reinterpret_cast<uint4 *>(tile + row * 32 + (((row >> 2) & 1) << 4)) = make_uint4(a, b, 0, 0);
+    *reinterpret_cast<uint4 *>(tile + row * 16) = make_uint4(a, b, 0, 0);
 }
 
 // 32 columns' values back as bf16 pairs in 16 columns.
@@ -114,11 +113,11 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dkv_kernel(const GradArgs a, 
     const Seq sq = sequence(g, it.seq);
     const int tiles = it.t1 - it.t0, steps = tiles * g.group;
     for (int i = t; i < TILE; i += THREADS) {
-        *reinterpret_cast<uint4 *>(ones + i * 32 + (((i >> 2) & 1) << 4)) = make_uint4(0x3f803f80u, 0x3f80u, 0, 0);
-        *reinterpret_cast<uint4 *>(ones + i * 32 + ((((i >> 2) & 1) ^ 1) << 4)) = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4 *>(ones + i * 16) = make_uint4(0x3f803f80u, 0x3f80u, 0, 0);
+        *reinterpret_cast<uint4 *>(ones + (TILE + i) * 16) = make_uint4(0, 0, 0, 0);
     }
     for (int i = t; i < a.stages * 2 * TILE; i += THREADS)
-        *reinterpret_cast<uint4 *>(extra + i * 32 + ((((i >> 2) & 1) ^ 1) << 4)) = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4 *>(extra + (i / TILE) * EXTRA + (TILE + i % TILE) * 16) = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
@@ -314,7 +313,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dkv_kernel(const GradArgs a, 
 
 // ------------------------------------------------------------------ dq
 struct QueryBars {
-    uint64_t q, full[SLOTS], empty[SLOTS], s[2], dp, ds, done, drain;
+    uint64_t q, fk[SLOTS], ek[SLOTS], fv[SLOTS], ev[SLOTS], s[2], dp, ds, done, drain;
     uint32_t tmem;
     int abort;
 };
@@ -327,14 +326,17 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dq_kernel(const GradArgs a, c
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     const uint32_t q_tile = (uint32_t)a.q_boxes * BOX, v_tile = (uint32_t)a.v_boxes * BOX;
     uint8_t *ring = smem + q_tile + v_tile;
-    QueryBars *bars = reinterpret_cast<QueryBars *>(ring + (size_t)a.slots * a.slot_bytes);
+    uint8_t *vring = ring + (size_t)a.k_slots * q_tile;
+    QueryBars *bars = reinterpret_cast<QueryBars *>(vring + (size_t)a.v_slots * v_tile);
     volatile int *abort = &bars->abort;
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
     if (t == 256) {
         mbar_init(&bars->q, 1);
-        for (int i = 0; i < a.slots; ++i) {
-            mbar_init(&bars->full[i], 1);
-            mbar_init(&bars->empty[i], 1);
+        for (int i = 0; i < SLOTS; ++i) {
+            mbar_init(&bars->fk[i], 1);
+            mbar_init(&bars->ek[i], 1);
+            mbar_init(&bars->fv[i], 1);
+            mbar_init(&bars->ev[i], 1);
         }
         mbar_init(&bars->s[0], 1);
         mbar_init(&bars->s[1], 1);
@@ -356,7 +358,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dq_kernel(const GradArgs a, c
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = bars->tmem, sb = smem_u32(smem), rb = smem_u32(ring);
+    const uint32_t tmem = bars->tmem, sb = smem_u32(smem), rb = smem_u32(ring), vb = smem_u32(vring);
 
     if (warp == 8) {
         const uint32_t id_s = idesc_f16(TILE, TILE, 1, 1, 0, 0), id_q = idesc_f16(TILE, (uint32_t)(g.d + 15) & ~15u, 1, 1, 0, 1);
@@ -364,28 +366,27 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dq_kernel(const GradArgs a, c
         bool ok = bar_wait(&bars->q, 0, a.hdr, 240, abort);
         const uint64_t qd = k_desc(sb), od = k_desc(sb + q_tile);
         // the ring's places of the keys whose scores come next, of the values whose dP does, and of the keys at hand
-        RingPos rk{0, 0}, rv{1, 0}, rc{0, 0};
-        auto loaded = [&](const RingPos &r) { return bar_wait(&bars->full[r.s], r.turn, a.hdr, 241, abort); };
+        RingPos rk{0, 0}, rv{0, 0}, rc{0, 0};
         auto scores = [&](int j) {
-            if (!loaded(rk)) return false;
+            if (!bar_wait(&bars->fk[rk.s], rk.turn, a.hdr, 241, abort)) return false;
             // keys behind the sequence's end meet zeros of dS, and may be anything
             const int have = sq.L - (it.t0 + j) * TILE;
-            if (have < TILE) zero_rows(ring + (size_t)rk.s * a.slot_bytes, a.q_boxes, have);
+            if (have < TILE) zero_rows(ring + (size_t)rk.s * q_tile, a.q_boxes, have);
             if (elect()) {
-                mma_tiles(tmem + 128 * (j & 1), qd, k_desc(rb + (uint32_t)rk.s * a.slot_bytes), id_s, kq);
+                mma_tiles(tmem + 128 * (j & 1), qd, k_desc(rb + (uint32_t)rk.s * q_tile), id_s, kq);
                 mma_commit(&bars->s[j & 1]);
             }
-            rk.step(2, a.slots);
+            rk.step(1, a.k_slots);
             return true;
         };
         auto dprobs = [&]() {
-            if (!loaded(rv)) return false;
+            if (!bar_wait(&bars->fv[rv.s], rv.turn, a.hdr, 250, abort)) return false;
             if (elect()) {
-                mma_tiles(tmem + 256, od, k_desc(rb + (uint32_t)rv.s * a.slot_bytes), id_s, ko);
+                mma_tiles(tmem + 256, od, k_desc(vb + (uint32_t)rv.s * v_tile), id_s, ko);
                 mma_commit(&bars->dp);
-                mma_commit(&bars->empty[rv.s]);
+                mma_commit(&bars->ev[rv.s]);
             }
-            rv.step(2, a.slots);
+            rv.step(1, a.v_slots);
             return true;
         };
         ok = ok && scores(0) && dprobs();
@@ -395,13 +396,13 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dq_kernel(const GradArgs a, c
             tc_fence_after();
             if (j + 1 < tiles && !(ok = dprobs())) break;
             if (elect()) {
-                const uint64_t k = mn_desc(rb + (uint32_t)rc.s * a.slot_bytes);
+                const uint64_t k = mn_desc(rb + (uint32_t)rc.s * q_tile);
                 const uint32_t ds = tmem + 128 * (j & 1);
 #pragma unroll
                 for (int s = 0; s < 8; ++s) mma_f16_tmem_a(tmem + 384, ds + half_col(s), k + mn_step(s), id_q, j > 0 || s > 0);
-                mma_commit(&bars->empty[rc.s]);
+                mma_commit(&bars->ek[rc.s]);
             }
-            rc.step(2, a.slots);
+            rc.step(1, a.k_slots);
         }
         if (ok && elect()) mma_commit(&bars->done);
         if (*abort) {
@@ -414,24 +415,33 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dq_kernel(const GradArgs a, c
             for (int b = 0; b < a.q_boxes; ++b) tma_load_4d(sb + b * BOX, &qmap, &bars->q, 64 * b, h, sq.row0 + it.tok0, sq.b);
             for (int b = 0; b < a.v_boxes; ++b) tma_load_4d(sb + q_tile + b * BOX, &omap, &bars->q, 64 * b, h, sq.row0 + it.tok0, sq.b);
         }
+        // keys wait for the products of two tiles before their place is free, values for one: rings of their own
         bool ok = true;
-        int issued = 0;
-        RingPos r{0, 1};
-        for (int c = 0; ok && c < 2 * tiles; ++c) {
-            const int s = r.s, row = sq.row0 + (it.t0 + (c >> 1)) * TILE;
-            if (!(ok = bar_wait(&bars->empty[s], r.turn, a.hdr, 244, abort))) break;
-            r.step(1, a.slots);
+        int keys = 0, values = 0;
+        RingPos rk{0, 1}, rv{0, 1};
+        for (int j = 0; ok && j < tiles; ++j) {
+            const int row = sq.row0 + (it.t0 + j) * TILE;
+            if (!(ok = bar_wait(&bars->ek[rk.s], rk.turn, a.hdr, 244, abort))) break;
             if (lane == 0) {
-                const int nb = c & 1 ? a.v_boxes : a.q_boxes;
-                mbar_arrive_expect_tx(&bars->full[s], BOX * nb);
-                for (int b = 0; b < nb; ++b) tma_load_4d(rb + s * a.slot_bytes + b * BOX, c & 1 ? &vmap : &kmap, &bars->full[s], 64 * b, kvh, row, sq.b);
+                mbar_arrive_expect_tx(&bars->fk[rk.s], q_tile);
+                for (int b = 0; b < a.q_boxes; ++b) tma_load_4d(rb + rk.s * q_tile + b * BOX, &kmap, &bars->fk[rk.s], 64 * b, kvh, row, sq.b);
             }
-            issued = c + 1;
+            ++keys;
+            rk.step(1, a.k_slots);
+            if (!(ok = bar_wait(&bars->ev[rv.s], rv.turn, a.hdr, 251, abort))) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&bars->fv[rv.s], v_tile);
+                for (int b = 0; b < a.v_boxes; ++b) tma_load_4d(vb + rv.s * v_tile + b * BOX, &vmap, &bars->fv[rv.s], 64 * b, kvh, row, sq.b);
+            }
+            ++values;
+            rv.step(1, a.v_slots);
         }
         if (*abort) {
             mbar_wait(&bars->q, 0, a.hdr, 245);
-            for (int c = issued > a.slots ? issued - a.slots : 0; c < issued; ++c)
-                mbar_wait(&bars->full[c % a.slots], (uint32_t)(c / a.slots) & 1u, a.hdr, 246);
+            for (int c = keys > a.k_slots ? keys - a.k_slots : 0; c < keys; ++c)
+                mbar_wait(&bars->fk[c % a.k_slots], (uint32_t)(c / a.k_slots) & 1u, a.hdr, 246);
+            for (int c = values > a.v_slots ? values - a.v_slots : 0; c < values; ++c)
+                mbar_wait(&bars->fv[c % a.v_slots], (uint32_t)(c / a.v_slots) & 1u, a.hdr, 252);
         }
     } else if (warp < 8) {
         const int w = warp >> 2, row = t & (TILE - 1), tok = it.tok0 + row;
@@ -556,9 +566,11 @@ gma_status_t tc_backward(const gma_attn_grad_t &g, void *ws, cudaStream_t st)
     const uint32_t k_stage = pair + 2 * EXTRA;
     x.stages = (int)((SMEM_MAX - k_fixed) / k_stage);
     if (x.stages > STAGES) x.stages = STAGES;
-    x.slot_bytes = BOX * (uint32_t)(x.q_boxes > x.v_boxes ? x.q_boxes : x.v_boxes);
-    x.slots = (int)((SMEM_MAX - q_fixed) / x.slot_bytes);
-    if (x.slots > SLOTS) x.slots = SLOTS;
+    const uint32_t q_room = SMEM_MAX - q_fixed;
+    x.v_slots = (int)(q_room / pair);                             // and one more of keys, where there is room
+    if (x.v_slots > SLOTS - 1) x.v_slots = SLOTS - 1;
+    x.k_slots = x.v_slots + (q_room - x.v_slots * pair >= BOX * (uint32_t)x.q_boxes ? 1 : 0);
+    const uint32_t q_ring = BOX * (uint32_t)(x.k_slots * x.q_boxes + x.v_slots * x.v_boxes);
     const long long B = a.offsets ? 1 : a.B;
     CUtensorMap qm, km, vm, om;
     if (!heads_map(&qm, a.q, B, a.N, a.H, a.d, 1, TILE) || !heads_map(&km, a.k, B, a.N, a.G, a.d, 1, TILE) ||
@@ -574,7 +586,7 @@ gma_status_t tc_backward(const gma_attn_grad_t &g, void *ws, cudaStream_t st)
         cudaFuncSetAttribute(attn_dq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_MAX) != cudaSuccess)
         return GMA_ERR_CUDA;
     GMA_LAUNCH(KID_ATTN_DKV, st, launch_pdl(attn_dkv_kernel, (unsigned)p.k.max_items * a.G, THREADS, k_fixed + x.stages * k_stage, st, x, qm, km, vm, om));
-    GMA_LAUNCH(KID_ATTN_DQ, st, launch_pdl(attn_dq_kernel, (unsigned)p.q.max_items * a.H, THREADS, q_fixed + x.slots * x.slot_bytes, st, x, qm, km, vm, om));
+    GMA_LAUNCH(KID_ATTN_DQ, st, launch_pdl(attn_dq_kernel, (unsigned)p.q.max_items * a.H, THREADS, q_fixed + q_ring, st, x, qm, km, vm, om));
     return GMA_OK;
 }
 
