@@ -39,16 +39,16 @@ struct GradArgs {
 };
 
 // A row's statistic enters its products as one more k-step: three bf16 terms that add up to it in fp32's 24 bits, against ones.
-// Tiles of 128 rows of 16 (K-major, not swizzled: 8 rows of 16 bytes at a time, the first eight columns of all rows before the others), 4 KB.
+// Tiles of 128 rows of 16 (K-major, 32-byte swizzle), 4 KB.
 constexpr uint32_t EXTRA = TILE * 32;
-__device__ __forceinline__ uint64_t extra_desc(uint32_t tile) { return smem_desc(tile, TILE * 16, 128, SW_NONE); }
+__device__ __forceinline__ uint64_t extra_desc(uint32_t tile) { return smem_desc(tile, 16, 256, SW_32B); }
 __device__ __forceinline__ void put_extra(uint8_t *tile, int row, float x)
 {
     const bf16 hi = __float2bfloat16_rn(x);
     const float r1 = x - __bfloat162float(hi);
     const bf16 mid = __float2bfloat16_rn(r1), lo = __float2bfloat16_rn(r1 - __bfloat162float(mid));
     const uint32_t a = (uint32_t)__bfloat16_as_ushort(hi) | (uint32_t)__bfloat16_as_ushort(mid) << 16, b = __bfloat16_as_ushort(lo);
-    *reinterpret_cast<uint4 *>(tile + row * 16) = make_uint4(a, b, 0, 0);
+    *reinterpret_cast<uint4 *>(tile + row * 32 + (((row >> 2) & 1) << 4)) = make_uint4(a, b, 0, 0);
 }
 
 // 32 columns' values back as bf16 pairs in 16 columns.
@@ -74,6 +74,7 @@ struct KeyBars {
     int abort;
 };
 
+template <bool EARLY>
 __global__ void __launch_bounds__(THREADS, 1) attn_dkv_kernel(const GradArgs a, const __grid_constant__ CUtensorMap qmap,
                                                               const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                                                               const __grid_constant__ CUtensorMap omap)
@@ -113,11 +114,11 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dkv_kernel(const GradArgs a, 
     const Seq sq = sequence(g, it.seq);
     const int tiles = it.t1 - it.t0, steps = tiles * g.group;
     for (int i = t; i < TILE; i += THREADS) {
-        *reinterpret_cast<uint4 *>(ones + i * 16) = make_uint4(0x3f803f80u, 0x3f80u, 0, 0);
-        *reinterpret_cast<uint4 *>(ones + (TILE + i) * 16) = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4 *>(ones + i * 32 + (((i >> 2) & 1) << 4)) = make_uint4(0x3f803f80u, 0x3f80u, 0, 0);
+        *reinterpret_cast<uint4 *>(ones + i * 32 + ((((i >> 2) & 1) ^ 1) << 4)) = make_uint4(0, 0, 0, 0);
     }
     for (int i = t; i < a.stages * 2 * TILE; i += THREADS)
-        *reinterpret_cast<uint4 *>(extra + (i / TILE) * EXTRA + (TILE + i % TILE) * 16) = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4 *>(extra + i * 32 + ((((i >> 2) & 1) ^ 1) << 4)) = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
@@ -136,8 +137,9 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dkv_kernel(const GradArgs a, 
         int js = 0, jp = 0;
         auto rows = [&](int j) { return sq.n - (it.t0 + j) * TILE; };
         // rows behind the sequence's end meet zeros of P and dS, and may be anything
+        auto q_there = [&]() { return bar_wait(&bars->fq[rs.s], rs.turn, a.hdr, 221, abort); };
+        auto o_there = [&]() { return bar_wait(&bars->fo[rp.s], rp.turn, a.hdr, 222, abort); };
         auto scores = [&]() {
-            if (!bar_wait(&bars->fq[rs.s], rs.turn, a.hdr, 221, abort)) return false;
             if (rows(js) < TILE) zero_rows(ring + rs.s * stage, a.q_boxes, rows(js));
             if (++js == tiles) js = 0;
             if (elect()) {
@@ -146,10 +148,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dkv_kernel(const GradArgs a, 
                 mma_commit(&bars->s);
             }
             rs.step(1, a.stages);
-            return true;
         };
         auto dprobs = [&]() {
-            if (!bar_wait(&bars->fo[rp.s], rp.turn, a.hdr, 222, abort)) return false;
             if (rows(jp) < TILE) zero_rows(ring + rp.s * stage + q_tile, a.v_boxes, rows(jp));
             if (++jp == tiles) jp = 0;
             if (elect()) {
@@ -158,10 +158,15 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dkv_kernel(const GradArgs a, 
                 mma_commit(&bars->dp);
             }
             rp.step(1, a.stages);
-            return true;
         };
-        ok = ok && scores() && dprobs();
+        // With tiles to spare their arrival is waited for before the warps' barriers, so that two products follow one another at once; with two
+        // stages they come late, and the first product does not wait for the second's (64 wide: 358 -> 346 us over 4 x 4096 x 16 heads so, 128
+        // wide: 358 -> 389 over 8192 x 16).
+        if ((ok = ok && q_there())) scores();
+        if ((ok = ok && o_there())) dprobs();
         for (int i = 0; ok && i < steps; ++i) {
+            const bool more = i + 1 < steps;
+            if (EARLY && more && !(ok = q_there())) break;
             if (!(ok = bar_wait(&bars->p, i & 1, a.hdr, 223, abort))) break;
             tc_fence_after();
             if (elect()) {
@@ -170,7 +175,11 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dkv_kernel(const GradArgs a, 
                 for (int s = 0; s < 8; ++s) mma_f16_tmem_a(tmem + 256, tmem + half_col(s), o + mn_step(s), id_v, i > 0 || s > 0);
                 mma_commit(&bars->eo[rc.s]);
             }
-            if (i + 1 < steps && !(ok = scores())) break;
+            if (more) {
+                if (!EARLY && !(ok = q_there())) break;
+                scores();
+                if (EARLY && !(ok = o_there())) break;
+            }
             if (!(ok = bar_wait(&bars->ds, i & 1, a.hdr, 224, abort))) break;
             tc_fence_after();
             if (elect()) {
@@ -179,7 +188,10 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dkv_kernel(const GradArgs a, 
                 for (int s = 0; s < 8; ++s) mma_f16_tmem_a(tmem + 384, tmem + 128 + half_col(s), q + mn_step(s), id_k, i > 0 || s > 0);
                 mma_commit(&bars->eq[rc.s]);
             }
-            if (i + 1 < steps && !(ok = dprobs())) break;
+            if (more) {
+                if (!EARLY && !(ok = o_there())) break;
+                dprobs();
+            }
             rc.step(1, a.stages);
         }
         if (ok && elect()) mma_commit(&bars->done);
@@ -379,22 +391,21 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dq_kernel(const GradArgs a, c
             rk.step(1, a.k_slots);
             return true;
         };
+        auto v_there = [&]() { return bar_wait(&bars->fv[rv.s], rv.turn, a.hdr, 250, abort); };
         auto dprobs = [&]() {
-            if (!bar_wait(&bars->fv[rv.s], rv.turn, a.hdr, 250, abort)) return false;
             if (elect()) {
                 mma_tiles(tmem + 256, od, k_desc(vb + (uint32_t)rv.s * v_tile), id_s, ko);
                 mma_commit(&bars->dp);
                 mma_commit(&bars->ev[rv.s]);
             }
             rv.step(1, a.v_slots);
-            return true;
         };
-        ok = ok && scores(0) && dprobs();
+        if ((ok = ok && scores(0) && v_there())) dprobs();
         for (int j = 0; ok && j < tiles; ++j) {
-            if (j + 1 < tiles && !(ok = scores(j + 1))) break;
+            if (j + 1 < tiles && !(ok = scores(j + 1) && v_there())) break;
             if (!(ok = bar_wait(&bars->ds, j & 1, a.hdr, 242, abort))) break;
             tc_fence_after();
-            if (j + 1 < tiles && !(ok = dprobs())) break;
+            if (j + 1 < tiles) dprobs();
             if (elect()) {
                 const uint64_t k = mn_desc(rb + (uint32_t)rc.s * q_tile);
                 const uint32_t ds = tmem + 128 * (j & 1);
@@ -582,10 +593,11 @@ gma_status_t tc_backward(const gma_attn_grad_t &g, void *ws, cudaStream_t st)
     gma_status_t r = launch_plan(first, &second, st);
     if (r != GMA_OK) return r;
     if ((r = launch_delta(g, delta, st)) != GMA_OK) return r;
-    if (cudaFuncSetAttribute(attn_dkv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_MAX) != cudaSuccess ||
+    auto dkv = x.stages > 2 ? attn_dkv_kernel<true> : attn_dkv_kernel<false>;
+    if (cudaFuncSetAttribute(dkv, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_MAX) != cudaSuccess ||
         cudaFuncSetAttribute(attn_dq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_MAX) != cudaSuccess)
         return GMA_ERR_CUDA;
-    GMA_LAUNCH(KID_ATTN_DKV, st, launch_pdl(attn_dkv_kernel, (unsigned)p.k.max_items * a.G, THREADS, k_fixed + x.stages * k_stage, st, x, qm, km, vm, om));
+    GMA_LAUNCH(KID_ATTN_DKV, st, launch_pdl(dkv, (unsigned)p.k.max_items * a.G, THREADS, k_fixed + x.stages * k_stage, st, x, qm, km, vm, om));
     GMA_LAUNCH(KID_ATTN_DQ, st, launch_pdl(attn_dq_kernel, (unsigned)p.q.max_items * a.H, THREADS, q_fixed + q_ring, st, x, qm, km, vm, om));
     return GMA_OK;
 }
