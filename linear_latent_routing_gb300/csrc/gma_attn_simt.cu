@@ -1,10 +1,11 @@
 // gma_attn_simt.cu -- softmax attention on the CUDA cores: fp32, and bf16 rows or pages that the tensor-core kernels
 // cannot read (strides off 16 bytes, pages of odd sizes).
 //
-// Forward: a block takes 64 rows ((token, head of a group) pairs where the keys come from a cache) and walks over its keys 64
-// at a time, with the running maximum and sum of each row in registers.  Scores are 4 x 4 a thread out of shared memory, four
-// elements of the head at a time: 8 loads of 16 bytes for 64 multiply-adds, so that the fp32 pipe and not shared memory bounds it.
-// Warps whose rows do not exist only copy.
+// Forward: a block takes R rows ((token, head of a group) pairs where the keys come from a cache) and walks over its keys 64
+// at a time, with the running maximum and sum of each row in registers.  Scores are R / 16 x 4 a thread out of shared memory, four
+// elements of the head at a time (R = 64: 8 loads of 16 bytes for 64 multiply-adds).  The next tile's rows are on their way by cp.async
+// while one is worked on.  Calls of less than two blocks of 64 rows an SM take R = 32, single tokens R = 16: latency, not the fp32 pipe,
+// bounds them.  Warps whose rows do not exist only copy.
 #include <algorithm>
 
 #include "attn_common.cuh"
@@ -13,7 +14,7 @@ namespace gma {
 namespace att {
 namespace {
 
-constexpr int R = 64;                 // rows of a tile
+constexpr int BR = 32;                // rows of a tile of the backward pass
 constexpr int KT = 64;                // keys of a tile
 constexpr int TH = 256;
 
@@ -34,44 +35,58 @@ template <typename T> struct Args {
 
 constexpr __host__ __device__ int pitch_of(int width) { return (width + 3) / 4 * 4 + 4; }
 
-// Rows of `width` elements into shared memory as fp32, zeros behind the width and for rows that `get` has not.
-template <typename F> __device__ __forceinline__ void stage(float *dst, int rows, int width, int pitch, F get)
+__device__ __forceinline__ void copy16(float *dst, const void *src, bool is)
 {
-    const int w4 = (width + 3) & ~3;
-    for (int i = threadIdx.x; i < rows * w4; i += TH) {
-        const int r = i / w4, c = i - r * w4;
-        dst[r * pitch + c] = c < width ? get(r, c) : 0.f;
+    const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(is ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// One row of `width` elements into shared memory as fp32 by the four threads of it; zeros behind the width and where it `is` not.
+// VEC: fp32 rows on 16-byte boundaries, copied asynchronously.
+template <bool VEC, typename T> __device__ __forceinline__ void stage_row(float *dst, const T *src, bool is, int width, int quarter)
+{
+    if (VEC) {
+        for (int c = 4 * quarter; c < width; c += 16) copy16(dst + c, src + (is ? c : 0), is);
+    } else {
+        const int w4 = (width + 3) & ~3;
+        for (int c = quarter; c < w4; c += 4) dst[c] = is && c < width ? to_f32<T>(src[c]) : 0.f;
     }
 }
 
-// Scores of rows 4 ty + i against columns tx + 16 j of two staged tiles.
-__device__ __forceinline__ void products(const float *a, const float *b, int pitch, int width, int tx, int ty, float (&s)[4][4])
+// Scores of rows RI ty + i against columns tx + 16 j of two staged tiles.
+template <int RI>
+__device__ __forceinline__ void products(const float *a, const float *b, int pitch, int width, int tx, int ty, float (&s)[RI][4])
 {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < RI; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+#pragma unroll 2
     for (int c = 0; c < width; c += 4) {
-        float4 x[4], y[4];
+        float4 x[RI], y[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4 *>(a + (4 * ty + i) * pitch + c);
+        for (int i = 0; i < RI; ++i) x[i] = *reinterpret_cast<const float4 *>(a + (RI * ty + i) * pitch + c);
 #pragma unroll
         for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const float4 *>(b + (tx + 16 * j) * pitch + c);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < RI; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 s[i][j] = fmaf(x[i].x, y[j].x, fmaf(x[i].y, y[j].y, fmaf(x[i].z, y[j].z, fmaf(x[i].w, y[j].w, s[i][j]))));
     }
 }
 
-// acc[i][4 c + e] += sum_k p[row 4 ty + i][k] x[k][64 c + 4 tx + e], over 64 k.
-__device__ __forceinline__ void accumulate(const float *p, const float *x, int pitch, int width, int tx, int ty, float (&acc)[4][8])
+// acc[i][4 c + e] += sum_k p[row RI ty + i][k] x[k][64 c + 4 tx + e], over 64 k.
+template <int RI>
+__device__ __forceinline__ void accumulate(const float *p, const float *x, int pitch, int width, int tx, int ty, float (&acc)[RI][8])
 {
+#pragma unroll 2
     for (int k = 0; k < KT; k += 4) {
-        float4 w[4];
+        float4 w[RI];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4 *>(p + (4 * ty + i) * (KT + 4) + k);
+        for (int i = 0; i < RI; ++i) w[i] = *reinterpret_cast<const float4 *>(p + (RI * ty + i) * (KT + 4) + k);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
             if (64 * c + 4 * tx >= width) break;
@@ -80,7 +95,7 @@ __device__ __forceinline__ void accumulate(const float *p, const float *x, int p
             for (int e = 0; e < 4; ++e) {
                 const float4 v = *reinterpret_cast<const float4 *>(y + e * pitch);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < RI; ++i) {
                     const float f = e == 0 ? w[i].x : e == 1 ? w[i].y : e == 2 ? w[i].z : w[i].w;
                     acc[i][4 * c] = fmaf(f, v.x, acc[i][4 * c]);
                     acc[i][4 * c + 1] = fmaf(f, v.y, acc[i][4 * c + 1]);
@@ -92,11 +107,11 @@ __device__ __forceinline__ void accumulate(const float *p, const float *x, int p
     }
 }
 
-template <typename T, bool PAGED>
-__global__ void __launch_bounds__(TH, 2) attn_simt_kernel(const Args<T> a)
+template <typename T, bool PAGED, bool VEC, int R>
+__global__ void __launch_bounds__(TH, 1) attn_simt_kernel(const Args<T> a)
 {
+    constexpr int RI = R / 16;
     extern __shared__ __align__(16) float smem[];
-    __shared__ long long page_at[KT];            // page * 2^20 + slot of every key of the tile, or -1
     if (PAGED) blk::let_next();
     blk::wait_previous();
     const int rank = blockIdx.x / a.heads, head = blockIdx.x % a.heads;
@@ -108,81 +123,95 @@ __global__ void __launch_bounds__(TH, 2) attn_simt_kernel(const Args<T> a)
     const int pack = a.pack, kvh = pack == 1 ? head / g.group : head;
     const int tokens = min(a.head->tokens, s.n - it.tok0), rows = tokens * pack;
     const int qp = pitch_of(g.d), vp = pitch_of(g.dv);
-    float *qs = smem, *ks = qs + R * qp, *vs = ks + KT * qp, *ps = vs + KT * vp;
-    const int t = threadIdx.x, tx = t & 15, ty = t >> 4;
+    float *qs = smem, *ps = qs + R * qp, *ring = ps + R * (KT + 4);      // two stages of a tile of keys and one of values
+    const int stage = KT * (qp + vp);
+    const int t = threadIdx.x, tx = t & 15, ty = t >> 4, mine = t >> 2, quarter = t & 3;
     // row r of the tile: token it.tok0 + r / pack, query head
     auto head_of = [&](int r) { return pack == 1 ? head : head * pack + r % pack; };
-    stage(qs, R, g.d, qp, [&](int r, int c) {
-        return r < rows ? to_f32<T>(a.q.at(s.b, s.row0 + it.tok0 + r / pack, head_of(r))[c]) : 0.f;
-    });
-    int seen[4];
+    const int end = min(it.t1 * KT, s.seen(g, it.tok0 + tokens - 1));
+    // the page of this thread's row of a tile, fetched a tile ahead of the copy that needs it
+    int slot = 0;
+    auto page = [&](int k0) { return PAGED && k0 + mine < end ? page_of(g, it.seq, k0 + mine, &slot) : -1; };
+    auto load = [&](int k0, int at, int p) {
+        const bool is = k0 + mine < end && (!PAGED || p >= 0);
+        const T *k, *v;
+        if (PAGED) {
+            k = a.k.at(is ? p : 0, is ? slot : 0, kvh);
+            v = a.v.at(is ? p : 0, is ? slot : 0, kvh);
+        } else {
+            const long long row = s.row0 + (is ? k0 + mine : 0);
+            k = a.k.at(s.b, row, kvh);
+            v = a.v.at(s.b, row, kvh);
+        }
+        stage_row<VEC>(ring + at * stage + mine * qp, k, is, g.d, quarter);
+        stage_row<VEC>(ring + at * stage + KT * qp + mine * vp, v, is, g.dv, quarter);
+    };
+    int k0 = it.t0 * KT, p = page(k0);
+    if (mine < R) {
+        const bool is = mine < rows;
+        const int r = is ? mine : 0;
+        stage_row<VEC>(qs + mine * qp, a.q.at(s.b, s.row0 + it.tok0 + r / pack, head_of(r)), is, g.d, quarter);
+    }
+    if (k0 < end) load(k0, 0, p);
+    copies_commit();
+    p = page(k0 + KT);
+    int seen[RI];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) seen[i] = 4 * ty + i < rows ? s.seen(g, it.tok0 + (4 * ty + i) / pack) : 0;
-    const bool busy = (t >> 5) * 8 < rows;       // this warp's rows exist
-    float m[4], l[4], acc[4][8];
+    for (int i = 0; i < RI; ++i) seen[i] = RI * ty + i < rows ? s.seen(g, it.tok0 + (RI * ty + i) / pack) : 0;
+    const bool busy = (t >> 5) * 2 * RI < rows;       // this warp's rows exist
+    float m[RI], l[RI], acc[RI][8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < RI; ++i) {
         m[i] = -INFINITY;
         l[i] = 0.f;
 #pragma unroll
         for (int c = 0; c < 8; ++c) acc[i][c] = 0.f;
     }
-    const int end = min(it.t1 * KT, s.seen(g, it.tok0 + tokens - 1));
-    for (int k0 = it.t0 * KT; k0 < end; k0 += KT) {
+    for (int at = 0; k0 < end; k0 += KT, at ^= 1) {
+        if (k0 + KT < end) load(k0 + KT, at ^ 1, p);
+        copies_commit();
+        p = page(k0 + 2 * KT);
+        copies_wait<1>();
         __syncthreads();
-        const int have = min(KT, end - k0);
-        if (PAGED) {
-            if (t < KT) {
-                int slot = 0;
-                const int p = t < have ? page_of(g, it.seq, k0 + t, &slot) : -1;
-                page_at[t] = p < 0 ? -1 : (long long)p << 20 | slot;
+        if (busy) {
+            const float *ks = ring + at * stage, *vs = ks + KT * qp;
+            float x[RI][4];
+            products<RI>(qs, ks, qp, g.d, tx, ty, x);
+#pragma unroll
+            for (int i = 0; i < RI; ++i) {
+                float top = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    x[i][j] = k0 + tx + 16 * j < seen[i] ? x[i][j] * g.sl2 : -INFINITY;
+                    top = fmaxf(top, x[i][j]);
+                }
+#pragma unroll
+                for (int o = 8; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+                const float now = fmaxf(m[i], top), base = now == -INFINITY ? 0.f : now, f = ex2(m[i] - base);
+                float sum = 0.f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float e = ex2(x[i][j] - base);
+                    sum += e;
+                    ps[(RI * ty + i) * (KT + 4) + tx + 16 * j] = e;
+                }
+                l[i] = l[i] * f + sum;               // this thread's keys; the row's threads are added at the end
+                m[i] = now;
+#pragma unroll
+                for (int c = 0; c < 8; ++c) acc[i][c] *= f;
             }
-            __syncthreads();
+            __syncwarp();                            // a warp reads the rows that it wrote
+            accumulate<RI>(ps, vs, vp, g.dv, tx, ty, acc);
         }
-        auto element = [&](const Heads<const T> &x, int r, int c) -> float {
-            if (r >= have) return 0.f;
-            if (!PAGED) return to_f32<T>(x.at(s.b, s.row0 + k0 + r, kvh)[c]);
-            const long long p = page_at[r];
-            return p < 0 ? 0.f : to_f32<T>(x.at(p >> 20, p & 0xfffff, kvh)[c]);
-        };
-        stage(ks, KT, g.d, qp, [&](int r, int c) { return element(a.k, r, c); });
-        stage(vs, KT, g.dv, vp, [&](int r, int c) { return element(a.v, r, c); });
         __syncthreads();
-        if (!busy) continue;
-        float x[4][4];
-        products(qs, ks, qp, g.d, tx, ty, x);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float top = -INFINITY;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                x[i][j] = k0 + tx + 16 * j < seen[i] ? x[i][j] * g.sl2 : -INFINITY;
-                top = fmaxf(top, x[i][j]);
-            }
-#pragma unroll
-            for (int o = 8; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-            const float now = fmaxf(m[i], top), base = now == -INFINITY ? 0.f : now, f = ex2(m[i] - base);
-            float sum = 0.f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float p = ex2(x[i][j] - base);
-                sum += p;
-                ps[(4 * ty + i) * (KT + 4) + tx + 16 * j] = p;
-            }
-#pragma unroll
-            for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-            l[i] = l[i] * f + sum;
-            m[i] = now;
-#pragma unroll
-            for (int c = 0; c < 8; ++c) acc[i][c] *= f;
-        }
-        __syncwarp();                            // a warp reads the rows that it wrote
-        accumulate(ps, vs, vp, g.dv, tx, ty, acc);
     }
+    copies_wait<0>();
     const bool whole = it.parts == 1;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = 4 * ty + i;
+    for (int i = 0; i < RI; ++i) {
+#pragma unroll
+        for (int o = 8; o; o >>= 1) l[i] += __shfl_xor_sync(~0u, l[i], o);
+        const int r = RI * ty + i;
         if (r >= rows) continue;
         const int h = head_of(r), tok = it.tok0 + r / pack;
         const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
@@ -206,9 +235,10 @@ __global__ void __launch_bounds__(TH, 2) attn_simt_kernel(const Args<T> a)
     }
 }
 
-// dq of 64 query rows of one head: ds = p (do . v - delta), dq = scale ds k over the keys that the rows see.
-template <typename T> __global__ void __launch_bounds__(TH, 1) attn_simt_dq_kernel(const Args<T> a)
+// dq of 32 query rows of one head: ds = p (do . v - delta), dq = scale ds k over the keys that the rows see.
+template <typename T, bool VEC> __global__ void __launch_bounds__(TH, 1) attn_simt_dq_kernel(const Args<T> a)
 {
+    constexpr int RI = BR / 16;
     extern __shared__ __align__(16) float smem[];
     blk::wait_previous();
     const int rank = blockIdx.x / a.heads, h = blockIdx.x % a.heads;
@@ -216,17 +246,31 @@ template <typename T> __global__ void __launch_bounds__(TH, 1) attn_simt_dq_kern
     const Geo &g = a.g;
     const Item it = a.items[rank];
     const Seq s = sequence(g, it.seq);
-    const int kvh = h / g.group, rows = min(R, s.n - it.tok0);
-    const int qp = pitch_of(g.d), vp = pitch_of(g.dv);
-    float *qs = smem, *os = qs + R * qp, *ks = os + R * vp, *vs = ks + KT * qp, *ps = vs + KT * vp;
-    const int t = threadIdx.x, tx = t & 15, ty = t >> 4;
-    stage(qs, R, g.d, qp, [&](int r, int c) { return r < rows ? to_f32<T>(a.q.at(s.b, s.row0 + it.tok0 + r, h)[c]) : 0.f; });
-    stage(os, R, g.dv, vp, [&](int r, int c) { return r < rows ? to_f32<T>(a.d_o.at(s.b, s.row0 + it.tok0 + r, h)[c]) : 0.f; });
-    float lse2[4], delta[4], acc[4][8];
-    int seen[4];
+    const int kvh = h / g.group, rows = min(BR, s.n - it.tok0);
+    const int qp = pitch_of(g.d), vp = pitch_of(g.dv), stage = KT * (qp + vp);
+    float *qs = smem, *os = qs + BR * qp, *ps = os + BR * vp, *ring = ps + BR * (KT + 4);
+    const int t = threadIdx.x, tx = t & 15, ty = t >> 4, mine = t >> 2, quarter = t & 3;
+    const int end = min(it.t1 * KT, s.L);
+    auto load = [&](int k0, int at) {
+        const bool is = k0 + mine < end;
+        const long long row = s.row0 + (is ? k0 + mine : 0);
+        stage_row<VEC>(ring + at * stage + mine * qp, a.k.at(s.b, row, kvh), is, g.d, quarter);
+        stage_row<VEC>(ring + at * stage + KT * qp + mine * vp, a.v.at(s.b, row, kvh), is, g.dv, quarter);
+    };
+    if (mine < BR) {
+        const bool is = mine < rows;
+        const long long row = s.row0 + it.tok0 + (is ? mine : 0);
+        stage_row<VEC>(qs + mine * qp, a.q.at(s.b, row, h), is, g.d, quarter);
+        stage_row<VEC>(os + mine * vp, a.d_o.at(s.b, row, h), is, g.dv, quarter);
+    }
+    int k0 = it.t0 * KT;
+    load(k0, 0);
+    copies_commit();
+    float lse2[RI], delta[RI], acc[RI][8];
+    int seen[RI];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = 4 * ty + i;
+    for (int i = 0; i < RI; ++i) {
+        const int r = RI * ty + i;
         const bool is = r < rows;
         const long long at = is ? stat_at(g, s, h, it.tok0 + r) : 0;
         seen[i] = is ? s.seen(g, it.tok0 + r) : 0;
@@ -235,30 +279,31 @@ template <typename T> __global__ void __launch_bounds__(TH, 1) attn_simt_dq_kern
 #pragma unroll
         for (int c = 0; c < 8; ++c) acc[i][c] = 0.f;
     }
-    const int end = min(it.t1 * KT, s.L);
-    for (int k0 = it.t0 * KT; k0 < end; k0 += KT) {
+    for (int at = 0; k0 < end; k0 += KT, at ^= 1) {
+        if (k0 + KT < end) load(k0 + KT, at ^ 1);
+        copies_commit();
+        copies_wait<1>();
         __syncthreads();
-        const int have = min(KT, s.L - k0);
-        stage(ks, KT, g.d, qp, [&](int r, int c) { return r < have ? to_f32<T>(a.k.at(s.b, s.row0 + k0 + r, kvh)[c]) : 0.f; });
-        stage(vs, KT, g.dv, vp, [&](int r, int c) { return r < have ? to_f32<T>(a.v.at(s.b, s.row0 + k0 + r, kvh)[c]) : 0.f; });
-        __syncthreads();
-        float x[4][4], y[4][4];
-        products(qs, ks, qp, g.d, tx, ty, x);
-        products(os, vs, vp, g.dv, tx, ty, y);
+        const float *ks = ring + at * stage, *vs = ks + KT * qp;
+        float x[RI][4], y[RI][4];
+        products<RI>(qs, ks, qp, g.d, tx, ty, x);
+        products<RI>(os, vs, vp, g.dv, tx, ty, y);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < RI; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float p = k0 + tx + 16 * j < seen[i] ? ex2(x[i][j] * g.sl2 - lse2[i]) : 0.f;
-                ps[(4 * ty + i) * (KT + 4) + tx + 16 * j] = p == 0.f ? 0.f : p * (y[i][j] - delta[i]);
+                ps[(RI * ty + i) * (KT + 4) + tx + 16 * j] = p == 0.f ? 0.f : p * (y[i][j] - delta[i]);
             }
         __syncwarp();
-        accumulate(ps, ks, qp, g.d, tx, ty, acc);
+        accumulate<RI>(ps, ks, qp, g.d, tx, ty, acc);
+        __syncthreads();
     }
+    copies_wait<0>();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (4 * ty + i >= rows) continue;
-        T *dq = a.dq.at(s.b, s.row0 + it.tok0 + 4 * ty + i, h);
+    for (int i = 0; i < RI; ++i) {
+        if (RI * ty + i >= rows) continue;
+        T *dq = a.dq.at(s.b, s.row0 + it.tok0 + RI * ty + i, h);
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
             const int col = 64 * (c >> 2) + 4 * tx + (c & 3);
@@ -267,60 +312,86 @@ template <typename T> __global__ void __launch_bounds__(TH, 1) attn_simt_dq_kern
     }
 }
 
-// dk and dv of 64 keys of one head, over the query heads of its group and the rows that see them: rows of the
+// dk and dv of 32 keys of one head, over the query heads of its group and the rows that see them: rows of the
 // tiles are keys here, columns queries.
-template <typename T> __global__ void __launch_bounds__(TH, 1) attn_simt_dkv_kernel(const Args<T> a)
+template <typename T, bool VEC> __global__ void __launch_bounds__(TH, 1) attn_simt_dkv_kernel(const Args<T> a)
 {
+    constexpr int RI = BR / 16;
     extern __shared__ __align__(16) float smem[];
-    __shared__ float lse2[KT], delta[KT];
+    __shared__ float lse2[2][KT], delta[2][KT];
+    blk::let_next();
     blk::wait_previous();
     const int rank = blockIdx.x / a.heads, kvh = blockIdx.x % a.heads;
     if (rank >= a.head->items) return;
     const Geo &g = a.g;
     const Item it = a.items[rank];
     const Seq s = sequence(g, it.seq);
-    const int rows = min(R, s.n - it.tok0);
-    const int qp = pitch_of(g.d), vp = pitch_of(g.dv);
-    float *ks = smem, *vs = ks + R * qp, *qs = vs + R * vp, *os = qs + KT * qp, *ps = os + KT * vp, *ds = ps + R * (KT + 4);
-    const int t = threadIdx.x, tx = t & 15, ty = t >> 4;
-    stage(ks, R, g.d, qp, [&](int r, int c) { return r < rows ? to_f32<T>(a.k.at(s.b, s.row0 + it.tok0 + r, kvh)[c]) : 0.f; });
-    stage(vs, R, g.dv, vp, [&](int r, int c) { return r < rows ? to_f32<T>(a.v.at(s.b, s.row0 + it.tok0 + r, kvh)[c]) : 0.f; });
-    float dk[4][8], dv[4][8];
+    const int rows = min(BR, s.n - it.tok0);
+    const int qp = pitch_of(g.d), vp = pitch_of(g.dv), stage = KT * (qp + vp);
+    float *ks = smem, *vs = ks + BR * qp, *ps = vs + BR * vp, *ds = ps + BR * (KT + 4), *ring = ds + BR * (KT + 4);
+    const int t = threadIdx.x, tx = t & 15, ty = t >> 4, mine = t >> 2, quarter = t & 3;
+    const int first = it.t0 * KT, last = min(it.t1 * KT, s.n);
+    auto load = [&](int h, int q0, int at) {
+        const bool is = q0 + mine < last;
+        const long long row = s.row0 + (is ? q0 + mine : 0);
+        stage_row<VEC>(ring + at * stage + mine * qp, a.q.at(s.b, row, h), is, g.d, quarter);
+        stage_row<VEC>(ring + at * stage + KT * qp + mine * vp, a.d_o.at(s.b, row, h), is, g.dv, quarter);
+        if (quarter == 0) {
+            const long long where = is ? stat_at(g, s, h, q0 + mine) : 0;
+            lse2[at][mine] = is ? a.stat_lse[where] * LOG2E : 0.f;
+            delta[at][mine] = is ? a.delta[where] : 0.f;
+        }
+    };
+    if (mine < BR) {
+        const bool is = mine < rows;
+        const long long row = s.row0 + it.tok0 + (is ? mine : 0);
+        stage_row<VEC>(ks + mine * qp, a.k.at(s.b, row, kvh), is, g.d, quarter);
+        stage_row<VEC>(vs + mine * vp, a.v.at(s.b, row, kvh), is, g.dv, quarter);
+    }
+    float dk[RI][8], dv[RI][8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < RI; ++i)
 #pragma unroll
         for (int c = 0; c < 8; ++c) dk[i][c] = dv[i][c] = 0.f;
-    for (int h = kvh * g.group; h < (kvh + 1) * g.group; ++h)
-        for (int q0 = it.t0 * KT; q0 < min(it.t1 * KT, s.n); q0 += KT) {
-            __syncthreads();
-            const int have = min(KT, s.n - q0);
-            stage(qs, KT, g.d, qp, [&](int r, int c) { return r < have ? to_f32<T>(a.q.at(s.b, s.row0 + q0 + r, h)[c]) : 0.f; });
-            stage(os, KT, g.dv, vp, [&](int r, int c) { return r < have ? to_f32<T>(a.d_o.at(s.b, s.row0 + q0 + r, h)[c]) : 0.f; });
-            if (t < have) {
-                const long long at = stat_at(g, s, h, q0 + t);
-                lse2[t] = a.stat_lse[at] * LOG2E;
-                delta[t] = a.delta[at];
-            }
-            __syncthreads();
-            float x[4][4], y[4][4];
-            products(ks, qs, qp, g.d, tx, ty, x);
-            products(vs, os, vp, g.dv, tx, ty, y);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int c = tx + 16 * j, key = it.tok0 + 4 * ty + i;
-                    const float p = c < have && key < s.seen(g, q0 + c) ? ex2(x[i][j] * g.sl2 - lse2[c]) : 0.f;
-                    ps[(4 * ty + i) * (KT + 4) + c] = p;
-                    ds[(4 * ty + i) * (KT + 4) + c] = p == 0.f ? 0.f : p * (y[i][j] - delta[c]);
-                }
-            __syncwarp();
-            accumulate(ps, os, vp, g.dv, tx, ty, dv);
-            accumulate(ds, qs, qp, g.d, tx, ty, dk);
+    int h = kvh * g.group, q0 = first;
+    const int heads_end = h + g.group;
+    load(h, q0, 0);
+    copies_commit();
+    for (int at = 0; h < heads_end; at ^= 1) {
+        int next_h = h, next = q0 + KT;
+        if (next >= last) {
+            next = first;
+            ++next_h;
         }
+        if (next_h < heads_end) load(next_h, next, at ^ 1);
+        copies_commit();
+        copies_wait<1>();
+        __syncthreads();
+        const float *qs = ring + at * stage, *os = qs + KT * qp;
+        const int have = min(KT, last - q0);
+        float x[RI][4], y[RI][4];
+        products<RI>(ks, qs, qp, g.d, tx, ty, x);
+        products<RI>(vs, os, vp, g.dv, tx, ty, y);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = 4 * ty + i;
+        for (int i = 0; i < RI; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int c = tx + 16 * j, key = it.tok0 + RI * ty + i;
+                const float p = c < have && key < s.seen(g, q0 + c) ? ex2(x[i][j] * g.sl2 - lse2[at][c]) : 0.f;
+                ps[(RI * ty + i) * (KT + 4) + c] = p;
+                ds[(RI * ty + i) * (KT + 4) + c] = p == 0.f ? 0.f : p * (y[i][j] - delta[at][c]);
+            }
+        __syncwarp();
+        accumulate<RI>(ps, os, vp, g.dv, tx, ty, dv);
+        accumulate<RI>(ds, qs, qp, g.d, tx, ty, dk);
+        __syncthreads();
+        h = next_h;
+        q0 = next;
+    }
+    copies_wait<0>();
+#pragma unroll
+    for (int i = 0; i < RI; ++i) {
+        const int r = RI * ty + i;
         if (r >= rows) continue;
         T *k = a.dk.at(s.b, s.row0 + it.tok0 + r, kvh), *v = a.dv.at(s.b, s.row0 + it.tok0 + r, kvh);
 #pragma unroll
@@ -333,7 +404,7 @@ template <typename T> __global__ void __launch_bounds__(TH, 1) attn_simt_dkv_ker
 }
 
 // ------------------------------------------------------------------ host side
-constexpr size_t MAX_SMEM = (size_t)(4 * 64 * 132 + 2 * 64 * 68) * sizeof(float);
+constexpr size_t MAX_SMEM = (size_t)(2 * 64 * 2 * 132 + 64 * 132 + 64 * 68) * sizeof(float);     // R = 64, 128 wide
 
 template <typename... P> bool allow(void (*kern)(P...))
 {
@@ -341,11 +412,25 @@ template <typename... P> bool allow(void (*kern)(P...))
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)MAX_SMEM) == cudaSuccess;
 }
 
-Plan plan_of(const gma_attn_t &a, const gma_attn_paged_t *paged, Carve *c)
+// Rows of a forward tile: by the rows that there may be.
+int rows_of(const gma_attn_t &a, int pack)
 {
-    const int group = a.H / a.G, pack = paged && group <= R ? group : 1;
-    return make_plan(a, pack, R, R, 6, SMS, paged != nullptr, c);
+    const long long n = (long long)(a.offsets ? 1 : a.B) * a.N, each = (a.offsets ? n : (long long)a.N) * pack;
+    if (each <= 16) return 16;
+    return n * a.H / 64 < 2 * SMS ? 32 : 64;
 }
+
+Plan plan_of(const gma_attn_t &a, const gma_attn_paged_t *paged, int *rows, Carve *c)
+{
+    const int group = a.H / a.G;
+    int pack = paged ? group : 1;
+    *rows = rows_of(a, pack);
+    if (pack > *rows) pack = 1;
+    return make_plan(a, pack, *rows, *rows, 6, SMS, paged != nullptr, c);
+}
+
+// fp32 rows that cp.async can copy.
+bool vec_heads(const gma_heads_t &r) { return (((uintptr_t)r.ptr | (uintptr_t)(r.batch * 4) | (uintptr_t)(r.token * 4) | (uintptr_t)(r.head * 4)) & 15u) == 0; }
 
 template <typename T>
 Args<T> args_of(const gma_attn_t &a, const gma_attn_paged_t *paged, const Plan &p, void *ws)
@@ -366,24 +451,22 @@ Args<T> args_of(const gma_attn_t &a, const gma_attn_paged_t *paged, const Plan &
     return x;
 }
 
-template <typename T> gma_status_t forward(const gma_attn_t &a, const gma_attn_paged_t *paged, void *ws, cudaStream_t st)
+template <typename T, bool PAGED, bool VEC>
+gma_status_t forward(const gma_attn_t &a, const gma_attn_paged_t *paged, void *ws, cudaStream_t st)
 {
     Carve c;
-    const Plan p = plan_of(a, paged, &c);
+    int rows;
+    const Plan p = plan_of(a, paged, &rows, &c);
     const Args<T> x = args_of<T>(a, paged, p, ws);
     gma_status_t r = launch_plan(plan_args(x.g, p, ws), nullptr, st);
     if (r != GMA_OK) return r;
-    const size_t smem = (size_t)(2 * 64 * pitch_of(a.d) + 64 * pitch_of(a.dv) + 64 * 68) * sizeof(float);
+    const int qp = pitch_of(a.d), vp = pitch_of(a.dv);
+    const size_t smem = (size_t)(rows * (qp + KT + 4) + 2 * KT * (qp + vp)) * sizeof(float);
     const unsigned grid = (unsigned)p.max_items * p.heads;
-    if (paged) {
-        if (!allow(attn_simt_kernel<T, true>)) return GMA_ERR_CUDA;
-        GMA_LAUNCH(KID_ATTN_SIMT, st, launch_pdl(attn_simt_kernel<T, true>, grid, TH, smem, st, x));
-        return launch_join(a, x.g, p, ws, st);
-    } else {
-        if (!allow(attn_simt_kernel<T, false>)) return GMA_ERR_CUDA;
-        GMA_LAUNCH(KID_ATTN_SIMT, st, launch_pdl(attn_simt_kernel<T, false>, grid, TH, smem, st, x));
-    }
-    return GMA_OK;
+    auto kern = rows == 64 ? attn_simt_kernel<T, PAGED, VEC, 64> : rows == 32 ? attn_simt_kernel<T, PAGED, VEC, 32> : attn_simt_kernel<T, PAGED, VEC, 16>;
+    if (!allow(kern)) return GMA_ERR_CUDA;
+    GMA_LAUNCH(KID_ATTN_SIMT, st, launch_pdl(kern, grid, TH, smem, st, x));
+    return PAGED ? launch_join(a, x.g, p, ws, st) : GMA_OK;
 }
 
 struct GradPlan {
@@ -394,16 +477,16 @@ struct GradPlan {
 GradPlan grad_plan(const gma_attn_t &a, Carve *c)
 {
     GradPlan p;
-    p.q = make_plan(a, 1, R, R, 6, SMS, false, c);
+    p.q = make_plan(a, 1, BR, BR, 6, SMS, false, c);
     gma_attn_t by = a;
     by.H = a.G;                       // a tile of keys serves the whole group
-    p.k = make_plan(by, 1, R, R, 6, SMS, false, c);
+    p.k = make_plan(by, 1, BR, BR, 6, SMS, false, c);
     p.k.by_keys = true;
     p.delta_at = c->take((size_t)(a.offsets ? 1 : a.B) * a.H * a.N * sizeof(float));
     return p;
 }
 
-template <typename T> gma_status_t backward(const gma_attn_grad_t &g, void *ws, cudaStream_t st)
+template <typename T, bool VEC> gma_status_t backward(const gma_attn_grad_t &g, void *ws, cudaStream_t st)
 {
     const gma_attn_t &a = g.fwd;
     Carve c;
@@ -424,10 +507,11 @@ template <typename T> gma_status_t backward(const gma_attn_grad_t &g, void *ws, 
     gma_status_t r = launch_plan(first, &second, st);
     if (r != GMA_OK) return r;
     if ((r = launch_delta(g, delta, st)) != GMA_OK) return r;
-    if (!allow(attn_simt_dq_kernel<T>) || !allow(attn_simt_dkv_kernel<T>)) return GMA_ERR_CUDA;
-    const size_t tiles = (size_t)(2 * 64 * pitch_of(a.d) + 2 * 64 * pitch_of(a.dv)) * sizeof(float), square = 64 * 68 * sizeof(float);
-    GMA_LAUNCH(KID_ATTN_SIMT_DKV, st, launch_pdl(attn_simt_dkv_kernel<T>, (unsigned)p.k.max_items * p.k.heads, TH, tiles + 2 * square, st, y));
-    GMA_LAUNCH(KID_ATTN_SIMT_DQ, st, launch_pdl(attn_simt_dq_kernel<T>, (unsigned)p.q.max_items * p.q.heads, TH, tiles + square, st, x));
+    if (!allow(attn_simt_dq_kernel<T, VEC>) || !allow(attn_simt_dkv_kernel<T, VEC>)) return GMA_ERR_CUDA;
+    const int both = pitch_of(a.d) + pitch_of(a.dv);
+    const size_t tiles = (size_t)(BR + 2 * KT) * both * sizeof(float), square = BR * (KT + 4) * sizeof(float);
+    GMA_LAUNCH(KID_ATTN_SIMT_DKV, st, launch_pdl(attn_simt_dkv_kernel<T, VEC>, (unsigned)p.k.max_items * p.k.heads, TH, tiles + 2 * square, st, y));
+    GMA_LAUNCH(KID_ATTN_SIMT_DQ, st, launch_pdl(attn_simt_dq_kernel<T, VEC>, (unsigned)p.q.max_items * p.q.heads, TH, tiles + square, st, x));
     return GMA_OK;
 }
 
@@ -436,13 +520,17 @@ template <typename T> gma_status_t backward(const gma_attn_grad_t &g, void *ws, 
 size_t simt_workspace(const gma_attn_t &a, const gma_attn_paged_t *paged)
 {
     Carve c;
-    plan_of(a, paged, &c);
+    int rows;
+    plan_of(a, paged, &rows, &c);
     return c.total();
 }
 
-gma_status_t simt_forward(const gma_attn_t &a, const gma_attn_paged_t *paged, void *ws, cudaStream_t st)
+gma_status_t simt_forward(const gma_attn_t &a, const gma_attn_paged_t *p, void *ws, cudaStream_t st)
 {
-    return a.dtype == GMA_BF16 ? forward<__nv_bfloat16>(a, paged, ws, st) : forward<float>(a, paged, ws, st);
+    if (a.dtype == GMA_BF16) return p ? forward<__nv_bfloat16, true, false>(a, p, ws, st) : forward<__nv_bfloat16, false, false>(a, p, ws, st);
+    const bool vec = a.d % 4 == 0 && a.dv % 4 == 0 && vec_heads(a.q) && vec_heads(p ? p->k_pages : a.k) && vec_heads(p ? p->v_pages : a.v);
+    if (p) return vec ? forward<float, true, true>(a, p, ws, st) : forward<float, true, false>(a, p, ws, st);
+    return vec ? forward<float, false, true>(a, p, ws, st) : forward<float, false, false>(a, p, ws, st);
 }
 
 size_t simt_backward_workspace(const gma_attn_grad_t &g)
@@ -454,7 +542,10 @@ size_t simt_backward_workspace(const gma_attn_grad_t &g)
 
 gma_status_t simt_backward(const gma_attn_grad_t &g, void *ws, cudaStream_t st)
 {
-    return g.fwd.dtype == GMA_BF16 ? backward<__nv_bfloat16>(g, ws, st) : backward<float>(g, ws, st);
+    const gma_attn_t &a = g.fwd;
+    if (a.dtype == GMA_BF16) return backward<__nv_bfloat16, false>(g, ws, st);
+    const bool vec = a.d % 4 == 0 && a.dv % 4 == 0 && vec_heads(a.q) && vec_heads(a.k) && vec_heads(a.v) && vec_heads(g.d_o);
+    return vec ? backward<float, true>(g, ws, st) : backward<float, false>(g, ws, st);
 }
 
 }  // namespace att
