@@ -15,6 +15,7 @@ constexpr int PT = 256;                // threads of the plan's block
 constexpr int BUCKETS = 1024;          // items are ordered by size up to so many key tiles
 constexpr int TILES = 2048;            // tiles up to which cutting is looked at
 constexpr int SIZES = 24;              // of parts that are tried
+constexpr double REPACK_FROM = 5e5;     // rows x rows x heads
 constexpr float ITEM_COST = 2.f;       // what an item costs beside its keys, in key tiles
 
 // Exclusive sum over the block's threads; *all: the sum of all of them.
@@ -379,6 +380,28 @@ __global__ void __launch_bounds__(256) attn_append_kernel(const Geo g, const Hea
     }
 }
 
+// Rows of up to four tensors into dense ones whose heads start on 16-byte boundaries: a warp a (row, head).
+struct Repack {
+    Heads<const bf16> from[4];
+    bf16 *to[4];
+    int heads[4], width[4], pitch[4], first[5];      // first: (row, head) pairs of the tensors before, divided by the rows
+    int count;
+};
+__global__ void __launch_bounds__(256) attn_repack_kernel(const Repack x, int N, long long rows)
+{
+    const int lane = threadIdx.x & 31;
+    const long long all = rows * x.first[x.count];
+    for (long long i = blockIdx.x * 8ll + (threadIdx.x >> 5); i < all; i += gridDim.x * 8ll) {
+        int k = 0;
+        while (k + 1 < x.count && i >= rows * x.first[k + 1]) ++k;
+        const long long j = i - rows * x.first[k], r = j / x.heads[k], b = r / N;
+        const int h = (int)(j - r * x.heads[k]);
+        const bf16 *s = x.from[k].at(b, r - b * N, h);
+        bf16 *d = x.to[k] + j * x.pitch[k];
+        for (int c = lane; c < x.width[k]; c += 32) d[c] = s[c];
+    }
+}
+
 unsigned row_blocks(long long rows) { return (unsigned)std::min<long long>((rows + 7) / 8, SMS * 16); }
 
 // ------------------------------------------------------------------ checks
@@ -575,6 +598,73 @@ gma_status_t launch_delta(const gma_attn_grad_t &g, float *delta, cudaStream_t s
     return a.dtype == GMA_BF16 ? launch(bf16(), Yes(), std::integral_constant<int, 16>()) : launch(float(), Yes(), std::integral_constant<int, 16>());
 }
 
+// bf16 calls on whole sequences whose rows TMA cannot read: dense copies in the workspace, behind what the kernels take of it.
+namespace {
+
+struct Packed {
+    gma_heads_t q, k, v, d_o;
+    size_t bytes;
+};
+
+Packed pack_places(const gma_attn_t &a, size_t at, void *ws)
+{
+    Packed p = {};
+    const int64_t rows = batches(a) * a.N;
+    size_t off = align_up(at, 256);
+    auto take = [&](int heads, int width) {
+        const int64_t pitch = (width + 7) & ~7;
+        const gma_heads_t h = {(char *)ws + off, a.N * heads * pitch, heads * pitch, pitch};
+        off = align_up(off + (size_t)(rows * heads * pitch) * sizeof(bf16), 256);
+        return h;
+    };
+    p.q = take(a.H, a.d);
+    p.k = take(a.G, a.d);
+    p.v = take(a.G, a.dv);
+    p.d_o = take(a.H, a.dv);
+    p.bytes = off;
+    return p;
+}
+
+gma_status_t launch_repack(const gma_attn_t &a, const gma_heads_t *d_o, const Packed &p, cudaStream_t st)
+{
+    Repack x = {};
+    auto add = [&](const gma_heads_t &from, const gma_heads_t &to, int heads, int width) {
+        const int k = x.count++;
+        x.from[k] = heads_of<const bf16>(from);
+        x.to[k] = (bf16 *)to.ptr;
+        x.heads[k] = heads;
+        x.width[k] = width;
+        x.pitch[k] = (int)to.head;
+        x.first[k + 1] = x.first[k] + heads;
+    };
+    add(a.q, p.q, a.H, a.d);
+    add(a.k, p.k, a.G, a.d);
+    add(a.v, p.v, a.G, a.dv);
+    if (d_o) add(*d_o, p.d_o, a.H, a.dv);
+    const long long rows = batches(a) * a.N;
+    GMA_LAUNCH(KID_ATTN_REPACK, st, attn_repack_kernel<<<row_blocks(rows * x.first[x.count]), 256, 0, st>>>(x, a.N, rows));
+    return GMA_OK;
+}
+
+gma_attn_t with(const gma_attn_t &a, const Packed &p)
+{
+    gma_attn_t b = a;
+    b.q = p.q;
+    b.k = p.k;
+    b.v = p.v;
+    return b;
+}
+
+// Copies cost a launch and the rows' bytes, the CUDA cores' products more than that from some scores on.  Both sides, forward and backward
+// in us: 2 x 128 x 8 heads of 63 (2.6e5) 23 and 46 with copies, 20 and 46 without; 2 x 256 x 8 (1e6) 27 and 50 against 31 and 77;
+// 4 x 2048 x 8 of 117 170 and 403 against 1314 and 6391.
+bool repacks(const gma_attn_t &a)
+{
+    return a.dtype == GMA_BF16 && (double)batches(a) * a.N * a.N * a.H >= REPACK_FROM;
+}
+
+}  // namespace
+
 }  // namespace att
 }  // namespace gma
 
@@ -585,7 +675,9 @@ extern "C" {
 
 size_t gma_attn_workspace_size(const gma_attn_t *a)
 {
-    return check(a, true) != GMA_OK ? 0 : tc_takes(*a, nullptr) ? tc_workspace(*a, nullptr) : simt_workspace(*a, nullptr);
+    if (check(a, true) != GMA_OK) return 0;
+    if (tc_takes(*a, nullptr)) return tc_workspace(*a, nullptr);
+    return repacks(*a) ? pack_places(*a, tc_workspace(*a, nullptr), nullptr).bytes : simt_workspace(*a, nullptr);
 }
 
 gma_status_t gma_attn_forward(const gma_attn_t *a, void *ws, size_t ws_bytes, gma_stream_t stream)
@@ -596,12 +688,18 @@ gma_status_t gma_attn_forward(const gma_attn_t *a, void *ws, size_t ws_bytes, gm
     if ((r = usable_device()) != GMA_OK) return r;
     cudaStream_t st = (cudaStream_t)stream;
     if ((r = zero_tail(*a, a->o, a->H, a->dv, st)) != GMA_OK) return r;
-    return tc_takes(*a, nullptr) ? tc_forward(*a, nullptr, ws, st) : simt_forward(*a, nullptr, ws, st);
+    if (tc_takes(*a, nullptr)) return tc_forward(*a, nullptr, ws, st);
+    if (!repacks(*a)) return simt_forward(*a, nullptr, ws, st);
+    const Packed p = pack_places(*a, tc_workspace(*a, nullptr), ws);
+    if ((r = launch_repack(*a, nullptr, p, st)) != GMA_OK) return r;
+    return tc_forward(with(*a, p), nullptr, ws, st);
 }
 
 size_t gma_attn_backward_workspace_size(const gma_attn_grad_t *g)
 {
-    return check_grad(g) != GMA_OK ? 0 : tc_takes_backward(*g) ? tc_backward_workspace(*g) : simt_backward_workspace(*g);
+    if (check_grad(g) != GMA_OK) return 0;
+    if (tc_takes_backward(*g)) return tc_backward_workspace(*g);
+    return repacks(g->fwd) ? pack_places(g->fwd, tc_backward_workspace(*g), nullptr).bytes : simt_backward_workspace(*g);
 }
 
 gma_status_t gma_attn_backward(const gma_attn_grad_t *g, void *ws, size_t ws_bytes, gma_stream_t stream)
@@ -615,7 +713,14 @@ gma_status_t gma_attn_backward(const gma_attn_grad_t *g, void *ws, size_t ws_byt
     if ((r = zero_tail(a, g->dq, a.H, a.d, st)) != GMA_OK) return r;
     if ((r = zero_tail(a, g->dk, a.G, a.d, st)) != GMA_OK) return r;
     if ((r = zero_tail(a, g->dv, a.G, a.dv, st)) != GMA_OK) return r;
-    return tc_takes_backward(*g) ? tc_backward(*g, ws, st) : simt_backward(*g, ws, st);
+    if (tc_takes_backward(*g)) return tc_backward(*g, ws, st);
+    if (!repacks(a)) return simt_backward(*g, ws, st);
+    const Packed p = pack_places(a, tc_backward_workspace(*g), ws);
+    if ((r = launch_repack(a, &g->d_o, p, st)) != GMA_OK) return r;
+    gma_attn_grad_t packed = *g;
+    packed.fwd = with(a, p);
+    packed.d_o = p.d_o;
+    return tc_backward(packed, ws, st);
 }
 
 gma_status_t gma_attn_append(const gma_attn_paged_t *p, gma_stream_t stream)

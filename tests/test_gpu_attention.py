@@ -57,6 +57,8 @@ PROMPTS = [  # lengths, H, G, d, dv, dtype, causal, layout
     ([333, 12], 3, 1, 100, 20, "bf16", True, "packed"),          # rows off 16-byte boundaries
     ([150, 9], 2, 1, 7, 5, "bf16", True, "padded"),
     ([270], 2, 1, 117, 117, "bf16", False, "plain"),
+    ([600, 9, 301], 4, 2, 117, 50, "bf16", True, "packed"),      # the same, copied first
+    ([411, 500], 3, 1, 30, 63, "bf16", False, "padded"),
     ([1, 0, 65], 4, 2, 64, 64, "f32", True, "packed"),
     ([200, 64, 63], 6, 3, 40, 40, "f32", True, "padded"),
     ([129, 300], 2, 2, 128, 100, "f32", False, "packed"),
