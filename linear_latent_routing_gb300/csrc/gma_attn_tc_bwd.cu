@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dkv_kernel(const GradArgs a, 
     uint8_t *ones = ring + (size_t)a.stages * stage, *extra = ones + EXTRA;      // extra: of each stage, -lse / scale and -delta
     KeyBars *bars = reinterpret_cast<KeyBars *>(extra + (size_t)a.stages * 2 * EXTRA);
     volatile int *abort = &bars->abort;
-    const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    const int t = threadIdx.x, warp = __shfl_sync(~0u, t >> 5, 0), lane = t & 31;      // uniform, as the compiler knows
     if (t == 256) {
         mbar_init(&bars->kv, 1);
         for (int i = 0; i < a.stages; ++i) {
@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dkv_kernel(const GradArgs a, 
     if (warp == 8) tmem_alloc(&bars->tmem, 512);
     const Item it = a.k_items[rank];
     const Seq sq = sequence(g, it.seq);
-    const int tiles = it.t1 - it.t0, steps = tiles * g.group;
+    const int tiles = __shfl_sync(~0u, it.t1 - it.t0, 0), steps = tiles * g.group;
     for (int i = t; i < TILE; i += THREADS) {
         *reinterpret_cast<uint4 *>(ones + i * 32 + (((i >> 2) & 1) << 4)) = make_uint4(0x3f803f80u, 0x3f80u, 0, 0);
         *reinterpret_cast<uint4 *>(ones + i * 32 + ((((i >> 2) & 1) ^ 1) << 4)) = make_uint4(0, 0, 0, 0);
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dkv_kernel(const GradArgs a, 
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = bars->tmem, sb = smem_u32(smem), rb = smem_u32(ring);
+    const uint32_t tmem = __shfl_sync(~0u, bars->tmem, 0), sb = smem_u32(smem), rb = smem_u32(ring);
 
     if (warp == 8) {
         const uint32_t id_s = idesc_f16(TILE, TILE, 1, 1, 0, 0);
@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dq_kernel(const GradArgs a, c
     uint8_t *vring = ring + (size_t)a.k_slots * q_tile;
     QueryBars *bars = reinterpret_cast<QueryBars *>(vring + (size_t)a.v_slots * v_tile);
     volatile int *abort = &bars->abort;
-    const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    const int t = threadIdx.x, warp = __shfl_sync(~0u, t >> 5, 0), lane = t & 31;      // uniform, as the compiler knows
     if (t == 256) {
         mbar_init(&bars->q, 1);
         for (int i = 0; i < SLOTS; ++i) {
@@ -366,11 +366,11 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dq_kernel(const GradArgs a, c
     if (warp == 8) tmem_alloc(&bars->tmem, 512);
     const Item it = a.q_items[rank];
     const Seq sq = sequence(g, it.seq);
-    const int tiles = it.t1 - it.t0;
+    const int tiles = __shfl_sync(~0u, it.t1 - it.t0, 0);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = bars->tmem, sb = smem_u32(smem), rb = smem_u32(ring), vb = smem_u32(vring);
+    const uint32_t tmem = __shfl_sync(~0u, bars->tmem, 0), sb = smem_u32(smem), rb = smem_u32(ring), vb = smem_u32(vring);
 
     if (warp == 8) {
         const uint32_t id_s = idesc_f16(TILE, TILE, 1, 1, 0, 0), id_q = idesc_f16(TILE, (uint32_t)(g.d + 15) & ~15u, 1, 1, 0, 1);
