@@ -212,7 +212,8 @@ gma_status_t gma_norm_backward(const gma_norm_grad_t *grad, void *workspace, siz
  * `offsets` (B + 1 int32 in device memory, not falling, taken as min(max(offset, 0), N)) the tensors are
  * [N][heads][width], sequence b is rows offsets[b] .. offsets[b + 1] - 1, batch strides are ignored and lengths is NULL.  Rows that belong to no
  * sequence are neither read nor written (outputs with GMA_ROWS_ZERO_TAIL: are written as zeros).
- * 1 <= d, dv <= 128; G divides H, H <= 4096; B <= 65535; B * N <= 2^28 rows (packed: N).  1e-12 <= scale <= 1e12.
+ * 1 <= d, dv <= 128; G divides H, H <= 4096; B <= 65535; B * N <= 2^28 rows (packed: N), and
+ * times H at most 2^34.  1e-12 <= scale <= 1e12.
  * The elements of a sequence's tokens are finite: where they are not, or a score overflows, that sequence's outputs are
  * unspecified; other sequences' are not touched.
  *
@@ -229,7 +230,9 @@ typedef struct {
     int32_t B, N, H, G;           /* sequences, rows of each (packed: in all), query heads, key and value heads */
     int32_t d, dv;                /* width of q and k, of v and o                                */
     int32_t dtype;                /* of q, k, v, o and their gradients                           */
-    uint32_t flags;               /* GMA_ATTN_CAUSAL, GMA_ROWS_ZERO_TAIL                         */
+    uint32_t flags;               /* GMA_ATTN_CAUSAL, GMA_ROWS_ZERO_TAIL; GMA_FLAG_TEST_WITHHOLD, for tests only:
+                                     the tensor-core kernels' first loads are left out and their waits give up
+                                     after about a millisecond                                    */
     float scale;                  /* 1e-12 .. 1e12                                               */
     uint32_t reserved;            /* 0                                                           */
     gma_heads_t q, k, v;          /* [B][N][H][d], [B][N][G][d], [B][N][G][dv]                   */

@@ -71,6 +71,26 @@ __device__ __forceinline__ Seq sequence(const Geo &g, int s)
     return q;
 }
 
+// Zeros in the rows of [rows][heads * width] that belong to no sequence, by warp `first` of `warps`.
+template <typename T>
+__device__ __forceinline__ void zero_dead_rows(const Geo &g, const Heads<T> &x, int heads, int width, long long rows, long long first, long long warps)
+{
+    const int lane = threadIdx.x & 31;
+    const int a = g.offsets ? max(g.offsets[0], 0) : 0, e = g.offsets ? g.offsets[g.B] : 0;
+    for (long long r = first; r < rows; r += warps) {
+        long long b = 0, i = r;
+        if (g.offsets) {
+            if (r >= a && r < e) continue;
+        } else {
+            b = r / g.N;
+            i = r - b * g.N;
+            if (i < blk::row_length(g.lengths, (int)b, g.N)) continue;
+        }
+        for (int h = 0; h < heads; ++h)
+            for (int c = lane; c < width; c += 32) x.at(b, i, h)[c] = from_f32<T>(0.f);
+    }
+}
+
 // Where lse and the like of (row of the tensors, head) lie: [B][H][N], packed [H][N].
 __device__ __forceinline__ long long stat_at(const Geo &g, const Seq &q, int h, int i)
 {
@@ -96,6 +116,8 @@ struct Item {
     int t0, t1;        // key tiles
     int slot, parts;   // first slot of the parts' results, how many parts (1: no slot)
     int part, pad;     // this part
+    Seq sq;            // the sequence: one access less between a block's start and its first tile
+    int pad2[3];
 };
 
 struct Join {          // an item that was cut
@@ -119,6 +141,7 @@ struct Plan {          // host side: sizes and places in the workspace
     int blocks;                // that run at a time
     int max_items, max_slots;  // of the list, and of the parts' results a head (0: items are not cut)
     int rows;                  // rows of a part's results
+    bool withhold;             // GMA_FLAG_TEST_WITHHOLD
     bool by_keys;              // items are tiles of keys, their cost the query tiles that see them (backward pass)
     size_t head_at, items_at, join_at, part_at, stat_at;
 };
@@ -131,6 +154,7 @@ struct PlanArgs {
     PlanHead *head;
     Item *items;
     Join *join;                // the items that were cut
+    int short_waits;           // GMA_FLAG_TEST_WITHHOLD
 };
 
 Plan make_plan(const gma_attn_t &a, int pack, int wide_rows, int narrow_rows, int key_shift, int blocks, bool cut, Carve *ws);

@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(PT) plan_kernel(const PlanArgs a0, const PlanA
 {
     const PlanArgs &a = blockIdx.x ? a1 : a0;
     __shared__ unsigned long long total;
-    __shared__ int slots, joins, largest, hist[BUCKETS], warps[PT / 32], first[PT + 1], rows[PT], keys[PT], costs[TILES], sizes[SIZES];
+    __shared__ int slots, joins, largest, hist[BUCKETS], warps[PT / 32], first[PT + 1], rows[PT], keys[PT], start_row[PT], costs[TILES], sizes[SIZES];
     __shared__ unsigned short seqs[TILES];
     __shared__ float times[SIZES];
     const int t = threadIdx.x, B = a.g.B, mask = (1 << a.key_shift) - 1;
@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(PT) plan_kernel(const PlanArgs a0, const PlanA
     if (t == 0) { total = 0; slots = 0; joins = 0; largest = 0; }
 #pragma unroll
     for (int i = 0; i < BUCKETS / PT; ++i) hist[t + i * PT] = 0;
-    if (a.hdr && t < (int)(sizeof(WsHeader) / 4)) reinterpret_cast<unsigned *>(a.hdr)[t] = 0;
+    if (a.hdr && t < (int)(sizeof(WsHeader) / 4)) reinterpret_cast<unsigned *>(a.hdr)[t] = t == 2 && a.short_waits;       // reserved[0]
     int tokens = a.wide, count = 0;
     // reads the sequences from `base` on; the tiles of those before each
     auto read = [&](int base) {
@@ -66,6 +66,7 @@ __global__ void __launch_bounds__(PT) plan_kernel(const PlanArgs a0, const PlanA
         __syncthreads();
         rows[t] = q.n;
         keys[t] = q.L;
+        start_row[t] = q.row0;
     };
     auto number = [&]() {
         const int n = rows[t], k = n ? (n - 1) / tokens + 1 : 0;
@@ -108,11 +109,12 @@ __global__ void __launch_bounds__(PT) plan_kernel(const PlanArgs a0, const PlanA
                         seqs[i] = (unsigned short)lo;
                     }
                 }
-                f(base + lo, tok, from, cost);
+                f(base + lo, tok, from, cost, lo);
             }
         }
     };
-    // wide tiles, or narrow ones where the wide ones are fewer than the SMs
+    // wide tiles, or narrow ones where the wide ones are fewer than the SMs (4 x 2048 x 8 heads of 64, 256 wide tiles: 38 us with those, 43
+    // with narrow ones)
     for (int base = 0; base < B; base += PT) {
         read(base);
         count += number();
@@ -126,7 +128,7 @@ __global__ void __launch_bounds__(PT) plan_kernel(const PlanArgs a0, const PlanA
     if (a.max_slots && B <= PT && count <= TILES && count) {     // more tiles than that fill the GPU as they are
         unsigned long long work = 0;
         int most = 0;
-        each([&](int, int, int, int cost) {
+        each([&](int, int, int, int cost, int) {
             work += cost;
             most = max(most, cost);
         });
@@ -179,7 +181,7 @@ __global__ void __launch_bounds__(PT) plan_kernel(const PlanArgs a0, const PlanA
     // how many of each size, where those of a size start, and the list
     auto parts_of = [&](int cost) { return cost <= share ? 1 : (cost - 1) / share + 1; };
     auto bucket_of = [&](int cost, int parts) { return BUCKETS - 1 - min(parts == 1 ? cost : (cost - 1) / parts + 1, BUCKETS - 1); };
-    each([&](int, int, int, int cost) {
+    each([&](int, int, int, int cost, int) {
         const int parts = parts_of(cost);
         atomicAdd(&hist[bucket_of(cost, parts)], parts);
     });
@@ -195,20 +197,21 @@ __global__ void __launch_bounds__(PT) plan_kernel(const PlanArgs a0, const PlanA
 #pragma unroll
     for (int i = 0; i < BUCKETS / PT; ++i) hist[t * (BUCKETS / PT) + i] = start + own[i];
     __syncthreads();
-    each([&](int s, int tok, int from, int cost) {
+    each([&](int s, int tok, int from, int cost, int at_seq) {
+        const int n = rows[at_seq], L = keys[at_seq];
+        const Seq q{a.g.offsets ? 0 : s, start_row[at_seq], n, L, a.g.cached ? L - n : 0};
         const int parts = parts_of(cost), size = parts == 1 ? cost : (cost - 1) / parts + 1;
         const int at = atomicAdd(&hist[bucket_of(cost, parts)], parts);
         if (parts == 1) {
-            if (at < a.max_items) a.items[at] = Item{s, tok, from, from + cost, 0, 1, 0, 0};
+            if (at < a.max_items) a.items[at] = Item{s, tok, from, from + cost, 0, 1, 0, 0, q, {}};
             return;
         }
         // cuts are within the bounds that the lists were made for (offsets that fall make tiles that are not cut: more than TILES, or too many)
         const int slot = atomicAdd(&slots, parts);
         const bool room = slot + parts <= a.max_slots && at + parts <= a.max_items;
         for (int p = 0; p < parts && at + p < a.max_items; ++p)
-            a.items[at + p] = Item{s, tok, min(p * size, cost), min((p + 1) * size, cost), room ? slot : 0, parts, room ? p : -1, 0};
+            a.items[at + p] = Item{s, tok, min(p * size, cost), min((p + 1) * size, cost), room ? slot : 0, parts, room ? p : -1, 0, q, {}};
         if (room) {
-            const Seq q = sequence(a.g, s);
             a.join[atomicAdd(&joins, 1)] = Join{slot, parts, q.b, q.row0 + tok, min(tokens, q.n - tok), 0, 0, 0};
         }
     });
@@ -216,7 +219,7 @@ __global__ void __launch_bounds__(PT) plan_kernel(const PlanArgs a0, const PlanA
     if (t == 0) {
         a.head->items = min(count, a.max_items);
         a.head->tokens = tokens;
-        a.head->ticket = 0;
+        a.head->ticket = a.blocks;       // a block's first item is that of its number
         a.head->joins = joins;
     }
 }
@@ -285,29 +288,17 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const Geo g, const PlanH
     }
 }
 
-// Rows that belong to no sequence: zeros.  A warp a row of [rows][heads * width].
+// Rows that belong to no sequence: zeros.
 template <typename T>
 __global__ void __launch_bounds__(256) attn_tail_kernel(const Geo g, const Heads<T> x, int heads, int width, long long rows)
 {
-    const int lane = threadIdx.x & 31;
-    for (long long r = blockIdx.x * 8ll + (threadIdx.x >> 5); r < rows; r += gridDim.x * 8ll) {
-        long long b = 0, i = r;
-        if (g.offsets) {
-            if (r >= max(g.offsets[0], 0) && r < g.offsets[g.B]) continue;
-        } else {
-            b = r / g.N;
-            i = r - b * g.N;
-            if (i < blk::row_length(g.lengths, (int)b, g.N)) continue;
-        }
-        for (int h = 0; h < heads; ++h)
-            for (int c = lane; c < width; c += 32) x.at(b, i, h)[c] = from_f32<T>(0.f);
-    }
+    zero_dead_rows(g, x, heads, width, rows, blockIdx.x * 8ll + (threadIdx.x >> 5), gridDim.x * 8ll);
 }
 
-// delta = do . o: LANES lanes a (row, head), eight elements each (VEC) or every LANES-th.
+// delta = do . o, and zeros in the gradients' rows that belong to no sequence: LANES lanes a (row, head), eight elements each (VEC) or every LANES-th.
 template <typename T, bool VEC, int LANES>
 __global__ void __launch_bounds__(256) attn_delta_kernel(const Geo g, const Heads<const T> o, const Heads<const T> d_o, float *delta,
-                                                         long long rows)
+                                                         long long rows, const Heads<T> dq, const Heads<T> dk, const Heads<T> dv, int zero)
 {
     const int lane = threadIdx.x % LANES;
     blk::let_next();
@@ -318,6 +309,14 @@ __global__ void __launch_bounds__(256) attn_delta_kernel(const Geo g, const Head
         const int h = (int)(r - bi * g.H), b = (int)(bi / g.N);
         const long long i = bi - (long long)b * g.N;
         if (is) is = g.offsets ? i >= max(g.offsets[0], 0) && i < g.offsets[g.B] : i < blk::row_length(g.lengths, b, g.N);
+        // the gradients' rows that belong to no sequence
+        if (zero && !is && r < rows) {
+            for (int c = lane; c < g.d; c += LANES) dq.at(b, i, h)[c] = from_f32<T>(0.f);
+            if (h < g.G) {
+                for (int c = lane; c < g.d; c += LANES) dk.at(b, i, h)[c] = from_f32<T>(0.f);
+                for (int c = lane; c < g.dv; c += LANES) dv.at(b, i, h)[c] = from_f32<T>(0.f);
+            }
+        }
         float s = 0.f;
         if (is) {
             const T *x = o.at(b, i, h), *y = d_o.at(b, i, h);
@@ -437,7 +436,8 @@ gma_status_t check_sizes(const gma_attn_t *a, uint32_t flags)
     if (a->lengths && a->offsets) return GMA_ERR_INVALID_ARG;
     if (!blk::opt_ok(a->lengths, 4) || !blk::opt_ok(a->offsets, 4) || !blk::opt_ok(a->lse, 4)) return GMA_ERR_INVALID_ARG;
     if (a->d > 128 || a->dv > 128 || a->H > 4096 || a->B > 65535) return GMA_ERR_UNSUPPORTED_SHAPE;
-    if ((a->offsets ? 1 : (long long)a->B) * a->N > (1 << 28)) return GMA_ERR_UNSUPPORTED_SHAPE;
+    const long long rows = (a->offsets ? 1 : (long long)a->B) * a->N;
+    if (rows > (1 << 28) || rows * a->H > (1ll << 34)) return GMA_ERR_UNSUPPORTED_SHAPE;       // tiles times heads stay below 2^31
     return GMA_OK;
 }
 
@@ -446,7 +446,7 @@ long long batches(const gma_attn_t &a) { return a.offsets ? 1 : a.B; }
 
 gma_status_t check(const gma_attn_t *a, bool out)
 {
-    gma_status_t r = check_sizes(a, GMA_ATTN_CAUSAL | GMA_ROWS_ZERO_TAIL);
+    gma_status_t r = check_sizes(a, GMA_ATTN_CAUSAL | GMA_ROWS_ZERO_TAIL | GMA_FLAG_TEST_WITHHOLD);
     if (r != GMA_OK) return r;
     const long long B = batches(*a), N = a->N;
     if (!heads_ok(a->q, a->dtype, B, N, a->H, a->d, false) || !heads_ok(a->k, a->dtype, B, N, a->G, a->d, false) ||
@@ -473,7 +473,7 @@ gma_status_t check_paged(const gma_attn_paged_t *p, bool attend)
 {
     if (!p || p->reserved) return GMA_ERR_INVALID_ARG;
     const gma_attn_t &a = p->attn;
-    gma_status_t r = check_sizes(&a, GMA_ROWS_ZERO_TAIL);
+    gma_status_t r = check_sizes(&a, GMA_ROWS_ZERO_TAIL | GMA_FLAG_TEST_WITHHOLD);
     if (r != GMA_OK) return r;
     if (p->pages < 1 || p->page < 1 || p->table_pages < 1 || p->table_stride < 0) return GMA_ERR_INVALID_ARG;
     if (!blk::ptr_ok(p->table, 4) || !blk::ptr_ok(p->cached, 4)) return GMA_ERR_INVALID_ARG;
@@ -523,6 +523,7 @@ Geo geo_of(const gma_attn_t &a, const gma_attn_paged_t *p)
 Plan make_plan(const gma_attn_t &a, int pack, int wide_rows, int narrow_rows, int key_shift, int blocks, bool cut, Carve *ws)
 {
     Plan p = {};
+    p.withhold = (a.flags & GMA_FLAG_TEST_WITHHOLD) != 0;
     p.pack = pack;
     p.heads = a.H / pack;
     p.narrow = std::max(narrow_rows / pack, 1);
@@ -532,7 +533,7 @@ Plan make_plan(const gma_attn_t &a, int pack, int wide_rows, int narrow_rows, in
     // tiles of n rows and of every sequence's last rows; wide tiles are the fewer
     const long long n = (long long)a.N * batches(a);
     long long narrow = n / p.narrow + a.B, wide = n / p.wide + a.B;
-    // narrow ones are taken where the wide ones are fewer than SMS / heads, so that they are at most twice as many and one
+    // narrow ones are taken where the wide ones are fewer than the SMs, so that they are at most twice as many and one
     const long long most = std::max(wide, std::min(narrow, (long long)(wide_rows / narrow_rows + 1) * (SMS / p.heads + 1)));
     // the call's work is `blocks` shares and a part at least half of one; items longer than a part make at most twice as many
     const long long extra = cut ? 4ll * blocks / p.heads + 2 : 0;
@@ -551,7 +552,7 @@ PlanArgs plan_args(const Geo &g, const Plan &p, void *ws)
 {
     char *w = (char *)ws;
     return PlanArgs{g, p.wide, p.narrow, p.key_shift, p.blocks, p.heads, p.max_items, p.max_slots, p.by_keys, 1.f + p.rows / 64.f, (WsHeader *)ws,
-                    (PlanHead *)(w + p.head_at), (Item *)(w + p.items_at), (Join *)(w + p.join_at)};
+                    (PlanHead *)(w + p.head_at), (Item *)(w + p.items_at), (Join *)(w + p.join_at), p.withhold};
 }
 
 gma_status_t launch_plan(const PlanArgs &a, const PlanArgs *second, cudaStream_t st)
@@ -586,7 +587,8 @@ gma_status_t launch_delta(const gma_attn_grad_t &g, float *delta, cudaStream_t s
         constexpr int LANES = decltype(lanes)::value;
         const unsigned blocks = (unsigned)std::min<long long>((rows + 256 / LANES - 1) / (256 / LANES), SMS * 32);
         GMA_LAUNCH(KID_ATTN_DELTA, st, launch_pdl(attn_delta_kernel<T, decltype(v)::value, LANES>, blocks, 256, 0, st, geo, heads_of<const T>(a.o),
-                                                  heads_of<const T>(g.d_o), delta, rows));
+                                                  heads_of<const T>(g.d_o), delta, rows, heads_of<T>(g.dq), heads_of<T>(g.dk), heads_of<T>(g.dv),
+                                                  (a.flags & GMA_ROWS_ZERO_TAIL) && (a.lengths || a.offsets)));
         return GMA_OK;
     };
     using Yes = std::true_type;
@@ -687,9 +689,11 @@ gma_status_t gma_attn_forward(const gma_attn_t *a, void *ws, size_t ws_bytes, gm
     if (!blk::ws_ok(ws, ws_bytes, gma_attn_workspace_size(a))) return GMA_ERR_WORKSPACE;
     if ((r = usable_device()) != GMA_OK) return r;
     cudaStream_t st = (cudaStream_t)stream;
-    if ((r = zero_tail(*a, a->o, a->H, a->dv, st)) != GMA_OK) return r;
     if (tc_takes(*a, nullptr)) return tc_forward(*a, nullptr, ws, st);
-    if (!repacks(*a)) return simt_forward(*a, nullptr, ws, st);
+    if (!repacks(*a)) {
+        if ((r = zero_tail(*a, a->o, a->H, a->dv, st)) != GMA_OK) return r;
+        return simt_forward(*a, nullptr, ws, st);
+    }
     const Packed p = pack_places(*a, tc_workspace(*a, nullptr), ws);
     if ((r = launch_repack(*a, nullptr, p, st)) != GMA_OK) return r;
     return tc_forward(with(*a, p), nullptr, ws, st);
@@ -710,9 +714,6 @@ gma_status_t gma_attn_backward(const gma_attn_grad_t *g, void *ws, size_t ws_byt
     if ((r = usable_device()) != GMA_OK) return r;
     cudaStream_t st = (cudaStream_t)stream;
     const gma_attn_t &a = g->fwd;
-    if ((r = zero_tail(a, g->dq, a.H, a.d, st)) != GMA_OK) return r;
-    if ((r = zero_tail(a, g->dk, a.G, a.d, st)) != GMA_OK) return r;
-    if ((r = zero_tail(a, g->dv, a.G, a.dv, st)) != GMA_OK) return r;
     if (tc_takes_backward(*g)) return tc_backward(*g, ws, st);
     if (!repacks(a)) return simt_backward(*g, ws, st);
     const Packed p = pack_places(a, tc_backward_workspace(*g), ws);
@@ -758,8 +759,9 @@ gma_status_t gma_attn_paged(const gma_attn_paged_t *p, void *ws, size_t ws_bytes
     if (!blk::ws_ok(ws, ws_bytes, gma_attn_paged_workspace_size(p))) return GMA_ERR_WORKSPACE;
     if ((r = usable_device()) != GMA_OK) return r;
     cudaStream_t st = (cudaStream_t)stream;
+    if (tc_takes(p->attn, p)) return tc_forward(p->attn, p, ws, st);
     if ((r = zero_tail(p->attn, p->attn.o, p->attn.H, p->attn.dv, st)) != GMA_OK) return r;
-    return tc_takes(p->attn, p) ? tc_forward(p->attn, p, ws, st) : simt_forward(p->attn, p, ws, st);
+    return simt_forward(p->attn, p, ws, st);
 }
 
 }  // extern "C"

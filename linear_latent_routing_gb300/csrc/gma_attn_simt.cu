@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(TH, 1) attn_simt_kernel(const Args<T> a)
     const Geo &g = a.g;
     const Item it = a.items[rank];
     if (it.part < 0) return;
-    const Seq s = sequence(g, it.seq);
+    const Seq s = it.sq;
     const int pack = a.pack, kvh = pack == 1 ? head / g.group : head;
     const int tokens = min(a.head->tokens, s.n - it.tok0), rows = tokens * pack;
     const int qp = pitch_of(g.d), vp = pitch_of(g.dv);
@@ -240,12 +240,13 @@ template <typename T, bool VEC> __global__ void __launch_bounds__(TH, 1) attn_si
 {
     constexpr int RI = BR / 16;
     extern __shared__ __align__(16) float smem[];
-    blk::wait_previous();
+    // (the blocks before read the same results, and had waited for them when they let this kernel start; its last block waits for theirs)
+    if (blockIdx.x == gridDim.x - 1) blk::wait_previous();
     const int rank = blockIdx.x / a.heads, h = blockIdx.x % a.heads;
     if (rank >= a.head->items) return;
     const Geo &g = a.g;
     const Item it = a.items[rank];
-    const Seq s = sequence(g, it.seq);
+    const Seq s = it.sq;
     const int kvh = h / g.group, rows = min(BR, s.n - it.tok0);
     const int qp = pitch_of(g.d), vp = pitch_of(g.dv), stage = KT * (qp + vp);
     float *qs = smem, *os = qs + BR * qp, *ps = os + BR * vp, *ring = ps + BR * (KT + 4);
@@ -319,13 +320,13 @@ template <typename T, bool VEC> __global__ void __launch_bounds__(TH, 1) attn_si
     constexpr int RI = BR / 16;
     extern __shared__ __align__(16) float smem[];
     __shared__ float lse2[2][KT], delta[2][KT];
-    blk::let_next();
     blk::wait_previous();
+    blk::let_next();       // what this kernel reads, the next one reads too: dq's blocks take the SMs that these leave
     const int rank = blockIdx.x / a.heads, kvh = blockIdx.x % a.heads;
     if (rank >= a.head->items) return;
     const Geo &g = a.g;
     const Item it = a.items[rank];
-    const Seq s = sequence(g, it.seq);
+    const Seq s = it.sq;
     const int rows = min(BR, s.n - it.tok0);
     const int qp = pitch_of(g.d), vp = pitch_of(g.dv), stage = KT * (qp + vp);
     float *ks = smem, *vs = ks + BR * qp, *ps = vs + BR * vp, *ds = ps + BR * (KT + 4), *ring = ds + BR * (KT + 4);

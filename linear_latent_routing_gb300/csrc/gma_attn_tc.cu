@@ -35,6 +35,7 @@ struct TcArgs {
     float *lse;
     int pack, heads;           // query heads in a row tile, heads of the grid
     int o_vec;
+    long long zero_rows;       // of o, to be looked through for such as belong to no sequence (0: none)
     PlanHead *head;
     const Item *items;
     Parts parts;
@@ -44,6 +45,7 @@ struct TcArgs {
     int slots;
     int page_rows, tile_pages; // rows of a page's box, such boxes in a tile
     int page_shift;            // pages are powers of two
+    int withhold;              // GMA_FLAG_TEST_WITHHOLD: a block's first tile of keys is never loaded
 };
 
 // An item of one head as its block's warps see it.
@@ -248,9 +250,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const TcArgs a, con
         RingPos r{0, 1};
         uint32_t qt = 1;
         jt = 1;
-        int ticket = 0;
-        if (lane == 0) ticket = atomicAdd(&a.head->ticket, 1);
-        ticket = __shfl_sync(~0u, ticket, 0);
+        int ticket = blockIdx.x;                   // the plan's counter starts behind these
         while (true) {
             Job job;
             job.tokens = 0;
@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const TcArgs a, con
                 const int rank = ticket / a.heads;
                 const Item it = a.items[rank];
                 job.head = ticket - rank * a.heads;
-                job.sq = sequence(g, it.seq);
+                job.sq = it.sq;
                 job.seq = it.seq;
                 job.tok0 = it.tok0;
                 job.tokens = min(tile_tokens, job.sq.n - it.tok0);
@@ -310,15 +310,16 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const TcArgs a, con
                         uint64_t *full = &bars->full[r.s];
                         const int nb = half ? a.v_boxes : a.q_boxes;
                         const CUtensorMap *map = half ? &vmap : &kmap;
-                        if (lane == 0) mbar_arrive_expect_tx(full, PAGED ? (uint32_t)(boxes * a.page_rows * 128 * nb) : BOX * nb);
+                        const bool held = a.withhold && !issued;
+                        if (lane == 0 && !held) mbar_arrive_expect_tx(full, PAGED ? (uint32_t)(boxes * a.page_rows * 128 * nb) : BOX * nb);
                         __syncwarp();
                         if (PAGED) {
                             // an entry that names no page: a coordinate behind the pool, which reads as zeros
                             const int page = entry >= 0 && entry < g.pages ? entry : g.pages;
-                            if (lane < boxes)
+                            if (lane < boxes && !held)
                                 for (int b = 0; b < nb; ++b)
                                     tma_load_4d(dst + b * BOX + lane * a.page_rows * 128, map, full, 64 * b, job.kvh, in_page, page);
-                        } else if (lane == 0) {
+                        } else if (lane == 0 && !held) {
                             for (int b = 0; b < nb; ++b) tma_load_4d(dst + b * BOX, map, full, 64 * b, job.kvh, sq.row0 + kt * TILE, sq.b);
                         }
                         ++issued;
@@ -516,6 +517,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const TcArgs a, con
         }
     } else {
         reg_dec<88>();
+        // the output's rows that belong to no sequence (no other kernel's results are read or written here)
+        if (a.zero_rows) zero_dead_rows(g, a.o, g.H, g.dv, a.zero_rows, blockIdx.x * 2 + (warp - 10), gridDim.x * 2);
     }
     tc_fence_before();
     __syncthreads();
@@ -587,10 +590,12 @@ gma_status_t tc_forward(const gma_attn_t &a, const gma_attn_paged_t *p, void *ws
     x.pack = pl.pack;
     x.heads = pl.heads;
     x.o_vec = store_vec(a.o, a.dv);
+    x.zero_rows = (a.flags & GMA_ROWS_ZERO_TAIL) && (a.lengths || a.offsets) ? (a.offsets ? 1ll : a.B) * a.N : 0;
     x.head = (PlanHead *)(w + pl.head_at);
     x.items = (const Item *)(w + pl.items_at);
     x.parts = parts_of(pl, a, ws);
     x.hdr = (WsHeader *)ws;
+    x.withhold = pl.withhold;
     x.q_boxes = (a.d + 63) / 64;
     x.v_boxes = (a.dv + 63) / 64;
     x.slot_bytes = BOX * (uint32_t)(x.q_boxes > x.v_boxes ? x.q_boxes : x.v_boxes);

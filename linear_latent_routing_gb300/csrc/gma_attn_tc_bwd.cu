@@ -36,6 +36,7 @@ struct GradArgs {
     WsHeader *hdr;
     int q_boxes, v_boxes;
     int stages, k_slots, v_slots; // of the two kernels' rings
+    int withhold;                 // GMA_FLAG_TEST_WITHHOLD: a block's own tiles are never loaded
 };
 
 // A row's statistic enters its products as one more k-step: three bf16 terms that add up to it in fp32's 24 bits, against ones.
@@ -104,14 +105,14 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dkv_kernel(const GradArgs a, 
         bars->abort = 0;
         fence_mbar_init();
     }
-    blk::let_next();
     blk::wait_previous();
+    blk::let_next();       // what this kernel reads, the next one reads too: dq's blocks take the SMs that these leave
     const Geo &g = a.g;
     const int rank = blockIdx.x / g.G, kvh = blockIdx.x % g.G;
     if (rank >= a.k_head->items) return;
     if (warp == 8) tmem_alloc(&bars->tmem, 512);
     const Item it = a.k_items[rank];
-    const Seq sq = sequence(g, it.seq);
+    const Seq sq = it.sq;
     const int tiles = __shfl_sync(~0u, it.t1 - it.t0, 0), steps = tiles * g.group;
     for (int i = t; i < TILE; i += THREADS) {
         *reinterpret_cast<uint4 *>(ones + i * 32 + (((i >> 2) & 1) << 4)) = make_uint4(0x3f803f80u, 0x3f80u, 0, 0);
@@ -200,7 +201,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dkv_kernel(const GradArgs a, 
             mbar_wait(&bars->drain, 0, a.hdr, 225);
         }
     } else if (warp == 9) {
-        if (lane == 0) {
+        if (lane == 0 && !a.withhold) {
             mbar_arrive_expect_tx(&bars->kv, stage);
             for (int b = 0; b < a.q_boxes; ++b) tma_load_4d(sb + b * BOX, &kmap, &bars->kv, 64 * b, kvh, sq.row0 + it.tok0, sq.b);
             for (int b = 0; b < a.v_boxes; ++b) tma_load_4d(sb + q_tile + b * BOX, &vmap, &bars->kv, 64 * b, kvh, sq.row0 + it.tok0, sq.b);
@@ -359,13 +360,14 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dq_kernel(const GradArgs a, c
         bars->abort = 0;
         fence_mbar_init();
     }
-    blk::wait_previous();
+    // (the blocks before read the same results, and had waited for them when they let this kernel start; its last block waits for theirs)
+    if (blockIdx.x == gridDim.x - 1) blk::wait_previous();
     const Geo &g = a.g;
     const int rank = blockIdx.x / g.H, h = blockIdx.x % g.H, kvh = h / g.group;
     if (rank >= a.q_head->items) return;
     if (warp == 8) tmem_alloc(&bars->tmem, 512);
     const Item it = a.q_items[rank];
-    const Seq sq = sequence(g, it.seq);
+    const Seq sq = it.sq;
     const int tiles = __shfl_sync(~0u, it.t1 - it.t0, 0);
     tc_fence_before();
     __syncthreads();
@@ -421,7 +423,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dq_kernel(const GradArgs a, c
             mbar_wait(&bars->drain, 0, a.hdr, 243);
         }
     } else if (warp == 9) {
-        if (lane == 0) {
+        if (lane == 0 && !a.withhold) {
             mbar_arrive_expect_tx(&bars->q, q_tile + v_tile);
             for (int b = 0; b < a.q_boxes; ++b) tma_load_4d(sb + b * BOX, &qmap, &bars->q, 64 * b, h, sq.row0 + it.tok0, sq.b);
             for (int b = 0; b < a.v_boxes; ++b) tma_load_4d(sb + q_tile + b * BOX, &omap, &bars->q, 64 * b, h, sq.row0 + it.tok0, sq.b);
@@ -570,6 +572,7 @@ gma_status_t tc_backward(const gma_attn_grad_t &g, void *ws, cudaStream_t st)
     x.k_vec = store_vec(g.dk, a.d);
     x.v_vec = store_vec(g.dv, a.dv);
     x.hdr = (WsHeader *)ws;
+    x.withhold = p.q.withhold;
     x.q_boxes = (a.d + 63) / 64;
     x.v_boxes = (a.dv + 63) / 64;
     const uint32_t pair = BOX * (uint32_t)(x.q_boxes + x.v_boxes), k_fixed = pair + EXTRA + 1024 + (uint32_t)sizeof(KeyBars),

@@ -573,3 +573,86 @@ def test_refusals():
         a.paged(q, kp[:3], vp, table, n)
     with pytest.raises(ValueError):
         a.paged(q, kp, vp, table, n, out=q)
+
+
+@pytest.mark.parametrize("which", ["forward", "paged", "backward"])
+def test_waits_give_up(which):
+    """A load that never comes (GMA_FLAG_TEST_WITHHOLD): every role of the kernels leaves its loop, the time-out is in the workspace,
+    and the next call runs as ever."""
+    import ctypes
+
+    import test_attention as C
+    from linear_latent_routing_gb300 import gma
+    r = _draw(14)
+    N, H, G, d = 300, 4, 2, 64
+    q, k, v, o = r(1, N, H, d), r(1, N, G, d), r(1, N, G, d), r(1, N, H, d)
+    want = A().prompt(q, k, v)
+    held = 0x80000000
+
+    def heads(t):
+        return (t.data_ptr(), t.stride(0), t.stride(1), t.stride(2))
+    lse = A().prompt_lse(q).zero_()
+    kw = dict(B=1, N=N, H=H, G=G, d=d, dv=d, q=heads(q), k=heads(k), v=heads(v), o=heads(o), lse=lse.data_ptr())
+    if which == "forward":
+        packed, size, call = C._forward(flags=held | 1, **kw), "gma_attn_workspace_size", "gma_attn_forward"
+    elif which == "backward":
+        g = [torch.empty_like(x) for x in (q, k, v)]
+        packed = C._grad(flags=held | 1, do=heads(o), dq=heads(g[0]), dk=heads(g[1]), dv_=heads(g[2]), **kw)
+        size, call = "gma_attn_backward_workspace_size", "gma_attn_backward"
+    else:
+        pages, table, cached = r(20, 16, G, d), torch.arange(20, device="cuda").int(), _ints([N])
+        packed = C._paged(flags=held, kp=heads(pages), vp=heads(pages), pages=20, page=16, table_pages=20, table_stride=20,
+                          table=table.data_ptr(), cached=cached.data_ptr(), **kw)
+        size, call = "gma_attn_paged_workspace_size", "gma_attn_paged"
+    sized, run = getattr(gma.lib, size), getattr(gma.lib, call)
+    sized.argtypes, sized.restype = [ctypes.c_void_p], ctypes.c_size_t
+    run.argtypes, run.restype = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p], ctypes.c_int
+    n = sized(packed)
+    assert n > 0
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    stream = torch.cuda.current_stream().cuda_stream
+    assert run(packed, ws.data_ptr(), n, stream) == 0
+    assert gma.gma_check_workspace(ws.data_ptr(), stream) == gma.GMA_ERR_TIMEOUT
+    assert torch.equal(A().prompt(q, k, v, check=True), want)
+
+
+def test_expanded_heads_and_shared_pages():
+    """Keys and values of one head given as several (a stride of zero), and two sequences that share their first pages."""
+    r = _draw(15)
+    q, k, v, do = r(2, 200, 4, 64), r(2, 200, 1, 64), r(2, 200, 1, 64), r(2, 200, 4, 64)
+    wide = [t.expand(2, 200, 4, 64) for t in (k, v)]
+    lse = A().prompt_lse(q)
+    o = A().prompt(q, *wide, lse=lse)
+    g = A().prompt_backward(do, q, *wide, o, lse)
+    for b in range(2):
+        ref = R.attend(q[b], wide[0][b], wide[1][b], 0.125, do=do[b])
+        R.check(o[b], ref[0], "o")
+        for name, w in zip("qkv", ref[2:]):
+            R.check(g[name][b], w, name)
+    kp, vp = r(6, 32, 2, 64), r(6, 32, 2, 64)
+    table, lengths, q = _ints([[0, 1, 2], [0, 1, 4]]), _ints([90, 70]), r(2, 4, 64)
+    o = A().paged(q, kp, vp, table, lengths)
+    for b, L in enumerate((90, 70)):
+        ref, _ = R.attend(q[b:b + 1], _cached(kp, table, b, L), _cached(vp, table, b, L), 0.125, L - 1)
+        R.check(o[b:b + 1], ref, "o")
+
+
+def test_two_host_threads():
+    import threading
+    cases = [_prompt(([333, 20], 4, 2, 64, 64, "bf16", True, "packed"), 16), _prompt(([150], 2, 1, 128, 128, "bf16", False, "plain"), 17)]
+    want = [A().prompt(*c[:3], **c[4]) for c in cases]
+    got = [[], []]
+
+    def work(i):
+        s = torch.cuda.Stream()
+        for _ in range(30):
+            got[i].append(A().prompt(*cases[i][:3], stream=s, **cases[i][4]))
+        s.synchronize()
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for i in range(2):
+        assert all(torch.equal(x, want[i]) for x in got[i])
