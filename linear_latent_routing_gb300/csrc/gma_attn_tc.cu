@@ -75,27 +75,24 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
-template <bool MAX>
-__device__ __forceinline__ void exponentials(const uint32_t (&r)[4][32], int c0, uint32_t ts, float sl2, float m, blk::f2 (&sum)[2], float (&x)[2])
+
+// exp2(s sl2 - m) of a row's scores as bf16 pairs into tensor memory, and their sums in fp32.
+__device__ __forceinline__ void exponentials(const uint32_t (&r)[4][32], uint32_t ts, float sl2, float m, blk::f2 (&sum)[2])
 {
     const float base = m == -INFINITY ? 0.f : -m;
     const blk::f2 scale = blk::pack2(sl2, sl2), shift = blk::pack2(base, base);
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
+    for (int c = 0; c < 4; ++c) {
         uint32_t p[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-            const float u = __uint_as_float(r[c0 + c][2 * e]), v = __uint_as_float(r[c0 + c][2 * e + 1]);
-            const blk::f2 y = blk::ex2_2(blk::fma2(blk::pack2(u, v), scale, shift));
-            if (MAX) {
-                x[0] = max3(x[0], u, v);
-                x[1] = max3(x[1], __uint_as_float(r[c0 + c + 2][2 * e]), __uint_as_float(r[c0 + c + 2][2 * e + 1]));
-            }
+            const blk::f2 y =
+                blk::ex2_2(blk::fma2(blk::pack2(__uint_as_float(r[c][2 * e]), __uint_as_float(r[c][2 * e + 1])), scale, shift));
             sum[e & 1] = blk::add2(sum[e & 1], y);
             const float2 z = blk::unpack2(y);
             p[e] = pack_bf16(z.x, z.y);
         }
-        tmem_st16(ts + 16 * (c0 + c), p);
+        tmem_st16(ts + 16 * c, p);
     }
 }
 
@@ -173,27 +170,24 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const TcArgs a, con
             const int step = two ? 1 : 2;
             auto loaded = [&](const RingPos &r) { return bar_wait(&bars->full[r.s], r.turn, a.hdr, 201, abort); };
             // S_w = Q_w K^T; after a tile's last one it is given back, after the job's last one the queries too
-            auto scores = [&](int w, const RingPos &k, bool last, int kt) {
-                if (elect()) {
-                    mma_tiles(tmem + w * TILE, q_desc + (w ? q_next : 0), k_desc(rb + (uint32_t)k.s * a.slot_bytes), id_s, ksteps);
-                    mma_commit(&bars->s[w]);
-                    if (last) {
-                        mma_commit(&bars->empty[k.s]);
-                        if (kt + 1 == t1) mma_commit(&bars->q_free);
-                    }
+            auto put_scores = [&](int w, const RingPos &k, bool last, int kt) {
+                mma_tiles(tmem + w * TILE, q_desc + (w ? q_next : 0), k_desc(rb + (uint32_t)k.s * a.slot_bytes), id_s, ksteps);
+                mma_commit(&bars->s[w]);
+                if (last) {
+                    mma_commit(&bars->empty[k.s]);
+                    if (kt + 1 == t1) mma_commit(&bars->q_free);
                 }
             };
+            auto scores = [&](int w, const RingPos &k, bool last, int kt) {
+                if (elect()) put_scores(w, k, last, kt);
+            };
             // O_w += P_w V
-            auto output = [&](int w, const RingPos &v, bool last) {
-                if (elect()) {
-                    const uint64_t desc = mn_desc(rb + (uint32_t)v.s * a.slot_bytes);
-                    const uint32_t p = tmem + w * TILE, o = tmem + 256 + w * TILE;
+            auto put_output = [&](int w, const RingPos &v, bool last) {
+                const uint64_t desc = mn_desc(rb + (uint32_t)v.s * a.slot_bytes);
+                const uint32_t p = tmem + w * TILE, o = tmem + 256 + w * TILE;
 #pragma unroll
-                    for (int s = 0; s < TILE / 16; ++s) mma_f16_tmem_a(o, p + 8 * s, desc + mn_step(s), id_o, s > 0 || begun[w]);
-                    if (last) mma_commit(&bars->empty[v.s]);
-                }
-                begun[w] = true;
-                turn[w] ^= 1u;
+                for (int s = 0; s < TILE / 16; ++s) mma_f16_tmem_a(o, p + 8 * s, desc + mn_step(s), id_o, s > 0 || begun[w]);
+                if (last) mma_commit(&bars->empty[v.s]);
             };
             // the keys that the next scores take
             RingPos k = kb;
@@ -209,24 +203,37 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const TcArgs a, con
                 k.step(2, a.slots);
             }
             for (int kt = t0; ok && kt < t1; ++kt) {
-                if (!(ok = loaded(v))) break;
-                const int have = L - kt * TILE;
-                // values behind the sequence's end meet probabilities of zero, and may be anything
-                if (have < TILE) zero_rows(ring + (size_t)v.s * a.slot_bytes, a.v_boxes, have);
-                const int next = kt + step;
+                const int next = kt + step, have = L - kt * TILE;
+                bool v_there = false, k_there = false;
 #pragma unroll
                 for (int w = 0; w < 2; ++w) {
                     if (two ? w == 0 && kt >= e0 : w != ((kt - t0) & 1)) continue;
-                    if (!(ok = bar_wait(&bars->p[w], turn[w], a.hdr, 202, abort))) break;
+                    const bool last = !two || w == 1, more = next < (two && w == 0 ? e0 : t1);
+                    // A barrier that is through costs some 80 cycles to find so, and this warp's time is what bounds the loop: the three that the
+                    // products wait for are asked at once.  Keys that are not there yet do not keep the first product.
+                    const bool p_now = mbar_test_wait(&bars->p[w], turn[w]);
+                    const bool v_now = v_there || mbar_test_wait(&bars->full[v.s], v.turn);
+                    const bool k_now = !more || k_there || mbar_test_wait(&bars->full[k.s], k.turn);
+                    if (!v_now && !(ok = loaded(v))) break;
+                    // values behind the sequence's end meet probabilities of zero, and may be anything
+                    if (have < TILE && !v_there) zero_rows(ring + (size_t)v.s * a.slot_bytes, a.v_boxes, have);
+                    v_there = true;
+                    if (!p_now && !(ok = bar_wait(&bars->p[w], turn[w], a.hdr, 202, abort))) break;
                     tc_fence_after();
-                    const bool last = !two || w == 1;
-                    output(w, v, last);
-                    if (next < (two && w == 0 ? e0 : t1)) {
+                    if (k_now) {
+                        if (elect()) {
+                            put_output(w, v, last);
+                            if (more) put_scores(w, k, last, next);
+                            else mma_commit(&bars->o[w]);
+                        }
+                    } else {
+                        if (elect()) put_output(w, v, last);
                         if (!(ok = loaded(k))) break;
                         scores(w, k, last, next);
-                    } else if (elect()) {
-                        mma_commit(&bars->o[w]);
                     }
+                    k_there = k_there || more;
+                    begun[w] = true;
+                    turn[w] ^= 1u;
                 }
                 v.step(2, a.slots);
                 k.step(2, a.slots);
@@ -362,7 +369,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const TcArgs a, con
             const int seen = valid ? job.sq.seen(g, tok) : job.sq.L;
             const int step = two ? 1 : 2, begin = two ? job.t0 : job.t0 + w, end = two && w == 0 ? job.e0 : job.t1;
             float m = -INFINITY;
-            blk::f2 l2 = blk::pack2(0.f, 0.f), l3 = l2;
+            blk::f2 sum[2] = {blk::pack2(0.f, 0.f), blk::pack2(0.f, 0.f)};
             bool ok = true;
             int n = 0;
             for (int kt = begin; kt < end; kt += step, ++n) {
@@ -370,68 +377,53 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const TcArgs a, con
                 st ^= 1u;
                 tc_fence_after();
                 if (busy) {
+                    const int lim = seen - kt * TILE;
+                    const bool edge = __any_sync(~0u, lim < TILE);
                     uint32_t r[4][32];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, r[c]);
                     tmem_ld_wait();
-                    const int lim = seen - kt * TILE;
-                    if (__any_sync(~0u, lim < TILE)) {
+                    if (edge) {
 #pragma unroll
                         for (int c = 0; c < 4; ++c)
 #pragma unroll
                             for (int e = 0; e < 32; ++e)
                                 if (32 * c + e >= lim) r[c][e] = 0xff800000u;
                     }
-                    blk::f2 half_sum[2];
-                    float top = -INFINITY;
-                    bool known = n > 0;
-                    while (true) {
-                        if (!known) {
+                    float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                float x = __uint_as_float(r[c][0]);
+                    for (int e = 0; e < 32; e += 2) {
 #pragma unroll
-                                for (int e = 1; e < 32; ++e) x = fmaxf(x, __uint_as_float(r[c][e]));
-                                top = fmaxf(top, x);
-                            }
-                            const float now = fmaxf(m, top * g.sl2), f = now == -INFINITY ? 1.f : ex2(m - now);
-                            m = now;
-                            const blk::f2 ff = blk::pack2(f, f);
-                            l2 = blk::mul2(l2, ff);
-                            l3 = blk::mul2(l3, ff);
-                            if (n) {
+                        for (int c = 0; c < 4; ++c) x[c] = max3(x[c], __uint_as_float(r[c][e]), __uint_as_float(r[c][e + 1]));
+                    }
+                    const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * g.sl2;
+                    // the maximum that the exponentials are relative to moves rarely, and with it what was summed up so far
+                    if (__any_sync(~0u, top > m + GROW)) {
+                        const float now = fmaxf(m, top), f = now == -INFINITY ? 1.f : ex2(m - now);
+                        m = now;
+                        const blk::f2 ff = blk::pack2(f, f);
+                        sum[0] = blk::mul2(sum[0], ff);
+                        sum[1] = blk::mul2(sum[1], ff);
+                        if (n) {
 #pragma unroll 1
-                                for (int c = 0; c < g.dv; c += 16) {
-                                    uint32_t v[16];
-                                    tmem_ld16(to + c, v);
-                                    tmem_ld_wait();
+                            for (int c = 0; c < g.dv; c += 16) {
+                                uint32_t v[16];
+                                tmem_ld16(to + c, v);
+                                tmem_ld_wait();
 #pragma unroll
-                                    for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
-                                    tmem_st16(to + c, v);
-                                }
+                                for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
+                                tmem_st16(to + c, v);
                             }
                         }
-                        half_sum[0] = l2;
-                        half_sum[1] = l3;
-                        float x[2] = {-INFINITY, -INFINITY};
-                        exponentials<true>(r, 0, ts, g.sl2, m, half_sum, x);
-                        if (!known) break;
-                        top = fmaxf(x[0], x[1]);
-                        if (!__any_sync(~0u, top * g.sl2 > m + GROW)) break;
-                        known = false;
-                        tmem_st_wait();
                     }
-                    float none[2];
-                    exponentials<false>(r, 2, ts, g.sl2, m, half_sum, none);
-                    l2 = half_sum[0];
-                    l3 = half_sum[1];
+                    exponentials(r, ts, g.sl2, m, sum);
                     tmem_st_wait();
                 }
                 tc_fence_before();
                 mbar_arrive(&bars->p[w]);
             }
             if (!ok) break;
-            const float2 la = blk::unpack2(blk::add2(l2, l3));
+            const float2 la = blk::unpack2(blk::add2(sum[0], sum[1]));
             float l = la.x + la.y;
             const bool shared = !two && job.t1 - job.t0 > 1;        // both streams have parts of the same rows
             if (n && !bar_wait(&bars->o[w], ot[w], a.hdr, 207, abort)) break;

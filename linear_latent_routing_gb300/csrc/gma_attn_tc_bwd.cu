@@ -381,41 +381,68 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dq_kernel(const GradArgs a, c
         const uint64_t qd = k_desc(sb), od = k_desc(sb + q_tile);
         // the ring's places of the keys whose scores come next, of the values whose dP does, and of the keys at hand
         RingPos rk{0, 0}, rv{0, 0}, rc{0, 0};
-        auto scores = [&](int j) {
-            if (!bar_wait(&bars->fk[rk.s], rk.turn, a.hdr, 241, abort)) return false;
-            // keys behind the sequence's end meet zeros of dS, and may be anything
+        // keys behind the sequence's end meet zeros of dS, and may be anything
+        auto keys = [&](int j, bool there) {
+            if (!there && !bar_wait(&bars->fk[rk.s], rk.turn, a.hdr, 241, abort)) return false;
             const int have = sq.L - (it.t0 + j) * TILE;
             if (have < TILE) zero_rows(ring + (size_t)rk.s * q_tile, a.q_boxes, have);
-            if (elect()) {
-                mma_tiles(tmem + 128 * (j & 1), qd, k_desc(rb + (uint32_t)rk.s * q_tile), id_s, kq);
-                mma_commit(&bars->s[j & 1]);
-            }
-            rk.step(1, a.k_slots);
             return true;
         };
-        auto v_there = [&]() { return bar_wait(&bars->fv[rv.s], rv.turn, a.hdr, 250, abort); };
-        auto dprobs = [&]() {
-            if (elect()) {
-                mma_tiles(tmem + 256, od, k_desc(vb + (uint32_t)rv.s * v_tile), id_s, ko);
-                mma_commit(&bars->dp);
-                mma_commit(&bars->ev[rv.s]);
+        auto put_scores = [&](int j) {
+            mma_tiles(tmem + 128 * (j & 1), qd, k_desc(rb + (uint32_t)rk.s * q_tile), id_s, kq);
+            mma_commit(&bars->s[j & 1]);
+        };
+        auto put_dprobs = [&]() {
+            mma_tiles(tmem + 256, od, k_desc(vb + (uint32_t)rv.s * v_tile), id_s, ko);
+            mma_commit(&bars->dp);
+            mma_commit(&bars->ev[rv.s]);
+        };
+        auto put_dq = [&](int j) {
+            const uint64_t k = mn_desc(rb + (uint32_t)rc.s * q_tile);
+            const uint32_t ds = tmem + 128 * (j & 1);
+#pragma unroll
+            for (int s = 0; s < 8; ++s) mma_f16_tmem_a(tmem + 384, ds + half_col(s), k + mn_step(s), id_q, j > 0 || s > 0);
+            mma_commit(&bars->ek[rc.s]);
+        };
+        auto values = [&]() { return bar_wait(&bars->fv[rv.s], rv.turn, a.hdr, 250, abort); };
+        if ((ok = ok && keys(0, false) && values()) && elect()) {
+            put_scores(0);
+            put_dprobs();
+        }
+        rk.step(1, a.k_slots);
+        rv.step(1, a.v_slots);
+        if (ok && tiles > 1 && (ok = keys(1, false))) {
+            if (elect()) put_scores(1);
+            rk.step(1, a.k_slots);
+        }
+        // dP of the next tile, dQ of this one and S of the one after next follow one another, their barriers asked at once: each costs some 80
+        // cycles to find that it is through, and this warp's time bounds the loop (4 x 4096 x 16 heads of 64: 268 -> 252 us)
+        for (int j = 0; ok && j < tiles; ++j) {
+            const bool more = j + 1 < tiles, after = j + 2 < tiles;
+            const bool now = mbar_test_wait(&bars->ds, j & 1);
+            const bool v_there = !more || mbar_test_wait(&bars->fv[rv.s], rv.turn);
+            const bool k_there = !after || mbar_test_wait(&bars->fk[rk.s], rk.turn);
+            if (!v_there && !(ok = values())) break;
+            if (!now && !(ok = bar_wait(&bars->ds, j & 1, a.hdr, 242, abort))) break;
+            tc_fence_after();
+            if (k_there) {
+                if (after && !(ok = keys(j + 2, true))) break;
+                if (elect()) {
+                    if (more) put_dprobs();
+                    put_dq(j);
+                    if (after) put_scores(j + 2);
+                }
+            } else {
+                if (elect()) {
+                    if (more) put_dprobs();
+                    put_dq(j);
+                }
+                if (!(ok = keys(j + 2, false))) break;
+                if (elect()) put_scores(j + 2);
             }
             rv.step(1, a.v_slots);
-        };
-        if ((ok = ok && scores(0) && v_there())) dprobs();
-        for (int j = 0; ok && j < tiles; ++j) {
-            if (j + 1 < tiles && !(ok = scores(j + 1) && v_there())) break;
-            if (!(ok = bar_wait(&bars->ds, j & 1, a.hdr, 242, abort))) break;
-            tc_fence_after();
-            if (j + 1 < tiles) dprobs();
-            if (elect()) {
-                const uint64_t k = mn_desc(rb + (uint32_t)rc.s * q_tile);
-                const uint32_t ds = tmem + 128 * (j & 1);
-#pragma unroll
-                for (int s = 0; s < 8; ++s) mma_f16_tmem_a(tmem + 384, ds + half_col(s), k + mn_step(s), id_q, j > 0 || s > 0);
-                mma_commit(&bars->ek[rc.s]);
-            }
             rc.step(1, a.k_slots);
+            if (after) rk.step(1, a.k_slots);
         }
         if (ok && elect()) mma_commit(&bars->done);
         if (*abort) {
