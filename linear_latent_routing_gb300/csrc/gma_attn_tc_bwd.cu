@@ -75,7 +75,6 @@ struct KeyBars {
     int abort;
 };
 
-template <bool EARLY>
 __global__ void __launch_bounds__(THREADS, 1) attn_dkv_kernel(const GradArgs a, const __grid_constant__ CUtensorMap qmap,
                                                               const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                                                               const __grid_constant__ CUtensorMap omap)
@@ -160,15 +159,15 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dkv_kernel(const GradArgs a, 
             }
             rp.step(1, a.stages);
         };
-        // With tiles to spare their arrival is waited for before the warps' barriers, so that two products follow one another at once; with two
-        // stages they come late, and the first product does not wait for the second's (64 wide: 358 -> 346 us over 4 x 4096 x 16 heads so, 128
-        // wide: 358 -> 389 over 8192 x 16).
+        // A barrier that is through costs some 80 cycles to find so, and this warp's time bounds the loop: the two that a pair of products waits
+        // for are asked at once.  A tile that is not there yet does not keep the first of the pair (waited for before it, 8192 x 16 heads
+        // of 128 take 389 us instead of 350).
         if ((ok = ok && q_there())) scores();
         if ((ok = ok && o_there())) dprobs();
         for (int i = 0; ok && i < steps; ++i) {
             const bool more = i + 1 < steps;
-            if (EARLY && more && !(ok = q_there())) break;
-            if (!(ok = bar_wait(&bars->p, i & 1, a.hdr, 223, abort))) break;
+            bool now = mbar_test_wait(&bars->p, i & 1), there = mbar_test_wait(&bars->fq[rs.s], rs.turn);
+            if (!now && !(ok = bar_wait(&bars->p, i & 1, a.hdr, 223, abort))) break;
             tc_fence_after();
             if (elect()) {
                 const uint64_t o = mn_desc(rb + rc.s * stage + q_tile);
@@ -177,11 +176,12 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dkv_kernel(const GradArgs a, 
                 mma_commit(&bars->eo[rc.s]);
             }
             if (more) {
-                if (!EARLY && !(ok = q_there())) break;
+                if (!there && !(ok = q_there())) break;
                 scores();
-                if (EARLY && !(ok = o_there())) break;
             }
-            if (!(ok = bar_wait(&bars->ds, i & 1, a.hdr, 224, abort))) break;
+            now = mbar_test_wait(&bars->ds, i & 1);
+            there = mbar_test_wait(&bars->fo[rp.s], rp.turn);
+            if (!now && !(ok = bar_wait(&bars->ds, i & 1, a.hdr, 224, abort))) break;
             tc_fence_after();
             if (elect()) {
                 const uint64_t q = mn_desc(rb + rc.s * stage);
@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dkv_kernel(const GradArgs a, 
                 mma_commit(&bars->eq[rc.s]);
             }
             if (more) {
-                if (!EARLY && !(ok = o_there())) break;
+                if (!there && !(ok = o_there())) break;
                 dprobs();
             }
             rc.step(1, a.stages);
@@ -623,11 +623,10 @@ gma_status_t tc_backward(const gma_attn_grad_t &g, void *ws, cudaStream_t st)
     gma_status_t r = launch_plan(first, &second, st);
     if (r != GMA_OK) return r;
     if ((r = launch_delta(g, delta, st)) != GMA_OK) return r;
-    auto dkv = x.stages > 2 ? attn_dkv_kernel<true> : attn_dkv_kernel<false>;
-    if (cudaFuncSetAttribute(dkv, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_MAX) != cudaSuccess ||
+    if (cudaFuncSetAttribute(attn_dkv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_MAX) != cudaSuccess ||
         cudaFuncSetAttribute(attn_dq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_MAX) != cudaSuccess)
         return GMA_ERR_CUDA;
-    GMA_LAUNCH(KID_ATTN_DKV, st, launch_pdl(dkv, (unsigned)p.k.max_items * a.G, THREADS, k_fixed + x.stages * k_stage, st, x, qm, km, vm, om));
+    GMA_LAUNCH(KID_ATTN_DKV, st, launch_pdl(attn_dkv_kernel, (unsigned)p.k.max_items * a.G, THREADS, k_fixed + x.stages * k_stage, st, x, qm, km, vm, om));
     GMA_LAUNCH(KID_ATTN_DQ, st, launch_pdl(attn_dq_kernel, (unsigned)p.q.max_items * a.H, THREADS, q_fixed + q_ring, st, x, qm, km, vm, om));
     return GMA_OK;
 }
