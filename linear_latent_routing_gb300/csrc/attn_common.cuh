@@ -71,23 +71,28 @@ __device__ __forceinline__ Seq sequence(const Geo &g, int s)
     return q;
 }
 
-// Zeros in the rows of [rows][heads * width] that belong to no sequence, by warp `first` of `warps`.
+// Zeros in the rows of [rows][heads * width] that belong to no sequence, by warp `first` of `warps`; `vec`: 16 bytes at a time.
 template <typename T>
-__device__ __forceinline__ void zero_dead_rows(const Geo &g, const Heads<T> &x, int heads, int width, long long rows, long long first, long long warps)
+__device__ __forceinline__ void zero_dead_rows(const Geo &g, const Heads<T> &x, int heads, int width, int rows, int first, int warps, bool vec)
 {
-    const int lane = threadIdx.x & 31;
-    const int a = g.offsets ? max(g.offsets[0], 0) : 0, e = g.offsets ? g.offsets[g.B] : 0;
-    for (long long r = first; r < rows; r += warps) {
-        long long b = 0, i = r;
+    constexpr int E = 16 / sizeof(T);
+    const int lane = threadIdx.x & 31, a = g.offsets ? max(g.offsets[0], 0) : 0, e = g.offsets ? g.offsets[g.B] : 0;
+    const int step = vec ? E : 1, each = width / step, all = heads * each;
+    for (int r = first; r < rows; r += warps) {
+        int b = 0, i = r;
         if (g.offsets) {
             if (r >= a && r < e) continue;
         } else {
             b = r / g.N;
             i = r - b * g.N;
-            if (i < blk::row_length(g.lengths, (int)b, g.N)) continue;
+            if (i < blk::row_length(g.lengths, b, g.N)) continue;
         }
-        for (int h = 0; h < heads; ++h)
-            for (int c = lane; c < width; c += 32) x.at(b, i, h)[c] = from_f32<T>(0.f);
+        for (int c = lane; c < all; c += 32) {
+            const int h = c / each;
+            T *at = x.at(b, i, h) + (c - h * each) * step;
+            if (vec) *reinterpret_cast<uint4 *>(at) = make_uint4(0, 0, 0, 0);
+            else *at = from_f32<T>(0.f);
+        }
     }
 }
 

@@ -290,9 +290,9 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const Geo g, const PlanH
 
 // Rows that belong to no sequence: zeros.
 template <typename T>
-__global__ void __launch_bounds__(256) attn_tail_kernel(const Geo g, const Heads<T> x, int heads, int width, long long rows)
+__global__ void __launch_bounds__(256) attn_tail_kernel(const Geo g, const Heads<T> x, int heads, int width, int rows, bool vec)
 {
-    zero_dead_rows(g, x, heads, width, rows, blockIdx.x * 8ll + (threadIdx.x >> 5), gridDim.x * 8ll);
+    zero_dead_rows(g, x, heads, width, rows, blockIdx.x * 8 + (threadIdx.x >> 5), gridDim.x * 8, vec);
 }
 
 // delta = do . o, and zeros in the gradients' rows that belong to no sequence: LANES lanes a (row, head), eight elements each (VEC) or every LANES-th.
@@ -311,10 +311,17 @@ __global__ void __launch_bounds__(256) attn_delta_kernel(const Geo g, const Head
         if (is) is = g.offsets ? i >= max(g.offsets[0], 0) && i < g.offsets[g.B] : i < blk::row_length(g.lengths, b, g.N);
         // the gradients' rows that belong to no sequence
         if (zero && !is && r < rows) {
-            for (int c = lane; c < g.d; c += LANES) dq.at(b, i, h)[c] = from_f32<T>(0.f);
+            auto clear = [&](T *at, int width) {
+                constexpr int E = 16 / sizeof(T);
+                if (zero > 1)
+                    for (int c = lane * E; c < width; c += LANES * E) *reinterpret_cast<uint4 *>(at + c) = make_uint4(0, 0, 0, 0);
+                else
+                    for (int c = lane; c < width; c += LANES) at[c] = from_f32<T>(0.f);
+            };
+            clear(dq.at(b, i, h), g.d);
             if (h < g.G) {
-                for (int c = lane; c < g.d; c += LANES) dk.at(b, i, h)[c] = from_f32<T>(0.f);
-                for (int c = lane; c < g.dv; c += LANES) dv.at(b, i, h)[c] = from_f32<T>(0.f);
+                clear(dk.at(b, i, h), g.d);
+                clear(dv.at(b, i, h), g.dv);
             }
         }
         float s = 0.f;
@@ -495,11 +502,12 @@ gma_status_t zero_tail(const gma_attn_t &a, const gma_heads_t &x, int heads, int
 {
     if (!(a.flags & GMA_ROWS_ZERO_TAIL) || (!a.lengths && !a.offsets)) return GMA_OK;
     const Geo g = geo_of(a, nullptr);
-    const long long rows = batches(a) * a.N;
+    const int rows = (int)(batches(a) * a.N);
+    const bool vec = width % (16 / (int)blk::elem_size(a.dtype)) == 0 && heads_vec(x, a.dtype);
     if (a.dtype == GMA_BF16)
-        GMA_LAUNCH(KID_ATTN_TAIL, st, attn_tail_kernel<__nv_bfloat16><<<row_blocks(rows), 256, 0, st>>>(g, heads_of<__nv_bfloat16>(x), heads, width, rows));
+        GMA_LAUNCH(KID_ATTN_TAIL, st, attn_tail_kernel<bf16><<<row_blocks(rows), 256, 0, st>>>(g, heads_of<bf16>(x), heads, width, rows, vec));
     else
-        GMA_LAUNCH(KID_ATTN_TAIL, st, attn_tail_kernel<float><<<row_blocks(rows), 256, 0, st>>>(g, heads_of<float>(x), heads, width, rows));
+        GMA_LAUNCH(KID_ATTN_TAIL, st, attn_tail_kernel<float><<<row_blocks(rows), 256, 0, st>>>(g, heads_of<float>(x), heads, width, rows, vec));
     return GMA_OK;
 }
 
@@ -582,13 +590,17 @@ gma_status_t launch_delta(const gma_attn_grad_t &g, float *delta, cudaStream_t s
     const Geo geo = geo_of(a, nullptr);
     const long long rows = batches(a) * a.H * a.N;
     const bool vec = a.dv % 8 == 0 && heads_vec(a.o, a.dtype) && heads_vec(g.d_o, a.dtype);
+    // rows of no sequence in the gradients: none to clear, element by element, 16 bytes at a time
+    const int e16 = 16 / (int)blk::elem_size(a.dtype);
+    const int zero = !((a.flags & GMA_ROWS_ZERO_TAIL) && (a.lengths || a.offsets)) ? 0
+                     : a.d % e16 == 0 && a.dv % e16 == 0 && heads_vec(g.dq, a.dtype) && heads_vec(g.dk, a.dtype) && heads_vec(g.dv, a.dtype) ? 2 : 1;
     auto launch = [&](auto type, auto v, auto lanes) -> gma_status_t {
         using T = decltype(type);
         constexpr int LANES = decltype(lanes)::value;
         const unsigned blocks = (unsigned)std::min<long long>((rows + 256 / LANES - 1) / (256 / LANES), SMS * 32);
         GMA_LAUNCH(KID_ATTN_DELTA, st, launch_pdl(attn_delta_kernel<T, decltype(v)::value, LANES>, blocks, 256, 0, st, geo, heads_of<const T>(a.o),
                                                   heads_of<const T>(g.d_o), delta, rows, heads_of<T>(g.dq), heads_of<T>(g.dk), heads_of<T>(g.dv),
-                                                  (a.flags & GMA_ROWS_ZERO_TAIL) && (a.lengths || a.offsets)));
+                                                  zero));
         return GMA_OK;
     };
     using Yes = std::true_type;

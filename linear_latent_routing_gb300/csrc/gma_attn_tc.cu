@@ -35,7 +35,7 @@ struct TcArgs {
     float *lse;
     int pack, heads;           // query heads in a row tile, heads of the grid
     int o_vec;
-    long long zero_rows;       // of o, to be looked through for such as belong to no sequence (0: none)
+    int zero_rows;             // of o, to be looked through for such as belong to no sequence (0: none)
     PlanHead *head;
     const Item *items;
     Parts parts;
@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const TcArgs a, con
     } else {
         reg_dec<88>();
         // the output's rows that belong to no sequence (no other kernel's results are read or written here)
-        if (a.zero_rows) zero_dead_rows(g, a.o, g.H, g.dv, a.zero_rows, blockIdx.x * 2 + (warp - 10), gridDim.x * 2);
+        if (a.zero_rows) zero_dead_rows(g, a.o, g.H, g.dv, a.zero_rows, blockIdx.x * 2 + (warp - 10), gridDim.x * 2, a.o_vec);
     }
     tc_fence_before();
     __syncthreads();
@@ -582,7 +582,7 @@ gma_status_t tc_forward(const gma_attn_t &a, const gma_attn_paged_t *p, void *ws
     x.pack = pl.pack;
     x.heads = pl.heads;
     x.o_vec = store_vec(a.o, a.dv);
-    x.zero_rows = (a.flags & GMA_ROWS_ZERO_TAIL) && (a.lengths || a.offsets) ? (a.offsets ? 1ll : a.B) * a.N : 0;
+    x.zero_rows = (a.flags & GMA_ROWS_ZERO_TAIL) && (a.lengths || a.offsets) ? (a.offsets ? 1 : a.B) * a.N : 0;
     x.head = (PlanHead *)(w + pl.head_at);
     x.items = (const Item *)(w + pl.items_at);
     x.parts = parts_of(pl, a, ws);
