@@ -125,6 +125,19 @@ struct Item {
     int pad2[3];
 };
 
+static_assert(sizeof(Item) == 64, "four 16-byte accesses");
+// (past the first-level cache, whose lines may be older than the launch that this one overlaps with)
+__device__ __forceinline__ Item load_item(const Item *at)
+{
+    union {
+        uint4 q[4];
+        Item it;
+    } u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u.q[i] = __ldcg(reinterpret_cast<const uint4 *>(at) + i);
+    return u.it;
+}
+
 struct Join {          // an item that was cut
     int slot, parts;   // its parts' results
     int b, row, tokens; // batch row, first row and tokens of the tile

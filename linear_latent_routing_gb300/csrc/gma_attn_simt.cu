@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(TH, 1) attn_simt_kernel(const Args<T> a)
     const int rank = blockIdx.x / a.heads, head = blockIdx.x % a.heads;
     if (rank >= a.head->items) return;
     const Geo &g = a.g;
-    const Item it = a.items[rank];
+    const Item it = load_item(a.items + rank);
     if (it.part < 0) return;
     const Seq s = it.sq;
     const int pack = a.pack, kvh = pack == 1 ? head / g.group : head;
@@ -243,9 +243,9 @@ template <typename T, bool VEC> __global__ void __launch_bounds__(TH, 1) attn_si
     // (the blocks before read the same results, and had waited for them when they let this kernel start; its last block waits for theirs)
     if (blockIdx.x == gridDim.x - 1) blk::wait_previous();
     const int rank = blockIdx.x / a.heads, h = blockIdx.x % a.heads;
-    if (rank >= a.head->items) return;
+    if (rank >= __ldcg(&a.head->items)) return;
     const Geo &g = a.g;
-    const Item it = a.items[rank];
+    const Item it = load_item(a.items + rank);
     const Seq s = it.sq;
     const int kvh = h / g.group, rows = min(BR, s.n - it.tok0);
     const int qp = pitch_of(g.d), vp = pitch_of(g.dv), stage = KT * (qp + vp);
@@ -275,8 +275,8 @@ template <typename T, bool VEC> __global__ void __launch_bounds__(TH, 1) attn_si
         const bool is = r < rows;
         const long long at = is ? stat_at(g, s, h, it.tok0 + r) : 0;
         seen[i] = is ? s.seen(g, it.tok0 + r) : 0;
-        lse2[i] = is ? a.stat_lse[at] * LOG2E : 0.f;
-        delta[i] = is ? a.delta[at] : 0.f;
+        lse2[i] = is ? __ldcg(a.stat_lse + at) * LOG2E : 0.f;
+        delta[i] = is ? __ldcg(a.delta + at) : 0.f;
 #pragma unroll
         for (int c = 0; c < 8; ++c) acc[i][c] = 0.f;
     }
@@ -325,7 +325,7 @@ template <typename T, bool VEC> __global__ void __launch_bounds__(TH, 1) attn_si
     const int rank = blockIdx.x / a.heads, kvh = blockIdx.x % a.heads;
     if (rank >= a.head->items) return;
     const Geo &g = a.g;
-    const Item it = a.items[rank];
+    const Item it = load_item(a.items + rank);
     const Seq s = it.sq;
     const int rows = min(BR, s.n - it.tok0);
     const int qp = pitch_of(g.d), vp = pitch_of(g.dv), stage = KT * (qp + vp);

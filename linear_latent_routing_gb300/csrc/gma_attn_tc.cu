@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const TcArgs a, con
             job.tokens = 0;
             if (ticket < all) {
                 const int rank = ticket / a.heads;
-                const Item it = a.items[rank];
+                const Item it = load_item(a.items + rank);
                 job.head = ticket - rank * a.heads;
                 job.sq = it.sq;
                 job.seq = it.seq;

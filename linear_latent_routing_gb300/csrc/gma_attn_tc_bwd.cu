@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dkv_kernel(const GradArgs a, 
     const int rank = blockIdx.x / g.G, kvh = blockIdx.x % g.G;
     if (rank >= a.k_head->items) return;
     if (warp == 8) tmem_alloc(&bars->tmem, 512);
-    const Item it = a.k_items[rank];
+    const Item it = load_item(a.k_items + rank);
     const Seq sq = it.sq;
     const int tiles = __shfl_sync(~0u, it.t1 - it.t0, 0), steps = tiles * g.group;
     for (int i = t; i < TILE; i += THREADS) {
@@ -364,9 +364,9 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dq_kernel(const GradArgs a, c
     if (blockIdx.x == gridDim.x - 1) blk::wait_previous();
     const Geo &g = a.g;
     const int rank = blockIdx.x / g.H, h = blockIdx.x % g.H, kvh = h / g.group;
-    if (rank >= a.q_head->items) return;
+    if (rank >= __ldcg(&a.q_head->items)) return;
     if (warp == 8) tmem_alloc(&bars->tmem, 512);
-    const Item it = a.q_items[rank];
+    const Item it = load_item(a.q_items + rank);
     const Seq sq = it.sq;
     const int tiles = __shfl_sync(~0u, it.t1 - it.t0, 0);
     tc_fence_before();
@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dq_kernel(const GradArgs a, c
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const int seen = valid ? sq.seen(g, tok) : sq.L;
         const long long at = valid ? stat_at(g, sq, h, tok) : 0;
-        const float lse2 = valid ? a.lse[at] * LOG2E : 0.f, delta = valid ? a.delta[at] : 0.f;
+        const float lse2 = valid ? __ldcg(a.lse + at) * LOG2E : 0.f, delta = valid ? __ldcg(a.delta + at) : 0.f;
         const blk::f2 scale = blk::pack2(g.sl2, g.sl2), less = blk::pack2(-lse2, -lse2), minus = blk::pack2(-delta, -delta);
         bool ok = true;
         for (int j = 0; j < tiles; ++j) {
