@@ -12,6 +12,8 @@ namespace {
 
 typedef __nv_bfloat16 bf16;
 constexpr int PT = 256;                // threads of the plan's block
+constexpr int SEQS = 1024;             // sequences that are held at a time
+constexpr int CUTS = 2 * SMS + 2;      // tiles that are cut, at most
 constexpr int BUCKETS = 1024;          // items are ordered by size up to so many key tiles
 constexpr int TILES = 2048;            // tiles up to which cutting is looked at
 constexpr int SIZES = 24;              // of parts that are tried
@@ -42,185 +44,184 @@ __device__ __forceinline__ int block_scan(int own, int *warps, int *all)
     return before + sum - own;
 }
 
-// A thread a sequence for their numbers of tiles, then a thread a tile (its sequence found by bisection) for everything else.  Up to PT
-// sequences are read once, and up to TILES tiles looked up once; more are gone through again in every pass.
-// Latency is all: 256 threads, whose barriers are cheap.
+// A thread a sequence (up to four of them) for their numbers of tiles, then a thread a tile (its sequence found by bisection) for everything
+// else.  Up to SEQS sequences are read once, and up to TILES tiles looked up once; more are gone through again in every pass.
+// Latency is all: 256 threads, whose barriers are cheap, a warp for each tile that is cut, and little code, since behind a long cache that has
+// gone through L2 it comes from DRAM (one loop for the three passes, where each had a copy of its own).  65536 cached tokens of one sequence,
+// 16 / 4 heads of 128: 43.7 -> 38.4 us a call; 512 sequences of 500 tokens but for one of 60000, when no more than 256 were cut: 439 -> 80 us.
 __global__ void __launch_bounds__(PT) plan_kernel(const PlanArgs a0, const PlanArgs a1)
 {
     const PlanArgs &a = blockIdx.x ? a1 : a0;
     __shared__ unsigned long long total;
-    __shared__ int slots, joins, largest, hist[BUCKETS], warps[PT / 32], first[PT + 1], rows[PT], keys[PT], start_row[PT], costs[TILES], sizes[SIZES];
+    __shared__ int slots, joins, largest, warps[PT / 32], first[SEQS + 1], rows[SEQS], keys[SEQS], start_row[SEQS], costs[TILES], sizes[SIZES];
+    __shared__ __align__(16) int hist[BUCKETS];
+    __shared__ int cut_at[CUTS], cut_slot[CUTS], cut_tile[CUTS];
     __shared__ unsigned short seqs[TILES];
     __shared__ float times[SIZES];
-    const int t = threadIdx.x, B = a.g.B, mask = (1 << a.key_shift) - 1;
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31, B = a.g.B, mask = (1 << a.key_shift) - 1;
+    const int per = min((B + PT - 1) / PT, SEQS / PT), held = per * PT, mine = t * per;      // sequences a thread, at a time, this thread's first
     blk::let_next();
     if (t == 0) { total = 0; slots = 0; joins = 0; largest = 0; }
-#pragma unroll
-    for (int i = 0; i < BUCKETS / PT; ++i) hist[t + i * PT] = 0;
+    *reinterpret_cast<int4 *>(hist + 4 * t) = make_int4(0, 0, 0, 0);
     if (a.hdr && t < (int)(sizeof(WsHeader) / 4)) reinterpret_cast<unsigned *>(a.hdr)[t] = t == 2 && a.short_waits;       // reserved[0]
-    int tokens = a.wide, count = 0;
-    // reads the sequences from `base` on; the tiles of those before each
-    auto read = [&](int base) {
-        Seq q = {};
-        if (base + t < B) q = sequence(a.g, base + t);
-        __syncthreads();
-        rows[t] = q.n;
-        keys[t] = q.L;
-        start_row[t] = q.row0;
-    };
-    auto number = [&]() {
-        const int n = rows[t], k = n ? (n - 1) / tokens + 1 : 0;
-        int all;
-        first[t] = block_scan(k, warps, &all);
-        if (t == PT - 1) first[PT] = all;
+    int tokens = a.wide;
+    // reads the sequences from `base` on (or has them), and numbers their tiles
+    auto number = [&](int base, bool have) {
+        int own = 0, all;
+        if (!have) __syncthreads();
+#pragma unroll 1
+        for (int k = mine; k < mine + per; ++k) {
+            if (!have) {
+                Seq q = {};
+                if (base + k < B) q = sequence(a.g, base + k);
+                rows[k] = q.n;
+                keys[k] = q.L;
+                start_row[k] = q.row0;
+            }
+            first[k] = own;                                          // of this thread's, so far
+            own += (unsigned)(rows[k] + tokens - 1) / (unsigned)tokens;
+        }
+        const int at = block_scan(own, warps, &all);
+#pragma unroll 1
+        for (int k = mine; k < mine + per; ++k) first[k] += at;
+        if (t == PT - 1) first[held] = all;
         __syncthreads();
         return all;
     };
-    bool known = false;          // costs and seqs hold all tiles
-    // f(sequence, first token, first key tile, key tiles) of every tile; by_keys: query tiles of a tile of keys
-    auto each = [&](auto f) {
-        for (int base = 0; base < B; base += PT) {
-            if (B > PT) {
-                read(base);
-                number();
-            }
-            for (int i = t; i < first[PT]; i += PT) {
-                int lo, cost, from = 0;
+    // wide tiles, or narrow ones where the wide ones are fewer than the SMs (4 x 2048 x 8 heads of 64, 256 wide tiles: 38 us with those, 43
+    // with narrow ones)
+    int count;
+    for (bool again = false;; again = true) {
+        count = 0;
+        for (int base = 0; base < B; base += held) count += number(base, again && B <= held);
+        if (again || (long long)count * a.heads >= SMS || a.narrow >= a.wide) break;
+        tokens = a.narrow;
+    }
+    const bool table = B <= held && count <= TILES;      // costs and seqs hold all tiles, after the first pass
+    // Three passes over the tiles: the work and the largest tile (where tiles may be cut; more of them than the table holds fill the GPU as they
+    // are), how many items of each size, and the list.
+    const bool cutting = a.max_slots && table && count;
+    int share = 0x7fffffff;                              // a part's key tiles
+#pragma unroll 1
+    for (int pass = cutting ? 0 : 1; pass < 3; ++pass) {
+        const bool known = table && (pass == 2 || (pass == 1 && cutting));
+        unsigned long long work = 0;
+        int most = 0;
+#pragma unroll 1
+        for (int base = 0; base < B; base += held) {
+            if (B > held) number(base, false);
+#pragma unroll 1
+            for (int i = t; i < first[held]; i += PT) {
+                int s = 0, cost;
                 if (known) {
-                    lo = seqs[i];
+                    s = seqs[i];
                 } else {
-                    int hi = PT;
-                    lo = 0;
-                    while (hi - lo > 1) {
-                        const int mid = (lo + hi) >> 1;
-                        if (first[mid] <= i) lo = mid; else hi = mid;
+                    int hi = held;
+                    while (hi - s > 1) {
+                        const int mid = (s + hi) >> 1;
+                        if (first[mid] <= i) s = mid; else hi = mid;
                     }
                 }
-                const int n = rows[lo], tok = (i - first[lo]) * tokens;
-                if (a.by_keys && a.g.causal) from = tok >> a.key_shift;
+                // (by_keys: query tiles of a tile of keys, from the first that sees it)
+                const int n = rows[s], L = keys[s], tok = (i - first[s]) * tokens, pos0 = a.g.cached ? L - n : 0;
+                const int from = a.by_keys && a.g.causal ? tok >> a.key_shift : 0;
                 if (known) {
                     cost = costs[i];
                 } else {
-                    const int L = keys[lo], last = min(tok + tokens, n) - 1, pos0 = a.g.cached ? L - n : 0;
-                    const int seen = a.g.causal ? min(max(pos0 + last + 1, 0), L) : L;
+                    const int last = min(tok + tokens, n) - 1, seen = a.g.causal ? min(max(pos0 + last + 1, 0), L) : L;
                     cost = a.by_keys ? ((n + mask) >> a.key_shift) - from : max((seen + mask) >> a.key_shift, 1);
-                    if (B <= PT && i < TILES) {
+                    if (table) {
                         costs[i] = cost;
-                        seqs[i] = (unsigned short)lo;
+                        seqs[i] = (unsigned short)s;
                     }
                 }
-                f(base + lo, tok, from, cost, lo);
+                if (pass == 0) {
+                    work += cost;
+                    most = max(most, cost);
+                    continue;
+                }
+                const int parts = cost <= share ? 1 : (cost - 1) / share + 1, size = parts == 1 ? cost : (cost - 1) / parts + 1;
+                const int at = atomicAdd(&hist[BUCKETS - 1 - min(size, BUCKETS - 1)], parts);
+                if (pass == 1) continue;
+                if (parts == 1) {
+                    const Seq q{a.g.offsets ? 0 : base + s, start_row[s], n, L, pos0};
+                    if (at < a.max_items) a.items[at] = Item{base + s, tok, from, from + cost, 0, 1, 0, 0, q, {}};
+                } else {
+                    const int cut = atomicAdd(&joins, 1), slot = atomicAdd(&slots, parts);
+                    if (cut < CUTS) cut_at[cut] = at, cut_slot[cut] = slot, cut_tile[cut] = i;
+                }
             }
         }
-    };
-    // wide tiles, or narrow ones where the wide ones are fewer than the SMs (4 x 2048 x 8 heads of 64, 256 wide tiles: 38 us with those, 43
-    // with narrow ones)
-    for (int base = 0; base < B; base += PT) {
-        read(base);
-        count += number();
-    }
-    if ((long long)count * a.heads < SMS && a.narrow < a.wide) {
-        tokens = a.narrow;
-        if (B <= PT) count = number();
-    }
-    // a part's key tiles: an estimate of the time with SIZES sizes, from half a block's share of the call to five of them
-    int share = 0x7fffffff;
-    if (a.max_slots && B <= PT && count <= TILES && count) {     // more tiles than that fill the GPU as they are
-        unsigned long long work = 0;
-        int most = 0;
-        each([&](int, int, int, int cost, int) {
-            work += cost;
-            most = max(most, cost);
-        });
-        known = true;
+        if (pass == 0) {
+            // the size of parts: an estimate of the time with SIZES sizes, from half a block's share of the call to five of them
 #pragma unroll
-        for (int o = 16; o; o >>= 1) {
-            work += __shfl_xor_sync(~0u, work, o);
-            most = max(most, __shfl_xor_sync(~0u, most, o));
-        }
-        if ((t & 31) == 0 && work) {
-            atomicAdd(&total, work);
-            atomicMax(&largest, most);
-        }
-        __syncthreads();
-        const float all = (float)total * a.heads, per = all / a.blocks;
-        const int warp = t >> 5, lane = t & 31, top = largest;
+            for (int o = 16; o; o >>= 1) {
+                work += __shfl_xor_sync(~0u, work, o);
+                most = max(most, __shfl_xor_sync(~0u, most, o));
+            }
+            if (lane == 0 && work) {
+                atomicAdd(&total, work);
+                atomicMax(&largest, most);
+            }
+            __syncthreads();
+            const float all = (float)total * a.heads, each = all / a.blocks;
+            const int top = largest;
 #pragma unroll 1
-        for (int c = warp; c < SIZES; c += PT / 32) {
-            const int size = max((int)ceilf(per * 0.5f * exp2f(c * (3.3f / (SIZES - 1)))), 1);
-            const float inv = 1.f / size;
-            int parts = 0, cut = 0;
-            for (int i = lane; i < count; i += 32) {
-                // (an estimate: the quotient may be off by one)
-                const int k = costs[i] <= size ? 1 : (int)((costs[i] - 1) * inv) + 1;
-                parts += k;
-                if (k > 1) cut += k;
+            for (int c = warp; c < SIZES; c += PT / 32) {
+                const int size = max((int)ceilf(each * 0.5f * exp2f(c * (3.3f / (SIZES - 1)))), 1);
+                const float inv = 1.f / size;
+                int parts = 0, cut = 0;
+#pragma unroll 1
+                for (int i = lane; i < count; i += 32) {
+                    // (an estimate: the quotient may be off by one)
+                    const int k = costs[i] <= size ? 1 : (int)((costs[i] - 1) * inv) + 1;
+                    parts += k;
+                    if (k > 1) cut += k;
+                }
+                parts = __reduce_add_sync(~0u, parts);
+                cut = __reduce_add_sync(~0u, cut);
+                const float items = (float)parts * a.heads, extra = ITEM_COST * items + a.part_cost * cut * a.heads;
+                const int cuts = top <= size ? 1 : (int)((top - 1) * inv) + 1;
+                const float longest = (float)((top - 1) / cuts + 1) + ITEM_COST + (cuts > 1 ? a.part_cost : 0.f);
+                const float mean = (all + extra) / items, waves = ceilf(items / a.blocks);
+                // equal items run in whole waves; unequal ones, the longest first, fill the gaps
+                const float time = longest < 1.2f * mean || items <= a.blocks ? waves * longest
+                                                                              : fmaxf((all + extra) / a.blocks + 0.5f * mean, longest);
+                if (lane == 0) times[c] = time, sizes[c] = size;
             }
-            parts = __reduce_add_sync(~0u, parts);
-            cut = __reduce_add_sync(~0u, cut);
-            const float items = (float)parts * a.heads, extra = ITEM_COST * items + a.part_cost * cut * a.heads;
-            const int cuts = top <= size ? 1 : (int)((top - 1) * inv) + 1;
-            const float longest = (float)((top - 1) / cuts + 1) + ITEM_COST + (cuts > 1 ? a.part_cost : 0.f);
-            const float mean = (all + extra) / items, waves = ceilf(items / a.blocks);
-            // equal items run in whole waves; unequal ones, the longest first, fill the gaps
-            const float time = longest < 1.2f * mean || items <= a.blocks ? waves * longest
-                                                                          : fmaxf((all + extra) / a.blocks + 0.5f * mean, longest);
-            if (lane == 0) times[c] = time, sizes[c] = size;
-        }
-        __syncthreads();
-        float best = times[0];
-        share = sizes[0];
-#pragma unroll
-        for (int w = 1; w < SIZES; ++w) {
-            const float x = times[w];
-            const int size = sizes[w];
-            share = x <= best ? size : share;
-            best = fminf(x, best);
+            __syncthreads();
+            // the largest of the best (times are not negative: their order is that of their bits)
+            const unsigned time = lane < SIZES ? __float_as_uint(times[lane]) : ~0u, best = __reduce_min_sync(~0u, time);
+            share = sizes[31 - __clz(__ballot_sync(~0u, time == best))];
+        } else if (pass == 1) {
+            // where the items of each size start, the largest first
+            __syncthreads();
+            const int4 h = *reinterpret_cast<const int4 *>(hist + 4 * t);
+            const int at = block_scan(h.x + h.y + h.z + h.w, warps, &count);
+            *reinterpret_cast<int4 *>(hist + 4 * t) = make_int4(at, at + h.x, at + h.x + h.y, at + h.x + h.y + h.z);
+            __syncthreads();
         }
     }
-    // how many of each size, where those of a size start, and the list
-    auto parts_of = [&](int cost) { return cost <= share ? 1 : (cost - 1) / share + 1; };
-    auto bucket_of = [&](int cost, int parts) { return BUCKETS - 1 - min(parts == 1 ? cost : (cost - 1) / parts + 1, BUCKETS - 1); };
-    each([&](int, int, int, int cost, int) {
-        const int parts = parts_of(cost);
-        atomicAdd(&hist[bucket_of(cost, parts)], parts);
-    });
-    known = known || (B <= PT && count <= TILES);
     __syncthreads();
-    int own[BUCKETS / PT], sum = 0;
-#pragma unroll
-    for (int i = 0; i < BUCKETS / PT; ++i) {
-        own[i] = sum;
-        sum += hist[t * (BUCKETS / PT) + i];
-    }
-    const int start = block_scan(sum, warps, &count);
-#pragma unroll
-    for (int i = 0; i < BUCKETS / PT; ++i) hist[t * (BUCKETS / PT) + i] = start + own[i];
-    __syncthreads();
-    each([&](int s, int tok, int from, int cost, int at_seq) {
-        const int n = rows[at_seq], L = keys[at_seq];
-        const Seq q{a.g.offsets ? 0 : s, start_row[at_seq], n, L, a.g.cached ? L - n : 0};
-        const int parts = parts_of(cost), size = parts == 1 ? cost : (cost - 1) / parts + 1;
-        const int at = atomicAdd(&hist[bucket_of(cost, parts)], parts);
-        if (parts == 1) {
-            if (at < a.max_items) a.items[at] = Item{s, tok, from, from + cost, 0, 1, 0, 0, q, {}};
-            return;
-        }
-        // cuts are within the bounds that the lists were made for (offsets that fall make tiles that are not cut: more than TILES, or too many)
-        const int slot = atomicAdd(&slots, parts);
+    // A warp a tile that is cut, a lane a part.  Cuts are within the bounds that the lists were made for (offsets that fall may make more tiles,
+    // which are left out).
+    const int cuts = min(min(joins, CUTS), a.max_slots);
+#pragma unroll 1
+    for (int c = warp; c < cuts; c += PT / 32) {
+        const int i = cut_tile[c], s = seqs[i], cost = costs[i], at = cut_at[c], slot = cut_slot[c], n = rows[s], L = keys[s];
+        const int tok = (i - first[s]) * tokens, parts = (cost - 1) / share + 1, size = (cost - 1) / parts + 1;
+        const Seq q{a.g.offsets ? 0 : s, start_row[s], n, L, a.g.cached ? L - n : 0};
         const bool room = slot + parts <= a.max_slots && at + parts <= a.max_items;
-        for (int p = 0; p < parts && at + p < a.max_items; ++p)
+#pragma unroll 1
+        for (int p = lane; p < parts && at + p < a.max_items; p += 32)
             a.items[at + p] = Item{s, tok, min(p * size, cost), min((p + 1) * size, cost), room ? slot : 0, parts, room ? p : -1, 0, q, {}};
-        if (room) {
-            a.join[atomicAdd(&joins, 1)] = Join{slot, parts, q.b, q.row0 + tok, min(tokens, q.n - tok), 0, 0, 0};
-        }
-    });
-    __syncthreads();
+        if (lane == 0) a.join[c] = Join{slot, room ? parts : 0, q.b, q.row0 + tok, min(tokens, n - tok), {}};
+    }
     if (t == 0) {
         a.head->items = min(count, a.max_items);
         a.head->tokens = tokens;
         a.head->ticket = a.blocks;       // a block's first item is that of its number
-        a.head->joins = joins;
+        a.head->joins = cuts;
     }
 }
 
@@ -230,12 +231,20 @@ template <typename T>
 __global__ void __launch_bounds__(256) attn_join_kernel(const Geo g, const PlanHead *head, const Join *join, const Parts p, const Heads<T> out,
                                                         float *lse, int pack)
 {
-    const unsigned lane = threadIdx.x & 31;
+    const unsigned lane = threadIdx.x & 31, step = gridDim.x * 8;
+    // (the plan was through when the kernel before let this one start)
+    const unsigned rows = (unsigned)__ldcg(&head->tokens) * pack, n = (unsigned)__ldcg(&head->joins) * p.heads * rows;
+    unsigned i = blockIdx.x * 8 + (threadIdx.x >> 5);
+    auto entry = [&]() {
+        const int4 *at = reinterpret_cast<const int4 *>(join + min(i, n - 1) / rows / p.heads);
+        const int4 x = __ldcg(at), y = __ldcg(at + 1);
+        return Join{x.x, x.y, x.z, x.w, y.x, {}};
+    };
+    Join it = {};
+    if (i < n) it = entry();
     blk::wait_previous();
-    const unsigned rows = (unsigned)head->tokens * pack, n = (unsigned)head->joins * p.heads * rows;
-    for (unsigned i = blockIdx.x * 8 + (threadIdx.x >> 5); i < n; i += gridDim.x * 8) {
+    for (; i < n; i += step, it = entry()) {
         const unsigned hj = i / rows, row = i - hj * rows, j = hj / p.heads, hd = hj - j * p.heads;
-        const Join it = join[j];
         const int tok = row / pack, h = pack == 1 ? hd : hd * pack + row % pack;
         if (tok >= it.tokens) continue;
         const float *stat = p.stat_at(it.slot, hd, row), *part = p.o_at(it.slot, hd, row) + 4 * lane;

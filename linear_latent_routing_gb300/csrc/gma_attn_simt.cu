@@ -112,13 +112,12 @@ __global__ void __launch_bounds__(TH, 1) attn_simt_kernel(const Args<T> a)
 {
     constexpr int RI = R / 16;
     extern __shared__ __align__(16) float smem[];
-    if (PAGED) blk::let_next();
     blk::wait_previous();
+    if (PAGED) blk::let_next();
     const int rank = blockIdx.x / a.heads, head = blockIdx.x % a.heads;
-    if (rank >= a.head->items) return;
     const Geo &g = a.g;
-    const Item it = load_item(a.items + rank);
-    if (it.part < 0) return;
+    const Item it = load_item(a.items + rank);       // beside the number of items
+    if (rank >= a.head->items || it.part < 0) return;
     const Seq s = it.sq;
     const int pack = a.pack, kvh = pack == 1 ? head / g.group : head;
     const int tokens = min(a.head->tokens, s.n - it.tok0), rows = tokens * pack;
@@ -243,9 +242,9 @@ template <typename T, bool VEC> __global__ void __launch_bounds__(TH, 1) attn_si
     // (the blocks before read the same results, and had waited for them when they let this kernel start; its last block waits for theirs)
     if (blockIdx.x == gridDim.x - 1) blk::wait_previous();
     const int rank = blockIdx.x / a.heads, h = blockIdx.x % a.heads;
-    if (rank >= __ldcg(&a.head->items)) return;
     const Geo &g = a.g;
     const Item it = load_item(a.items + rank);
+    if (rank >= __ldcg(&a.head->items)) return;
     const Seq s = it.sq;
     const int kvh = h / g.group, rows = min(BR, s.n - it.tok0);
     const int qp = pitch_of(g.d), vp = pitch_of(g.dv), stage = KT * (qp + vp);
@@ -323,9 +322,9 @@ template <typename T, bool VEC> __global__ void __launch_bounds__(TH, 1) attn_si
     blk::wait_previous();
     blk::let_next();       // what this kernel reads, the next one reads too: dq's blocks take the SMs that these leave
     const int rank = blockIdx.x / a.heads, kvh = blockIdx.x % a.heads;
-    if (rank >= a.head->items) return;
     const Geo &g = a.g;
     const Item it = load_item(a.items + rank);
+    if (rank >= a.head->items) return;
     const Seq s = it.sq;
     const int rows = min(BR, s.n - it.tok0);
     const int qp = pitch_of(g.d), vp = pitch_of(g.dv), stage = KT * (qp + vp);

@@ -249,8 +249,9 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const TcArgs a, con
     } else if (warp == 9) {
         // ================================================================ jobs and loads
         reg_dec<88>();
-        if (PAGED) blk::let_next();
         blk::wait_previous();
+        if (PAGED) blk::let_next();
+        Item it = load_item(a.items + blockIdx.x / a.heads);       // beside the number of items: the list has a place for every block's first
         const int all = a.head->items * a.heads, tile_tokens = a.head->tokens;
         bool ok = true;
         int issued = 0, queries = 0;
@@ -263,7 +264,6 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const TcArgs a, con
             job.tokens = 0;
             if (ticket < all) {
                 const int rank = ticket / a.heads;
-                const Item it = load_item(a.items + rank);
                 job.head = ticket - rank * a.heads;
                 job.sq = it.sq;
                 job.seq = it.seq;
@@ -339,6 +339,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const TcArgs a, con
             // taken when this one's last tiles are on their way, not before: a block with a long item would hold on to a second one
             if (lane == 0) ticket = atomicAdd(&a.head->ticket, 1);
             ticket = __shfl_sync(~0u, ticket, 0);
+            if (ticket < all) it = load_item(a.items + ticket / a.heads);
         }
         // loads that no product waited for (a wait gave up) end before the block does
         if (*abort) {

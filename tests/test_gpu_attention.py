@@ -504,6 +504,23 @@ def test_more_sequences_than_blocks():
             R.check(rows(g[name], i), w, f"d{name} of sequence {i}")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B", [257, 700, 1024, 1500])
+def test_single_tokens_of_many_sequences(B, dtype):
+    """More sequences than the plan's threads, short ones but for a few that are cut into parts (up to 1024 sequences)."""
+    total = [(5 * i) % 23 for i in range(B)]
+    total[3], total[B - 1] = 4000, 2500
+    case = ([1] * B, total, 4, 2, 64, 64, dtype, 16, "single")
+    q, k, v, kp, vp, table, lengths, how, rows = _paged(case, 13)
+    lse = torch.full((B, 4), float("nan"), device="cuda")
+    o = A().paged(q, kp, vp, table, lengths, lse=lse, check=True, **how)
+    for b in [0, 1, 2, 3, 4, 46, 255, 256, B - 2, B - 1] + list(range(5, B, 41)):
+        L = total[b]
+        ref, stat = R.attend(q[b:b + 1], _cached(kp, table, b, L), _cached(vp, table, b, L), 64 ** -0.5, L - 1, True, T=TYPES[dtype])
+        R.check(o[b:b + 1], ref, f"o of sequence {b}")
+        R.check(lse[b][:, None], stat, f"lse of sequence {b}")
+
+
 def test_offsets_that_fall_or_reach_out():
     """Offsets outside the tensors are cut, falling ones make empty sequences; nothing outside the tensors is touched."""
     r = _draw(12)
