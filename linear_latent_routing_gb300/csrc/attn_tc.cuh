@@ -75,8 +75,7 @@ __device__ __forceinline__ bool elect()
     return is != 0;
 }
 
-// mbar_wait_abortable without its long suspension: the products and the warps that feed them wait for one another several
-// times a tile, and a thread that sleeps in try_wait comes back late (the 8192-token prompt with 16 heads of 128: %s).
+// mbar_wait_abortable with a try that comes first and without the clock: most waits here are short or over, several of them a tile.
 __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, WsHeader *hdr, unsigned where, volatile int *abort)
 {
     if (mbar_try_wait(bar, parity)) return true;
