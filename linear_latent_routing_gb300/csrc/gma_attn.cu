@@ -60,9 +60,10 @@ __global__ void __launch_bounds__(PT) plan_kernel(const PlanArgs a0, const PlanA
     __shared__ float times[SIZES];
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31, B = a.g.B, mask = (1 << a.key_shift) - 1;
     const int per = min((B + PT - 1) / PT, SEQS / PT), held = per * PT, mine = t * per;      // sequences a thread, at a time, this thread's first
-    blk::let_next();
     if (t == 0) { total = 0; slots = 0; joins = 0; largest = 0; }
     *reinterpret_cast<int4 *>(hist + 4 * t) = make_int4(0, 0, 0, 0);
+    blk::wait_previous();
+    blk::let_next();             // what came before is through, then: the next kernel's zeros need not wait
     if (a.hdr && t < (int)(sizeof(WsHeader) / 4)) reinterpret_cast<unsigned *>(a.hdr)[t] = t == 2 && a.short_waits;       // reserved[0]
     int tokens = a.wide;
     // reads the sequences from `base` on (or has them), and numbers their tiles
@@ -361,6 +362,7 @@ __global__ void __launch_bounds__(256) attn_append_kernel(const Geo g, const Hea
                                                           const Heads<T> vp, long long rows)
 {
     const int lane = threadIdx.x & 31;
+    blk::let_next();             // the plan of a call on the cache, which waits for this one's end
     for (long long r = blockIdx.x * 8ll + (threadIdx.x >> 5); r < rows; r += gridDim.x * 8ll) {
         const int h = (int)(r % g.G);
         const long long tok = r / g.G;
@@ -574,7 +576,7 @@ PlanArgs plan_args(const Geo &g, const Plan &p, void *ws)
 
 gma_status_t launch_plan(const PlanArgs &a, const PlanArgs *second, cudaStream_t st)
 {
-    GMA_LAUNCH(KID_ATTN_PLAN, st, plan_kernel<<<second ? 2 : 1, PT, 0, st>>>(a, second ? *second : a));
+    GMA_LAUNCH(KID_ATTN_PLAN, st, launch_pdl(plan_kernel, second ? 2 : 1, PT, 0, st, a, second ? *second : a));
     return GMA_OK;
 }
 
