@@ -1,5 +1,5 @@
 // gma_attn.cu -- softmax attention: the entry points' checks, the plan of a call, and the small kernels around the
-// products: tokens into the cache's pages, zeros behind sequences, do . o of every row.
+// products: tokens into the cache's pages, do . o of every row with zeros behind sequences in the gradients, dense copies, the join.
 #include <algorithm>
 #include <type_traits>
 
@@ -298,13 +298,6 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const Geo g, const PlanH
     }
 }
 
-// Rows that belong to no sequence: zeros.
-template <typename T>
-__global__ void __launch_bounds__(256) attn_tail_kernel(const Geo g, const Heads<T> x, int heads, int width, int rows, bool vec)
-{
-    zero_dead_rows(g, x, heads, width, rows, blockIdx.x * 8 + (threadIdx.x >> 5), gridDim.x * 8, vec);
-}
-
 // delta = do . o, and zeros in the gradients' rows that belong to no sequence: LANES lanes a (row, head), eight elements each (VEC) or every LANES-th.
 template <typename T, bool VEC, int LANES>
 __global__ void __launch_bounds__(256) attn_delta_kernel(const Geo g, const Heads<const T> o, const Heads<const T> d_o, float *delta,
@@ -508,20 +501,6 @@ gma_status_t check_paged(const gma_attn_paged_t *p, bool attend)
     return GMA_OK;
 }
 
-// Zeros in the rows of an output that no sequence has.
-gma_status_t zero_tail(const gma_attn_t &a, const gma_heads_t &x, int heads, int width, cudaStream_t st)
-{
-    if (!(a.flags & GMA_ROWS_ZERO_TAIL) || (!a.lengths && !a.offsets)) return GMA_OK;
-    const Geo g = geo_of(a, nullptr);
-    const int rows = (int)(batches(a) * a.N);
-    const bool vec = width % (16 / (int)blk::elem_size(a.dtype)) == 0 && heads_vec(x, a.dtype);
-    if (a.dtype == GMA_BF16)
-        GMA_LAUNCH(KID_ATTN_TAIL, st, attn_tail_kernel<bf16><<<row_blocks(rows), 256, 0, st>>>(g, heads_of<bf16>(x), heads, width, rows, vec));
-    else
-        GMA_LAUNCH(KID_ATTN_TAIL, st, attn_tail_kernel<float><<<row_blocks(rows), 256, 0, st>>>(g, heads_of<float>(x), heads, width, rows, vec));
-    return GMA_OK;
-}
-
 }  // namespace
 
 Geo geo_of(const gma_attn_t &a, const gma_attn_paged_t *p)
@@ -713,10 +692,7 @@ gma_status_t gma_attn_forward(const gma_attn_t *a, void *ws, size_t ws_bytes, gm
     if ((r = usable_device()) != GMA_OK) return r;
     cudaStream_t st = (cudaStream_t)stream;
     if (tc_takes(*a, nullptr)) return tc_forward(*a, nullptr, ws, st);
-    if (!repacks(*a)) {
-        if ((r = zero_tail(*a, a->o, a->H, a->dv, st)) != GMA_OK) return r;
-        return simt_forward(*a, nullptr, ws, st);
-    }
+    if (!repacks(*a)) return simt_forward(*a, nullptr, ws, st);
     const Packed p = pack_places(*a, tc_workspace(*a, nullptr), ws);
     if ((r = launch_repack(*a, nullptr, p, st)) != GMA_OK) return r;
     return tc_forward(with(*a, p), nullptr, ws, st);
@@ -783,7 +759,6 @@ gma_status_t gma_attn_paged(const gma_attn_paged_t *p, void *ws, size_t ws_bytes
     if ((r = usable_device()) != GMA_OK) return r;
     cudaStream_t st = (cudaStream_t)stream;
     if (tc_takes(p->attn, p)) return tc_forward(p->attn, p, ws, st);
-    if ((r = zero_tail(p->attn, p->attn.o, p->attn.H, p->attn.dv, st)) != GMA_OK) return r;
     return simt_forward(p->attn, p, ws, st);
 }
 

@@ -8,7 +8,7 @@
 // bounds them.  Warps whose rows do not exist only copy.
 //
 // Measured: 4 x 2048 x 8 heads of 117 in bf16 1.31 ms forward, 6.4 ms backward; three sequences of up to 301
-// tokens, 6 heads of 40 in fp32: 27 us a call with its two launches, five single tokens over 300 cached ones 14 us.
+// tokens, 6 heads of 40 in fp32: 23 us a call with its two launches, five single tokens over 300 cached ones 14 us.
 #include <algorithm>
 
 #include "attn_common.cuh"
@@ -27,6 +27,7 @@ template <typename T> struct Args {
     Heads<T> o;
     float *lse;
     int pack, heads;
+    int zero_rows, o_vec;              // rows of o to be looked through for such as belong to no sequence (0: none)
     const PlanHead *head;
     const Item *items;
     Parts parts;
@@ -115,6 +116,8 @@ __global__ void __launch_bounds__(TH, 1) attn_simt_kernel(const Args<T> a)
 {
     constexpr int RI = R / 16;
     extern __shared__ __align__(16) float smem[];
+    // beside the plan (no other kernel's results are read or written here)
+    if (a.zero_rows) zero_dead_rows(a.g, a.o, a.g.H, a.g.dv, a.zero_rows, blockIdx.x * (TH / 32) + (threadIdx.x >> 5), gridDim.x * (TH / 32), a.o_vec);
     blk::wait_previous();
     if (PAGED) blk::let_next();
     const int rank = blockIdx.x / a.heads, head = blockIdx.x % a.heads;
@@ -432,8 +435,9 @@ Plan plan_of(const gma_attn_t &a, const gma_attn_paged_t *paged, int *rows, Carv
     return make_plan(a, pack, *rows, *rows, 6, SMS, paged != nullptr, c);
 }
 
-// fp32 rows that cp.async can copy.
-bool vec_heads(const gma_heads_t &r) { return (((uintptr_t)r.ptr | (uintptr_t)(r.batch * 4) | (uintptr_t)(r.token * 4) | (uintptr_t)(r.head * 4)) & 15u) == 0; }
+// Rows of elements of e bytes on 16-byte boundaries; fp32 ones cp.async can copy.
+bool vec_rows(const gma_heads_t &r, size_t e) { return (((uintptr_t)r.ptr | (uintptr_t)(r.batch * e) | (uintptr_t)(r.token * e) | (uintptr_t)(r.head * e)) & 15u) == 0; }
+bool vec_heads(const gma_heads_t &r) { return vec_rows(r, 4); }
 
 template <typename T>
 Args<T> args_of(const gma_attn_t &a, const gma_attn_paged_t *paged, const Plan &p, void *ws)
@@ -448,6 +452,8 @@ Args<T> args_of(const gma_attn_t &a, const gma_attn_paged_t *paged, const Plan &
     x.lse = a.lse;
     x.pack = p.pack;
     x.heads = p.heads;
+    x.zero_rows = (a.flags & GMA_ROWS_ZERO_TAIL) && (a.lengths || a.offsets) ? (a.offsets ? 1 : a.B) * a.N : 0;
+    x.o_vec = a.dv % (int)(16 / sizeof(T)) == 0 && vec_rows(a.o, sizeof(T));
     x.head = (const PlanHead *)(w + p.head_at);
     x.items = (const Item *)(w + p.items_at);
     x.parts = parts_of(p, a, ws);

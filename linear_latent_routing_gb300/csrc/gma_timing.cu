@@ -80,7 +80,6 @@ const char *kernel_name(int id)
     case KID_ATTN_SIMT_DQ: return "attn_simt_backward_dq";
     case KID_ATTN_DELTA: return "attn_delta";
     case KID_ATTN_APPEND: return "attn_append";
-    case KID_ATTN_TAIL: return "attn_zero_rows";
     case KID_ATTN_REPACK: return "attn_repack";
     case KID_ATTN_JOIN: return "attn_join";
     }
