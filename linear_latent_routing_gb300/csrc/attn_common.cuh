@@ -203,6 +203,29 @@ inline Parts parts_of(const Plan &p, const gma_attn_t &a, void *ws)
 // Adds up the parts of the items that the plan cut, in their order.
 gma_status_t launch_join(const gma_attn_t &a, const Geo &g, const Plan &p, void *ws, cudaStream_t st);
 
+// ------------------------------------------------------------------ the pieces of a group
+// dk and dv of a head sum over its group's query heads.  Where that leaves SMs without work the group is cut into pieces, a block each, whose
+// fp32 sums [piece][head][row][pitch] a last launch adds up in their order.
+struct Pieces {
+    int count;                  // 1: dk and dv are written at once
+    float *k, *v;
+    int k_pitch, v_pitch, heads;
+    long long rows;
+    __device__ __forceinline__ long long at(int piece, int head, long long row) const { return ((long long)piece * heads + head) * rows + row; }
+    __device__ __forceinline__ float *k_at(int piece, int head, long long row) const { return k + at(piece, head, row) * k_pitch; }
+    __device__ __forceinline__ float *v_at(int piece, int head, long long row) const { return v + at(piece, head, row) * v_pitch; }
+};
+
+struct PiecePlan {
+    int count;
+    size_t k_at, v_at;
+};
+
+// For tiles of so many keys that walk over rows by steps of so many, each of so many us.
+PiecePlan plan_pieces(const gma_attn_t &a, int tile, int step, double step_us, Carve *ws);
+Pieces pieces_of(const PiecePlan &p, const gma_attn_t &a, void *ws);
+gma_status_t launch_pieces(const gma_attn_grad_t &g, const Pieces &p, cudaStream_t st);
+
 // ------------------------------------------------------------------ kernels
 Geo geo_of(const gma_attn_t &a, const gma_attn_paged_t *paged);
 

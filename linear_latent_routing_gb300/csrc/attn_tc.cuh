@@ -138,6 +138,21 @@ __device__ __forceinline__ void store_row(uint32_t tl, int width, float f, bool 
     }
 }
 
+// The same without a factor as a row of fp32, columns up to the next multiple of four.
+__device__ __forceinline__ void store_row_f32(uint32_t tl, int width, bool valid, float *row)
+{
+#pragma unroll 1
+    for (int c = 0; c < width; c += 32) {
+        uint32_t r[32];
+        tmem_ld32(tl + c, r);
+        tmem_ld_wait();
+        if (!valid) continue;
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            if (c + 4 * q < width) *reinterpret_cast<uint4 *>(row + c + 4 * q) = make_uint4(r[4 * q], r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]);
+    }
+}
+
 // ------------------------------------------------------------------ host side
 // Whether TMA can read these heads: bf16, 16-byte aligned strides that step.
 bool tma_heads(const gma_heads_t &r, long long B, long long N, long long heads);

@@ -349,6 +349,34 @@ __global__ void __launch_bounds__(256) attn_delta_kernel(const Geo g, const Head
     blk::wait_previous();
 }
 
+// dk and dv of a head from its group's pieces: a warp a (row, head), four columns a lane.
+template <typename T>
+__global__ void __launch_bounds__(256) attn_pieces_kernel(const Geo g, const Pieces p, const Heads<T> dk, const Heads<T> dv)
+{
+    const int lane = threadIdx.x & 31;
+    const long long all = p.rows * g.G;
+    blk::wait_previous();
+    for (long long i = blockIdx.x * 8ll + (threadIdx.x >> 5); i < all; i += gridDim.x * 8ll) {
+        const long long r = i / g.G, tok = r % g.N;
+        const int h = (int)(i - r * g.G), b = (int)(r / g.N);
+        if (g.offsets ? tok < max(g.offsets[0], 0) || tok >= g.offsets[g.B] : tok >= blk::row_length(g.lengths, b, g.N)) continue;
+        auto sum = [&](const float *at, int pitch, int width, float f, T *out) {
+            if (4 * lane >= width) return;
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = 0; k < p.count; ++k) {
+                const float4 x = *reinterpret_cast<const float4 *>(at + p.at(k, h, r) * pitch + 4 * lane);
+                s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+            }
+            const float y[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                if (4 * lane + c < width) out[4 * lane + c] = from_f32<T>(y[c] * f);
+        };
+        sum(p.k, p.k_pitch, g.d, g.scale, dk.at(b, tok, h));
+        sum(p.v, p.v_pitch, g.dv, 1.f, dv.at(b, tok, h));
+    }
+}
+
 // The new tokens' keys and values into their slots: a warp a (token, head), both tensors.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) attn_append_kernel(const Geo g, const Heads<const T> k, const Heads<const T> v, const Heads<T> kp,
@@ -571,6 +599,52 @@ gma_status_t launch_join(const gma_attn_t &a, const Geo &g, const Plan &p, void 
         GMA_LAUNCH(KID_ATTN_JOIN, st, launch_pdl(attn_join_kernel<bf16>, blocks, 256, 0, st, g, head, join, parts, heads_of<bf16>(a.o), a.lse, p.pack));
     else
         GMA_LAUNCH(KID_ATTN_JOIN, st, launch_pdl(attn_join_kernel<float>, blocks, 256, 0, st, g, head, join, parts, heads_of<float>(a.o), a.lse, p.pack));
+    return GMA_OK;
+}
+
+// An estimate of the time in steps, by sequences of equal length: the longest block's, or an SM's share of this kernel's and dq's (three quarters of
+// it), whose blocks fill the gaps; pieces add the sums' stores and loads and a launch.  us of a backward pass without and with pieces, bf16, causal:
+// 1 x 2048 x 16 heads of 128 over 2 187 and 75, 1 x 4096 x 16 of 64 over 1 574 and 142, 1 x 8192 x 16 of 128 over 2 851 and 606,
+// 1 x 4096 x 16 of 128 over 4 233 and 194, fp32 5 x 200 x 4 of 48 over 2 60 and 39; not taken for 1 x 2048 x 16 of 128 over 8: 67 and 81.
+PiecePlan plan_pieces(const gma_attn_t &a, int tile, int step, double step_us, Carve *ws)
+{
+    const int group = a.H / a.G;
+    const long long rows = batches(a) * a.N, n = a.offsets ? (a.N + a.B - 1) / a.B : a.N, tiles = (n + tile - 1) / tile * a.B * a.G;
+    const double steps = (double)((n + step - 1) / step), longest = steps * group;
+    const double share = 1.75 * (a.flags & GMA_ATTN_CAUSAL ? (steps + 1) / 2 : steps) * group * tiles / SMS;
+    const int width = ((a.d + 3) & ~3) + ((a.dv + 3) & ~3);
+    PiecePlan p = {1, 0, 0};
+    double best = std::max(longest, share) + 2;
+    for (int c = 2; c <= std::min(group, 64); ++c) {
+        if (group % c) continue;
+        const double time = std::max(longest / c + 2, share + (tiles * c > SMS ? longest / c / 24 : 0.)) +
+                            (6 + (double)(rows * a.G * c * width) * 8 / 3e6) / step_us;
+        if (time < best) {
+            best = time;
+            p.count = c;
+        }
+    }
+    if (p.count == 1) return p;
+    p.k_at = ws->take((size_t)p.count * a.G * rows * ((a.d + 3) & ~3) * sizeof(float));
+    p.v_at = ws->take((size_t)p.count * a.G * rows * ((a.dv + 3) & ~3) * sizeof(float));
+    return p;
+}
+
+Pieces pieces_of(const PiecePlan &p, const gma_attn_t &a, void *ws)
+{
+    return Pieces{p.count, (float *)((char *)ws + p.k_at), (float *)((char *)ws + p.v_at), (a.d + 3) & ~3, (a.dv + 3) & ~3, a.G, batches(a) * a.N};
+}
+
+gma_status_t launch_pieces(const gma_attn_grad_t &g, const Pieces &p, cudaStream_t st)
+{
+    if (p.count == 1) return GMA_OK;
+    const gma_attn_t &a = g.fwd;
+    const Geo geo = geo_of(a, nullptr);
+    const unsigned blocks = row_blocks(p.rows * a.G);
+    if (a.dtype == GMA_BF16)
+        GMA_LAUNCH(KID_ATTN_PIECES, st, launch_pdl(attn_pieces_kernel<bf16>, blocks, 256, 0, st, geo, p, heads_of<bf16>(g.dk), heads_of<bf16>(g.dv)));
+    else
+        GMA_LAUNCH(KID_ATTN_PIECES, st, launch_pdl(attn_pieces_kernel<float>, blocks, 256, 0, st, geo, p, heads_of<float>(g.dk), heads_of<float>(g.dv)));
     return GMA_OK;
 }
 

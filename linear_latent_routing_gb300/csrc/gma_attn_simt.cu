@@ -35,6 +35,7 @@ template <typename T> struct Args {
     Heads<const T> d_o;
     Heads<T> dq, dk, dv;
     const float *stat_lse, *delta;
+    Pieces pieces;
 };
 
 constexpr __host__ __device__ int pitch_of(int width) { return (width + 3) / 4 * 4 + 4; }
@@ -318,7 +319,7 @@ template <typename T, bool VEC> __global__ void __launch_bounds__(TH, 1) attn_si
     }
 }
 
-// dk and dv of 32 keys of one head, over the query heads of its group and the rows that see them: rows of the
+// dk and dv of 32 keys of one head, over the query heads of its group (or of a piece of it) and the rows that see them: rows of the
 // tiles are keys here, columns queries.
 template <typename T, bool VEC> __global__ void __launch_bounds__(TH, 1) attn_simt_dkv_kernel(const Args<T> a)
 {
@@ -327,7 +328,7 @@ template <typename T, bool VEC> __global__ void __launch_bounds__(TH, 1) attn_si
     __shared__ float lse2[2][KT], delta[2][KT];
     blk::wait_previous();
     blk::let_next();       // what this kernel reads, the next one reads too: dq's blocks take the SMs that these leave
-    const int rank = blockIdx.x / a.heads, kvh = blockIdx.x % a.heads;
+    const int parts = a.pieces.count, rank = blockIdx.x / a.heads, at_head = blockIdx.x - rank * a.heads, kvh = at_head / parts, piece = at_head - kvh * parts;
     const Geo &g = a.g;
     const Item it = load_item(a.items + rank);
     if (rank >= a.head->items) return;
@@ -359,8 +360,8 @@ template <typename T, bool VEC> __global__ void __launch_bounds__(TH, 1) attn_si
     for (int i = 0; i < RI; ++i)
 #pragma unroll
         for (int c = 0; c < 8; ++c) dk[i][c] = dv[i][c] = 0.f;
-    int h = kvh * g.group, q0 = first;
-    const int heads_end = h + g.group;
+    int h = kvh * g.group + piece * (g.group / parts), q0 = first;
+    const int heads_end = h + g.group / parts;
     load(h, q0, 0);
     copies_commit();
     for (int at = 0; h < heads_end; at ^= 1) {
@@ -399,6 +400,17 @@ template <typename T, bool VEC> __global__ void __launch_bounds__(TH, 1) attn_si
     for (int i = 0; i < RI; ++i) {
         const int r = RI * ty + i;
         if (r >= rows) continue;
+        if (parts > 1) {
+            const long long row = (long long)s.b * g.N + s.row0 + it.tok0 + r;
+            float *k = a.pieces.k_at(piece, kvh, row), *v = a.pieces.v_at(piece, kvh, row);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                const int col = 64 * (c >> 2) + 4 * tx + (c & 3);
+                if (col < g.d) k[col] = dk[i][c];
+                if (col < g.dv) v[col] = dv[i][c];
+            }
+            continue;
+        }
         T *k = a.dk.at(s.b, s.row0 + it.tok0 + r, kvh), *v = a.dv.at(s.b, s.row0 + it.tok0 + r, kvh);
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
@@ -480,6 +492,7 @@ gma_status_t forward(const gma_attn_t &a, const gma_attn_paged_t *paged, void *w
 
 struct GradPlan {
     Plan q, k;
+    PiecePlan pieces;
     size_t delta_at;
 };
 
@@ -488,7 +501,8 @@ GradPlan grad_plan(const gma_attn_t &a, Carve *c)
     GradPlan p;
     p.q = make_plan(a, 1, BR, BR, 6, SMS, false, c);
     gma_attn_t by = a;
-    by.H = a.G;                       // a tile of keys serves the whole group
+    p.pieces = plan_pieces(a, BR, KT, 5., c);
+    by.H = a.G * p.pieces.count;      // a tile of keys serves the group or a piece of it
     p.k = make_plan(by, 1, BR, BR, 6, SMS, false, c);
     p.k.by_keys = true;
     p.delta_at = c->take((size_t)(a.offsets ? 1 : a.B) * a.H * a.N * sizeof(float));
@@ -508,6 +522,7 @@ template <typename T, bool VEC> gma_status_t backward(const gma_attn_grad_t &g, 
     x.delta = delta;
     Args<T> y = x;
     y.heads = p.k.heads;
+    y.pieces = pieces_of(p.pieces, a, ws);
     y.head = (const PlanHead *)((char *)ws + p.k.head_at);
     y.items = (const Item *)((char *)ws + p.k.items_at);
     const PlanArgs first = plan_args(x.g, p.q, ws);
@@ -521,7 +536,7 @@ template <typename T, bool VEC> gma_status_t backward(const gma_attn_grad_t &g, 
     const size_t tiles = (size_t)(BR + 2 * KT) * both * sizeof(float), square = BR * (KT + 4) * sizeof(float);
     GMA_LAUNCH(KID_ATTN_SIMT_DKV, st, launch_pdl(attn_simt_dkv_kernel<T, VEC>, (unsigned)p.k.max_items * p.k.heads, TH, tiles + 2 * square, st, y));
     GMA_LAUNCH(KID_ATTN_SIMT_DQ, st, launch_pdl(attn_simt_dq_kernel<T, VEC>, (unsigned)p.q.max_items * p.q.heads, TH, tiles + square, st, x));
-    return GMA_OK;
+    return launch_pieces(g, y.pieces, st);
 }
 
 }  // namespace

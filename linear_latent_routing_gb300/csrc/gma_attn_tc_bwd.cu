@@ -4,7 +4,8 @@
 // (dq): seven products of a tile instead of five, but every sum is one block's in one order, without atomics and without an
 // fp32 copy of dq, so that repeated calls give the same bits.
 //
-// dk, dv: a block owns 128 keys of one key head and walks over the query tiles that see them, of every query head of the group.
+// dk, dv: a block owns 128 keys of one key head and walks over the query tiles that see them, of every query head of the group or, where that
+// leaves SMs without work, of a piece of it.
 //   S^T = K Q^T - lse / scale, dP^T = V dO^T - delta, P^T = exp(scale S^T), dS^T = P^T dP^T, dV += P^T dO, dK += dS^T Q.
 // lse and delta belong to the columns here.  Read from shared memory they doubled the time of the exponentials (whose loads wait behind the
 // products'); so they are a k-step of the products, in three bf16 terms each.
@@ -41,6 +42,7 @@ struct GradArgs {
     WsHeader *hdr;
     int q_boxes, v_boxes;
     int stages, k_slots, v_slots; // of the two kernels' rings
+    Pieces pieces;
     int withhold;                 // GMA_FLAG_TEST_WITHHOLD: a block's own tiles are never loaded
 };
 
@@ -112,12 +114,13 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dkv_kernel(const GradArgs a, 
     blk::wait_previous();
     blk::let_next();       // what this kernel reads, the next one reads too: dq's blocks take the SMs that these leave
     const Geo &g = a.g;
-    const int rank = blockIdx.x / g.G, kvh = blockIdx.x % g.G;
+    const int parts = a.pieces.count, rank = blockIdx.x / (g.G * parts), at = blockIdx.x - rank * g.G * parts;
+    const int kvh = at / parts, piece = at - kvh * parts, heads = g.group / parts;
     if (rank >= a.k_head->items) return;
     if (warp == 8) tmem_alloc(&bars->tmem, 512);
     const Item it = load_item(a.k_items + rank);
     const Seq sq = it.sq;
-    const int tiles = __shfl_sync(~0u, it.t1 - it.t0, 0), steps = tiles * g.group;
+    const int tiles = __shfl_sync(~0u, it.t1 - it.t0, 0), steps = tiles * heads;
     for (int i = t; i < TILE; i += THREADS) {
         *reinterpret_cast<uint4 *>(ones + i * 32 + (((i >> 2) & 1) << 4)) = make_uint4(0x3f803f80u, 0x3f80u, 0, 0);
         *reinterpret_cast<uint4 *>(ones + i * 32 + ((((i >> 2) & 1) ^ 1) << 4)) = make_uint4(0, 0, 0, 0);
@@ -215,7 +218,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dkv_kernel(const GradArgs a, 
         int issued_q = 0, issued_o = 0;
         RingPos r{0, 1};
         const float inv_scale = 1.f / g.scale;
-        int h = kvh * g.group, j = 0;
+        int h = kvh * g.group + piece * heads, j = 0;
         for (int i = 0; ok && i < steps; ++i) {
             const int q0 = (it.t0 + j) * TILE, s = r.s;
             const uint32_t free = r.turn;
@@ -320,7 +323,11 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dkv_kernel(const GradArgs a, 
             tc_fence_after();
             const bool valid = key < sq.n;
             const int r = sq.row0 + (valid ? key : it.tok0);
-            if (w == 0) store_row(tmem + lanes + 256, g.dv, 1.f, valid, a.dv.at(sq.b, r, kvh), a.v_vec);
+            if (parts > 1) {
+                const long long at = (long long)sq.b * g.N + r;
+                if (w == 0) store_row_f32(tmem + lanes + 256, g.dv, valid, a.pieces.v_at(piece, kvh, at));
+                else store_row_f32(tmem + lanes + 384, g.d, valid, a.pieces.k_at(piece, kvh, at));
+            } else if (w == 0) store_row(tmem + lanes + 256, g.dv, 1.f, valid, a.dv.at(sq.b, r, kvh), a.v_vec);
             else store_row(tmem + lanes + 384, g.d, g.scale, valid, a.dk.at(sq.b, r, kvh), a.k_vec);
         }
     }
@@ -553,6 +560,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dq_kernel(const GradArgs a, c
 
 struct GradPlan {
     Plan q, k;
+    PiecePlan pieces;
     size_t delta_at;
 };
 
@@ -561,7 +569,8 @@ GradPlan grad_plan(const gma_attn_t &a, Carve *c)
     GradPlan p;
     p.q = make_plan(a, 1, TILE, TILE, 7, SMS, false, c);
     gma_attn_t by = a;
-    by.H = a.G;                       // a tile of keys serves the whole group
+    p.pieces = plan_pieces(a, TILE, TILE, 1.5, c);
+    by.H = a.G * p.pieces.count;      // a tile of keys serves the group or a piece of it
     p.k = make_plan(by, 1, TILE, TILE, 7, SMS, false, c);
     p.k.by_keys = true;
     p.delta_at = c->take((size_t)(a.offsets ? 1 : a.B) * a.H * a.N * sizeof(float));
@@ -605,6 +614,7 @@ gma_status_t tc_backward(const gma_attn_grad_t &g, void *ws, cudaStream_t st)
     x.v_vec = store_vec(g.dv, a.dv);
     x.hdr = (WsHeader *)ws;
     x.withhold = p.q.withhold;
+    x.pieces = pieces_of(p.pieces, a, ws);
     x.q_boxes = (a.d + 63) / 64;
     x.v_boxes = (a.dv + 63) / 64;
     const uint32_t pair = BOX * (uint32_t)(x.q_boxes + x.v_boxes), k_fixed = pair + EXTRA + 1024 + (uint32_t)sizeof(KeyBars),
@@ -631,9 +641,9 @@ gma_status_t tc_backward(const gma_attn_grad_t &g, void *ws, cudaStream_t st)
     if (cudaFuncSetAttribute(attn_dkv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_MAX) != cudaSuccess ||
         cudaFuncSetAttribute(attn_dq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_MAX) != cudaSuccess)
         return GMA_ERR_CUDA;
-    GMA_LAUNCH(KID_ATTN_DKV, st, launch_pdl(attn_dkv_kernel, (unsigned)p.k.max_items * a.G, THREADS, k_fixed + x.stages * k_stage, st, x, qm, km, vm, om));
+    GMA_LAUNCH(KID_ATTN_DKV, st, launch_pdl(attn_dkv_kernel, (unsigned)p.k.max_items * p.k.heads, THREADS, k_fixed + x.stages * k_stage, st, x, qm, km, vm, om));
     GMA_LAUNCH(KID_ATTN_DQ, st, launch_pdl(attn_dq_kernel, (unsigned)p.q.max_items * a.H, THREADS, q_fixed + q_ring, st, x, qm, km, vm, om));
-    return GMA_OK;
+    return launch_pieces(g, x.pieces, st);
 }
 
 }  // namespace att

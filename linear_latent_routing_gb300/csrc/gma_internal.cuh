@@ -74,7 +74,7 @@ enum KernelId {
     KID_SCAN = 64, KID_SCAN_STEP, KID_SCAN_BWD, KID_SCAN_BC, KID_CONV, KID_CONV_STEP, KID_CONV_BWD, KID_NORM,
     KID_NORM_BWD, KID_SUM_ROWS, KID_SCAN_STATE, KID_SCAN_JOIN, KID_SCAN_ADJ,
     KID_ATTN_PLAN = 80, KID_ATTN, KID_ATTN_DKV, KID_ATTN_DQ, KID_ATTN_SIMT, KID_ATTN_SIMT_DKV, KID_ATTN_SIMT_DQ, KID_ATTN_DELTA,
-    KID_ATTN_APPEND, KID_ATTN_REPACK, KID_ATTN_JOIN, KID_COUNT
+    KID_ATTN_APPEND, KID_ATTN_REPACK, KID_ATTN_JOIN, KID_ATTN_PIECES, KID_COUNT
 };
 const char *kernel_name(int id);
 void timing_begin(cudaStream_t st, int kernel_id);

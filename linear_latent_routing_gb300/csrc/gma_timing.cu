@@ -82,6 +82,7 @@ const char *kernel_name(int id)
     case KID_ATTN_APPEND: return "attn_append";
     case KID_ATTN_REPACK: return "attn_repack";
     case KID_ATTN_JOIN: return "attn_join";
+    case KID_ATTN_PIECES: return "attn_sum_pieces";
     }
     return "unknown";
 }

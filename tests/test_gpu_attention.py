@@ -126,6 +126,29 @@ def test_prompt_backward(case):
             R.check(rows(g[name], i), w, f"d{name} of sequence {i}")
 
 
+@pytest.mark.parametrize("case", [
+    ([300, 129, 0, 41], 12, 1, 64, 128, "bf16", True, "padded"),
+    ([260, 1, 77], 14, 2, 117, 50, "bf16", False, "packed"),
+    ([40, 9], 45, 3, 21, 36, "bf16", True, "padded"),
+    ([65, 33, 2], 64, 1, 40, 24, "f32", True, "packed"),
+    ([100], 13, 1, 128, 72, "f32", False, "plain"),
+], ids=_id)
+def test_gradients_of_widely_shared_heads(case):
+    """Many query heads a key head: few tiles of keys, each of whose sums is many heads'.  Repeated calls give the same bits."""
+    q, k, v, do, how, rows = _prompt(case, 14, extra=5 if case[7] == "packed" else 0)
+    lse = A().prompt_lse(q).fill_(float("nan"))
+    o = A().prompt(q, k, v, lse=lse, **how)
+    g = A().prompt_backward(do, q, k, v, o, lse, check=True, **how)
+    for i in range(len(case[0])):
+        want = R.attend(rows(q, i), rows(k, i), rows(v, i), how["scale"], 0, how["causal"], do=rows(do, i), T=TYPES[case[5]])
+        for name, w in zip("qkv", want[2:]):
+            R.check(rows(g[name], i), w, f"d{name} of sequence {i}")
+    again = A().prompt_backward(do, q, k, v, o, lse, out={"k": torch.full_like(g["k"], 3), "v": torch.full_like(g["v"], 3)}, **how)
+    for name in "qkv":
+        for i in range(len(case[0])):
+            assert torch.equal(rows(again[name], i), rows(g[name], i)), name
+
+
 @pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 20), ("f32", 24)])
 def test_gradients_against_differences(dtype, d):
     """The gradients against central differences of the forward pass in 64 bits along random directions."""
