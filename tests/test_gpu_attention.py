@@ -149,6 +149,25 @@ def test_gradients_of_widely_shared_heads(case):
             assert torch.equal(rows(again[name], i), rows(g[name], i)), name
 
 
+@pytest.mark.parametrize("case", [
+    ([3001], 1, 1, 64, 64, "bf16", True, "plain"),
+    ([2047, 1300], 3, 1, 128, 64, "bf16", False, "padded"),
+    ([1500, 0, 2, 1111], 4, 2, 96, 128, "bf16", True, "packed"),
+    ([1100], 8, 8, 63, 30, "bf16", True, "mixer"),
+], ids=_id)
+def test_long_prompts_of_few_heads(case):
+    """Fewer tiles than SMs, each over many keys.  Repeated calls give the same bits."""
+    q, k, v, _, how, rows = _prompt(case, 15)
+    lse = A().prompt_lse(q).fill_(float("nan"))
+    o = A().prompt(q, k, v, lse=lse, check=True, **how)
+    for i in range(len(case[0])):
+        want, stat = R.attend(rows(q, i), rows(k, i), rows(v, i), how["scale"], 0, how["causal"], T=TYPES[case[5]])
+        R.check(rows(o, i), want, f"o of sequence {i}")
+        R.check(_stat_rows(lse, rows, i, case), stat, f"lse of sequence {i}")
+    again = A().prompt(q, k, v, **how)
+    assert all(torch.equal(rows(again, i), rows(o, i)) for i in range(len(case[0])))
+
+
 @pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 20), ("f32", 24)])
 def test_gradients_against_differences(dtype, d):
     """The gradients against central differences of the forward pass in 64 bits along random directions."""
