@@ -531,6 +531,61 @@ def test_streams_and_graphs():
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_graphs_whose_calls_follow_copies_and_joins(dtype):
+    """Calls captured as a graph's first node, behind a copy, behind two streams that meet, and behind append; replayed with new inputs."""
+    r = _draw(16)
+    B, H, G, d, page, P = 3, 4, 2, 64, 16, 20
+    q, k, v, do = r(B, 90, H, d, dtype=dtype), r(B, 90, G, d, dtype=dtype), r(B, 90, G, d, dtype=dtype), r(B, 90, H, d, dtype=dtype)
+    kp, vp, q1, k1, v1 = (r(*s, d, dtype=dtype) for s in ((B * P, page, G), (B * P, page, G), (B, H), (B, G), (B, G)))
+    table, total = torch.randperm(B * P, device="cuda").int().view(B, P), _ints([5, 300, 161])
+    new = [torch.empty_like(t) for t in (q, q1, k1)]
+    side = torch.cuda.Stream()
+
+    def run(fresh):
+        lse = A().prompt_lse(q)
+        o = A().prompt(q, k, v, lse=lse)                              # a first node
+        for t, f in zip((q, q1, k1), fresh):
+            t.copy_(f)
+        o1 = A().paged(q1, kp, vp, table, total)                      # behind copies
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        o2 = A().prompt(q, k, v, lse=lse)
+        A().append(k1, v1, kp, vp, table, total, stream=side)
+        o3 = A().paged(q1, kp, vp, table, total, stream=side)         # behind append
+        main.wait_stream(side)
+        g = A().prompt_backward(do, q, k, v, o2, lse)                 # behind both
+        o4 = A().paged(q1, kp, vp, table, total)
+        o3.record_stream(main)
+        return [o, o1, o2, o3, o4, g["q"], g["k"], g["v"]]
+
+    start = [t.clone() for t in (q, q1, k1, kp, vp)]
+
+    def again():
+        for t, x in zip((q, q1, k1, kp, vp), start):
+            t.copy_(x)
+        for t in new:
+            t.copy_(r(*t.shape, dtype=dtype))
+        torch.cuda.synchronize()
+
+    again()
+    run(new)                                                          # warm
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = run(new)
+    for _ in range(2):
+        again()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in outs]
+        for t, x in zip((q, q1, k1, kp, vp), start):
+            t.copy_(x)
+        want = run(new)
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
 def test_more_sequences_than_blocks():
     """Many short sequences, packed: more tiles than the GPU has SMs, and sequences without tokens between them."""
     n = [(7 * i) % 19 for i in range(1500)]
