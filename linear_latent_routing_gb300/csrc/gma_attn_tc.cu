@@ -404,7 +404,9 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const TcArgs a, con
 #pragma unroll
                         for (int c = 0; c < 4; ++c) x[c] = max3(x[c], __uint_as_float(r[c][e]), __uint_as_float(r[c][e + 1]));
                     }
-                    const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * g.sl2;
+                    // (a row that does not exist holds the next sequence's queries, or what was left in shared memory: it must not move the
+                    // others' maximum, by which their probabilities are rounded)
+                    const float top = valid ? fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * g.sl2 : -INFINITY;
                     // the maximum that the exponentials are relative to moves rarely, and with it what was summed up so far
                     if (__any_sync(~0u, top > m + GROW)) {
                         const float now = fmaxf(m, top), f = now == -INFINITY ? 1.f : ex2(m - now);

@@ -770,3 +770,68 @@ def test_two_host_threads():
         t.join()
     for i in range(2):
         assert all(torch.equal(x, want[i]) for x in got[i])
+
+
+# ------------------------------------------------------------------ rows that are not the call's
+
+def _grow(k, by):
+    """Keys whose scores grow along the sequence, so that a row's maximum keeps moving a little."""
+    n = torch.arange(k.shape[-3], device="cuda") / by + 1
+    return k.mul_(n[:, None, None].to(k.dtype))
+
+
+@pytest.mark.parametrize("case", [
+    ([700, 31, 900], 4, 2, 64, 64, "bf16", True, "packed"),
+    ([333, 60, 500], 3, 1, 128, 64, "bf16", False, "packed"),
+    ([1100, 620], 2, 1, 64, 128, "bf16", False, "padded"),
+    ([1000, 75], 4, 4, 128, 128, "bf16", True, "padded"),
+    ([411, 500], 3, 1, 30, 63, "bf16", True, "padded"),
+    ([200, 64, 63], 6, 3, 40, 40, "f32", True, "packed"),
+], ids=_id)
+def test_rows_of_others_do_not_round_a_sequence(case):
+    """Behind a sequence's last row lie the next one's, or rows of no sequence.  Whatever their values, finite and large ones too,
+    the sequence's results keep their bits."""
+    packed = case[7] == "packed"
+    kept = [0] if packed else range(len(case[0]))
+    got = []
+    for other in (0.0, 60.0, "infinities"):
+        q, k, v, do, how, rows = _prompt(case, 18, extra=40)
+        _grow(k, 1500)
+        used = torch.zeros(q.shape[:-2], dtype=torch.bool, device="cuda")
+        for i in kept:
+            rows(used, i).fill_(True)
+        r = _draw(19)
+        for t in (q, k, v, do):
+            x = r(*t.shape, dtype=case[5], std=1.0 if other == "infinities" else other)
+            if other == "infinities":
+                x[..., ::5] = float("inf")
+            t[~used] = x[~used]
+        lse = A().prompt_lse(q)
+        o = A().prompt(q, k, v, lse=lse, check=True, **how)
+        g = A().prompt_backward(do, q, k, v, o, lse, check=True, **how)
+        got.append([rows(t, i).clone() for i in kept for t in (o, lse.transpose(-1, -2), g["q"], g["k"], g["v"])])
+    for x in got[1:]:
+        for a, b in zip(got[0], x):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("H,G,N,d", [(12, 4, 1500, 64), (10, 2, 2000, 64), (14, 2, 700, 128), (12, 1, 33, 64), (3, 1, 1, 64), (24, 2, 10, 128)])
+def test_groups_that_do_not_divide_a_tile_repeat_bits(H, G, N, d):
+    """Tiles of 128 rows hold 126, 125, 120 of such groups.  What other calls left where the rest would lie changes no bit."""
+    case = ([N, max(N // 3, 1)], [4500, 1900], H, G, d, 64, "bf16", 32, "packed")
+    q, _, _, kp, vp, table, lengths, how, rows = _paged(case, 20)
+    for b, L in enumerate(case[1]):
+        for j in range(0, L, 32):
+            kp[table[b, j // 32]] *= 1 + j / 3000
+    r = _draw(21)
+    got = []
+    for std in (0.0, 60.0, 1e4):
+        x, y = r(8, 1024, 16, d, std=std), r(8, 1024, 16, d)
+        A().prompt(x, y, y)                                        # every SM's query tiles, full
+        lse = torch.full((H, q.shape[0]), float("nan"), device="cuda")
+        got.append([A().paged(q, kp, vp, table, lengths, lse=lse, check=True, **how), lse])
+    for x in got[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(got[0], x))
+    for b, (n, L) in enumerate(zip(*case[:2])):
+        ref, _ = R.attend(rows(q, b), _cached(kp, table, b, L), _cached(vp, table, b, L), d ** -0.5, L - n)
+        R.check(rows(got[0][0], b), ref, f"o of sequence {b}")
