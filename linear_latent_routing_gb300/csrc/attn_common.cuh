@@ -71,14 +71,17 @@ __device__ __forceinline__ Seq sequence(const Geo &g, int s)
     return q;
 }
 
-// Zeros in the rows of [rows][heads * width] that belong to no sequence, by warp `first` of `warps`; `vec`: 16 bytes at a time.
+// Zeros in the rows of [rows][heads * width] that belong to no sequence, by warp `first` of `warps` (64 bits: a grid may have 2^31 blocks);
+// `vec`: 16 bytes at a time.
 template <typename T>
-__device__ __forceinline__ void zero_dead_rows(const Geo &g, const Heads<T> &x, int heads, int width, int rows, int first, int warps, bool vec)
+__device__ __forceinline__ void zero_dead_rows(const Geo &g, const Heads<T> &x, int heads, int width, int rows, long long first, long long warps,
+                                               bool vec)
 {
     constexpr int E = 16 / sizeof(T);
     const int lane = threadIdx.x & 31, a = g.offsets ? max(g.offsets[0], 0) : 0, e = g.offsets ? g.offsets[g.B] : 0;
     const int step = vec ? E : 1, each = width / step, all = heads * each;
-    for (int r = first; r < rows; r += warps) {
+    for (long long at_row = first; at_row < rows; at_row += warps) {
+        const int r = (int)at_row;
         int b = 0, i = r;
         if (g.offsets) {
             if (r >= a && r < e) continue;

@@ -118,7 +118,8 @@ __global__ void __launch_bounds__(TH, 1) attn_simt_kernel(const Args<T> a)
     constexpr int RI = R / 16;
     extern __shared__ __align__(16) float smem[];
     // beside the plan (no other kernel's results are read or written here)
-    if (a.zero_rows) zero_dead_rows(a.g, a.o, a.g.H, a.g.dv, a.zero_rows, blockIdx.x * (TH / 32) + (threadIdx.x >> 5), gridDim.x * (TH / 32), a.o_vec);
+    if (a.zero_rows)
+        zero_dead_rows(a.g, a.o, a.g.H, a.g.dv, a.zero_rows, blockIdx.x * (TH / 32ll) + (threadIdx.x >> 5), gridDim.x * (TH / 32ll), a.o_vec);
     blk::wait_previous();
     if (PAGED) blk::let_next();
     const int rank = blockIdx.x / a.heads, head = blockIdx.x % a.heads;

@@ -835,3 +835,19 @@ def test_groups_that_do_not_divide_a_tile_repeat_bits(H, G, N, d):
     for b, (n, L) in enumerate(zip(*case[:2])):
         ref, _ = R.attend(rows(q, b), _cached(kp, table, b, L), _cached(vp, table, b, L), d ** -0.5, L - n)
         R.check(rows(got[0][0], b), ref, f"o of sequence {b}")
+
+
+# ------------------------------------------------------------------ the largest sizes
+
+def test_the_most_blocks():
+    """The largest batch of one token each with the most heads, mostly padding: 2^28 blocks and more, eight warps each."""
+    B, H = 65535, 4096
+    r = _draw(22)
+    q, k, v = r(B, 1, H, 1, dtype="f32"), r(B, 1, 1, 1, dtype="f32"), r(B, 1, 1, 1, dtype="f32")
+    lengths = torch.zeros(B, dtype=torch.int32, device="cuda")
+    lengths[::97] = 1
+    lengths[-1] = 1
+    filled = torch.full((B, 1, H, 1), 7.0, device="cuda")              # the block that the output takes next
+    del filled
+    o = A().prompt(q, k, v, lengths=lengths, check=True)
+    assert torch.equal(o, (v * lengths[:, None, None, None]).expand_as(o))
