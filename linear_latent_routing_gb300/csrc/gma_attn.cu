@@ -684,7 +684,7 @@ struct Packed {
     size_t bytes;
 };
 
-Packed pack_places(const gma_attn_t &a, size_t at, void *ws)
+Packed pack_places(const gma_attn_t &a, bool grad, size_t at, void *ws)
 {
     Packed p = {};
     const int64_t rows = batches(a) * a.N;
@@ -698,7 +698,7 @@ Packed pack_places(const gma_attn_t &a, size_t at, void *ws)
     p.q = take(a.H, a.d);
     p.k = take(a.G, a.d);
     p.v = take(a.G, a.dv);
-    p.d_o = take(a.H, a.dv);
+    if (grad) p.d_o = take(a.H, a.dv);
     p.bytes = off;
     return p;
 }
@@ -755,7 +755,7 @@ size_t gma_attn_workspace_size(const gma_attn_t *a)
 {
     if (check(a, true) != GMA_OK) return 0;
     if (tc_takes(*a, nullptr)) return tc_workspace(*a, nullptr);
-    return repacks(*a) ? pack_places(*a, tc_workspace(*a, nullptr), nullptr).bytes : simt_workspace(*a, nullptr);
+    return repacks(*a) ? pack_places(*a, false, tc_workspace(*a, nullptr), nullptr).bytes : simt_workspace(*a, nullptr);
 }
 
 gma_status_t gma_attn_forward(const gma_attn_t *a, void *ws, size_t ws_bytes, gma_stream_t stream)
@@ -767,7 +767,7 @@ gma_status_t gma_attn_forward(const gma_attn_t *a, void *ws, size_t ws_bytes, gm
     cudaStream_t st = (cudaStream_t)stream;
     if (tc_takes(*a, nullptr)) return tc_forward(*a, nullptr, ws, st);
     if (!repacks(*a)) return simt_forward(*a, nullptr, ws, st);
-    const Packed p = pack_places(*a, tc_workspace(*a, nullptr), ws);
+    const Packed p = pack_places(*a, false, tc_workspace(*a, nullptr), ws);
     if ((r = launch_repack(*a, nullptr, p, st)) != GMA_OK) return r;
     return tc_forward(with(*a, p), nullptr, ws, st);
 }
@@ -776,7 +776,7 @@ size_t gma_attn_backward_workspace_size(const gma_attn_grad_t *g)
 {
     if (check_grad(g) != GMA_OK) return 0;
     if (tc_takes_backward(*g)) return tc_backward_workspace(*g);
-    return repacks(g->fwd) ? pack_places(g->fwd, tc_backward_workspace(*g), nullptr).bytes : simt_backward_workspace(*g);
+    return repacks(g->fwd) ? pack_places(g->fwd, true, tc_backward_workspace(*g), nullptr).bytes : simt_backward_workspace(*g);
 }
 
 gma_status_t gma_attn_backward(const gma_attn_grad_t *g, void *ws, size_t ws_bytes, gma_stream_t stream)
@@ -789,7 +789,7 @@ gma_status_t gma_attn_backward(const gma_attn_grad_t *g, void *ws, size_t ws_byt
     const gma_attn_t &a = g->fwd;
     if (tc_takes_backward(*g)) return tc_backward(*g, ws, st);
     if (!repacks(a)) return simt_backward(*g, ws, st);
-    const Packed p = pack_places(a, tc_backward_workspace(*g), ws);
+    const Packed p = pack_places(a, true, tc_backward_workspace(*g), ws);
     if ((r = launch_repack(a, &g->d_o, p, st)) != GMA_OK) return r;
     gma_attn_grad_t packed = *g;
     packed.fwd = with(a, p);

@@ -124,6 +124,21 @@ def test_workspaces(lib):
         assert call(packed, FAKE, n - 1, None) == 4 and call(packed, FAKE + 16, n, None) == 4 and call(packed, None, n, None) == 4
 
 
+def test_copies_take_what_is_copied(lib):
+    """bf16 rows off 16-byte boundaries are copied to dense ones of 64 here: q, k and v in the forward pass, do too in the backward pass."""
+    B, N, H, G = 2, 1000, 4, 2
+    size = dict(B=B, N=N, H=H, G=G)
+    plain, odd = dict(size, d=64, dv=64), dict(size, d=63, dv=63)
+
+    def grads(w):
+        return dict(do=_heads(B, N, H, w), dq=_heads(B, N, H, w), dk=_heads(B, N, G, w), dv_=_heads(B, N, G, w))
+    dense, slack = 2 * B * N * 64, 5 * 256
+    more = lib.workspace(_forward(**odd)) - lib.workspace(_forward(**plain))
+    assert dense * (H + 2 * G) <= more <= dense * (H + 2 * G) + slack
+    more = lib.backward_workspace(_grad(**odd, **grads(63))) - lib.backward_workspace(_grad(**plain, **grads(64)))
+    assert dense * (2 * H + 2 * G) <= more <= dense * (2 * H + 2 * G) + slack
+
+
 def test_no_device(lib):
     if torch.cuda.is_available():
         pytest.skip("there is a device")
