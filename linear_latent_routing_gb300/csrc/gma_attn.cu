@@ -691,7 +691,7 @@ Packed pack_places(const gma_attn_t &a, bool grad, size_t at, void *ws)
     size_t off = align_up(at, 256);
     auto take = [&](int heads, int width) {
         const int64_t pitch = (width + 7) & ~7;
-        const gma_heads_t h = {(char *)ws + off, a.N * heads * pitch, heads * pitch, pitch};
+        const gma_heads_t h = {(char *)ws + off, a.N * (heads * pitch), heads * pitch, pitch};      // 64 bits from the first product on
         off = align_up(off + (size_t)(rows * heads * pitch) * sizeof(bf16), 256);
         return h;
     };

@@ -851,3 +851,23 @@ def test_the_most_blocks():
     del filled
     o = A().prompt(q, k, v, lengths=lengths, check=True)
     assert torch.equal(o, (v * lengths[:, None, None, None]).expand_as(o))
+
+
+def test_copied_rows_with_strides_beyond_32_bits():
+    """Rows off 16-byte boundaries whose copies' batch rows lie 2^31 heads apart: the largest padded batch of two, mostly padding."""
+    B, N, H, n = 2, 1 << 19, 4096, [70, 131]
+    r = _draw(23)
+    q, k, v = (torch.zeros(B, N, 1, 1, dtype=torch.bfloat16, device="cuda") for _ in range(3))
+    for t in (q, k, v):
+        for b in range(B):
+            t[b, :n[b]] = r(n[b], 1, 1)
+    torch.cuda.empty_cache()
+    out = torch.empty(B, N, H, 1, dtype=torch.bfloat16, device="cuda")
+    A().prompt(q.expand(B, N, H, 1), k, v, lengths=_ints(n), out=out, check=True)
+    for b in range(B):
+        ref, _ = R.attend(q[b, :n[b]], k[b, :n[b]], v[b, :n[b]], 1.0)
+        o = out[b, :n[b]]
+        R.check(o[:, :1], ref, f"o of sequence {b}")
+        assert (o == o[:, :1]).all()
+    del out
+    torch.cuda.empty_cache()
