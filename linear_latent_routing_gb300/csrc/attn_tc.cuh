@@ -75,8 +75,29 @@ __device__ __forceinline__ bool elect()
     return is != 0;
 }
 
+// Whole warps wait, and get one answer: every lane sees a barrier for itself, at a time of its own, and what follows (an elected lane's products,
+// shuffles, tensor memory) wants all of them on the same path.
+__device__ __forceinline__ bool bar_there(uint64_t *bar, uint32_t parity) { return __all_sync(~0u, mbar_test_wait(bar, parity)); }
+__device__ __forceinline__ bool aborted(volatile int *abort) { return __any_sync(~0u, *abort != 0); }
+
 // mbar_wait_abortable with a try that comes first and without the clock: most waits here are short or over, several of them a tile.
 __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, WsHeader *hdr, unsigned where, volatile int *abort)
+{
+    if (__all_sync(~0u, mbar_try_wait(bar, parity))) return true;
+    const long long t0 = clock64();
+    while (!__all_sync(~0u, mbar_try_wait(bar, parity))) {
+        if (aborted(abort)) return false;
+        if (__any_sync(~0u, wait_expired(clock64() - t0, hdr))) {
+            record_error(hdr, GMA_ERR_TIMEOUT, where);
+            *abort = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
+// The same for each lane by itself: for code that takes no branch by the answer before its lanes meet again.
+__device__ __forceinline__ bool lane_wait(uint64_t *bar, uint32_t parity, WsHeader *hdr, unsigned where, volatile int *abort)
 {
     if (mbar_try_wait(bar, parity)) return true;
     const long long t0 = clock64();

@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dkv_kernel(const GradArgs a, 
         if ((ok = ok && o_there())) dprobs();
         for (int i = 0; ok && i < steps; ++i) {
             const bool more = i + 1 < steps;
-            bool now = mbar_test_wait(&bars->p, i & 1), there = mbar_test_wait(&bars->fq[rs.s], rs.turn);
+            bool now = bar_there(&bars->p, i & 1), there = bar_there(&bars->fq[rs.s], rs.turn);
             if (!now && !(ok = bar_wait(&bars->p, i & 1, a.hdr, 223, abort))) break;
             tc_fence_after();
             if (elect()) {
@@ -187,8 +187,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dkv_kernel(const GradArgs a, 
                 if (!there && !(ok = q_there())) break;
                 scores();
             }
-            now = mbar_test_wait(&bars->ds, i & 1);
-            there = mbar_test_wait(&bars->fo[rp.s], rp.turn);
+            now = bar_there(&bars->ds, i & 1);
+            there = bar_there(&bars->fo[rp.s], rp.turn);
             if (!now && !(ok = bar_wait(&bars->ds, i & 1, a.hdr, 224, abort))) break;
             tc_fence_after();
             if (elect()) {
@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dkv_kernel(const GradArgs a, 
             rc.step(1, a.stages);
         }
         if (ok && elect()) mma_commit(&bars->done);
-        if (*abort) {
+        if (aborted(abort)) {
             if (elect()) mma_commit(&bars->drain);
             mbar_wait(&bars->drain, 0, a.hdr, 225);
         }
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dkv_kernel(const GradArgs a, 
                 ++h;
             }
         }
-        if (*abort) {          // loads that no product waited for
+        if (aborted(abort)) {          // loads that no product waited for
             mbar_wait(&bars->kv, 0, a.hdr, 228);
             for (int i = issued_q > a.stages ? issued_q - a.stages : 0; i < issued_q; ++i)
                 mbar_wait(&bars->fq[i % a.stages], (uint32_t)(i / a.stages) & 1u, a.hdr, 229);
@@ -431,9 +431,9 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dq_kernel(const GradArgs a, c
         // cycles to find that it is through, and this warp's time bounds the loop (4 x 4096 x 16 heads of 64: 268 -> 252 us)
         for (int j = 0; ok && j < tiles; ++j) {
             const bool more = j + 1 < tiles, after = j + 2 < tiles;
-            const bool now = mbar_test_wait(&bars->ds, j & 1);
-            const bool v_there = !more || mbar_test_wait(&bars->fv[rv.s], rv.turn);
-            const bool k_there = !after || mbar_test_wait(&bars->fk[rk.s], rk.turn);
+            const bool now = bar_there(&bars->ds, j & 1);
+            const bool v_there = !more || bar_there(&bars->fv[rv.s], rv.turn);
+            const bool k_there = !after || bar_there(&bars->fk[rk.s], rk.turn);
             if (!v_there && !(ok = values())) break;
             if (!now && !(ok = bar_wait(&bars->ds, j & 1, a.hdr, 242, abort))) break;
             tc_fence_after();
@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dq_kernel(const GradArgs a, c
             if (after) rk.step(1, a.k_slots);
         }
         if (ok && elect()) mma_commit(&bars->done);
-        if (*abort) {
+        if (aborted(abort)) {
             if (elect()) mma_commit(&bars->drain);
             mbar_wait(&bars->drain, 0, a.hdr, 243);
         }
@@ -488,7 +488,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_dq_kernel(const GradArgs a, c
             ++values;
             rv.step(1, a.v_slots);
         }
-        if (*abort) {
+        if (aborted(abort)) {
             mbar_wait(&bars->q, 0, a.hdr, 245);
             for (int c = keys > a.k_slots ? keys - a.k_slots : 0; c < keys; ++c)
                 mbar_wait(&bars->fk[c % a.k_slots], (uint32_t)(c / a.k_slots) & 1u, a.hdr, 246);

@@ -871,3 +871,76 @@ def test_copied_rows_with_strides_beyond_32_bits():
         assert (o == o[:, :1]).all()
     del out
     torch.cuda.empty_cache()
+
+
+# ------------------------------------------------------------------ waits
+
+@pytest.mark.parametrize("which,N,H,G,d,dv,seqs", [
+    ("forward", 100, 4, 4, 128, 128, 1),           # both streams on the same rows
+    ("forward", 1000, 16, 2, 128, 64, 3),          # more items than blocks take at a time
+    ("forward", 700, 5, 1, 32, 128, 8),
+    ("paged", 1, 16, 2, 128, 128, 40),
+    ("paged", 300, 6, 2, 64, 128, 4),
+    ("backward", 1, 1, 1, 64, 64, 1),
+    ("backward", 130, 4, 1, 128, 128, 2),
+    ("backward", 900, 16, 16, 64, 64, 3),
+    ("backward", 513, 8, 2, 128, 40, 2),
+])
+def test_waits_give_up_together(which, N, H, G, d, dv, seqs):
+    """A load that never comes, in every shape of the kernels' loops: the lanes of a warp leave a wait with one answer, the warps one
+    after another, and the next calls give the bits of those before."""
+    import ctypes
+
+    import test_attention as C
+    from linear_latent_routing_gb300 import gma
+    r = _draw(24)
+    q, k, v, do = r(seqs, N, H, d), r(seqs, N, G, d), r(seqs, N, G, dv), r(seqs, N, H, dv)
+
+    def train():
+        lse = A().prompt_lse(q)
+        o = A().prompt(q, k, v, lse=lse, check=True)
+        return [o, lse, *A().prompt_backward(do, q, k, v, o, lse, check=True).values()]
+    want = train()
+    heads = lambda t: (t.data_ptr(), t.stride(0), t.stride(1), t.stride(2))      # noqa: E731
+    held, out, lse = 0x80000000, torch.empty_like(do), torch.zeros(seqs, H, N, device="cuda")
+    kw = dict(B=seqs, N=N, H=H, G=G, d=d, dv=dv, q=heads(q), k=heads(k), v=heads(v), o=heads(out), lse=lse.data_ptr())
+    if which == "forward":
+        packed, name = C._forward(flags=held | 1, **kw), "gma_attn_forward"
+    elif which == "backward":
+        g = [torch.empty_like(x) for x in (q, k, v)]
+        packed = C._grad(flags=held | 1, do=heads(do), dq=heads(g[0]), dk=heads(g[1]), dv_=heads(g[2]), **kw)
+        name = "gma_attn_backward"
+    else:
+        kp, vp, table = r(20, 64, G, d), r(20, 64, G, dv), torch.arange(20, device="cuda").int().expand(seqs, 20)
+        cached = _ints([1200 - 7 * b for b in range(seqs)])
+        packed = C._paged(flags=held, kp=heads(kp), vp=heads(vp), pages=20, page=64, table_pages=20, table_stride=0, table=table.data_ptr(),
+                          cached=cached.data_ptr(), **kw)
+        name = "gma_attn_paged"
+    sized, run = getattr(gma.lib, name.replace("attn_forward", "attn") + "_workspace_size"), getattr(gma.lib, name)
+    sized.argtypes, sized.restype = [ctypes.c_void_p], ctypes.c_size_t
+    run.argtypes, run.restype = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p], ctypes.c_int
+    n = sized(packed)
+    ws, stream = torch.empty(n, dtype=torch.uint8, device="cuda"), torch.cuda.current_stream().cuda_stream
+    for _ in range(3):
+        assert n > 0 and run(packed, ws.data_ptr(), n, stream) == 0
+        assert gma.gma_check_workspace(ws.data_ptr(), stream) == gma.GMA_ERR_TIMEOUT
+    assert all(torch.equal(x, y) for x, y in zip(train(), want))
+
+
+@pytest.mark.parametrize("d,H,G", [(64, 8, 8), (128, 8, 2), (32, 6, 3)])
+def test_long_runs_repeat_bits(d, H, G):
+    """Many tiles a block, whose loads and products meet at other times in every run."""
+    case = ([5000, 3000, 7, 1200], H, G, d, d, "bf16", True, "packed")
+    q, k, v, do, how, _ = _prompt(case, 25)
+    side, noise = torch.cuda.Stream(), torch.empty(1 << 26, device="cuda")
+    got = []
+    for i in range(6):
+        if i % 2:
+            with torch.cuda.stream(side):
+                noise.normal_()                                        # another stream takes bandwidth and SMs
+        lse = A().prompt_lse(q)
+        o = A().prompt(q, k, v, lse=lse, check=True, **how)
+        g = A().prompt_backward(do, q, k, v, o, lse, check=True, **how)
+        got.append([o, lse, g["q"], g["k"], g["v"]])
+    for x in got[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(got[0], x))
