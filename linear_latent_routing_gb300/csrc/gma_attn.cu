@@ -234,8 +234,10 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const Geo g, const PlanH
 {
     const unsigned lane = threadIdx.x & 31, step = gridDim.x * 8;
     // (the plan was through when the kernel before let this one start)
-    const unsigned rows = (unsigned)__ldcg(&head->tokens) * pack, n = (unsigned)__ldcg(&head->joins) * p.heads * rows;
-    unsigned i = blockIdx.x * 8 + (threadIdx.x >> 5);
+    const unsigned rows = min((unsigned)__ldcg(&head->tokens) * pack, (unsigned)p.rows), n = (unsigned)__ldcg(&head->joins) * p.heads * rows;
+    // Rows that are fewer than the blocks lie on SMs of their own (16 rows of 38 parts each in two blocks took 2 us more: one token over 65536); more of
+    // them fill the first blocks, which start on the first SMs that are free (32 x 6 drafted tokens 2 us less than over all blocks).
+    unsigned i = n <= gridDim.x ? (threadIdx.x >> 5) * gridDim.x + blockIdx.x : blockIdx.x * 8 + (threadIdx.x >> 5);
     auto entry = [&]() {
         const int4 *at = reinterpret_cast<const int4 *>(join + min(i, n - 1) / rows / p.heads);
         const int4 x = __ldcg(at), y = __ldcg(at + 1);
@@ -565,7 +567,7 @@ Plan make_plan(const gma_attn_t &a, int pack, int wide_rows, int narrow_rows, in
     const long long extra = cut ? 4ll * blocks / p.heads + 2 : 0;
     p.max_items = (int)(most + extra);
     p.max_slots = (int)extra;
-    p.rows = (int)std::min<long long>(p.wide, n) * pack;
+    p.rows = std::min(p.wide, a.N) * pack;          // a tile does not span sequences (packed: N rows in all)
     p.head_at = ws->take(sizeof(PlanHead));
     p.items_at = ws->take((size_t)p.max_items * sizeof(Item));
     p.join_at = ws->take((size_t)p.max_slots * sizeof(Join));
@@ -577,7 +579,10 @@ Plan make_plan(const gma_attn_t &a, int pack, int wide_rows, int narrow_rows, in
 PlanArgs plan_args(const Geo &g, const Plan &p, void *ws)
 {
     char *w = (char *)ws;
-    return PlanArgs{g, p.wide, p.narrow, p.key_shift, p.blocks, p.heads, p.max_items, p.max_slots, p.by_keys, 1.f + p.rows / 64.f, (WsHeader *)ws,
+    // a part's cost, in key tiles: its chain into the join and its rows (1 and 3 for the first, 2 as it is: 32 single tokens over up to 2048, 8 heads
+    // of 64: 32.7, 30.5 and 30.5 us)
+    const float part_cost = 2.f + p.rows / 64.f;
+    return PlanArgs{g, p.wide, p.narrow, p.key_shift, p.blocks, p.heads, p.max_items, p.max_slots, p.by_keys, part_cost, (WsHeader *)ws,
                     (PlanHead *)(w + p.head_at), (Item *)(w + p.items_at), (Join *)(w + p.join_at), p.withhold};
 }
 

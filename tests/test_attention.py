@@ -124,6 +124,17 @@ def test_workspaces(lib):
         assert call(packed, FAKE, n - 1, None) == 4 and call(packed, FAKE + 16, n, None) == 4 and call(packed, None, n, None) == 4
 
 
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("B,N,H,G", [(128, 1, 16, 2), (64, 1, 16, 4), (512, 1, 8, 8), (32, 6, 10, 2)])
+def test_parts_take_a_tile_of_one_sequence(lib, dtype, B, N, H, G):
+    """A part holds at most a sequence's rows, however many sequences there are: an SM's four parts and two more, dv sums and two numbers a row."""
+    pages = dict(kp=(FAKE, 16 * G * 128, G * 128, 128), vp=(FAKE, 16 * G * 128, G * 128, 128), pages=9000, page=16, table_pages=600, table_stride=600)
+    n = lib.paged_workspace(_paged(B=B, N=N, H=H, G=G, d=128, dv=128, dtype=dtype, **pages))
+    parts = 4 * (152 // G + 1) + 2
+    lists = 4096 + 128 * (B + 4 * 152)               # headers, an item of 64 bytes a sequence and part, a join of 32 a part
+    assert 0 < n <= parts * H * N * (128 + 2) * 4 + lists
+
+
 def test_copies_take_what_is_copied(lib):
     """bf16 rows off 16-byte boundaries are copied to dense ones of 64 here: q, k and v in the forward pass, do too in the backward pass."""
     B, N, H, G = 2, 1000, 4, 2
