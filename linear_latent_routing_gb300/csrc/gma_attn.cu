@@ -300,14 +300,124 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const Geo g, const PlanH
     }
 }
 
+// Rows that see at most so many keys have a delta of their own in the backward pass of bf16 tensors.  A stored o is off by 2^-9 of itself in the
+// mean, and do . o with it, which over few keys is not small beside ds = p (do . v - delta); delta = sum p do . v / sum p is the same and reads no o.
+// How far dq is off (normwise; the rounding of dq alone 1.66e-3), with do . o for all rows and so: 200 sequences of 2 tokens 3.65e-3 and 2.34e-3,
+// 20 of 33 2.72e-3 and 2.40e-3, 2 of 1000 2.46e-3 and 2.40e-3.  Rows over 17 keys with do . o: 2.54e-3; up to 32 keys cost train steps of
+// 64 x 100 x 16 heads of 128 11 us more.
+constexpr int FEW = 16;
+
+struct FewArgs {
+    Heads<const bf16> q, k, v;
+    const float *lse;
+    unsigned blocks;           // the first ones of the launch, 0: none
+    int pairs;                 // two neighbouring elements lie on 4-byte boundaries
+};
+
+// Those rows' delta: a warp a sequence and head, by mma.sync.  16 x 16 scores are too small for tcgen05, whose loads, barriers and tensor memory take
+// longer than the products; latency is all, and the blocks of the other rows run beside these (5 blocks an SM for their sake: 4 x 2048 tokens, forward
+// and backward, 131.5 us without and 131.0 with it; as a launch of its own 144).
+template <bool PAIR> __device__ __forceinline__ void delta_of_few(const Geo &g, const FewArgs &a, const Heads<const bf16> &d_o, float *delta)
+{
+    const int lane = threadIdx.x & 31, gr = lane >> 2, t2 = 2 * (lane & 3);
+    const long long tiles = (long long)g.B * g.H;
+    // elements c and c + 1 of a row, zeros behind its width and where it `is` not; without branches, so that the loads of a product are on their way
+    // together
+    auto pair = [&](const bf16 *row, int c, int width, bool is) -> uint32_t {
+        const bool lo = is && c < width, hi = is && c + 1 < width;
+        if (PAIR) {
+            const uint32_t x = *reinterpret_cast<const uint32_t *>(row + (lo ? c : 0));
+            return lo ? x : 0u;
+        }
+        const uint32_t x = __bfloat16_as_ushort(row[lo ? c : 0]), y = __bfloat16_as_ushort(row[hi ? c + 1 : 0]);
+        return (lo ? x : 0u) | (hi ? y : 0u) << 16;
+    };
+    for (long long w = blockIdx.x * 8ll + (threadIdx.x >> 5); w < tiles; w += a.blocks * 8ll) {
+        const int h = (int)(w % g.H), kvh = h / g.group, i0 = gr, i1 = gr + 8;
+        const Seq s = sequence(g, (int)(w / g.H));
+        const int rows = g.causal || s.n <= FEW ? min(s.n, FEW) : 0;      // and keys
+        if (!rows) continue;
+        // rows i0 (the first two of four) and i1 of x times the keys' rows of y, columns 8 n + t2 and the next one
+        auto product = [&](const Heads<const bf16> &x, const Heads<const bf16> &y, int width, float (&d)[2][4]) {
+            const bf16 *x0 = x.at(s.b, s.row0 + (i0 < rows ? i0 : 0), h), *x1 = x.at(s.b, s.row0 + (i1 < rows ? i1 : 0), h), *yn[2];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                yn[n] = y.at(s.b, s.row0 + (8 * n + gr < rows ? 8 * n + gr : 0), kvh);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) d[n][c] = 0.f;
+            }
+#pragma unroll 1
+            for (int c0 = 0; c0 < width; c0 += 16) {
+                const int c = c0 + t2;
+                const uint32_t a0 = pair(x0, c, width, i0 < rows), a1 = pair(x1, c, width, i1 < rows);
+                const uint32_t a2 = pair(x0, c + 8, width, i0 < rows), a3 = pair(x1, c + 8, width, i1 < rows);
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const bool is = 8 * n + gr < rows;
+                    const uint32_t b0 = pair(yn[n], c, width, is), b1 = pair(yn[n], c + 8, width, is);
+                    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                        : "+f"(d[n][0]), "+f"(d[n][1]), "+f"(d[n][2]), "+f"(d[n][3])
+                        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+                }
+            }
+        };
+        float score[2][4], dp[2][4];
+        product(a.q, a.k, g.d, score);
+        product(d_o, a.v, g.dv, dp);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int i = half ? i1 : i0, seen = i < rows ? (g.causal ? i + 1 : s.n) : 0;
+            const long long at = stat_at(g, s, h, i < rows ? i : 0);
+            const float lse2 = a.lse[at] * LOG2E;
+            float sum = 0.f, dot = 0.f;
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const float p = 8 * n + t2 + c < seen ? ex2(score[n][2 * half + c] * g.sl2 - lse2) : 0.f;
+                    sum += p;
+                    dot = fmaf(p, dp[n][2 * half + c], dot);
+                }
+#pragma unroll
+            for (int o = 2; o; o >>= 1) {
+                sum += __shfl_xor_sync(~0u, sum, o);
+                dot += __shfl_xor_sync(~0u, dot, o);
+            }
+            if (i < rows && t2 == 0) delta[at] = dot / sum;
+        }
+    }
+}
+
+// Whether row i of the packed tensors, which belongs to a sequence, sees few keys.
+__device__ __forceinline__ bool sees_few(const Geo &g, int i)
+{
+    int lo = 0, hi = g.B;              // the last sequence that starts at or before the row: empty ones may share a start
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (g.offsets[mid] <= i) lo = mid; else hi = mid;
+    }
+    const int start = max(g.offsets[lo], 0);
+    return g.causal ? i - start < FEW : min(g.offsets[lo + 1], g.N) - start <= FEW;
+}
+
 // delta = do . o, and zeros in the gradients' rows that belong to no sequence: LANES lanes a (row, head), eight elements each (VEC) or every LANES-th.
 template <typename T, bool VEC, int LANES>
-__global__ void __launch_bounds__(256) attn_delta_kernel(const Geo g, const Heads<const T> o, const Heads<const T> d_o, float *delta,
-                                                         long long rows, const Heads<T> dq, const Heads<T> dk, const Heads<T> dv, int zero)
+__global__ void __launch_bounds__(256, 5) attn_delta_kernel(const Geo g, const Heads<const T> o, const Heads<const T> d_o, float *delta,
+                                                         long long rows, const Heads<T> dq, const Heads<T> dk, const Heads<T> dv, int zero,
+                                                         const FewArgs few)
 {
     const int lane = threadIdx.x % LANES;
     blk::let_next();
-    for (long long r0 = blockIdx.x * (256ll / LANES); r0 < rows; r0 += gridDim.x * (256ll / LANES)) {
+    if constexpr (sizeof(T) == 2) {
+        if (blockIdx.x < few.blocks) {
+            if (few.pairs) delta_of_few<true>(g, few, d_o, delta);
+            else delta_of_few<false>(g, few, d_o, delta);
+            blk::wait_previous();
+            return;
+        }
+    }
+    const unsigned block = blockIdx.x - few.blocks, blocks = gridDim.x - few.blocks;
+    for (long long r0 = block * (256ll / LANES); r0 < rows; r0 += blocks * (256ll / LANES)) {
         const long long r = r0 + threadIdx.x / LANES;         // heads inner: neighbouring rows of lanes read neighbouring heads
         bool is = r < rows;
         const long long bi = r / g.H;
@@ -346,7 +456,9 @@ __global__ void __launch_bounds__(256) attn_delta_kernel(const Geo g, const Head
         }
 #pragma unroll
         for (int m = LANES / 2; m; m >>= 1) s += __shfl_xor_sync(~0u, s, m);
-        if (is && lane == 0) delta[((long long)b * g.H + h) * g.N + i] = s;
+        bool mine = is;
+        if (few.blocks && is) mine = g.offsets ? !sees_few(g, (int)i) : g.causal ? i >= FEW : blk::row_length(g.lengths, b, g.N) > FEW;
+        if (mine && lane == 0) delta[((long long)b * g.H + h) * g.N + i] = s;
     }
     blk::wait_previous();
 }
@@ -663,13 +775,20 @@ gma_status_t launch_delta(const gma_attn_grad_t &g, float *delta, cudaStream_t s
     const int e16 = 16 / (int)blk::elem_size(a.dtype);
     const int zero = !((a.flags & GMA_ROWS_ZERO_TAIL) && (a.lengths || a.offsets)) ? 0
                      : a.d % e16 == 0 && a.dv % e16 == 0 && heads_vec(g.dq, a.dtype) && heads_vec(g.dk, a.dtype) && heads_vec(g.dv, a.dtype) ? 2 : 1;
+    // rows that see few keys: the first of causal sequences, all of short ones
+    FewArgs few = {heads_of<const bf16>(a.q), heads_of<const bf16>(a.k), heads_of<const bf16>(a.v), a.lse, 0, 0};
+    if (a.dtype == GMA_BF16 && (geo.causal || a.N <= FEW || a.lengths || a.offsets)) {
+        auto even = [](const gma_heads_t &x) { return (((uintptr_t)x.ptr | (uintptr_t)(x.batch * 2) | (uintptr_t)(x.token * 2) | (uintptr_t)(x.head * 2)) & 3u) == 0; };
+        few.blocks = (unsigned)std::min<long long>(((long long)a.B * a.H + 7) / 8, SMS * 16);
+        few.pairs = a.d % 2 == 0 && a.dv % 2 == 0 && even(a.q) && even(a.k) && even(a.v) && even(g.d_o);
+    }
     auto launch = [&](auto type, auto v, auto lanes) -> gma_status_t {
         using T = decltype(type);
         constexpr int LANES = decltype(lanes)::value;
-        const unsigned blocks = (unsigned)std::min<long long>((rows + 256 / LANES - 1) / (256 / LANES), SMS * 32);
+        const unsigned blocks = few.blocks + (unsigned)std::min<long long>((rows + 256 / LANES - 1) / (256 / LANES), SMS * 32);
         GMA_LAUNCH(KID_ATTN_DELTA, st, launch_pdl(attn_delta_kernel<T, decltype(v)::value, LANES>, blocks, 256, 0, st, geo, heads_of<const T>(a.o),
                                                   heads_of<const T>(g.d_o), delta, rows, heads_of<T>(g.dq), heads_of<T>(g.dk), heads_of<T>(g.dv),
-                                                  zero));
+                                                  zero, few));
         return GMA_OK;
     };
     using Yes = std::true_type;

@@ -944,3 +944,69 @@ def test_long_runs_repeat_bits(d, H, G):
         got.append([o, lse, g["q"], g["k"], g["v"]])
     for x in got[1:]:
         assert all(torch.equal(a, b) for a, b in zip(got[0], x))
+
+
+# ------------------------------------------------------------------ gradients over few keys
+
+def _gradients(q, k, v, do, scale, causal, T):
+    """dq, dk and dv of one sequence in 64 bits, each as (value, how far off it may be) where delta is the sum of p dp itself: off by what p
+    (relative e) and dp are, and by fp32 sums, but not by the rounding of the stored o.  Symbols and steps as in attn_ref.py."""
+    q, k, v, do = (t.double() for t in (q, k, v, do))
+    (n, H, d), (_, G, width) = q.shape, v.shape
+    u, W = R.half_step(T), R.W
+    hidden = torch.ones(n, n, device="cuda", dtype=torch.bool).triu(1) if causal else torch.zeros(n, n, device="cuda", dtype=torch.bool)
+    got = [[torch.zeros_like(t), torch.zeros_like(t)] for t in (q, k, v)]
+    for h in range(H):
+        g = h // (H // G)
+        Q, K, V, D = q[:, h], k[:, g], v[:, g], do[:, h]
+        s = (Q @ K.T * scale).masked_fill(hidden, float("-inf"))
+        size = (Q.abs() @ K.abs().T * scale).masked_fill(hidden, 0)
+        p, o = torch.softmax(s, -1), torch.softmax(s, -1) @ V
+        e = 2 * ((d + 6) * W * size.amax(-1, keepdim=True) + 4 * W * s.amax(-1, keepdim=True).abs()) + (n + 8) * W
+        dp = D @ V.T
+        ds = p * (dp - (p * dp).sum(-1, keepdim=True))
+        delta0 = (1 + u) * (D.abs() * o.abs()).sum(-1, keepdim=True)
+        tdp = (width + 5) * W * (D.abs() @ V.abs().T + delta0)
+        tdelta = (p * (e * dp.abs() + tdp * (1 + e))).sum(-1, keepdim=True)
+        tdelta = tdelta + (e + (n + 8) * W) * (delta0 + (p * dp.abs()).sum(-1, keepdim=True))
+        tds = p * (tdelta + tdp) * (1 + u + e) + (u * (1 + u) + e + 4 * W) * ds.abs()
+        grow = 1 + (2 * n + 4) * W
+        for t, at, x, b in ((got[0], h, ds @ K * scale, tds @ K.abs() + (n + 4) * W * (ds.abs() @ K.abs())),
+                            (got[1], g, ds.T @ Q * scale, tds.T @ Q.abs() + (H // G * n + 4) * W * (ds.abs().T @ Q.abs())),
+                            (got[2], g, p.T @ D, ((u * (1 + u) + e) * p).T @ D.abs() + (H // G * n + 4) * W * (p.T @ D.abs()))):
+            t[0][:, at] += x
+            t[1][:, at] += b * grow * (scale if t is not got[2] else 1.0)
+    return [(x, b * (1 + u) + u * x.abs()) for x, b in got]
+
+
+@pytest.mark.parametrize("case", [
+    ([1, 2, 3, 5, 0, 17, 64, 100, 128], 4, 2, 64, 64, "bf16", True, "packed"),
+    ([2, 1, 3] * 13, 8, 8, 64, 16, "bf16", True, "padded"),
+    ([127, 128, 2, 30], 3, 1, 128, 128, "bf16", False, "padded"),
+    ([300, 7, 129], 6, 2, 128, 64, "bf16", True, "packed"),
+    ([90, 41, 32, 0, 31, 9], 12, 1, 32, 128, "bf16", False, "packed"),
+    ([128, 128, 128], 40, 1, 64, 64, "bf16", True, "plain"),           # a group in pieces
+    ([3, 2, 32, 9], 6, 3, 19, 19, "bf16", True, "packed"),             # the CUDA cores
+    ([32, 5], 2, 2, 50, 30, "bf16", False, "padded"),
+    ([40, 20], 8, 1, 21, 36, "bf16", True, "packed"),
+    ([100, 60, 120], 8, 2, 63, 40, "bf16", True, "padded"),
+    ([32, 200, 300], 12, 2, 63, 41, "bf16", True, "padded"),           # copied first
+    ([33, 32, 1], 4, 2, 100, 20, "bf16", True, "mixer"),
+    ([70, 2, 9], 4, 2, 40, 24, "f32", True, "packed"),
+], ids=_id)
+def test_gradients_over_few_keys(case):
+    """Peaked rows over up to 16 keys, where ds is a small difference of large terms: the stored o's rounding does not enter dq, dk and dv."""
+    most = 16
+    q, k, v, do, how, rows = _prompt(case, 26)
+    how["scale"] = 3.0 * case[3] ** -0.5
+    lse = A().prompt_lse(q)
+    o = A().prompt(q, k, v, lse=lse, **how)
+    g = A().prompt_backward(do, q, k, v, o, lse, check=True, **how)
+    for i, n in enumerate(case[0]):
+        if not n or (n > most and not how["causal"]):
+            continue
+        dq, dk, dv = _gradients(*(rows(t, i) for t in (q, k, v, do)), how["scale"], how["causal"], TYPES[case[5]])
+        R.check(rows(g["q"], i)[:most], tuple(t[:most] for t in dq), f"dq of sequence {i}")
+        if n <= most:
+            R.check(rows(g["k"], i), dk, f"dk of sequence {i}")
+            R.check(rows(g["v"], i), dv, f"dv of sequence {i}")
