@@ -211,14 +211,16 @@ gma_status_t gma_norm_backward(const gma_norm_grad_t *grad, void *workspace, siz
  * Padded: `lengths` (NULL: N each) gives every batch row's tokens, taken as min(max(length, 0), N).  Packed: with
  * `offsets` (B + 1 int32 in device memory, not falling, taken as min(max(offset, 0), N)) the tensors are
  * [N][heads][width], sequence b is rows offsets[b] .. offsets[b + 1] - 1, batch strides are ignored and lengths is NULL.  Rows that belong to no
- * sequence are neither read nor written (outputs with GMA_ROWS_ZERO_TAIL: are written as zeros).
+ * sequence are not written (outputs with GMA_ROWS_ZERO_TAIL: are written as zeros), and whatever they hold enters no result, not even its
+ * rounding (tiles are fetched whole, so that they may be read).
  * 1 <= d, dv <= 128; G divides H, H <= 4096; B <= 65535; B * N <= 2^28 rows (packed: N), and
  * times H at most 2^34.  1e-12 <= scale <= 1e12.
  * The elements of a sequence's tokens are finite: where they are not, or a score overflows, that sequence's outputs are
- * unspecified; other sequences' are not touched.
+ * unspecified; other sequences' keep their bits.
  *
  * bf16 runs on the tensor cores (products of bf16 values in fp32; the probabilities, and in the backward
- * pass ds, are rounded to bf16 for the second product), fp32 on the CUDA cores.  Sums, statistics and lse are fp32. */
+ * pass ds, are rounded to bf16 for the second product), fp32 on the CUDA cores.  Sums, statistics and lse are fp32.  The
+ * backward pass takes do . o from o as it was stored, but for rows of bf16 tensors that see at most 16 keys, whose o it does not read. */
 #define GMA_ATTN_CAUSAL 0x1u
 
 typedef struct {

@@ -8,8 +8,8 @@ of H reads key and value head h // (H // G) of G.
 
 Sequences of different lengths are padded (``lengths``, int32 [B] on the device) or packed: [T, heads, width]
 with ``offsets`` (int32 [B + 1] on the device, sequence b is rows offsets[b] to offsets[b + 1] - 1).  Rows of no sequence
-are neither read nor written (in outputs allocated here they are zero).  The elements of a sequence must be finite; where they are
-not, that sequence's outputs are unspecified and other sequences' as usual.
+are not written (in outputs allocated here they are zero), and nothing in them enters a result.  The elements of a sequence must be
+finite; where they are not, that sequence's outputs are unspecified and other sequences' keep their bits.
 
 ``stream`` is the stream to run on (default: the current one).  Nothing here waits for the GPU, but with ``check=True``, which
 raises on a time-out recorded on the device.  Tensors that do not fit raise TypeError or ValueError, what the library refuses

@@ -203,8 +203,11 @@ __device__ __forceinline__ int row_length(const int *lengths, int b, int N)
 
 // Launches of one call follow one another by programmatic dependent launch: a kernel lets the next one be
 // scheduled when it starts, and waits for the one before it to finish where it first reads what that
-// wrote, or before it returns.  A call's first launch is an ordinary one, which waits for all work
-// before the call, and its last one lets nothing start early.
+// wrote, or before it returns.  The first launch of a call waits for all work before the call, before it writes
+// anything or reads what may have been written: as an ordinary launch, or with the first thing that it does (attention's
+// plan, which may start beside the kernel before it).  Only when it is through with that may it let the next one start.
+// A call's last launch lets nothing start early, but for attention's append: what follows an append and is launched so has to
+// wait first.
 __device__ __forceinline__ void let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

@@ -7,8 +7,10 @@
 // while one is worked on.  Calls of less than two blocks of 64 rows an SM take R = 32, single tokens R = 16: latency, not the fp32 pipe,
 // bounds them.  Warps whose rows do not exist only copy.
 //
-// Measured: 4 x 2048 x 8 heads of 117 in bf16 1.31 ms forward, 6.4 ms backward; three sequences of up to 301
-// tokens, 6 heads of 40 in fp32: 23 us a call with its two launches, five single tokens over 300 cached ones 14 us.
+// Measured in fp32: 4 x 2048 tokens, 8 heads of 128, causal, 1.01 ms (34 TFLOP/s of the CUDA cores' 74) and 5.0 ms backward (17 by five products a
+// pair; seven are made), heads of 64 0.60 and 2.87 ms; 64 single tokens over 8192 cached ones each, 16 heads of 128 over 4, 1.04 ms (2.07 TB/s: the two
+// warps whose rows exist work for all); three sequences of up to 301 tokens, 6 heads of 40, 23 us a call with its two launches.  In bf16 the same single
+// tokens with pages of 24 take 2.4 ms (0.45 TB/s: two bytes a load, none ahead), against 0.19 ms with pages of 128 on the tensor cores.
 #include <algorithm>
 
 #include "attn_common.cuh"

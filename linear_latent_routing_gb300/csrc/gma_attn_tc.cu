@@ -14,11 +14,12 @@
 //
 // Warps: 0-3 and 4-7 the streams (a thread a row), 8 issues the products, 9 loads, 10 and 11 write zeros where rows belong to no sequence.
 //
-// Measured: 32768 tokens, 16 heads of 128 over 4, causal 2.55 ms (1720 TFLOP/s; the power limit lowers the clock there), 8192 tokens 187 us
-// (1470; tensor pipe 64 % busy), 4 x 4096 x 16 heads of 64 182 us (750; tensor pipe 41 %, exponentials' pipe 37 %).  At 128 columns the
+// Measured, calls one after another: 32768 tokens, 16 heads of 128 over 4, causal 2.71 ms for seconds on end (1620 TFLOP/s; the power limit lowers
+// the clock to 1.9 GHz), 2.57 for some of them (1710), 8192 tokens 201 us (1370; the kernel alone 189, tensor pipe 64 % busy), 4 x 4096 x 16 heads of 64
+// 179 us (770; at 8192 tokens tensor pipe 40 %, exponentials' pipe 37 %).  At 128 columns the
 // products' warp and the two streams' turns bound it, at 64 the turn of a stream as such: wait, load, maximum, 128 exponentials a thread,
 // store, hand over, which two streams do not cover when the products take half as long.  64 sequences x 8192 cached tokens in pages of 128: 6.2
-// TB/s; pages of 16 cost 6 to 17 % (boxes of 2 KB).
+// TB/s in the kernel (5.6 the call from a cold cache); pages of 16 cost 6 to 17 % (boxes of 2 KB).
 #include "attn_tc.cuh"
 #include "attn_tc_host.cuh"
 

@@ -18,10 +18,11 @@
 //
 // Warps: 0-3 and 4-7 each take half a tile's columns (a thread a row), 8 issues the products, 9 loads.
 //
-// Measured: 8192 tokens, 16 heads of 128 over 4, causal: dk and dv 344 us, dq 266 us alone, 590 us together (dq's blocks take the SMs that
-// the others leave; 1165 TFLOP/s by five products a tile, 1630 by the seven that are made), tensor pipe 75 and 70 % busy; 4 x 4096 x 16 heads of
-// 64: 350 and 250 us.  The chain scores - exponentials - products of one tile bounds both: tensor memory is full, and shared memory holds two
-// query tiles at 128 columns, so that there is no second tile to work on meanwhile.
+// Measured: 8192 tokens, 16 heads of 128 over 4, causal: dk and dv 333 us, dq 254 us alone, 565 us together with the plan and delta (dq's blocks take
+// the SMs that the others leave; 1220 TFLOP/s by five products a tile, 1700 by the seven that are made), tensor pipe 78 and 72 % busy; 4 x 4096 x 16
+// heads of 64 558 us.  The chain scores - exponentials - products of one tile bounds both.  At 128 columns there is no second tile to work on
+// meanwhile: tensor memory is full, and shared memory holds two query tiles.  At 64 columns 128 columns of tensor memory are free in dk and dv, 64 in
+// dq, which this order of products does not use.
 #include "attn_tc.cuh"
 #include "attn_tc_host.cuh"
 
